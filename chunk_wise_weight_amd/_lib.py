@@ -4,6 +4,7 @@ declare (the C ABI sees only raw pointers), allocate outputs and workspace
 with torch on the tensors' device, and pass pointers and the current stream."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -72,6 +73,27 @@ class LactShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("batch", "heads", "seq_len", "head_dim", "hidden", "chunk")]
 
 
+class DeltaShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seq_len", "k_heads", "v_heads", "k_dim", "v_dim")]
+
+
+class DeltaStepShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "states", "k_heads", "v_heads", "k_dim", "v_dim")]
+
+
+class DeltaStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "head", "token")]
+
+
+class DeltaLayout(ctypes.Structure):
+    _fields_ = [(n, DeltaStrides) for n in ("q", "k", "v", "g", "beta", "O")]
+
+
+class DeltaOptions(ctypes.Structure):
+    _fields_ = [("W_init", ctypes.c_void_p), ("seq_starts", ctypes.c_void_p), ("num_seqs", ctypes.c_int64),
+                ("layout", ctypes.POINTER(DeltaLayout))]
+
+
 class TTTError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)}")
@@ -125,6 +147,13 @@ _SIGNATURES = {
     "ttt_lact_swiglu_backward": (_I, [ctypes.POINTER(LactShape), _I, _I, _F] + [_P] * 13 + [_P, _S, _P]),
     "ttt_lact_swiglu_backward_ex": (_I, [ctypes.POINTER(LactShape), _I, _F] + [_P] * 7 +
                                     [ctypes.POINTER(LactOptions)] + [_P] * 6 + [_P, _S, _P]),
+    "ttt_gated_delta_workspace_bytes": (_I, [ctypes.POINTER(DeltaShape), _I, ctypes.c_int64, ctypes.POINTER(_S)]),
+    "ttt_gated_delta": (_I, [ctypes.POINTER(DeltaShape), _I, _F] + [_P] * 5 + [ctypes.POINTER(DeltaOptions)] +
+                        [_P] * 3 + [_S, _P]),
+    "ttt_gated_delta_step": (_I, [ctypes.POINTER(DeltaStepShape), _I, _F] + [_P] * 9),
+    "ttt_layer_norm": (_I, [ctypes.c_int64, ctypes.c_int64, _I, _F] + [_P] * 7),
+    "ttt_layer_norm_backward_workspace_bytes": (_I, [ctypes.c_int64, ctypes.c_int64, _I, ctypes.POINTER(_S)]),
+    "ttt_layer_norm_backward": (_I, [ctypes.c_int64, ctypes.c_int64, _I] + [_P] * 9 + [_S, _P]),
 }
 
 _lib = None
@@ -747,3 +776,185 @@ def ttt_lact_swiglu_backward(q, k, v, W1, W3, W2, dO, chunk: int, eta: float, or
                                           _ptr(W1), _ptr(W3), _ptr(W2), _ptr(dO), *[_ptr(g) for g in grads],
                                           _ptr(ws), nbytes, _stream(dev)), "ttt_lact_swiglu_backward")
     return grads
+
+
+# ---------------------------------------------------------------------------------- gated delta rule, layer norm
+
+
+def _on(device: torch.device):
+    """Makes the tensors' device the current one for a launch, where it is not."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _strided(t, name, shape, dtype, device, rows=True, out=False) -> DeltaStrides:
+    """Checks a [B, H, n, d] (or, with rows=False, a [B, H, n]) tensor of any batch, head and token strides, and
+    gives them.  Outputs must not hold two elements at one place."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (the layer runs only in the HIP library)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    st = t.stride()
+    if rows and t.numel() and (st[3] != 1 or t.data_ptr() % 16 or
+                               any(s * t.element_size() % 16 for s, n in zip(st[:3], shape) if n > 1)):
+        raise ValueError(f"{name}'s last index must be contiguous and its rows 16-byte aligned (strides {st})")
+    if out and t.numel():
+        reach = 1
+        for s, n in sorted((s, n) for s, n in zip(st, shape) if n > 1):
+            if s < reach:
+                raise ValueError(f"{name} is written and must not overlap itself (strides {st})")
+            reach = s * n
+    return DeltaStrides(*(s if n > 1 else 0 for s, n in zip(st[:3], shape)))
+
+
+def _seq_starts(seq_starts, B, device):
+    """Checks packed rows' starts [sequences + 1] (int32, device); the number of sequences, or -1."""
+    if seq_starts is None:
+        return -1
+    if not isinstance(seq_starts, torch.Tensor) or seq_starts.dim() != 1 or seq_starts.numel() < 1:
+        raise ValueError("seq_starts must be a tensor [sequences + 1]")
+    _need(seq_starts, "seq_starts", seq_starts.shape, torch.int32, device)
+    if B != 1:
+        raise ValueError(f"packed sequences lie in one batch row, got {B}")
+    return seq_starts.numel() - 1
+
+
+def ttt_gated_delta_workspace_bytes(shape: DeltaShape, dtype: torch.dtype, num_seqs: int = -1) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_gated_delta_workspace_bytes(ctypes.byref(shape), _dt(dtype), int(num_seqs), ctypes.byref(out)),
+           "ttt_gated_delta_workspace_bytes")
+    return out.value
+
+
+def ttt_gated_delta(q, k, v, g, beta, scale=None, W_init=None, seq_starts=None, O=None, W_final=None,
+                    workspace=None):
+    """The gated delta rule over whole sequences: per value head W_t = exp(g_t) W_{t-1} + beta_t (v_t -
+    exp(g_t) W_{t-1} k_t) k_t^T, o_t = scale W_t q_t.  Returns (O [B, Hv, n, dv], W_final [sequences, Hv, dv, dk]
+    fp32).
+
+    q, k [B, Hk, n, dk] and v [B, Hv, n, dv] share a dtype, g and beta [B, Hv, n] are fp32; each may have any
+    batch, head and token strides (a token-major tensor's transpose(1, 2)), and O, if not given, is laid out like
+    v.  Hv is a multiple of Hk: value head h reads key head h // (Hv // Hk).  scale: dk ** -0.5 if None.
+    W_init [sequences, Hv, dv, dk] fp32: the states to start from (zero if None).  seq_starts, an int32 device
+    tensor [sequences + 1]: packed sequences of any lengths in one batch row; tokens behind the last of them are
+    not read and their rows of O are left as they are."""
+    B, Hk, n, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[3]
+    dt, dev = q.dtype, q.device
+    sq = _strided(q, "q", (B, Hk, n, dk), dt, dev)
+    sk = _strided(k, "k", (B, Hk, n, dk), dt, dev)
+    sv = _strided(v, "v", (B, Hv, n, dv), dt, dev)
+    sg = _strided(g, "g", (B, Hv, n), torch.float32, dev, rows=False)
+    sb = _strided(beta, "beta", (B, Hv, n), torch.float32, dev, rows=False)
+    num = _seq_starts(seq_starts, B, dev)
+    rows = B if num < 0 else num
+    if W_init is not None:
+        _need(W_init, "W_init", (rows, Hv, dv, dk), torch.float32, dev)
+    O = torch.empty_like(v) if O is None else O
+    so = _strided(O, "O", (B, Hv, n, dv), dt, dev, out=True)
+    W_final = torch.empty(rows, Hv, dv, dk, dtype=torch.float32, device=dev) if W_final is None else W_final
+    _need(W_final, "W_final", (rows, Hv, dv, dk), torch.float32, dev)
+    shape = DeltaShape(B, n, Hk, Hv, dk, dv)
+    nbytes = ttt_gated_delta_workspace_bytes(shape, dt, num)
+    ws = _workspace(nbytes, dev, workspace)
+    layout = DeltaLayout(sq, sk, sv, sg, sb, so)
+    opts = DeltaOptions(_vp(W_init), _vp(seq_starts), max(num, 0), ctypes.pointer(layout))
+    with _on(dev):
+        _check(lib().ttt_gated_delta(ctypes.byref(shape), _dt(dt), dk ** -0.5 if scale is None else float(scale),
+                                     _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), ctypes.byref(opts), _vp(O),
+                                     _vp(W_final), _vp(ws), nbytes, _stream(dev)), "ttt_gated_delta")
+    return O, W_final
+
+
+def ttt_gated_delta_step(q, k, v, g, beta, W, slots=None, scale=None, O=None):
+    """One token of the gated delta rule for each row of a serving batch.  q, k [rows, Hk, dk], v [rows, Hv, dv] of
+    one dtype, g, beta [rows, Hv] fp32; W [states, Hv, dv, dk] fp32 is the pool of states, updated in place; slots
+    [rows] int32 on the device names each row's state (a slot outside the pool, such as -1: a padding row, whose
+    output is zero; rows of one slot go in row order; None: row r's state is W[r]).  Returns O [rows, Hv, dv]."""
+    R, Hk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    dt, dev = q.dtype, q.device
+    _need(q, "q", (R, Hk, dk), dt, dev)
+    _need(k, "k", (R, Hk, dk), dt, dev)
+    _need(v, "v", (R, Hv, dv), dt, dev)
+    _need(g, "g", (R, Hv), torch.float32, dev)
+    _need(beta, "beta", (R, Hv), torch.float32, dev)
+    _need(W, "W", (W.shape[0], Hv, dv, dk), torch.float32, dev)
+    if slots is not None:
+        _need(slots, "slots", (R,), torch.int32, dev)
+    O = torch.empty_like(v) if O is None else O
+    _need(O, "O", (R, Hv, dv), dt, dev)
+    shape = DeltaStepShape(R, W.shape[0], Hk, Hv, dk, dv)
+    with _on(dev):
+        _check(lib().ttt_gated_delta_step(ctypes.byref(shape), _dt(dt), dk ** -0.5 if scale is None else float(scale),
+                                          _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), _vp(W), _vp(slots), _vp(O),
+                                          _stream(dev)), "ttt_gated_delta_step")
+    return O
+
+
+def _norm_vector(t, name, d, dt, dev):
+    if t is not None:
+        _need(t, name, (d,), dt, dev)
+
+
+def ttt_layer_norm(x, weight=None, bias=None, eps=1e-5, Y=None, mean=None, rstd=None):
+    """Layer norm over the last index of x [..., d] (contiguous): returns (Y like x, mean [...], rstd [...] fp32).
+    weight and bias [d] of x's dtype, or None."""
+    d = x.shape[-1]
+    dt, dev = x.dtype, x.device
+    _need(x, "x", x.shape, dt, dev)
+    _norm_vector(weight, "weight", d, dt, dev)
+    _norm_vector(bias, "bias", d, dt, dev)
+    Y = torch.empty_like(x) if Y is None else Y
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if mean is None else mean
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if rstd is None else rstd
+    _need(Y, "Y", x.shape, dt, dev)
+    _need(mean, "mean", x.shape[:-1], torch.float32, dev)
+    _need(rstd, "rstd", x.shape[:-1], torch.float32, dev)
+    with _on(dev):
+        _check(lib().ttt_layer_norm(mean.numel(), d, _dt(dt), float(eps), _vp(x), _vp(weight), _vp(bias), _vp(Y),
+                                    _vp(mean), _vp(rstd), _stream(dev)), "ttt_layer_norm")
+    return Y, mean, rstd
+
+
+def ttt_layer_norm_backward_workspace_bytes(rows: int, dim: int, dtype: torch.dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_layer_norm_backward_workspace_bytes(int(rows), int(dim), _dt(dtype), ctypes.byref(out)),
+           "ttt_layer_norm_backward_workspace_bytes")
+    return out.value
+
+
+def ttt_layer_norm_backward(x, weight, dY, mean, rstd, bias=True, dx=None, dweight=None, dbias=None,
+                            workspace=None):
+    """Backward of ttt_layer_norm given its mean and rstd.  Returns (dx like x, dweight [d] fp32 or None where
+    weight is None, dbias [d] fp32 or None with bias=False)."""
+    d = x.shape[-1]
+    dt, dev = x.dtype, x.device
+    _need(x, "x", x.shape, dt, dev)
+    _need(dY, "dY", x.shape, dt, dev)
+    _norm_vector(weight, "weight", d, dt, dev)
+    _need(mean, "mean", x.shape[:-1], torch.float32, dev)
+    _need(rstd, "rstd", x.shape[:-1], torch.float32, dev)
+    dx = torch.empty_like(x) if dx is None else dx
+    _need(dx, "dx", x.shape, dt, dev)
+    if weight is not None and dweight is None:
+        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+    if bias and dbias is None:
+        dbias = torch.empty(d, dtype=torch.float32, device=dev)
+    _norm_vector(dweight, "dweight", d, torch.float32, dev)
+    _norm_vector(dbias, "dbias", d, torch.float32, dev)
+    rows = mean.numel()
+    nbytes = ttt_layer_norm_backward_workspace_bytes(rows, d, dt)
+    ws = _workspace(nbytes, dev, workspace)
+    with _on(dev):
+        _check(lib().ttt_layer_norm_backward(rows, d, _dt(dt), _vp(x), _vp(weight), _vp(dY), _vp(mean), _vp(rstd),
+                                             _vp(dx), _vp(dweight), _vp(dbias), _vp(ws), nbytes, _stream(dev)),
+               "ttt_layer_norm_backward")
+    return dx, dweight, dbias

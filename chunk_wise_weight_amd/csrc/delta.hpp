@@ -1,0 +1,220 @@
+// What the kernels of the gated delta rule share (gfx950).
+//
+// Tokens go in chunks of 64.  Within a chunk, b is the running sum of the log
+// decays, S the state [dk, dv] (W^T) before the chunk, and row i a token:
+//   L_ij = (k_i . k_j) exp(b_i - b_j)  (j < i),   T = (I + L diag(beta))^-1
+//   E    = T (V - exp(b) K S)                     the tokens' errors before beta
+//   O    = scale exp(b) Q S + P E,  P_ij = scale (q_i . k_j) exp(b_i - b_j) beta_j  (j <= i)
+//   S'   = exp(b_63) S + K^T (exp(b_63 - b) beta E)
+// T and P depend on the inputs alone and are made for all chunks at once
+// (k_delta_chunks); the walk over the chunks (k_delta_walk) keeps a slice of
+// the state's columns in registers.
+//
+// Operands.  Every product is made of 16 x 16 MFMA blocks whose operand lanes
+// hold row lane & 15 and 16 bytes along the contraction.  Result rows are
+// dealt to the blocks such (Mat::row) that the registers a lane holds of a
+// result are, in order, the operand of the next product contracted over those
+// rows: state, errors and their scaled forms go from product to product
+// without leaving the registers.
+//
+// Precision (bf16 inputs).  A product's bf16 operand that comes from fp32
+// registers is a pair hi + lo of bf16 values (2^-17 relative), with hi x hi,
+// hi x lo and lo x hi summed in fp32, wherever it feeds the state, which is
+// fp32: the state keeps fp32's digits over long rows.  What feeds only the
+// output O, which is rounded to bf16 at the end, is rounded once to bf16.
+#pragma once
+#include "gemm.hpp"
+#include "launch.hpp"
+
+namespace ttt {
+
+constexpr int kDC = 64;          // tokens of a chunk
+
+template <typename T> struct Mat;
+
+template <> struct Mat<bf16> {
+  static constexpr int KB = 32;            // contraction per product step
+  static constexpr int TPS = 2;            // result blocks whose rows make one step
+  static constexpr int kTri = 6;           // operand fragments of a lower triangular 64 x 64 matrix
+  static constexpr bool kSplit = true;
+  // Row of the matrix that block `tile`, block row m stands for: lane group g
+  // holds rows g * 8 + 0..3 of a step in its even block and + 4..7 in its odd one.
+  __device__ static __forceinline__ int row(int tile, int m) {
+    return ((tile >> 1) << 5) + ((m >> 2) << 3) + ((tile & 1) << 2) + (m & 3);
+  }
+  // steps of a triangular matrix that block `tile` has
+  __device__ static constexpr int steps(int tile) { return (tile >> 1) + 1; }
+  __device__ static constexpr int tri(int tile, int s) { return tile < 2 ? tile : 2 + (tile - 2) * 2 + s; }
+  __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  // The operand made of a step's result blocks, rounded to bf16.
+  __device__ static __forceinline__ u32x4 frag(const f32x4* c) {
+    return (u32x4){pack2_bf16(c[0][0], c[0][1]), pack2_bf16(c[0][2], c[0][3]), pack2_bf16(c[1][0], c[1][1]),
+                   pack2_bf16(c[1][2], c[1][3])};
+  }
+  __device__ static __forceinline__ void split(const f32x4* c, u32x4& hi, u32x4& lo) {
+    hi = frag(c);
+    f32x4 r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const unsigned w = hi[2 * i + j];
+        r[i][2 * j] = c[i][2 * j] - __uint_as_float(w << 16);
+        r[i][2 * j + 1] = c[i][2 * j + 1] - __uint_as_float(w & 0xffff0000u);
+      }
+    lo = frag(r);
+  }
+  // 8 consecutive values to one operand's 16 bytes, and the rest
+  __device__ static __forceinline__ void split8(const float* x, u32x4& hi, u32x4& lo) {
+    const f32x4 c[2] = {{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
+    split(c, hi, lo);
+  }
+};
+
+template <> struct Mat<float> {
+  static constexpr int KB = 16, TPS = 1, kTri = 10;
+  static constexpr bool kSplit = false;
+  __device__ static __forceinline__ int row(int tile, int m) { return tile * 16 + m; }
+  __device__ static constexpr int steps(int tile) { return tile + 1; }
+  __device__ static constexpr int tri(int tile, int s) { return tile * (tile + 1) / 2 + s; }
+  // lane group g holds contraction indices 4 g + r; instruction r takes index 4 g + r of every group
+  __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[r]), __uint_as_float(b[r]), c, 0, 0, 0);
+    return c;
+  }
+  __device__ static __forceinline__ u32x4 frag(const f32x4* c) { return __builtin_bit_cast(u32x4, c[0]); }
+  __device__ static __forceinline__ void split(const f32x4* c, u32x4& hi, u32x4& lo) {
+    hi = frag(c);
+    lo = (u32x4){0, 0, 0, 0};
+  }
+};
+
+// c + a b with b = hi + lo and a exact; with a = hi + lo too.
+template <typename T>
+__device__ __forceinline__ f32x4 mma_split(u32x4 a, u32x4 bh, u32x4 bl, f32x4 c) {
+  c = Mat<T>::mma(a, bh, c);
+  if (Mat<T>::kSplit) c = Mat<T>::mma(a, bl, c);
+  return c;
+}
+template <typename T>
+__device__ __forceinline__ f32x4 mma_split2(u32x4 ah, u32x4 al, u32x4 bh, u32x4 bl, f32x4 c) {
+  c = Mat<T>::mma(ah, bh, c);
+  if (Mat<T>::kSplit) {
+    c = Mat<T>::mma(ah, bl, c);
+    c = Mat<T>::mma(al, bh, c);
+  }
+  return c;
+}
+
+// What k_delta_chunks leaves of a chunk and value head: T (hi, then lo), P, in
+// operand order (fragment, lane, 16 bytes), then exp(b), beta and
+// exp(b_63 - b) of its 64 tokens.
+template <typename T> struct ChunkRec {
+  static constexpr int kFrag = Mat<T>::kTri * 1024;
+  static constexpr int kTl = kFrag;
+  static constexpr int kP = Mat<T>::kSplit ? 2 * kFrag : kFrag;
+  static constexpr int kGate = kP + kFrag;
+  static constexpr int kBytes = kGate + 1024;       // three rows of 64 floats, one spare
+};
+
+// 64 rows of up to DK elements in LDS: panels of 128 bytes a row, the 16-byte
+// chunk c of row r in slot c ^ panel_swz(r).  The 16 rows of an operand read
+// (Mat::row: rows 0-3, 8-11, 16-19, 24-27 of a step, or the other four of each
+// eight) differ in row & 1 and the three bits used here, so they fall into 16
+// different 16-byte bank groups.
+__device__ __forceinline__ int panel_swz(int r) { return ((r >> 1) & 1) | (((r >> 3) & 3) << 1); }
+template <typename T> struct Panels {
+  static constexpr int bytes(int DK) { return DK * (int)sizeof(T) * kDC; }
+  // 16 bytes of row r at contraction step s, lane group g
+  __device__ static __forceinline__ u32x4 frag(const char* t, int r, int s, int g) {
+    return *reinterpret_cast<const u32x4*>(t + (s >> 1) * 8192 + r * 128 + (((4 * (s & 1) + g) ^ panel_swz(r)) << 4));
+  }
+  // The transpose's operand: row = column Mat::row(tile, lane & 15), contraction over the 64 rows, step s.
+  __device__ static __forceinline__ u32x4 frag_t(const char* t, int tile, int s, int lane) {
+    const int j = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+      // ds_read_b64_tr_b16: lane j of a 16-lane group addresses 4 columns of row j >> 2 and receives
+      // column j of the 16 addressed, rows 0..3
+      const int col = ((tile >> 1) << 5) + ((j & 3) << 3), r = s * 32 + g * 8 + (j >> 2);
+      const char* p = t + (col >> 6) * 8192 + ((tile & 1) << 3);
+      const int c = (col & 63) >> 3;
+      const s16x4 x = lds_read_tr16(p + r * 128 + ((c ^ panel_swz(r)) << 4));
+      const s16x4 y = lds_read_tr16(p + (r + 4) * 128 + ((c ^ panel_swz(r + 4)) << 4));
+      const u32x2 a = __builtin_bit_cast(u32x2, x), b = __builtin_bit_cast(u32x2, y);
+      return (u32x4){a[0], a[1], b[0], b[1]};
+    } else {
+      const int col = tile * 16 + j, c = (col & 31) >> 2;
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = s * 16 + g * 4 + i;
+        o[i] = *reinterpret_cast<const unsigned*>(t + (col >> 5) * 8192 + r * 128 + ((c ^ panel_swz(r)) << 4) +
+                                                  ((col & 3) << 2));
+      }
+      return o;
+    }
+  }
+  // DMA instructions that bring all panels, the i-th of them: rows 8 b .. 8 b + 7 of a panel.  Rows >= len
+  // and columns >= row_bytes read as zero.
+  static constexpr int loads(int DK) { return bytes(DK) / 1024; }
+  __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int i, int len, unsigned pitch,
+                                              unsigned row_bytes, char* t) {
+    const int L = lane_id(), b = i & 7, r = b * 8 + (L >> 3);
+    const unsigned byte = (unsigned)(i >> 3) * 128u +
+                          (unsigned)(((L & 7) ^ (((L >> 4) & 1) | ((b & 3) << 1))) << 4);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
+                                             r < len && byte < row_bytes ? (unsigned)r * pitch + byte : kOOB, 0, 0, 0);
+  }
+};
+
+// ------------------------------------------------------------------ sequences and their chunks
+
+// Packed rows: sequence i's chunks take the slots from starts[i] / 64 + i on.
+// That leaves every sequence room for its chunks (a sequence touches at most
+// one more 64-token cell than it has full chunks) and needs no prefix sum: the
+// slots number n / 64 + num.  Starts are brought into 0..n and an end before
+// its start counts as the start, so no value of theirs leads out of the rows.
+__device__ __forceinline__ int seq_start(const DeltaSeqs& q, int i) { return min(max(q.starts[i], 0), q.n); }
+inline __host__ __device__ int64_t delta_slots(const DeltaSeqs& q, int batch) {
+  return q.starts ? (int64_t)q.n / kDC + q.num : (int64_t)batch * ((q.n + kDC - 1) / kDC);
+}
+
+// Where sequence s lies: batch row, first token, tokens, first chunk slot.
+struct SeqPlace {
+  int b, tok0, len, slot0;
+};
+__device__ __forceinline__ SeqPlace seq_place(const DeltaSeqs& q, int s) {
+  if (q.starts) {
+    const int a = seq_start(q, s), e = max(seq_start(q, s + 1), a);
+    return {0, a, e - a, a / kDC + s};
+  }
+  return {s, 0, q.n, s * ((q.n + kDC - 1) / kDC)};
+}
+
+// Where a chunk slot's tokens lie; len <= 0: the slot has none.
+struct ChunkPlace {
+  int b, tok0, len;
+  int seq;
+  bool first, last;             // of its sequence
+};
+__device__ __forceinline__ ChunkPlace chunk_place(const DeltaSeqs& q, int slot) {
+  if (!q.starts) {
+    const int m = (q.n + kDC - 1) / kDC, b = slot / m, c = slot - b * m;
+    return {b, c * kDC, min(kDC, q.n - c * kDC), b, c == 0, c == m - 1};
+  }
+  int lo = 0, hi = q.num;       // the last sequence whose first slot is not past this one
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_start(q, mid) / kDC + mid <= slot) lo = mid; else hi = mid;
+  }
+  const int a = seq_start(q, lo), e = max(seq_start(q, lo + 1), a), c = slot - (a / kDC + lo);
+  if (c < 0 || c * kDC >= e - a) return {0, 0, 0, lo, false, false};
+  return {0, a + c * kDC, min(kDC, e - a - c * kDC), lo, c == 0, (c + 1) * kDC >= e - a};
+}
+
+}  // namespace ttt

@@ -203,4 +203,55 @@ size_t lact_workspace_bytes(int B, int H, int n, int dh, int m, int C);
 template <typename T>
 hipError_t launch_lact(const LactArgs& a, hipStream_t s);
 
+// Layer norm over rows of d elements; mean and rstd [rows] are written.
+template <typename T>
+hipError_t launch_norm(const T* x, const T* w, const T* b, T* y, float* mean, float* rstd, int64_t rows, int d,
+                       float eps, hipStream_t s);
+// Workgroups of the backward pass = rows of its scratch `part` [blocks, 2, d].
+template <typename T>
+int norm_grad_blocks(int64_t rows, int d);
+template <typename T>
+hipError_t launch_norm_grad(const T* x, const T* w, const T* dy, const float* mean, const float* rstd, T* dx,
+                            float* dw, float* db, float* part, int64_t rows, int d, hipStream_t s);
+
+// Gated delta rule.  Strides in elements of a [B, H, n, d] (gates: [B, H, n]) tensor.
+struct DeltaStrides {
+  int64_t b, h, t;
+};
+// Sequence s of `num` (device starts [num + 1]; null: one sequence a batch row of n tokens).
+struct DeltaSeqs {
+  const int32_t* starts;
+  int num;
+  int n;
+};
+struct DeltaStepArgs {
+  int rows, Hk, Hv, dk, dv;
+  int64_t pool;
+  const void *q, *k, *v;               // [rows, H, d]
+  const float *g, *beta;               // [rows, Hv]
+  float* W;                            // [pool, Hv, dv, dk]
+  const int32_t* slots;                // [rows] or null: row r's state is W[r]
+  void* O;                             // [rows, Hv, dv]
+  float scale;
+};
+template <typename T>
+hipError_t launch_delta_step(const DeltaStepArgs& a, hipStream_t s);
+
+struct DeltaArgs {
+  int batch, Hk, Hv, dk, dv;
+  DeltaSeqs seqs;
+  const void *q, *k, *v;
+  const float *g, *beta;
+  DeltaStrides sq, sk, sv, sg, sbeta, so;
+  const float* W_init;                 // [sequences, Hv, dv, dk] or null: zero
+  void* O;
+  float* W_final;                      // [sequences, Hv, dv, dk]
+  char* ws;
+  float scale;
+};
+template <typename T>
+size_t delta_workspace_bytes(const DeltaArgs& a);
+template <typename T>
+hipError_t launch_delta(const DeltaArgs& a, hipStream_t s);
+
 }  // namespace ttt

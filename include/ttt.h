@@ -688,6 +688,118 @@ int ttt_lact_swiglu_backward_ex(const ttt_lact_shape* shape, int dtype, float et
                                 void* dq, void* dk, void* dv, float* dW1, float* dW3, float* dW2,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ gated delta rule */
+
+/* The token-wise sibling of the MSE objective: per value head, the state W
+ * [dv, dk] decays and takes one gradient step of rate beta_t on its own
+ * token's squared error, then is applied to the token's query:
+ *   e_t = v_t - exp(g_t) W_{t-1} k_t
+ *   W_t = exp(g_t) W_{t-1} + beta_t e_t k_t^T
+ *   o_t = scale W_t q_t                      (update, then apply)
+ * n = seq_len; value head h reads key head h / (v_heads / k_heads).
+ * Supported: v_heads a multiple of k_heads (else TTT_ERR_SHAPE); k_dim and
+ * v_dim multiples of 8, k_dim <= 256, v_dim <= 4096, batch * seq_len <= 2^30,
+ * chunks of 64 tokens times value heads below 2^24 (else
+ * TTT_ERR_UNSUPPORTED). */
+typedef struct {
+  int64_t batch, seq_len, k_heads, v_heads, k_dim, v_dim;
+} ttt_delta_shape;
+
+/* Strides, in elements, of a [B, H, n, d] tensor whose last index is
+ * contiguous (gates: of a [B, H, n] tensor).  Nonnegative; token strides at
+ * most 2^22; for all but the gates multiples of 16 bytes.  Zero strides
+ * repeat a row, in inputs only.  (Else TTT_ERR_ARG.) */
+typedef struct {
+  int64_t batch, head, token;
+} ttt_delta_strides;
+typedef struct {
+  ttt_delta_strides q, k, v, g, beta, O;
+} ttt_delta_layout;
+
+/* Options; a NULL pointer or all fields zero: rows of one sequence each that
+ * start from W = 0, every tensor contiguous. */
+typedef struct {
+  /* State before each sequence's first token [sequences, Hv, dv, dk] fp32
+   * (an earlier call's W_final), or NULL: zero. */
+  const float* W_init;
+  /* Packed sequences of any lengths (batch must be 1, else TTT_ERR_SHAPE):
+   * num_seqs + 1 int32, DEVICE, not decreasing; sequence i holds tokens
+   * seq_starts[i] .. seq_starts[i+1] - 1, possibly none.  Tokens before the
+   * first start and from the last one on belong to no sequence: they are not
+   * read, and their output rows are left as they are.  Values outside 0 ..
+   * seq_len are taken as the nearer of the two, and an end before its start
+   * as the start; with starts that decrease the outputs are undefined. */
+  const int32_t* seq_starts;
+  int64_t num_seqs;
+  const ttt_delta_layout* layout;  /* HOST; NULL: contiguous */
+} ttt_delta_options;
+
+/* Workspace of ttt_gated_delta; num_seqs < 0: not packed. */
+int ttt_gated_delta_workspace_bytes(const ttt_delta_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
+
+/* The rule over whole sequences.
+ *   q, k      [B, Hk, n, dk]  dtype
+ *   v         [B, Hv, n, dv]  dtype
+ *   g, beta   [B, Hv, n]      fp32 (4-byte aligned)   log decay; rate
+ *   O         [B, Hv, n, dv]  dtype   (written)
+ *   W_final   [sequences, Hv, dv, dk] fp32 (written)  sequences = B, or num_seqs
+ * A log decay of -inf (or below -200) sets the state to zero before the
+ * token's step: a document boundary inside a sequence.  With bf16 inputs the
+ * state and what feeds it keep 16 bits or more of mantissa throughout.
+ * seq_len == 0 or an empty sequence: W_final is W_init (or zero). */
+int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const void* q, const void* k, const void* v,
+                    const float* g, const float* beta, const ttt_delta_options* options, void* O, float* W_final,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sizes of a step: rows of a serving batch, states in the pool. */
+typedef struct {
+  int64_t rows, states, k_heads, v_heads, k_dim, v_dim;
+} ttt_delta_step_shape;
+
+/* One token for each row of a serving batch, on states that stay in a pool
+ * and are updated IN PLACE (the one exception to read-only inputs).
+ *   q, k      [rows, Hk, dk]  dtype
+ *   v         [rows, Hv, dv]  dtype
+ *   g, beta   [rows, Hv]      fp32 (4-byte aligned)
+ *   W         [states, Hv, dv, dk] fp32   (read and written)
+ *   slots     [rows] int32, DEVICE: row r's state is W[slots[r]]; a slot
+ *             outside 0 .. states - 1 (for instance -1) marks a padding row:
+ *             no state is touched and its output is zero.  Rows that name the
+ *             same state take their tokens in row order.  NULL: row r's
+ *             state is W[r] (rows <= states, else TTT_ERR_SHAPE).
+ *   O         [rows, Hv, dv]  dtype   (written)
+ * All arithmetic and the state are fp32.  rows * v_heads * ceil(v_dim / 16)
+ * below 2^24, else TTT_ERR_UNSUPPORTED. */
+int ttt_gated_delta_step(const ttt_delta_step_shape* shape, int dtype, float scale, const void* q, const void* k,
+                         const void* v, const float* g, const float* beta, float* W, const int32_t* slots, void* O,
+                         void* stream);
+
+/* ------------------------------------------------------------------ layer norm */
+
+/* Layer norm of rows of `dim` elements (the hidden states a layer takes, or
+ * each head's output): y = (x - mean) rstd weight + bias, rstd = 1 /
+ * sqrt(mean((x - mean)^2) + eps), statistics in fp32 in two passes.
+ *   x, y          [rows, dim]  dtype
+ *   weight, bias  [dim]        dtype, or NULL: 1, resp. 0
+ *   mean, rstd    [rows]       fp32 (written; 4-byte aligned)
+ * dim <= 65536 (else TTT_ERR_UNSUPPORTED); eps finite and not negative.
+ * Where dim is no multiple of 16 bytes the tensors need their elements'
+ * alignment only. */
+int ttt_layer_norm(int64_t rows, int64_t dim, int dtype, float eps, const void* x, const void* weight,
+                   const void* bias, void* y, float* mean, float* rstd, void* stream);
+
+int ttt_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim, int dtype, size_t* bytes);
+
+/* Its backward, given the forward's mean and rstd: with h = (x - mean) rstd
+ * and a = dy weight,
+ *   dx      [rows, dim] dtype   rstd (a - mean(a) - h mean(a h))
+ *   dweight [dim] fp32          sum over rows of dy h, or NULL: not wanted
+ *   dbias   [dim] fp32          sum over rows of dy, or NULL: not wanted
+ * rows == 0 gives zero sums.  The sums are made in a fixed order. */
+int ttt_layer_norm_backward(int64_t rows, int64_t dim, int dtype, const void* x, const void* weight, const void* dy,
+                            const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
