@@ -45,6 +45,9 @@ template <> struct Mat<bf16> {
   // steps of a triangular matrix that block `tile` has
   __device__ static constexpr int steps(int tile) { return (tile >> 1) + 1; }
   __device__ static constexpr int tri(int tile, int s) { return tile < 2 ? tile : 2 + (tile - 2) * 2 + s; }
+  // the same of an upper triangular one: steps first(tile) .. 64 / KB - 1
+  __device__ static constexpr int first(int tile) { return tile >> 1; }
+  __device__ static constexpr int triu(int tile, int s) { return tile < 2 ? tile * 2 + s : 4 + (tile - 2); }
   __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
@@ -80,6 +83,8 @@ template <> struct Mat<float> {
   __device__ static __forceinline__ int row(int tile, int m) { return tile * 16 + m; }
   __device__ static constexpr int steps(int tile) { return tile + 1; }
   __device__ static constexpr int tri(int tile, int s) { return tile * (tile + 1) / 2 + s; }
+  __device__ static constexpr int first(int tile) { return tile; }
+  __device__ static constexpr int triu(int tile, int s) { return tile * 4 - tile * (tile - 1) / 2 + (s - tile); }
   // lane group g holds contraction indices 4 g + r; instruction r takes index 4 g + r of every group
   __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 #pragma unroll
@@ -111,15 +116,23 @@ __device__ __forceinline__ f32x4 mma_split2(u32x4 ah, u32x4 al, u32x4 bh, u32x4 
   return c;
 }
 
-// What k_delta_chunks leaves of a chunk and value head: T (hi, then lo), P, in
-// operand order (fragment, lane, 16 bytes), then exp(b), beta and
-// exp(b_63 - b) of its 64 tokens.
+// What k_delta_chunks leaves of a chunk and value head, in operand order
+// (fragment, lane, 16 bytes): T (hi, then lo), the gates, P.
 template <typename T> struct ChunkRec {
   static constexpr int kFrag = Mat<T>::kTri * 1024;
   static constexpr int kTl = kFrag;
+  static constexpr int kGate = Mat<T>::kSplit ? 2 * kFrag : kFrag;   // exp(b), beta exp(b_63 - b): 64 floats each
+  static constexpr int kP = kGate + 1024;
+  static constexpr int kBytes = kP + kFrag;
+};
+// The same for the backward pass: the transposes of T and P (hi, lo each), the gates.
+template <typename T> struct ChunkRecT {
+  static constexpr int kFrag = ChunkRec<T>::kFrag;
+  static constexpr int kTl = kFrag;
   static constexpr int kP = Mat<T>::kSplit ? 2 * kFrag : kFrag;
-  static constexpr int kGate = kP + kFrag;
-  static constexpr int kBytes = kGate + 1024;       // three rows of 64 floats, one spare
+  static constexpr int kPl = kP + kFrag;
+  static constexpr int kGate = 2 * kP;
+  static constexpr int kBytes = kGate + 1024;
 };
 
 // 64 rows of up to DK elements in LDS: panels of 128 bytes a row, the 16-byte
@@ -159,18 +172,71 @@ template <typename T> struct Panels {
       return o;
     }
   }
-  // DMA instructions that bring all panels, the i-th of them: rows 8 b .. 8 b + 7 of a panel.  Rows >= len
-  // and columns >= row_bytes read as zero.
-  static constexpr int loads(int DK) { return bytes(DK) / 1024; }
-  __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int i, int len, unsigned pitch,
-                                              unsigned row_bytes, char* t) {
-    const int L = lane_id(), b = i & 7, r = b * 8 + (L >> 3);
-    const unsigned byte = (unsigned)(i >> 3) * 128u +
-                          (unsigned)(((L & 7) ^ (((L >> 4) & 1) | ((b & 3) << 1))) << 4);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
-                                             r < len && byte < row_bytes ? (unsigned)r * pitch + byte : kOOB, 0, 0, 0);
+  // DMA of all panels by NW waves, instruction i = rows 8 (i & 7) .. + 7 of panel i >> 3.  Rows >= len and columns
+  // >= row_bytes read as zero: a whole chunk of full rows needs no test of either.
+  template <int DK, int NW>
+  __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int len, unsigned pitch, unsigned row_bytes,
+                                              char* t) {
+    constexpr int N = bytes(DK) / 1024;
+    const int L = lane_id(), w = wave_id() % NW;
+    const bool full = len >= kDC && row_bytes == DK * sizeof(T);
+#pragma unroll
+    for (int j = 0; j < N / NW; ++j) {
+      const int i = j * NW + w, b = i & 7;
+      const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4), at = (unsigned)(i >> 3) * 128u;
+      unsigned off = (unsigned)(L >> 3) * pitch + byte + ((unsigned)b * 8u * pitch + at);
+      if (!full && ((L >> 3) >= len - b * 8 || byte + at >= row_bytes)) off = kOOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, off, 0, 0, 0);
+    }
   }
 };
+
+// Rows from `base` on: loads through it test rows and columns themselves.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base) { return make_rsrc(base, kOOB); }
+
+// 64 rows of a wave group's own columns: NW waves with 16 columns each, row by row.
+template <typename T, int NW> struct Columns {
+  static constexpr int kPitch = 16 * NW * (int)sizeof(T), kBytes = kDC * kPitch;
+  // cols: valid columns from this group's first on
+  __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int len, unsigned pitch, int cols, char* t) {
+    constexpr int N = kBytes / 1024, GPR = kPitch / 16, RPI = 64 / GPR;      // 16-byte pieces a row, rows a load
+    const int L = lane_id(), w = wave_id() % NW;
+#pragma unroll
+    for (int j = 0; j < N / NW; ++j) {
+      const int i = j * NW + w, r = i * RPI + L / GPR, c = L % GPR;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (lds_ptr_t)(t + i * 1024), 16,
+          r < len && c * (16 / (int)sizeof(T)) < cols ? (unsigned)r * pitch + c * 16u : kOOB, 0, 0, 0);
+    }
+  }
+  // column lane & 15 of wave w's, rows Mat::row(tile, 4 g + 0..3)
+  __device__ static __forceinline__ f32x4 read(const char* t, int w, int tile, int lane) {
+    const int m = lane & 15, r = Mat<T>::row(tile, (lane >> 4) * 4);
+    if constexpr (sizeof(T) == 2) {
+      const u32x2 x = __builtin_bit_cast(u32x2, lds_read_tr16(t + (r + (m >> 2)) * kPitch + w * 32 + (m & 3) * 8));
+      return (f32x4){__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
+                     __uint_as_float(x[1] & 0xffff0000u)};
+    } else {
+      f32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const float*>(t + (r + i) * kPitch + (w * 16 + m) * 4);
+      return o;
+    }
+  }
+};
+
+// `N` KB that lie one after the other, by NW waves.
+template <int N, int NW>
+__device__ __forceinline__ void load_block(__amdgpu_buffer_rsrc_t rs, char* t) {
+  const int w = wave_id() % NW;
+#pragma unroll
+  for (int j = 0; j < (N + NW - 1) / NW; ++j) {
+    const int i = j * NW + w;
+    if (N % NW == 0 || i < N)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, (unsigned)(i * 1024 + lane_id() * 16),
+                                               0, 0, 0);
+  }
+}
 
 // ------------------------------------------------------------------ sequences and their chunks
 

@@ -1,0 +1,411 @@
+// The kernels that the gated delta rule's forward and backward pass share
+// (gfx950); the mathematics and the operand layout are in delta.hpp.
+#pragma once
+#include "delta.hpp"
+
+namespace ttt {
+namespace {
+
+// ------------------------------------------------------------------ T, P and the gates of every chunk
+
+// One workgroup of 4 waves per chunk slot and value head.  Wave w makes row
+// block w (16 tokens) of K K^T and Q K^T, the decays in fp64 (differences of
+// sums that may have grown large), then T: the four 16 x 16 diagonal blocks by
+// substitution, one a wave, and the blocks below them column by column,
+//   T_ij = -T_ii sum_{j <= l < i} A_il T_lj,   A = L diag(beta),
+// wave j taking column j: fp32 MFMA products, the running block column staying
+// in registers as the next product's operand.
+constexpr int kChunkThreads = 256;
+constexpr int kLd = 68;           // pitch of a 64 x 64 fp32 matrix in LDS
+
+__device__ __forceinline__ f32x4 mma_f32(const float* a, f32x4 b, f32x4 c) {
+  return Mat<float>::mma(*reinterpret_cast<const u32x4*>(a), __builtin_bit_cast(u32x4, b), c);
+}
+
+// The lower triangle X (or, with TRANS, its transpose) to memory in operand
+// order, in T's type, with SPLIT what that leaves too (for bf16).
+template <typename T, bool TRANS, bool SPLIT>
+__device__ __forceinline__ void put_triangle(const float* X, char* hi, char* lo) {
+  constexpr int E = 16 / sizeof(T);
+  const int lane = lane_id(), m = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int s = 0; s < kDC / Mat<T>::KB; ++s) {
+      if (TRANS ? s < Mat<T>::first(t) : s >= Mat<T>::steps(t)) continue;
+      const int f = TRANS ? Mat<T>::triu(t, s) : Mat<T>::tri(t, s);
+      if ((f & 3) != wave_id()) continue;
+      const int r = Mat<T>::row(t, m), k = s * Mat<T>::KB + g * E;
+      f32x4 v[E / 4];
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i / 4][i % 4] = TRANS ? X[(k + i) * kLd + r] : X[r * kLd + k + i];
+      u32x4 h, l;
+      Mat<T>::split(v, h, l);
+      *reinterpret_cast<u32x4*>(hi + f * 1024 + lane * 16) = h;
+      if (SPLIT && Mat<T>::kSplit) *reinterpret_cast<u32x4*>(lo + f * 1024 + lane * 16) = l;
+    }
+}
+
+// With BACK, T goes to rec and the transposes of T and P to rect.
+template <typename T, bool BACK>
+__global__ __launch_bounds__(kChunkThreads) void k_delta_chunks(DeltaArgs p, char* rec, char* rect) {
+  constexpr int KB = Mat<T>::KB;
+  __shared__ __attribute__((aligned(16))) float A[kDC * kLd], X[kDC * kLd];   // X: P, then T
+  __shared__ double b[kDC];
+  __shared__ float beta[kDC];
+  const int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int h = id % p.Hv, slot = id / p.Hv;
+  const ChunkPlace c = chunk_place(p.seqs, slot);
+  if (c.len <= 0) return;
+  char* out = rec + (int64_t)id * ChunkRec<T>::kBytes;
+  const int w = wave_id(), lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int kh = h / (p.Hv / p.Hk);
+
+  if (w == 0) {
+    float gi = 0.f, bi = 0.f;
+    if (lane < c.len) {
+      gi = p.g[c.b * p.sg.b + h * p.sg.h + (c.tok0 + lane) * p.sg.t];
+      bi = p.beta[c.b * p.sbeta.b + h * p.sbeta.h + (c.tok0 + lane) * p.sbeta.t];
+    }
+    // exp(-200) is zero in fp32: a decay of -inf (a state reset) keeps the running sum finite
+    double s = gi < -200.f ? -200.0 : (double)gi;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double up = __shfl_up(s, d, 64);
+      if (lane >= d) s += up;
+    }
+    const double last = __shfl(s, 63, 64);
+    b[lane] = s;
+    beta[lane] = bi;
+    float* gate = reinterpret_cast<float*>(out + ChunkRec<T>::kGate);
+    const float up = __expf((float)s), left = bi * __expf((float)(last - s));
+    gate[lane] = up;
+    gate[64 + lane] = left;
+    if (BACK) {
+      gate = reinterpret_cast<float*>(rect + (int64_t)id * ChunkRecT<T>::kBytes + ChunkRecT<T>::kGate);
+      gate[lane] = up;
+      gate[64 + lane] = left;
+    }
+  }
+
+  // rows of this wave's block against all blocks up to it
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) kk[t] = qk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const __amdgpu_buffer_rsrc_t rk =
+      make_rsrc((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t, (uint64_t)kOOB);
+  const __amdgpu_buffer_rsrc_t rq =
+      make_rsrc((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t, (uint64_t)kOOB);
+  const unsigned row_bytes = p.dk * sizeof(T), kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T);
+  for (int s = 0; s * KB < p.dk; ++s) {
+    const unsigned byte = s * 64 + g * 16;
+    const int r = w * 16 + m;
+    const u32x4 fq =
+        __builtin_amdgcn_raw_buffer_load_b128(rq, r < c.len && byte < row_bytes ? r * qp + byte : kOOB, 0, 0);
+    u32x4 fk[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (t <= w) {
+        const int j = t * 16 + m;
+        fk[t] = __builtin_amdgcn_raw_buffer_load_b128(rk, j < c.len && byte < row_bytes ? j * kp + byte : kOOB, 0, 0);
+      }
+    u32x4 mine = fk[0];
+#pragma unroll
+    for (int t = 1; t < 4; ++t)
+      if (t == w) mine = fk[t];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (t <= w) {
+        kk[t] = Mat<T>::mma(mine, fk[t], kk[t]);
+        qk[t] = Mat<T>::mma(fq, fk[t], qk[t]);
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (t > (w | 1)) continue;      // a block above the diagonal is zero where a fragment holds it too
+    const int j = t * 16 + m;
+    const float bj = beta[j];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = w * 16 + g * 4 + r;
+      const float d = i >= j ? __expf((float)(b[i] - b[j])) * bj : 0.f;
+      A[i * kLd + j] = i > j ? kk[t][r] * d : 0.f;
+      X[i * kLd + j] = i >= j ? p.scale * qk[t][r] * d : 0.f;
+    }
+  }
+  __syncthreads();
+  // P to memory in operand order
+  char* outt = rect + (int64_t)id * ChunkRecT<T>::kBytes;
+  if (BACK)
+    put_triangle<T, true, true>(X, outt + ChunkRecT<T>::kP, outt + ChunkRecT<T>::kPl);
+  else
+    put_triangle<T, false, false>(X, out + ChunkRec<T>::kP, nullptr);
+  // the diagonal block's inverse: lane m has column m; x_i = [i = m] - sum_{l < i} A_il x_l
+  float x[16];
+  {
+    const float* a = A + (w * 16) * kLd + w * 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == m ? 1.f : 0.f;
+#pragma unroll
+      for (int l = 0; l < i; ++l) v -= a[i * kLd + l] * x[l];
+      x[i] = v;
+    }
+  }
+  __syncthreads();                // P has left X
+  if (g == 0)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) X[(w * 16 + i) * kLd + w * 16 + m] = x[i];
+  if ((w & 1) == 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) X[(w * 16 + g * 4 + i) * kLd + w * 16 + 16 + m] = 0.f;
+  __syncthreads();
+  f32x4 col[4];                   // blocks T_lj of this wave's column j = w, rows g * 4 + r
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    if (w != j) continue;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) col[j][r] = X[(j * 16 + g * 4 + r) * kLd + j * 16 + m];
+#pragma unroll
+    for (int i = j + 1; i < 4; ++i) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int l = j; l < i; ++l) acc = mma_f32(A + (i * 16 + m) * kLd + l * 16 + g * 4, col[l], acc);
+      acc = -acc;
+      col[i] = mma_f32(X + (i * 16 + m) * kLd + i * 16 + g * 4, acc, (f32x4){0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int r = 0; r < 4; ++r) X[(i * 16 + g * 4 + r) * kLd + j * 16 + m] = col[i][r];
+    }
+  }
+  __syncthreads();
+  put_triangle<T, false, true>(X, out, out + ChunkRec<T>::kTl);
+  if (BACK) put_triangle<T, true, true>(X, outt, outt + ChunkRecT<T>::kTl);
+}
+
+// ------------------------------------------------------------------ the walk over the chunks
+
+// Fragments of one wave's 16 state columns to memory as rows of W [dv, dk].
+template <typename T, int SS>
+__device__ __forceinline__ void put_state(const u32x4 (&S)[SS], T* W, int dk, bool in) {
+  const int g = lane_id() >> 4;
+#pragma unroll
+  for (int s = 0; s < SS; ++s) {
+    const int d = s * Mat<T>::KB + g * (16 / (int)sizeof(T));
+    if (in && d < dk) *reinterpret_cast<u32x4*>(W + d) = S[s];
+  }
+}
+
+// A workgroup walks one sequence of one value head with NW state waves, each
+// keeping 16 columns of the state (dv), which need nothing of the others.
+// A state wave's chunk is a chain of dependent products (K S, T R, K^T E), so
+// everything that can leave it has left it: with OUT as many helper waves, one
+// chunk behind, make O from the state and the errors that the state waves left
+// in LDS, their Q and P coming straight from memory a chunk ahead.  K, the
+// chunk's record and the group's columns of V are brought to LDS by DMA while
+// the chunk before is worked on (STAGES = 2; the widest heads have room for one
+// stage only).  One barrier a chunk.  Without OUT (the backward's recompute)
+// the states before each chunk and the errors go to memory instead.
+template <typename T, int DK, int NW, int STAGES, bool OUT> struct Walk {
+  static constexpr int SS = DK / Mat<T>::KB;
+  static constexpr int kK = 0, kRec = Panels<T>::bytes(DK), kV = kRec + ChunkRec<T>::kP;
+  static constexpr int kStage = kV + Columns<T, NW>::kBytes;
+  static constexpr int kSwap = SS * 1024 + 4096;           // a state wave's state operands and errors (fp32)
+  static constexpr int kSmem = STAGES * kStage + (OUT ? 2 * NW * kSwap : 0);
+  static constexpr int kThreads = 64 * NW * (OUT ? 2 : 1);
+};
+
+template <typename T, int DK, int NW, int STAGES, bool OUT>
+__device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec, void* states, void* errors, int part,
+                                            int h, int seq, const SeqPlace& sp, char* smem) {
+  using M = Mat<T>;
+  using G = Walk<T, DK, NW, STAGES, OUT>;
+  constexpr int ST = DK / 16, SS = G::SS, CS = kDC / M::KB;   // state blocks, steps over dk, steps over the tokens
+  const int w = wave_id() % NW, lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int first = part * NW * 16, col = first + w * 16 + m;
+  const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
+  const unsigned kp = p.sk.t * sizeof(T), vp = p.sv.t * sizeof(T), krow = p.dk * sizeof(T);
+  const T* k0 = (const T*)p.k + sp.b * p.sk.b + kh * p.sk.h + sp.tok0 * p.sk.t;
+  const T* v0 = (const T*)p.v + sp.b * p.sv.b + h * p.sv.h + sp.tok0 * p.sv.t + first;
+  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes;
+  const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
+
+  auto fetch = [&](int c) {
+    char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
+    const int len = min(kDC, sp.len - c * kDC);
+    Panels<T>::template load<DK, NW>(rows_rsrc(k0 + (int64_t)c * kDC * p.sk.t), len, kp, krow, st + G::kK);
+    load_block<ChunkRec<T>::kP / 1024, NW>(make_rsrc(rec0 + c * rstep, ChunkRec<T>::kP), st + G::kRec);
+    Columns<T, NW>::load(rows_rsrc(v0 + (int64_t)c * kDC * p.sv.t), len, vp, p.dv - first, st + G::kV);
+  };
+  if (STAGES == 2 && chunks > 0) fetch(0);
+  // state block t, register r: dk = row(t, 4 g + r), dv = col
+  f32x4 S[ST];
+  const int64_t wbase = (((int64_t)seq * p.Hv + h) * p.dv + col) * p.dk;
+#pragma unroll
+  for (int t = 0; t < ST; ++t) {
+    const int d = M::row(t, g * 4);
+    S[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if (p.W_init && d < p.dk && col < p.dv) S[t] = *reinterpret_cast<const f32x4*>(p.W_init + wbase + d);
+  }
+
+  for (int c = 0; c < chunks; ++c) {
+    const char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
+    if (STAGES == 1) {
+      if (c > 0) __syncthreads();                    // the stage has been read
+      fetch(c);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);              // vmcnt(0): this chunk's loads
+    __syncthreads();
+    if (STAGES == 2 && c + 1 < chunks) fetch(c + 1);
+    const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRec<T>::kGate);
+    char* swap = smem + STAGES * G::kStage + ((c & 1) * NW + w) * G::kSwap + lane * 16;
+
+    u32x4 Sh[SS], Sl[SS];
+#pragma unroll
+    for (int s = 0; s < SS; ++s) M::split(S + s * M::TPS, Sh[s], Sl[s]);
+    const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
+    if constexpr (OUT) {
+#pragma unroll
+      for (int s = 0; s < SS; ++s) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
+    } else {
+      put_state<T, SS>(Sh, (T*)states + (slot * p.dv + col) * p.dk, p.dk, col < p.dv);
+    }
+    // V - exp(b) K S
+    f32x4 e[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      const int r = M::row(t, m);
+#pragma unroll
+      for (int s = 0; s < SS; ++s) acc = mma_split<T>(Panels<T>::frag(st + G::kK, r, s, g), Sh[s], Sl[s], acc);
+      e[t] = Columns<T, NW>::read(st + G::kV, w, t, lane) -
+             *reinterpret_cast<const f32x4*>(gate + M::row(t, g * 4)) * acc;
+    }
+    u32x4 Rh[CS], Rl[CS];
+#pragma unroll
+    for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Rh[s], Rl[s]);
+    // E = T (V - exp(b) K S)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < M::steps(t); ++s) {
+        const char* f = st + G::kRec + M::tri(t, s) * 1024 + lane * 16;
+        const u32x4 th = *reinterpret_cast<const u32x4*>(f);
+        const u32x4 tl = M::kSplit ? *reinterpret_cast<const u32x4*>(f + ChunkRec<T>::kTl) : th;
+        acc = mma_split2<T>(th, tl, Rh[s], Rl[s], acc);
+      }
+      e[t] = acc;
+      if constexpr (OUT) *reinterpret_cast<f32x4*>(swap + SS * 1024 + t * 1024) = acc;
+    }
+    if constexpr (!OUT) {
+      T* E = (T*)errors + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
+#pragma unroll
+      for (int s = 0; s < CS; ++s)
+        if (col < p.dv) *reinterpret_cast<u32x4*>(E + s * M::KB) = M::frag(e + s * M::TPS);
+    }
+    // S = exp(b_63) S + K^T (exp(b_63 - b) beta E)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) e[t] *= *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
+#pragma unroll
+    for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Rh[s], Rl[s]);
+    const float decay = gate[63];
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      S[t] *= decay;
+#pragma unroll
+      for (int s = 0; s < CS; ++s) S[t] = mma_split<T>(Panels<T>::frag_t(st + G::kK, t, s, lane), Rh[s], Rl[s], S[t]);
+    }
+  }
+  if (OUT && chunks > 0) {
+    if (STAGES == 1) __syncthreads();
+    __syncthreads();                                 // the helpers' last turn
+  }
+  if (p.W_final) {
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      const int d = M::row(t, g * 4);
+      if (d < p.dk && col < p.dv) *reinterpret_cast<f32x4*>(p.W_final + wbase + d) = S[t];
+    }
+  }
+}
+
+// The helpers' side: O of chunk c while the state waves are at chunk c + 1.
+template <typename T, int DK, int NW, int STAGES>
+__device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec, int part, int h, const SeqPlace& sp,
+                                             const char* smem) {
+  using M = Mat<T>;
+  using G = Walk<T, DK, NW, STAGES, true>;
+  constexpr int SS = G::SS, CS = kDC / M::KB;
+  constexpr bool AHEAD = SS <= 8;                    // Q a chunk ahead in registers, where it leaves room
+  const int w = wave_id() % NW, lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int col0 = (part * NW + w) * 16 + g * 4;
+  const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
+  const unsigned qp = p.sq.t * sizeof(T), qrow = p.dk * sizeof(T);
+  const T* q0 = (const T*)p.q + sp.b * p.sq.b + kh * p.sq.h + sp.tok0 * p.sq.t;
+  T* o0 = (T*)p.O + sp.b * p.so.b + h * p.so.h + sp.tok0 * p.so.t + col0;
+  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes;
+  const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
+  u32x4 Q[AHEAD ? 4 : 1][SS], P[M::kTri];
+  float ga[4];
+  auto fetch_q = [&](int c, int t, u32x4 (&q)[SS]) {
+    const int len = min(kDC, sp.len - c * kDC), r = M::row(t, m);
+    const __amdgpu_buffer_rsrc_t rq = rows_rsrc(q0 + (int64_t)c * kDC * p.sq.t);
+#pragma unroll
+    for (int s = 0; s < SS; ++s) {
+      const unsigned byte = s * 64u + g * 16u;
+      q[s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
+    }
+  };
+  auto fetch = [&](int c) {
+    if constexpr (AHEAD)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) fetch_q(c, t, Q[t]);
+    const char* r = rec0 + c * rstep;
+#pragma unroll
+    for (int f = 0; f < M::kTri; ++f) P[f] = *reinterpret_cast<const u32x4*>(r + ChunkRec<T>::kP + f * 1024 + lane * 16);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      ga[t] = reinterpret_cast<const float*>(r + ChunkRec<T>::kGate)[M::row(t, m)];
+  };
+  if (chunks > 0) fetch(0);
+  for (int c = 0; c <= chunks; ++c) {
+    if (STAGES == 1 && c > 0) __syncthreads();
+    __syncthreads();
+    if (c == 0) continue;
+    const int d = c - 1, len = min(kDC, sp.len - d * kDC);     // the chunk whose O is made
+    const char* swap = smem + STAGES * G::kStage + ((d & 1) * NW + w) * G::kSwap + lane * 16;
+    u32x4 Eh[CS], El[CS];
+#pragma unroll
+    for (int s = 0; s < CS; ++s) {
+      f32x4 e[M::TPS];
+#pragma unroll
+      for (int t = 0; t < M::TPS; ++t)
+        e[t] = *reinterpret_cast<const f32x4*>(swap + SS * 1024 + (s * M::TPS + t) * 1024);
+      M::split(e, Eh[s], El[s]);
+    }
+    u32x4 Sh[SS];
+#pragma unroll
+    for (int s = 0; s < SS; ++s) Sh[s] = *reinterpret_cast<const u32x4*>(swap + s * 1024);
+    // the state's columns in the instruction's rows, tokens in its columns: a lane gets 4 columns of one token
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (!AHEAD) fetch_q(d, t, Q[0]);
+      const int r = M::row(t, m);
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < SS; ++s) o = M::mma(Sh[s], Q[AHEAD ? t : 0][s], o);
+      o *= p.scale * ga[t];
+#pragma unroll
+      for (int s = 0; s < M::steps(t); ++s) {
+        o = M::mma(Eh[s], P[M::tri(t, s)], o);
+        if (M::kSplit) o = M::mma(El[s], P[M::tri(t, s)], o);
+      }
+      if (r < len && col0 < p.dv) store4(o0 + (int64_t)(d * kDC + r) * p.so.t, o[0], o[1], o[2], o[3]);
+    }
+    if (c < chunks) fetch(c);
+  }
+}
+
+}  // namespace
+}  // namespace ttt
