@@ -11,7 +11,7 @@ Functions keep the C names:
   ttt_core_backward_mse, ttt_layer_backward, ttt_layer_backward_mse, ttt_produce_z,
   ttt_produce_vhat, ttt_chunk_delta, ttt_chunk_scan, ttt_chunk_update_scan,
   ttt_chunk_apply, ttt_lact_swiglu, ttt_lact_swiglu_backward (and its _ex form), ttt_gated_delta,
-  ttt_gated_delta_step, ttt_layer_norm, ttt_layer_norm_backward, plus the workspace queries.
+  ttt_gated_delta_backward, ttt_gated_delta_step, ttt_layer_norm, ttt_layer_norm_backward, plus the workspace queries.
 """
 from ._lib import (  # noqa: F401
     TTT_OK, TTT_ERR_ARG, TTT_ERR_SHAPE, TTT_ERR_DTYPE, TTT_ERR_WORKSPACE, TTT_ERR_DEVICE,
@@ -27,7 +27,8 @@ from ._lib import (  # noqa: F401
     ttt_chunk_apply_update, ttt_chunk_apply_update_noalloc, ttt_core_apply_update, ttt_produce_z, ttt_produce_vhat,
     ttt_chunk_delta, ttt_chunk_scan, ttt_chunk_update_scan, ttt_chunk_apply, ttt_lact_swiglu,
     ttt_lact_backward_workspace_bytes, ttt_lact_swiglu_backward,
-    DeltaShape, DeltaStepShape, DeltaStrides, DeltaLayout, DeltaOptions,
+    DeltaShape, DeltaStepShape, DeltaStrides, DeltaLayout, DeltaGradLayout, DeltaOptions,
     ttt_gated_delta_workspace_bytes, ttt_gated_delta, ttt_gated_delta_step,
+    ttt_gated_delta_backward_workspace_bytes, ttt_gated_delta_backward,
     ttt_layer_norm, ttt_layer_norm_backward_workspace_bytes, ttt_layer_norm_backward,
 )

@@ -89,6 +89,10 @@ class DeltaLayout(ctypes.Structure):
     _fields_ = [(n, DeltaStrides) for n in ("q", "k", "v", "g", "beta", "O")]
 
 
+class DeltaGradLayout(ctypes.Structure):
+    _fields_ = [(n, DeltaStrides) for n in ("dO", "dq", "dk", "dv", "dg", "dbeta")]
+
+
 class DeltaOptions(ctypes.Structure):
     _fields_ = [("W_init", ctypes.c_void_p), ("seq_starts", ctypes.c_void_p), ("num_seqs", ctypes.c_int64),
                 ("layout", ctypes.POINTER(DeltaLayout))]
@@ -150,6 +154,10 @@ _SIGNATURES = {
     "ttt_gated_delta_workspace_bytes": (_I, [ctypes.POINTER(DeltaShape), _I, ctypes.c_int64, ctypes.POINTER(_S)]),
     "ttt_gated_delta": (_I, [ctypes.POINTER(DeltaShape), _I, _F] + [_P] * 5 + [ctypes.POINTER(DeltaOptions)] +
                         [_P] * 3 + [_S, _P]),
+    "ttt_gated_delta_backward_workspace_bytes": (_I, [ctypes.POINTER(DeltaShape), _I, ctypes.c_int64,
+                                                      ctypes.POINTER(_S)]),
+    "ttt_gated_delta_backward": (_I, [ctypes.POINTER(DeltaShape), _I, _F] + [_P] * 7 +
+                                 [ctypes.POINTER(DeltaOptions), ctypes.POINTER(DeltaGradLayout)] + [_P] * 7 + [_S, _P]),
     "ttt_gated_delta_step": (_I, [ctypes.POINTER(DeltaStepShape), _I, _F] + [_P] * 9),
     "ttt_layer_norm": (_I, [ctypes.c_int64, ctypes.c_int64, _I, _F] + [_P] * 7),
     "ttt_layer_norm_backward_workspace_bytes": (_I, [ctypes.c_int64, ctypes.c_int64, _I, ctypes.POINTER(_S)]),
@@ -833,6 +841,22 @@ def ttt_gated_delta_workspace_bytes(shape: DeltaShape, dtype: torch.dtype, num_s
     return out.value
 
 
+def _delta_inputs(q, k, v, g, beta, W_init, seq_starts):
+    """What the forward and the backward call check alike: (DeltaShape, sequences' rows, packed count or -1, strides of
+    q, k, v, g, beta)."""
+    B, Hk, n, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[3]
+    dt, dev = q.dtype, q.device
+    strides = (_strided(q, "q", (B, Hk, n, dk), dt, dev), _strided(k, "k", (B, Hk, n, dk), dt, dev),
+               _strided(v, "v", (B, Hv, n, dv), dt, dev), _strided(g, "g", (B, Hv, n), torch.float32, dev, rows=False),
+               _strided(beta, "beta", (B, Hv, n), torch.float32, dev, rows=False))
+    num = _seq_starts(seq_starts, B, dev)
+    rows = B if num < 0 else num
+    if W_init is not None:
+        _need(W_init, "W_init", (rows, Hv, dv, dk), torch.float32, dev)
+    return DeltaShape(B, n, Hk, Hv, dk, dv), rows, num, strides
+
+
 def ttt_gated_delta(q, k, v, g, beta, scale=None, W_init=None, seq_starts=None, O=None, W_final=None,
                     workspace=None):
     """The gated delta rule over whole sequences: per value head W_t = exp(g_t) W_{t-1} + beta_t (v_t -
@@ -845,32 +869,66 @@ def ttt_gated_delta(q, k, v, g, beta, scale=None, W_init=None, seq_starts=None, 
     W_init [sequences, Hv, dv, dk] fp32: the states to start from (zero if None).  seq_starts, an int32 device
     tensor [sequences + 1]: packed sequences of any lengths in one batch row; tokens behind the last of them are
     not read and their rows of O are left as they are."""
-    B, Hk, n, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[3]
+    shape, rows, num, strides = _delta_inputs(q, k, v, g, beta, W_init, seq_starts)
+    B, n, Hv, dk, dv = shape.batch, shape.seq_len, shape.v_heads, shape.k_dim, shape.v_dim
     dt, dev = q.dtype, q.device
-    sq = _strided(q, "q", (B, Hk, n, dk), dt, dev)
-    sk = _strided(k, "k", (B, Hk, n, dk), dt, dev)
-    sv = _strided(v, "v", (B, Hv, n, dv), dt, dev)
-    sg = _strided(g, "g", (B, Hv, n), torch.float32, dev, rows=False)
-    sb = _strided(beta, "beta", (B, Hv, n), torch.float32, dev, rows=False)
-    num = _seq_starts(seq_starts, B, dev)
-    rows = B if num < 0 else num
-    if W_init is not None:
-        _need(W_init, "W_init", (rows, Hv, dv, dk), torch.float32, dev)
     O = torch.empty_like(v) if O is None else O
     so = _strided(O, "O", (B, Hv, n, dv), dt, dev, out=True)
     W_final = torch.empty(rows, Hv, dv, dk, dtype=torch.float32, device=dev) if W_final is None else W_final
     _need(W_final, "W_final", (rows, Hv, dv, dk), torch.float32, dev)
-    shape = DeltaShape(B, n, Hk, Hv, dk, dv)
     nbytes = ttt_gated_delta_workspace_bytes(shape, dt, num)
     ws = _workspace(nbytes, dev, workspace)
-    layout = DeltaLayout(sq, sk, sv, sg, sb, so)
+    layout = DeltaLayout(*strides, so)
     opts = DeltaOptions(_vp(W_init), _vp(seq_starts), max(num, 0), ctypes.pointer(layout))
     with _on(dev):
         _check(lib().ttt_gated_delta(ctypes.byref(shape), _dt(dt), dk ** -0.5 if scale is None else float(scale),
                                      _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), ctypes.byref(opts), _vp(O),
                                      _vp(W_final), _vp(ws), nbytes, _stream(dev)), "ttt_gated_delta")
     return O, W_final
+
+
+def ttt_gated_delta_backward_workspace_bytes(shape: DeltaShape, dtype: torch.dtype, num_seqs: int = -1) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_gated_delta_backward_workspace_bytes(ctypes.byref(shape), _dt(dtype), int(num_seqs),
+                                                          ctypes.byref(out)),
+           "ttt_gated_delta_backward_workspace_bytes")
+    return out.value
+
+
+def ttt_gated_delta_backward(q, k, v, g, beta, dO, dW_final=None, scale=None, W_init=None, seq_starts=None, dq=None,
+                             dk=None, dv=None, dg=None, dbeta=None, dW_init=None, workspace=None):
+    """Backward of ttt_gated_delta from its inputs (the states are made again), dO = dLoss/dO [B, Hv, n, dv] and, where
+    the loss depends on the final states too, dW_final [sequences, Hv, dv, dk] fp32.  Returns (dq, dk, dv, dg, dbeta)
+    in q's dtype, each laid out like its input if not given, and dW_init [sequences, Hv, dv, dk] fp32 (None without
+    W_init, unless given).  dO and the gradients may have any strides that the inputs may; rows of tokens that belong
+    to no sequence are left as they are."""
+    shape, rows, num, strides = _delta_inputs(q, k, v, g, beta, W_init, seq_starts)
+    B, n, Hk, Hv, ek, ev = shape.batch, shape.seq_len, shape.k_heads, shape.v_heads, shape.k_dim, shape.v_dim
+    dt, dev = q.dtype, q.device
+    dq, dk, dv = (torch.empty_like(x) if t is None else t for t, x in ((dq, q), (dk, k), (dv, v)))
+    dg, dbeta = (torch.empty_like(x, dtype=dt) if t is None else t for t, x in ((dg, g), (dbeta, beta)))
+    grad_strides = [_strided(dO, "dO", (B, Hv, n, ev), dt, dev)]
+    grad_strides += [_strided(t, name, shp, dt, dev, out=True) for t, name, shp in (
+        (dq, "dq", (B, Hk, n, ek)), (dk, "dk", (B, Hk, n, ek)), (dv, "dv", (B, Hv, n, ev)))]
+    grad_strides += [_strided(t, name, (B, Hv, n), dt, dev, rows=False, out=True)
+                     for t, name in ((dg, "dg"), (dbeta, "dbeta"))]
+    if W_init is not None and dW_init is None:
+        dW_init = torch.empty_like(W_init)
+    for t, name in ((dW_final, "dW_final"), (dW_init, "dW_init")):
+        if t is not None:
+            _need(t, name, (rows, Hv, ev, ek), torch.float32, dev)
+    nbytes = ttt_gated_delta_backward_workspace_bytes(shape, dt, num)
+    ws = _workspace(nbytes, dev, workspace)
+    layout = DeltaLayout(*strides, DeltaStrides())
+    opts = DeltaOptions(_vp(W_init), _vp(seq_starts), max(num, 0), ctypes.pointer(layout))
+    grad_layout = DeltaGradLayout(*grad_strides)
+    with _on(dev):
+        _check(lib().ttt_gated_delta_backward(ctypes.byref(shape), _dt(dt), ek ** -0.5 if scale is None else float(scale),
+                                              _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), _vp(dO), _vp(dW_final),
+                                              ctypes.byref(opts), ctypes.byref(grad_layout), _vp(dq), _vp(dk), _vp(dv),
+                                              _vp(dg), _vp(dbeta), _vp(dW_init), _vp(ws), nbytes, _stream(dev)),
+               "ttt_gated_delta_backward")
+    return dq, dk, dv, dg, dbeta, dW_init
 
 
 def ttt_gated_delta_step(q, k, v, g, beta, W, slots=None, scale=None, O=None):

@@ -14,8 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libttt.so")
-SOURCES = ["inplace.hip", "lact.hip", "lact_bwd.hip", "delta.hip", "delta_step.hip", "norm.hip", "api.cpp",
-           "api_delta.cpp"]
+SOURCES = ["inplace.hip", "lact.hip", "lact_bwd.hip", "delta.hip", "delta_bwd.hip", "delta_step.hip", "norm.hip",
+           "api.cpp", "api_delta.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

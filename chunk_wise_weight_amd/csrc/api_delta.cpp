@@ -152,6 +152,52 @@ int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const 
   return dev(dtype == TTT_BF16 ? ttt::launch_delta<bf16>(a, s) : ttt::launch_delta<float>(a, s));
 }
 
+int ttt_gated_delta_backward_workspace_bytes(const ttt_delta_shape* shape, int dtype, int64_t num_seqs,
+                                             size_t* bytes) {
+  if (bytes == nullptr) return TTT_ERR_ARG;
+  if (int st = check_delta(shape, dtype, num_seqs)) return st;
+  const ttt::DeltaArgs a = sizes(shape, num_seqs);
+  *bytes = dtype == TTT_BF16 ? ttt::delta_grad_workspace_bytes<bf16>(a) : ttt::delta_grad_workspace_bytes<float>(a);
+  return TTT_OK;
+}
+
+int ttt_gated_delta_backward(const ttt_delta_shape* shape, int dtype, float scale, const void* q, const void* k,
+                             const void* v, const float* g, const float* beta, const void* dO, const float* dW_final,
+                             const ttt_delta_options* options, const ttt_delta_grad_layout* grad_layout, void* dq,
+                             void* dk, void* dv, void* dg, void* dbeta, float* dW_init, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  ttt::DeltaGradArgs a{};
+  if (int st = take_inputs(shape, dtype, scale, q, k, v, g, beta, options, &a.f)) return st;
+  const int64_t num = a.f.seqs.starts ? a.f.seqs.num : -1;
+  const ttt_delta_grad_layout* l = grad_layout;
+  const int64_t n = shape->seq_len, u = 16 / esize(dtype), Hk = shape->k_heads, Hv = shape->v_heads;
+  if (!take_strides(l ? &l->dO : nullptr, Hv, n, shape->v_dim, u, &a.sdo) ||
+      !take_strides(l ? &l->dq : nullptr, Hk, n, shape->k_dim, u, &a.sdq) ||
+      !take_strides(l ? &l->dk : nullptr, Hk, n, shape->k_dim, u, &a.sdk) ||
+      !take_strides(l ? &l->dv : nullptr, Hv, n, shape->v_dim, u, &a.sdv) ||
+      !take_strides(l ? &l->dg : nullptr, Hv, n, 1, 1, &a.sdg) ||
+      !take_strides(l ? &l->dbeta : nullptr, Hv, n, 1, 1, &a.sdbeta))
+    return TTT_ERR_ARG;
+  if (shape->batch * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, esize(dtype)) ||
+                               !ok_ptr(dbeta, esize(dtype))))
+    return TTT_ERR_ARG;
+  if (!aligned(dW_final, 16) || !aligned(dW_init, 16)) return TTT_ERR_ARG;
+  size_t need = 0;
+  if (int st = ttt_gated_delta_backward_workspace_bytes(shape, dtype, num, &need)) return st;
+  if (need > 0 && (!ok_ptr(workspace) || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
+  a.f.ws = (char*)workspace;
+  a.dO = dO;
+  a.dW_final = dW_final;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.dW_init = dW_init;
+  hipStream_t s = (hipStream_t)stream;
+  return dev(dtype == TTT_BF16 ? ttt::launch_delta_grad<bf16>(a, s) : ttt::launch_delta_grad<float>(a, s));
+}
+
 int ttt_gated_delta_step(const ttt_delta_step_shape* shape, int dtype, float scale, const void* q, const void* k,
                          const void* v, const float* g, const float* beta, float* W, const int32_t* slots, void* O,
                          void* stream) {

@@ -135,26 +135,27 @@ template <typename T> struct ChunkRecT {
   static constexpr int kBytes = kGate + 1024;
 };
 
-// 64 rows of up to DK elements in LDS: panels of 128 bytes a row, the 16-byte
+// R (64) rows of up to DK elements in LDS: panels of 128 bytes a row, the 16-byte
 // chunk c of row r in slot c ^ panel_swz(r).  The 16 rows of an operand read
 // (Mat::row: rows 0-3, 8-11, 16-19, 24-27 of a step, or the other four of each
 // eight) differ in row & 1 and the three bits used here, so they fall into 16
 // different 16-byte bank groups.
 __device__ __forceinline__ int panel_swz(int r) { return ((r >> 1) & 1) | (((r >> 3) & 3) << 1); }
-template <typename T> struct Panels {
-  static constexpr int bytes(int DK) { return DK * (int)sizeof(T) * kDC; }
+template <typename T, int R = kDC> struct Panels {
+  static constexpr int kPanel = R * 128;
+  static constexpr int bytes(int DK) { return DK * (int)sizeof(T) * R; }
   // 16 bytes of row r at contraction step s, lane group g
   __device__ static __forceinline__ u32x4 frag(const char* t, int r, int s, int g) {
-    return *reinterpret_cast<const u32x4*>(t + (s >> 1) * 8192 + r * 128 + (((4 * (s & 1) + g) ^ panel_swz(r)) << 4));
+    return *reinterpret_cast<const u32x4*>(t + (s >> 1) * kPanel + r * 128 + (((4 * (s & 1) + g) ^ panel_swz(r)) << 4));
   }
-  // The transpose's operand: row = column Mat::row(tile, lane & 15), contraction over the 64 rows, step s.
+  // The transpose's operand: row = column Mat::row(tile, lane & 15), contraction over the rows, step s.
   __device__ static __forceinline__ u32x4 frag_t(const char* t, int tile, int s, int lane) {
     const int j = lane & 15, g = lane >> 4;
     if constexpr (sizeof(T) == 2) {
       // ds_read_b64_tr_b16: lane j of a 16-lane group addresses 4 columns of row j >> 2 and receives
       // column j of the 16 addressed, rows 0..3
       const int col = ((tile >> 1) << 5) + ((j & 3) << 3), r = s * 32 + g * 8 + (j >> 2);
-      const char* p = t + (col >> 6) * 8192 + ((tile & 1) << 3);
+      const char* p = t + (col >> 6) * kPanel + ((tile & 1) << 3);
       const int c = (col & 63) >> 3;
       const s16x4 x = lds_read_tr16(p + r * 128 + ((c ^ panel_swz(r)) << 4));
       const s16x4 y = lds_read_tr16(p + (r + 4) * 128 + ((c ^ panel_swz(r + 4)) << 4));
@@ -166,24 +167,29 @@ template <typename T> struct Panels {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = s * 16 + g * 4 + i;
-        o[i] = *reinterpret_cast<const unsigned*>(t + (col >> 5) * 8192 + r * 128 + ((c ^ panel_swz(r)) << 4) +
+        o[i] = *reinterpret_cast<const unsigned*>(t + (col >> 5) * kPanel + r * 128 + ((c ^ panel_swz(r)) << 4) +
                                                   ((col & 3) << 2));
       }
       return o;
     }
   }
-  // DMA of all panels by NW waves, instruction i = rows 8 (i & 7) .. + 7 of panel i >> 3.  Rows >= len and columns
+  // place of element (r, col)
+  __device__ static __forceinline__ int at(int r, int col) {
+    const int byte = col * (int)sizeof(T);
+    return (byte >> 7) * kPanel + r * 128 + ((((byte & 127) >> 4) ^ panel_swz(r)) << 4) + (byte & 15);
+  }
+  // DMA of all panels by NW waves, 8 rows of a panel an instruction.  Rows >= len and columns
   // >= row_bytes read as zero: a whole chunk of full rows needs no test of either.
   template <int DK, int NW>
   __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int len, unsigned pitch, unsigned row_bytes,
                                               char* t) {
     constexpr int N = bytes(DK) / 1024;
     const int L = lane_id(), w = wave_id() % NW;
-    const bool full = len >= kDC && row_bytes == DK * sizeof(T);
+    const bool full = len >= R && row_bytes == DK * sizeof(T);
 #pragma unroll
     for (int j = 0; j < N / NW; ++j) {
-      const int i = j * NW + w, b = i & 7;
-      const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4), at = (unsigned)(i >> 3) * 128u;
+      const int i = j * NW + w, b = i % (R / 8);
+      const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4), at = (unsigned)(i / (R / 8)) * 128u;
       unsigned off = (unsigned)(L >> 3) * pitch + byte + ((unsigned)b * 8u * pitch + at);
       if (!full && ((L >> 3) >= len - b * 8 || byte + at >= row_bytes)) off = kOOB;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, off, 0, 0, 0);

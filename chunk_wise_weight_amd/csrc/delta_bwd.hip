@@ -1,0 +1,548 @@
+// The backward pass of the gated delta rule (gfx950).  Notation of delta.hpp;
+// dS' is the gradient of the state after a chunk.
+//
+// Within a chunk, with bE = beta E the step each token takes,
+//   dbE = P0^T dO + exp(b_63 - b) K dS'             (P = P0 diag(beta))
+//   X   = T^T (beta dbE)                            = dV, the residual's gradient
+//   dS  = exp(b_63) dS' + Q^T (scale exp(b) dO) - K^T (exp(b) X)
+// so a reverse walk over the chunks needs T^T, P^T and the gates alone, as the
+// forward one does, and the two walks do not need each other: one launch runs
+// both (the forward one to remake the states S before each chunk and the
+// errors E).  They leave S, dS', E and X in memory, and the rest is local to a
+// chunk (k_delta_grads):
+//   Mq_ij = scale D_ij beta_j (dO_i . E_j)   j <= i,  D_ij = exp(b_i - b_j)
+//   Mk_ij =      -D_ij beta_j (X_i . E_j)    j <  i
+//   dQ = scale exp(b) dO S^T + Mq K
+//   dK = Mq^T Q + (Mk + Mk^T) K - exp(b) X S^T + exp(b_63 - b) beta E dS'^T
+//   dbeta_j = (sum_i Mq_ij q_i.k_j + Mk_ij k_i.k_j) / beta_j + exp(b_63 - b_j) k_j.(dS'^T E_j)
+//   db_i = q_i.dQ_i - k_i.dK_i in its parts, + exp(b_63) <S, dS'> and the
+//          tokens' parts through exp(b_63) at the chunk's end; dg = suffix sums of db
+// (the division is by a factor of the summands, which are taken without it).
+// Gradients of a key head sum over its value heads, one after the other in one
+// workgroup: no atomics.
+#include "delta_walk.hpp"
+
+namespace ttt {
+namespace {
+
+// ------------------------------------------------------------------ the reverse walk
+
+template <typename T, int DK, int NW, int STAGES> struct WalkBack {
+  static constexpr int SS = DK / Mat<T>::KB;
+  static constexpr int kK = 0, kQ = Panels<T>::bytes(DK), kRec = 2 * kQ, kD = kRec + ChunkRecT<T>::kBytes;
+  static constexpr int kStage = kD + Columns<T, NW>::kBytes;
+  static constexpr int kSmem = STAGES * kStage;
+};
+
+template <typename T, int DK, int NW, int STAGES>
+__device__ __forceinline__ void walk_back(const DeltaGradArgs& a, const char* rec, void* dstates, void* xs, int part,
+                                          int h, int seq, const SeqPlace& sp, char* smem) {
+  using M = Mat<T>;
+  using G = WalkBack<T, DK, NW, STAGES>;
+  const DeltaArgs& p = a.f;
+  constexpr int ST = DK / 16, SS = G::SS, CS = kDC / M::KB;
+  const int w = wave_id() % NW, lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int first = part * NW * 16, col = first + w * 16 + m;
+  const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
+  const unsigned kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T), dp = a.sdo.t * sizeof(T), row = p.dk * sizeof(T);
+  const T* k0 = (const T*)p.k + sp.b * p.sk.b + kh * p.sk.h + sp.tok0 * p.sk.t;
+  const T* q0 = (const T*)p.q + sp.b * p.sq.b + kh * p.sq.h + sp.tok0 * p.sq.t;
+  const T* d0 = (const T*)a.dO + sp.b * a.sdo.b + h * a.sdo.h + sp.tok0 * a.sdo.t + first;
+  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRecT<T>::kBytes;
+  const int64_t rstep = (int64_t)p.Hv * ChunkRecT<T>::kBytes;
+
+  auto fetch = [&](int c) {
+    char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
+    const int len = min(kDC, sp.len - c * kDC);
+    Panels<T>::template load<DK, NW>(rows_rsrc(k0 + (int64_t)c * kDC * p.sk.t), len, kp, row, st + G::kK);
+    Panels<T>::template load<DK, NW>(rows_rsrc(q0 + (int64_t)c * kDC * p.sq.t), len, qp, row, st + G::kQ);
+    load_block<ChunkRecT<T>::kBytes / 1024, NW>(make_rsrc(rec0 + c * rstep, ChunkRecT<T>::kBytes), st + G::kRec);
+    Columns<T, NW>::load(rows_rsrc(d0 + (int64_t)c * kDC * a.sdo.t), len, dp, p.dv - first, st + G::kD);
+  };
+  if (STAGES == 2 && chunks > 0) fetch(chunks - 1);
+  f32x4 S[ST];                    // dS': block t, register r: dk = row(t, 4 g + r), dv = col
+  const int64_t wbase = (((int64_t)seq * p.Hv + h) * p.dv + col) * p.dk;
+#pragma unroll
+  for (int t = 0; t < ST; ++t) {
+    const int d = M::row(t, g * 4);
+    S[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if (a.dW_final && d < p.dk && col < p.dv) S[t] = *reinterpret_cast<const f32x4*>(a.dW_final + wbase + d);
+  }
+
+  for (int c = chunks - 1; c >= 0; --c) {
+    const char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
+    if (STAGES == 1) {
+      if (c < chunks - 1) __syncthreads();
+      fetch(c);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);              // vmcnt(0): this chunk's loads
+    __syncthreads();
+    if (STAGES == 2 && c > 0) fetch(c - 1);
+    const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRecT<T>::kGate);
+    const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
+    u32x4 Sh[SS], Sl[SS];
+#pragma unroll
+    for (int s = 0; s < SS; ++s) M::split(S + s * M::TPS, Sh[s], Sl[s]);
+    put_state<T, SS>(Sh, (T*)dstates + (slot * p.dv + col) * p.dk, p.dk, col < p.dv);
+    // beta dbE = P^T dO + beta exp(b_63 - b) K dS'
+    f32x4 d[4], x[4];
+    u32x4 D[CS], Rh[CS], Rl[CS];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) d[t] = Columns<T, NW>::read(st + G::kD, w, t, lane);
+#pragma unroll
+    for (int s = 0; s < CS; ++s) D[s] = M::frag(d + s * M::TPS);       // exact: dO is of type T
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      const int r = M::row(t, m);
+#pragma unroll
+      for (int s = 0; s < SS; ++s) acc = mma_split<T>(Panels<T>::frag(st + G::kK, r, s, g), Sh[s], Sl[s], acc);
+      acc *= *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
+#pragma unroll
+      for (int s = M::first(t); s < CS; ++s) {
+        const char* f = st + G::kRec + ChunkRecT<T>::kP + M::triu(t, s) * 1024 + lane * 16;
+        acc = M::mma(*reinterpret_cast<const u32x4*>(f), D[s], acc);
+        if (M::kSplit) acc = M::mma(*reinterpret_cast<const u32x4*>(f + ChunkRecT<T>::kFrag), D[s], acc);
+      }
+      x[t] = acc;
+    }
+#pragma unroll
+    for (int s = 0; s < CS; ++s) M::split(x + s * M::TPS, Rh[s], Rl[s]);
+    // X = T^T (beta dbE)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = M::first(t); s < CS; ++s) {
+        const char* f = st + G::kRec + M::triu(t, s) * 1024 + lane * 16;
+        const u32x4 th = *reinterpret_cast<const u32x4*>(f);
+        const u32x4 tl = M::kSplit ? *reinterpret_cast<const u32x4*>(f + ChunkRecT<T>::kTl) : th;
+        acc = mma_split2<T>(th, tl, Rh[s], Rl[s], acc);
+      }
+      x[t] = acc;
+    }
+    T* xo = (T*)xs + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
+#pragma unroll
+    for (int s = 0; s < CS; ++s)
+      if (col < p.dv) *reinterpret_cast<u32x4*>(xo + s * M::KB) = M::frag(x + s * M::TPS);
+    // dS = exp(b_63) dS' + Q^T (scale exp(b) dO) - K^T (exp(b) X)
+    u32x4 Dh[CS], Dl[CS];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const f32x4 up = *reinterpret_cast<const f32x4*>(gate + M::row(t, g * 4));
+      x[t] *= -up;
+      d[t] *= p.scale * up;
+    }
+#pragma unroll
+    for (int s = 0; s < CS; ++s) {
+      M::split(x + s * M::TPS, Rh[s], Rl[s]);
+      M::split(d + s * M::TPS, Dh[s], Dl[s]);
+    }
+    const float decay = gate[63];
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      S[t] *= decay;
+#pragma unroll
+      for (int s = 0; s < CS; ++s) {
+        S[t] = mma_split<T>(Panels<T>::frag_t(st + G::kQ, t, s, lane), Dh[s], Dl[s], S[t]);
+        S[t] = mma_split<T>(Panels<T>::frag_t(st + G::kK, t, s, lane), Rh[s], Rl[s], S[t]);
+      }
+    }
+  }
+  if (a.dW_init) {
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      const int d = M::row(t, g * 4);
+      if (d < p.dk && col < p.dv) *reinterpret_cast<f32x4*>(a.dW_init + wbase + d) = S[t];
+    }
+  }
+}
+
+// Both walks: the first half of the workgroups goes forward, the second back.
+template <typename T, int DK, int NW, int SF, int SB>
+__global__ __launch_bounds__(64 * NW) void k_delta_walks(DeltaGradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const DeltaArgs& p = a.f;
+  const int half = gridDim.x / 2, parts = (p.dv + 16 * NW - 1) / (16 * NW);
+  const bool back = (int)blockIdx.x >= half;
+  const int id = xcd_remap(back ? blockIdx.x - half : blockIdx.x, half);
+  const int part = id % parts, h = (id / parts) % p.Hv, seq = id / parts / p.Hv;
+  const SeqPlace sp = seq_place(p.seqs, seq);
+  if (back)
+    walk_back<T, DK, NW, SB>(a, a.rect, a.dstates, a.xs, part, h, seq, sp, smem);
+  else
+    walk_states<T, DK, NW, SF, false>(p, a.rec, a.states, a.errors, part, h, seq, sp, smem);
+}
+
+// ------------------------------------------------------------------ what is local to a chunk
+
+// One workgroup of 4 waves per chunk slot and key head; wave w makes the rows
+// of tokens row(w, .).  Every product has the tokens as the instruction's
+// columns and the features (dk, or the other token) as its rows, so that a
+// lane holds 4 consecutive features of one token.  dv goes by in blocks of 128
+// bytes: the block's rows of S and dS' ([dv, dk]) and of E and X ([dv, 64])
+// and the block of dO come to LDS; what is contracted over dv in them is read
+// transposed.
+template <typename T, int DK> struct Grads {
+  static constexpr int BV = 128 / (int)sizeof(T);            // columns of a dv block
+  using Rows = Panels<T, BV>;                                // its rows of S, dS', E, X
+  // Q and K take the place of S and dS' after the last block
+  static constexpr int kS = 0, kDS = Rows::bytes(DK), kQ = 0, kK = Panels<T>::bytes(DK);
+  static constexpr int kE = 2 * kK, kX = kE + Rows::bytes(kDC), kD = kX + Rows::bytes(kDC);
+  static constexpr int kSmem = kD + Panels<T>::bytes(BV);
+  // Mq and Mk take the place of E, X and dO: both at once, where there is room
+  static constexpr int kM = kE, kMBytes = Panels<T>::bytes(kDC);
+  static constexpr bool kBoth = kE + 2 * kMBytes <= kSmem;
+};
+
+template <typename T, int DK>
+__global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
+  using M = Mat<T>;
+  using G = Grads<T, DK>;
+  using Rows = typename G::Rows;
+  constexpr int ST = DK / 16, SS = DK / M::KB, CS = kDC / M::KB, E = 16 / (int)sizeof(T);
+  constexpr int VS = G::BV / M::KB;                          // steps over a dv block: 2
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  __shared__ double b[kDC];
+  __shared__ float beta[kDC], db[kDC], colsum[4][kDC], part[4];
+  const DeltaArgs& p = a.f;
+  const int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int kh = id % p.Hk, slot = id / p.Hk, group = p.Hv / p.Hk;
+  const ChunkPlace c = chunk_place(p.seqs, slot);
+  if (c.len <= 0) return;
+  const int w = wave_id(), lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int i = M::row(w, m);                                // this lane's token
+  const unsigned row = p.dk * sizeof(T);
+  f32x4 dq[ST], dk[ST];
+#pragma unroll
+  for (int t = 0; t < ST; ++t) dq[t] = dk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+
+  for (int h = kh * group; h < (kh + 1) * group; ++h) {
+    const int64_t sh = (int64_t)slot * p.Hv + h;
+    __syncthreads();                                         // the head before is done with LDS
+    if (w == 0) {
+      float gi = 0.f, bi = 0.f;
+      if (lane < c.len) {
+        gi = p.g[c.b * p.sg.b + h * p.sg.h + (c.tok0 + lane) * p.sg.t];
+        bi = p.beta[c.b * p.sbeta.b + h * p.sbeta.h + (c.tok0 + lane) * p.sbeta.t];
+      }
+      double s = gi < -200.f ? -200.0 : (double)gi;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const double up = __shfl_up(s, d, 64);
+        if (lane >= d) s += up;
+      }
+      b[lane] = s;
+      beta[lane] = bi;
+    }
+    f32x4 os[ST], xs[ST], es[ST];                            // S dO, S X, dS' E by token
+#pragma unroll
+    for (int t = 0; t < ST; ++t) os[t] = xs[t] = es[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    f32x4 oe[4], xe[4];                                      // E_j . dO_i, E_j . X_i: j = row(t, 4 g + r)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) oe[t] = xe[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    float ss = 0.f;                                          // <S, dS'>
+    for (int v0 = 0; v0 < p.dv; v0 += G::BV) {
+      if (v0 > 0) __syncthreads();
+      const int rows = min(G::BV, p.dv - v0);
+      const int64_t so = (sh * p.dv + v0) * p.dk, eo = (sh * p.dv + v0) * kDC;
+      Rows::template load<DK, 4>(rows_rsrc((const T*)a.states + so), rows, row, row, smem + G::kS);
+      Rows::template load<DK, 4>(rows_rsrc((const T*)a.dstates + so), rows, row, row, smem + G::kDS);
+      Rows::template load<kDC, 4>(rows_rsrc((const T*)a.errors + eo), rows, kDC * sizeof(T), kDC * sizeof(T),
+                                  smem + G::kE);
+      Rows::template load<kDC, 4>(rows_rsrc((const T*)a.xs + eo), rows, kDC * sizeof(T), kDC * sizeof(T),
+                                  smem + G::kX);
+      Panels<T>::template load<G::BV, 4>(
+          rows_rsrc((const T*)a.dO + c.b * a.sdo.b + h * a.sdo.h + c.tok0 * a.sdo.t + v0), c.len, a.sdo.t * sizeof(T),
+          rows * sizeof(T), smem + G::kD);
+      __builtin_amdgcn_s_waitcnt(0x0f70);
+      __syncthreads();
+      u32x4 fo[VS], fx[VS], fe[VS];                          // this lane's token, contraction over the block
+#pragma unroll
+      for (int s = 0; s < VS; ++s) {
+        fo[s] = Panels<T>::frag(smem + G::kD, i, s, g);
+        fx[s] = Rows::frag_t(smem + G::kX, w, s, lane);
+        fe[s] = Rows::frag_t(smem + G::kE, w, s, lane);
+      }
+      // dV = X
+      if (i < c.len) {
+        T* o = (T*)a.dv + c.b * a.sdv.b + h * a.sdv.h + (int64_t)(c.tok0 + i) * a.sdv.t + v0 + g * E;
+#pragma unroll
+        for (int s = 0; s < VS; ++s)
+          if (s * M::KB + g * E < rows) *reinterpret_cast<u32x4*>(o + s * M::KB) = fx[s];
+      }
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          const u32x4 fs = Rows::frag_t(smem + G::kS, t, s, lane);
+          os[t] = M::mma(fs, fo[s], os[t]);
+          xs[t] = M::mma(fs, fx[s], xs[t]);
+          es[t] = M::mma(Rows::frag_t(smem + G::kDS, t, s, lane), fe[s], es[t]);
+        }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          const u32x4 f = Rows::frag_t(smem + G::kE, t, s, lane);
+          oe[t] = M::mma(f, fo[s], oe[t]);
+          xe[t] = M::mma(f, fx[s], xe[t]);
+        }
+      // rows past the block's are zero in LDS; the same slots of both panels hold the same element
+      for (int at = threadIdx.x * 16; at < Rows::bytes(DK); at += 256 * 16) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(smem + G::kS + at);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(smem + G::kDS + at);
+        if constexpr (sizeof(T) == 2) {
+          float u[8], v[8];
+          unpack8(x, u);
+          unpack8(y, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss += u[j] * v[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ss += __uint_as_float(x[j]) * __uint_as_float(y[j]);
+        }
+      }
+    }
+    __syncthreads();                                         // the block has been read
+    Panels<T>::template load<DK, 4>(rows_rsrc((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t), c.len,
+                                    p.sq.t * sizeof(T), row, smem + G::kQ);
+    Panels<T>::template load<DK, 4>(rows_rsrc((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t), c.len,
+                                    p.sk.t * sizeof(T), row, smem + G::kK);
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    __syncthreads();
+    // q_i . k_j and k_i . k_j
+    f32x4 qk[4], kk[4];
+    {
+      u32x4 fq[SS], fk[SS];
+#pragma unroll
+      for (int s = 0; s < SS; ++s) {
+        fq[s] = Panels<T>::frag(smem + G::kQ, i, s, g);
+        fk[s] = Panels<T>::frag(smem + G::kK, i, s, g);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        qk[t] = kk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < SS; ++s) {
+          const u32x4 f = Panels<T>::frag(smem + G::kK, M::row(t, m), s, g);
+          qk[t] = M::mma(f, fq[s], qk[t]);
+          kk[t] = M::mma(f, fk[s], kk[t]);
+        }
+      }
+    }
+    const double bi = b[i], last = b[kDC - 1];
+    f32x4 mq[4], mk[4];
+    float rows = 0.f;                                        // sum_j N_ij, N_ij = Mq_ij q_i.k_j + Mk_ij k_i.k_j
+    float cols[4][4];                                        // sum over this wave's i of N_ij / beta_j
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = M::row(t, g * 4 + r);
+        const float bj = beta[j], d = j <= i ? __expf((float)(bi - b[j])) : 0.f;
+        const float uq = j <= i ? p.scale * d * oe[t][r] : 0.f, uk = j < i ? -d * xe[t][r] : 0.f;
+        mq[t][r] = uq * bj;
+        mk[t][r] = uk * bj;
+        const float n = uq * qk[t][r] + uk * kk[t][r];
+        rows += n * bj;
+        cols[t][r] = n;
+      }
+    auto put_m = [&](const f32x4 (&x)[4], int to) {          // rows of tokens i, columns j
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        store4(reinterpret_cast<T*>(smem + to + Panels<T>::at(i, M::row(t, g * 4))), x[t][0], x[t][1], x[t][2], x[t][3]);
+    };
+    put_m(mq, G::kM);
+    if (G::kBoth) put_m(mk, G::kM + G::kMBytes);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float s = cols[t][r];
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) s += __shfl_xor(s, d, 64);
+        if (m == 0) colsum[w][M::row(t, g * 4 + r)] = s;
+      }
+    rows += __shfl_xor(rows, 16, 64);
+    rows += __shfl_xor(rows, 32, 64);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d, 64);
+    if (lane == 0) part[w] = ss;
+    // this token's own products: scale exp(b) q.(S dO), exp(b) k.(S X), k.(dS' E)
+    float qos = 0.f, kxs = 0.f, kes = 0.f;
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      const int at = Panels<T>::at(i, M::row(t, g * 4));
+      const f32x4 q = load4(reinterpret_cast<const T*>(smem + G::kQ + at));
+      const f32x4 k = load4(reinterpret_cast<const T*>(smem + G::kK + at));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        qos += q[r] * os[t][r];
+        kxs += k[r] * xs[t][r];
+        kes += k[r] * es[t][r];
+      }
+    }
+#pragma unroll
+    for (int d = 16; d < 64; d <<= 1) {
+      qos += __shfl_xor(qos, d, 64);
+      kxs += __shfl_xor(kxs, d, 64);
+      kes += __shfl_xor(kes, d, 64);
+    }
+    const float up = __expf((float)bi), left = __expf((float)(last - bi)), bet = beta[i];
+    const float us = p.scale * up, le = left * bet;
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      dq[t] += us * os[t];
+      dk[t] += le * es[t] - up * xs[t];
+    }
+    __syncthreads();                                         // Mq, Mk, column sums
+    // dQ += Mq K; dK += Mk K + Mk^T K + Mq^T Q
+    {
+      u32x4 a_q[CS], a_k[CS], t_q[CS], t_k[CS];
+#pragma unroll
+      for (int s = 0; s < CS; ++s) {
+        a_q[s] = M::frag(mq + s * M::TPS);
+        a_k[s] = M::frag(mk + s * M::TPS);
+        t_q[s] = Panels<T>::frag_t(smem + G::kM, w, s, lane);
+      }
+      if (!G::kBoth) {
+        __syncthreads();
+        put_m(mk, G::kM);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int s = 0; s < CS; ++s)
+        t_k[s] = Panels<T>::frag_t(smem + G::kM + (G::kBoth ? G::kMBytes : 0), w, s, lane);
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int s = 0; s < CS; ++s) {
+          const u32x4 fk = Panels<T>::frag_t(smem + G::kK, t, s, lane), fq = Panels<T>::frag_t(smem + G::kQ, t, s, lane);
+          dq[t] = M::mma(fk, a_q[s], dq[t]);
+          dk[t] = M::mma(fk, a_k[s], dk[t]);
+          dk[t] = M::mma(fk, t_k[s], dk[t]);
+          dk[t] = M::mma(fq, t_q[s], dk[t]);
+        }
+    }
+    if (g == 0) {
+      const float n = colsum[0][i] + colsum[1][i] + colsum[2][i] + colsum[3][i];
+      const float end = le * kes;                            // through exp(b_63 - b_i)
+      db[i] = us * qos - up * kxs + rows - bet * n - end;
+      colsum[0][i] = end;
+      if (i < c.len) {
+        const int64_t t = c.tok0 + i;
+        ((T*)a.dbeta)[c.b * a.sdbeta.b + h * a.sdbeta.h + t * a.sdbeta.t] = from_f32<T>(n + left * kes);
+      }
+    }
+    __syncthreads();
+    if (w == 0) {
+      float all = colsum[0][lane];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
+      all += __expf((float)last) * (part[0] + part[1] + part[2] + part[3]);
+      float s = db[lane] + (lane == 63 ? all : 0.f);         // suffix sums
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const float down = __shfl_down(s, d, 64);
+        if (lane + d < 64) s += down;
+      }
+      if (lane < c.len)
+        ((T*)a.dg)[c.b * a.sdg.b + h * a.sdg.h + (int64_t)(c.tok0 + lane) * a.sdg.t] = from_f32<T>(s);
+    }
+  }
+  if (i < c.len) {
+    T* oq = (T*)a.dq + c.b * a.sdq.b + kh * a.sdq.h + (int64_t)(c.tok0 + i) * a.sdq.t;
+    T* ok = (T*)a.dk + c.b * a.sdk.b + kh * a.sdk.h + (int64_t)(c.tok0 + i) * a.sdk.t;
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+      const int d = M::row(t, g * 4);
+      if (d < p.dk) {
+        store4(oq + d, dq[t][0], dq[t][1], dq[t][2], dq[t][3]);
+        store4(ok + d, dk[t][0], dk[t][1], dk[t][2], dk[t][3]);
+      }
+    }
+  }
+}
+
+constexpr size_t kAlign = 256;
+size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// The workspace: both records, S, dS' (T), E, X (T), in this order.
+template <typename T>
+size_t place(DeltaGradArgs& a) {
+  const size_t n = (size_t)delta_slots(a.f.seqs, a.f.batch) * a.f.Hv;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* r = a.f.ws + at;
+    at += up(bytes);
+    return r;
+  };
+  a.rec = take(n * ChunkRec<T>::kBytes);
+  a.rect = take(n * ChunkRecT<T>::kBytes);
+  a.states = take(n * a.f.dv * a.f.dk * sizeof(T));
+  a.dstates = take(n * a.f.dv * a.f.dk * sizeof(T));
+  a.errors = take(n * a.f.dv * kDC * sizeof(T));
+  a.xs = take(n * a.f.dv * kDC * sizeof(T));
+  return at;
+}
+
+template <typename F>
+hipError_t with_smem(F kern, int bytes) {
+  return hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename T, int DK, int NW>
+hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hipStream_t s) {
+  constexpr int kMax = 160 * 1024;
+  constexpr int SF = Walk<T, DK, NW, 2, false>::kSmem <= kMax ? 2 : 1;
+  constexpr int SB = WalkBack<T, DK, NW, 2>::kSmem <= kMax ? 2 : 1;
+  constexpr int F = Walk<T, DK, NW, SF, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
+  static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 2048, "LDS of a CU");
+  auto walks = k_delta_walks<T, DK, NW, SF, SB>;
+  auto grads = k_delta_grads<T, DK>;
+  static const hipError_t set = [&] {
+    hipError_t e = with_smem(walks, W);
+    return e != hipSuccess ? e : with_smem(grads, Grads<T, DK>::kSmem);
+  }();
+  if (set != hipSuccess) return set;
+  if (sequences > 0) {
+    const int64_t parts = (a.f.dv + 16 * NW - 1) / (16 * NW);
+    walks<<<dim3((unsigned)(2 * parts * a.f.Hv * sequences)), 64 * NW, W, s>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (slots > 0) grads<<<dim3((unsigned)(slots * a.f.Hk)), 256, Grads<T, DK>::kSmem, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+template <typename T>
+size_t delta_grad_workspace_bytes(const DeltaArgs& f) {
+  DeltaGradArgs a{};
+  a.f = f;
+  a.f.ws = nullptr;
+  return place<T>(a);
+}
+
+template <typename T>
+hipError_t launch_delta_grad(const DeltaGradArgs& given, hipStream_t s) {
+  DeltaGradArgs a = given;
+  place<T>(a);
+  const int64_t slots = a.f.seqs.n > 0 ? delta_slots(a.f.seqs, a.f.batch) : 0;
+  if (slots > 0) {
+    k_delta_chunks<T, true><<<dim3((unsigned)(slots * a.f.Hv)), kChunkThreads, 0, s>>>(a.f, a.rec, a.rect);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  const int sequences = a.f.seqs.starts ? a.f.seqs.num : a.f.batch;
+  if (a.f.dk <= 64) return launch_sizes<T, 64, 4>(a, slots, sequences, s);
+  if (a.f.dk <= 128) return launch_sizes<T, 128, 4>(a, slots, sequences, s);
+  return launch_sizes<T, 256, sizeof(T) == 2 ? 4 : 2>(a, slots, sequences, s);
+}
+
+template size_t delta_grad_workspace_bytes<bf16>(const DeltaArgs&);
+template size_t delta_grad_workspace_bytes<float>(const DeltaArgs&);
+template hipError_t launch_delta_grad<bf16>(const DeltaGradArgs&, hipStream_t);
+template hipError_t launch_delta_grad<float>(const DeltaGradArgs&, hipStream_t);
+
+}  // namespace ttt

@@ -254,4 +254,20 @@ size_t delta_workspace_bytes(const DeltaArgs& a);
 template <typename T>
 hipError_t launch_delta(const DeltaArgs& a, hipStream_t s);
 
+struct DeltaGradArgs {
+  DeltaArgs f;                         // O and W_final unused
+  const void* dO;
+  const float* dW_final;               // or null: zero
+  void *dq, *dk, *dv, *dg, *dbeta;
+  float* dW_init;                      // or null: not wanted
+  DeltaStrides sdo, sdq, sdk, sdv, sdg, sdbeta;
+  // regions of the workspace, placed by launch_delta_grad
+  char *rec, *rect;
+  void *states, *dstates, *errors, *xs;
+};
+template <typename T>
+size_t delta_grad_workspace_bytes(const DeltaArgs& a);
+template <typename T>
+hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s);
+
 }  // namespace ttt

@@ -751,6 +751,33 @@ int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const 
                     const float* g, const float* beta, const ttt_delta_options* options, void* O, float* W_final,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* Strides of the backward call's own tensors, as in ttt_delta_layout. */
+typedef struct {
+  ttt_delta_strides dO, dq, dk, dv, dg, dbeta;
+} ttt_delta_grad_layout;
+
+/* Workspace of ttt_gated_delta_backward; num_seqs < 0: not packed. */
+int ttt_gated_delta_backward_workspace_bytes(const ttt_delta_shape* shape, int dtype, int64_t num_seqs,
+                                             size_t* bytes);
+
+/* The backward of ttt_gated_delta, from the forward call's inputs alone (the
+ * states are made again), given dO = dLoss/dO and, where the loss depends on
+ * the final states too, dW_final (else NULL):
+ *   dq, dk     [B, Hk, n, dk]  dtype   (written) summed over the value heads of a key head
+ *   dv         [B, Hv, n, dv]  dtype   (written)
+ *   dg, dbeta  [B, Hv, n]      dtype   (written) the sums fp32, rounded once
+ *   dW_init    [sequences, Hv, dv, dk] fp32 (written), or NULL: not wanted
+ * options' layout gives the inputs' strides (its O is not used), grad_layout
+ * (NULL: contiguous) those of dO and the gradients.  Rows of tokens that
+ * belong to no sequence are left as they are.  At a reset (g below -200) dg
+ * is that of a decay of zero, up to rounding.  No atomics: the same bits at
+ * every call. */
+int ttt_gated_delta_backward(const ttt_delta_shape* shape, int dtype, float scale, const void* q, const void* k,
+                             const void* v, const float* g, const float* beta, const void* dO, const float* dW_final,
+                             const ttt_delta_options* options, const ttt_delta_grad_layout* grad_layout, void* dq,
+                             void* dk, void* dv, void* dg, void* dbeta, float* dW_init, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Sizes of a step: rows of a serving batch, states in the pool. */
 typedef struct {
   int64_t rows, states, k_heads, v_heads, k_dim, v_dim;

@@ -53,7 +53,7 @@ def delta_rule_backward(q, k, v, g, beta, scale, dO, W0=None, dWn=None):
         dA = dW - de[:, :, None] * k[:, t][:, None, :]
         dg[:, t] = (A * dA).sum((-1, -2))
         dW = a[:, t, None, None] * dA
-    fold = lambda x: x.reshape(Hk, Hv // Hk, n, -1).sum(1)
+    fold = lambda x: x.reshape(Hk, Hv // Hk, n, x.shape[-1]).sum(1)
     return fold(dq), fold(dk), dv_, dg, dbeta, dW
 
 
