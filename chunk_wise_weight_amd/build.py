@@ -26,6 +26,9 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
     "-Wno-unused-command-line-argument",
 ]
+# The walks over a state keep it in fp32 accumulators that vector instructions scale and split between products:
+# MFMA results in ordinary registers spare a copy each way per element and product.
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("delta.hip", "delta_bwd.hip")}
 
 
 def _run(cmd):
@@ -45,7 +48,7 @@ def build(verbose: bool = False, jobs: int = 3) -> str:
             obj = os.path.join(tmp, src + ".o")
             objs.append(obj)
             lang = ["-x", "hip"] if src.endswith(".cpp") else []
-            cmd = [HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = [HIPCC, *FLAGS, *EXTRA.get(src, ()), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
             procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         errors = []
         for cmd, p in procs:

@@ -5,7 +5,7 @@ namespace ttt {
 namespace {
 
 template <typename T, int DK, int NW, int STAGES>
-__global__ __launch_bounds__(128 * NW) void k_delta_walk(DeltaArgs p, const char* rec) {
+__global__ __launch_bounds__(128 * NW) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_delta_walk(DeltaArgs p, const char* rec) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int parts = (p.dv + 16 * NW - 1) / (16 * NW);
   const int id = xcd_remap(blockIdx.x, gridDim.x);

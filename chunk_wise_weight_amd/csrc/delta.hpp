@@ -23,6 +23,8 @@
 // fp32: the state keeps fp32's digits over long rows.  What feeds only the
 // output O, which is rounded to bf16 at the end, is rounded once to bf16.
 #pragma once
+#include <type_traits>
+
 #include "gemm.hpp"
 #include "launch.hpp"
 
@@ -135,6 +137,9 @@ template <typename T> struct ChunkRecT {
   static constexpr int kBytes = kGate + 1024;
 };
 
+// Rows from `base` on: loads through it test rows and columns themselves.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base) { return make_rsrc(base, kOOB); }
+
 // R (64) rows of up to DK elements in LDS: panels of 128 bytes a row, the 16-byte
 // chunk c of row r in slot c ^ panel_swz(r).  The 16 rows of an operand read
 // (Mat::row: rows 0-3, 8-11, 16-19, 24-27 of a step, or the other four of each
@@ -178,50 +183,69 @@ template <typename T, int R = kDC> struct Panels {
     const int byte = col * (int)sizeof(T);
     return (byte >> 7) * kPanel + r * 128 + ((((byte & 127) >> 4) ^ panel_swz(r)) << 4) + (byte & 15);
   }
-  // DMA of all panels by NW waves, 8 rows of a panel an instruction.  Rows >= len and columns
-  // >= row_bytes read as zero: a whole chunk of full rows needs no test of either.
-  template <int DK, int NW>
-  __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int len, unsigned pitch, unsigned row_bytes,
-                                              char* t) {
-    constexpr int N = bytes(DK) / 1024;
-    const int L = lane_id(), w = wave_id() % NW;
-    const bool full = len >= R && row_bytes == DK * sizeof(T);
-#pragma unroll
-    for (int j = 0; j < N / NW; ++j) {
-      const int i = j * NW + w, b = i % (R / 8);
-      const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4), at = (unsigned)(i / (R / 8)) * 128u;
-      unsigned off = (unsigned)(L >> 3) * pitch + byte + ((unsigned)b * 8u * pitch + at);
-      if (!full && ((L >> 3) >= len - b * 8 || byte + at >= row_bytes)) off = kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, off, 0, 0, 0);
-    }
-  }
 };
 
-// Rows from `base` on: loads through it test rows and columns themselves.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base) { return make_rsrc(base, kOOB); }
+// DMA of all panels by NW waves, 8 rows of a panel an instruction.  Rows >= len and columns >= row_bytes read as
+// zero; the lanes' offsets are the same for every chunk of a walk and made once.
+  template <typename T, int DK, int NW, int R = kDC> struct PanelLoader {
+    static constexpr int N = DK * (int)sizeof(T) * R / 1024 / NW;
+    unsigned off[N];
+    __device__ __forceinline__ PanelLoader(unsigned pitch, unsigned row_bytes) {
+      const int L = lane_id(), w = wave_id() % NW;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int i = j * NW + w, b = i % (R / 8);
+        const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4) + (unsigned)(i / (R / 8)) * 128u;
+        off[j] = byte < row_bytes ? (unsigned)(b * 8 + (L >> 3)) * pitch + byte : kOOB;
+      }
+    }
+  // (left out of the host's pass, which drops kernels that call it from here)
+    __device__ __forceinline__ void issue(const void* rows, int len, char* t) const {
+#if __HIP_DEVICE_COMPILE__
+      const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
+      const int L = lane_id(), w = wave_id() % NW;
+      if (len >= R) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + w * 1024 + j * (NW * 1024)), 16, off[j], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int i = j * NW + w;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
+                                                   (i % (R / 8)) * 8 + (L >> 3) < len ? off[j] : kOOB, 0, 0, 0);
+        }
+      }
+#endif
+    }
+  };
 
 // 64 rows of a wave group's own columns: NW waves with 16 columns each, row by row.
 template <typename T, int NW> struct Columns {
   static constexpr int kPitch = 16 * NW * (int)sizeof(T), kBytes = kDC * kPitch;
+  static constexpr int N = kBytes / 1024 / NW, GPR = kPitch / 16, RPI = 64 / GPR;   // 16-byte pieces a row, rows a load
+  unsigned off[N];
   // cols: valid columns from this group's first on
-  __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int len, unsigned pitch, int cols, char* t) {
-    constexpr int N = kBytes / 1024, GPR = kPitch / 16, RPI = 64 / GPR;      // 16-byte pieces a row, rows a load
+  __device__ __forceinline__ Columns(unsigned pitch, int cols) {
+    const int L = lane_id(), w = wave_id() % NW, c = L % GPR;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      off[j] = c * (16 / (int)sizeof(T)) < cols ? (unsigned)((j * NW + w) * RPI + L / GPR) * pitch + c * 16u : kOOB;
+  }
+  __device__ __forceinline__ void issue(const void* rows, int len, char* t) const {
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
     const int L = lane_id(), w = wave_id() % NW;
 #pragma unroll
-    for (int j = 0; j < N / NW; ++j) {
-      const int i = j * NW + w, r = i * RPI + L / GPR, c = L % GPR;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (lds_ptr_t)(t + i * 1024), 16,
-          r < len && c * (16 / (int)sizeof(T)) < cols ? (unsigned)r * pitch + c * 16u : kOOB, 0, 0, 0);
-    }
+    for (int j = 0; j < N; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + (j * NW + w) * 1024), 16,
+                                               (j * NW + w) * RPI + L / GPR < len ? off[j] : kOOB, 0, 0, 0);
   }
-  // column lane & 15 of wave w's, rows Mat::row(tile, 4 g + 0..3)
-  __device__ static __forceinline__ f32x4 read(const char* t, int w, int tile, int lane) {
+  // Column lane & 15 of wave w's, rows Mat::row(tile, 4 g + 0..3), as it lies in LDS and widened.
+  using Raw = typename std::conditional<sizeof(T) == 2, u32x2, f32x4>::type;
+  __device__ static __forceinline__ Raw read(const char* t, int w, int tile, int lane) {
     const int m = lane & 15, r = Mat<T>::row(tile, (lane >> 4) * 4);
     if constexpr (sizeof(T) == 2) {
-      const u32x2 x = __builtin_bit_cast(u32x2, lds_read_tr16(t + (r + (m >> 2)) * kPitch + w * 32 + (m & 3) * 8));
-      return (f32x4){__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
-                     __uint_as_float(x[1] & 0xffff0000u)};
+      return __builtin_bit_cast(u32x2, lds_read_tr16(t + (r + (m >> 2)) * kPitch + w * 32 + (m & 3) * 8));
     } else {
       f32x4 o;
 #pragma unroll
@@ -229,11 +253,17 @@ template <typename T, int NW> struct Columns {
       return o;
     }
   }
+  __device__ static __forceinline__ f32x4 wide(u32x2 x) {
+    return (f32x4){__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
+                   __uint_as_float(x[1] & 0xffff0000u)};
+  }
+  __device__ static __forceinline__ f32x4 wide(f32x4 x) { return x; }
 };
 
 // `N` KB that lie one after the other, by NW waves.
 template <int N, int NW>
-__device__ __forceinline__ void load_block(__amdgpu_buffer_rsrc_t rs, char* t) {
+__device__ __forceinline__ void load_block(const void* base, char* t) {
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, N * 1024);
   const int w = wave_id() % NW;
 #pragma unroll
   for (int j = 0; j < (N + NW - 1) / NW; ++j) {

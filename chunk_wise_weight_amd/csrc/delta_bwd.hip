@@ -51,13 +51,15 @@ __device__ __forceinline__ void walk_back(const DeltaGradArgs& a, const char* re
   const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRecT<T>::kBytes;
   const int64_t rstep = (int64_t)p.Hv * ChunkRecT<T>::kBytes;
 
+  const PanelLoader<T, DK, NW> kload(kp, row), qload(qp, row);
+  const Columns<T, NW> dload(dp, p.dv - first);
   auto fetch = [&](int c) {
     char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
     const int len = min(kDC, sp.len - c * kDC);
-    Panels<T>::template load<DK, NW>(rows_rsrc(k0 + (int64_t)c * kDC * p.sk.t), len, kp, row, st + G::kK);
-    Panels<T>::template load<DK, NW>(rows_rsrc(q0 + (int64_t)c * kDC * p.sq.t), len, qp, row, st + G::kQ);
-    load_block<ChunkRecT<T>::kBytes / 1024, NW>(make_rsrc(rec0 + c * rstep, ChunkRecT<T>::kBytes), st + G::kRec);
-    Columns<T, NW>::load(rows_rsrc(d0 + (int64_t)c * kDC * a.sdo.t), len, dp, p.dv - first, st + G::kD);
+    kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
+    qload.issue(q0 + (int64_t)c * kDC * p.sq.t, len, st + G::kQ);
+    load_block<ChunkRecT<T>::kBytes / 1024, NW>(rec0 + c * rstep, st + G::kRec);
+    dload.issue(d0 + (int64_t)c * kDC * a.sdo.t, len, st + G::kD);
   };
   if (STAGES == 2 && chunks > 0) fetch(chunks - 1);
   f32x4 S[ST];                    // dS': block t, register r: dk = row(t, 4 g + r), dv = col
@@ -88,7 +90,7 @@ __device__ __forceinline__ void walk_back(const DeltaGradArgs& a, const char* re
     f32x4 d[4], x[4];
     u32x4 D[CS], Rh[CS], Rl[CS];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) d[t] = Columns<T, NW>::read(st + G::kD, w, t, lane);
+    for (int t = 0; t < 4; ++t) d[t] = Columns<T, NW>::wide(Columns<T, NW>::read(st + G::kD, w, t, lane));
 #pragma unroll
     for (int s = 0; s < CS; ++s) D[s] = M::frag(d + s * M::TPS);       // exact: dO is of type T
 #pragma unroll
@@ -213,6 +215,9 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
   const int w = wave_id(), lane = lane_id(), m = lane & 15, g = lane >> 4;
   const int i = M::row(w, m);                                // this lane's token
   const unsigned row = p.dk * sizeof(T);
+  const PanelLoader<T, DK, 4, G::BV> sload(row, row);
+  const PanelLoader<T, kDC, 4, G::BV> eload(kDC * sizeof(T), kDC * sizeof(T));
+  const PanelLoader<T, DK, 4> qload(p.sq.t * sizeof(T), row), kload(p.sk.t * sizeof(T), row);
   f32x4 dq[ST], dk[ST];
 #pragma unroll
   for (int t = 0; t < ST; ++t) dq[t] = dk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -246,15 +251,12 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
       if (v0 > 0) __syncthreads();
       const int rows = min(G::BV, p.dv - v0);
       const int64_t so = (sh * p.dv + v0) * p.dk, eo = (sh * p.dv + v0) * kDC;
-      Rows::template load<DK, 4>(rows_rsrc((const T*)a.states + so), rows, row, row, smem + G::kS);
-      Rows::template load<DK, 4>(rows_rsrc((const T*)a.dstates + so), rows, row, row, smem + G::kDS);
-      Rows::template load<kDC, 4>(rows_rsrc((const T*)a.errors + eo), rows, kDC * sizeof(T), kDC * sizeof(T),
-                                  smem + G::kE);
-      Rows::template load<kDC, 4>(rows_rsrc((const T*)a.xs + eo), rows, kDC * sizeof(T), kDC * sizeof(T),
-                                  smem + G::kX);
-      Panels<T>::template load<G::BV, 4>(
-          rows_rsrc((const T*)a.dO + c.b * a.sdo.b + h * a.sdo.h + c.tok0 * a.sdo.t + v0), c.len, a.sdo.t * sizeof(T),
-          rows * sizeof(T), smem + G::kD);
+      sload.issue((const T*)a.states + so, rows, smem + G::kS);
+      sload.issue((const T*)a.dstates + so, rows, smem + G::kDS);
+      eload.issue((const T*)a.errors + eo, rows, smem + G::kE);
+      eload.issue((const T*)a.xs + eo, rows, smem + G::kX);
+      const PanelLoader<T, G::BV, 4> dload(a.sdo.t * sizeof(T), rows * sizeof(T));
+      dload.issue((const T*)a.dO + c.b * a.sdo.b + h * a.sdo.h + c.tok0 * a.sdo.t + v0, c.len, smem + G::kD);
       __builtin_amdgcn_s_waitcnt(0x0f70);
       __syncthreads();
       u32x4 fo[VS], fx[VS], fe[VS];                          // this lane's token, contraction over the block
@@ -305,10 +307,8 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
       }
     }
     __syncthreads();                                         // the block has been read
-    Panels<T>::template load<DK, 4>(rows_rsrc((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t), c.len,
-                                    p.sq.t * sizeof(T), row, smem + G::kQ);
-    Panels<T>::template load<DK, 4>(rows_rsrc((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t), c.len,
-                                    p.sk.t * sizeof(T), row, smem + G::kK);
+    qload.issue((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t, c.len, smem + G::kQ);
+    kload.issue((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t, c.len, smem + G::kK);
     __builtin_amdgcn_s_waitcnt(0x0f70);
     __syncthreads();
     // q_i . k_j and k_i . k_j

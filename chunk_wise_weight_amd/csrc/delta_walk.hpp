@@ -210,6 +210,7 @@ template <typename T, int DK, int NW, int STAGES, bool OUT> struct Walk {
   static constexpr int SS = DK / Mat<T>::KB;
   static constexpr int kK = 0, kRec = Panels<T>::bytes(DK), kV = kRec + ChunkRec<T>::kP;
   static constexpr int kStage = kV + Columns<T, NW>::kBytes;
+  static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
   static constexpr int kSwap = SS * 1024 + 4096;           // a state wave's state operands and errors (fp32)
   static constexpr int kSmem = STAGES * kStage + (OUT ? 2 * NW * kSwap : 0);
   static constexpr int kThreads = 64 * NW * (OUT ? 2 : 1);
@@ -230,12 +231,14 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
   const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes;
   const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
 
+  const PanelLoader<T, DK, NW> kload(kp, krow);
+  const Columns<T, NW> vload(vp, p.dv - first);
   auto fetch = [&](int c) {
     char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
     const int len = min(kDC, sp.len - c * kDC);
-    Panels<T>::template load<DK, NW>(rows_rsrc(k0 + (int64_t)c * kDC * p.sk.t), len, kp, krow, st + G::kK);
-    load_block<ChunkRec<T>::kP / 1024, NW>(make_rsrc(rec0 + c * rstep, ChunkRec<T>::kP), st + G::kRec);
-    Columns<T, NW>::load(rows_rsrc(v0 + (int64_t)c * kDC * p.sv.t), len, vp, p.dv - first, st + G::kV);
+    kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
+    load_block<ChunkRec<T>::kP / 1024, NW>(rec0 + c * rstep, st + G::kRec);
+    vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
   };
   if (STAGES == 2 && chunks > 0) fetch(0);
   // state block t, register r: dk = row(t, 4 g + r), dv = col
@@ -256,14 +259,34 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);              // vmcnt(0): this chunk's loads
     __syncthreads();
-    if (STAGES == 2 && c + 1 < chunks) fetch(c + 1);
     const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRec<T>::kGate);
     char* swap = smem + STAGES * G::kStage + ((c & 1) * NW + w) * G::kSwap + lane * 16;
+    const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
 
+    // Reads from LDS go out ahead of the arithmetic that hides them: one wave a SIMD has nobody else to do it.
+    u32x4 Kf[G::kHoist ? 4 : 1][SS], Th[M::kTri], Tl[M::kSplit ? M::kTri : 1];
+    typename Columns<T, NW>::Raw v[4];
+    f32x4 up[4], left[4];
+    auto read_k = [&](int t, u32x4 (&f)[SS]) {
+      const int r = M::row(t, m);
+#pragma unroll
+      for (int s = 0; s < SS; ++s) f[s] = Panels<T>::frag(st + G::kK, r, s, g);
+    };
+    if constexpr (G::kHoist)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) read_k(t, Kf[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v[t] = Columns<T, NW>::read(st + G::kV, w, t, lane);
+      up[t] = *reinterpret_cast<const f32x4*>(gate + M::row(t, g * 4));
+      left[t] = *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
+    }
+    const float decay = gate[63];
+    if (STAGES == 2 && c + 1 < chunks) fetch(c + 1);
+    __builtin_amdgcn_sched_barrier(0);
     u32x4 Sh[SS], Sl[SS];
 #pragma unroll
     for (int s = 0; s < SS; ++s) M::split(S + s * M::TPS, Sh[s], Sl[s]);
-    const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
     if constexpr (OUT) {
 #pragma unroll
       for (int s = 0; s < SS; ++s) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
@@ -273,32 +296,58 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
     // V - exp(b) K S
     f32x4 e[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      const int r = M::row(t, m);
+    for (int t = 0; t < 4; ++t) e[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if constexpr (G::kHoist) {
 #pragma unroll
-      for (int s = 0; s < SS; ++s) acc = mma_split<T>(Panels<T>::frag(st + G::kK, r, s, g), Sh[s], Sl[s], acc);
-      e[t] = Columns<T, NW>::read(st + G::kV, w, t, lane) -
-             *reinterpret_cast<const f32x4*>(gate + M::row(t, g * 4)) * acc;
+      for (int s = 0; s < SS; ++s)
+#pragma unroll
+        for (int i = 0; i < (M::kSplit ? 2 : 1); ++i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) e[t] = M::mma(Kf[t][s], i ? Sl[s] : Sh[s], e[t]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        read_k(t, Kf[0]);
+#pragma unroll
+        for (int s = 0; s < SS; ++s) e[t] = mma_split<T>(Kf[0][s], Sh[s], Sl[s], e[t]);
+      }
     }
+#pragma unroll
+    for (int f = 0; f < M::kTri; ++f) {
+      Th[f] = *reinterpret_cast<const u32x4*>(st + G::kRec + f * 1024 + lane * 16);
+      if (M::kSplit) Tl[f] = *reinterpret_cast<const u32x4*>(st + G::kRec + ChunkRec<T>::kTl + f * 1024 + lane * 16);
+    }
+    u32x4 Kt[G::kHoist ? ST : 1][CS];
+    if constexpr (G::kHoist)
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int s = 0; s < CS; ++s) Kt[t][s] = Panels<T>::frag_t(st + G::kK, t, s, lane);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < ST; ++t) S[t] *= decay;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) e[t] = Columns<T, NW>::wide(v[t]) - up[t] * e[t];
     u32x4 Rh[CS], Rl[CS];
 #pragma unroll
     for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Rh[s], Rl[s]);
     // E = T (V - exp(b) K S)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) e[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < M::steps(t); ++s) {
-        const char* f = st + G::kRec + M::tri(t, s) * 1024 + lane * 16;
-        const u32x4 th = *reinterpret_cast<const u32x4*>(f);
-        const u32x4 tl = M::kSplit ? *reinterpret_cast<const u32x4*>(f + ChunkRec<T>::kTl) : th;
-        acc = mma_split2<T>(th, tl, Rh[s], Rl[s], acc);
-      }
-      e[t] = acc;
-      if constexpr (OUT) *reinterpret_cast<f32x4*>(swap + SS * 1024 + t * 1024) = acc;
-    }
-    if constexpr (!OUT) {
+    for (int s = 0; s < CS; ++s)
+#pragma unroll
+      for (int i = 0; i < (M::kSplit ? 3 : 1); ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (s < M::steps(t)) {
+            const int f = M::tri(t, s);
+            e[t] = M::mma(i == 2 ? Tl[M::kSplit ? f : 0] : Th[f], i == 1 ? Rl[s] : Rh[s], e[t]);
+          }
+    if constexpr (OUT) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(swap + SS * 1024 + t * 1024) = e[t];
+    } else {
       T* E = (T*)errors + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
 #pragma unroll
       for (int s = 0; s < CS; ++s)
@@ -306,16 +355,17 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
     }
     // S = exp(b_63) S + K^T (exp(b_63 - b) beta E)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) e[t] *= *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
+    for (int t = 0; t < 4; ++t) e[t] *= left[t];
 #pragma unroll
     for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Rh[s], Rl[s]);
-    const float decay = gate[63];
 #pragma unroll
-    for (int t = 0; t < ST; ++t) {
-      S[t] *= decay;
+    for (int s = 0; s < CS; ++s)
 #pragma unroll
-      for (int s = 0; s < CS; ++s) S[t] = mma_split<T>(Panels<T>::frag_t(st + G::kK, t, s, lane), Rh[s], Rl[s], S[t]);
-    }
+      for (int t = 0; t < ST; ++t) {
+        const u32x4 f = G::kHoist ? Kt[G::kHoist ? t : 0][s] : Panels<T>::frag_t(st + G::kK, t, s, lane);
+        S[t] = M::mma(f, Rh[s], S[t]);
+        if (M::kSplit) S[t] = M::mma(f, Rl[s], S[t]);
+      }
   }
   if (OUT && chunks > 0) {
     if (STAGES == 1) __syncthreads();
