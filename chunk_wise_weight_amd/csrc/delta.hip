@@ -4,30 +4,34 @@
 namespace ttt {
 namespace {
 
-template <typename T, int DK, int NW, int STAGES>
-__global__ __launch_bounds__(128 * NW) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_delta_walk(DeltaArgs p, const char* rec) {
+template <typename T, int DK, int NW, int STAGES, bool QLDS>
+__global__ __launch_bounds__(64 * (1 + 2 * NW)) void k_delta_walk(DeltaArgs p, const char* rec, int sequences) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int parts = (p.dv + 16 * NW - 1) / (16 * NW);
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int part = id % parts, h = (id / parts) % p.Hv, seq = id / parts / p.Hv;
-  const SeqPlace sp = seq_place(p.seqs, seq);
-  if (wave_id() < NW)
-    walk_states<T, DK, NW, STAGES, true>(p, rec, nullptr, nullptr, part, h, seq, sp, smem);
-  else if (sp.len > 0)
-    walk_outputs<T, DK, NW, STAGES>(p, rec, part, h, sp, smem);
+  WalkPlace at;
+  if (!walk_place(blockIdx.x, sequences, p.Hk, p.Hv / p.Hk, (p.dv + 16 * NW - 1) / (16 * NW), &at)) return;
+  const SeqPlace sp = seq_place(p.seqs, at.seq);
+  const int w = wave_id();
+  if (w == 0)
+    walk_loads<T, DK, NW, STAGES, true, QLDS>(p, rec, at, sp, smem);
+  else if (w <= NW)
+    walk_states<T, DK, NW, STAGES, true, QLDS>(p, w - 1, nullptr, nullptr, at, sp, smem);
+  else
+    walk_outputs<T, DK, NW, STAGES, QLDS>(p, rec, w - 1 - NW, at, sp, smem);
 }
 
 template <typename T, int DK, int NW>
 hipError_t launch_walk(const DeltaArgs& a, int sequences, hipStream_t s) {
-  constexpr int STAGES = Walk<T, DK, NW, 2, true>::kSmem <= 160 * 1024 ? 2 : 1;
-  using G = Walk<T, DK, NW, STAGES, true>;
-  static_assert(G::kSmem <= 160 * 1024, "one stage has to fit");
-  auto kern = k_delta_walk<T, DK, NW, STAGES>;
+  constexpr int kMax = 160 * 1024;
+  constexpr bool QLDS = Walk<T, DK, NW, 2, true, true>::kSmem <= kMax;
+  constexpr int STAGES = Walk<T, DK, NW, 2, true, QLDS>::kSmem <= kMax ? 2 : 1;
+  using G = Walk<T, DK, NW, STAGES, true, QLDS>;
+  static_assert(G::kSmem <= kMax, "one stage has to fit");
+  auto kern = k_delta_walk<T, DK, NW, STAGES, QLDS>;
   static const hipError_t set =
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (set != hipSuccess) return set;
-  const int64_t parts = (a.dv + 16 * NW - 1) / (16 * NW);
-  kern<<<dim3((unsigned)(parts * a.Hv * sequences)), G::kThreads, G::kSmem, s>>>(a, a.ws);
+  const int64_t blocks = walk_blocks((int64_t)sequences * a.Hk, a.Hv / a.Hk * ((a.dv + 16 * NW - 1) / (16 * NW)));
+  kern<<<dim3((unsigned)blocks), G::kThreads, G::kSmem, s>>>(a, a.ws, sequences);
   return hipGetLastError();
 }
 

@@ -59,6 +59,7 @@ template <> struct Mat<bf16> {
     return (u32x4){pack2_bf16(c[0][0], c[0][1]), pack2_bf16(c[0][2], c[0][3]), pack2_bf16(c[1][0], c[1][1]),
                    pack2_bf16(c[1][2], c[1][3])};
   }
+  // Values and what their rounding to bf16 left.
   __device__ static __forceinline__ void split(const f32x4* c, u32x4& hi, u32x4& lo) {
     hi = frag(c);
     f32x4 r[2];
@@ -71,11 +72,6 @@ template <> struct Mat<bf16> {
         r[i][2 * j + 1] = c[i][2 * j + 1] - __uint_as_float(w & 0xffff0000u);
       }
     lo = frag(r);
-  }
-  // 8 consecutive values to one operand's 16 bytes, and the rest
-  __device__ static __forceinline__ void split8(const float* x, u32x4& hi, u32x4& lo) {
-    const f32x4 c[2] = {{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
-    split(c, hi, lo);
   }
 };
 
@@ -187,58 +183,58 @@ template <typename T, int R = kDC> struct Panels {
 
 // DMA of all panels by NW waves, 8 rows of a panel an instruction.  Rows >= len and columns >= row_bytes read as
 // zero; the lanes' offsets are the same for every chunk of a walk and made once.
-  template <typename T, int DK, int NW, int R = kDC> struct PanelLoader {
-    static constexpr int N = DK * (int)sizeof(T) * R / 1024 / NW;
-    unsigned off[N];
-    __device__ __forceinline__ PanelLoader(unsigned pitch, unsigned row_bytes) {
-      const int L = lane_id(), w = wave_id() % NW;
+template <typename T, int DK, int NW, int R = kDC> struct PanelLoader {
+  static constexpr int N = DK * (int)sizeof(T) * R / 1024 / NW;
+  unsigned off[N];
+  __device__ __forceinline__ PanelLoader(unsigned pitch, unsigned row_bytes) {
+    const int L = lane_id(), w = wave_id() % NW;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = j * NW + w, b = i % (R / 8);
+      const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4) + (unsigned)(i / (R / 8)) * 128u;
+      off[j] = byte < row_bytes ? (unsigned)(b * 8 + (L >> 3)) * pitch + byte : kOOB;
+    }
+  }
+  // (left out of the host's pass, which drops kernels that call it from here)
+  __device__ __forceinline__ void issue(const void* rows, int len, char* t) const {
+#if __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
+    const int L = lane_id(), w = wave_id() % NW;
+    if (len >= R) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + w * 1024 + j * (NW * 1024)), 16, off[j], 0, 0, 0);
+    } else {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int i = j * NW + w, b = i % (R / 8);
-        const unsigned byte = (unsigned)(((L & 7) ^ ((L >> 4) & 1) ^ ((b & 3) << 1)) << 4) + (unsigned)(i / (R / 8)) * 128u;
-        off[j] = byte < row_bytes ? (unsigned)(b * 8 + (L >> 3)) * pitch + byte : kOOB;
+        const int i = j * NW + w;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
+                                                 (i % (R / 8)) * 8 + (L >> 3) < len ? off[j] : kOOB, 0, 0, 0);
       }
     }
-  // (left out of the host's pass, which drops kernels that call it from here)
-    __device__ __forceinline__ void issue(const void* rows, int len, char* t) const {
-#if __HIP_DEVICE_COMPILE__
-      const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
-      const int L = lane_id(), w = wave_id() % NW;
-      if (len >= R) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + w * 1024 + j * (NW * 1024)), 16, off[j], 0, 0, 0);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int i = j * NW + w;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
-                                                   (i % (R / 8)) * 8 + (L >> 3) < len ? off[j] : kOOB, 0, 0, 0);
-        }
-      }
 #endif
-    }
-  };
+  }
+};
 
 // 64 rows of a wave group's own columns: NW waves with 16 columns each, row by row.
 template <typename T, int NW> struct Columns {
   static constexpr int kPitch = 16 * NW * (int)sizeof(T), kBytes = kDC * kPitch;
-  static constexpr int N = kBytes / 1024 / NW, GPR = kPitch / 16, RPI = 64 / GPR;   // 16-byte pieces a row, rows a load
+  static constexpr int N = kBytes / 1024, GPR = kPitch / 16, RPI = 64 / GPR;   // 16-byte pieces a row, rows a load
   unsigned off[N];
   // cols: valid columns from this group's first on
   __device__ __forceinline__ Columns(unsigned pitch, int cols) {
-    const int L = lane_id(), w = wave_id() % NW, c = L % GPR;
+    const int L = lane_id(), c = L % GPR;
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      off[j] = c * (16 / (int)sizeof(T)) < cols ? (unsigned)((j * NW + w) * RPI + L / GPR) * pitch + c * 16u : kOOB;
+      off[j] = c * (16 / (int)sizeof(T)) < cols ? (unsigned)(j * RPI + L / GPR) * pitch + c * 16u : kOOB;
   }
   __device__ __forceinline__ void issue(const void* rows, int len, char* t) const {
     const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
-    const int L = lane_id(), w = wave_id() % NW;
+    const int L = lane_id();
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + (j * NW + w) * 1024), 16,
-                                               (j * NW + w) * RPI + L / GPR < len ? off[j] : kOOB, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + j * 1024), 16,
+                                               j * RPI + L / GPR < len ? off[j] : kOOB, 0, 0, 0);
   }
   // Column lane & 15 of wave w's, rows Mat::row(tile, 4 g + 0..3), as it lies in LDS and widened.
   using Raw = typename std::conditional<sizeof(T) == 2, u32x2, f32x4>::type;
@@ -260,18 +256,96 @@ template <typename T, int NW> struct Columns {
   __device__ static __forceinline__ f32x4 wide(f32x4 x) { return x; }
 };
 
-// `N` KB that lie one after the other, by NW waves.
-template <int N, int NW>
+// `N` KB that lie one after the other, by one wave.
+template <int N>
 __device__ __forceinline__ void load_block(const void* base, char* t) {
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, N * 1024);
-  const int w = wave_id() % NW;
 #pragma unroll
-  for (int j = 0; j < (N + NW - 1) / NW; ++j) {
-    const int i = j * NW + w;
-    if (N % NW == 0 || i < N)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, (unsigned)(i * 1024 + lane_id() * 16),
-                                               0, 0, 0);
+  for (int i = 0; i < N; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, (unsigned)(i * 1024 + lane_id() * 16),
+                                             0, 0, 0);
+}
+
+// Waits until at most N of this wave's memory operations are under way.
+template <int N> __device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "vmcnt has 6 bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// One load a 128-byte line brings what a later DMA will read into this XCD's
+// L2: N lines of each of up to 64 rows, or 64 N lines that follow one another.
+template <int N>
+__device__ __forceinline__ void touch_rows(const void* rows, int len, unsigned pitch, unsigned row_bytes, unsigned* t) {
+  const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
+  const int L = lane_id();
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    t[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, L < len && i * 128u < row_bytes ? (unsigned)L * pitch + i * 128u : kOOB,
+                                                0, 0);
+}
+template <int N> __device__ __forceinline__ void touch_block(const void* base, unsigned bytes, unsigned* t) {
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, bytes);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    t[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (unsigned)(i * 64 + lane_id()) * 128u, 0, 0);
+}
+
+// The DMA wave of a walk of `chunks` chunks: issue(i) brings what the i-th
+// turn works on, touch(i, t) reaches for a later turn's lines.  With two
+// stages turn i's work hides turn i + 1's loads, with one they follow one
+// another.  Turns: one more than there are chunks, with EXTRA.
+template <int STAGES, bool EXTRA, int TOUCH, typename I, typename P>
+__device__ __forceinline__ void dma_wave(int chunks, I issue, P touch) {
+  if (chunks == 0) return;
+  const int turns = chunks + (EXTRA ? 1 : 0);
+  unsigned t[TOUCH];
+#pragma unroll
+  for (int j = 0; j < TOUCH; ++j) t[j] = 0;
+  if (STAGES == 2) {
+    issue(0);
+    __builtin_amdgcn_sched_barrier(0);               // the waits count on this order
+    touch(1, t);
+    __builtin_amdgcn_sched_barrier(0);
   }
+  for (int i = 0; i < turns; ++i) {
+    if (STAGES == 1) {
+      if (i > 0) __syncthreads();                    // the stage has been read
+      issue(i);
+      wait_vm<0>();
+    } else {
+      wait_vm<TOUCH>();                              // all but the last touches
+    }
+    __syncthreads();
+    if (STAGES == 2) {
+#pragma unroll
+      for (int j = 0; j < TOUCH; ++j) asm volatile("" ::"v"(t[j]));
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 1 < turns) issue(i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      touch(i + 2, t);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+// The other waves' side of a turn.
+template <int STAGES> __device__ __forceinline__ void next_turn(bool first) {
+  if (STAGES == 1 && !first) __syncthreads();
+  __syncthreads();
+}
+
+// Which (sequence, value head, part of dv) a workgroup of a walk has.  The
+// workgroups of a key head read the same K (and Q): they go to one XCD, whose
+// L2 then brings it once; the key heads (of all sequences, in order) are dealt
+// to the XCDs in turn, so that long sequences spread over the chip.
+struct WalkPlace {
+  int seq, h, part;
+};
+inline __host__ __device__ int64_t walk_blocks(int64_t units, int64_t per) { return (units + 7) / 8 * 8 * per; }
+__device__ __forceinline__ bool walk_place(int bid, int sequences, int Hk, int group, int parts, WalkPlace* o) {
+  const int per = group * parts, unit = bid / 8 / per * 8 + (bid & 7), j = bid / 8 % per;
+  if (unit >= sequences * Hk) return false;
+  *o = {unit / Hk, unit % Hk * group + j / parts, j % parts};
+  return true;
 }
 
 // ------------------------------------------------------------------ sequences and their chunks

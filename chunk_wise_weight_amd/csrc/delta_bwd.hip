@@ -32,36 +32,52 @@ template <typename T, int DK, int NW, int STAGES> struct WalkBack {
   static constexpr int kK = 0, kQ = Panels<T>::bytes(DK), kRec = 2 * kQ, kD = kRec + ChunkRecT<T>::kBytes;
   static constexpr int kStage = kD + Columns<T, NW>::kBytes;
   static constexpr int kSmem = STAGES * kStage;
+  static constexpr int kLines = DK * (int)sizeof(T) / 128, kRecLines = (ChunkRecT<T>::kBytes + 8191) / 8192;
+  static constexpr int kTouch = 2 * kLines + kRecLines + 1;
 };
 
 template <typename T, int DK, int NW, int STAGES>
-__device__ __forceinline__ void walk_back(const DeltaGradArgs& a, const char* rec, void* dstates, void* xs, int part,
-                                          int h, int seq, const SeqPlace& sp, char* smem) {
+__device__ __forceinline__ void walk_back_loads(const DeltaGradArgs& a, const WalkPlace& at, const SeqPlace& sp,
+                                                char* smem) {
+  using G = WalkBack<T, DK, NW, STAGES>;
+  const DeltaArgs& p = a.f;
+  const int first = at.part * NW * 16, kh = at.h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
+  const unsigned kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T), dp = a.sdo.t * sizeof(T), row = p.dk * sizeof(T);
+  const T* k0 = (const T*)p.k + sp.b * p.sk.b + kh * p.sk.h + sp.tok0 * p.sk.t;
+  const T* q0 = (const T*)p.q + sp.b * p.sq.b + kh * p.sq.h + sp.tok0 * p.sq.t;
+  const T* d0 = (const T*)a.dO + sp.b * a.sdo.b + at.h * a.sdo.h + sp.tok0 * a.sdo.t + first;
+  const char* rec0 = a.rect + ((int64_t)sp.slot0 * p.Hv + at.h) * ChunkRecT<T>::kBytes;
+  const int64_t rstep = (int64_t)p.Hv * ChunkRecT<T>::kBytes;
+  const PanelLoader<T, DK, 1> kload(kp, row), qload(qp, row);
+  const Columns<T, NW> dload(dp, p.dv - first);
+  auto issue = [&](int turn) {
+    const int c = chunks - 1 - turn, len = min(kDC, sp.len - c * kDC);
+    char* st = smem + turn % STAGES * G::kStage;
+    kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
+    qload.issue(q0 + (int64_t)c * kDC * p.sq.t, len, st + G::kQ);
+    load_block<ChunkRecT<T>::kBytes / 1024>(rec0 + c * rstep, st + G::kRec);
+    dload.issue(d0 + (int64_t)c * kDC * a.sdo.t, len, st + G::kD);
+  };
+  auto touch = [&](int turn, unsigned* t) {
+    const int c = max(chunks - 1 - turn, 0), len = min(kDC, sp.len - c * kDC);
+    touch_rows<G::kLines>(k0 + (int64_t)c * kDC * p.sk.t, len, kp, row, t);
+    touch_rows<G::kLines>(q0 + (int64_t)c * kDC * p.sq.t, len, qp, row, t + G::kLines);
+    touch_block<G::kRecLines>(rec0 + c * rstep, ChunkRecT<T>::kBytes, t + 2 * G::kLines);
+    touch_rows<1>(d0 + (int64_t)c * kDC * a.sdo.t, len, dp, 1, t + 2 * G::kLines + G::kRecLines);
+  };
+  dma_wave<STAGES, false, G::kTouch>(chunks, issue, touch);
+}
+
+template <typename T, int DK, int NW, int STAGES>
+__device__ __forceinline__ void walk_back(const DeltaGradArgs& a, int w, const WalkPlace& at, const SeqPlace& sp,
+                                          const char* smem) {
   using M = Mat<T>;
   using G = WalkBack<T, DK, NW, STAGES>;
   const DeltaArgs& p = a.f;
   constexpr int ST = DK / 16, SS = G::SS, CS = kDC / M::KB;
-  const int w = wave_id() % NW, lane = lane_id(), m = lane & 15, g = lane >> 4;
-  const int first = part * NW * 16, col = first + w * 16 + m;
-  const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
-  const unsigned kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T), dp = a.sdo.t * sizeof(T), row = p.dk * sizeof(T);
-  const T* k0 = (const T*)p.k + sp.b * p.sk.b + kh * p.sk.h + sp.tok0 * p.sk.t;
-  const T* q0 = (const T*)p.q + sp.b * p.sq.b + kh * p.sq.h + sp.tok0 * p.sq.t;
-  const T* d0 = (const T*)a.dO + sp.b * a.sdo.b + h * a.sdo.h + sp.tok0 * a.sdo.t + first;
-  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRecT<T>::kBytes;
-  const int64_t rstep = (int64_t)p.Hv * ChunkRecT<T>::kBytes;
-
-  const PanelLoader<T, DK, NW> kload(kp, row), qload(qp, row);
-  const Columns<T, NW> dload(dp, p.dv - first);
-  auto fetch = [&](int c) {
-    char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
-    const int len = min(kDC, sp.len - c * kDC);
-    kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
-    qload.issue(q0 + (int64_t)c * kDC * p.sq.t, len, st + G::kQ);
-    load_block<ChunkRecT<T>::kBytes / 1024, NW>(rec0 + c * rstep, st + G::kRec);
-    dload.issue(d0 + (int64_t)c * kDC * a.sdo.t, len, st + G::kD);
-  };
-  if (STAGES == 2 && chunks > 0) fetch(chunks - 1);
+  const int lane = lane_id(), m = lane & 15, g = lane >> 4, h = at.h, seq = at.seq;
+  const int col = (at.part * NW + w) * 16 + m, chunks = (sp.len + kDC - 1) / kDC;
+  void *dstates = a.dstates, *xs = a.xs;
   f32x4 S[ST];                    // dS': block t, register r: dk = row(t, 4 g + r), dv = col
   const int64_t wbase = (((int64_t)seq * p.Hv + h) * p.dv + col) * p.dk;
 #pragma unroll
@@ -72,14 +88,8 @@ __device__ __forceinline__ void walk_back(const DeltaGradArgs& a, const char* re
   }
 
   for (int c = chunks - 1; c >= 0; --c) {
-    const char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
-    if (STAGES == 1) {
-      if (c < chunks - 1) __syncthreads();
-      fetch(c);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0f70);              // vmcnt(0): this chunk's loads
-    __syncthreads();
-    if (STAGES == 2 && c > 0) fetch(c - 1);
+    const char* st = smem + (chunks - 1 - c) % STAGES * G::kStage;
+    next_turn<STAGES>(c == chunks - 1);
     const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRecT<T>::kGate);
     const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
     u32x4 Sh[SS], Sl[SS];
@@ -162,18 +172,27 @@ __device__ __forceinline__ void walk_back(const DeltaGradArgs& a, const char* re
 
 // Both walks: the first half of the workgroups goes forward, the second back.
 template <typename T, int DK, int NW, int SF, int SB>
-__global__ __launch_bounds__(64 * NW) void k_delta_walks(DeltaGradArgs a) {
+__global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, int sequences) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const DeltaArgs& p = a.f;
-  const int half = gridDim.x / 2, parts = (p.dv + 16 * NW - 1) / (16 * NW);
+  const int half = gridDim.x / 2;
   const bool back = (int)blockIdx.x >= half;
-  const int id = xcd_remap(back ? blockIdx.x - half : blockIdx.x, half);
-  const int part = id % parts, h = (id / parts) % p.Hv, seq = id / parts / p.Hv;
-  const SeqPlace sp = seq_place(p.seqs, seq);
-  if (back)
-    walk_back<T, DK, NW, SB>(a, a.rect, a.dstates, a.xs, part, h, seq, sp, smem);
-  else
-    walk_states<T, DK, NW, SF, false>(p, a.rec, a.states, a.errors, part, h, seq, sp, smem);
+  WalkPlace at;
+  if (!walk_place(back ? blockIdx.x - half : blockIdx.x, sequences, p.Hk, p.Hv / p.Hk,
+                  (p.dv + 16 * NW - 1) / (16 * NW), &at))
+    return;
+  const SeqPlace sp = seq_place(p.seqs, at.seq);
+  const int w = wave_id();
+  if (back) {
+    if (w == 0)
+      walk_back_loads<T, DK, NW, SB>(a, at, sp, smem);
+    else
+      walk_back<T, DK, NW, SB>(a, w - 1, at, sp, smem);
+  } else if (w == 0) {
+    walk_loads<T, DK, NW, SF, false, false>(p, a.rec, at, sp, smem);
+  } else {
+    walk_states<T, DK, NW, SF, false, false>(p, w - 1, a.states, a.errors, at, sp, smem);
+  }
 }
 
 // ------------------------------------------------------------------ what is local to a chunk
@@ -495,9 +514,9 @@ hipError_t with_smem(F kern, int bytes) {
 template <typename T, int DK, int NW>
 hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hipStream_t s) {
   constexpr int kMax = 160 * 1024;
-  constexpr int SF = Walk<T, DK, NW, 2, false>::kSmem <= kMax ? 2 : 1;
+  constexpr int SF = Walk<T, DK, NW, 2, false, false>::kSmem <= kMax ? 2 : 1;
   constexpr int SB = WalkBack<T, DK, NW, 2>::kSmem <= kMax ? 2 : 1;
-  constexpr int F = Walk<T, DK, NW, SF, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
+  constexpr int F = Walk<T, DK, NW, SF, false, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
   static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 2048, "LDS of a CU");
   auto walks = k_delta_walks<T, DK, NW, SF, SB>;
   auto grads = k_delta_grads<T, DK>;
@@ -507,8 +526,9 @@ hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hi
   }();
   if (set != hipSuccess) return set;
   if (sequences > 0) {
-    const int64_t parts = (a.f.dv + 16 * NW - 1) / (16 * NW);
-    walks<<<dim3((unsigned)(2 * parts * a.f.Hv * sequences)), 64 * NW, W, s>>>(a);
+    const int64_t blocks =
+        walk_blocks((int64_t)sequences * a.f.Hk, a.f.Hv / a.f.Hk * ((a.f.dv + 16 * NW - 1) / (16 * NW)));
+    walks<<<dim3((unsigned)(2 * blocks)), 64 * (1 + NW), W, s>>>(a, sequences);
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (slots > 0) grads<<<dim3((unsigned)(slots * a.f.Hk)), 256, Grads<T, DK>::kSmem, s>>>(a);

@@ -199,48 +199,80 @@ __device__ __forceinline__ void put_state(const u32x4 (&S)[SS], T* W, int dk, bo
 // A workgroup walks one sequence of one value head with NW state waves, each
 // keeping 16 columns of the state (dv), which need nothing of the others.
 // A state wave's chunk is a chain of dependent products (K S, T R, K^T E), so
-// everything that can leave it has left it: with OUT as many helper waves, one
-// chunk behind, make O from the state and the errors that the state waves left
-// in LDS, their Q and P coming straight from memory a chunk ahead.  K, the
-// chunk's record and the group's columns of V are brought to LDS by DMA while
-// the chunk before is worked on (STAGES = 2; the widest heads have room for one
-// stage only).  One barrier a chunk.  Without OUT (the backward's recompute)
-// the states before each chunk and the errors go to memory instead.
-template <typename T, int DK, int NW, int STAGES, bool OUT> struct Walk {
+// everything that can leave it has left it.  Wave 0 brings each chunk's K, T,
+// gates and the group's columns of V to LDS by DMA while the chunk before is
+// worked on (two stages; the widest heads have room for one only), and reaches
+// for the chunk behind that, so that the DMA finds it in L2.  With OUT as many
+// helper waves, one chunk behind, make O from the state and the errors that
+// the state waves left in LDS; their Q and P come with the DMA too, where
+// there is room, else straight from memory.  One barrier a chunk.  Without OUT
+// (the backward's recompute) the states before each chunk and the errors go to
+// memory instead.
+template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS> struct Walk {
   static constexpr int SS = DK / Mat<T>::KB;
   static constexpr int kK = 0, kRec = Panels<T>::bytes(DK), kV = kRec + ChunkRec<T>::kP;
   static constexpr int kStage = kV + Columns<T, NW>::kBytes;
+  // the helpers' stages: gates and P, then Q
+  static constexpr int kG = STAGES * kStage, kQ = ChunkRec<T>::kBytes - ChunkRec<T>::kGate;
+  static constexpr int kStageQ = OUT && QLDS ? kQ + Panels<T>::bytes(DK) : 0;
+  static constexpr int kSwap = kG + STAGES * kStageQ;      // a state wave's state operands and errors (fp32), twice
+  static constexpr int kSwapBytes = SS * 1024 + 4096;
+  static constexpr int kSmem = kSwap + (OUT ? 2 * NW * kSwapBytes : 0);
+  static constexpr int kThreads = 64 * (1 + NW * (OUT ? 2 : 1));
   static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
-  static constexpr int kSwap = SS * 1024 + 4096;           // a state wave's state operands and errors (fp32)
-  static constexpr int kSmem = STAGES * kStage + (OUT ? 2 * NW * kSwap : 0);
-  static constexpr int kThreads = 64 * NW * (OUT ? 2 : 1);
+  static constexpr int kLines = DK * (int)sizeof(T) / 128;
+  static constexpr int kRecLines = (ChunkRec<T>::kBytes + 8191) / 8192;
+  static constexpr int kTouch = kLines * (OUT && QLDS ? 2 : 1) + 1 + kRecLines;
 };
 
-template <typename T, int DK, int NW, int STAGES, bool OUT>
-__device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec, void* states, void* errors, int part,
-                                            int h, int seq, const SeqPlace& sp, char* smem) {
-  using M = Mat<T>;
-  using G = Walk<T, DK, NW, STAGES, OUT>;
-  constexpr int ST = DK / 16, SS = G::SS, CS = kDC / M::KB;   // state blocks, steps over dk, steps over the tokens
-  const int w = wave_id() % NW, lane = lane_id(), m = lane & 15, g = lane >> 4;
-  const int first = part * NW * 16, col = first + w * 16 + m;
-  const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
-  const unsigned kp = p.sk.t * sizeof(T), vp = p.sv.t * sizeof(T), krow = p.dk * sizeof(T);
+template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS>
+__device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, const WalkPlace& at, const SeqPlace& sp,
+                                           char* smem) {
+  using G = Walk<T, DK, NW, STAGES, OUT, QLDS>;
+  const int first = at.part * NW * 16, kh = at.h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
+  const unsigned kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T), vp = p.sv.t * sizeof(T), row = p.dk * sizeof(T);
   const T* k0 = (const T*)p.k + sp.b * p.sk.b + kh * p.sk.h + sp.tok0 * p.sk.t;
-  const T* v0 = (const T*)p.v + sp.b * p.sv.b + h * p.sv.h + sp.tok0 * p.sv.t + first;
-  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes;
+  const T* q0 = (const T*)p.q + sp.b * p.sq.b + kh * p.sq.h + sp.tok0 * p.sq.t;
+  const T* v0 = (const T*)p.v + sp.b * p.sv.b + at.h * p.sv.h + sp.tok0 * p.sv.t + first;
+  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + at.h) * ChunkRec<T>::kBytes;
   const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
-
-  const PanelLoader<T, DK, NW> kload(kp, krow);
+  const PanelLoader<T, DK, 1> kload(kp, row), qload(qp, row);
   const Columns<T, NW> vload(vp, p.dv - first);
-  auto fetch = [&](int c) {
-    char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
-    const int len = min(kDC, sp.len - c * kDC);
-    kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
-    load_block<ChunkRec<T>::kP / 1024, NW>(rec0 + c * rstep, st + G::kRec);
-    vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
+  // turn c: the state waves at chunk c, the helpers at c - 1
+  auto issue = [&](int c) {
+    if (c < chunks) {
+      char* st = smem + c % STAGES * G::kStage;
+      const int len = min(kDC, sp.len - c * kDC);
+      kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
+      load_block<ChunkRec<T>::kP / 1024>(rec0 + c * rstep, st + G::kRec);
+      vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
+    }
+    if (OUT && QLDS && c > 0) {
+      char* st = smem + G::kG + (c - 1) % STAGES * G::kStageQ;
+      qload.issue(q0 + (int64_t)(c - 1) * kDC * p.sq.t, min(kDC, sp.len - (c - 1) * kDC), st + G::kQ);
+      load_block<G::kQ / 1024>(rec0 + (c - 1) * rstep + ChunkRec<T>::kGate, st);
+    }
   };
-  if (STAGES == 2 && chunks > 0) fetch(0);
+  auto touch = [&](int c, unsigned* t) {
+    c = min(c, chunks - 1);                          // the same number of loads at every turn
+    const int len = min(kDC, sp.len - c * kDC);
+    touch_rows<G::kLines>(k0 + (int64_t)c * kDC * p.sk.t, len, kp, row, t);
+    touch_block<G::kRecLines>(rec0 + c * rstep, ChunkRec<T>::kBytes, t + G::kLines);
+    touch_rows<1>(v0 + (int64_t)c * kDC * p.sv.t, len, vp, 1, t + G::kLines + G::kRecLines);
+    if constexpr (OUT && QLDS)
+      touch_rows<G::kLines>(q0 + (int64_t)c * kDC * p.sq.t, len, qp, row, t + G::kLines + G::kRecLines + 1);
+  };
+  dma_wave<STAGES, OUT, G::kTouch>(chunks, issue, touch);
+}
+
+template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS>
+__device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* states, void* errors, const WalkPlace& at,
+                                            const SeqPlace& sp, char* smem) {
+  using M = Mat<T>;
+  using G = Walk<T, DK, NW, STAGES, OUT, QLDS>;
+  constexpr int ST = DK / 16, SS = G::SS, CS = kDC / M::KB;   // state blocks, steps over dk, steps over the tokens
+  const int lane = lane_id(), m = lane & 15, g = lane >> 4, h = at.h, seq = at.seq;
+  const int col = (at.part * NW + w) * 16 + m, chunks = (sp.len + kDC - 1) / kDC;
   // state block t, register r: dk = row(t, 4 g + r), dv = col
   f32x4 S[ST];
   const int64_t wbase = (((int64_t)seq * p.Hv + h) * p.dv + col) * p.dk;
@@ -252,15 +284,10 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
   }
 
   for (int c = 0; c < chunks; ++c) {
-    const char* st = smem + (STAGES == 2 ? (c & 1) * G::kStage : 0);
-    if (STAGES == 1) {
-      if (c > 0) __syncthreads();                    // the stage has been read
-      fetch(c);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0f70);              // vmcnt(0): this chunk's loads
-    __syncthreads();
+    const char* st = smem + c % STAGES * G::kStage;
+    next_turn<STAGES>(c == 0);
     const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRec<T>::kGate);
-    char* swap = smem + STAGES * G::kStage + ((c & 1) * NW + w) * G::kSwap + lane * 16;
+    char* swap = smem + G::kSwap + ((c & 1) * NW + w) * G::kSwapBytes + lane * 16;
     const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
 
     // Reads from LDS go out ahead of the arithmetic that hides them: one wave a SIMD has nobody else to do it.
@@ -282,15 +309,14 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
       left[t] = *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
     }
     const float decay = gate[63];
-    if (STAGES == 2 && c + 1 < chunks) fetch(c + 1);
     __builtin_amdgcn_sched_barrier(0);
     u32x4 Sh[SS], Sl[SS];
 #pragma unroll
-    for (int s = 0; s < SS; ++s) M::split(S + s * M::TPS, Sh[s], Sl[s]);
-    if constexpr (OUT) {
-#pragma unroll
-      for (int s = 0; s < SS; ++s) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
-    } else {
+    for (int s = 0; s < SS; ++s) {
+      M::split(S + s * M::TPS, Sh[s], Sl[s]);
+      if constexpr (OUT) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
+    }
+    if constexpr (!OUT) {
       put_state<T, SS>(Sh, (T*)states + (slot * p.dv + col) * p.dk, p.dk, col < p.dv);
     }
     // V - exp(b) K S
@@ -367,10 +393,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
         if (M::kSplit) S[t] = M::mma(f, Rl[s], S[t]);
       }
   }
-  if (OUT && chunks > 0) {
-    if (STAGES == 1) __syncthreads();
-    __syncthreads();                                 // the helpers' last turn
-  }
+  if (OUT && chunks > 0) next_turn<STAGES>(false);   // the helpers' last one
   if (p.W_final) {
 #pragma unroll
     for (int t = 0; t < ST; ++t) {
@@ -381,79 +404,65 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, const char* rec,
 }
 
 // The helpers' side: O of chunk c while the state waves are at chunk c + 1.
-template <typename T, int DK, int NW, int STAGES>
-__device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec, int part, int h, const SeqPlace& sp,
-                                             const char* smem) {
+template <typename T, int DK, int NW, int STAGES, bool QLDS>
+__device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec, int w, const WalkPlace& at,
+                                             const SeqPlace& sp, const char* smem) {
   using M = Mat<T>;
-  using G = Walk<T, DK, NW, STAGES, true>;
+  using G = Walk<T, DK, NW, STAGES, true, QLDS>;
   constexpr int SS = G::SS, CS = kDC / M::KB;
-  constexpr bool AHEAD = SS <= 8;                    // Q a chunk ahead in registers, where it leaves room
-  const int w = wave_id() % NW, lane = lane_id(), m = lane & 15, g = lane >> 4;
-  const int col0 = (part * NW + w) * 16 + g * 4;
+  const int lane = lane_id(), m = lane & 15, g = lane >> 4, h = at.h;
+  const int col0 = (at.part * NW + w) * 16 + g * 4;
   const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
   const unsigned qp = p.sq.t * sizeof(T), qrow = p.dk * sizeof(T);
   const T* q0 = (const T*)p.q + sp.b * p.sq.b + kh * p.sq.h + sp.tok0 * p.sq.t;
   T* o0 = (T*)p.O + sp.b * p.so.b + h * p.so.h + sp.tok0 * p.so.t + col0;
-  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes;
+  const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes + ChunkRec<T>::kGate;
   const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
-  u32x4 Q[AHEAD ? 4 : 1][SS], P[M::kTri];
-  float ga[4];
-  auto fetch_q = [&](int c, int t, u32x4 (&q)[SS]) {
-    const int len = min(kDC, sp.len - c * kDC), r = M::row(t, m);
+  if (chunks > 0) next_turn<STAGES>(true);
+  for (int c = 0; c < chunks; ++c) {
+    next_turn<STAGES>(false);
+    const int len = min(kDC, sp.len - c * kDC);
+    const char* swap = smem + G::kSwap + ((c & 1) * NW + w) * G::kSwapBytes + lane * 16;
+    const char* st = smem + G::kG + c % STAGES * G::kStageQ;
+    const char* gp = QLDS ? st : rec0 + c * rstep;           // gates, P
     const __amdgpu_buffer_rsrc_t rq = rows_rsrc(q0 + (int64_t)c * kDC * p.sq.t);
-#pragma unroll
-    for (int s = 0; s < SS; ++s) {
-      const unsigned byte = s * 64u + g * 16u;
-      q[s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
-    }
-  };
-  auto fetch = [&](int c) {
-    if constexpr (AHEAD)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) fetch_q(c, t, Q[t]);
-    const char* r = rec0 + c * rstep;
-#pragma unroll
-    for (int f = 0; f < M::kTri; ++f) P[f] = *reinterpret_cast<const u32x4*>(r + ChunkRec<T>::kP + f * 1024 + lane * 16);
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      ga[t] = reinterpret_cast<const float*>(r + ChunkRec<T>::kGate)[M::row(t, m)];
-  };
-  if (chunks > 0) fetch(0);
-  for (int c = 0; c <= chunks; ++c) {
-    if (STAGES == 1 && c > 0) __syncthreads();
-    __syncthreads();
-    if (c == 0) continue;
-    const int d = c - 1, len = min(kDC, sp.len - d * kDC);     // the chunk whose O is made
-    const char* swap = smem + STAGES * G::kStage + ((d & 1) * NW + w) * G::kSwap + lane * 16;
-    u32x4 Eh[CS], El[CS];
-#pragma unroll
-    for (int s = 0; s < CS; ++s) {
-      f32x4 e[M::TPS];
-#pragma unroll
-      for (int t = 0; t < M::TPS; ++t)
-        e[t] = *reinterpret_cast<const f32x4*>(swap + SS * 1024 + (s * M::TPS + t) * 1024);
-      M::split(e, Eh[s], El[s]);
-    }
-    u32x4 Sh[SS];
+    u32x4 Sh[SS], Eh[CS], El[CS];
 #pragma unroll
     for (int s = 0; s < SS; ++s) Sh[s] = *reinterpret_cast<const u32x4*>(swap + s * 1024);
+    f32x4 e[4], o[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) e[t] = *reinterpret_cast<const f32x4*>(swap + SS * 1024 + t * 1024);
+#pragma unroll
+    for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Eh[s], El[s]);
     // the state's columns in the instruction's rows, tokens in its columns: a lane gets 4 columns of one token
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if constexpr (!AHEAD) fetch_q(d, t, Q[0]);
       const int r = M::row(t, m);
-      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+      u32x4 q[SS];
 #pragma unroll
-      for (int s = 0; s < SS; ++s) o = M::mma(Sh[s], Q[AHEAD ? t : 0][s], o);
-      o *= p.scale * ga[t];
+      for (int s = 0; s < SS; ++s) {
+        const unsigned byte = s * 64u + g * 16u;
+        q[s] = QLDS ? Panels<T>::frag(st + G::kQ, r, s, g)
+                    : __builtin_amdgcn_raw_buffer_load_b128(
+                          rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
+      }
+      o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < SS; ++s) o[t] = M::mma(Sh[s], q[s], o[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int r = M::row(t, m);
+      o[t] *= p.scale * reinterpret_cast<const float*>(gp)[r];
 #pragma unroll
       for (int s = 0; s < M::steps(t); ++s) {
-        o = M::mma(Eh[s], P[M::tri(t, s)], o);
-        if (M::kSplit) o = M::mma(El[s], P[M::tri(t, s)], o);
+        const u32x4 f = *reinterpret_cast<const u32x4*>(gp + 1024 + M::tri(t, s) * 1024 + lane * 16);
+        o[t] = M::mma(Eh[s], f, o[t]);
+        if (M::kSplit) o[t] = M::mma(El[s], f, o[t]);
       }
-      if (r < len && col0 < p.dv) store4(o0 + (int64_t)(d * kDC + r) * p.so.t, o[0], o[1], o[2], o[3]);
+      if (r < len && col0 < p.dv)
+        store4(o0 + (int64_t)(c * kDC + r) * p.so.t, o[t][0], o[t][1], o[t][2], o[t][3]);
     }
-    if (c < chunks) fetch(c);
   }
 }
 
