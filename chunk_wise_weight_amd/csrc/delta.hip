@@ -6,17 +6,16 @@ namespace {
 
 template <typename T, int DK, int NW, int STAGES, bool QLDS>
 __global__ __launch_bounds__(64 * (1 + 2 * NW)) void k_delta_walk(DeltaArgs p, const char* rec, int sequences) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
   WalkPlace at;
   if (!walk_place(blockIdx.x, sequences, p.Hk, p.Hv / p.Hk, (p.dv + 16 * NW - 1) / (16 * NW), &at)) return;
   const SeqPlace sp = seq_place(p.seqs, at.seq);
   const int w = wave_id();
   if (w == 0)
-    walk_loads<T, DK, NW, STAGES, true, QLDS>(p, rec, at, sp, smem);
+    walk_loads<T, DK, NW, STAGES, true, QLDS>(p, rec, at, sp);
   else if (w <= NW)
-    walk_states<T, DK, NW, STAGES, true, QLDS>(p, w - 1, nullptr, nullptr, at, sp, smem);
+    walk_states<T, DK, NW, STAGES, true, QLDS>(p, w - 1, nullptr, nullptr, at, sp);
   else
-    walk_outputs<T, DK, NW, STAGES, QLDS>(p, rec, w - 1 - NW, at, sp, smem);
+    walk_outputs<T, DK, NW, STAGES, QLDS>(p, rec, w - 1 - NW, at, sp);
 }
 
 template <typename T, int DK, int NW>

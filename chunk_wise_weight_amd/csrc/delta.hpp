@@ -272,67 +272,28 @@ template <int N> __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 
-// One load a 128-byte line brings what a later DMA will read into this XCD's
-// L2: N lines of each of up to 64 rows, or 64 N lines that follow one another.
-template <int N>
-__device__ __forceinline__ void touch_rows(const void* rows, int len, unsigned pitch, unsigned row_bytes, unsigned* t) {
-  const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
-  const int L = lane_id();
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    t[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, L < len && i * 128u < row_bytes ? (unsigned)L * pitch + i * 128u : kOOB,
-                                                0, 0);
-}
-template <int N> __device__ __forceinline__ void touch_block(const void* base, unsigned bytes, unsigned* t) {
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, bytes);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    t[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (unsigned)(i * 64 + lane_id()) * 128u, 0, 0);
-}
-
-// The DMA wave of a walk of `chunks` chunks: issue(i) brings what the i-th
-// turn works on, touch(i, t) reaches for a later turn's lines.  With two
-// stages turn i's work hides turn i + 1's loads, with one they follow one
-// another.  Turns: one more than there are chunks, with EXTRA.
-template <int STAGES, bool EXTRA, int TOUCH, typename I, typename P>
-__device__ __forceinline__ void dma_wave(int chunks, I issue, P touch) {
-  if (chunks == 0) return;
-  const int turns = chunks + (EXTRA ? 1 : 0);
-  unsigned t[TOUCH];
-#pragma unroll
-  for (int j = 0; j < TOUCH; ++j) t[j] = 0;
-  if (STAGES == 2) {
-    issue(0);
-    __builtin_amdgcn_sched_barrier(0);               // the waits count on this order
-    touch(1, t);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  for (int i = 0; i < turns; ++i) {
-    if (STAGES == 1) {
-      if (i > 0) __syncthreads();                    // the stage has been read
-      issue(i);
-      wait_vm<0>();
-    } else {
-      wait_vm<TOUCH>();                              // all but the last touches
-    }
-    __syncthreads();
-    if (STAGES == 2) {
-#pragma unroll
-      for (int j = 0; j < TOUCH; ++j) asm volatile("" ::"v"(t[j]));
-      __builtin_amdgcn_sched_barrier(0);
-      if (i + 1 < turns) issue(i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      touch(i + 2, t);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-}
-// The other waves' side of a turn.
+// A turn's barrier; with one stage another before it, when the stage has been read.
 template <int STAGES> __device__ __forceinline__ void next_turn(bool first) {
   if (STAGES == 1 && !first) __syncthreads();
   __syncthreads();
 }
 
+// The DMA wave of a walk: issue(i) brings what the i-th turn works on.  With
+// two stages turn i's work hides turn i + 1's loads, with one they follow one
+// another.
+template <int STAGES, typename I>
+__device__ __forceinline__ void dma_wave(int turns, I issue) {
+  if (STAGES == 2 && turns > 0) issue(0);
+  for (int i = 0; i < turns; ++i) {
+    if (STAGES == 1) {
+      if (i > 0) __syncthreads();
+      issue(i);
+    }
+    wait_vm<0>();
+    __syncthreads();
+    if (STAGES == 2 && i + 1 < turns) issue(i + 1);
+  }
+}
 // Which (sequence, value head, part of dv) a workgroup of a walk has.  The
 // workgroups of a key head read the same K (and Q): they go to one XCD, whose
 // L2 then brings it once; the key heads (of all sequences, in order) are dealt

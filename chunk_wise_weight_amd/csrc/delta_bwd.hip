@@ -32,13 +32,11 @@ template <typename T, int DK, int NW, int STAGES> struct WalkBack {
   static constexpr int kK = 0, kQ = Panels<T>::bytes(DK), kRec = 2 * kQ, kD = kRec + ChunkRecT<T>::kBytes;
   static constexpr int kStage = kD + Columns<T, NW>::kBytes;
   static constexpr int kSmem = STAGES * kStage;
-  static constexpr int kLines = DK * (int)sizeof(T) / 128, kRecLines = (ChunkRecT<T>::kBytes + 8191) / 8192;
-  static constexpr int kTouch = 2 * kLines + kRecLines + 1;
 };
 
 template <typename T, int DK, int NW, int STAGES>
-__device__ __forceinline__ void walk_back_loads(const DeltaGradArgs& a, const WalkPlace& at, const SeqPlace& sp,
-                                                char* smem) {
+__device__ __forceinline__ void walk_back_loads(const DeltaGradArgs& a, const WalkPlace& at, const SeqPlace& sp) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   using G = WalkBack<T, DK, NW, STAGES>;
   const DeltaArgs& p = a.f;
   const int first = at.part * NW * 16, kh = at.h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
@@ -50,7 +48,7 @@ __device__ __forceinline__ void walk_back_loads(const DeltaGradArgs& a, const Wa
   const int64_t rstep = (int64_t)p.Hv * ChunkRecT<T>::kBytes;
   const PanelLoader<T, DK, 1> kload(kp, row), qload(qp, row);
   const Columns<T, NW> dload(dp, p.dv - first);
-  auto issue = [&](int turn) {
+  auto issue = [&](int turn) __attribute__((always_inline)) {
     const int c = chunks - 1 - turn, len = min(kDC, sp.len - c * kDC);
     char* st = smem + turn % STAGES * G::kStage;
     kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
@@ -58,19 +56,12 @@ __device__ __forceinline__ void walk_back_loads(const DeltaGradArgs& a, const Wa
     load_block<ChunkRecT<T>::kBytes / 1024>(rec0 + c * rstep, st + G::kRec);
     dload.issue(d0 + (int64_t)c * kDC * a.sdo.t, len, st + G::kD);
   };
-  auto touch = [&](int turn, unsigned* t) {
-    const int c = max(chunks - 1 - turn, 0), len = min(kDC, sp.len - c * kDC);
-    touch_rows<G::kLines>(k0 + (int64_t)c * kDC * p.sk.t, len, kp, row, t);
-    touch_rows<G::kLines>(q0 + (int64_t)c * kDC * p.sq.t, len, qp, row, t + G::kLines);
-    touch_block<G::kRecLines>(rec0 + c * rstep, ChunkRecT<T>::kBytes, t + 2 * G::kLines);
-    touch_rows<1>(d0 + (int64_t)c * kDC * a.sdo.t, len, dp, 1, t + 2 * G::kLines + G::kRecLines);
-  };
-  dma_wave<STAGES, false, G::kTouch>(chunks, issue, touch);
+  dma_wave<STAGES>(chunks, issue);
 }
 
 template <typename T, int DK, int NW, int STAGES>
-__device__ __forceinline__ void walk_back(const DeltaGradArgs& a, int w, const WalkPlace& at, const SeqPlace& sp,
-                                          const char* smem) {
+__device__ __forceinline__ void walk_back(const DeltaGradArgs& a, int w, const WalkPlace& at, const SeqPlace& sp) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   using M = Mat<T>;
   using G = WalkBack<T, DK, NW, STAGES>;
   const DeltaArgs& p = a.f;
@@ -173,7 +164,6 @@ __device__ __forceinline__ void walk_back(const DeltaGradArgs& a, int w, const W
 // Both walks: the first half of the workgroups goes forward, the second back.
 template <typename T, int DK, int NW, int SF, int SB>
 __global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, int sequences) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
   const DeltaArgs& p = a.f;
   const int half = gridDim.x / 2;
   const bool back = (int)blockIdx.x >= half;
@@ -185,13 +175,13 @@ __global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, 
   const int w = wave_id();
   if (back) {
     if (w == 0)
-      walk_back_loads<T, DK, NW, SB>(a, at, sp, smem);
+      walk_back_loads<T, DK, NW, SB>(a, at, sp);
     else
-      walk_back<T, DK, NW, SB>(a, w - 1, at, sp, smem);
+      walk_back<T, DK, NW, SB>(a, w - 1, at, sp);
   } else if (w == 0) {
-    walk_loads<T, DK, NW, SF, false, false>(p, a.rec, at, sp, smem);
+    walk_loads<T, DK, NW, SF, false, false>(p, a.rec, at, sp);
   } else {
-    walk_states<T, DK, NW, SF, false, false>(p, w - 1, a.states, a.errors, at, sp, smem);
+    walk_states<T, DK, NW, SF, false, false>(p, w - 1, a.states, a.errors, at, sp);
   }
 }
 
@@ -367,7 +357,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
         rows += n * bj;
         cols[t][r] = n;
       }
-    auto put_m = [&](const f32x4 (&x)[4], int to) {          // rows of tokens i, columns j
+    auto put_m = [&](const f32x4 (&x)[4], int to) __attribute__((always_inline)) {          // rows of tokens i, columns j
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         store4(reinterpret_cast<T*>(smem + to + Panels<T>::at(i, M::row(t, g * 4))), x[t][0], x[t][1], x[t][2], x[t][3]);

@@ -201,8 +201,7 @@ __device__ __forceinline__ void put_state(const u32x4 (&S)[SS], T* W, int dk, bo
 // A state wave's chunk is a chain of dependent products (K S, T R, K^T E), so
 // everything that can leave it has left it.  Wave 0 brings each chunk's K, T,
 // gates and the group's columns of V to LDS by DMA while the chunk before is
-// worked on (two stages; the widest heads have room for one only), and reaches
-// for the chunk behind that, so that the DMA finds it in L2.  With OUT as many
+// worked on (two stages; the widest heads have room for one only).  With OUT as many
 // helper waves, one chunk behind, make O from the state and the errors that
 // the state waves left in LDS; their Q and P come with the DMA too, where
 // there is room, else straight from memory.  One barrier a chunk.  Without OUT
@@ -220,14 +219,12 @@ template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS> struct Wa
   static constexpr int kSmem = kSwap + (OUT ? 2 * NW * kSwapBytes : 0);
   static constexpr int kThreads = 64 * (1 + NW * (OUT ? 2 : 1));
   static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
-  static constexpr int kLines = DK * (int)sizeof(T) / 128;
-  static constexpr int kRecLines = (ChunkRec<T>::kBytes + 8191) / 8192;
-  static constexpr int kTouch = kLines * (OUT && QLDS ? 2 : 1) + 1 + kRecLines;
 };
 
 template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS>
-__device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, const WalkPlace& at, const SeqPlace& sp,
-                                           char* smem) {
+__device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, const WalkPlace& at,
+                                           const SeqPlace& sp) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   using G = Walk<T, DK, NW, STAGES, OUT, QLDS>;
   const int first = at.part * NW * 16, kh = at.h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
   const unsigned kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T), vp = p.sv.t * sizeof(T), row = p.dk * sizeof(T);
@@ -239,7 +236,7 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, 
   const PanelLoader<T, DK, 1> kload(kp, row), qload(qp, row);
   const Columns<T, NW> vload(vp, p.dv - first);
   // turn c: the state waves at chunk c, the helpers at c - 1
-  auto issue = [&](int c) {
+  auto issue = [&](int c) __attribute__((always_inline)) {
     if (c < chunks) {
       char* st = smem + c % STAGES * G::kStage;
       const int len = min(kDC, sp.len - c * kDC);
@@ -253,21 +250,13 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, 
       load_block<G::kQ / 1024>(rec0 + (c - 1) * rstep + ChunkRec<T>::kGate, st);
     }
   };
-  auto touch = [&](int c, unsigned* t) {
-    c = min(c, chunks - 1);                          // the same number of loads at every turn
-    const int len = min(kDC, sp.len - c * kDC);
-    touch_rows<G::kLines>(k0 + (int64_t)c * kDC * p.sk.t, len, kp, row, t);
-    touch_block<G::kRecLines>(rec0 + c * rstep, ChunkRec<T>::kBytes, t + G::kLines);
-    touch_rows<1>(v0 + (int64_t)c * kDC * p.sv.t, len, vp, 1, t + G::kLines + G::kRecLines);
-    if constexpr (OUT && QLDS)
-      touch_rows<G::kLines>(q0 + (int64_t)c * kDC * p.sq.t, len, qp, row, t + G::kLines + G::kRecLines + 1);
-  };
-  dma_wave<STAGES, OUT, G::kTouch>(chunks, issue, touch);
+  dma_wave<STAGES>(chunks > 0 ? chunks + (OUT ? 1 : 0) : 0, issue);
 }
 
 template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS>
 __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* states, void* errors, const WalkPlace& at,
-                                            const SeqPlace& sp, char* smem) {
+                                            const SeqPlace& sp) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   using M = Mat<T>;
   using G = Walk<T, DK, NW, STAGES, OUT, QLDS>;
   constexpr int ST = DK / 16, SS = G::SS, CS = kDC / M::KB;   // state blocks, steps over dk, steps over the tokens
@@ -294,7 +283,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
     u32x4 Kf[G::kHoist ? 4 : 1][SS], Th[M::kTri], Tl[M::kSplit ? M::kTri : 1];
     typename Columns<T, NW>::Raw v[4];
     f32x4 up[4], left[4];
-    auto read_k = [&](int t, u32x4 (&f)[SS]) {
+    auto read_k = [&](int t, u32x4 (&f)[SS]) __attribute__((always_inline)) {
       const int r = M::row(t, m);
 #pragma unroll
       for (int s = 0; s < SS; ++s) f[s] = Panels<T>::frag(st + G::kK, r, s, g);
@@ -406,7 +395,8 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
 // The helpers' side: O of chunk c while the state waves are at chunk c + 1.
 template <typename T, int DK, int NW, int STAGES, bool QLDS>
 __device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec, int w, const WalkPlace& at,
-                                             const SeqPlace& sp, const char* smem) {
+                                             const SeqPlace& sp) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
   using M = Mat<T>;
   using G = Walk<T, DK, NW, STAGES, true, QLDS>;
   constexpr int SS = G::SS, CS = kDC / M::KB;
