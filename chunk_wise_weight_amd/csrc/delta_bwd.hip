@@ -179,9 +179,9 @@ __global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, 
     else
       walk_back<T, DK, NW, SB>(a, w - 1, at, sp);
   } else if (w == 0) {
-    walk_loads<T, DK, NW, SF, false, false>(p, a.rec, at, sp);
+    walk_loads<T, DK, NW, SF, kKeep, false>(p, a.rec, at, sp);
   } else {
-    walk_states<T, DK, NW, SF, false, false>(p, w - 1, a.states, a.errors, at, sp);
+    walk_states<T, DK, NW, SF, kKeep, false>(p, w - 1, a.states, a.errors, at, sp);
   }
 }
 
@@ -504,9 +504,9 @@ hipError_t with_smem(F kern, int bytes) {
 template <typename T, int DK, int NW>
 hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hipStream_t s) {
   constexpr int kMax = 160 * 1024;
-  constexpr int SF = Walk<T, DK, NW, 2, false, false>::kSmem <= kMax ? 2 : 1;
+  constexpr int SF = Walk<T, DK, NW, 2, kKeep, false>::kSmem <= kMax ? 2 : 1;
   constexpr int SB = WalkBack<T, DK, NW, 2>::kSmem <= kMax ? 2 : 1;
-  constexpr int F = Walk<T, DK, NW, SF, false, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
+  constexpr int F = Walk<T, DK, NW, SF, kKeep, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
   static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 2048, "LDS of a CU");
   auto walks = k_delta_walks<T, DK, NW, SF, SB>;
   auto grads = k_delta_grads<T, DK>;

@@ -196,32 +196,85 @@ __device__ __forceinline__ void put_state(const u32x4 (&S)[SS], T* W, int dk, bo
   }
 }
 
+// O of a chunk's tokens at 16 columns, from operands of the state and the
+// errors (fp32): the columns in the instruction's rows, tokens in its columns,
+// so that a lane gets 4 columns of one token.  gp: the chunk's gates and P; Q
+// in panels at q, or from memory through rq.
+template <typename T, int SS, bool QLDS = true>
+__device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const f32x4 (&e)[4], const char* gp, const char* q,
+                                             float scale, int len, bool in, int64_t pitch, T* out,
+                                             const void* q_rows = nullptr, unsigned qp = 0, unsigned qrow = 0) {
+  using M = Mat<T>;
+  constexpr int CS = kDC / M::KB;
+  const int lane = lane_id(), m = lane & 15, g = lane >> 4;
+  u32x4 Eh[CS], El[CS];
+#pragma unroll
+  for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Eh[s], El[s]);
+  f32x4 o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = M::row(t, m);
+    u32x4 f[SS];
+    if constexpr (QLDS) {
+#pragma unroll
+      for (int s = 0; s < SS; ++s) f[s] = Panels<T>::frag(q, r, s, g);
+    } else {
+      const __amdgpu_buffer_rsrc_t rq = rows_rsrc(q_rows);
+#pragma unroll
+      for (int s = 0; s < SS; ++s) {
+        const unsigned byte = s * 64u + g * 16u;
+        f[s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
+      }
+    }
+    o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < SS; ++s) o[t] = M::mma(Sh[s], f[s], o[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = M::row(t, m);
+    o[t] *= scale * reinterpret_cast<const float*>(gp)[r];
+#pragma unroll
+    for (int s = 0; s < M::steps(t); ++s) {
+      const u32x4 f = *reinterpret_cast<const u32x4*>(gp + 1024 + M::tri(t, s) * 1024 + lane * 16);
+      o[t] = M::mma(Eh[s], f, o[t]);
+      if (M::kSplit) o[t] = M::mma(El[s], f, o[t]);
+    }
+    if (r < len && in) store4(out + (int64_t)r * pitch, o[t][0], o[t][1], o[t][2], o[t][3]);
+  }
+}
+
 // A workgroup walks one sequence of one value head with NW state waves, each
 // keeping 16 columns of the state (dv), which need nothing of the others.
-// A state wave's chunk is a chain of dependent products (K S, T R, K^T E), so
-// everything that can leave it has left it.  Wave 0 brings each chunk's K, T,
-// gates and the group's columns of V to LDS by DMA while the chunk before is
-// worked on (two stages; the widest heads have room for one only).  With OUT as many
-// helper waves, one chunk behind, make O from the state and the errors that
-// the state waves left in LDS; their Q and P come with the DMA too, where
-// there is room, else straight from memory.  One barrier a chunk.  Without OUT
-// (the backward's recompute) the states before each chunk and the errors go to
-// memory instead.
-template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS> struct Walk {
+// Wave 0 brings each chunk's K, T, gates and the group's columns of V to LDS by
+// DMA while the chunk before is worked on (two stages; the widest heads have
+// room for one only).  A state wave's chunk is a chain of dependent products
+// (K S, T R, K^T E).  One barrier a chunk.  By OUT:
+//   kHelped  as many helper waves, one chunk behind, make O from the state and
+//            the errors that the state waves left in LDS, their Q and P coming
+//            with the DMA too where there is room, else straight from memory:
+//            the shortest chain, for walks that do not fill the chip
+//   kOwn     the state waves make O themselves: four of them to a workgroup,
+//            one a SIMD, for walks that do
+//   kKeep    (the backward's recompute) no O: the states before each chunk and
+//            the errors go to memory
+enum { kKeep = 0, kHelped = 1, kOwn = 2 };
+template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS> struct Walk {
   static constexpr int SS = DK / Mat<T>::KB;
   static constexpr int kK = 0, kRec = Panels<T>::bytes(DK), kV = kRec + ChunkRec<T>::kP;
   static constexpr int kStage = kV + Columns<T, NW>::kBytes;
   // the helpers' stages: gates and P, then Q
   static constexpr int kG = STAGES * kStage, kQ = ChunkRec<T>::kBytes - ChunkRec<T>::kGate;
-  static constexpr int kStageQ = OUT && QLDS ? kQ + Panels<T>::bytes(DK) : 0;
+  static constexpr int kStageQ = OUT != kKeep && QLDS ? kQ + Panels<T>::bytes(DK) : 0;
   static constexpr int kSwap = kG + STAGES * kStageQ;      // a state wave's state operands and errors (fp32), twice
   static constexpr int kSwapBytes = SS * 1024 + 4096;
-  static constexpr int kSmem = kSwap + (OUT ? 2 * NW * kSwapBytes : 0);
-  static constexpr int kThreads = 64 * (1 + NW * (OUT ? 2 : 1));
+  static constexpr int kSmem = kSwap + (OUT == kHelped ? 2 * NW * kSwapBytes : 0);
+  static constexpr int kThreads = 64 * (1 + NW * (OUT == kHelped ? 2 : 1));
+  static constexpr int kLag = OUT == kHelped ? 1 : 0;      // turns that O is behind
   static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
 };
 
-template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS>
+template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS>
 __device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, const WalkPlace& at,
                                            const SeqPlace& sp) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -235,7 +288,7 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, 
   const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
   const PanelLoader<T, DK, 1> kload(kp, row), qload(qp, row);
   const Columns<T, NW> vload(vp, p.dv - first);
-  // turn c: the state waves at chunk c, the helpers at c - 1
+  // turn c: the state waves at chunk c, O at chunk c - kLag
   auto issue = [&](int c) __attribute__((always_inline)) {
     if (c < chunks) {
       char* st = smem + c % STAGES * G::kStage;
@@ -244,16 +297,17 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, 
       load_block<ChunkRec<T>::kP / 1024>(rec0 + c * rstep, st + G::kRec);
       vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
     }
-    if (OUT && QLDS && c > 0) {
-      char* st = smem + G::kG + (c - 1) % STAGES * G::kStageQ;
-      qload.issue(q0 + (int64_t)(c - 1) * kDC * p.sq.t, min(kDC, sp.len - (c - 1) * kDC), st + G::kQ);
-      load_block<G::kQ / 1024>(rec0 + (c - 1) * rstep + ChunkRec<T>::kGate, st);
+    const int d = c - G::kLag;
+    if (OUT != kKeep && QLDS && d >= 0) {
+      char* st = smem + G::kG + d % STAGES * G::kStageQ;
+      qload.issue(q0 + (int64_t)d * kDC * p.sq.t, min(kDC, sp.len - d * kDC), st + G::kQ);
+      load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, st);
     }
   };
-  dma_wave<STAGES>(chunks > 0 ? chunks + (OUT ? 1 : 0) : 0, issue);
+  dma_wave<STAGES>(chunks > 0 ? chunks + G::kLag : 0, issue);
 }
 
-template <typename T, int DK, int NW, int STAGES, bool OUT, bool QLDS>
+template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS>
 __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* states, void* errors, const WalkPlace& at,
                                             const SeqPlace& sp) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -276,7 +330,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
     const char* st = smem + c % STAGES * G::kStage;
     next_turn<STAGES>(c == 0);
     const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRec<T>::kGate);
-    char* swap = smem + G::kSwap + ((c & 1) * NW + w) * G::kSwapBytes + lane * 16;
+    [[maybe_unused]] char* swap = smem + G::kSwap + ((c & 1) * NW + w) * G::kSwapBytes + lane * 16;
     const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
 
     // Reads from LDS go out ahead of the arithmetic that hides them: one wave a SIMD has nobody else to do it.
@@ -303,9 +357,9 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
 #pragma unroll
     for (int s = 0; s < SS; ++s) {
       M::split(S + s * M::TPS, Sh[s], Sl[s]);
-      if constexpr (OUT) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
+      if constexpr (OUT == kHelped) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
     }
-    if constexpr (!OUT) {
+    if constexpr (OUT == kKeep) {
       put_state<T, SS>(Sh, (T*)states + (slot * p.dv + col) * p.dk, p.dk, col < p.dv);
     }
     // V - exp(b) K S
@@ -359,9 +413,14 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
             const int f = M::tri(t, s);
             e[t] = M::mma(i == 2 ? Tl[M::kSplit ? f : 0] : Th[f], i == 1 ? Rl[s] : Rh[s], e[t]);
           }
-    if constexpr (OUT) {
+    if constexpr (OUT == kHelped) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(swap + SS * 1024 + t * 1024) = e[t];
+    } else if constexpr (OUT == kOwn) {
+      const char* sq = smem + G::kG + c % STAGES * G::kStageQ;
+      const int len = min(kDC, sp.len - c * kDC), col0 = (at.part * NW + w) * 16 + g * 4;
+      T* o = (T*)p.O + sp.b * p.so.b + h * p.so.h + (int64_t)(sp.tok0 + c * kDC) * p.so.t + col0;
+      make_outputs<T, SS>(Sh, e, sq, sq + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o);
     } else {
       T* E = (T*)errors + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
 #pragma unroll
@@ -382,7 +441,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
         if (M::kSplit) S[t] = M::mma(f, Rl[s], S[t]);
       }
   }
-  if (OUT && chunks > 0) next_turn<STAGES>(false);   // the helpers' last one
+  if (OUT == kHelped && chunks > 0) next_turn<STAGES>(false);   // the helpers' last one
   if (p.W_final) {
 #pragma unroll
     for (int t = 0; t < ST; ++t) {
@@ -397,10 +456,9 @@ template <typename T, int DK, int NW, int STAGES, bool QLDS>
 __device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec, int w, const WalkPlace& at,
                                              const SeqPlace& sp) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  using M = Mat<T>;
-  using G = Walk<T, DK, NW, STAGES, true, QLDS>;
-  constexpr int SS = G::SS, CS = kDC / M::KB;
-  const int lane = lane_id(), m = lane & 15, g = lane >> 4, h = at.h;
+  using G = Walk<T, DK, NW, STAGES, kHelped, QLDS>;
+  constexpr int SS = G::SS;
+  const int lane = lane_id(), g = lane >> 4, h = at.h;
   const int col0 = (at.part * NW + w) * 16 + g * 4;
   const int kh = h / (p.Hv / p.Hk), chunks = (sp.len + kDC - 1) / kDC;
   const unsigned qp = p.sq.t * sizeof(T), qrow = p.dk * sizeof(T);
@@ -415,44 +473,14 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec
     const char* swap = smem + G::kSwap + ((c & 1) * NW + w) * G::kSwapBytes + lane * 16;
     const char* st = smem + G::kG + c % STAGES * G::kStageQ;
     const char* gp = QLDS ? st : rec0 + c * rstep;           // gates, P
-    const __amdgpu_buffer_rsrc_t rq = rows_rsrc(q0 + (int64_t)c * kDC * p.sq.t);
-    u32x4 Sh[SS], Eh[CS], El[CS];
+    u32x4 Sh[SS];
 #pragma unroll
     for (int s = 0; s < SS; ++s) Sh[s] = *reinterpret_cast<const u32x4*>(swap + s * 1024);
-    f32x4 e[4], o[4];
+    f32x4 e[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) e[t] = *reinterpret_cast<const f32x4*>(swap + SS * 1024 + t * 1024);
-#pragma unroll
-    for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Eh[s], El[s]);
-    // the state's columns in the instruction's rows, tokens in its columns: a lane gets 4 columns of one token
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = M::row(t, m);
-      u32x4 q[SS];
-#pragma unroll
-      for (int s = 0; s < SS; ++s) {
-        const unsigned byte = s * 64u + g * 16u;
-        q[s] = QLDS ? Panels<T>::frag(st + G::kQ, r, s, g)
-                    : __builtin_amdgcn_raw_buffer_load_b128(
-                          rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
-      }
-      o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < SS; ++s) o[t] = M::mma(Sh[s], q[s], o[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = M::row(t, m);
-      o[t] *= p.scale * reinterpret_cast<const float*>(gp)[r];
-#pragma unroll
-      for (int s = 0; s < M::steps(t); ++s) {
-        const u32x4 f = *reinterpret_cast<const u32x4*>(gp + 1024 + M::tri(t, s) * 1024 + lane * 16);
-        o[t] = M::mma(Eh[s], f, o[t]);
-        if (M::kSplit) o[t] = M::mma(El[s], f, o[t]);
-      }
-      if (r < len && col0 < p.dv)
-        store4(o0 + (int64_t)(c * kDC + r) * p.so.t, o[t][0], o[t][1], o[t][2], o[t][3]);
-    }
+    make_outputs<T, SS, QLDS>(Sh, e, gp, st + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o0 + (int64_t)c * kDC * p.so.t,
+                              q0 + (int64_t)c * kDC * p.sq.t, qp, qrow);
   }
 }
 
