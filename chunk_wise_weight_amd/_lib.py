@@ -4,8 +4,8 @@ declare (the C ABI sees only raw pointers), allocate outputs and workspace
 with torch on the tensors' device, and pass pointers and the current stream."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -215,6 +215,9 @@ def _stream(device: torch.device):
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype, device):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == device
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device.type != "cuda":
@@ -787,39 +790,81 @@ def ttt_lact_swiglu_backward(q, k, v, W1, W3, W2, dO, chunk: int, eta: float, or
 
 
 # ---------------------------------------------------------------------------------- gated delta rule, layer norm
+#
+# What follows from shapes, strides and types alone (checks, the C structs, workspace sizes) is made once for each
+# combination and kept; a call looks it up, checks devices and addresses, allocates and launches.
 
 
-def _on(device: torch.device):
-    """Makes the tensors' device the current one for a launch, where it is not."""
+def _launch(device: torch.device, what: str, fn, *args):
+    """Calls a C entry on the tensors' device and its current stream."""
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status != TTT_OK:
+        raise TTTError(status, what)
 
 
-def _strided(t, name, shape, dtype, device, rows=True, out=False) -> DeltaStrides:
-    """Checks a [B, H, n, d] (or, with rows=False, a [B, H, n]) tensor of any batch, head and token strides, and
-    gives them.  Outputs must not hold two elements at one place."""
+def _at(t):
+    """A tensor's address, or None for a missing or empty one."""
+    return (t.data_ptr() or None) if t is not None else None
+
+
+def _meta(t, name, device, aligned=True):
+    """A tensor's shape, strides and type, its kind, device and (rows') address checked."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (the layer runs only in the HIP library)")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    st = t.stride()
-    if rows and t.numel() and (st[3] != 1 or t.data_ptr() % 16 or
-                               any(s * t.element_size() % 16 for s, n in zip(st[:3], shape) if n > 1)):
-        raise ValueError(f"{name}'s last index must be contiguous and its rows 16-byte aligned (strides {st})")
-    if out and t.numel():
+    if aligned and t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    return t.shape, t.stride(), t.dtype
+
+
+def _strides(meta, name, shape, dtype, rows=True, out=False) -> DeltaStrides:
+    """Checks a [B, H, n, d] (or, with rows=False, a [B, H, n]) tensor of any batch, head and token strides, and
+    gives them.  Outputs must not hold two elements at one place."""
+    size, st, dt = meta
+    if size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {shape}")
+    if dt != dtype:
+        raise TypeError(f"{name} has dtype {dt}, expected {dtype}")
+    if 0 not in shape:
+        if rows and (st[3] != 1 and shape[3] > 1 or any(s * dtype.itemsize % 16 for s, n in zip(st[:3], shape) if n > 1)):
+            raise ValueError(f"{name}'s last index must be contiguous and its rows 16-byte aligned (strides {st})")
         reach = 1
         for s, n in sorted((s, n) for s, n in zip(st, shape) if n > 1):
-            if s < reach:
+            if out and s < reach:
                 raise ValueError(f"{name} is written and must not overlap itself (strides {st})")
             reach = s * n
     return DeltaStrides(*(s if n > 1 else 0 for s, n in zip(st[:3], shape)))
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_plan(q, k, v, g, beta, O, num):
+    """(byref of DeltaShape, its dtype code, DeltaLayout, workspace bytes, states' rows) of a forward call."""
+    shape, strides = _delta_strides(q, k, v, g, beta)
+    layout = DeltaLayout(*strides, _strides(O, "O", tuple(v[0]), q[2], out=True))
+    return (ctypes.byref(shape), _dt(q[2]), layout, ttt_gated_delta_workspace_bytes(shape, q[2], num),
+            (shape.batch if num < 0 else num, shape.v_heads, shape.v_dim, shape.k_dim))
+
+
+def _delta_strides(q, k, v, g, beta):
+    if len(q[0]) != 4 or len(v[0]) != 4:
+        raise ValueError(f"q and v are [B, H, n, d], got {tuple(q[0])} and {tuple(v[0])}")
+    (B, Hk, n, dk), Hv, dv, dt = q[0], v[0][1], v[0][3], q[2]
+    return DeltaShape(B, n, Hk, Hv, dk, dv), (
+        _strides(q, "q", (B, Hk, n, dk), dt), _strides(k, "k", (B, Hk, n, dk), dt), _strides(v, "v", (B, Hv, n, dv), dt),
+        _strides(g, "g", (B, Hv, n), torch.float32, rows=False),
+        _strides(beta, "beta", (B, Hv, n), torch.float32, rows=False))
+
+
+def _delta_metas(q, k, v, g, beta, dev):
+    return (_meta(q, "q", dev), _meta(k, "k", dev), _meta(v, "v", dev), _meta(g, "g", dev, False),
+            _meta(beta, "beta", dev, False))
 
 
 def _seq_starts(seq_starts, B, device):
@@ -841,22 +886,6 @@ def ttt_gated_delta_workspace_bytes(shape: DeltaShape, dtype: torch.dtype, num_s
     return out.value
 
 
-def _delta_inputs(q, k, v, g, beta, W_init, seq_starts):
-    """What the forward and the backward call check alike: (DeltaShape, sequences' rows, packed count or -1, strides of
-    q, k, v, g, beta)."""
-    B, Hk, n, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[3]
-    dt, dev = q.dtype, q.device
-    strides = (_strided(q, "q", (B, Hk, n, dk), dt, dev), _strided(k, "k", (B, Hk, n, dk), dt, dev),
-               _strided(v, "v", (B, Hv, n, dv), dt, dev), _strided(g, "g", (B, Hv, n), torch.float32, dev, rows=False),
-               _strided(beta, "beta", (B, Hv, n), torch.float32, dev, rows=False))
-    num = _seq_starts(seq_starts, B, dev)
-    rows = B if num < 0 else num
-    if W_init is not None:
-        _need(W_init, "W_init", (rows, Hv, dv, dk), torch.float32, dev)
-    return DeltaShape(B, n, Hk, Hv, dk, dv), rows, num, strides
-
-
 def ttt_gated_delta(q, k, v, g, beta, scale=None, W_init=None, seq_starts=None, O=None, W_final=None,
                     workspace=None):
     """The gated delta rule over whole sequences: per value head W_t = exp(g_t) W_{t-1} + beta_t (v_t -
@@ -869,21 +898,19 @@ def ttt_gated_delta(q, k, v, g, beta, scale=None, W_init=None, seq_starts=None, 
     W_init [sequences, Hv, dv, dk] fp32: the states to start from (zero if None).  seq_starts, an int32 device
     tensor [sequences + 1]: packed sequences of any lengths in one batch row; tokens behind the last of them are
     not read and their rows of O are left as they are."""
-    shape, rows, num, strides = _delta_inputs(q, k, v, g, beta, W_init, seq_starts)
-    B, n, Hv, dk, dv = shape.batch, shape.seq_len, shape.v_heads, shape.k_dim, shape.v_dim
-    dt, dev = q.dtype, q.device
+    dev = q.device
+    metas = _delta_metas(q, k, v, g, beta, dev)
+    num = _seq_starts(seq_starts, q.shape[0], dev)
     O = torch.empty_like(v) if O is None else O
-    so = _strided(O, "O", (B, Hv, n, dv), dt, dev, out=True)
-    W_final = torch.empty(rows, Hv, dv, dk, dtype=torch.float32, device=dev) if W_final is None else W_final
-    _need(W_final, "W_final", (rows, Hv, dv, dk), torch.float32, dev)
-    nbytes = ttt_gated_delta_workspace_bytes(shape, dt, num)
+    shape, dt, layout, nbytes, states = _delta_plan(*metas, _meta(O, "O", dev), num)
+    if W_init is not None:
+        _need(W_init, "W_init", states, torch.float32, dev)
+    W_final = torch.empty(states, dtype=torch.float32, device=dev) if W_final is None else W_final
+    _need(W_final, "W_final", states, torch.float32, dev)
     ws = _workspace(nbytes, dev, workspace)
-    layout = DeltaLayout(*strides, so)
-    opts = DeltaOptions(_vp(W_init), _vp(seq_starts), max(num, 0), ctypes.pointer(layout))
-    with _on(dev):
-        _check(lib().ttt_gated_delta(ctypes.byref(shape), _dt(dt), dk ** -0.5 if scale is None else float(scale),
-                                     _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), ctypes.byref(opts), _vp(O),
-                                     _vp(W_final), _vp(ws), nbytes, _stream(dev)), "ttt_gated_delta")
+    opts = DeltaOptions(_at(W_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
+    _launch(dev, "ttt_gated_delta", lib().ttt_gated_delta, shape, dt,
+            states[3] ** -0.5 if scale is None else float(scale), _at(q), _at(k), _at(v), _at(g), _at(beta), ctypes.byref(opts), _at(O), _at(W_final), _at(ws), nbytes)
     return O, W_final
 
 
@@ -895,6 +922,19 @@ def ttt_gated_delta_backward_workspace_bytes(shape: DeltaShape, dtype: torch.dty
     return out.value
 
 
+@functools.lru_cache(maxsize=256)
+def _delta_backward_plan(q, k, v, g, beta, dO, dq, dk, dv, dg, dbeta, num):
+    shape, strides = _delta_strides(q, k, v, g, beta)
+    qs, vs, gs, dt = tuple(q[0]), tuple(v[0]), tuple(g[0]), q[2]
+    grads = DeltaGradLayout(_strides(dO, "dO", vs, dt), _strides(dq, "dq", qs, dt, out=True),
+                            _strides(dk, "dk", qs, dt, out=True), _strides(dv, "dv", vs, dt, out=True),
+                            _strides(dg, "dg", gs, dt, rows=False, out=True),
+                            _strides(dbeta, "dbeta", gs, dt, rows=False, out=True))
+    return (ctypes.byref(shape), _dt(dt), DeltaLayout(*strides, DeltaStrides()), grads,
+            ttt_gated_delta_backward_workspace_bytes(shape, dt, num),
+            (shape.batch if num < 0 else num, shape.v_heads, shape.v_dim, shape.k_dim))
+
+
 def ttt_gated_delta_backward(q, k, v, g, beta, dO, dW_final=None, scale=None, W_init=None, seq_starts=None, dq=None,
                              dk=None, dv=None, dg=None, dbeta=None, dW_init=None, workspace=None):
     """Backward of ttt_gated_delta from its inputs (the states are made again), dO = dLoss/dO [B, Hv, n, dv] and, where
@@ -902,33 +942,31 @@ def ttt_gated_delta_backward(q, k, v, g, beta, dO, dW_final=None, scale=None, W_
     in q's dtype, each laid out like its input if not given, and dW_init [sequences, Hv, dv, dk] fp32 (None without
     W_init, unless given).  dO and the gradients may have any strides that the inputs may; rows of tokens that belong
     to no sequence are left as they are."""
-    shape, rows, num, strides = _delta_inputs(q, k, v, g, beta, W_init, seq_starts)
-    B, n, Hk, Hv, ek, ev = shape.batch, shape.seq_len, shape.k_heads, shape.v_heads, shape.k_dim, shape.v_dim
-    dt, dev = q.dtype, q.device
-    dq, dk, dv = (torch.empty_like(x) if t is None else t for t, x in ((dq, q), (dk, k), (dv, v)))
-    dg, dbeta = (torch.empty_like(x, dtype=dt) if t is None else t for t, x in ((dg, g), (dbeta, beta)))
-    grad_strides = [_strided(dO, "dO", (B, Hv, n, ev), dt, dev)]
-    grad_strides += [_strided(t, name, shp, dt, dev, out=True) for t, name, shp in (
-        (dq, "dq", (B, Hk, n, ek)), (dk, "dk", (B, Hk, n, ek)), (dv, "dv", (B, Hv, n, ev)))]
-    grad_strides += [_strided(t, name, (B, Hv, n), dt, dev, rows=False, out=True)
-                     for t, name in ((dg, "dg"), (dbeta, "dbeta"))]
+    dev, t = q.device, q.dtype
+    metas = _delta_metas(q, k, v, g, beta, dev)
+    num = _seq_starts(seq_starts, q.shape[0], dev)
+    dq, dk, dv = (torch.empty_like(x) if d is None else d for d, x in ((dq, q), (dk, k), (dv, v)))
+    dg, dbeta = (torch.empty_like(x, dtype=t) if d is None else d for d, x in ((dg, g), (dbeta, beta)))
+    shape, dt, layout, grads, nbytes, states = _delta_backward_plan(
+        *metas, _meta(dO, "dO", dev), _meta(dq, "dq", dev), _meta(dk, "dk", dev), _meta(dv, "dv", dev),
+        _meta(dg, "dg", dev, False), _meta(dbeta, "dbeta", dev, False), num)
     if W_init is not None and dW_init is None:
         dW_init = torch.empty_like(W_init)
-    for t, name in ((dW_final, "dW_final"), (dW_init, "dW_init")):
-        if t is not None:
-            _need(t, name, (rows, Hv, ev, ek), torch.float32, dev)
-    nbytes = ttt_gated_delta_backward_workspace_bytes(shape, dt, num)
+    for d, name in ((W_init, "W_init"), (dW_final, "dW_final"), (dW_init, "dW_init")):
+        if d is not None:
+            _need(d, name, states, torch.float32, dev)
     ws = _workspace(nbytes, dev, workspace)
-    layout = DeltaLayout(*strides, DeltaStrides())
-    opts = DeltaOptions(_vp(W_init), _vp(seq_starts), max(num, 0), ctypes.pointer(layout))
-    grad_layout = DeltaGradLayout(*grad_strides)
-    with _on(dev):
-        _check(lib().ttt_gated_delta_backward(ctypes.byref(shape), _dt(dt), ek ** -0.5 if scale is None else float(scale),
-                                              _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), _vp(dO), _vp(dW_final),
-                                              ctypes.byref(opts), ctypes.byref(grad_layout), _vp(dq), _vp(dk), _vp(dv),
-                                              _vp(dg), _vp(dbeta), _vp(dW_init), _vp(ws), nbytes, _stream(dev)),
-               "ttt_gated_delta_backward")
+    opts = DeltaOptions(_at(W_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
+    _launch(dev, "ttt_gated_delta_backward", lib().ttt_gated_delta_backward, shape, dt,
+            states[3] ** -0.5 if scale is None else float(scale), _at(q), _at(k), _at(v), _at(g), _at(beta), _at(dO),
+            _at(dW_final), ctypes.byref(opts), ctypes.byref(grads), _at(dq), _at(dk), _at(dv), _at(dg), _at(dbeta),
+            _at(dW_init), _at(ws), nbytes)
     return dq, dk, dv, dg, dbeta, dW_init
+
+
+@functools.lru_cache(maxsize=256)
+def _step_shape(*sizes):
+    return ctypes.byref(DeltaStepShape(*sizes))
 
 
 def ttt_gated_delta_step(q, k, v, g, beta, W, slots=None, scale=None, O=None):
@@ -936,24 +974,23 @@ def ttt_gated_delta_step(q, k, v, g, beta, W, slots=None, scale=None, O=None):
     one dtype, g, beta [rows, Hv] fp32; W [states, Hv, dv, dk] fp32 is the pool of states, updated in place; slots
     [rows] int32 on the device names each row's state (a slot outside the pool, such as -1: a padding row, whose
     output is zero; rows of one slot go in row order; None: row r's state is W[r]).  Returns O [rows, Hv, dv]."""
-    R, Hk, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[2]
+    (R, Hk, dk), (_, Hv, dv), P = q.shape, v.shape, W.shape[0]
     dt, dev = q.dtype, q.device
     _need(q, "q", (R, Hk, dk), dt, dev)
     _need(k, "k", (R, Hk, dk), dt, dev)
     _need(v, "v", (R, Hv, dv), dt, dev)
     _need(g, "g", (R, Hv), torch.float32, dev)
     _need(beta, "beta", (R, Hv), torch.float32, dev)
-    _need(W, "W", (W.shape[0], Hv, dv, dk), torch.float32, dev)
+    _need(W, "W", (P, Hv, dv, dk), torch.float32, dev)
     if slots is not None:
         _need(slots, "slots", (R,), torch.int32, dev)
-    O = torch.empty_like(v) if O is None else O
-    _need(O, "O", (R, Hv, dv), dt, dev)
-    shape = DeltaStepShape(R, W.shape[0], Hk, Hv, dk, dv)
-    with _on(dev):
-        _check(lib().ttt_gated_delta_step(ctypes.byref(shape), _dt(dt), dk ** -0.5 if scale is None else float(scale),
-                                          _vp(q), _vp(k), _vp(v), _vp(g), _vp(beta), _vp(W), _vp(slots), _vp(O),
-                                          _stream(dev)), "ttt_gated_delta_step")
+    if O is None:
+        O = torch.empty_like(v)
+    else:
+        _need(O, "O", (R, Hv, dv), dt, dev)
+    _launch(dev, "ttt_gated_delta_step", lib().ttt_gated_delta_step, _step_shape(R, P, Hk, Hv, dk, dv), _dt(dt),
+            dk ** -0.5 if scale is None else float(scale), _at(q), _at(k), _at(v), _at(g), _at(beta), _at(W), _at(slots),
+            _at(O))
     return O
 
 
@@ -965,23 +1002,23 @@ def _norm_vector(t, name, d, dt, dev):
 def ttt_layer_norm(x, weight=None, bias=None, eps=1e-5, Y=None, mean=None, rstd=None):
     """Layer norm over the last index of x [..., d] (contiguous): returns (Y like x, mean [...], rstd [...] fp32).
     weight and bias [d] of x's dtype, or None."""
-    d = x.shape[-1]
-    dt, dev = x.dtype, x.device
-    _need(x, "x", x.shape, dt, dev)
+    shape, dt, dev = x.shape, x.dtype, x.device
+    d, lead = shape[-1], shape[:-1]
+    _need(x, "x", shape, dt, dev)
     _norm_vector(weight, "weight", d, dt, dev)
     _norm_vector(bias, "bias", d, dt, dev)
     Y = torch.empty_like(x) if Y is None else Y
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if mean is None else mean
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if rstd is None else rstd
-    _need(Y, "Y", x.shape, dt, dev)
-    _need(mean, "mean", x.shape[:-1], torch.float32, dev)
-    _need(rstd, "rstd", x.shape[:-1], torch.float32, dev)
-    with _on(dev):
-        _check(lib().ttt_layer_norm(mean.numel(), d, _dt(dt), float(eps), _vp(x), _vp(weight), _vp(bias), _vp(Y),
-                                    _vp(mean), _vp(rstd), _stream(dev)), "ttt_layer_norm")
+    mean = torch.empty(lead, dtype=torch.float32, device=dev) if mean is None else mean
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
+    _need(Y, "Y", shape, dt, dev)
+    _need(mean, "mean", lead, torch.float32, dev)
+    _need(rstd, "rstd", lead, torch.float32, dev)
+    _launch(dev, "ttt_layer_norm", lib().ttt_layer_norm, mean.numel(), d, _dt(dt), float(eps), _at(x), _at(weight),
+            _at(bias), _at(Y), _at(mean), _at(rstd))
     return Y, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def ttt_layer_norm_backward_workspace_bytes(rows: int, dim: int, dtype: torch.dtype) -> int:
     out = ctypes.c_size_t(0)
     _check(lib().ttt_layer_norm_backward_workspace_bytes(int(rows), int(dim), _dt(dtype), ctypes.byref(out)),
@@ -993,15 +1030,15 @@ def ttt_layer_norm_backward(x, weight, dY, mean, rstd, bias=True, dx=None, dweig
                             workspace=None):
     """Backward of ttt_layer_norm given its mean and rstd.  Returns (dx like x, dweight [d] fp32 or None where
     weight is None, dbias [d] fp32 or None with bias=False)."""
-    d = x.shape[-1]
-    dt, dev = x.dtype, x.device
-    _need(x, "x", x.shape, dt, dev)
-    _need(dY, "dY", x.shape, dt, dev)
+    shape, dt, dev = x.shape, x.dtype, x.device
+    d, lead = shape[-1], shape[:-1]
+    _need(x, "x", shape, dt, dev)
+    _need(dY, "dY", shape, dt, dev)
     _norm_vector(weight, "weight", d, dt, dev)
-    _need(mean, "mean", x.shape[:-1], torch.float32, dev)
-    _need(rstd, "rstd", x.shape[:-1], torch.float32, dev)
+    _need(mean, "mean", lead, torch.float32, dev)
+    _need(rstd, "rstd", lead, torch.float32, dev)
     dx = torch.empty_like(x) if dx is None else dx
-    _need(dx, "dx", x.shape, dt, dev)
+    _need(dx, "dx", shape, dt, dev)
     if weight is not None and dweight is None:
         dweight = torch.empty(d, dtype=torch.float32, device=dev)
     if bias and dbias is None:
@@ -1011,8 +1048,6 @@ def ttt_layer_norm_backward(x, weight, dY, mean, rstd, bias=True, dx=None, dweig
     rows = mean.numel()
     nbytes = ttt_layer_norm_backward_workspace_bytes(rows, d, dt)
     ws = _workspace(nbytes, dev, workspace)
-    with _on(dev):
-        _check(lib().ttt_layer_norm_backward(rows, d, _dt(dt), _vp(x), _vp(weight), _vp(dY), _vp(mean), _vp(rstd),
-                                             _vp(dx), _vp(dweight), _vp(dbias), _vp(ws), nbytes, _stream(dev)),
-               "ttt_layer_norm_backward")
+    _launch(dev, "ttt_layer_norm_backward", lib().ttt_layer_norm_backward, rows, d, _dt(dt), _at(x), _at(weight), _at(dY),
+            _at(mean), _at(rstd), _at(dx), _at(dweight), _at(dbias), _at(ws), nbytes)
     return dx, dweight, dbias

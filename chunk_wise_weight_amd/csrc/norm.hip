@@ -9,9 +9,11 @@
 // the registers, so a large common offset costs no digits), and written once.
 // TPR threads share a row, each holding NV vectors of VEC elements; vector i
 // of thread t starts at element (i TPR + t) VEC, so a wave's loads are
-// contiguous.  Rows of up to 64 x 8 vectors belong to one wave or a part of
-// one: no barrier, and a workgroup works on 4 rows or more.  VEC = 16 bytes
-// where the row length keeps every row 16-byte aligned, else 1.
+// contiguous.  Rows of up to 128 vectors belong to one wave or a quarter of
+// one: no barrier, and a workgroup works on 4 rows or more.  Wider rows have a
+// workgroup of as many waves as they fill (TPR = 0: its size, up to 1024), one
+// vector a thread while that reaches.  VEC = 16 bytes where the row length
+// keeps every row 16-byte aligned, else 1.
 #include <algorithm>
 
 #include "common.hpp"
@@ -54,54 +56,53 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& v) {
   *reinterpret_cast<Pack<T, VEC>*>(p) = v;
 }
 
-// Sums of N values over the TPR threads of a row, given to all of them.  Above
-// one wave the waves' sums meet in `red`; `turn` alternates between its two
-// halves, so that one barrier a sum is enough.
+// Sums of N values over the threads of a row, given to all of them.  Where a
+// workgroup has the row (TPR = 0) the waves' sums meet in `red`; `turn`
+// alternates between its two halves, so that one barrier a sum is enough.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& turn) {
 #pragma unroll
-  for (int m = (TPR < 64 ? TPR : 64) / 2; m > 0; m >>= 1)
+  for (int m = (TPR > 0 && TPR < 64 ? TPR : 64) / 2; m > 0; m >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m, 64);
-  if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
-    float* half = red + turn * (N * W);
+  if constexpr (TPR == 0) {
+    const int waves = blockDim.x >> 6;
+    float* half = red + turn * (N * 16);
     turn ^= 1;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) half[i * W + (threadIdx.x >> 6)] = v[i];
+      for (int i = 0; i < N; ++i) half[i * 16 + (threadIdx.x >> 6)] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) v[i] += half[i * W + w];
+      for (int w = 0; w < waves; ++w) v[i] += half[i * 16 + w];
     }
   }
 }
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_norm(
+__global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
     const T* __restrict__ x, const T* __restrict__ weight, const T* __restrict__ bias, T* __restrict__ y,
     float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d, float eps) {
-  constexpr int BT = TPR > kNormThreads ? TPR : kNormThreads, RPB = BT / TPR;
-  __shared__ float red[TPR > 64 ? 2 * (TPR / 64) : 1];
-  const int t = threadIdx.x % TPR;
+  const int tpr = TPR ? TPR : (int)blockDim.x, rpb = TPR ? kNormThreads / TPR : 1;
+  __shared__ float red[TPR ? 1 : 2 * 16];
+  const int t = threadIdx.x % tpr;
   int turn = 0;
   // one turn of this loop, unless there are more rows than a grid may have workgroups
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < rows; row += (int64_t)gridDim.x * RPB) {
+  for (int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr; row < rows; row += (int64_t)gridDim.x * rpb) {
     const T* xr = x + row * d;
     Pack<T, VEC> raw[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (e < d) raw[i] = load_pack<T, VEC>(xr + e);
     }
     float v[NV][VEC];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * TPR + t) * VEC < d) {
+      if ((i * tpr + t) * VEC < d) {
         widen(raw[i], v[i]);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) s[0] += v[i][j];
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
     s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * TPR + t) * VEC < d) {
+      if ((i * tpr + t) * VEC < d) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           v[i][j] -= mu;
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
     T* yr = y + row * d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (e < d) {
         float w[VEC], b[VEC];
         if (weight) {
@@ -154,24 +155,25 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
   }
 }
 
-// Each workgroup takes rows blockIdx.x RPB + i, stepping by gridDim.x RPB, and
-// keeps the sums of its columns' dY h and dY in registers; the RPB row slots'
-// sums meet in LDS at the end and go to part[blockIdx.x][2][d], which
-// k_norm_grad_sum adds up in block order: no atomics, the same bits every run.
+// Each workgroup takes rows blockIdx.x rpb + i, stepping by gridDim.x rpb, the
+// next row's loads under way while this one's sums are made, and keeps the sums
+// of its columns' dY h and dY in registers; its rows' sums meet in LDS at the
+// end and go to part[blockIdx.x][2][d], which k_norm_grad_sum adds up in block
+// order: no atomics, the same bits every run.
 template <typename T, int VEC, int TPR, int NV>
-__global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_norm_grad(
+__global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
     const T* __restrict__ x, const T* __restrict__ weight, const T* __restrict__ dy, const float* __restrict__ mean,
     const float* __restrict__ rstd, T* __restrict__ dx, float* __restrict__ part, int64_t rows, int d, bool want_db) {
-  constexpr int BT = TPR > kNormThreads ? TPR : kNormThreads, RPB = BT / TPR;
-  __shared__ float red[TPR > 64 ? 4 * (TPR / 64) : 1];
-  // sums of the row slots: one slot's columns at a time
-  __shared__ float cols[RPB > 1 ? TPR * VEC * RPB : 1];
-  const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  constexpr int RPB = TPR ? kNormThreads / TPR : 1;
+  const int tpr = TPR ? TPR : (int)blockDim.x;
+  __shared__ float red[TPR ? 1 : 4 * 16];
+  __shared__ float cols[RPB > 1 ? TPR * VEC * RPB : 1];       // one vector's sums of every row slot
+  const int t = threadIdx.x % tpr, slot = threadIdx.x / tpr;
   int turn = 0;
   float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (i * TPR + t) * VEC;
+    const int e = (i * tpr + t) * VEC;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       w[i][j] = 1.f;
@@ -179,30 +181,40 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
     }
     if (weight && e < d) widen(load_pack<T, VEC>(weight + e), w[i]);
   }
-  const int64_t step = (int64_t)gridDim.x * RPB;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + slot; row < rows; row += step) {
-    const T* xr = x + row * d;
-    const T* gr = dy + row * d;
-    Pack<T, VEC> px[NV], pg[NV];
+  struct Row {
+    Pack<T, VEC> x[NV], g[NV];
+    float mu, r;
+  };
+  auto load = [&](int64_t row, Row& o) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (e < d) {
-        px[i] = load_pack<T, VEC>(xr + e);
-        pg[i] = load_pack<T, VEC>(gr + e);
+        o.x[i] = load_pack<T, VEC>(x + row * d + e);
+        o.g[i] = load_pack<T, VEC>(dy + row * d + e);
       }
     }
-    const float mu = mean[row], r = rstd[row];
+    o.mu = mean[row];
+    o.r = rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + slot;
+  Row now, next;
+  constexpr bool AHEAD = VEC > 1 && NV <= 2;      // where registers allow it
+  if (AHEAD && row < rows) load(row, now);
+  for (; row < rows; row += step) {
+    if (!AHEAD) load(row, now);
+    if (AHEAD && row + step < rows) load(row + step, next);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * TPR + t) * VEC < d) {
+      if ((i * tpr + t) * VEC < d) {
         float xv[VEC], gv[VEC];
-        widen(px[i], xv);
-        widen(pg[i], gv);
+        widen(now.x[i], xv);
+        widen(now.g[i], gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float h = (xv[j] - mu) * r, a = gv[j] * w[i][j];
+          const float h = (xv[j] - now.mu) * now.r, a = gv[j] * w[i][j];
           s[0] += a;
           s[1] += a * h;
           dw[i][j] += gv[j] * h;
@@ -212,24 +224,24 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
     }
     row_sum<TPR>(s, red, turn);
     const float ma = s[0] / (float)d, mah = s[1] / (float)d;
-    T* dr = dx + row * d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       if (e < d) {
         float xv[VEC], gv[VEC], o[VEC];
-        widen(px[i], xv);
-        widen(pg[i], gv);
+        widen(now.x[i], xv);
+        widen(now.g[i], gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float h = (xv[j] - mu) * r;
-          o[j] = r * (gv[j] * w[i][j] - ma - h * mah);
+          const float h = (xv[j] - now.mu) * now.r;
+          o[j] = now.r * (gv[j] * w[i][j] - ma - h * mah);
         }
         Pack<T, VEC> p;
         narrow(o, p);
-        store_pack<T, VEC>(dr + e, p);
+        store_pack<T, VEC>(dx + row * d + e, p);
       }
     }
+    if (AHEAD) now = next;
   }
   float* pw = part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
@@ -237,7 +249,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
     if (q == 1 && !want_db) break;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (i * TPR + t) * VEC;
+      const int e = (i * tpr + t) * VEC;
       float* mine = q == 0 ? dw[i] : db[i];
       if constexpr (RPB > 1) {
         __syncthreads();
@@ -259,86 +271,92 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void k_nor
   }
 }
 
-// dw[c], db[c] = the sums of part[0..G)[.][c]: a workgroup takes 64 columns of
-// one of the two, its 16 rows of threads every 16th block each, joined in LDS.
+// dw[c], db[c] = the sums of part[0..G)[.][c]: a workgroup takes 16 columns of
+// one of the two, its 64 rows of threads every 64th block each (narrow columns
+// of many rows, so that few blocks' sums are read one after the other also
+// where d is small), joined in LDS in a fixed order.
 __global__ __launch_bounds__(1024) void k_norm_grad_sum(const float* __restrict__ part, int G, int d,
                                                         float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sum[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6, q = blockIdx.y;
+  __shared__ float sum[64][16];
+  const int j = threadIdx.x & 15, k = threadIdx.x >> 4, c = blockIdx.x * 16 + j, q = blockIdx.y;
   float* out = q == 0 ? dw : db;
   if (out == nullptr) return;
   float a = 0.f;
-  if (c < d)
-    for (int g = k; g < G; g += 16) a += part[((int64_t)g * 2 + q) * d + c];
-  sum[k][threadIdx.x & 63] = a;
+  if (c < d) {
+#pragma unroll 4
+    for (int g = k; g < G; g += 64) a += part[((int64_t)g * 2 + q) * d + c];
+  }
+  sum[k][j] = a;
   __syncthreads();
   if (k == 0 && c < d) {
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a += sum[i][threadIdx.x & 63];
+    for (int i = 0; i < 64; ++i) a += sum[i][j];
     out[c] = a;
   }
 }
 
-// The variant for rows of d elements: the fewest threads a row (16, 64, 256,
-// 1024) that hold it in at most 8 vectors each (64 single elements).
+// The variant for rows of d elements.
 struct NormPlan {
   bool vec;
-  int tpr, nv;
+  int tpr, threads, nv;           // threads: of a workgroup; tpr 0: all of them share a row
 };
+// A wave has rows of up to 64 `most` vectors (twice as many single elements): forward 8, backward 2.  Measured
+// (bf16, us; a wave a row / a workgroup a row): forward 131072 x 2560 296 / 411, 32768 x 1024 fp32 46 / 57; backward
+// 131072 x 2560 545 / 396, 16384 x 4096 153 / 103.  The forward pass has nothing to wait for but its loads, which a wave's
+// own registers keep under way; the backward's three rows of registers leave too few waves for that.
 template <typename T>
-NormPlan norm_plan(int d) {
+NormPlan norm_plan(int d, int most) {
   constexpr int V = Vec<T>::V;
   NormPlan p;
   p.vec = d % V == 0;
-  const int units = p.vec ? d / V : d;
-  const int most = p.vec ? 8 : 16;
-  p.tpr = units <= 16 ? 16 : units <= 64 * most ? 64 : units <= 256 * most ? 256 : 1024;
-  p.nv = (units + p.tpr - 1) / p.tpr;
+  const int units = p.vec ? d / V : d, few = p.vec ? 1 : 4;
+  p.threads = kNormThreads;
+  p.nv = 1;
+  if (units <= 16) {
+    p.tpr = 16;
+  } else if (units <= 64 * most * (p.vec ? 1 : 2)) {
+    p.tpr = 64;
+    p.nv = (units + 63) / 64;
+  } else {
+    p.tpr = 0;
+    p.nv = std::max(few, (units + 1023) / 1024);
+    p.threads = (units + 64 * p.nv - 1) / (64 * p.nv) * 64;
+  }
   return p;
 }
 
 // Counts of vectors a thread that have a kernel: the next larger one serves.
-template <bool VECTORS, typename F>
-hipError_t with_nv(int nv, F f) {
-  if constexpr (VECTORS) {
-    switch (nv) {
-      case 1: return f(std::integral_constant<int, 1>());
-      case 2: return f(std::integral_constant<int, 2>());
-      case 3: return f(std::integral_constant<int, 3>());
-      case 4: return f(std::integral_constant<int, 4>());
-      case 5: return f(std::integral_constant<int, 5>());
-      case 6: return f(std::integral_constant<int, 6>());
-      case 7:
-      case 8: return f(std::integral_constant<int, 8>());
-      default: return f(std::integral_constant<int, 16>());   // fp32 rows of more than 32768
-    }
-  } else {
-    if (nv <= 4) return f(std::integral_constant<int, 4>());
-    if (nv <= 16) return f(std::integral_constant<int, 16>());
-    return f(std::integral_constant<int, 64>());
-  }
-}
-
 template <typename T, typename F>
 hipError_t with_plan(const NormPlan& p, F f) {
-  auto tpr = [&](auto vec) {
-    constexpr int VEC = decltype(vec)::value;
-    return with_nv<(VEC > 1)>(p.nv, [&](auto nv) {
-      constexpr int NV = decltype(nv)::value;
-      if constexpr (VEC > 1 ? NV == 1 : NV == 4) {
-        if (p.tpr == 16) return f(vec, std::integral_constant<int, 16>(), nv);
-      }
-      if constexpr (NV <= (VEC > 1 ? 8 : 16)) {
-        if (p.tpr == 64) return f(vec, std::integral_constant<int, 64>(), nv);
-        if (p.tpr == 256) return f(vec, std::integral_constant<int, 256>(), nv);
-      }
-      if constexpr (NV == 16 && VEC == 8) return hipErrorInvalidValue;    // 1024 x 8 x 8 is the widest row
-      else return f(vec, std::integral_constant<int, 1024>(), nv);
-    });
+  using std::integral_constant;
+  auto go = [&](auto vec, auto nv) {
+    if (p.tpr == 0) return f(vec, integral_constant<int, 0>(), nv);
+    if constexpr (decltype(nv)::value <= (decltype(vec)::value > 1 ? 8 : 16)) {
+      if (p.tpr == 64) return f(vec, integral_constant<int, 64>(), nv);
+    }
+    if constexpr (decltype(nv)::value <= 4) {
+      if (p.tpr == 16) return f(vec, integral_constant<int, 16>(), nv);
+    }
+    return hipErrorInvalidValue;
   };
-  if (p.vec) return tpr(std::integral_constant<int, Vec<T>::V>());
-  return tpr(std::integral_constant<int, 1>());
+  if (p.vec) {
+    const integral_constant<int, Vec<T>::V> vec;
+    if (p.nv <= 1) return go(vec, integral_constant<int, 1>());
+    if (p.nv <= 2) return go(vec, integral_constant<int, 2>());
+    if (p.nv <= 3) return go(vec, integral_constant<int, 3>());
+    if (p.nv <= 4) return go(vec, integral_constant<int, 4>());
+    if (p.nv <= 5) return go(vec, integral_constant<int, 5>());
+    if (p.nv <= 6) return go(vec, integral_constant<int, 6>());
+    if (p.nv <= 8 || sizeof(T) == 2) return go(vec, integral_constant<int, 8>());
+    if constexpr (sizeof(T) == 4) return go(vec, integral_constant<int, 16>());
+    return hipErrorInvalidValue;
+  }
+  const integral_constant<int, 1> one;
+  if (p.nv <= 4) return go(one, integral_constant<int, 4>());
+  if (p.nv <= 8) return go(one, integral_constant<int, 8>());
+  if (p.nv <= 16) return go(one, integral_constant<int, 16>());
+  return go(one, integral_constant<int, 64>());
 }
 
 }  // namespace
@@ -346,42 +364,41 @@ hipError_t with_plan(const NormPlan& p, F f) {
 template <typename T>
 hipError_t launch_norm(const T* x, const T* w, const T* b, T* y, float* mean, float* rstd, int64_t rows, int d,
                        float eps, hipStream_t s) {
-  const NormPlan p = norm_plan<T>(d);
+  const NormPlan p = norm_plan<T>(d, 8);
+  const int rpb = p.tpr ? p.threads / p.tpr : 1;
+  const int64_t grid = std::min<int64_t>((rows + rpb - 1) / rpb, 1 << 21);
   return with_plan<T>(p, [&](auto vec, auto tpr, auto nv) {
-    constexpr int VEC = decltype(vec)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr int BT = TPR > kNormThreads ? TPR : kNormThreads, RPB = BT / TPR;
-    const int64_t grid = std::min<int64_t>((rows + RPB - 1) / RPB, 1 << 21);
-    k_norm<T, VEC, TPR, NV><<<dim3((unsigned)grid), BT, 0, s>>>(x, w, b, y, mean, rstd, rows, d, eps);
+    k_norm<T, decltype(vec)::value, decltype(tpr)::value, decltype(nv)::value>
+        <<<dim3((unsigned)grid), p.threads, 0, s>>>(x, w, b, y, mean, rstd, rows, d, eps);
     return hipGetLastError();
   });
 }
 
-// Workgroups of the backward pass: enough to fill the 256 CUs, and no more
-// than 4 a CU, so that the partial sums (8 d bytes a workgroup) stay small.
+// Workgroups of the backward pass: enough to keep the 256 CUs' loads under
+// way, and few enough that the partial sums (8 d bytes a workgroup, written and
+// read) stay small beside the rows.
 template <typename T>
 int norm_grad_blocks(int64_t rows, int d) {
-  const NormPlan p = norm_plan<T>(d);
-  const int64_t rpb = std::max(kNormThreads, p.tpr) / p.tpr;
-  return (int)std::min<int64_t>((rows + rpb - 1) / rpb, p.tpr == 1024 ? 512 : 1024);
+  const NormPlan p = norm_plan<T>(d, 2);
+  const int64_t rpb = p.tpr ? p.threads / p.tpr : 1;
+  return (int)std::min<int64_t>((rows + rpb - 1) / rpb, p.tpr ? 1280 : p.threads > 512 ? 512 : 768);
 }
 
 template <typename T>
 hipError_t launch_norm_grad(const T* x, const T* w, const T* dy, const float* mean, const float* rstd, T* dx,
                             float* dw, float* db, float* part, int64_t rows, int d, hipStream_t s) {
-  const NormPlan p = norm_plan<T>(d);
+  const NormPlan p = norm_plan<T>(d, 2);
   const int G = norm_grad_blocks<T>(rows, d);
   if (G > 0) {
     hipError_t e = with_plan<T>(p, [&](auto vec, auto tpr, auto nv) {
-      constexpr int VEC = decltype(vec)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-      constexpr int BT = TPR > kNormThreads ? TPR : kNormThreads;
-      k_norm_grad<T, VEC, TPR, NV><<<dim3((unsigned)G), BT, 0, s>>>(x, w, dy, mean, rstd, dx, part, rows, d,
-                                                                   db != nullptr);
+      k_norm_grad<T, decltype(vec)::value, decltype(tpr)::value, decltype(nv)::value>
+          <<<dim3((unsigned)G), p.threads, 0, s>>>(x, w, dy, mean, rstd, dx, part, rows, d, db != nullptr);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
   }
   if (dw == nullptr && db == nullptr) return hipSuccess;
-  k_norm_grad_sum<<<dim3((unsigned)((d + 63) / 64), 2), 1024, 0, s>>>(part, G, d, dw, db);
+  k_norm_grad_sum<<<dim3((unsigned)((d + 15) / 16), 2), 1024, 0, s>>>(part, G, d, dw, db);
   return hipGetLastError();
 }
 
