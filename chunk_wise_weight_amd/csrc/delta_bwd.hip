@@ -32,6 +32,7 @@ template <typename T, int DK, int NW, int STAGES> struct WalkBack {
   static constexpr int kK = 0, kQ = Panels<T>::bytes(DK), kRec = 2 * kQ, kD = kRec + ChunkRecT<T>::kBytes;
   static constexpr int kStage = kD + Columns<T, NW>::kBytes;
   static constexpr int kSmem = STAGES * kStage;
+  static constexpr bool kHoist = SS <= 4;
 };
 
 template <typename T, int DK, int NW, int STAGES>
@@ -83,74 +84,136 @@ __device__ __forceinline__ void walk_back(const DeltaGradArgs& a, int w, const W
     next_turn<STAGES>(c == chunks - 1);
     const float* gate = reinterpret_cast<const float*>(st + G::kRec + ChunkRecT<T>::kGate);
     const int64_t slot = (int64_t)(sp.slot0 + c) * p.Hv + h;
+    // As in the forward walk, reads from LDS go out a stage of arithmetic ahead.
+    u32x4 Kf[G::kHoist ? 4 : 1][SS];
+    typename Columns<T, NW>::Raw raw[4];
+    f32x4 up[4], left[4];
+    auto read_k = [&](int t, u32x4 (&f)[SS]) __attribute__((always_inline)) {
+      const int r = M::row(t, m);
+#pragma unroll
+      for (int s = 0; s < SS; ++s) f[s] = Panels<T>::frag(st + G::kK, r, s, g);
+    };
+    if constexpr (G::kHoist)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) read_k(t, Kf[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      raw[t] = Columns<T, NW>::read(st + G::kD, w, t, lane);
+      up[t] = *reinterpret_cast<const f32x4*>(gate + M::row(t, g * 4));
+      left[t] = *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
+    }
+    const float decay = gate[63];
+    __builtin_amdgcn_sched_barrier(0);
     u32x4 Sh[SS], Sl[SS];
 #pragma unroll
     for (int s = 0; s < SS; ++s) M::split(S + s * M::TPS, Sh[s], Sl[s]);
     put_state<T, SS>(Sh, (T*)dstates + (slot * p.dv + col) * p.dk, p.dk, col < p.dv);
-    // beta dbE = P^T dO + beta exp(b_63 - b) K dS'
-    f32x4 d[4], x[4];
-    u32x4 D[CS], Rh[CS], Rl[CS];
+    // beta dbE = beta exp(b_63 - b) K dS' + P^T dO
+    f32x4 x[4], d[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) d[t] = Columns<T, NW>::wide(Columns<T, NW>::read(st + G::kD, w, t, lane));
+    for (int t = 0; t < 4; ++t) x[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if constexpr (G::kHoist) {
+#pragma unroll
+      for (int s = 0; s < SS; ++s)
+#pragma unroll
+        for (int i = 0; i < (M::kSplit ? 2 : 1); ++i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) x[t] = M::mma(Kf[t][s], i ? Sl[s] : Sh[s], x[t]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        read_k(t, Kf[0]);
+#pragma unroll
+        for (int s = 0; s < SS; ++s) x[t] = mma_split<T>(Kf[0][s], Sh[s], Sl[s], x[t]);
+      }
+    }
+    const char* rl = st + G::kRec + lane * 16;
+    u32x4 Ph[M::kTri], Pl[M::kSplit ? M::kTri : 1], Qt[G::kHoist ? ST : 1][CS];
+#pragma unroll
+    for (int f = 0; f < M::kTri; ++f) {
+      Ph[f] = *reinterpret_cast<const u32x4*>(rl + ChunkRecT<T>::kP + f * 1024);
+      if (M::kSplit) Pl[f] = *reinterpret_cast<const u32x4*>(rl + ChunkRecT<T>::kPl + f * 1024);
+    }
+    if constexpr (G::kHoist)
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int s = 0; s < CS; ++s) Qt[t][s] = Panels<T>::frag_t(st + G::kQ, t, s, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 D[CS], Dh[CS], Dl[CS];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      d[t] = Columns<T, NW>::wide(raw[t]);
+      x[t] *= left[t];
+    }
 #pragma unroll
     for (int s = 0; s < CS; ++s) D[s] = M::frag(d + s * M::TPS);       // exact: dO is of type T
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      const int r = M::row(t, m);
+    for (int s = 0; s < CS; ++s)
 #pragma unroll
-      for (int s = 0; s < SS; ++s) acc = mma_split<T>(Panels<T>::frag(st + G::kK, r, s, g), Sh[s], Sl[s], acc);
-      acc *= *reinterpret_cast<const f32x4*>(gate + 64 + M::row(t, g * 4));
+      for (int i = 0; i < (M::kSplit ? 2 : 1); ++i)
 #pragma unroll
-      for (int s = M::first(t); s < CS; ++s) {
-        const char* f = st + G::kRec + ChunkRecT<T>::kP + M::triu(t, s) * 1024 + lane * 16;
-        acc = M::mma(*reinterpret_cast<const u32x4*>(f), D[s], acc);
-        if (M::kSplit) acc = M::mma(*reinterpret_cast<const u32x4*>(f + ChunkRecT<T>::kFrag), D[s], acc);
+        for (int t = 0; t < 4; ++t)
+          if (s >= M::first(t)) x[t] = M::mma(i ? Pl[M::kSplit ? M::triu(t, s) : 0] : Ph[M::triu(t, s)], D[s], x[t]);
+    // dS = exp(b_63) dS' + Q^T (scale exp(b) dO) - K^T (exp(b) X): the second term has nothing to wait for
+#pragma unroll
+    for (int t = 0; t < 4; ++t) d[t] *= p.scale * up[t];
+#pragma unroll
+    for (int s = 0; s < CS; ++s) M::split(d + s * M::TPS, Dh[s], Dl[s]);
+#pragma unroll
+    for (int t = 0; t < ST; ++t) S[t] *= decay;
+#pragma unroll
+    for (int s = 0; s < CS; ++s)
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        const u32x4 f = G::kHoist ? Qt[G::kHoist ? t : 0][s] : Panels<T>::frag_t(st + G::kQ, t, s, lane);
+        S[t] = M::mma(f, Dh[s], S[t]);
+        if (M::kSplit) S[t] = M::mma(f, Dl[s], S[t]);
       }
-      x[t] = acc;
+    u32x4 Th[M::kTri], Tl[M::kSplit ? M::kTri : 1], Kt[G::kHoist ? ST : 1][CS];
+#pragma unroll
+    for (int f = 0; f < M::kTri; ++f) {
+      Th[f] = *reinterpret_cast<const u32x4*>(rl + f * 1024);
+      if (M::kSplit) Tl[f] = *reinterpret_cast<const u32x4*>(rl + ChunkRecT<T>::kTl + f * 1024);
     }
+    if constexpr (G::kHoist)
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int s = 0; s < CS; ++s) Kt[t][s] = Panels<T>::frag_t(st + G::kK, t, s, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 Rh[CS], Rl[CS];
 #pragma unroll
     for (int s = 0; s < CS; ++s) M::split(x + s * M::TPS, Rh[s], Rl[s]);
     // X = T^T (beta dbE)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) x[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = M::first(t); s < CS; ++s) {
-        const char* f = st + G::kRec + M::triu(t, s) * 1024 + lane * 16;
-        const u32x4 th = *reinterpret_cast<const u32x4*>(f);
-        const u32x4 tl = M::kSplit ? *reinterpret_cast<const u32x4*>(f + ChunkRecT<T>::kTl) : th;
-        acc = mma_split2<T>(th, tl, Rh[s], Rl[s], acc);
-      }
-      x[t] = acc;
-    }
+    for (int s = 0; s < CS; ++s)
+#pragma unroll
+      for (int i = 0; i < (M::kSplit ? 3 : 1); ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (s >= M::first(t)) {
+            const int f = M::triu(t, s);
+            x[t] = M::mma(i == 2 ? Tl[M::kSplit ? f : 0] : Th[f], i == 1 ? Rl[s] : Rh[s], x[t]);
+          }
     T* xo = (T*)xs + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
 #pragma unroll
     for (int s = 0; s < CS; ++s)
       if (col < p.dv) *reinterpret_cast<u32x4*>(xo + s * M::KB) = M::frag(x + s * M::TPS);
-    // dS = exp(b_63) dS' + Q^T (scale exp(b) dO) - K^T (exp(b) X)
-    u32x4 Dh[CS], Dl[CS];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const f32x4 up = *reinterpret_cast<const f32x4*>(gate + M::row(t, g * 4));
-      x[t] *= -up;
-      d[t] *= p.scale * up;
-    }
+    for (int t = 0; t < 4; ++t) x[t] *= -up[t];
 #pragma unroll
-    for (int s = 0; s < CS; ++s) {
-      M::split(x + s * M::TPS, Rh[s], Rl[s]);
-      M::split(d + s * M::TPS, Dh[s], Dl[s]);
-    }
-    const float decay = gate[63];
+    for (int s = 0; s < CS; ++s) M::split(x + s * M::TPS, Rh[s], Rl[s]);
 #pragma unroll
-    for (int t = 0; t < ST; ++t) {
-      S[t] *= decay;
+    for (int s = 0; s < CS; ++s)
 #pragma unroll
-      for (int s = 0; s < CS; ++s) {
-        S[t] = mma_split<T>(Panels<T>::frag_t(st + G::kQ, t, s, lane), Dh[s], Dl[s], S[t]);
-        S[t] = mma_split<T>(Panels<T>::frag_t(st + G::kK, t, s, lane), Rh[s], Rl[s], S[t]);
+      for (int t = 0; t < ST; ++t) {
+        const u32x4 f = G::kHoist ? Kt[G::kHoist ? t : 0][s] : Panels<T>::frag_t(st + G::kK, t, s, lane);
+        S[t] = M::mma(f, Rh[s], S[t]);
+        if (M::kSplit) S[t] = M::mma(f, Rl[s], S[t]);
       }
-    }
   }
   if (a.dW_init) {
 #pragma unroll
@@ -187,8 +250,8 @@ __global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, 
 
 // ------------------------------------------------------------------ what is local to a chunk
 
-// One workgroup of 4 waves per chunk slot and key head; wave w makes the rows
-// of tokens row(w, .).  Every product has the tokens as the instruction's
+// One workgroup of 8 waves per chunk slot and key head; waves w and w + 4 make
+// the rows of tokens row(w, .), each half of the features.  Every product has the tokens as the instruction's
 // columns and the features (dk, or the other token) as its rows, so that a
 // lane holds 4 consecutive features of one token.  dv goes by in blocks of 128
 // bytes: the block's rows of S and dS' ([dv, dk]) and of E and X ([dv, 64])
@@ -207,34 +270,35 @@ template <typename T, int DK> struct Grads {
 };
 
 template <typename T, int DK>
-__global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
+__global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
   using M = Mat<T>;
   using G = Grads<T, DK>;
   using Rows = typename G::Rows;
-  constexpr int ST = DK / 16, SS = DK / M::KB, CS = kDC / M::KB, E = 16 / (int)sizeof(T);
+  constexpr int HT = DK / 32, SS = DK / M::KB, CS = kDC / M::KB, E = 16 / (int)sizeof(T);   // HT: half the blocks of dk
   constexpr int VS = G::BV / M::KB;                          // steps over a dv block: 2
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ double b[kDC];
-  __shared__ float beta[kDC], db[kDC], colsum[4][kDC], part[4];
+  __shared__ float beta[kDC], db[kDC], colsum[4][kDC], half[2][4][kDC], part[8];
   const DeltaArgs& p = a.f;
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   const int kh = id % p.Hk, slot = id / p.Hk, group = p.Hv / p.Hk;
   const ChunkPlace c = chunk_place(p.seqs, slot);
   if (c.len <= 0) return;
-  const int w = wave_id(), lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int wave = wave_id(), w = wave & 3, hf = wave >> 2, lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int t0 = hf * HT, j0 = hf * 2;                       // first block of dk, of the other tokens
   const int i = M::row(w, m);                                // this lane's token
   const unsigned row = p.dk * sizeof(T);
-  const PanelLoader<T, DK, 4, G::BV> sload(row, row);
-  const PanelLoader<T, kDC, 4, G::BV> eload(kDC * sizeof(T), kDC * sizeof(T));
-  const PanelLoader<T, DK, 4> qload(p.sq.t * sizeof(T), row), kload(p.sk.t * sizeof(T), row);
-  f32x4 dq[ST], dk[ST];
+  const PanelLoader<T, DK, 8, G::BV> sload(row, row);
+  const PanelLoader<T, kDC, 8, G::BV> eload(kDC * sizeof(T), kDC * sizeof(T));
+  const PanelLoader<T, DK, 8> qload(p.sq.t * sizeof(T), row), kload(p.sk.t * sizeof(T), row);
+  f32x4 dq[HT], dk[HT];
 #pragma unroll
-  for (int t = 0; t < ST; ++t) dq[t] = dk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < HT; ++t) dq[t] = dk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
   for (int h = kh * group; h < (kh + 1) * group; ++h) {
     const int64_t sh = (int64_t)slot * p.Hv + h;
     __syncthreads();                                         // the head before is done with LDS
-    if (w == 0) {
+    if (wave == 0) {
       float gi = 0.f, bi = 0.f;
       if (lane < c.len) {
         gi = p.g[c.b * p.sg.b + h * p.sg.h + (c.tok0 + lane) * p.sg.t];
@@ -249,12 +313,12 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
       b[lane] = s;
       beta[lane] = bi;
     }
-    f32x4 os[ST], xs[ST], es[ST];                            // S dO, S X, dS' E by token
+    f32x4 os[HT], xs[HT], es[HT];                            // S dO, S X, dS' E by token
 #pragma unroll
-    for (int t = 0; t < ST; ++t) os[t] = xs[t] = es[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    f32x4 oe[4], xe[4];                                      // E_j . dO_i, E_j . X_i: j = row(t, 4 g + r)
+    for (int t = 0; t < HT; ++t) os[t] = xs[t] = es[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    f32x4 oe[2], xe[2];                                      // E_j . dO_i, E_j . X_i: j = row(j0 + t, 4 g + r)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) oe[t] = xe[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 2; ++t) oe[t] = xe[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float ss = 0.f;                                          // <S, dS'>
     for (int v0 = 0; v0 < p.dv; v0 += G::BV) {
       if (v0 > 0) __syncthreads();
@@ -264,7 +328,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
       sload.issue((const T*)a.dstates + so, rows, smem + G::kDS);
       eload.issue((const T*)a.errors + eo, rows, smem + G::kE);
       eload.issue((const T*)a.xs + eo, rows, smem + G::kX);
-      const PanelLoader<T, G::BV, 4> dload(a.sdo.t * sizeof(T), rows * sizeof(T));
+      const PanelLoader<T, G::BV, 8> dload(a.sdo.t * sizeof(T), rows * sizeof(T));
       dload.issue((const T*)a.dO + c.b * a.sdo.b + h * a.sdo.h + c.tok0 * a.sdo.t + v0, c.len, smem + G::kD);
       __builtin_amdgcn_s_waitcnt(0x0f70);
       __syncthreads();
@@ -280,27 +344,27 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
         T* o = (T*)a.dv + c.b * a.sdv.b + h * a.sdv.h + (int64_t)(c.tok0 + i) * a.sdv.t + v0 + g * E;
 #pragma unroll
         for (int s = 0; s < VS; ++s)
-          if (s * M::KB + g * E < rows) *reinterpret_cast<u32x4*>(o + s * M::KB) = fx[s];
+          if (s == hf && s * M::KB + g * E < rows) *reinterpret_cast<u32x4*>(o + s * M::KB) = fx[s];
       }
 #pragma unroll
-      for (int t = 0; t < ST; ++t)
+      for (int t = 0; t < HT; ++t)
 #pragma unroll
         for (int s = 0; s < VS; ++s) {
-          const u32x4 fs = Rows::frag_t(smem + G::kS, t, s, lane);
+          const u32x4 fs = Rows::frag_t(smem + G::kS, t0 + t, s, lane);
           os[t] = M::mma(fs, fo[s], os[t]);
           xs[t] = M::mma(fs, fx[s], xs[t]);
-          es[t] = M::mma(Rows::frag_t(smem + G::kDS, t, s, lane), fe[s], es[t]);
+          es[t] = M::mma(Rows::frag_t(smem + G::kDS, t0 + t, s, lane), fe[s], es[t]);
         }
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int s = 0; s < VS; ++s) {
-          const u32x4 f = Rows::frag_t(smem + G::kE, t, s, lane);
+          const u32x4 f = Rows::frag_t(smem + G::kE, j0 + t, s, lane);
           oe[t] = M::mma(f, fo[s], oe[t]);
           xe[t] = M::mma(f, fx[s], xe[t]);
         }
       // rows past the block's are zero in LDS; the same slots of both panels hold the same element
-      for (int at = threadIdx.x * 16; at < Rows::bytes(DK); at += 256 * 16) {
+      for (int at = threadIdx.x * 16; at < Rows::bytes(DK); at += 512 * 16) {
         const u32x4 x = *reinterpret_cast<const u32x4*>(smem + G::kS + at);
         const u32x4 y = *reinterpret_cast<const u32x4*>(smem + G::kDS + at);
         if constexpr (sizeof(T) == 2) {
@@ -321,7 +385,7 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
     __builtin_amdgcn_s_waitcnt(0x0f70);
     __syncthreads();
     // q_i . k_j and k_i . k_j
-    f32x4 qk[4], kk[4];
+    f32x4 qk[2], kk[2];
     {
       u32x4 fq[SS], fk[SS];
 #pragma unroll
@@ -330,25 +394,25 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
         fk[s] = Panels<T>::frag(smem + G::kK, i, s, g);
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2; ++t) {
         qk[t] = kk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
-          const u32x4 f = Panels<T>::frag(smem + G::kK, M::row(t, m), s, g);
+          const u32x4 f = Panels<T>::frag(smem + G::kK, M::row(j0 + t, m), s, g);
           qk[t] = M::mma(f, fq[s], qk[t]);
           kk[t] = M::mma(f, fk[s], kk[t]);
         }
       }
     }
     const double bi = b[i], last = b[kDC - 1];
-    f32x4 mq[4], mk[4];
+    f32x4 mq[2], mk[2];
     float rows = 0.f;                                        // sum_j N_ij, N_ij = Mq_ij q_i.k_j + Mk_ij k_i.k_j
-    float cols[4][4];                                        // sum over this wave's i of N_ij / beta_j
+    float cols[2][4];                                        // sum over this wave's i of N_ij / beta_j
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int j = M::row(t, g * 4 + r);
+        const int j = M::row(j0 + t, g * 4 + r);
         const float bj = beta[j], d = j <= i ? __expf((float)(bi - b[j])) : 0.f;
         const float uq = j <= i ? p.scale * d * oe[t][r] : 0.f, uk = j < i ? -d * xe[t][r] : 0.f;
         mq[t][r] = uq * bj;
@@ -357,62 +421,60 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
         rows += n * bj;
         cols[t][r] = n;
       }
-    auto put_m = [&](const f32x4 (&x)[4], int to) __attribute__((always_inline)) {          // rows of tokens i, columns j
+    auto put_m = [&](const f32x4 (&x)[2], int to) __attribute__((always_inline)) {   // rows of tokens i, columns j
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        store4(reinterpret_cast<T*>(smem + to + Panels<T>::at(i, M::row(t, g * 4))), x[t][0], x[t][1], x[t][2], x[t][3]);
+      for (int t = 0; t < 2; ++t)
+        store4(reinterpret_cast<T*>(smem + to + Panels<T>::at(i, M::row(j0 + t, g * 4))), x[t][0], x[t][1], x[t][2],
+               x[t][3]);
     };
     put_m(mq, G::kM);
     if (G::kBoth) put_m(mk, G::kM + G::kMBytes);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float s = cols[t][r];
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) s += __shfl_xor(s, d, 64);
-        if (m == 0) colsum[w][M::row(t, g * 4 + r)] = s;
+        if (m == 0) colsum[w][M::row(j0 + t, g * 4 + r)] = s;
       }
-    rows += __shfl_xor(rows, 16, 64);
-    rows += __shfl_xor(rows, 32, 64);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d, 64);
-    if (lane == 0) part[w] = ss;
-    // this token's own products: scale exp(b) q.(S dO), exp(b) k.(S X), k.(dS' E)
-    float qos = 0.f, kxs = 0.f, kes = 0.f;
+    if (lane == 0) part[wave] = ss;
+    // this token's own products: scale exp(b) q.(S dO), exp(b) k.(S X), k.(dS' E), over this wave's half of dk
+    float own[4] = {rows, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < ST; ++t) {
-      const int at = Panels<T>::at(i, M::row(t, g * 4));
+    for (int t = 0; t < HT; ++t) {
+      const int at = Panels<T>::at(i, M::row(t0 + t, g * 4));
       const f32x4 q = load4(reinterpret_cast<const T*>(smem + G::kQ + at));
       const f32x4 k = load4(reinterpret_cast<const T*>(smem + G::kK + at));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        qos += q[r] * os[t][r];
-        kxs += k[r] * xs[t][r];
-        kes += k[r] * es[t][r];
+        own[1] += q[r] * os[t][r];
+        own[2] += k[r] * xs[t][r];
+        own[3] += k[r] * es[t][r];
       }
     }
 #pragma unroll
-    for (int d = 16; d < 64; d <<= 1) {
-      qos += __shfl_xor(qos, d, 64);
-      kxs += __shfl_xor(kxs, d, 64);
-      kes += __shfl_xor(kes, d, 64);
+    for (int j = 0; j < 4; ++j) {
+      own[j] += __shfl_xor(own[j], 16, 64);
+      own[j] += __shfl_xor(own[j], 32, 64);
+      if (g == 0) half[hf][j][i] = own[j];
     }
     const float up = __expf((float)bi), left = __expf((float)(last - bi)), bet = beta[i];
     const float us = p.scale * up, le = left * bet;
 #pragma unroll
-    for (int t = 0; t < ST; ++t) {
+    for (int t = 0; t < HT; ++t) {
       dq[t] += us * os[t];
       dk[t] += le * es[t] - up * xs[t];
     }
-    __syncthreads();                                         // Mq, Mk, column sums
+    __syncthreads();                                         // Mq, Mk, the sums
     // dQ += Mq K; dK += Mk K + Mk^T K + Mq^T Q
     {
       u32x4 a_q[CS], a_k[CS], t_q[CS], t_k[CS];
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
-        a_q[s] = M::frag(mq + s * M::TPS);
-        a_k[s] = M::frag(mk + s * M::TPS);
+        a_q[s] = Panels<T>::frag(smem + G::kM, i, s, g);
         t_q[s] = Panels<T>::frag_t(smem + G::kM, w, s, lane);
       }
       if (!G::kBoth) {
@@ -421,20 +483,26 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
         __syncthreads();
       }
 #pragma unroll
-      for (int s = 0; s < CS; ++s)
+      for (int s = 0; s < CS; ++s) {
+        a_k[s] = Panels<T>::frag(smem + G::kM + (G::kBoth ? G::kMBytes : 0), i, s, g);
         t_k[s] = Panels<T>::frag_t(smem + G::kM + (G::kBoth ? G::kMBytes : 0), w, s, lane);
+      }
 #pragma unroll
-      for (int t = 0; t < ST; ++t)
+      for (int t = 0; t < HT; ++t)
 #pragma unroll
         for (int s = 0; s < CS; ++s) {
-          const u32x4 fk = Panels<T>::frag_t(smem + G::kK, t, s, lane), fq = Panels<T>::frag_t(smem + G::kQ, t, s, lane);
+          const u32x4 fk = Panels<T>::frag_t(smem + G::kK, t0 + t, s, lane);
+          const u32x4 fq = Panels<T>::frag_t(smem + G::kQ, t0 + t, s, lane);
           dq[t] = M::mma(fk, a_q[s], dq[t]);
           dk[t] = M::mma(fk, a_k[s], dk[t]);
           dk[t] = M::mma(fk, t_k[s], dk[t]);
           dk[t] = M::mma(fq, t_q[s], dk[t]);
         }
     }
-    if (g == 0) {
+    if (hf == 0 && g == 0) {
+      rows = half[0][0][i] + half[1][0][i];
+      const float qos = half[0][1][i] + half[1][1][i], kxs = half[0][2][i] + half[1][2][i];
+      const float kes = half[0][3][i] + half[1][3][i];
       const float n = colsum[0][i] + colsum[1][i] + colsum[2][i] + colsum[3][i];
       const float end = le * kes;                            // through exp(b_63 - b_i)
       db[i] = us * qos - up * kxs + rows - bet * n - end;
@@ -445,11 +513,11 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
       }
     }
     __syncthreads();
-    if (w == 0) {
+    if (wave == 0) {
       float all = colsum[0][lane];
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
-      all += __expf((float)last) * (part[0] + part[1] + part[2] + part[3]);
+      all += __expf((float)last) * (part[0] + part[1] + part[2] + part[3] + part[4] + part[5] + part[6] + part[7]);
       float s = db[lane] + (lane == 63 ? all : 0.f);         // suffix sums
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -464,8 +532,8 @@ __global__ __launch_bounds__(256) void k_delta_grads(DeltaGradArgs a) {
     T* oq = (T*)a.dq + c.b * a.sdq.b + kh * a.sdq.h + (int64_t)(c.tok0 + i) * a.sdq.t;
     T* ok = (T*)a.dk + c.b * a.sdk.b + kh * a.sdk.h + (int64_t)(c.tok0 + i) * a.sdk.t;
 #pragma unroll
-    for (int t = 0; t < ST; ++t) {
-      const int d = M::row(t, g * 4);
+    for (int t = 0; t < HT; ++t) {
+      const int d = M::row(t0 + t, g * 4);
       if (d < p.dk) {
         store4(oq + d, dq[t][0], dq[t][1], dq[t][2], dq[t][3]);
         store4(ok + d, dk[t][0], dk[t][1], dk[t][2], dk[t][3]);
@@ -507,7 +575,7 @@ hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hi
   constexpr int SF = Walk<T, DK, NW, 2, kKeep, false>::kSmem <= kMax ? 2 : 1;
   constexpr int SB = WalkBack<T, DK, NW, 2>::kSmem <= kMax ? 2 : 1;
   constexpr int F = Walk<T, DK, NW, SF, kKeep, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
-  static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 2048, "LDS of a CU");
+  static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 4608, "LDS of a CU");
   auto walks = k_delta_walks<T, DK, NW, SF, SB>;
   auto grads = k_delta_grads<T, DK>;
   static const hipError_t set = [&] {
@@ -521,7 +589,7 @@ hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hi
     walks<<<dim3((unsigned)(2 * blocks)), 64 * (1 + NW), W, s>>>(a, sequences);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  if (slots > 0) grads<<<dim3((unsigned)(slots * a.f.Hk)), 256, Grads<T, DK>::kSmem, s>>>(a);
+  if (slots > 0) grads<<<dim3((unsigned)(slots * a.f.Hk)), 512, Grads<T, DK>::kSmem, s>>>(a);
   return hipGetLastError();
 }
 
