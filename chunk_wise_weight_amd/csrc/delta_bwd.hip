@@ -260,13 +260,18 @@ __global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, 
 template <typename T, int DK> struct Grads {
   static constexpr int BV = 128 / (int)sizeof(T);            // columns of a dv block
   using Rows = Panels<T, BV>;                                // its rows of S, dS', E, X
-  // Q and K take the place of S and dS' after the last block
-  static constexpr int kS = 0, kDS = Rows::bytes(DK), kQ = 0, kK = Panels<T>::bytes(DK);
-  static constexpr int kE = 2 * kK, kX = kE + Rows::bytes(kDC), kD = kX + Rows::bytes(kDC);
-  static constexpr int kSmem = kD + Panels<T>::bytes(BV);
+  static constexpr int kS = 0, kDS = Rows::bytes(DK), kE = 2 * kDS, kX = kE + Rows::bytes(kDC), kD = kX + Rows::bytes(kDC);
+  static constexpr int kBlock = kD + Panels<T>::bytes(BV), kQK = 2 * Panels<T>::bytes(DK);
+  // Where LDS has room Q and K have a place of their own, and where it has more, a block comes while the one before
+  // is worked on; the widest fp32 heads load Q and K in the place of S and dS' after a head's last block.
+  static constexpr int kLds = 160 * 1024 - 4608;             // but for the arrays of single values
+  static constexpr bool kOwnQ = kBlock + kQK <= kLds, kTwo = 2 * kBlock + kQK <= kLds;
+  static constexpr int kQ = kOwnQ ? (kTwo ? 2 : 1) * kBlock : 0, kK = kQ + kQK / 2;
+  static constexpr int kSmem = kOwnQ ? kQ + kQK : (kBlock > kQK + kBlock - kE ? kBlock : kQK + kBlock - kE);
+  static constexpr int kShift = kOwnQ ? 0 : (kQK > kE ? kQK - kE : 0);   // E, X and dO lie behind Q and K then
   // Mq and Mk take the place of E, X and dO: both at once, where there is room
-  static constexpr int kM = kE, kMBytes = Panels<T>::bytes(kDC);
-  static constexpr bool kBoth = kE + 2 * kMBytes <= kSmem;
+  static constexpr int kM = kE + kShift, kMBytes = Panels<T>::bytes(kDC);
+  static constexpr bool kBoth = kBlock - kE >= 2 * kMBytes;
 };
 
 template <typename T, int DK>
@@ -291,6 +296,24 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
   const PanelLoader<T, DK, 8, G::BV> sload(row, row);
   const PanelLoader<T, kDC, 8, G::BV> eload(kDC * sizeof(T), kDC * sizeof(T));
   const PanelLoader<T, DK, 8> qload(p.sq.t * sizeof(T), row), kload(p.sk.t * sizeof(T), row);
+  const int blocks = (p.dv + G::BV - 1) / G::BV;             // of a head; n counts them over all heads
+  auto load_qk = [&]() __attribute__((always_inline)) {
+    qload.issue((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t, c.len, smem + G::kQ);
+    kload.issue((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t, c.len, smem + G::kK);
+  };
+  auto load_block = [&](int n) __attribute__((always_inline)) {
+    char* st = smem + (G::kTwo ? (n & 1) * G::kBlock : 0);
+    const int h = kh * group + n / blocks, v0 = n % blocks * G::BV, rows = min(G::BV, p.dv - v0);
+    const int64_t sh = (int64_t)slot * p.Hv + h, so = (sh * p.dv + v0) * p.dk, eo = (sh * p.dv + v0) * kDC;
+    sload.issue((const T*)a.states + so, rows, st + G::kS);
+    sload.issue((const T*)a.dstates + so, rows, st + G::kDS);
+    eload.issue((const T*)a.errors + eo, rows, st + G::kE + G::kShift);
+    eload.issue((const T*)a.xs + eo, rows, st + G::kX + G::kShift);
+    const PanelLoader<T, G::BV, 8> dload(a.sdo.t * sizeof(T), rows * sizeof(T));
+    dload.issue((const T*)a.dO + c.b * a.sdo.b + h * a.sdo.h + c.tok0 * a.sdo.t + v0, c.len, st + G::kD + G::kShift);
+  };
+  if (G::kOwnQ) load_qk();
+  if (G::kTwo) load_block(0);
   f32x4 dq[HT], dk[HT];
 #pragma unroll
   for (int t = 0; t < HT; ++t) dq[t] = dk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -321,23 +344,21 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
     for (int t = 0; t < 2; ++t) oe[t] = xe[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float ss = 0.f;                                          // <S, dS'>
     for (int v0 = 0; v0 < p.dv; v0 += G::BV) {
-      if (v0 > 0) __syncthreads();
-      const int rows = min(G::BV, p.dv - v0);
-      const int64_t so = (sh * p.dv + v0) * p.dk, eo = (sh * p.dv + v0) * kDC;
-      sload.issue((const T*)a.states + so, rows, smem + G::kS);
-      sload.issue((const T*)a.dstates + so, rows, smem + G::kDS);
-      eload.issue((const T*)a.errors + eo, rows, smem + G::kE);
-      eload.issue((const T*)a.xs + eo, rows, smem + G::kX);
-      const PanelLoader<T, G::BV, 8> dload(a.sdo.t * sizeof(T), rows * sizeof(T));
-      dload.issue((const T*)a.dO + c.b * a.sdo.b + h * a.sdo.h + c.tok0 * a.sdo.t + v0, c.len, smem + G::kD);
-      __builtin_amdgcn_s_waitcnt(0x0f70);
+      const int rows = min(G::BV, p.dv - v0), n = (h - kh * group) * blocks + v0 / G::BV;
+      if (!G::kTwo) {
+        if (v0 > 0) __syncthreads();
+        load_block(n);
+      }
+      wait_vm<0>();
       __syncthreads();
+      if (G::kTwo && n + 1 < group * blocks) load_block(n + 1);
+      const char* st = smem + (G::kTwo ? (n & 1) * G::kBlock : 0);
       u32x4 fo[VS], fx[VS], fe[VS];                          // this lane's token, contraction over the block
 #pragma unroll
       for (int s = 0; s < VS; ++s) {
-        fo[s] = Panels<T>::frag(smem + G::kD, i, s, g);
-        fx[s] = Rows::frag_t(smem + G::kX, w, s, lane);
-        fe[s] = Rows::frag_t(smem + G::kE, w, s, lane);
+        fo[s] = Panels<T>::frag(st + G::kD + G::kShift, i, s, g);
+        fx[s] = Rows::frag_t(st + G::kX + G::kShift, w, s, lane);
+        fe[s] = Rows::frag_t(st + G::kE + G::kShift, w, s, lane);
       }
       // dV = X
       if (i < c.len) {
@@ -350,23 +371,23 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
       for (int t = 0; t < HT; ++t)
 #pragma unroll
         for (int s = 0; s < VS; ++s) {
-          const u32x4 fs = Rows::frag_t(smem + G::kS, t0 + t, s, lane);
+          const u32x4 fs = Rows::frag_t(st + G::kS, t0 + t, s, lane);
           os[t] = M::mma(fs, fo[s], os[t]);
           xs[t] = M::mma(fs, fx[s], xs[t]);
-          es[t] = M::mma(Rows::frag_t(smem + G::kDS, t0 + t, s, lane), fe[s], es[t]);
+          es[t] = M::mma(Rows::frag_t(st + G::kDS, t0 + t, s, lane), fe[s], es[t]);
         }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int s = 0; s < VS; ++s) {
-          const u32x4 f = Rows::frag_t(smem + G::kE, j0 + t, s, lane);
+          const u32x4 f = Rows::frag_t(st + G::kE + G::kShift, j0 + t, s, lane);
           oe[t] = M::mma(f, fo[s], oe[t]);
           xe[t] = M::mma(f, fx[s], xe[t]);
         }
       // rows past the block's are zero in LDS; the same slots of both panels hold the same element
       for (int at = threadIdx.x * 16; at < Rows::bytes(DK); at += 512 * 16) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(smem + G::kS + at);
-        const u32x4 y = *reinterpret_cast<const u32x4*>(smem + G::kDS + at);
+        const u32x4 x = *reinterpret_cast<const u32x4*>(st + G::kS + at);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(st + G::kDS + at);
         if constexpr (sizeof(T) == 2) {
           float u[8], v[8];
           unpack8(x, u);
@@ -380,10 +401,12 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
       }
     }
     __syncthreads();                                         // the block has been read
-    qload.issue((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t, c.len, smem + G::kQ);
-    kload.issue((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t, c.len, smem + G::kK);
-    __builtin_amdgcn_s_waitcnt(0x0f70);
-    __syncthreads();
+    if (!G::kOwnQ) {
+      load_qk();
+      wait_vm<0>();
+      __syncthreads();
+    }
+    const int m0 = G::kM + (G::kTwo ? ((h + 1 - kh * group) * blocks - 1 & 1) * G::kBlock : 0);   // Mq, Mk
     // q_i . k_j and k_i . k_j
     f32x4 qk[2], kk[2];
     {
@@ -427,8 +450,8 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
         store4(reinterpret_cast<T*>(smem + to + Panels<T>::at(i, M::row(j0 + t, g * 4))), x[t][0], x[t][1], x[t][2],
                x[t][3]);
     };
-    put_m(mq, G::kM);
-    if (G::kBoth) put_m(mk, G::kM + G::kMBytes);
+    put_m(mq, m0);
+    if (G::kBoth) put_m(mk, m0 + G::kMBytes);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -474,18 +497,18 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
       u32x4 a_q[CS], a_k[CS], t_q[CS], t_k[CS];
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
-        a_q[s] = Panels<T>::frag(smem + G::kM, i, s, g);
-        t_q[s] = Panels<T>::frag_t(smem + G::kM, w, s, lane);
+        a_q[s] = Panels<T>::frag(smem + m0, i, s, g);
+        t_q[s] = Panels<T>::frag_t(smem + m0, w, s, lane);
       }
       if (!G::kBoth) {
         __syncthreads();
-        put_m(mk, G::kM);
+        put_m(mk, m0);
         __syncthreads();
       }
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
-        a_k[s] = Panels<T>::frag(smem + G::kM + (G::kBoth ? G::kMBytes : 0), i, s, g);
-        t_k[s] = Panels<T>::frag_t(smem + G::kM + (G::kBoth ? G::kMBytes : 0), w, s, lane);
+        a_k[s] = Panels<T>::frag(smem + m0 + (G::kBoth ? G::kMBytes : 0), i, s, g);
+        t_k[s] = Panels<T>::frag_t(smem + m0 + (G::kBoth ? G::kMBytes : 0), w, s, lane);
       }
 #pragma unroll
       for (int t = 0; t < HT; ++t)
