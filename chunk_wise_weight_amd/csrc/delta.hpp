@@ -123,7 +123,7 @@ template <typename T> struct ChunkRec {
   static constexpr int kP = kGate + 1024;
   static constexpr int kBytes = kP + kFrag;
 };
-// The same for the backward pass: the transposes of T and P (hi, lo each), the gates.
+// The same for the backward pass: the transposes of T and P (hi, lo each), the gates, and b itself (64 doubles).
 template <typename T> struct ChunkRecT {
   static constexpr int kFrag = ChunkRec<T>::kFrag;
   static constexpr int kTl = kFrag;

@@ -283,7 +283,7 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
   constexpr int VS = G::BV / M::KB;                          // steps over a dv block: 2
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ double b[kDC];
-  __shared__ float beta[kDC], db[kDC], colsum[4][kDC], half[2][4][kDC], part[8];
+  __shared__ float beta[kDC], colsum[4][kDC], half[2][4][kDC], part[8];
   const DeltaArgs& p = a.f;
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   const int kh = id % p.Hk, slot = id / p.Hk, group = p.Hv / p.Hk;
@@ -322,19 +322,10 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
     const int64_t sh = (int64_t)slot * p.Hv + h;
     __syncthreads();                                         // the head before is done with LDS
     if (wave == 0) {
-      float gi = 0.f, bi = 0.f;
-      if (lane < c.len) {
-        gi = p.g[c.b * p.sg.b + h * p.sg.h + (c.tok0 + lane) * p.sg.t];
-        bi = p.beta[c.b * p.sbeta.b + h * p.sbeta.h + (c.tok0 + lane) * p.sbeta.t];
-      }
-      double s = gi < -200.f ? -200.0 : (double)gi;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double up = __shfl_up(s, d, 64);
-        if (lane >= d) s += up;
-      }
-      b[lane] = s;
-      beta[lane] = bi;
+      const char* gate = a.rect + sh * ChunkRecT<T>::kBytes + ChunkRecT<T>::kGate;
+      b[lane] = reinterpret_cast<const double*>(gate + 512)[lane];
+      beta[lane] =
+          lane < c.len ? p.beta[c.b * p.sbeta.b + h * p.sbeta.h + (c.tok0 + lane) * p.sbeta.t] : 0.f;
     }
     f32x4 os[HT], xs[HT], es[HT];                            // S dO, S X, dS' E by token
 #pragma unroll
@@ -492,6 +483,27 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
       dk[t] += le * es[t] - up * xs[t];
     }
     __syncthreads();                                         // Mq, Mk, the sums
+    if (wave == 0) {                                         // lane: token
+      const float row_sum = half[0][0][lane] + half[1][0][lane], qos = half[0][1][lane] + half[1][1][lane];
+      const float kxs = half[0][2][lane] + half[1][2][lane], kes = half[0][3][lane] + half[1][3][lane];
+      const float n = colsum[0][lane] + colsum[1][lane] + colsum[2][lane] + colsum[3][lane];
+      const float up = __expf((float)b[lane]), left = __expf((float)(last - b[lane])), end = left * beta[lane] * kes;
+      float s = p.scale * up * qos - up * kxs + row_sum - beta[lane] * n - end, all = end;   // db, and its part at 63
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
+      all += __expf((float)last) * (part[0] + part[1] + part[2] + part[3] + part[4] + part[5] + part[6] + part[7]);
+      if (lane == 63) s += all;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {                     // suffix sums
+        const float down = __shfl_down(s, d, 64);
+        if (lane + d < 64) s += down;
+      }
+      if (lane < c.len) {
+        const int64_t t = c.tok0 + lane;
+        ((T*)a.dg)[c.b * a.sdg.b + h * a.sdg.h + t * a.sdg.t] = from_f32<T>(s);
+        ((T*)a.dbeta)[c.b * a.sdbeta.b + h * a.sdbeta.h + t * a.sdbeta.t] = from_f32<T>(n + left * kes);
+      }
+    }
     // dQ += Mq K; dK += Mk K + Mk^T K + Mq^T Q
     {
       u32x4 a_q[CS], a_k[CS], t_q[CS], t_k[CS];
@@ -521,34 +533,6 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
           dk[t] = M::mma(fk, t_k[s], dk[t]);
           dk[t] = M::mma(fq, t_q[s], dk[t]);
         }
-    }
-    if (hf == 0 && g == 0) {
-      rows = half[0][0][i] + half[1][0][i];
-      const float qos = half[0][1][i] + half[1][1][i], kxs = half[0][2][i] + half[1][2][i];
-      const float kes = half[0][3][i] + half[1][3][i];
-      const float n = colsum[0][i] + colsum[1][i] + colsum[2][i] + colsum[3][i];
-      const float end = le * kes;                            // through exp(b_63 - b_i)
-      db[i] = us * qos - up * kxs + rows - bet * n - end;
-      colsum[0][i] = end;
-      if (i < c.len) {
-        const int64_t t = c.tok0 + i;
-        ((T*)a.dbeta)[c.b * a.sdbeta.b + h * a.sdbeta.h + t * a.sdbeta.t] = from_f32<T>(n + left * kes);
-      }
-    }
-    __syncthreads();
-    if (wave == 0) {
-      float all = colsum[0][lane];
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
-      all += __expf((float)last) * (part[0] + part[1] + part[2] + part[3] + part[4] + part[5] + part[6] + part[7]);
-      float s = db[lane] + (lane == 63 ? all : 0.f);         // suffix sums
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const float down = __shfl_down(s, d, 64);
-        if (lane + d < 64) s += down;
-      }
-      if (lane < c.len)
-        ((T*)a.dg)[c.b * a.sdg.b + h * a.sdg.h + (int64_t)(c.tok0 + lane) * a.sdg.t] = from_f32<T>(s);
     }
   }
   if (i < c.len) {

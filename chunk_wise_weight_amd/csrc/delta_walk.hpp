@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_chunks(DeltaArgs p, cha
       gate = reinterpret_cast<float*>(rect + (int64_t)id * ChunkRecT<T>::kBytes + ChunkRecT<T>::kGate);
       gate[lane] = up;
       gate[64 + lane] = left;
+      reinterpret_cast<double*>(gate + 128)[lane] = s;
     }
   }
 
