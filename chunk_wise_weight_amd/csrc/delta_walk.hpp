@@ -61,6 +61,31 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_chunks(DeltaArgs p, cha
   const int w = wave_id(), lane = lane_id(), m = lane & 15, g = lane >> 4;
   const int kh = h / (p.Hv / p.Hk);
 
+  // Rows of this wave's block against all blocks up to it, GS steps' operands at a time straight from memory, the
+  // first of them under way while the gates are made.  Columns past dk read as zero.
+  constexpr int GS = 4;
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) kk[t] = qk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const __amdgpu_buffer_rsrc_t rk = rows_rsrc((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t);
+  const __amdgpu_buffer_rsrc_t rq = rows_rsrc((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t);
+  const unsigned row_bytes = p.dk * sizeof(T), kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T);
+  u32x4 fk[GS][4], fq[GS];
+  auto load = [&](int s0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < GS; ++s) {
+      const unsigned byte = (s0 + s) * 64 + g * 16;
+      const int r = w * 16 + m;
+      fq[s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < c.len && byte < row_bytes ? r * qp + byte : kOOB, 0, 0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t <= w) {
+          const int j = t * 16 + m;
+          fk[s][t] = __builtin_amdgcn_raw_buffer_load_b128(rk, j < c.len && byte < row_bytes ? j * kp + byte : kOOB, 0, 0);
+        }
+    }
+  };
+  load(0);
   if (w == 0) {
     float gi = 0.f, bi = 0.f;
     if (lane < c.len) {
@@ -89,37 +114,21 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_chunks(DeltaArgs p, cha
     }
   }
 
-  // rows of this wave's block against all blocks up to it
-  f32x4 kk[4], qk[4];
+  for (int s0 = 0; s0 * KB < p.dk; s0 += GS) {
+    if (s0 > 0) load(s0);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) kk[t] = qk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  const __amdgpu_buffer_rsrc_t rk =
-      make_rsrc((const T*)p.k + c.b * p.sk.b + kh * p.sk.h + c.tok0 * p.sk.t, (uint64_t)kOOB);
-  const __amdgpu_buffer_rsrc_t rq =
-      make_rsrc((const T*)p.q + c.b * p.sq.b + kh * p.sq.h + c.tok0 * p.sq.t, (uint64_t)kOOB);
-  const unsigned row_bytes = p.dk * sizeof(T), kp = p.sk.t * sizeof(T), qp = p.sq.t * sizeof(T);
-  for (int s = 0; s * KB < p.dk; ++s) {
-    const unsigned byte = s * 64 + g * 16;
-    const int r = w * 16 + m;
-    const u32x4 fq =
-        __builtin_amdgcn_raw_buffer_load_b128(rq, r < c.len && byte < row_bytes ? r * qp + byte : kOOB, 0, 0);
-    u32x4 fk[4];
+    for (int s = 0; s < GS; ++s) {
+      u32x4 mine = fk[s][0];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t <= w) {
-        const int j = t * 16 + m;
-        fk[t] = __builtin_amdgcn_raw_buffer_load_b128(rk, j < c.len && byte < row_bytes ? j * kp + byte : kOOB, 0, 0);
-      }
-    u32x4 mine = fk[0];
+      for (int t = 1; t < 4; ++t)
+        if (t == w) mine = fk[s][t];
 #pragma unroll
-    for (int t = 1; t < 4; ++t)
-      if (t == w) mine = fk[t];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t <= w) {
-        kk[t] = Mat<T>::mma(mine, fk[t], kk[t]);
-        qk[t] = Mat<T>::mma(fq, fk[t], qk[t]);
-      }
+      for (int t = 0; t < 4; ++t)
+        if (t <= w) {
+          kk[t] = Mat<T>::mma(mine, fk[s][t], kk[t]);
+          qk[t] = Mat<T>::mma(fq[s], fk[s][t], qk[t]);
+        }
+    }
   }
   __syncthreads();
 #pragma unroll
