@@ -28,9 +28,6 @@ hipError_t launch_walk(const DeltaArgs& a, int sequences, hipStream_t s) {
   using G = Walk<T, DK, NW, STAGES, OUT, QLDS>;
   static_assert(G::kSmem <= kMaxLds, "one stage has to fit");
   auto kern = k_delta_walk<T, DK, NW, STAGES, OUT, QLDS>;
-  static const hipError_t set =
-      hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
-  if (set != hipSuccess) return set;
   const int64_t blocks = walk_blocks((int64_t)sequences * a.Hk, a.Hv / a.Hk * ((a.dv + 16 * NW - 1) / (16 * NW)));
   kern<<<dim3((unsigned)blocks), G::kThreads, G::kSmem, s>>>(a, a.ws, sequences);
   return hipGetLastError();

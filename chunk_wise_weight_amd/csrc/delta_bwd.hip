@@ -571,11 +571,6 @@ size_t place(DeltaGradArgs& a) {
   return at;
 }
 
-template <typename F>
-hipError_t with_smem(F kern, int bytes) {
-  return hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <typename T, int DK, int NW>
 hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hipStream_t s) {
   constexpr int kMax = 160 * 1024;
@@ -585,11 +580,6 @@ hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hi
   static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 4608, "LDS of a CU");
   auto walks = k_delta_walks<T, DK, NW, SF, SB>;
   auto grads = k_delta_grads<T, DK>;
-  static const hipError_t set = [&] {
-    hipError_t e = with_smem(walks, W);
-    return e != hipSuccess ? e : with_smem(grads, Grads<T, DK>::kSmem);
-  }();
-  if (set != hipSuccess) return set;
   if (sequences > 0) {
     const int64_t blocks =
         walk_blocks((int64_t)sequences * a.f.Hk, a.f.Hv / a.f.Hk * ((a.f.dv + 16 * NW - 1) / (16 * NW)));

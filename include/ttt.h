@@ -744,7 +744,8 @@ int ttt_gated_delta_workspace_bytes(const ttt_delta_shape* shape, int dtype, int
  *   O         [B, Hv, n, dv]  dtype   (written)
  *   W_final   [sequences, Hv, dv, dk] fp32 (written)  sequences = B, or num_seqs
  * A log decay of -inf (or below -200) sets the state to zero before the
- * token's step: a document boundary inside a sequence.  With bf16 inputs the
+ * token's step: a document boundary inside a sequence.  beta = 0 leaves the
+ * state as it is (the token's k and v have to be finite all the same).  With bf16 inputs the
  * state and what feeds it keep 16 bits or more of mantissa throughout.
  * seq_len == 0 or an empty sequence: W_final is W_init (or zero). */
 int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const void* q, const void* k, const void* v,

@@ -13,8 +13,11 @@ Modules:
   lact     -- the LaCT SwiGLU fast weight: full-chunk MSE gradient, plain GD,
               update-then-apply (or apply-then-update) over chunks.
 
+  delta    -- the gated delta rule token by token, its reverse recurrence,
+              and layer norm with its backward.
+
 Every function is pinned by the CPU tests against something other than
 itself (library routines, closed forms, brute force, finite differences,
 autograd).  Nothing here is "parity unpinned".
 """
-from . import inplace, lact  # noqa: F401
+from . import delta, inplace, lact  # noqa: F401
