@@ -13,12 +13,12 @@ __global__ __launch_bounds__((Walk<T, DK, NW, STAGES, OUT, QLDS>::kThreads)) voi
   if (!walk_place(blockIdx.x, sequences, p.Hk, p.Hv / p.Hk, (p.dv + 16 * NW - 1) / (16 * NW), &at)) return;
   const SeqPlace sp = seq_place(p.seqs, at.seq);
   const int w = wave_id();
-  if (w == 0)
-    walk_loads<T, DK, NW, STAGES, OUT, QLDS>(p, rec, at, sp);
-  else if (w <= NW)
-    walk_states<T, DK, NW, STAGES, OUT, QLDS>(p, w - 1, nullptr, nullptr, at, sp);
+  if (w < 2)
+    walk_loads<T, DK, NW, STAGES, OUT, QLDS>(p, 1 << w, rec, at, sp);
+  else if (w < 2 + NW)
+    walk_states<T, DK, NW, STAGES, OUT, QLDS>(p, w - 2, nullptr, nullptr, at, sp);
   else if constexpr (OUT == kHelped)
-    walk_outputs<T, DK, NW, STAGES, QLDS>(p, rec, w - 1 - NW, at, sp);
+    walk_outputs<T, DK, NW, STAGES, QLDS>(p, rec, w - 2 - NW, at, sp);
 }
 
 constexpr int kMaxLds = 160 * 1024;

@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * (1 + NW)) void k_delta_walks(DeltaGradArgs a, 
     else
       walk_back<T, DK, NW, SB>(a, w - 1, at, sp);
   } else if (w == 0) {
-    walk_loads<T, DK, NW, SF, kKeep, false>(p, a.rec, at, sp);
+    walk_loads<T, DK, NW, SF, kKeep, false>(p, 3, a.rec, at, sp);
   } else {
     walk_states<T, DK, NW, SF, kKeep, false>(p, w - 1, a.states, a.errors, at, sp);
   }

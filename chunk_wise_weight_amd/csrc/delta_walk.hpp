@@ -256,9 +256,13 @@ __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const f32x4 
 
 // A workgroup walks one sequence of one value head with NW state waves, each
 // keeping 16 columns of the state (dv), which need nothing of the others.
-// Wave 0 brings each chunk's K, T, gates and the group's columns of V to LDS by
-// DMA while the chunk before is worked on (two stages; the widest heads have
-// room for one only).  A state wave's chunk is a chain of dependent products
+// Waves 0 and 1 bring each chunk's K, T, gates and the group's columns of V to
+// LDS by DMA while the chunk before is worked on (two stages; the widest heads
+// have room for one only).  One wave takes longer to issue all of a chunk's
+// loads: 1.77 instead of 1.69 ms for 64K tokens of 32 heads; the backward's
+// walks, whose workgroups fill the chip, are better off with one (233 instead
+// of 247 us for 4 x 4K of 16).
+// A state wave's chunk is a chain of dependent products
 // (K S, T R, K^T E).  One barrier a chunk.  By OUT:
 //   kHelped  as many helper waves, one chunk behind, make O from the state and
 //            the errors that the state waves left in LDS, their Q and P coming
@@ -279,13 +283,13 @@ template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS> struct Wal
   static constexpr int kSwap = kG + STAGES * kStageQ;      // a state wave's state operands and errors (fp32), twice
   static constexpr int kSwapBytes = SS * 1024 + 4096;
   static constexpr int kSmem = kSwap + (OUT == kHelped ? 2 * NW * kSwapBytes : 0);
-  static constexpr int kThreads = 64 * (1 + NW * (OUT == kHelped ? 2 : 1));
+  static constexpr int kThreads = 64 * (2 + NW * (OUT == kHelped ? 2 : 1));   // kKeep: with one DMA wave, 64 fewer
   static constexpr int kLag = OUT == kHelped ? 1 : 0;      // turns that O is behind
   static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
 };
 
 template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS>
-__device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, const WalkPlace& at,
+__device__ __forceinline__ void walk_loads(const DeltaArgs& p, int parts, const char* rec, const WalkPlace& at,
                                            const SeqPlace& sp) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   using G = Walk<T, DK, NW, STAGES, OUT, QLDS>;
@@ -300,18 +304,20 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, const char* rec, 
   const Columns<T, NW> vload(vp, p.dv - first);
   // turn c: the state waves at chunk c, O at chunk c - kLag
   auto issue = [&](int c) __attribute__((always_inline)) {
-    if (c < chunks) {
-      char* st = smem + c % STAGES * G::kStage;
-      const int len = min(kDC, sp.len - c * kDC);
-      kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
-      load_block<ChunkRec<T>::kP / 1024>(rec0 + c * rstep, st + G::kRec);
-      vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
+    const int d = c - G::kLag, len = min(kDC, sp.len - c * kDC);
+    char* st = smem + c % STAGES * G::kStage;
+    char* sq = smem + G::kG + d % STAGES * G::kStageQ;
+    const bool out = OUT != kKeep && QLDS && d >= 0;
+    if (parts & 1) {
+      if (c < chunks) {
+        kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
+        vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
+      }
+      if (out) load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, sq);
     }
-    const int d = c - G::kLag;
-    if (OUT != kKeep && QLDS && d >= 0) {
-      char* st = smem + G::kG + d % STAGES * G::kStageQ;
-      qload.issue(q0 + (int64_t)d * kDC * p.sq.t, min(kDC, sp.len - d * kDC), st + G::kQ);
-      load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, st);
+    if (parts & 2) {
+      if (c < chunks) load_block<ChunkRec<T>::kP / 1024>(rec0 + c * rstep, st + G::kRec);
+      if (out) qload.issue(q0 + (int64_t)d * kDC * p.sq.t, min(kDC, sp.len - d * kDC), sq + G::kQ);
     }
   };
   dma_wave<STAGES>(chunks > 0 ? chunks + G::kLag : 0, issue);
