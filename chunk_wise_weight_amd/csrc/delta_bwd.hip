@@ -20,6 +20,15 @@
 // (the division is by a factor of the summands, which are taken without it).
 // Gradients of a key head sum over its value heads, one after the other in one
 // workgroup: no atomics.
+//
+// Rounding (bf16).  The walks' states are fp32 with operands in pairs, as in
+// the forward pass, so dW_init keeps fp32's digits; what they leave in memory
+// is bf16, each value rounded once, and so are Mq and Mk: they feed only
+// gradients that are rounded to bf16 themselves (dq, dk, dg, dbeta are off by
+// 2.9e-3 of their norm, 1.7e-3 being the last rounding).
+//
+// 4 x 4096 tokens, 16 value heads of 128: walks 235 us, chunk-local gradients
+// 226 us (56 KB of operands a head and dv block; bound by those and by LDS).
 #include "delta_walk.hpp"
 
 namespace ttt {
