@@ -312,3 +312,42 @@ def test_other_stream_and_two_calls_at_once():
             y = cw.ttt_gated_delta(*other)
         torch.cuda.synchronize()
         assert all(torch.equal(s, t) for s, t in zip(x + y, ref + ref2))
+
+
+def test_starts_outside_the_row_are_taken_as_its_ends():
+    q, k, v, g, beta = make(1, 1, 2, 100, 64, 64, torch.bfloat16)
+    starts = lambda *s: torch.tensor(s, dtype=torch.int32, device="cuda")
+    O, W = cw.ttt_gated_delta(q, k, v, g, beta, seq_starts=starts(0, 40, 100, 100))
+    O2, W2 = cw.ttt_gated_delta(q, k, v, g, beta, seq_starts=starts(-5, 40, 1000, 1 << 30))
+    assert torch.equal(O, O2) and torch.equal(W, W2)
+
+
+def test_offsets_past_32_bits():
+    """Rows further apart than 2^31 elements, and a state of the pool further in than that."""
+    n, far = 70, (1 << 31) + 4096
+    base = torch.zeros(far + 64 * n, dtype=torch.bfloat16, device="cuda")
+    near = make(2, 1, 1, n, 64, 64, torch.bfloat16, "head", seed=8)
+    views = []
+    for t in near[:3]:                              # one tensor after the other at the same far places
+        view = base.as_strided((2, 1, n, 64), (far, n * 64, 64, 1))
+        view.copy_(t)
+        args = [view if x is t else x for x in near]
+        O, W = cw.ttt_gated_delta(*args)
+        ref = cw.ttt_gated_delta(*near)
+        assert torch.equal(O, ref[0]) and torch.equal(W, ref[1])
+        views.append(view)
+    out = views[0]
+    out.zero_()
+    cw.ttt_gated_delta(*near, O=out)
+    assert torch.equal(out, cw.ttt_gated_delta(*near)[0])
+    dO = torch.randn_like(near[2])
+    d = cw.ttt_gated_delta_backward(*near, dO)
+    d2 = cw.ttt_gated_delta_backward(*near, dO, dk=out)
+    assert all(torch.equal(a, b) for a, b in zip(d[:5], d2[:5]))
+    del base, views, view, out, args, d2
+    q, k, v, g, beta, W = make_step(2, 2, 1, 32, 128, 128, torch.bfloat16)
+    P = 4100                                        # 4100 x 32 x 128 x 128 > 2^31
+    pool = torch.empty(P, 32, 128, 128, device="cuda")
+    pool[[P - 1, 0]] = W
+    o = cw.ttt_gated_delta_step(q, k, v, g, beta, pool, slots=torch.tensor([P - 1, 0], dtype=torch.int32, device="cuda"))
+    assert torch.equal(o, cw.ttt_gated_delta_step(q, k, v, g, beta, W)) and torch.equal(pool[[P - 1, 0]], W)

@@ -168,3 +168,21 @@ def test_norm_in_front_of_the_layer_and_back():
     dHr = orc.layer_backward(Hr, *(ti.to_f64(t[k].cpu()) for k in names), cfg.chunk, cfg.eta, f64(dO))[0]
     dxr, dwr, dbr = od.layer_norm_backward(f64(x).reshape(512, 64), f64(w), dHr.reshape(512, 64), mr, rr)
     assert rel(O, Or) <= 1e-4 and rel(dx.reshape(512, 64), dxr) <= 1e-4 and rel(dw, dwr) <= 1e-4 and rel(db, dbr) <= 1e-4
+
+
+def test_offsets_past_32_bits():
+    rows, d = 270000, 8192                          # 2.2e9 elements
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    tail, w, b, dy = make(3, d, torch.bfloat16)
+    x[-3:] = tail
+    y, mean, rstd = cw.ttt_layer_norm(x, w, b)
+    ref = cw.ttt_layer_norm(tail, w, b)
+    assert torch.equal(y[-3:], ref[0]) and torch.equal(mean[-3:], ref[1]) and torch.equal(rstd[-3:], ref[2])
+    assert torch.equal(y[:2], b.expand(2, d))
+    y.zero_()                                       # as dY
+    y[-3:] = dy
+    dx, dw, db = cw.ttt_layer_norm_backward(x, w, y, mean, rstd)
+    rx, rw, rb = cw.ttt_layer_norm_backward(tail, w, dy, *ref[1:])
+    assert torch.equal(dx[-3:], rx) and not dx[:2].any()
+    # three rows' sums among zeros: fp32 sums of three terms in another order, 3 * 2^-24 each
+    assert rel(dw, f64(rw)) <= 2.0 ** -21 and rel(db, f64(rb)) <= 2.0 ** -21
