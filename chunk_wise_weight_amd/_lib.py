@@ -910,7 +910,8 @@ def ttt_gated_delta(q, k, v, g, beta, scale=None, W_init=None, seq_starts=None, 
     ws = _workspace(nbytes, dev, workspace)
     opts = DeltaOptions(_at(W_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
     _launch(dev, "ttt_gated_delta", lib().ttt_gated_delta, shape, dt,
-            states[3] ** -0.5 if scale is None else float(scale), _at(q), _at(k), _at(v), _at(g), _at(beta), ctypes.byref(opts), _at(O), _at(W_final), _at(ws), nbytes)
+            states[3] ** -0.5 if scale is None else float(scale), _at(q), _at(k), _at(v), _at(g), _at(beta),
+            ctypes.byref(opts), _at(O), _at(W_final), _at(ws), nbytes)
     return O, W_final
 
 

@@ -17,7 +17,9 @@
  * with Z = silu(H W_gate^T) * (H W_up^T) (eq. (2)) and the target
  * V^ = CausalDepthwiseConv1D(X0) W_target (eq. (5), causal padding of §3).
  * A LaCT SwiGLU fast weight (review of "Test-Time Training Done Right",
- * LaCT Model Architecture §1, eq. (3)-(4)) is the second layer family.
+ * LaCT Model Architecture §1, eq. (3)-(4)) is the second layer family.  The
+ * gated delta rule (one decayed gradient step a token) is the third; layer
+ * norm stands beside them.
  *
  * Conventions common to every entry point:
  *   - Every tensor pointer is a DEVICE pointer owned by the caller (e.g.
