@@ -15,8 +15,12 @@ namespace {
 //   T_ij = -T_ii sum_{j <= l < i} A_il T_lj,   A = L diag(beta),
 // wave j taking column j: fp32 MFMA products, the running block column staying
 // in registers as the next product's operand.  64K tokens of 32 heads of 128:
-// 419 us, of which the operands' loads and products about 150, the inverse 100,
-// the exponentials 30 and the stores 60.
+// 372 us, of which the operands' loads and products about 150, the inverse 100,
+// the exponentials 30 and the stores 60: each workgroup is a chain of short
+// phases, so the more of them a CU holds the better.  Forward: operands of two
+// steps at a time and four waves a SIMD (372 us; four steps and three waves
+// 419); the backward's form, with twice the stores, is better off with the
+// latter (70 us for 4 x 4096 tokens of 16 heads; 79).
 constexpr int kChunkThreads = 256;
 constexpr int kLd = 68;           // pitch of a 64 x 64 fp32 matrix in LDS
 
@@ -50,7 +54,8 @@ __device__ __forceinline__ void put_triangle(const float* X, char* hi, char* lo)
 
 // With BACK, T goes to rec and the transposes of T and P to rect.
 template <typename T, bool BACK>
-__global__ __launch_bounds__(kChunkThreads) void k_delta_chunks(DeltaArgs p, char* rec, char* rect) {
+__global__ __launch_bounds__(kChunkThreads) __attribute__((amdgpu_waves_per_eu(BACK ? 3 : 4))) void k_delta_chunks(
+    DeltaArgs p, char* rec, char* rect) {
   constexpr int KB = Mat<T>::KB;
   __shared__ __attribute__((aligned(16))) float A[kDC * kLd], X[kDC * kLd];   // X: P, then T
   __shared__ double b[kDC];
@@ -65,7 +70,7 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_chunks(DeltaArgs p, cha
 
   // Rows of this wave's block against all blocks up to it, GS steps' operands at a time straight from memory, the
   // first of them under way while the gates are made.  Columns past dk read as zero.
-  constexpr int GS = 4;
+  constexpr int GS = BACK ? 4 : 2;
   f32x4 kk[4], qk[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) kk[t] = qk[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
