@@ -12,8 +12,9 @@
 // contiguous.  Rows of up to 128 vectors belong to one wave or a quarter of
 // one: no barrier, and a workgroup works on 4 rows or more.  Wider rows have a
 // workgroup of as many waves as they fill (TPR = 0: its size, up to 1024), one
-// vector a thread while that reaches.  VEC = 16 bytes where the row length
-// keeps every row 16-byte aligned, else 1.  Forward 131072 x 2560 bf16: 280
+// vector a thread while that reaches.  VEC = 16 bytes.  RAG: row lengths that
+// are no multiple of it: rows then start at any element, so the vectors are
+// read and written without alignment, and a row's last one element by element.  Forward 131072 x 2560 bf16: 280
 // us, 4.8 TB/s; backward 32768 x 2560: 106 us, 524288 x 128: 81 us, 5 TB/s.
 #include <algorithm>
 
@@ -29,32 +30,47 @@ constexpr int kNormThreads = 256;
 template <typename T, int VEC> struct Pack;
 template <> struct Pack<bf16, 8> { u32x4 w; };
 template <> struct Pack<float, 4> { f32x4 w; };
-template <> struct Pack<bf16, 1> { bf16 w; };
-template <> struct Pack<float, 1> { float w; };
 
 __device__ __forceinline__ void widen(const Pack<bf16, 8>& p, float* o) { unpack8(p.w, o); }
 __device__ __forceinline__ void widen(const Pack<float, 4>& p, float* o) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = p.w[i];
 }
-__device__ __forceinline__ void widen(const Pack<bf16, 1>& p, float* o) { o[0] = to_f32(p.w); }
-__device__ __forceinline__ void widen(const Pack<float, 1>& p, float* o) { o[0] = p.w; }
 
 __device__ __forceinline__ void narrow(const float* o, Pack<bf16, 8>& p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) p.w[i] = pack2_bf16(o[2 * i], o[2 * i + 1]);
 }
 __device__ __forceinline__ void narrow(const float* o, Pack<float, 4>& p) { p.w = (f32x4){o[0], o[1], o[2], o[3]}; }
-__device__ __forceinline__ void narrow(const float* o, Pack<bf16, 1>& p) { p.w = from_f32<bf16>(o[0]); }
-__device__ __forceinline__ void narrow(const float* o, Pack<float, 1>& p) { p.w = o[0]; }
 
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_pack(const T* p) {
-  return *reinterpret_cast<const Pack<T, VEC>*>(p);
+// `left` elements remain from p to the row's end (RAG; else they are VEC or more); those past it are zero.
+template <typename T, int VEC, bool RAG>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T* p, int left) {
+  if constexpr (!RAG) return *reinterpret_cast<const Pack<T, VEC>*>(p);
+  Pack<T, VEC> o;
+  if (left >= VEC) {
+    __builtin_memcpy(&o, p, sizeof(o));
+  } else {
+    T e[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) e[j] = j < left ? p[j] : (T)0.f;
+    __builtin_memcpy(&o, e, sizeof(o));
+  }
+  return o;
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& v) {
-  *reinterpret_cast<Pack<T, VEC>*>(p) = v;
+template <typename T, int VEC, bool RAG>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& v, int left) {
+  if constexpr (!RAG) {
+    *reinterpret_cast<Pack<T, VEC>*>(p) = v;
+  } else if (left >= VEC) {
+    __builtin_memcpy(p, &v, sizeof(v));
+  } else {
+    T e[VEC];
+    __builtin_memcpy(e, &v, sizeof(v));
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < left) p[j] = e[j];
+  }
 }
 
 // Sums of N values over the threads of a row, given to all of them.  Where a
@@ -82,10 +98,11 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& turn) {
   }
 }
 
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, bool RAG, int TPR, int NV>
 __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
     const T* __restrict__ x, const T* __restrict__ weight, const T* __restrict__ bias, T* __restrict__ y,
     float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int d, float eps) {
+  constexpr int VEC = Vec<T>::V;
   const int tpr = TPR ? TPR : (int)blockDim.x, rpb = TPR ? kNormThreads / TPR : 1;
   __shared__ float red[TPR ? 1 : 2 * 16];
   const int t = threadIdx.x % tpr;
@@ -97,7 +114,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + t) * VEC;
-      if (e < d) raw[i] = load_pack<T, VEC>(xr + e);
+      if (e < d) raw[i] = load_pack<T, VEC, RAG>(xr + e, d - e);
     }
     float v[NV][VEC];
     float s[1] = {0.f};
@@ -117,7 +134,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
       if ((i * tpr + t) * VEC < d) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          v[i][j] -= mu;
+          v[i][j] = !RAG || (i * tpr + t) * VEC + j < d ? v[i][j] - mu : 0.f;
           s[0] += v[i][j] * v[i][j];
         }
       }
@@ -135,13 +152,13 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
       if (e < d) {
         float w[VEC], b[VEC];
         if (weight) {
-          widen(load_pack<T, VEC>(weight + e), w);
+          widen(load_pack<T, VEC, RAG>(weight + e, d - e), w);
         } else {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) w[j] = 1.f;
         }
         if (bias) {
-          widen(load_pack<T, VEC>(bias + e), b);
+          widen(load_pack<T, VEC, RAG>(bias + e, d - e), b);
         } else {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) b[j] = 0.f;
@@ -150,7 +167,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
         for (int j = 0; j < VEC; ++j) v[i][j] = v[i][j] * r * w[j] + b[j];
         Pack<T, VEC> o;
         narrow(v[i], o);
-        store_pack<T, VEC>(yr + e, o);
+        store_pack<T, VEC, RAG>(yr + e, o, d - e);
       }
     }
   }
@@ -161,11 +178,11 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm(
 // of its columns' dY h and dY in registers; its rows' sums meet in LDS at the
 // end and go to part[blockIdx.x][2][d], which k_norm_grad_sum adds up in block
 // order: no atomics, the same bits every run.
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, bool RAG, int TPR, int NV>
 __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
     const T* __restrict__ x, const T* __restrict__ weight, const T* __restrict__ dy, const float* __restrict__ mean,
     const float* __restrict__ rstd, T* __restrict__ dx, float* __restrict__ part, int64_t rows, int d, bool want_db) {
-  constexpr int RPB = TPR ? kNormThreads / TPR : 1;
+  constexpr int VEC = Vec<T>::V, RPB = TPR ? kNormThreads / TPR : 1;
   const int tpr = TPR ? TPR : (int)blockDim.x;
   __shared__ float red[TPR ? 1 : 4 * 16];
   __shared__ float cols[RPB > 1 ? TPR * VEC * RPB : 1];       // one vector's sums of every row slot
@@ -180,7 +197,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
       w[i][j] = 1.f;
       dw[i][j] = db[i][j] = 0.f;
     }
-    if (weight && e < d) widen(load_pack<T, VEC>(weight + e), w[i]);
+    if (weight && e < d) widen(load_pack<T, VEC, RAG>(weight + e, d - e), w[i]);
   }
   struct Row {
     Pack<T, VEC> x[NV], g[NV];
@@ -191,8 +208,8 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + t) * VEC;
       if (e < d) {
-        o.x[i] = load_pack<T, VEC>(x + row * d + e);
-        o.g[i] = load_pack<T, VEC>(dy + row * d + e);
+        o.x[i] = load_pack<T, VEC, RAG>(x + row * d + e, d - e);
+        o.g[i] = load_pack<T, VEC, RAG>(dy + row * d + e, d - e);
       }
     }
     o.mu = mean[row];
@@ -201,7 +218,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + slot;
   Row now, next;
-  constexpr bool AHEAD = VEC > 1 && NV <= 2;      // where registers allow it
+  constexpr bool AHEAD = NV <= 2;                 // where registers allow it
   if (AHEAD && row < rows) load(row, now);
   for (; row < rows; row += step) {
     if (!AHEAD) load(row, now);
@@ -239,7 +256,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
         }
         Pack<T, VEC> p;
         narrow(o, p);
-        store_pack<T, VEC>(dx + row * d + e, p);
+        store_pack<T, VEC, RAG>(dx + row * d + e, p, d - e);
       }
     }
     if (AHEAD) now = next;
@@ -262,11 +279,12 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_norm_grad(
           for (int j = 0; j < VEC; ++j) {
             float a = 0.f;
             for (int k = 0; k < RPB; ++k) a += cols[(k * VEC + j) * TPR + t];
-            pw[(int64_t)q * d + e + j] = a;
+            if (!RAG || e + j < d) pw[(int64_t)q * d + e + j] = a;
           }
       } else if (e < d) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) pw[(int64_t)q * d + e + j] = mine[j];
+        for (int j = 0; j < VEC; ++j)
+          if (!RAG || e + j < d) pw[(int64_t)q * d + e + j] = mine[j];
       }
     }
   }
@@ -299,31 +317,31 @@ __global__ __launch_bounds__(1024) void k_norm_grad_sum(const float* __restrict_
 
 // The variant for rows of d elements.
 struct NormPlan {
-  bool vec;
+  bool rag;
   int tpr, threads, nv;           // threads: of a workgroup; tpr 0: all of them share a row
 };
-// A wave has rows of up to 64 `most` vectors (twice as many single elements):
-// forward 8, backward 2.  Measured (bf16, us; a wave a row / a workgroup a
-// row): forward 131072 x 2560 296 / 411, 32768 x 1024 fp32 46 / 57; backward
-// 131072 x 2560 545 / 396, 16384 x 4096 153 / 103.  The forward pass has
-// nothing to wait for but its loads, which a wave's own registers keep under
-// way; the backward's three rows of registers leave too few waves for that.
+// A wave has rows of up to 64 `most` vectors: forward 8, backward 2.  Measured
+// (bf16, us; a wave a row / a workgroup a row): forward 131072 x 2560 296 /
+// 411, 32768 x 1024 fp32 46 / 57; backward 131072 x 2560 545 / 396, 16384 x
+// 4096 153 / 103.  The forward pass has nothing to wait for but its loads, which
+// a wave's own registers keep under way; the backward's three rows of registers
+// leave too few waves for that.
 template <typename T>
 NormPlan norm_plan(int d, int most) {
   constexpr int V = Vec<T>::V;
   NormPlan p;
-  p.vec = d % V == 0;
-  const int units = p.vec ? d / V : d, few = p.vec ? 1 : 4;
+  p.rag = d % V != 0;
+  const int units = (d + V - 1) / V;
   p.threads = kNormThreads;
   p.nv = 1;
   if (units <= 16) {
     p.tpr = 16;
-  } else if (units <= 64 * most * (p.vec ? 1 : 2)) {
+  } else if (units <= 64 * most) {
     p.tpr = 64;
     p.nv = (units + 63) / 64;
   } else {
     p.tpr = 0;
-    p.nv = std::max(few, (units + 1023) / 1024);
+    p.nv = (units + 1023) / 1024;
     p.threads = (units + 64 * p.nv - 1) / (64 * p.nv) * 64;
   }
   return p;
@@ -333,33 +351,33 @@ NormPlan norm_plan(int d, int most) {
 template <typename T, typename F>
 hipError_t with_plan(const NormPlan& p, F f) {
   using std::integral_constant;
-  auto go = [&](auto vec, auto nv) {
-    if (p.tpr == 0) return f(vec, integral_constant<int, 0>(), nv);
-    if constexpr (decltype(nv)::value <= (decltype(vec)::value > 1 ? 8 : 16)) {
-      if (p.tpr == 64) return f(vec, integral_constant<int, 64>(), nv);
+  auto with_tpr = [&](auto rag, auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    if (p.tpr == 0) return f(rag, integral_constant<int, 0>(), nv);
+    if constexpr (NV <= 8) {
+      if (p.tpr == 64) return f(rag, integral_constant<int, 64>(), nv);
     }
-    if constexpr (decltype(nv)::value <= 4) {
-      if (p.tpr == 16) return f(vec, integral_constant<int, 16>(), nv);
+    if constexpr (NV == 1) {
+      if (p.tpr == 16) return f(rag, integral_constant<int, 16>(), nv);
     }
     return hipErrorInvalidValue;
   };
-  if (p.vec) {
-    const integral_constant<int, Vec<T>::V> vec;
-    if (p.nv <= 1) return go(vec, integral_constant<int, 1>());
-    if (p.nv <= 2) return go(vec, integral_constant<int, 2>());
-    if (p.nv <= 3) return go(vec, integral_constant<int, 3>());
-    if (p.nv <= 4) return go(vec, integral_constant<int, 4>());
-    if (p.nv <= 5) return go(vec, integral_constant<int, 5>());
-    if (p.nv <= 6) return go(vec, integral_constant<int, 6>());
-    if (p.nv <= 8 || sizeof(T) == 2) return go(vec, integral_constant<int, 8>());
-    if constexpr (sizeof(T) == 4) return go(vec, integral_constant<int, 16>());
-    return hipErrorInvalidValue;
-  }
-  const integral_constant<int, 1> one;
-  if (p.nv <= 4) return go(one, integral_constant<int, 4>());
-  if (p.nv <= 8) return go(one, integral_constant<int, 8>());
-  if (p.nv <= 16) return go(one, integral_constant<int, 16>());
-  return go(one, integral_constant<int, 64>());
+  auto go = [&](auto rag) {
+    switch (p.nv) {
+      case 1: return with_tpr(rag, integral_constant<int, 1>());
+      case 2: return with_tpr(rag, integral_constant<int, 2>());
+      case 3: return with_tpr(rag, integral_constant<int, 3>());
+      case 4: return with_tpr(rag, integral_constant<int, 4>());
+      case 5: return with_tpr(rag, integral_constant<int, 5>());
+      case 6: return with_tpr(rag, integral_constant<int, 6>());
+      case 7:
+      case 8: return with_tpr(rag, integral_constant<int, 8>());
+      default:                    // fp32 rows of more than 32768
+        if constexpr (sizeof(T) == 4) return with_tpr(rag, integral_constant<int, 16>());
+        return hipErrorInvalidValue;
+    }
+  };
+  return p.rag ? go(std::true_type()) : go(std::false_type());
 }
 
 }  // namespace
@@ -370,8 +388,8 @@ hipError_t launch_norm(const T* x, const T* w, const T* b, T* y, float* mean, fl
   const NormPlan p = norm_plan<T>(d, 8);
   const int rpb = p.tpr ? p.threads / p.tpr : 1;
   const int64_t grid = std::min<int64_t>((rows + rpb - 1) / rpb, 1 << 21);
-  return with_plan<T>(p, [&](auto vec, auto tpr, auto nv) {
-    k_norm<T, decltype(vec)::value, decltype(tpr)::value, decltype(nv)::value>
+  return with_plan<T>(p, [&](auto rag, auto tpr, auto nv) {
+    k_norm<T, decltype(rag)::value, decltype(tpr)::value, decltype(nv)::value>
         <<<dim3((unsigned)grid), p.threads, 0, s>>>(x, w, b, y, mean, rstd, rows, d, eps);
     return hipGetLastError();
   });
@@ -393,8 +411,8 @@ hipError_t launch_norm_grad(const T* x, const T* w, const T* dy, const float* me
   const NormPlan p = norm_plan<T>(d, 2);
   const int G = norm_grad_blocks<T>(rows, d);
   if (G > 0) {
-    hipError_t e = with_plan<T>(p, [&](auto vec, auto tpr, auto nv) {
-      k_norm_grad<T, decltype(vec)::value, decltype(tpr)::value, decltype(nv)::value>
+    hipError_t e = with_plan<T>(p, [&](auto rag, auto tpr, auto nv) {
+      k_norm_grad<T, decltype(rag)::value, decltype(tpr)::value, decltype(nv)::value>
           <<<dim3((unsigned)G), p.threads, 0, s>>>(x, w, dy, mean, rstd, dx, part, rows, d, db != nullptr);
       return hipGetLastError();
     });
