@@ -9,7 +9,7 @@
 // the registers, so a large common offset costs no digits), and written once.
 // TPR threads share a row, each holding NV vectors of VEC elements; vector i
 // of thread t starts at element (i TPR + t) VEC, so a wave's loads are
-// contiguous.  Rows of up to 128 vectors belong to one wave or a quarter of
+// contiguous.  Narrower rows (norm_plan) belong to one wave or a quarter of
 // one: no barrier, and a workgroup works on 4 rows or more.  Wider rows have a
 // workgroup of as many waves as they fill (TPR = 0: its size, up to 1024), one
 // vector a thread while that reaches.  VEC = 16 bytes.  RAG: row lengths that
