@@ -40,7 +40,7 @@ int check_delta(const ttt_delta_shape* s, int dtype, int64_t num_seqs) {
   if (packed && s->batch != 1) return TTT_ERR_SHAPE;
   const int64_t lim = (int64_t)1 << 30, seqs = packed ? num_seqs : s->batch;
   if (s->seq_len > lim || seqs > lim || (!packed && s->batch * s->seq_len > lim)) return TTT_ERR_UNSUPPORTED;
-  const int64_t slots = packed ? s->seq_len / 64 + num_seqs : s->batch * ((s->seq_len + 63) / 64);
+  const int64_t slots = packed ? (num_seqs > 0 ? s->seq_len / 64 + num_seqs : 0) : s->batch * ((s->seq_len + 63) / 64);
   // a walk's grid: key heads in eights, and twice that in the backward pass
   if (slots * s->v_heads > kMaxBlocks || 2 * (seqs + 8) * s->v_heads * ((s->v_dim + 15) / 16) > kMaxBlocks)
     return TTT_ERR_UNSUPPORTED;

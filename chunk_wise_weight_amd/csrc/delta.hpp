@@ -316,11 +316,14 @@ __device__ __forceinline__ bool walk_place(int bid, int sequences, int Hk, int g
 // Packed rows: sequence i's chunks take the slots from starts[i] / 64 + i on.
 // That leaves every sequence room for its chunks (a sequence touches at most
 // one more 64-token cell than it has full chunks) and needs no prefix sum: the
-// slots number n / 64 + num.  Starts are brought into 0..n and an end before
-// its start counts as the start, so no value of theirs leads out of the rows.
+// slots number n / 64 + num, and none where there is no sequence (the single
+// start has no end behind it to read).  Starts are brought into 0..n and an end
+// before its start counts as the start, so no value of theirs leads out of the
+// rows.
 __device__ __forceinline__ int seq_start(const DeltaSeqs& q, int i) { return min(max(q.starts[i], 0), q.n); }
 inline __host__ __device__ int64_t delta_slots(const DeltaSeqs& q, int batch) {
-  return q.starts ? (int64_t)q.n / kDC + q.num : (int64_t)batch * ((q.n + kDC - 1) / kDC);
+  if (q.starts) return q.num > 0 ? (int64_t)q.n / kDC + q.num : 0;
+  return (int64_t)batch * ((q.n + kDC - 1) / kDC);
 }
 
 // Where sequence s lies: batch row, first token, tokens, first chunk slot.

@@ -728,7 +728,8 @@ typedef struct {
    * num_seqs + 1 int32, DEVICE, not decreasing; sequence i holds tokens
    * seq_starts[i] .. seq_starts[i+1] - 1, possibly none.  Tokens before the
    * first start and from the last one on belong to no sequence: they are not
-   * read, and their output rows are left as they are.  Values outside 0 ..
+   * read, and their output rows are left as they are (with num_seqs == 0:
+   * every token; no workspace is needed then).  Values outside 0 ..
    * seq_len are taken as the nearer of the two, and an end before its start
    * as the start; with starts that decrease the outputs are undefined. */
   const int32_t* seq_starts;
