@@ -15,9 +15,13 @@
 //   dQ = scale exp(b) dO S^T + Mq K
 //   dK = Mq^T Q + (Mk + Mk^T) K - exp(b) X S^T + exp(b_63 - b) beta E dS'^T
 //   dbeta_j = (sum_i Mq_ij q_i.k_j + Mk_ij k_i.k_j) / beta_j + exp(b_63 - b_j) k_j.(dS'^T E_j)
-//   db_i = q_i.dQ_i - k_i.dK_i in its parts, + exp(b_63) <S, dS'> and the
-//          tokens' parts through exp(b_63) at the chunk's end; dg = suffix sums of db
+//   dg_t = sum_{j < t <= i} N_ij + sum_{i >= t} exp(b_i) (scale q_i.(S dO_i) - k_i.(S X_i))
+//          + sum_{j < t} exp(b_63 - b_j) beta_j k_j.(dS'^T E_j) + exp(b_63) <S, dS'>,
+//   N_ij = Mq_ij q_i.k_j + Mk_ij k_i.k_j   (j < i)
 // (the division is by a factor of the summands, which are taken without it).
+// Every term of dg_t has exp(g_t) in its decay: the sums are made so that no
+// other terms come in that would have to cancel, and a strong decay's small
+// gradient keeps its digits.
 // Gradients of a key head sum over its value heads, one after the other in one
 // workgroup: no atomics.
 //
@@ -273,7 +277,7 @@ template <typename T, int DK> struct Grads {
   static constexpr int kBlock = kD + Panels<T>::bytes(BV), kQK = 2 * Panels<T>::bytes(DK);
   // Where LDS has room Q and K have a place of their own, and where it has more, a block comes while the one before
   // is worked on; the widest fp32 heads load Q and K in the place of S and dS' after a head's last block.
-  static constexpr int kLds = 160 * 1024 - 4608;             // but for the arrays of single values
+  static constexpr int kLds = 160 * 1024 - 6144;             // but for the arrays of single values
   static constexpr bool kOwnQ = kBlock + kQK <= kLds, kTwo = 2 * kBlock + kQK <= kLds;
   static constexpr int kQ = kOwnQ ? (kTwo ? 2 : 1) * kBlock : 0, kK = kQ + kQK / 2;
   static constexpr int kSmem = kOwnQ ? kQ + kQK : (kBlock > kQK + kBlock - kE ? kBlock : kQK + kBlock - kE);
@@ -282,6 +286,16 @@ template <typename T, int DK> struct Grads {
   static constexpr int kM = kE + kShift, kMBytes = Panels<T>::bytes(kDC);
   static constexpr bool kBoth = kBlock - kE >= 2 * kMBytes;
 };
+
+// x of the lane groups in front of group g (lanes of equal lane & 15), summed.
+__device__ __forceinline__ float groups_before(float x, int g) {
+  float up = __shfl_up(x, 16, 64);
+  if (g >= 1) x += up;
+  up = __shfl_up(x, 32, 64);
+  if (g >= 2) x += up;
+  up = __shfl_up(x, 16, 64);
+  return g >= 1 ? up : 0.f;
+}
 
 template <typename T, int DK>
 __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
@@ -292,7 +306,7 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
   constexpr int VS = G::BV / M::KB;                          // steps over a dv block: 2
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ double b[kDC];
-  __shared__ float beta[kDC], colsum[4][kDC], half[2][4][kDC], part[8];
+  __shared__ float beta[kDC], colsum[2][4][kDC], half[2][4][kDC], part[8];   // colsum: of N_ij / beta_j; dg's
   const DeltaArgs& p = a.f;
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   const int kh = id % p.Hk, slot = id / p.Hk, group = p.Hv / p.Hk;
@@ -429,10 +443,11 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
     }
     const double bi = b[i], last = b[kDC - 1];
     f32x4 mq[2], mk[2];
-    float rows = 0.f;                                        // sum_j N_ij, N_ij = Mq_ij q_i.k_j + Mk_ij k_i.k_j
-    float cols[2][4];                                        // sum over this wave's i of N_ij / beta_j
+    float sums[16];                                          // [t, r]: N_ij / beta_j (j <= i), then dg's part of row i
+    float N[2][4], total[2];                                 // N_ij, j < i, and its sums over r
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t) {
+      total[t] = 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = M::row(j0 + t, g * 4 + r);
@@ -441,9 +456,30 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
         mq[t][r] = uq * bj;
         mk[t][r] = uk * bj;
         const float n = uq * qk[t][r] + uk * kk[t][r];
-        rows += n * bj;
-        cols[t][r] = n;
+        sums[t * 4 + r] = n;
+        N[t][r] = j < i ? n * bj : 0.f;
+        total[t] += N[t][r];
       }
+    }
+    // Row i's part of dg_j: the sum of N_ij' over this half's j' < j, where j <= i.
+    const float rows = total[0] + total[1];
+    {
+      float before[2];
+      if constexpr (M::TPS == 2) {                           // a lane's j: g * 8 + 0..7
+        before[0] = groups_before(rows, g);
+        before[1] = before[0] + total[0];
+      } else {                                               // t * 16 + g * 4 + 0..3
+        before[0] = groups_before(total[0], g);
+        before[1] = groups_before(total[1], g) + __shfl(before[0] + total[0], 48 + m, 64);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sums[8 + t * 4 + r] = M::row(j0 + t, g * 4 + r) <= i ? before[t] : 0.f;
+          before[t] += N[t][r];
+        }
+    }
     auto put_m = [&](const f32x4 (&x)[2], int to) __attribute__((always_inline)) {   // rows of tokens i, columns j
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -452,15 +488,15 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
     };
     put_m(mq, m0);
     if (G::kBoth) put_m(mk, m0 + G::kMBytes);
+    // Summed over this wave's 16 tokens: each step halves the sums that a lane holds, and lane m ends with the m-th.
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int d = 8; d > 0; d >>= 1)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float s = cols[t][r];
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) s += __shfl_xor(s, d, 64);
-        if (m == 0) colsum[w][M::row(j0 + t, g * 4 + r)] = s;
+      for (int x = 0; x < d; ++x) {
+        const float other = __shfl_xor((m & d) ? sums[x] : sums[x + d], d, 64);
+        sums[x] = ((m & d) ? sums[x + d] : sums[x]) + other;
       }
+    colsum[m >> 3][w][M::row(j0 + ((m >> 2) & 1), g * 4 + (m & 3))] = sums[0];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d, 64);
     if (lane == 0) part[wave] = ss;
@@ -493,23 +529,29 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
     }
     __syncthreads();                                         // Mq, Mk, the sums
     if (wave == 0) {                                         // lane: token
-      const float row_sum = half[0][0][lane] + half[1][0][lane], qos = half[0][1][lane] + half[1][1][lane];
+      const float qos = half[0][1][lane] + half[1][1][lane];
       const float kxs = half[0][2][lane] + half[1][2][lane], kes = half[0][3][lane] + half[1][3][lane];
-      const float n = colsum[0][lane] + colsum[1][lane] + colsum[2][lane] + colsum[3][lane];
-      const float up = __expf((float)b[lane]), left = __expf((float)(last - b[lane])), end = left * beta[lane] * kes;
-      float s = p.scale * up * qos - up * kxs + row_sum - beta[lane] * n - end, all = end;   // db, and its part at 63
+      const float n = colsum[0][0][lane] + colsum[0][1][lane] + colsum[0][2][lane] + colsum[0][3][lane];
+      const float up = __expf((float)b[lane]), left = __expf((float)(last - b[lane]));
+      float after = p.scale * up * qos - up * kxs;           // summed over the tokens from this one on
+      float low = half[0][0][lane];                          // N_ij over the first half's j: of the second half's dg
+      float end = left * beta[lane] * kes;                   // summed over the tokens before this one
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
-      all += __expf((float)last) * (part[0] + part[1] + part[2] + part[3] + part[4] + part[5] + part[6] + part[7]);
-      if (lane == 63) s += all;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {                     // suffix sums
-        const float down = __shfl_down(s, d, 64);
-        if (lane + d < 64) s += down;
+      for (int d = 1; d < 64; d <<= 1) {
+        const float x = __shfl_down(after, d, 64), y = __shfl_down(low, d, 64), z = __shfl_up(end, d, 64);
+        if (lane + d < 64) {
+          after += x;
+          low += y;
+        }
+        if (lane >= d) end += z;
       }
+      end = __shfl_up(end, 1, 64);
+      const float all = part[0] + part[1] + part[2] + part[3] + part[4] + part[5] + part[6] + part[7];
+      const float dg = after + (lane > 0 ? end : 0.f) + (lane >= 32 ? low : 0.f) + __expf((float)last) * all +
+                       (colsum[1][0][lane] + colsum[1][1][lane] + colsum[1][2][lane] + colsum[1][3][lane]);
       if (lane < c.len) {
         const int64_t t = c.tok0 + lane;
-        ((T*)a.dg)[c.b * a.sdg.b + h * a.sdg.h + t * a.sdg.t] = from_f32<T>(s);
+        ((T*)a.dg)[c.b * a.sdg.b + h * a.sdg.h + t * a.sdg.t] = from_f32<T>(dg);
         ((T*)a.dbeta)[c.b * a.sdbeta.b + h * a.sdbeta.h + t * a.sdbeta.t] = from_f32<T>(n + left * kes);
       }
     }
@@ -586,7 +628,7 @@ hipError_t launch_sizes(const DeltaGradArgs& a, int64_t slots, int sequences, hi
   constexpr int SF = Walk<T, DK, NW, 2, kKeep, false>::kSmem <= kMax ? 2 : 1;
   constexpr int SB = WalkBack<T, DK, NW, 2>::kSmem <= kMax ? 2 : 1;
   constexpr int F = Walk<T, DK, NW, SF, kKeep, false>::kSmem, B = WalkBack<T, DK, NW, SB>::kSmem, W = F > B ? F : B;
-  static_assert(W <= kMax && Grads<T, DK>::kSmem <= kMax - 4608, "LDS of a CU");
+  static_assert(W <= kMax && Grads<T, DK>::kSmem <= Grads<T, DK>::kLds, "LDS of a CU");
   auto walks = k_delta_walks<T, DK, NW, SF, SB>;
   auto grads = k_delta_grads<T, DK>;
   if (sequences > 0) {

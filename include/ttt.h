@@ -774,7 +774,7 @@ int ttt_gated_delta_backward_workspace_bytes(const ttt_delta_shape* shape, int d
  * options' layout gives the inputs' strides (its O is not used), grad_layout
  * (NULL: contiguous) those of dO and the gradients.  Rows of tokens that
  * belong to no sequence are left as they are.  At a reset (g below -200) dg
- * is that of a decay of zero, up to rounding.  No atomics: the same bits at
+ * is zero.  No atomics: the same bits at
  * every call. */
 int ttt_gated_delta_backward(const ttt_delta_shape* shape, int dtype, float scale, const void* q, const void* k,
                              const void* v, const float* g, const float* beta, const void* dO, const float* dW_final,

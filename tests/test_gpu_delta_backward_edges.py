@@ -1,10 +1,12 @@
 """The gated delta rule's backward at the edges of what it takes.  Tolerances are those of test_gpu_delta_backward."""
+import numpy as np
 import pytest
 import torch
 
 import chunk_wise_weight_amd as cw
-from test_gpu_delta import make
-from test_gpu_delta_backward import B16, F32, NAMES
+from oracle import delta as od
+from test_gpu_delta import f64, make
+from test_gpu_delta_backward import B16, F32, NAMES, TOL, extras
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +22,42 @@ def test_no_sequences(dtype, n):
     got = cw.ttt_gated_delta_backward(*args, torch.ones_like(args[2]), seq_starts=starts, **outs)
     torch.cuda.synchronize()
     assert all((t == 7).all() for t in got[:5]) and got[5] is None
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+def test_small_gradients_of_strong_decays(dtype):
+    """dg_t is of the size of exp(g_t): it keeps its digits, head by head, under decays that are strong throughout (-8,
+    -12, -16) and, token by token, under single ones of -14 among weak ones, inside a chunk and at its ends, where the
+    neighbours' gradients are larger by a factor of 10^6.  (exp's own error at -16 is 2 * 16 * 2^-24, 2e-6.)"""
+    Hv, n = 4, 200
+    args = make(1, 2, Hv, n, 32, 40, dtype, "head", seed=11)
+    dO, W0, dWn = extras(1, Hv, n, 32, 40, dtype, "head")
+    g = args[3]
+    for h, x in enumerate((-8.0, -12.0, -16.0)):
+        g[:, h] = x
+    g[:, 3] = -0.02
+    strong = [5, 31, 32, 40, 63, 64, 100, 127, 128, 150, 191, 192, 199]
+    g[:, 3, strong] = -14.0
+    got = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0)
+    ref = od.delta_rule_backward(*(f64(t[0]) for t in args), 32 ** -0.5, f64(dO[0]), f64(W0[0]), f64(dWn[0]))
+    dg, want = f64(got[3][0]), ref[3]
+    weak = [t for t in range(n) if t not in strong]
+    parts = [(0, slice(None)), (1, slice(None)), (2, slice(None)), (3, strong), (3, weak)]
+    errs = [np.linalg.norm(dg[h, at] - want[h, at]) / np.linalg.norm(want[h, at]) for h, at in parts]
+    print(dtype, errs, flush=True)
+    assert max(errs) <= TOL[dtype]["dg"], errs
+    for name, a, b in zip(NAMES, got, ref):
+        for h in range(Hv if b.shape[0] == Hv else 0):
+            e = np.linalg.norm(f64(a[0, h]) - b[h]) / np.linalg.norm(b[h])
+            assert e <= TOL[dtype][name], (name, h, e)
+
+
+def test_gradient_of_a_reset_is_zero():
+    """A decay of zero (g = -inf): nothing passes it, and dg there is zero itself, not what a cancelled sum leaves."""
+    for dtype in (F32, B16):
+        args = make(1, 1, 2, 150, 64, 64, dtype, "head", seed=9)
+        at = [0, 17, 64, 127, 149]
+        args[3][:, :, at] = float("-inf")
+        dO, W0, dWn = extras(1, 2, 150, 64, 64, dtype, "head")
+        dg = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0)[3]
+        assert not dg[:, :, at].any() and not dg.isnan().any()
