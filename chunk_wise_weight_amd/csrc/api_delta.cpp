@@ -62,6 +62,24 @@ bool take_strides(const ttt_delta_strides* in, int64_t H, int64_t n, int64_t d, 
   return true;
 }
 
+// The same of a tensor that is written: no two of its elements may lie at one place.
+bool take_out_strides(const ttt_delta_strides* in, int64_t B, int64_t H, int64_t n, int64_t d, int64_t unit,
+                      ttt::DeltaStrides* out) {
+  if (!take_strides(in, H, n, d, unit, out)) return false;
+  if (in == nullptr || B == 0 || n == 0) return true;
+  struct {
+    int64_t stride, count;
+  } at[3] = {{out->b, B}, {out->h, H}, {out->t, n}};
+  std::sort(at, at + 3, [](const auto& x, const auto& y) { return x.stride < y.stride; });
+  int64_t reach = d;                  // elements that lie within one stride of the next index
+  for (const auto& x : at) {
+    if (x.count == 1) continue;
+    if (x.stride < reach || x.stride > INT64_MAX / x.count) return false;
+    reach = x.stride * x.count;
+  }
+  return true;
+}
+
 ttt::DeltaArgs sizes(const ttt_delta_shape* s, int64_t num_seqs) {
   ttt::DeltaArgs a{};
   a.batch = (int)s->batch;
@@ -139,8 +157,8 @@ int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const 
   ttt::DeltaArgs a;
   if (int st = take_inputs(shape, dtype, scale, q, k, v, g, beta, options, &a)) return st;
   const int64_t num = a.seqs.starts ? a.seqs.num : -1;
-  if (!take_strides(options && options->layout ? &options->layout->O : nullptr, shape->v_heads, shape->seq_len,
-                    shape->v_dim, 16 / esize(dtype), &a.so))
+  if (!take_out_strides(options && options->layout ? &options->layout->O : nullptr, shape->batch, shape->v_heads,
+                        shape->seq_len, shape->v_dim, 16 / esize(dtype), &a.so))
     return TTT_ERR_ARG;
   if (sequences(shape, num) > 0 && !ok_ptr(W_final)) return TTT_ERR_ARG;
   if (shape->batch * shape->seq_len > 0 && !ok_ptr(O)) return TTT_ERR_ARG;
@@ -171,15 +189,15 @@ int ttt_gated_delta_backward(const ttt_delta_shape* shape, int dtype, float scal
   if (int st = take_inputs(shape, dtype, scale, q, k, v, g, beta, options, &a.f)) return st;
   const int64_t num = a.f.seqs.starts ? a.f.seqs.num : -1;
   const ttt_delta_grad_layout* l = grad_layout;
-  const int64_t n = shape->seq_len, u = 16 / esize(dtype), Hk = shape->k_heads, Hv = shape->v_heads;
+  const int64_t B = shape->batch, n = shape->seq_len, u = 16 / esize(dtype), Hk = shape->k_heads, Hv = shape->v_heads;
   if (!take_strides(l ? &l->dO : nullptr, Hv, n, shape->v_dim, u, &a.sdo) ||
-      !take_strides(l ? &l->dq : nullptr, Hk, n, shape->k_dim, u, &a.sdq) ||
-      !take_strides(l ? &l->dk : nullptr, Hk, n, shape->k_dim, u, &a.sdk) ||
-      !take_strides(l ? &l->dv : nullptr, Hv, n, shape->v_dim, u, &a.sdv) ||
-      !take_strides(l ? &l->dg : nullptr, Hv, n, 1, 1, &a.sdg) ||
-      !take_strides(l ? &l->dbeta : nullptr, Hv, n, 1, 1, &a.sdbeta))
+      !take_out_strides(l ? &l->dq : nullptr, B, Hk, n, shape->k_dim, u, &a.sdq) ||
+      !take_out_strides(l ? &l->dk : nullptr, B, Hk, n, shape->k_dim, u, &a.sdk) ||
+      !take_out_strides(l ? &l->dv : nullptr, B, Hv, n, shape->v_dim, u, &a.sdv) ||
+      !take_out_strides(l ? &l->dg : nullptr, B, Hv, n, 1, 1, &a.sdg) ||
+      !take_out_strides(l ? &l->dbeta : nullptr, B, Hv, n, 1, 1, &a.sdbeta))
     return TTT_ERR_ARG;
-  if (shape->batch * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, esize(dtype)) ||
+  if (B * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, esize(dtype)) ||
                                !ok_ptr(dbeta, esize(dtype))))
     return TTT_ERR_ARG;
   if (!aligned(dW_final, 16) || !aligned(dW_init, 16)) return TTT_ERR_ARG;

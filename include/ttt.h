@@ -710,7 +710,9 @@ typedef struct {
 /* Strides, in elements, of a [B, H, n, d] tensor whose last index is
  * contiguous (gates: of a [B, H, n] tensor).  Nonnegative; token strides at
  * most 2^22; for all but the gates multiples of 16 bytes.  Zero strides
- * repeat a row, in inputs only.  (Else TTT_ERR_ARG.) */
+ * repeat a row, in inputs only: a written tensor's strides, each over an index
+ * of more than one value, put no two elements at one place (sorted, each
+ * reaches past all that the smaller ones span).  (Else TTT_ERR_ARG.) */
 typedef struct {
   int64_t batch, head, token;
 } ttt_delta_strides;

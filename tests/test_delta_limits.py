@@ -1,9 +1,11 @@
 """Host-side checks of the gated delta rule's C entry points at their limits, without a GPU: what takes no workspace,
 what is refused before any device work.  Pointers are never followed: any aligned address serves."""
+import ctypes
+
 import pytest
 
 import chunk_wise_weight_amd as cw
-from test_delta_host import shape, size
+from test_delta_host import ARG, backward, forward, shape, size
 
 WORKSPACES = ("ttt_gated_delta_workspace_bytes", "ttt_gated_delta_backward_workspace_bytes")
 
@@ -16,3 +18,35 @@ def test_no_sequences_have_no_chunks(what, dtype):
     for n in (0, 10, 64, 256, 1 << 20):
         assert size(shape(n=n), dtype, 0, what) == (0, 0)
     assert size(shape(n=256), dtype, 1, what)[1] > 0
+
+
+# Strides (batch, head, token) of a tensor [2, 2, 100, 64], and whether a written one may have them
+LAYOUTS = [((12800, 6400, 64), True), ((12800, 64, 128), True), ((6400, 12800, 64), True), ((20000, 64, 160), True),
+           ((64, 128, 256), True), ((12800, 6400, 0), False), ((12800, 0, 64), False), ((0, 6400, 64), False),
+           ((12800, 6400, 56), False), ((12800, 32, 128), False), ((6400, 6400, 64), False), ((6400, 6336, 64), False),
+           ((1 << 62, 6400, 64), False)]
+
+
+@pytest.mark.parametrize("strides,apart", LAYOUTS)
+def test_written_tensors_do_not_overlap_themselves(strides, apart):
+    """Zero strides, and others that put two elements at one place, are for inputs only.  A call that passes the strides'
+    check ends at the missing workspace, with another status than a refused one."""
+    s, z, ok = shape(B=2), cw.DeltaStrides, (12800, 6400, 64)
+    gate = (200, 100, 1)
+    lay = cw.DeltaLayout(*(z(*ok) for _ in range(3)), z(*gate), z(*gate), z(*strides))
+    opts = cw.DeltaOptions(None, None, 0, ctypes.pointer(lay))
+    assert forward(s, opts=opts, ws=None) == (cw.TTT_ERR_WORKSPACE if apart else ARG)
+    for at in (1, 2, 3):                                                   # dq, dk [2, 1, 100, 64], dv
+        rows = [z(*ok) for _ in range(4)]
+        rows[at] = z(*strides)
+        fine = apart or at < 3 and strides in ((12800, 0, 64), (12800, 32, 128), (6400, 6336, 64), (6400, 6400, 64))
+        got = backward(s, grads=cw.DeltaGradLayout(*rows, z(*gate), z(*gate)), ws=None)
+        assert got == (cw.TTT_ERR_WORKSPACE if fine else ARG), (at, strides)
+    for bad in ((200, 100, 0), (200, 0, 1), (0, 100, 1), (100, 100, 1)):
+        for i in (0, 1):
+            gates = [z(*gate), z(*gate)]
+            gates[i] = z(*bad)
+            assert backward(s, grads=cw.DeltaGradLayout(*(z(*ok) for _ in range(4)), *gates), ws=None) == ARG
+    # inputs may repeat rows
+    lay = cw.DeltaLayout(*(z(0, 0, 0) for _ in range(5)), z(*ok))
+    assert forward(s, opts=cw.DeltaOptions(None, None, 0, ctypes.pointer(lay)), ws=None) == cw.TTT_ERR_WORKSPACE
