@@ -20,8 +20,9 @@ inline int dev(hipError_t e) { return e == hipSuccess ? TTT_OK : TTT_ERR_DEVICE;
 inline bool ok_dtype(int t) { return t == TTT_F32 || t == TTT_BF16; }
 inline int64_t esize(int t) { return t == TTT_BF16 ? 2 : 4; }
 
-// A grid has fewer than 2^32 threads; the kernels' workgroups have up to 256.
-constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
+// A grid has fewer than 2^32 threads.  kMaxBlocks holds workgroups of 256 (chunk and step kernels) to that; a
+// forward walk's, of up to 384, are at most half as many.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1, kMaxBlocks = kMaxThreads / 256;
 constexpr int64_t kMaxDim = 256, kMaxVDim = 4096, kMaxTokenStride = (int64_t)1 << 22;
 
 int check_heads(int64_t Hk, int64_t Hv, int64_t dk, int64_t dv) {
@@ -30,7 +31,12 @@ int check_heads(int64_t Hk, int64_t Hv, int64_t dk, int64_t dv) {
   return TTT_OK;
 }
 
-// num_seqs < 0: one sequence a batch row.
+// Chunk slots; num_seqs < 0: one sequence a batch row.
+int64_t slots_of(const ttt_delta_shape* s, int64_t num_seqs) {
+  if (num_seqs >= 0) return num_seqs > 0 ? s->seq_len / 64 + num_seqs : 0;
+  return s->batch * ((s->seq_len + 63) / 64);
+}
+
 int check_delta(const ttt_delta_shape* s, int dtype, int64_t num_seqs) {
   if (s == nullptr) return TTT_ERR_ARG;
   if (!ok_dtype(dtype)) return TTT_ERR_DTYPE;
@@ -40,14 +46,24 @@ int check_delta(const ttt_delta_shape* s, int dtype, int64_t num_seqs) {
   if (packed && s->batch != 1) return TTT_ERR_SHAPE;
   const int64_t lim = (int64_t)1 << 30, seqs = packed ? num_seqs : s->batch;
   if (s->seq_len > lim || seqs > lim || (!packed && s->batch * s->seq_len > lim)) return TTT_ERR_UNSUPPORTED;
-  const int64_t slots = packed ? (num_seqs > 0 ? s->seq_len / 64 + num_seqs : 0) : s->batch * ((s->seq_len + 63) / 64);
-  // a walk's grid: key heads in eights, and twice that in the backward pass
+  const int64_t slots = slots_of(s, num_seqs);
+  // a walk's grid: key heads in eights (and twice that in the backward pass)
   if (slots * s->v_heads > kMaxBlocks || 2 * (seqs + 8) * s->v_heads * ((s->v_dim + 15) / 16) > kMaxBlocks)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 
 int64_t sequences(const ttt_delta_shape* s, int64_t num_seqs) { return num_seqs >= 0 ? num_seqs : s->batch; }
+
+// What the backward pass takes less of: its walks have 320 threads, half of the workgroups going back, and the
+// chunk-local kernel 512 a chunk slot and key head.
+int check_delta_backward(const ttt_delta_shape* s, int dtype, int64_t num_seqs) {
+  const int64_t columns = s->k_dim <= 128 || dtype == TTT_BF16 ? 64 : 32;
+  const int64_t per = s->v_heads / s->k_heads * ((s->v_dim + columns - 1) / columns);
+  const int64_t walks = 2 * ((sequences(s, num_seqs) * s->k_heads + 7) / 8 * 8) * per;
+  const int64_t chunks = slots_of(s, num_seqs) * s->k_heads;
+  return walks * 320 > kMaxThreads || chunks * 512 > kMaxThreads ? TTT_ERR_UNSUPPORTED : TTT_OK;
+}
 
 // Strides of a [B, H, n, d] tensor: given ones, or contiguous.  unit: elements of 16 bytes (1 for gates).
 bool take_strides(const ttt_delta_strides* in, int64_t H, int64_t n, int64_t d, int64_t unit, ttt::DeltaStrides* out) {
@@ -175,6 +191,7 @@ int ttt_gated_delta_backward_workspace_bytes(const ttt_delta_shape* shape, int d
                                              size_t* bytes) {
   if (bytes == nullptr) return TTT_ERR_ARG;
   if (int st = check_delta(shape, dtype, num_seqs)) return st;
+  if (int st = check_delta_backward(shape, dtype, num_seqs)) return st;
   const ttt::DeltaArgs a = sizes(shape, num_seqs);
   *bytes = dtype == TTT_BF16 ? ttt::delta_grad_workspace_bytes<bf16>(a) : ttt::delta_grad_workspace_bytes<float>(a);
   return TTT_OK;

@@ -762,7 +762,10 @@ typedef struct {
   ttt_delta_strides dO, dq, dk, dv, dg, dbeta;
 } ttt_delta_grad_layout;
 
-/* Workspace of ttt_gated_delta_backward; num_seqs < 0: not packed. */
+/* Workspace of ttt_gated_delta_backward; num_seqs < 0: not packed.  Chunks
+ * times key heads below 2^23, and 2 * sequences * v_heads * ceil(v_dim / 64)
+ * (fp32, k_dim > 128: ceil(v_dim / 32)) below 2^32 / 320, key heads counted in
+ * eights, else TTT_ERR_UNSUPPORTED. */
 int ttt_gated_delta_backward_workspace_bytes(const ttt_delta_shape* shape, int dtype, int64_t num_seqs,
                                              size_t* bytes);
 

@@ -50,3 +50,21 @@ def test_written_tensors_do_not_overlap_themselves(strides, apart):
     # inputs may repeat rows
     lay = cw.DeltaLayout(*(z(0, 0, 0) for _ in range(5)), z(*ok))
     assert forward(s, opts=cw.DeltaOptions(None, None, 0, ctypes.pointer(lay)), ws=None) == cw.TTT_ERR_WORKSPACE
+
+
+def test_the_backward_grids_stay_below_two_to_the_32_threads():
+    fwd, back = WORKSPACES
+    U = cw.TTT_ERR_UNSUPPORTED
+    # one workgroup of 512 a chunk and key head
+    long = shape(n=(1 << 30) - 64, Hv=1, dk=8, dv=8)
+    assert size(long, num=-1, what=fwd)[0] == cw.TTT_OK and size(long, num=-1, what=back)[0] == U
+    assert size(shape(n=(1 << 29) - 64, Hv=1, dk=8, dv=8), what=back)[0] == cw.TTT_OK
+    assert size(shape(n=(1 << 29), Hv=1, dk=8, dv=8), what=back)[0] == U
+    # one of 320 each way for a sequence and value head
+    many = shape(n=0, Hv=1, dk=8, dv=8)
+    assert size(many, num=8000000, what=fwd)[0] == cw.TTT_OK and size(many, num=8000000, what=back)[0] == U
+    assert size(many, num=6700000, what=back)[0] == cw.TTT_OK
+    # shared key heads: fewer chunk workgroups for the same walks
+    assert size(shape(n=(1 << 29) - 64, Hk=1, Hv=2, dk=8, dv=8), what=back)[0] == cw.TTT_OK
+    assert size(shape(n=(1 << 29) - 64, Hk=2, Hv=2, dk=8, dv=8), what=back)[0] == U
+    assert backward(long) == U and backward(many, opts=cw.DeltaOptions(None, 1 << 20, 8000000, None)) == U
