@@ -90,7 +90,7 @@ class DeltaLayout(ctypes.Structure):
 
 
 class DeltaGradLayout(ctypes.Structure):
-    _fields_ = [(n, DeltaStrides) for n in ("dO", "dq", "dk", "dv", "dg", "dbeta")]
+    _fields_ = [(n, DeltaStrides) for n in ("dO", "dq", "dk", "dv", "dg", "dbeta")] + [("gates_f32", ctypes.c_int)]
 
 
 class DeltaOptions(ctypes.Structure):
@@ -924,33 +924,37 @@ def ttt_gated_delta_backward_workspace_bytes(shape: DeltaShape, dtype: torch.dty
 
 
 @functools.lru_cache(maxsize=256)
-def _delta_backward_plan(q, k, v, g, beta, dO, dq, dk, dv, dg, dbeta, num):
+def _delta_backward_plan(q, k, v, g, beta, dO, dq, dk, dv, dg, dbeta, gate, num):
     shape, strides = _delta_strides(q, k, v, g, beta)
     qs, vs, gs, dt = tuple(q[0]), tuple(v[0]), tuple(g[0]), q[2]
     grads = DeltaGradLayout(_strides(dO, "dO", vs, dt), _strides(dq, "dq", qs, dt, out=True),
                             _strides(dk, "dk", qs, dt, out=True), _strides(dv, "dv", vs, dt, out=True),
-                            _strides(dg, "dg", gs, dt, rows=False, out=True),
-                            _strides(dbeta, "dbeta", gs, dt, rows=False, out=True))
+                            _strides(dg, "dg", gs, gate, rows=False, out=True),
+                            _strides(dbeta, "dbeta", gs, gate, rows=False, out=True), gate == torch.float32)
     return (ctypes.byref(shape), _dt(dt), DeltaLayout(*strides, DeltaStrides()), grads,
             ttt_gated_delta_backward_workspace_bytes(shape, dt, num),
             (shape.batch if num < 0 else num, shape.v_heads, shape.v_dim, shape.k_dim))
 
 
 def ttt_gated_delta_backward(q, k, v, g, beta, dO, dW_final=None, scale=None, W_init=None, seq_starts=None, dq=None,
-                             dk=None, dv=None, dg=None, dbeta=None, dW_init=None, workspace=None):
+                             dk=None, dv=None, dg=None, dbeta=None, dW_init=None, workspace=None, gate_dtype=None):
     """Backward of ttt_gated_delta from its inputs (the states are made again), dO = dLoss/dO [B, Hv, n, dv] and, where
     the loss depends on the final states too, dW_final [sequences, Hv, dv, dk] fp32.  Returns (dq, dk, dv, dg, dbeta)
     in q's dtype, each laid out like its input if not given, and dW_init [sequences, Hv, dv, dk] fp32 (None without
-    W_init, unless given).  dO and the gradients may have any strides that the inputs may; rows of tokens that belong
-    to no sequence are left as they are."""
+    W_init, unless given).  gate_dtype: the dtype of dg and dbeta, torch.float32 (as g and beta are; the sums as they
+    are made) or q's (None: rounded once).  dO and the gradients may have any strides that the inputs may; rows of tokens
+    that belong to no sequence are left as they are."""
     dev, t = q.device, q.dtype
+    gate = t if gate_dtype is None else gate_dtype
+    if gate not in (t, torch.float32):
+        raise TypeError(f"gate_dtype must be float32 or {t}, got {gate}")
     metas = _delta_metas(q, k, v, g, beta, dev)
     num = _seq_starts(seq_starts, q.shape[0], dev)
     dq, dk, dv = (torch.empty_like(x) if d is None else d for d, x in ((dq, q), (dk, k), (dv, v)))
-    dg, dbeta = (torch.empty_like(x, dtype=t) if d is None else d for d, x in ((dg, g), (dbeta, beta)))
+    dg, dbeta = (torch.empty_like(x, dtype=gate) if d is None else d for d, x in ((dg, g), (dbeta, beta)))
     shape, dt, layout, grads, nbytes, states = _delta_backward_plan(
         *metas, _meta(dO, "dO", dev), _meta(dq, "dq", dev), _meta(dk, "dk", dev), _meta(dv, "dv", dev),
-        _meta(dg, "dg", dev, False), _meta(dbeta, "dbeta", dev, False), num)
+        _meta(dg, "dg", dev, False), _meta(dbeta, "dbeta", dev, False), gate, num)
     if W_init is not None and dW_init is None:
         dW_init = torch.empty_like(W_init)
     for d, name in ((W_init, "W_init"), (dW_final, "dW_final"), (dW_init, "dW_init")):

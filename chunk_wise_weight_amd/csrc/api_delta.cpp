@@ -214,8 +214,9 @@ int ttt_gated_delta_backward(const ttt_delta_shape* shape, int dtype, float scal
       !take_out_strides(l ? &l->dg : nullptr, B, Hv, n, 1, 1, &a.sdg) ||
       !take_out_strides(l ? &l->dbeta : nullptr, B, Hv, n, 1, 1, &a.sdbeta))
     return TTT_ERR_ARG;
-  if (B * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, esize(dtype)) ||
-                               !ok_ptr(dbeta, esize(dtype))))
+  a.gates_f32 = l && l->gates_f32;
+  const size_t gate = a.gates_f32 ? 4 : esize(dtype);
+  if (B * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, gate) || !ok_ptr(dbeta, gate)))
     return TTT_ERR_ARG;
   if (!aligned(dW_final, 16) || !aligned(dW_init, 16)) return TTT_ERR_ARG;
   size_t need = 0;

@@ -551,8 +551,16 @@ __global__ __launch_bounds__(512) void k_delta_grads(DeltaGradArgs a) {
                        (colsum[1][0][lane] + colsum[1][1][lane] + colsum[1][2][lane] + colsum[1][3][lane]);
       if (lane < c.len) {
         const int64_t t = c.tok0 + lane;
-        ((T*)a.dg)[c.b * a.sdg.b + h * a.sdg.h + t * a.sdg.t] = from_f32<T>(dg);
-        ((T*)a.dbeta)[c.b * a.sdbeta.b + h * a.sdbeta.h + t * a.sdbeta.t] = from_f32<T>(n + left * kes);
+        const int64_t og = c.b * a.sdg.b + h * a.sdg.h + t * a.sdg.t;
+        const int64_t ob = c.b * a.sdbeta.b + h * a.sdbeta.h + t * a.sdbeta.t;
+        const float db = n + left * kes;
+        if (a.gates_f32) {
+          ((float*)a.dg)[og] = dg;
+          ((float*)a.dbeta)[ob] = db;
+        } else {
+          ((T*)a.dg)[og] = from_f32<T>(dg);
+          ((T*)a.dbeta)[ob] = from_f32<T>(db);
+        }
       }
     }
     // dQ += Mq K; dK += Mk K + Mk^T K + Mq^T Q

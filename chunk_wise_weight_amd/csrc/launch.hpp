@@ -261,6 +261,7 @@ struct DeltaGradArgs {
   void *dq, *dk, *dv, *dg, *dbeta;
   float* dW_init;                      // or null: not wanted
   DeltaStrides sdo, sdq, sdk, sdv, sdg, sdbeta;
+  bool gates_f32;                      // dg and dbeta are fp32, else of the inputs' type
   // regions of the workspace, placed by launch_delta_grad
   char *rec, *rect;
   void *states, *dstates, *errors, *xs;

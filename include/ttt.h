@@ -760,6 +760,7 @@ int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const 
 /* Strides of the backward call's own tensors, as in ttt_delta_layout. */
 typedef struct {
   ttt_delta_strides dO, dq, dk, dv, dg, dbeta;
+  int gates_f32;  /* nonzero: dg and dbeta are fp32, as g and beta are */
 } ttt_delta_grad_layout;
 
 /* Workspace of ttt_gated_delta_backward; num_seqs < 0: not packed.  Chunks
@@ -774,7 +775,8 @@ int ttt_gated_delta_backward_workspace_bytes(const ttt_delta_shape* shape, int d
  * the final states too, dW_final (else NULL):
  *   dq, dk     [B, Hk, n, dk]  dtype   (written) summed over the value heads of a key head
  *   dv         [B, Hv, n, dv]  dtype   (written)
- *   dg, dbeta  [B, Hv, n]      dtype   (written) the sums fp32, rounded once
+ *   dg, dbeta  [B, Hv, n]      dtype   (written) the sums fp32, rounded once;
+ *                              fp32, not rounded, with grad_layout's gates_f32
  *   dW_init    [sequences, Hv, dv, dk] fp32 (written), or NULL: not wanted
  * options' layout gives the inputs' strides (its O is not used), grad_layout
  * (NULL: contiguous) those of dO and the gradients.  Rows of tokens that

@@ -68,3 +68,11 @@ def test_the_backward_grids_stay_below_two_to_the_32_threads():
     assert size(shape(n=(1 << 29) - 64, Hk=1, Hv=2, dk=8, dv=8), what=back)[0] == cw.TTT_OK
     assert size(shape(n=(1 << 29) - 64, Hk=2, Hv=2, dk=8, dv=8), what=back)[0] == U
     assert backward(long) == U and backward(many, opts=cw.DeltaOptions(None, 1 << 20, 8000000, None)) == U
+
+
+def test_fp32_gate_gradients_are_aligned_as_such():
+    lay = lambda f32: cw.DeltaGradLayout(*(cw.DeltaStrides(12800, 6400, 64) for _ in range(4)),
+                                         cw.DeltaStrides(200, 100, 1), cw.DeltaStrides(200, 100, 1), f32)
+    assert backward(shape(), grads=lay(0), dg=(1 << 20) + 2, ws=None) == cw.TTT_ERR_WORKSPACE
+    assert backward(shape(), grads=lay(1), dg=(1 << 20) + 2, ws=None) == ARG
+    assert backward(shape(), grads=lay(1), ws=None) == cw.TTT_ERR_WORKSPACE

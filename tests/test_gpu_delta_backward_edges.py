@@ -61,3 +61,29 @@ def test_gradient_of_a_reset_is_zero():
         dO, W0, dWn = extras(1, 2, 150, 64, 64, dtype, "head")
         dg = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0)[3]
         assert not dg[:, :, at].any() and not dg.isnan().any()
+
+
+@pytest.mark.parametrize("layout", ["head", "token"])
+def test_gate_gradients_in_fp32(layout):
+    """g and beta are fp32, and so are their gradients where asked for: the same sums, not rounded to the inputs' type."""
+    args = make(2, 2, 4, 130, 64, 72, B16, layout, seed=21)
+    dO, W0, dWn = extras(2, 4, 130, 64, 72, B16, layout)
+    call = lambda **o: cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0, **o)
+    low, full = call(), call(gate_dtype=F32)
+    assert full[3].dtype == full[4].dtype == F32 and full[3].stride() == args[3].stride()
+    assert all(torch.equal(a, b) for i, (a, b) in enumerate(zip(low, full)) if i not in (3, 4))
+    for i in (3, 4):
+        assert torch.equal(full[i].to(B16), low[i]) and not torch.equal(full[i], low[i].float())
+    out = torch.full((2, 130, 5, 4), 7.0, device="cuda")                    # given, between other values
+    given = [out[:, :, i].transpose(1, 2) for i in (1, 3)]
+    call(gate_dtype=F32, dg=given[0], dbeta=given[1])
+    assert torch.equal(given[0], full[3]) and torch.equal(given[1], full[4]) and (out[:, :, ::2] == 7).all()
+    assert call(gate_dtype=B16)[3].dtype == B16
+    for err, o in ((TypeError, dict(gate_dtype=torch.float16)), (TypeError, dict(gate_dtype=F32, dg=low[3])),
+                   (TypeError, dict(gate_dtype=B16, dbeta=full[4]))):
+        with pytest.raises(err):
+            call(**o)
+    x = make(1, 1, 1, 5, 64, 64, F32)
+    assert cw.ttt_gated_delta_backward(*x, torch.ones_like(x[2]))[3].dtype == F32
+    with pytest.raises(TypeError):
+        cw.ttt_gated_delta_backward(*x, torch.ones_like(x[2]), gate_dtype=B16)
