@@ -3,7 +3,8 @@ import pytest
 import torch
 
 import chunk_wise_weight_amd as cw
-from test_gpu_delta import DTYPES, make
+from oracle import delta as od
+from test_gpu_delta import DTYPES, TOL_O, TOL_W, f64, make, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,54 @@ def test_no_sequences(dtype, n):
     _, W = cw.ttt_gated_delta(*args, seq_starts=starts, O=O)
     torch.cuda.synchronize()
     assert W.shape == (0, 2, 64, 64) and (O == 7).all()
+
+
+# Batches whose walks fill the chip, for which the state waves make O themselves: B, Hk, Hv, n, dk, dv, layout
+FULL = [(8, 8, 32, 130, 128, 128, "token"), (8, 16, 32, 130, 64, 128, "head"), (8, 8, 32, 65, 128, 136, "token"),
+        (20, 4, 32, 129, 64, 48, "head"), (6, 16, 64, 191, 96, 112, "token"), (40, 32, 32, 1, 64, 64, "token"),
+        (9, 32, 32, 200, 40, 64, "token")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", FULL)
+def test_batches_that_fill_the_chip(case, dtype):
+    """Against the oracle (some rows and heads), and bit for bit against rows on their own, whose walks do not fill it."""
+    B, Hk, Hv, n, dk, dv, layout = case
+    print("full", case, dtype, flush=True)
+    args = make(B, Hk, Hv, n, dk, dv, dtype, layout, seed=31)
+    W0 = torch.randn(B, Hv, dv, dk, generator=torch.Generator().manual_seed(32)).mul(0.3).cuda()
+    O, W = cw.ttt_gated_delta(*args, W_init=W0)
+    group = Hv // Hk
+    for b, kh in ((0, 0), (B // 2, Hk - 1), (B - 1, Hk // 2)):
+        v = slice(kh * group, (kh + 1) * group)
+        one = [t[b, kh:kh + 1] for t in args[:2]] + [t[b, v] for t in args[2:]]
+        Or, Wr = od.delta_rule(*(f64(t) for t in one), dk ** -0.5, f64(W0[b, v]))
+        assert rel(O[b, v], Or) <= TOL_O[dtype] and rel(W[b, v], Wr) <= TOL_W[dtype]
+        Oa, Wa = cw.ttt_gated_delta(*(t[None] for t in one), W_init=W0[b:b + 1, v].contiguous())
+        assert torch.equal(Oa[0], O[b, v]) and torch.equal(Wa[0], W[b, v])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dk", [64, 128])
+def test_many_packed_sequences(dk, dtype):
+    """Enough packed sequences to fill the chip, of 0 to 200 tokens, with NaN around them."""
+    Hk, Hv, dv, front, behind = 8, 16, 128, 3, 70
+    lens = [(i * 37) % 201 for i in range(90)]
+    n = front + sum(lens) + behind
+    args = make(1, Hk, Hv, n, dk, dv, dtype, seed=33)
+    for t in args:
+        t[:, :, :front] = float("nan")
+        t[:, :, n - behind:] = float("nan")
+    starts = torch.tensor([front] + lens).cumsum(0).to(torch.int32)
+    W0 = torch.randn(len(lens), Hv, dv, dk, generator=torch.Generator().manual_seed(34)).mul(0.3).cuda()
+    O = torch.full_like(args[2], 7.0)
+    _, W = cw.ttt_gated_delta(*args, W_init=W0, seq_starts=starts.cuda(), O=O)
+    assert (O[:, :, :front] == 7).all() and (O[:, :, n - behind:] == 7).all() and not O.isnan().any()
+    for i in (0, 1, 11, 38, 89):
+        at = slice(int(starts[i]), int(starts[i + 1]))
+        Oa, Wa = cw.ttt_gated_delta(*(t[:, :, at] for t in args), W_init=W0[i:i + 1])
+        assert torch.equal(Oa, O[:, :, at]) and torch.equal(Wa[0], W[i])
+        h, kh = (i * 5) % Hv, (i * 5) % Hv // 2
+        part = [f64(t[0, kh:kh + 1, at]) for t in args[:2]] + [f64(t[0, h:h + 1, at]) for t in args[2:]]
+        Or, Wr = od.delta_rule(*part, dk ** -0.5, f64(W0[i, h:h + 1]))
+        assert rel(O[0, h:h + 1, at], Or) <= TOL_O[dtype] and rel(W[i, h:h + 1], Wr) <= TOL_W[dtype], i
