@@ -87,3 +87,59 @@ def test_gate_gradients_in_fp32(layout):
     assert cw.ttt_gated_delta_backward(*x, torch.ones_like(x[2]))[3].dtype == F32
     with pytest.raises(TypeError):
         cw.ttt_gated_delta_backward(*x, torch.ones_like(x[2]), gate_dtype=B16)
+
+
+def check_by_scale(got, ref, dtype, what):
+    """As test_gpu_delta_backward's check, with an error measured against the largest gradient's norm where a gradient is
+    zero in exact arithmetic (dg and parts of dk of a sequence's first tokens)."""
+    largest = max(float(np.abs(b).max(initial=0.0)) for b in ref)
+    for name, a, b in zip(NAMES, got, ref):
+        if a is None:
+            continue
+        n = np.linalg.norm(b)
+        err = np.linalg.norm(f64(a) - b) / (n if n > 1e-12 else largest * b.size ** 0.5)
+        print("  ", what, name, err, flush=True)
+        assert err <= TOL[dtype][name], (what, name)
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+@pytest.mark.parametrize("n", [1, 2])
+@pytest.mark.parametrize("start", [False, True])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 72), (256, 128)])
+def test_one_and_two_tokens(dk, dv, start, n, dtype):
+    B, Hk, Hv = 3, 2, 4
+    args = make(B, Hk, Hv, n, dk, dv, dtype, seed=41)
+    dO, W0, dWn = extras(B, Hv, n, dk, dv, dtype, "token")
+    if not start:
+        W0 = dWn = None
+    got = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0)
+    refs = [od.delta_rule_backward(*(f64(t[b]) for t in args), dk ** -0.5, f64(dO[b]), f64(W0[b]) if start else None,
+                                   f64(dWn[b]) if start else None) for b in range(B)]
+    ref = [np.stack(r) for r in zip(*refs)]
+    check_by_scale(got if start else got[:5], ref, dtype, f"{n} tokens")
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+@pytest.mark.parametrize("lens", [[70, 0, 1, 64, 129], [1] * 9, [2, 1, 1, 0, 2, 65, 1]])
+def test_packed_single_tokens(lens, dtype):
+    """All sequences' gradients of a kind together: a gate's gradient of one token is one number, whose own error has no
+    norm to be held against."""
+    Hk, Hv, dk, dv, front, behind = 1, 2, 64, 48, 5, 37
+    n = front + sum(lens) + behind
+    args = make(1, Hk, Hv, n, dk, dv, dtype, seed=len(lens))
+    dO, _, _ = extras(1, Hv, n, dk, dv, dtype, "token")
+    _, W0, dWn = extras(len(lens), Hv, 1, dk, dv, dtype, "token")
+    for t in (*args, dO):
+        t[:, :, :front] = float("nan")
+        t[:, :, n - behind:] = float("nan")
+    starts = torch.tensor([front] + lens).cumsum(0).to(torch.int32)
+    outs = {x: torch.full_like(t, 7.0, dtype=dtype) for x, t in zip(NAMES, args)}
+    got = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0, seq_starts=starts.cuda(), **outs)
+    refs = []
+    for i, m in enumerate(lens):
+        cut = lambda t: f64(t[0, :, int(starts[i]):int(starts[i]) + m])
+        refs.append(od.delta_rule_backward(*(cut(t) for t in args), dk ** -0.5, cut(dO), f64(W0[i]), f64(dWn[i])))
+    ref = [np.concatenate(r, 1) for r in list(zip(*refs))[:5]] + [np.stack([r[5] for r in refs])]
+    for t in got[:5]:
+        assert (t[:, :, :front] == 7).all() and (t[:, :, n - behind:] == 7).all()
+    check_by_scale([t[0, :, front:n - behind] for t in got[:5]] + [got[5]], ref, dtype, f"{lens}")
