@@ -33,6 +33,7 @@
 namespace ttt {
 
 constexpr int kDC = 64;          // tokens of a chunk
+constexpr float kResetDecay = -200.f;   // log decays below it empty the state
 
 template <typename T> struct Mat;
 

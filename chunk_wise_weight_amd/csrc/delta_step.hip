@@ -81,7 +81,7 @@ __global__ __launch_bounds__(64 * kStepWaves) void k_delta_step(DeltaStepArgs p)
     const float kq = lanes_sum<LPR>(k[0] * q[0] + k[1] * q[1] + k[2] * q[2] + k[3] * q[3]);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      w[i] *= a;
+      w[i] = a == 0.f ? (f32x4){0.f, 0.f, 0.f, 0.f} : w[i] * a;   // a reset also clears what is not finite
       const float wk = lanes_sum<LPR>(w[i][0] * k[0] + w[i][1] * k[1] + w[i][2] * k[2] + w[i][3] * k[3]);
       const float wq = lanes_sum<LPR>(w[i][0] * q[0] + w[i][1] * q[1] + w[i][2] * q[2] + w[i][3] * q[3]);
       const float u = beta * (vj[i] - wk);

@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kChunkThreads) __attribute__((amdgpu_waves_per_eu(B
       bi = p.beta[c.b * p.sbeta.b + h * p.sbeta.h + (c.tok0 + lane) * p.sbeta.t];
     }
     // exp(-200) is zero in fp32: a decay of -inf (a state reset) keeps the running sum finite
-    double s = gi < -200.f ? -200.0 : (double)gi;
+    double s = gi < kResetDecay ? kResetDecay : gi;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double up = __shfl_up(s, d, 64);
@@ -344,11 +344,14 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
   // state block t, register r: dk = row(t, 4 g + r), dv = col
   f32x4 S[ST];
   const int64_t wbase = (((int64_t)seq * p.Hv + h) * p.dv + col) * p.dk;
+  // A sequence that begins with a reset takes nothing from W_init, whatever values it holds.
+  const bool resumed =
+      p.W_init && !(sp.len > 0 && p.g[sp.b * p.sg.b + h * p.sg.h + sp.tok0 * p.sg.t] < kResetDecay);
 #pragma unroll
   for (int t = 0; t < ST; ++t) {
     const int d = M::row(t, g * 4);
     S[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    if (p.W_init && d < p.dk && col < p.dv) S[t] = *reinterpret_cast<const f32x4*>(p.W_init + wbase + d);
+    if (resumed && d < p.dk && col < p.dv) S[t] = *reinterpret_cast<const f32x4*>(p.W_init + wbase + d);
   }
 
   for (int c = 0; c < chunks; ++c) {

@@ -749,8 +749,13 @@ int ttt_gated_delta_workspace_bytes(const ttt_delta_shape* shape, int dtype, int
  *   O         [B, Hv, n, dv]  dtype   (written)
  *   W_final   [sequences, Hv, dv, dk] fp32 (written)  sequences = B, or num_seqs
  * A log decay of -inf (or below -200) sets the state to zero before the
- * token's step: a document boundary inside a sequence.  beta = 0 leaves the
- * state as it is (the token's k and v have to be finite all the same).  With bf16 inputs the
+ * token's step: a document boundary inside a sequence; at a sequence's first
+ * token W_init's values are not looked at.  beta = 0 leaves the state as it is.
+ * All other inputs of tokens that belong to a sequence have to be finite, also
+ * where beta = 0: one that is not leaves every output of its sequence and
+ * heads undefined, those of earlier tokens of its 64 and of tokens behind a
+ * later reset among them, but none of other sequences or heads (in the backward
+ * pass: of other key heads).  With bf16 inputs the
  * state and what feeds it keep 16 bits or more of mantissa throughout.
  * seq_len == 0 or an empty sequence: W_final is W_init (or zero). */
 int ttt_gated_delta(const ttt_delta_shape* shape, int dtype, float scale, const void* q, const void* k, const void* v,
@@ -806,7 +811,8 @@ typedef struct {
  *             same state take their tokens in row order.  NULL: row r's
  *             state is W[r] (rows <= states, else TTT_ERR_SHAPE).
  *   O         [rows, Hv, dv]  dtype   (written)
- * All arithmetic and the state are fp32.  rows * v_heads * ceil(v_dim / 16)
+ * A log decay of -inf (or below -200) empties the state, whatever values it
+ * holds.  All arithmetic and the state are fp32.  rows * v_heads * ceil(v_dim / 16)
  * below 2^24, else TTT_ERR_UNSUPPORTED. */
 int ttt_gated_delta_step(const ttt_delta_step_shape* shape, int dtype, float scale, const void* q, const void* k,
                          const void* v, const float* g, const float* beta, float* W, const int32_t* slots, void* O,

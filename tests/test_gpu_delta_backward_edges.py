@@ -143,3 +143,36 @@ def test_packed_single_tokens(lens, dtype):
     for t in got[:5]:
         assert (t[:, :, :front] == 7).all() and (t[:, :, n - behind:] == 7).all()
     check_by_scale([t[0, :, front:n - behind] for t in got[:5]] + [got[5]], ref, dtype, f"{lens}")
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+def test_reset_at_the_first_token_clears_any_state(dtype):
+    """As in the forward pass: the state to start from is not looked at, and its gradient is zero."""
+    args = make(2, 1, 2, 100, 64, 48, dtype, "head", seed=51)
+    dO, W0, dWn = extras(2, 2, 100, 64, 48, dtype, "head")
+    args[3][1, :, 0] = float("-inf")
+    zero = W0.clone()
+    W0[1], zero[1] = float("nan"), 0.0
+    got = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0)
+    ref = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=zero)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and not got[5][1].any() and got[5][0].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+def test_values_that_are_not_finite_stay_in_their_sequence_and_key_heads(dtype):
+    lens, Hk, Hv = [70, 64, 100, 5], 2, 4
+    n = sum(lens)
+    args = make(1, Hk, Hv, n, 64, 64, dtype, seed=53)
+    dO = extras(1, Hv, n, 64, 64, dtype, "token")[0]
+    starts = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    call = lambda x, d: cw.ttt_gated_delta_backward(*x, d, seq_starts=starts.cuda())
+    ref = call(args, dO)
+    inside = torch.zeros(n, dtype=torch.bool, device="cuda")
+    inside[int(starts[1]):int(starts[2])] = True
+    for t in range(6):                                                     # dO is the last
+        bad = [x.clone() for x in (*args, dO)]
+        bad[t][:, 0, 75] = float("nan")
+        got = call(bad[:5], bad[5])
+        for a, b in zip(got[:5], ref):
+            other = slice(1, None) if a.shape[1] == Hk else slice(Hv // Hk, None)
+            assert torch.equal(a[:, other], b[:, other]) and torch.equal(a[:, :, ~inside], b[:, :, ~inside])

@@ -4,7 +4,7 @@ import torch
 
 import chunk_wise_weight_amd as cw
 from oracle import delta as od
-from test_gpu_delta import DTYPES, TOL_O, TOL_W, f64, make, rel
+from test_gpu_delta import DTYPES, TOL_O, TOL_W, f64, make, make_step, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,47 @@ def test_many_packed_sequences(dk, dtype):
         part = [f64(t[0, kh:kh + 1, at]) for t in args[:2]] + [f64(t[0, h:h + 1, at]) for t in args[2:]]
         Or, Wr = od.delta_rule(*part, dk ** -0.5, f64(W0[i, h:h + 1]))
         assert rel(O[0, h:h + 1, at], Or) <= TOL_O[dtype] and rel(W[i, h:h + 1], Wr) <= TOL_W[dtype], i
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_reset_at_the_first_token_clears_any_state(dtype):
+    """Fresh sequences among resumed ones: g = -inf at the first token, and a state that was never written (NaN, inf).
+    An empty sequence has no such token and keeps its state."""
+    lens, Hk, Hv, dk, dv = [70, 0, 1, 130], 1, 2, 64, 48
+    args = make(1, Hk, Hv, sum(lens), dk, dv, dtype, seed=51)
+    starts = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    W0 = torch.randn(4, Hv, dv, dk, generator=torch.Generator().manual_seed(52)).cuda()
+    zero = W0.clone()
+    for i in (0, 2):
+        args[3][:, :, int(starts[i])] = float("-inf")
+        W0[i], zero[i] = float("nan"), 0.0
+        W0[i, :, ::2] = float("inf")
+    O, W = cw.ttt_gated_delta(*args, W_init=W0, seq_starts=starts.cuda())
+    Or, Wr = cw.ttt_gated_delta(*args, W_init=zero, seq_starts=starts.cuda())
+    assert torch.equal(O, Or) and torch.equal(W, Wr) and not O.isnan().any() and torch.equal(W[1], W0[1])
+    q, k, v, g, beta, pool = make_step(3, 3, Hk, Hv, dk, dv, dtype)
+    g[1] = float("-inf")
+    clean = pool.clone()
+    pool[1], clean[1] = float("nan"), 0.0
+    pool[1, 0] = float("-inf")
+    o, c = (cw.ttt_gated_delta_step(q, k, v, g, beta, w) for w in (pool, clean))
+    assert torch.equal(o, c) and torch.equal(pool, clean) and not o.isnan().any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_values_that_are_not_finite_stay_in_their_sequence_and_heads(dtype):
+    lens, Hk, Hv = [70, 64, 100, 5], 2, 4
+    args = make(1, Hk, Hv, sum(lens), 64, 64, dtype, seed=53)
+    starts = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    ref = cw.ttt_gated_delta(*args, seq_starts=starts.cuda())
+    at, same = 75, [i for i in range(4) if i != 1]
+    inside = torch.zeros(sum(lens), dtype=torch.bool, device="cuda")
+    inside[int(starts[1]):int(starts[2])] = True
+    for t, heads in ((0, [0, 1]), (1, [0, 1]), (2, [1]), (3, [1]), (4, [1])):      # q and k: both heads that read them
+        bad = [x.clone() for x in args]
+        bad[t][:, heads[0] if t > 1 else 0, at] = float("nan")
+        O, W = cw.ttt_gated_delta(*bad, seq_starts=starts.cuda())
+        others = [h for h in range(Hv) if h not in heads]
+        assert torch.equal(O[:, others], ref[0][:, others]) and torch.equal(W[:, others], ref[1][:, others])
+        assert torch.equal(O[:, :, ~inside], ref[0][:, :, ~inside]) and torch.equal(W[same], ref[1][same])
+        assert O[:, heads, at].isnan().any()
