@@ -33,22 +33,34 @@ hipError_t launch_walk(const DeltaArgs& a, int sequences, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Whether the state waves make O themselves.  A chunk takes a helped walk about
-// 1.4 us and a walk of its own 2.2 us (dk = 128, bf16), but the latter's
-// workgroup has 64 columns of the state instead of 32; a walk cannot end
-// before its longest chain, nor the launch before its workgroups have gone
-// over the 256 CUs.  One call, dk = dv = 128, 32 value heads, helped / own: 1 x
-// 64K tokens 2.20 / 3.4 ms, 8 x 8K 1.41 / 1.11 ms, 32 x 2K 1.44 / 1.11 ms; 12
-// packed prompts, 16 heads, the longest 6007 of 16456 tokens 0.22 / 0.30 ms.
+// Whether the state waves make O themselves.  A chunk takes a helped walk less
+// time than a walk of its own, but the latter's workgroup has 64 columns of the
+// state instead of 32.  LDS has room for one workgroup a CU, so rows of equal
+// length take as many rounds as there are times 256 workgroups; packed
+// sequences take their longest's time at least, and otherwise their chunks'
+// over 256 CUs.  Microseconds a chunk where the chip is full, helped / own: bf16
+// heads of up to 128 (kernels of 128) 1.9 / 2.65, of up to 64 1.55 / 2.05, fp32
+// of up to 64 3.35 / 5.5.  Both forms, rows x tokens, heads k x v (us, 32 value
+// heads but where said):
+//   bf16 128 x 128  1 x 16K 422 / 617   4 x 4K 244 / 174   8 x 2K 247 / 186, 8 heads 57 / 81, 48 heads 374 / 258
+//   bf16 64 x 64    1 x 16K 298 / 413   4 x 4K  99 / 113   8 x 2K 102 /  68, 8 heads 36 / 55, 48 heads 163 / 138
+//   bf16 96 x 96    1 x 16K 451 / 593   4 x 4K 236 / 166   8 x 2K 201 / 167, 8 heads 51 / 79, 48 heads 298 / 246
+//   fp32 64 x 64    1 x 16K 805 / 1269  4 x 4K 212 / 334   8 x 2K 216 / 178, 8 heads 103 / 163, 48 heads 321 / 339
+// 12 packed prompts, 16 heads of 128, the longest 6007 of 16456 tokens: 150 / 236.
 // The lengths of packed sequences are known on the device only: the longest is
 // taken for four times the mean.
+template <typename T, int DK>
 inline bool own_outputs(const DeltaArgs& a, int sequences) {
-  const double all = (double)a.batch * ((a.seqs.n + kDC - 1) / kDC);      // chunks of all rows
-  const double mean = all / std::max(sequences, 1), longest = a.seqs.starts ? std::min(all, 4 * mean) : mean;
+  constexpr double kHelpedUs = sizeof(T) == 4 ? 3.35 : DK == 64 ? 1.55 : 1.9;
+  constexpr double kOwnUs = sizeof(T) == 4 ? 5.5 : DK == 64 ? 2.05 : 2.65;
+  const double row = (a.seqs.n + kDC - 1) / kDC;                          // chunks of a row
+  const double longest = std::min(row, 4 * row / std::max(sequences, 1));  // packed: of a sequence, taken for
   auto time = [&](int columns, double chunk) {
-    return std::max(longest, all * a.Hv * ((a.dv + columns - 1) / columns) / 256.0) * chunk;
+    const int64_t parts = (int64_t)a.Hv * ((a.dv + columns - 1) / columns);
+    if (a.seqs.starts) return std::max(longest, row * parts / 256.0) * chunk;
+    return (double)((sequences * parts + 255) / 256) * row * chunk;
   };
-  return time(64, 2.2) < time(32, 1.4);
+  return time(64, kOwnUs) < time(32, kHelpedUs);
 }
 
 template <typename T, int DK>
@@ -57,7 +69,7 @@ hipError_t launch_walks(const DeltaArgs& a, int sequences, hipStream_t s) {
   constexpr bool QLDS = Walk<T, DK, NW, 2, kHelped, true>::kSmem <= kMaxLds;
   constexpr int STAGES = Walk<T, DK, NW, 2, kHelped, QLDS>::kSmem <= kMaxLds ? 2 : 1;
   if constexpr (Walk<T, DK, 4, 2, kOwn, true>::kSmem <= kMaxLds)
-    if (own_outputs(a, sequences))
+    if (own_outputs<T, DK>(a, sequences))
       return launch_walk<T, DK, 4, 2, kOwn, true>(a, sequences, s);
   return launch_walk<T, DK, NW, STAGES, kHelped, QLDS>(a, sequences, s);
 }
