@@ -24,6 +24,7 @@ inline int64_t esize(int t) { return t == TTT_BF16 ? 2 : 4; }
 // forward walk's, of up to 384, are at most half as many.
 constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1, kMaxBlocks = kMaxThreads / 256;
 constexpr int64_t kMaxDim = 256, kMaxVDim = 4096, kMaxTokenStride = (int64_t)1 << 22;
+constexpr int64_t kMaxNamedRows = 65536;     // of a step with slots: each workgroup looks through all of them
 
 int check_heads(int64_t Hk, int64_t Hv, int64_t dk, int64_t dv) {
   if (Hk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0 || Hv % Hk) return TTT_ERR_SHAPE;
@@ -245,6 +246,7 @@ int ttt_gated_delta_step(const ttt_delta_step_shape* shape, int dtype, float sca
   if (shape->states > INT32_MAX || shape->rows > INT32_MAX ||
       shape->rows * shape->v_heads * ((shape->v_dim + 15) / 16) > kMaxBlocks)
     return TTT_ERR_UNSUPPORTED;
+  if (slots != nullptr && shape->rows > kMaxNamedRows) return TTT_ERR_UNSUPPORTED;
   if (slots == nullptr && shape->rows > shape->states) return TTT_ERR_SHAPE;
   if (!isfinite(scale)) return TTT_ERR_ARG;
   if (shape->rows == 0) return TTT_OK;

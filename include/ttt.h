@@ -813,7 +813,7 @@ typedef struct {
  *   O         [rows, Hv, dv]  dtype   (written)
  * A log decay of -inf (or below -200) empties the state, whatever values it
  * holds.  All arithmetic and the state are fp32.  rows * v_heads * ceil(v_dim / 16)
- * below 2^24, else TTT_ERR_UNSUPPORTED. */
+ * below 2^24, and at most 65536 rows with slots, else TTT_ERR_UNSUPPORTED. */
 int ttt_gated_delta_step(const ttt_delta_step_shape* shape, int dtype, float scale, const void* q, const void* k,
                          const void* v, const float* g, const float* beta, float* W, const int32_t* slots, void* O,
                          void* stream);

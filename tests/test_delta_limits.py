@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import chunk_wise_weight_amd as cw
-from test_delta_host import ARG, backward, forward, shape, size
+from test_delta_host import ARG, backward, forward, shape, size, step
 
 WORKSPACES = ("ttt_gated_delta_workspace_bytes", "ttt_gated_delta_backward_workspace_bytes")
 
@@ -76,3 +76,11 @@ def test_fp32_gate_gradients_are_aligned_as_such():
     assert backward(shape(), grads=lay(0), dg=(1 << 20) + 2, ws=None) == cw.TTT_ERR_WORKSPACE
     assert backward(shape(), grads=lay(1), dg=(1 << 20) + 2, ws=None) == ARG
     assert backward(shape(), grads=lay(1), ws=None) == cw.TTT_ERR_WORKSPACE
+
+
+def test_rows_that_name_their_states_are_limited():
+    """Their number's square is what looking for rows of one state takes; a call past the limit is refused, one at it goes on
+    to the pointers' checks."""
+    U = cw.TTT_ERR_UNSUPPORTED
+    assert step(R=65537, Hv=1, dv=8) == U and step(R=65536, Hv=1, dv=8, q=None) == ARG
+    assert step(R=65537, S=70000, Hv=1, dv=8, slots=None, q=None) == ARG

@@ -4,7 +4,7 @@ import torch
 
 import chunk_wise_weight_amd as cw
 from oracle import delta as od
-from test_gpu_delta import DTYPES, TOL_O, TOL_W, f64, make, make_step, rel
+from test_gpu_delta import DTYPES, TOL_O, TOL_STEP, TOL_W, f64, make, make_step, rel, step_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,22 @@ def test_values_that_are_not_finite_stay_in_their_sequence_and_heads(dtype):
         assert torch.equal(O[:, others], ref[0][:, others]) and torch.equal(W[:, others], ref[1][:, others])
         assert torch.equal(O[:, :, ~inside], ref[0][:, :, ~inside]) and torch.equal(W[same], ref[1][same])
         assert O[:, heads, at].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,P", [(511, 300), (512, 512), (513, 2), (1600, 700), (3000, 2000)])
+def test_step_of_many_rows(R, P, dtype):
+    """Rows of one state near and far from each other, at the ends of the blocks that are looked through, and padding."""
+    gen = torch.Generator().manual_seed(R)
+    slots = torch.randint(-1, P, (R,), generator=gen).to(torch.int32)
+    for i in (0, 1, 63, 64, 255, 256, 510, 511, 512, 513, 1023, 1024, 1535, 1536, 2559, R - 1):
+        if i < R:
+            slots[i] = 1
+    q, k, v, g, beta, W = make_step(R, P, 1, 1, 16, 8, dtype, seed=R)
+    Or, Wr = step_reference(q, k, v, g, beta, W, slots.tolist(), 0.25)
+    O = cw.ttt_gated_delta_step(q, k, v, g, beta, W, slots=slots.cuda(), scale=0.25)
+    assert rel(O, Or) <= TOL_STEP[dtype] and not O[slots.cuda() < 0].any()
+    # a state's roundings of its rows one after the other: 2^-24 times dk a row, which later rows' decays and
+    # corrections shrink; the longest run here is R / 2 rows (513 rows on 2 states), whose decays are e^-0.5 on average:
+    # less than 3 rows' roundings remain
+    assert rel(W, Wr) <= 3 * TOL_STEP[torch.float32]
