@@ -5,7 +5,7 @@ import torch
 
 import chunk_wise_weight_amd as cw
 from oracle import delta as od
-from test_gpu_delta import f64, make
+from test_gpu_delta import TOL_O, TOL_W, f64, make, rel
 from test_gpu_delta_backward import B16, F32, NAMES, TOL, extras
 
 pytestmark = pytest.mark.gpu
@@ -176,3 +176,42 @@ def test_values_that_are_not_finite_stay_in_their_sequence_and_key_heads(dtype):
         for a, b in zip(got[:5], ref):
             other = slice(1, None) if a.shape[1] == Hk else slice(Hv // Hk, None)
             assert torch.equal(a[:, other], b[:, other]) and torch.equal(a[:, :, ~inside], b[:, :, ~inside])
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+@pytest.mark.parametrize("dk,dv", [(64, 4096), (256, 520), (8, 8), (192, 104), (136, 264)])
+def test_widths_between_and_at_the_limits(dk, dv, dtype):
+    """Forward and backward of the widest values, of keys between the kernels' widths, and of the narrowest heads."""
+    args = make(1, 1, 2, 70, dk, dv, dtype, seed=61)
+    dO, W0, dWn = extras(1, 2, 70, dk, dv, dtype, "token")
+    O, W = cw.ttt_gated_delta(*args, W_init=W0)
+    got = cw.ttt_gated_delta_backward(*args, dO, dW_final=dWn, W_init=W0)
+    x = [f64(t[0]) for t in args]
+    Or, Wr = od.delta_rule(*x, dk ** -0.5, f64(W0[0]))
+    assert rel(O[0], Or) <= TOL_O[dtype] and rel(W[0], Wr) <= TOL_W[dtype]
+    ref = od.delta_rule_backward(*x, dk ** -0.5, f64(dO[0]), f64(W0[0]), f64(dWn[0]))
+    check_by_scale([t[0] for t in got], ref, dtype, f"{dk} x {dv}")
+
+
+@pytest.mark.parametrize("dtype", [F32, B16])
+def test_largest_token_strides(dtype):
+    """Tokens 2^22 elements apart, the most that is taken, one tensor at a time, given and written."""
+    n, d, far = 70, 64, 1 << 22
+    args = make(1, 1, 1, n, d, d, dtype, "head", seed=62)
+    dO = extras(1, 1, n, d, d, dtype, "head")[0]
+    base = torch.empty((n - 1) * far + d, dtype=dtype, device="cuda")
+    wide = base.as_strided((1, 1, n, d), (n * far, far, far, 1))
+    ref, grads = cw.ttt_gated_delta(*args), cw.ttt_gated_delta_backward(*args, dO)
+    for i in range(4):
+        x = [*args[:3], dO]
+        wide.copy_(x[i])
+        x[i] = wide
+        got = cw.ttt_gated_delta(*x[:3], *args[3:])
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        assert all(torch.equal(a, b) for a, b in zip(cw.ttt_gated_delta_backward(*x[:3], *args[3:], x[3]), grads[:5]))
+    assert torch.equal(cw.ttt_gated_delta(*args, O=wide)[0], ref[0])
+    for i, name in enumerate(NAMES[:3]):
+        wide.zero_()
+        assert torch.equal(cw.ttt_gated_delta_backward(*args, dO, **{name: wide})[i], grads[i])
+    with pytest.raises(cw.TTTError):
+        cw.ttt_gated_delta(base.as_strided((1, 1, 3, d), (3 * far, far, far + 64, 1)), *(t[:, :, :3] for t in args[1:]))
