@@ -154,7 +154,7 @@ int check_norm(int64_t rows, int64_t dim, int dtype) {
   return TTT_OK;
 }
 
-// Rows of whole 16-byte vectors are read as such; others element by element.
+// Rows of whole 16-byte vectors are read as aligned ones; others need their elements' alignment only.
 size_t norm_align(int64_t dim, int dtype) { return dim * esize(dtype) % 16 ? (size_t)esize(dtype) : 16; }
 
 }  // namespace

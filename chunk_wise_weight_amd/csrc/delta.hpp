@@ -23,7 +23,10 @@
 // fp32: the state is off by 3e-6 of its norm after 64K tokens.  What feeds only
 // the output O, which is rounded to bf16 at the end, is rounded once to bf16 (the
 // state in Q S, P), but for the errors in P E, the larger part of O, which are
-// a pair too: O is off by 2.4e-3, its own rounding being 1.7e-3 of that.
+// a pair too: O is off by 2.4e-3 of its norm, of which 1.7e-3 is its own
+// rounding and the rest, of the same size, that of S and P.  Pairs there too
+// would take 22 products a chunk beside 110, and 6 KB a chunk and head to write
+// and read, for the step from 2.4e-3 to 1.7e-3 in O alone.
 #pragma once
 #include <type_traits>
 
@@ -100,20 +103,11 @@ template <> struct Mat<float> {
   }
 };
 
-// c + a b with b = hi + lo and a exact; with a = hi + lo too.
+// c + a b with b = hi + lo and a exact.
 template <typename T>
 __device__ __forceinline__ f32x4 mma_split(u32x4 a, u32x4 bh, u32x4 bl, f32x4 c) {
   c = Mat<T>::mma(a, bh, c);
   if (Mat<T>::kSplit) c = Mat<T>::mma(a, bl, c);
-  return c;
-}
-template <typename T>
-__device__ __forceinline__ f32x4 mma_split2(u32x4 ah, u32x4 al, u32x4 bh, u32x4 bl, f32x4 c) {
-  c = Mat<T>::mma(ah, bh, c);
-  if (Mat<T>::kSplit) {
-    c = Mat<T>::mma(ah, bl, c);
-    c = Mat<T>::mma(al, bh, c);
-  }
   return c;
 }
 

@@ -15,9 +15,9 @@ namespace {
 //   T_ij = -T_ii sum_{j <= l < i} A_il T_lj,   A = L diag(beta),
 // wave j taking column j: fp32 MFMA products, the running block column staying
 // in registers as the next product's operand.  64K tokens of 32 heads of 128:
-// 372 us, of which the operands' loads and products about 150, the inverse 100,
-// the exponentials 30 and the stores 60: each workgroup is a chain of short
-// phases, so the more of them a CU holds the better.  Forward: operands of two
+// 361 to 374 us (an earlier form's 419: the operands' loads and products about
+// 150, the inverse 100, the exponentials 30, the stores 60): each workgroup is a
+// chain of short phases, so the more of them a CU holds the better.  Forward: operands of two
 // steps at a time and four waves a SIMD (372 us; four steps and three waves
 // 419); the backward's form, with twice the stores, is better off with the
 // latter (70 us for 4 x 4096 tokens of 16 heads; 79).

@@ -6,7 +6,9 @@
 //
 // Both passes are bound by HBM: a row is read once, held in registers between
 // the statistics and the output (the variance is the second of two passes over
-// the registers, so a large common offset costs no digits), and written once.
+// the registers, so a large common offset is not squared; the mean itself is
+// fp32, so y is off by some 2^-24 of the offset over the row's spread), and
+// written once.
 // TPR threads share a row, each holding NV vectors of VEC elements; vector i
 // of thread t starts at element (i TPR + t) VEC, so a wave's loads are
 // contiguous.  Narrower rows (norm_plan) belong to one wave or a quarter of
@@ -15,7 +17,9 @@
 // vector a thread while that reaches.  VEC = 16 bytes.  RAG: row lengths that
 // are no multiple of it: rows then start at any element, so the vectors are
 // read and written without alignment, and a row's last one element by element.  Forward 131072 x 2560 bf16: 280
-// us, 4.8 TB/s; backward 32768 x 2560: 106 us, 524288 x 128: 81 us, 5 TB/s.
+// us, 4.8 TB/s; backward 32768 x 2560: 106 us, 524288 x 128: 81 us, 5 TB/s.  fp32
+// 32768 x 1024: forward 44 us, backward 96 us (4.2 TB/s); 16384 x 2560, wider than
+// a wave's rows: 99 and 100 us (3.4 and 5.0 TB/s).
 #include <algorithm>
 
 #include "common.hpp"
