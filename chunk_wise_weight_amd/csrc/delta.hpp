@@ -19,14 +19,13 @@
 //
 // Precision (bf16 inputs).  A product's bf16 operand that comes from fp32
 // registers is a pair hi + lo of bf16 values (2^-17 relative), with hi x hi,
-// hi x lo and lo x hi summed in fp32, wherever it feeds the state, which is
-// fp32: the state is off by 3e-6 of its norm after 64K tokens.  What feeds only
-// the output O, which is rounded to bf16 at the end, is rounded once to bf16 (the
-// state in Q S, P), but for the errors in P E, the larger part of O, which are
-// a pair too: O is off by 2.4e-3 of its norm, of which 1.7e-3 is its own
-// rounding and the rest, of the same size, that of S and P.  Pairs there too
-// would take 22 products a chunk beside 110, and 6 KB a chunk and head to write
-// and read, for the step from 2.4e-3 to 1.7e-3 in O alone.
+// hi x lo and lo x hi summed in fp32: the fp32 state is off by 3e-6 of its norm
+// after 64K tokens, and O by its own rounding (1.7e-3; from the exact O rounded,
+// 1.4e-4).  A third bf16 value a number would take the state to fp32's own error
+// at 44 products and 160 vector instructions more in a chunk's chain of 82 and
+// 250; two keep it a thousand times closer than the bf16 inputs are to what they
+// stand for.  One operand is rounded once: the state in Q S for heads past 128,
+// whose pairs LDS has no room for (O off by up to 2.2e-3, where decays are weak).
 #pragma once
 #include <type_traits>
 
@@ -112,17 +111,39 @@ __device__ __forceinline__ f32x4 mma_split(u32x4 a, u32x4 bh, u32x4 bl, f32x4 c)
 }
 
 // What k_delta_chunks leaves of a chunk and value head, in operand order
-// (fragment, lane, 16 bytes): T (hi, then lo), the gates, P.
+// (fragment, lane, 16 bytes): T (hi, then lo), the gates, P (hi, then lo).  In
+// bf16 a fragment on the diagonal is zero in the lanes whose 8 columns lie
+// behind their row (lane group g > (lane & 15) >> 2): it is kept as its 40
+// other lanes, group by group, and 16 bytes of zeros for those.
 template <typename T> struct ChunkRec {
-  static constexpr int kFrag = Mat<T>::kTri * 1024;
-  static constexpr int kTl = kFrag;
-  static constexpr int kGate = Mat<T>::kSplit ? 2 * kFrag : kFrag;   // exp(b), beta exp(b_63 - b): 64 floats each
-  static constexpr int kP = kGate + 1024;
-  static constexpr int kBytes = kP + kFrag;
+  static constexpr bool kPacked = sizeof(T) == 2;
+  static constexpr int kDiag = 41 * 16;
+  static constexpr int kPart = kPacked ? 4 * kDiag + 2 * 1024 : Mat<T>::kTri * 1024;  // one triangular matrix
+  static constexpr int kTl = kPart;
+  static constexpr int kGate = Mat<T>::kSplit ? 2 * kPart : kPart;   // exp(b), beta exp(b_63 - b): 64 floats each
+  static constexpr int kP = kGate + (kPacked ? 512 : 1024), kPl = kP + kPart;
+  static constexpr int kBytes = (Mat<T>::kSplit ? 2 * kGate + 512 : kGate + 1024 + kPart) + 1023 & ~1023;
+  // KB that hold T and the gates, and the gates and P
+  static constexpr int kLoadT = (kP + 1023) / 1024, kLoadP = (kBytes - kGate + 1023) / 1024;
+  // A lane's place in the fragments of a part: on the diagonal, elsewhere.
+  __device__ static __forceinline__ int diag(int lane) {
+    const int g = lane >> 4, m = lane & 15;
+    return kPacked ? (g <= m >> 2 ? m + 14 * g - 2 * g * g : 40) * 16 : lane * 16;
+  }
+  // Where fragment (t, s) is in a part, from the lane's place on.
+  __device__ static constexpr bool on_diag(int t, int s) { return kPacked && s == t >> 1; }
+  __device__ static constexpr int at(int t, int s) {
+    return !kPacked ? Mat<T>::tri(t, s) * 1024 : on_diag(t, s) ? t * kDiag : 4 * kDiag + (t - 2) * 1024;
+  }
+  // A lane's operand of fragment (t, s): part + diag(lane), part + 16 lane.
+  __device__ static __forceinline__ u32x4 frag(const char* d, const char* f, int t, int s) {
+    return *reinterpret_cast<const u32x4*>((on_diag(t, s) ? d : f) + at(t, s));
+  }
 };
+static_assert(ChunkRec<bf16>::kBytes == 19 * 1024 && ChunkRec<float>::kBytes == 21 * 1024, "the header states them");
 // The same for the backward pass: the transposes of T and P (hi, lo each), the gates, and b itself (64 doubles).
 template <typename T> struct ChunkRecT {
-  static constexpr int kFrag = ChunkRec<T>::kFrag;
+  static constexpr int kFrag = Mat<T>::kTri * 1024;
   static constexpr int kTl = kFrag;
   static constexpr int kP = Mat<T>::kSplit ? 2 * kFrag : kFrag;
   static constexpr int kPl = kP + kFrag;
@@ -253,10 +274,10 @@ template <typename T, int NW> struct Columns {
   __device__ static __forceinline__ f32x4 wide(f32x4 x) { return x; }
 };
 
-// `N` KB that lie one after the other, by one wave.
+// `N` KB that lie one after the other, by one wave; bytes from `most` on read as zero.
 template <int N>
-__device__ __forceinline__ void load_block(const void* base, char* t) {
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, N * 1024);
+__device__ __forceinline__ void load_block(const void* base, char* t, int most = N * 1024) {
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, most);
 #pragma unroll
   for (int i = 0; i < N; ++i)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16, (unsigned)(i * 1024 + lane_id() * 16),

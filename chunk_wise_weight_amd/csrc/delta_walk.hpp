@@ -15,10 +15,10 @@ namespace {
 //   T_ij = -T_ii sum_{j <= l < i} A_il T_lj,   A = L diag(beta),
 // wave j taking column j: fp32 MFMA products, the running block column staying
 // in registers as the next product's operand.  64K tokens of 32 heads of 128:
-// 361 to 374 us (an earlier form's 419: the operands' loads and products about
+// 356 us (an earlier form's 419: the operands' loads and products about
 // 150, the inverse 100, the exponentials 30, the stores 60): each workgroup is a
 // chain of short phases, so the more of them a CU holds the better.  Forward: operands of two
-// steps at a time and four waves a SIMD (372 us; four steps and three waves
+// steps at a time and four waves a SIMD (an earlier form's 372 us; four steps and three waves
 // 419); the backward's form, with twice the stores, is better off with the
 // latter (70 us for 4 x 4096 tokens of 16 heads; 79).
 constexpr int kChunkThreads = 256;
@@ -29,9 +29,9 @@ __device__ __forceinline__ f32x4 mma_f32(const float* a, f32x4 b, f32x4 c) {
 }
 
 // The lower triangle X (or, with TRANS, its transpose) to memory in operand
-// order, in T's type, with SPLIT what that leaves too (for bf16).
-template <typename T, bool TRANS, bool SPLIT>
-__device__ __forceinline__ void put_triangle(const float* X, char* hi, char* lo) {
+// order, in T's type, for bf16 with what that leaves: whole fragments, by waves.
+template <typename T, bool TRANS>
+__device__ __forceinline__ void put_fragments(const float* X, char* hi, char* lo) {
   constexpr int E = 16 / sizeof(T);
   const int lane = lane_id(), m = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -48,8 +48,40 @@ __device__ __forceinline__ void put_triangle(const float* X, char* hi, char* lo)
       u32x4 h, l;
       Mat<T>::split(v, h, l);
       *reinterpret_cast<u32x4*>(hi + f * 1024 + lane * 16) = h;
-      if (SPLIT && Mat<T>::kSplit) *reinterpret_cast<u32x4*>(lo + f * 1024 + lane * 16) = l;
+      if (Mat<T>::kSplit) *reinterpret_cast<u32x4*>(lo + f * 1024 + lane * 16) = l;
     }
+}
+
+// The lower triangle X as a part of ChunkRec: in bf16 its 16 bytes one after the other, by threads.
+template <typename T>
+__device__ __forceinline__ void put_triangle(const float* X, char* hi, char* lo) {
+  using R = ChunkRec<T>;
+  if constexpr (!R::kPacked) {
+    put_fragments<T, false>(X, hi, lo);
+  } else {
+    for (int i = threadIdx.x; i < R::kPart / 16; i += kChunkThreads) {
+      int t, s = 0, lane;
+      if (i < 4 * 41) {                                    // on the diagonal; diag()'s inverse
+        t = i / 41;
+        s = t >> 1;
+        const int p = i - t * 41, g = p < 16 ? 0 : p < 28 ? 1 : p < 36 ? 2 : 3;
+        lane = g * 16 + p - 14 * g + 2 * g * g;
+        if (p == 40) {                                     // the zeros: four rows' columns behind the diagonal
+          t &= 2;
+          lane = 48;
+        }
+      } else {
+        t = 2 + (i - 4 * 41) / 64;
+        lane = (i - 4 * 41) & 63;
+      }
+      const float* x = X + Mat<T>::row(t, lane & 15) * kLd + s * 32 + (lane >> 4) * 8;
+      const f32x4 v[2] = {*reinterpret_cast<const f32x4*>(x), *reinterpret_cast<const f32x4*>(x + 4)};
+      u32x4 h, l;
+      Mat<T>::split(v, h, l);
+      *reinterpret_cast<u32x4*>(hi + i * 16) = h;
+      *reinterpret_cast<u32x4*>(lo + i * 16) = l;
+    }
+  }
 }
 
 // With BACK, T goes to rec and the transposes of T and P to rect.
@@ -155,9 +187,9 @@ __global__ __launch_bounds__(kChunkThreads) __attribute__((amdgpu_waves_per_eu(B
   // P to memory in operand order
   char* outt = rect + (int64_t)id * ChunkRecT<T>::kBytes;
   if (BACK)
-    put_triangle<T, true, true>(X, outt + ChunkRecT<T>::kP, outt + ChunkRecT<T>::kPl);
+    put_fragments<T, true>(X, outt + ChunkRecT<T>::kP, outt + ChunkRecT<T>::kPl);
   else
-    put_triangle<T, false, false>(X, out + ChunkRec<T>::kP, nullptr);
+    put_triangle<T>(X, out + ChunkRec<T>::kP, out + ChunkRec<T>::kPl);
   // the diagonal block's inverse: lane m has column m; x_i = [i = m] - sum_{l < i} A_il x_l
   float x[16];
   {
@@ -196,8 +228,8 @@ __global__ __launch_bounds__(kChunkThreads) __attribute__((amdgpu_waves_per_eu(B
     }
   }
   __syncthreads();
-  put_triangle<T, false, true>(X, out, out + ChunkRec<T>::kTl);
-  if (BACK) put_triangle<T, true, true>(X, outt, outt + ChunkRecT<T>::kTl);
+  put_triangle<T>(X, out, out + ChunkRec<T>::kTl);
+  if (BACK) put_fragments<T, true>(X, outt, outt + ChunkRecT<T>::kTl);
 }
 
 // ------------------------------------------------------------------ the walk over the chunks
@@ -213,13 +245,13 @@ __device__ __forceinline__ void put_state(const u32x4 (&S)[SS], T* W, int dk, bo
   }
 }
 
-// O of a chunk's tokens at 16 columns, from operands of the state and the
-// errors (fp32): the columns in the instruction's rows, tokens in its columns,
-// so that a lane gets 4 columns of one token.  gp: the chunk's gates and P; Q
-// in panels at q, or from memory through rq.
-template <typename T, int SS, bool QLDS = true>
-__device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const f32x4 (&e)[4], const char* gp, const char* q,
-                                             float scale, int len, bool in, int64_t pitch, T* out,
+// O of a chunk's tokens at 16 columns, from operands of the state (Sl: what Sh
+// leaves, LO) and the errors (fp32): the columns in the instruction's rows,
+// tokens in its columns, so that a lane gets 4 columns of one token.  gp: the
+// chunk's gates and P; Q in panels at q, or from memory through rq.
+template <typename T, int SS, bool LO, bool QLDS = true>
+__device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const u32x4 (&Sl)[SS], const f32x4 (&e)[4],
+                                             const char* gp, const char* q, float scale, int len, bool in, int64_t pitch, T* out,
                                              const void* q_rows = nullptr, unsigned qp = 0, unsigned qrow = 0) {
   using M = Mat<T>;
   constexpr int CS = kDC / M::KB;
@@ -227,37 +259,57 @@ __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const f32x4 
   u32x4 Eh[CS], El[CS];
 #pragma unroll
   for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Eh[s], El[s]);
-  f32x4 o[4];
+  constexpr int TB = M::kSplit ? 2 : 1;     // blocks of tokens at a time, whose sums do not wait for each other
+  using R = ChunkRec<T>;
+  const char *pd = gp + R::kP - R::kGate + R::diag(lane), *pf = gp + R::kP - R::kGate + lane * 16;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int r = M::row(t, m);
-    u32x4 f[SS];
-    if constexpr (QLDS) {
+  for (int t0 = 0; t0 < 4; t0 += TB) {
+    f32x4 o[TB];
+    u32x4 f[TB][SS];
 #pragma unroll
-      for (int s = 0; s < SS; ++s) f[s] = Panels<T>::frag(q, r, s, g);
-    } else {
-      const __amdgpu_buffer_rsrc_t rq = rows_rsrc(q_rows);
+    for (int i = 0; i < TB; ++i) {
+      const int r = M::row(t0 + i, m);
+      o[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if constexpr (QLDS) {
 #pragma unroll
-      for (int s = 0; s < SS; ++s) {
-        const unsigned byte = s * 64u + g * 16u;
-        f[s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
+        for (int s = 0; s < SS; ++s) f[i][s] = Panels<T>::frag(q, r, s, g);
+      } else {
+        const __amdgpu_buffer_rsrc_t rq = rows_rsrc(q_rows);
+#pragma unroll
+        for (int s = 0; s < SS; ++s) {
+          const unsigned byte = s * 64u + g * 16u;
+          f[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
+        }
       }
     }
-    o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < SS; ++s) o[t] = M::mma(Sh[s], f[s], o[t]);
-  }
+    for (int s = 0; s < SS; ++s)
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int r = M::row(t, m);
-    o[t] *= scale * reinterpret_cast<const float*>(gp)[r];
+      for (int l = 0; l < (LO ? 2 : 1); ++l)
 #pragma unroll
-    for (int s = 0; s < M::steps(t); ++s) {
-      const u32x4 f = *reinterpret_cast<const u32x4*>(gp + 1024 + M::tri(t, s) * 1024 + lane * 16);
-      o[t] = M::mma(Eh[s], f, o[t]);
-      if (M::kSplit) o[t] = M::mma(El[s], f, o[t]);
+        for (int i = 0; i < TB; ++i) o[i] = M::mma(l ? Sl[s] : Sh[s], f[i][s], o[i]);
+#pragma unroll
+    for (int i = 0; i < TB; ++i) o[i] *= scale * reinterpret_cast<const float*>(gp)[M::row(t0 + i, m)];
+#pragma unroll
+    for (int s = 0; s < CS; ++s) {
+      u32x4 ph[TB], pl[TB];
+#pragma unroll
+      for (int i = 0; i < TB; ++i)
+        if (s < M::steps(t0 + i)) {
+          ph[i] = R::frag(pd, pf, t0 + i, s);
+          if (M::kSplit) pl[i] = R::frag(pd + R::kPart, pf + R::kPart, t0 + i, s);
+        }
+#pragma unroll
+      for (int l = 0; l < (M::kSplit ? 3 : 1); ++l)
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+          if (s < M::steps(t0 + i)) o[i] = M::mma(l == 1 ? El[s] : Eh[s], l == 2 ? pl[i] : ph[i], o[i]);
     }
-    if (r < len && in) store4(out + (int64_t)r * pitch, o[t][0], o[t][1], o[t][2], o[t][3]);
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+      const int r = M::row(t0 + i, m);
+      if (r < len && in) store4(out + (int64_t)r * pitch, o[i][0], o[i][1], o[i][2], o[i][3]);
+    }
   }
 }
 
@@ -274,7 +326,8 @@ __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const f32x4 
 // instructions, 1.33 us with every load taken out; that bounds the walk.  One
 // barrier a chunk.  By OUT:
 //   kHelped  as many helper waves, one chunk behind, make O from the state and
-//            the errors that the state waves left in LDS, their Q and P coming
+//            the errors that the state waves left in LDS (after their own reads
+//            from it, which they wait for), their Q and P coming
 //            with the DMA too where there is room, else straight from memory:
 //            the shortest chain, for walks that do not fill the chip
 //   kOwn     the state waves make O themselves: four of them to a workgroup,
@@ -284,17 +337,20 @@ __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const f32x4 
 enum { kKeep = 0, kHelped = 1, kOwn = 2 };
 template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS> struct Walk {
   static constexpr int SS = DK / Mat<T>::KB;
-  static constexpr int kK = 0, kRec = Panels<T>::bytes(DK), kV = kRec + ChunkRec<T>::kP;
+  static constexpr int kK = 0, kRec = Panels<T>::bytes(DK), kV = kRec + ChunkRec<T>::kLoadT * 1024;
   static constexpr int kStage = kV + Columns<T, NW>::kBytes;
   // the helpers' stages: gates and P, then Q
-  static constexpr int kG = STAGES * kStage, kQ = ChunkRec<T>::kBytes - ChunkRec<T>::kGate;
+  static constexpr int kG = STAGES * kStage, kQ = ChunkRec<T>::kLoadP * 1024;
   static constexpr int kStageQ = OUT != kKeep && QLDS ? kQ + Panels<T>::bytes(DK) : 0;
   static constexpr int kSwap = kG + STAGES * kStageQ;      // a state wave's state operands and errors (fp32), twice
-  static constexpr int kSwapBytes = SS * 1024 + 4096;
+  // whether O takes the state as a pair: for all but the bf16 heads past 128, for which LDS has no room
+  static constexpr bool kLo = Mat<T>::kSplit && DK <= 128;
+  static constexpr int kSwapE = SS * (kLo ? 2048 : 1024), kSwapBytes = kSwapE + 4096;
   static constexpr int kSmem = kSwap + (OUT == kHelped ? 2 * NW * kSwapBytes : 0);
   static constexpr int kThreads = 64 * (2 + NW * (OUT == kHelped ? 2 : 1));   // kKeep: with one DMA wave, 64 fewer
   static constexpr int kLag = OUT == kHelped ? 1 : 0;      // turns that O is behind
   static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
+  static constexpr bool kLateK = OUT == kOwn && kLo;       // K^T's only behind O, which needs the state's low parts
 };
 
 template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS>
@@ -320,12 +376,14 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, int parts, const 
     if (parts & 1) {
       if (c < chunks) {
         kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
-        vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
       }
-      if (out) load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, sq);
+      if (out) load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, sq, ChunkRec<T>::kBytes - ChunkRec<T>::kGate);
     }
     if (parts & 2) {
-      if (c < chunks) load_block<ChunkRec<T>::kP / 1024>(rec0 + c * rstep, st + G::kRec);
+      if (c < chunks) {
+        load_block<ChunkRec<T>::kLoadT>(rec0 + c * rstep, st + G::kRec);
+        vload.issue(v0 + (int64_t)c * kDC * p.sv.t, len, st + G::kV);
+      }
       if (out) qload.issue(q0 + (int64_t)d * kDC * p.sq.t, min(kDC, sp.len - d * kDC), sq + G::kQ);
     }
   };
@@ -383,10 +441,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
     __builtin_amdgcn_sched_barrier(0);
     u32x4 Sh[SS], Sl[SS];
 #pragma unroll
-    for (int s = 0; s < SS; ++s) {
-      M::split(S + s * M::TPS, Sh[s], Sl[s]);
-      if constexpr (OUT == kHelped) *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
-    }
+    for (int s = 0; s < SS; ++s) M::split(S + s * M::TPS, Sh[s], Sl[s]);
     if constexpr (OUT == kKeep) {
       put_state<T, SS>(Sh, (T*)states + (slot * p.dv + col) * p.dk, p.dk, col < p.dv);
     }
@@ -409,18 +464,28 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
         for (int s = 0; s < SS; ++s) e[t] = mma_split<T>(Kf[0][s], Sh[s], Sl[s], e[t]);
       }
     }
+    const char *td = st + G::kRec + ChunkRec<T>::diag(lane), *tf = st + G::kRec + lane * 16;
 #pragma unroll
-    for (int f = 0; f < M::kTri; ++f) {
-      Th[f] = *reinterpret_cast<const u32x4*>(st + G::kRec + f * 1024 + lane * 16);
-      if (M::kSplit) Tl[f] = *reinterpret_cast<const u32x4*>(st + G::kRec + ChunkRec<T>::kTl + f * 1024 + lane * 16);
-    }
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int s = 0; s < M::steps(t); ++s) {
+        Th[M::tri(t, s)] = ChunkRec<T>::frag(td, tf, t, s);
+        if (M::kSplit) Tl[M::tri(t, s)] = ChunkRec<T>::frag(td + ChunkRec<T>::kTl, tf + ChunkRec<T>::kTl, t, s);
+      }
     u32x4 Kt[G::kHoist ? ST : 1][CS];
-    if constexpr (G::kHoist)
+    if constexpr (G::kHoist && !G::kLateK)
 #pragma unroll
       for (int t = 0; t < ST; ++t)
 #pragma unroll
         for (int s = 0; s < CS; ++s) Kt[t][s] = Panels<T>::frag_t(st + G::kK, t, s, lane);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (OUT == kHelped) {                          // behind the reads, which are waited for first
+#pragma unroll
+      for (int s = 0; s < SS; ++s) {
+        *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
+        if (G::kLo) *reinterpret_cast<u32x4*>(swap + (SS + s) * 1024) = Sl[s];
+      }
+    }
 #pragma unroll
     for (int t = 0; t < ST; ++t) S[t] *= decay;
 #pragma unroll
@@ -443,17 +508,24 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
           }
     if constexpr (OUT == kHelped) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(swap + SS * 1024 + t * 1024) = e[t];
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(swap + G::kSwapE + t * 1024) = e[t];
     } else if constexpr (OUT == kOwn) {
       const char* sq = smem + G::kG + c % STAGES * G::kStageQ;
       const int len = min(kDC, sp.len - c * kDC), col0 = (at.part * NW + w) * 16 + g * 4;
       T* o = (T*)p.O + sp.b * p.so.b + h * p.so.h + (int64_t)(sp.tok0 + c * kDC) * p.so.t + col0;
-      make_outputs<T, SS>(Sh, e, sq, sq + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o);
+      make_outputs<T, SS, G::kLo>(Sh, Sl, e, sq, sq + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o);
     } else {
       T* E = (T*)errors + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
 #pragma unroll
       for (int s = 0; s < CS; ++s)
         if (col < p.dv) *reinterpret_cast<u32x4*>(E + s * M::KB) = M::frag(e + s * M::TPS);
+    }
+    if constexpr (G::kHoist && G::kLateK) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int s = 0; s < CS; ++s) Kt[t][s] = Panels<T>::frag_t(st + G::kK, t, s, lane);
     }
     // S = exp(b_63) S + K^T (exp(b_63 - b) beta E)
 #pragma unroll
@@ -501,13 +573,16 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec
     const char* swap = smem + G::kSwap + ((c & 1) * NW + w) * G::kSwapBytes + lane * 16;
     const char* st = smem + G::kG + c % STAGES * G::kStageQ;
     const char* gp = QLDS ? st : rec0 + c * rstep;           // gates, P
-    u32x4 Sh[SS];
+    u32x4 Sh[SS], Sl[SS];
 #pragma unroll
-    for (int s = 0; s < SS; ++s) Sh[s] = *reinterpret_cast<const u32x4*>(swap + s * 1024);
+    for (int s = 0; s < SS; ++s) {
+      Sh[s] = *reinterpret_cast<const u32x4*>(swap + s * 1024);
+      if (G::kLo) Sl[s] = *reinterpret_cast<const u32x4*>(swap + (SS + s) * 1024);
+    }
     f32x4 e[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) e[t] = *reinterpret_cast<const f32x4*>(swap + SS * 1024 + t * 1024);
-    make_outputs<T, SS, QLDS>(Sh, e, gp, st + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o0 + (int64_t)c * kDC * p.so.t,
+    for (int t = 0; t < 4; ++t) e[t] = *reinterpret_cast<const f32x4*>(swap + G::kSwapE + t * 1024);
+    make_outputs<T, SS, G::kLo, QLDS>(Sh, Sl, e, gp, st + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o0 + (int64_t)c * kDC * p.so.t,
                               q0 + (int64_t)c * kDC * p.sq.t, qp, qrow);
   }
 }

@@ -136,3 +136,21 @@ def test_step_of_many_rows(R, P, dtype):
     # corrections shrink; the longest run here is R / 2 rows (513 rows on 2 states), whose decays are e^-0.5 on average:
     # less than 3 rows' roundings remain
     assert rel(W, Wr) <= 3 * TOL_STEP[torch.float32]
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("Hk,Hv,n,dk,dv", [(2, 4, 300, 128, 128), (1, 3, 200, 64, 72), (2, 2, 130, 96, 80), (1, 2, 700, 128, 136)])
+def test_outputs_are_off_by_their_own_rounding(Hk, Hv, n, dk, dv, full):
+    """With heads of up to 128, what O is made of is off by no more than the state (test_gpu_delta: c = 2 sqrt(5) 2^-16 of
+    its norm), so O is the oracle's rounded to bf16 but where that little moves a value past the middle between two bf16
+    numbers: with a share e / u of the values, e the error and u <= 2^-7 of the value a step, which moves them by u.  The
+    squares of those moves add up to sum(e u) <= c 2^-7 of O's squares: sqrt(c 2^-7), 7.3e-4, of its norm.  `full`: as a
+    row of a batch whose state waves make O themselves."""
+    B = -(-520 // Hv) if full else 1
+    args = make(B, Hk, Hv, n, dk, dv, torch.bfloat16, seed=71)
+    W0 = torch.randn(B, Hv, dv, dk, generator=torch.Generator().manual_seed(72)).mul(0.3).cuda()
+    O, _ = cw.ttt_gated_delta(*args, W_init=W0)
+    Or, _ = od.delta_rule(*(f64(t[0]) for t in args), dk ** -0.5, f64(W0[0]))
+    err = rel(O[0], f64(torch.from_numpy(Or).bfloat16()))
+    print("from the rounded oracle", err, flush=True)
+    assert err <= (TOL_W[torch.bfloat16] * 2.0 ** -7) ** 0.5
