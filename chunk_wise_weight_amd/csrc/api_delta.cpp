@@ -217,7 +217,8 @@ int ttt_gated_delta_backward(const ttt_delta_shape* shape, int dtype, float scal
     return TTT_ERR_ARG;
   a.gates_f32 = l && l->gates_f32;
   const size_t gate = a.gates_f32 ? 4 : esize(dtype);
-  if (B * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, gate) || !ok_ptr(dbeta, gate)))
+  if (B * n > 0 && (!ok_ptr(dO) || !ok_ptr(dq) || !ok_ptr(dk) || !ok_ptr(dv) || !ok_ptr(dg, gate) ||
+                    !ok_ptr(dbeta, gate)))
     return TTT_ERR_ARG;
   if (!aligned(dW_final, 16) || !aligned(dW_init, 16)) return TTT_ERR_ARG;
   size_t need = 0;

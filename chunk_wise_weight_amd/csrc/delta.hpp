@@ -114,7 +114,8 @@ __device__ __forceinline__ f32x4 mma_split(u32x4 a, u32x4 bh, u32x4 bl, f32x4 c)
 // (fragment, lane, 16 bytes): T (hi, then lo), the gates, P (hi, then lo).  In
 // bf16 a fragment on the diagonal is zero in the lanes whose 8 columns lie
 // behind their row (lane group g > (lane & 15) >> 2): it is kept as its 40
-// other lanes, group by group, and 16 bytes of zeros for those.
+// other lanes, dealt such that the lanes that LDS serves together (0-3 and 12-15
+// of a group with 4-11 of the next) lie in different banks, and 16 bytes of zeros.
 template <typename T> struct ChunkRec {
   static constexpr bool kPacked = sizeof(T) == 2;
   static constexpr int kDiag = 41 * 16;
@@ -128,7 +129,14 @@ template <typename T> struct ChunkRec {
   // A lane's place in the fragments of a part: on the diagonal, elsewhere.
   __device__ static __forceinline__ int diag(int lane) {
     const int g = lane >> 4, m = lane & 15;
-    return kPacked ? (g <= m >> 2 ? m + 14 * g - 2 * g * g : 40) * 16 : lane * 16;
+    if (!kPacked) return lane * 16;
+    return (g > m >> 2 ? 40 : g == 0 ? m : g == 1 ? 16 + m : g == 2 ? 32 + ((m & 7) ^ 4) : 4 + m) * 16;
+  }
+  // The same for a loop over chunks: kept in a register, not made again at every turn.
+  __device__ static __forceinline__ int diag_kept(int lane) {
+    int d = diag(lane);
+    asm volatile("" : "+v"(d));
+    return d;
   }
   // Where fragment (t, s) is in a part, from the lane's place on.
   __device__ static constexpr bool on_diag(int t, int s) { return kPacked && s == t >> 1; }

@@ -32,8 +32,10 @@
 // 1.7e-3, which is its own rounding; dq and dk 2.7e-3 to 3.2e-3; dg and dbeta
 // 2e-3 to 4e-3 over a hundred tokens or more, but up to 6e-3 and 1.3e-2 over a
 // sequence of a few, where a gate's gradient is a handful of dots of those
-// roundings that cancel in part.  Pairs in memory would write and read twice the
-// 400 MB that S, dS', E and X are at the size below, 160 us at a copy's rate.
+// roundings that cancel in part.  Of dq's and dk's error that of E and that of
+// Mq and Mk are the larger parts, of dg's that of S and dS' under weak decays;
+// X's matters little.  Pairs in memory would write and read twice the 400 MB that
+// S, dS', E and X are at the size below, 160 us at a copy's rate.
 //
 // Workspace (delta_grad_workspace_bytes): 140 KB a chunk and value head of 128 x
 // 128 in bf16: 44 KB of records, 64 of S and dS', 32 of E and X.

@@ -64,8 +64,8 @@ __device__ __forceinline__ void put_triangle(const float* X, char* hi, char* lo)
       if (i < 4 * 41) {                                    // on the diagonal; diag()'s inverse
         t = i / 41;
         s = t >> 1;
-        const int p = i - t * 41, g = p < 16 ? 0 : p < 28 ? 1 : p < 36 ? 2 : 3;
-        lane = g * 16 + p - 14 * g + 2 * g * g;
+        const int p = i - t * 41;
+        lane = p < 16 ? p : p < 20 ? 48 + p - 4 : p < 32 ? p : 32 + 8 + ((p - 32) ^ 4);
         if (p == 40) {                                     // the zeros: four rows' columns behind the diagonal
           t &= 2;
           lane = 48;
@@ -248,20 +248,19 @@ __device__ __forceinline__ void put_state(const u32x4 (&S)[SS], T* W, int dk, bo
 // O of a chunk's tokens at 16 columns, from operands of the state (Sl: what Sh
 // leaves, LO) and the errors (fp32): the columns in the instruction's rows,
 // tokens in its columns, so that a lane gets 4 columns of one token.  gp: the
-// chunk's gates and P; Q in panels at q, or from memory through rq.
-template <typename T, int SS, bool LO, bool QLDS = true>
+// chunk's gates and P, diag: the lane's place in P; Q in panels at q, or from memory through rq.
+template <typename T, int SS, bool LO, int TB, bool QLDS = true>
 __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const u32x4 (&Sl)[SS], const f32x4 (&e)[4],
-                                             const char* gp, const char* q, float scale, int len, bool in, int64_t pitch, T* out,
-                                             const void* q_rows = nullptr, unsigned qp = 0, unsigned qrow = 0) {
+                                             const char* gp, int diag, const char* q, float scale, int len, bool in,
+                                             int64_t pitch, T* out, const void* q_rows = nullptr, unsigned qp = 0, unsigned qrow = 0) {
   using M = Mat<T>;
   constexpr int CS = kDC / M::KB;
   const int lane = lane_id(), m = lane & 15, g = lane >> 4;
   u32x4 Eh[CS], El[CS];
 #pragma unroll
   for (int s = 0; s < CS; ++s) M::split(e + s * M::TPS, Eh[s], El[s]);
-  constexpr int TB = M::kSplit ? 2 : 1;     // blocks of tokens at a time, whose sums do not wait for each other
   using R = ChunkRec<T>;
-  const char *pd = gp + R::kP - R::kGate + R::diag(lane), *pf = gp + R::kP - R::kGate + lane * 16;
+  const char *pd = gp + R::kP - R::kGate + diag, *pf = gp + R::kP - R::kGate + lane * 16;
 #pragma unroll
   for (int t0 = 0; t0 < 4; t0 += TB) {
     f32x4 o[TB];
@@ -278,7 +277,8 @@ __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const u32x4 
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
           const unsigned byte = s * 64u + g * 16u;
-          f[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rq, r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB, 0, 0);
+          const unsigned at = r < len && byte < qrow ? (unsigned)r * qp + byte : kOOB;
+          f[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rq, at, 0, 0);
         }
       }
     }
@@ -326,8 +326,7 @@ __device__ __forceinline__ void make_outputs(const u32x4 (&Sh)[SS], const u32x4 
 // instructions, 1.33 us with every load taken out; that bounds the walk.  One
 // barrier a chunk.  By OUT:
 //   kHelped  as many helper waves, one chunk behind, make O from the state and
-//            the errors that the state waves left in LDS (after their own reads
-//            from it, which they wait for), their Q and P coming
+//            the errors that the state waves left in LDS, their Q and P coming
 //            with the DMA too where there is room, else straight from memory:
 //            the shortest chain, for walks that do not fill the chip
 //   kOwn     the state waves make O themselves: four of them to a workgroup,
@@ -349,6 +348,11 @@ template <typename T, int DK, int NW, int STAGES, int OUT, bool QLDS> struct Wal
   static constexpr int kSmem = kSwap + (OUT == kHelped ? 2 * NW * kSwapBytes : 0);
   static constexpr int kThreads = 64 * (2 + NW * (OUT == kHelped ? 2 : 1));   // kKeep: with one DMA wave, 64 fewer
   static constexpr int kLag = OUT == kHelped ? 1 : 0;      // turns that O is behind
+  // Blocks of 16 tokens that O's sums go by at a time, so that they (and loads of Q from memory) do not wait for each
+  // other.  1, 2, 4 blocks: helped, bf16 128 x 128, 64K tokens of 32 heads 1.70, 1.73, 1.68 ms; own, 64 x 64, 8 x 2K
+  // 74, 71, 73 us; Q from memory, 4096 tokens of 8 fp32 heads of 256 x 512 2.02, 1.84, 1.73 ms; of 16 of 128 526, 439,
+  // 488 us.
+  static constexpr int kTB = QLDS ? (!Mat<T>::kSplit ? 1 : OUT == kHelped ? 4 : 2) : DK > 128 ? 4 : 2;
   static constexpr bool kHoist = SS <= 4;                  // whether a chunk's operands fit in registers
   static constexpr bool kLateK = OUT == kOwn && kLo;       // K^T's only behind O, which needs the state's low parts
 };
@@ -377,7 +381,8 @@ __device__ __forceinline__ void walk_loads(const DeltaArgs& p, int parts, const 
       if (c < chunks) {
         kload.issue(k0 + (int64_t)c * kDC * p.sk.t, len, st + G::kK);
       }
-      if (out) load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, sq, ChunkRec<T>::kBytes - ChunkRec<T>::kGate);
+      if (out)
+        load_block<G::kQ / 1024>(rec0 + d * rstep + ChunkRec<T>::kGate, sq, ChunkRec<T>::kBytes - ChunkRec<T>::kGate);
     }
     if (parts & 2) {
       if (c < chunks) {
@@ -412,6 +417,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
     if (resumed && d < p.dk && col < p.dv) S[t] = *reinterpret_cast<const f32x4*>(p.W_init + wbase + d);
   }
 
+  const int diag = ChunkRec<T>::diag_kept(lane);
   for (int c = 0; c < chunks; ++c) {
     const char* st = smem + c % STAGES * G::kStage;
     next_turn<STAGES>(c == 0);
@@ -464,7 +470,15 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
         for (int s = 0; s < SS; ++s) e[t] = mma_split<T>(Kf[0][s], Sh[s], Sl[s], e[t]);
       }
     }
-    const char *td = st + G::kRec + ChunkRec<T>::diag(lane), *tf = st + G::kRec + lane * 16;
+    // Behind K's reads, under the products: before them 16K tokens of 32 heads take 449 us instead of 432.
+    if constexpr (OUT == kHelped) {
+#pragma unroll
+      for (int s = 0; s < SS; ++s) {
+        *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
+        if (G::kLo) *reinterpret_cast<u32x4*>(swap + (SS + s) * 1024) = Sl[s];
+      }
+    }
+    const char *td = st + G::kRec + diag, *tf = st + G::kRec + lane * 16;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -479,13 +493,6 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
 #pragma unroll
         for (int s = 0; s < CS; ++s) Kt[t][s] = Panels<T>::frag_t(st + G::kK, t, s, lane);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (OUT == kHelped) {                          // behind the reads, which are waited for first
-#pragma unroll
-      for (int s = 0; s < SS; ++s) {
-        *reinterpret_cast<u32x4*>(swap + s * 1024) = Sh[s];
-        if (G::kLo) *reinterpret_cast<u32x4*>(swap + (SS + s) * 1024) = Sl[s];
-      }
-    }
 #pragma unroll
     for (int t = 0; t < ST; ++t) S[t] *= decay;
 #pragma unroll
@@ -513,7 +520,7 @@ __device__ __forceinline__ void walk_states(const DeltaArgs& p, int w, void* sta
       const char* sq = smem + G::kG + c % STAGES * G::kStageQ;
       const int len = min(kDC, sp.len - c * kDC), col0 = (at.part * NW + w) * 16 + g * 4;
       T* o = (T*)p.O + sp.b * p.so.b + h * p.so.h + (int64_t)(sp.tok0 + c * kDC) * p.so.t + col0;
-      make_outputs<T, SS, G::kLo>(Sh, Sl, e, sq, sq + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o);
+      make_outputs<T, SS, G::kLo, G::kTB>(Sh, Sl, e, sq, diag, sq + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o);
     } else {
       T* E = (T*)errors + (slot * p.dv + col) * kDC + g * (16 / (int)sizeof(T));
 #pragma unroll
@@ -566,6 +573,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec
   T* o0 = (T*)p.O + sp.b * p.so.b + h * p.so.h + sp.tok0 * p.so.t + col0;
   const char* rec0 = rec + ((int64_t)sp.slot0 * p.Hv + h) * ChunkRec<T>::kBytes + ChunkRec<T>::kGate;
   const int64_t rstep = (int64_t)p.Hv * ChunkRec<T>::kBytes;
+  const int diag = ChunkRec<T>::diag_kept(lane);
   if (chunks > 0) next_turn<STAGES>(true);
   for (int c = 0; c < chunks; ++c) {
     next_turn<STAGES>(false);
@@ -582,8 +590,8 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& p, const char* rec
     f32x4 e[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) e[t] = *reinterpret_cast<const f32x4*>(swap + G::kSwapE + t * 1024);
-    make_outputs<T, SS, G::kLo, QLDS>(Sh, Sl, e, gp, st + G::kQ, p.scale, len, col0 < p.dv, p.so.t, o0 + (int64_t)c * kDC * p.so.t,
-                              q0 + (int64_t)c * kDC * p.sq.t, qp, qrow);
+    make_outputs<T, SS, G::kLo, G::kTB, QLDS>(Sh, Sl, e, gp, diag, st + G::kQ, p.scale, len, col0 < p.dv, p.so.t,
+                                              o0 + (int64_t)c * kDC * p.so.t, q0 + (int64_t)c * kDC * p.sq.t, qp, qrow);
   }
 }
 
