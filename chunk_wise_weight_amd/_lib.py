@@ -978,7 +978,8 @@ def ttt_gated_delta_step(q, k, v, g, beta, W, slots=None, scale=None, O=None):
     """One token of the gated delta rule for each row of a serving batch.  q, k [rows, Hk, dk], v [rows, Hv, dv] of
     one dtype, g, beta [rows, Hv] fp32; W [states, Hv, dv, dk] fp32 is the pool of states, updated in place; slots
     [rows] int32 on the device names each row's state (a slot outside the pool, such as -1: a padding row, whose
-    output is zero; rows of one slot go in row order; None: row r's state is W[r]).  Returns O [rows, Hv, dv]."""
+    output is zero; rows of one slot go in row order; at most 65536 rows; None: row r's state is W[r]).  Returns O
+    [rows, Hv, dv]."""
     (R, Hk, dk), (_, Hv, dv), P = q.shape, v.shape, W.shape[0]
     dt, dev = q.dtype, q.device
     _need(q, "q", (R, Hk, dk), dt, dev)
