@@ -21,10 +21,11 @@
 // registers is a pair hi + lo of bf16 values (2^-17 relative), with hi x hi,
 // hi x lo and lo x hi summed in fp32: the fp32 state is off by 3e-6 of its norm
 // after 64K tokens, and O by its own rounding (1.7e-3; from the exact O rounded,
-// 1e-4 to 2e-4).  A third bf16 value a number would bring the state closer to
-// fp32's own error at 44 products and 160 vector instructions more in a chunk's
-// chain of 82 and 250; two keep it hundreds of times closer than the bf16 inputs
-// are to what they stand for.  One operand is rounded once: the state in Q S for heads past 128,
+// 1e-4 to 2e-4).  Of the state's 3e-6 nearly all comes from the two operands of T
+// R and K^T E; a third bf16 value for those would leave 8e-7 (emulated in fp64) at
+// 22 products and 80 vector instructions more in a chunk's chain of 82 and 250.
+// Two keep it hundreds of times closer than the bf16 inputs are to what they
+// stand for.  One operand is rounded once: the state in Q S for heads past 128,
 // whose pairs LDS has no room for (O off by up to 2.2e-3, where decays are weak).
 #pragma once
 #include <type_traits>
