@@ -98,6 +98,31 @@ class DeltaOptions(ctypes.Structure):
                 ("layout", ctypes.POINTER(DeltaLayout))]
 
 
+class ConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seq_len", "dim", "taps")]
+
+
+class RowStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "token")]
+
+
+class ConvLayout(ctypes.Structure):
+    _fields_ = [(n, RowStrides) for n in ("x", "y")]
+
+
+class ConvGradLayout(ctypes.Structure):
+    _fields_ = [(n, RowStrides) for n in ("dy", "dx")]
+
+
+class ConvOptions(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("silu", ctypes.c_int), ("x_init", ctypes.c_void_p),
+                ("seq_starts", ctypes.c_void_p), ("num_seqs", ctypes.c_int64), ("layout", ctypes.POINTER(ConvLayout))]
+
+
+class ScanStepShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "states", "heads", "groups", "head_dim", "state")]
+
+
 class TTTError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)}")
@@ -162,6 +187,15 @@ _SIGNATURES = {
     "ttt_layer_norm": (_I, [ctypes.c_int64, ctypes.c_int64, _I, _F] + [_P] * 7),
     "ttt_layer_norm_backward_workspace_bytes": (_I, [ctypes.c_int64, ctypes.c_int64, _I, ctypes.POINTER(_S)]),
     "ttt_layer_norm_backward": (_I, [ctypes.c_int64, ctypes.c_int64, _I] + [_P] * 9 + [_S, _P]),
+    "ttt_rms_norm": (_I, [ctypes.c_int64, ctypes.c_int64, _I, _F] + [_P] * 7 + [ctypes.c_int64, _P]),
+    "ttt_rms_norm_backward_workspace_bytes": (_I, [ctypes.c_int64, ctypes.c_int64, _I, ctypes.POINTER(_S)]),
+    "ttt_rms_norm_backward": (_I, [ctypes.c_int64, ctypes.c_int64, _I] + [_P] * 8 + [_S, _P]),
+    "ttt_short_conv": (_I, [ctypes.POINTER(ConvShape), _I, _P, _P, ctypes.POINTER(ConvOptions), _P, _P, _P]),
+    "ttt_short_conv_backward_workspace_bytes": (_I, [ctypes.POINTER(ConvShape), _I, ctypes.c_int64, ctypes.POINTER(_S)]),
+    "ttt_short_conv_backward": (_I, [ctypes.POINTER(ConvShape), _I] + [_P] * 4 + [ctypes.POINTER(ConvOptions),
+                                     ctypes.POINTER(ConvGradLayout)] + [_P] * 5 + [_S, _P]),
+    "ttt_short_conv_step": (_I, [ctypes.c_int64] * 4 + [_I, _I] + [_P] * 7),
+    "ttt_selective_scan_step": (_I, [ctypes.POINTER(ScanStepShape), _I] + [_P] * 7 + [_I] + [_P] * 4),
 }
 
 _lib = None
@@ -1057,3 +1091,240 @@ def ttt_layer_norm_backward(x, weight, dY, mean, rstd, bias=True, dx=None, dweig
     _launch(dev, "ttt_layer_norm_backward", lib().ttt_layer_norm_backward, rows, d, _dt(dt), _at(x), _at(weight), _at(dY),
             _at(mean), _at(rstd), _at(dx), _at(dweight), _at(dbias), _at(ws), nbytes)
     return dx, dweight, dbias
+
+
+# -------------------------------------------------- root-mean-square norm, short convolution, selective scan
+
+
+def ttt_rms_norm(x, weight=None, residual=None, eps=1e-5, out_dtype=None, group=None, Y=None, H=None, rstd=None,
+                 scale=None):
+    """Root-mean-square norm over the last index of H = x + residual (x where residual is None), x [..., d]
+    (contiguous), weight [d] of x's dtype or None.  Returns (Y, H, rstd [...] fp32, scale).
+
+    out_dtype None: Y of x's dtype, scale None.  torch.float8_e4m3fn: Y = H rstd weight / scale in 8 bits, scale [...]
+    fp32 the largest |H rstd weight| of a row over 448, or, with group 32, 64 or 128, [..., ceil(d / group)] that of
+    each group of columns; at least 2^-126."""
+    shape, dt, dev = x.shape, x.dtype, x.device
+    d, lead = shape[-1], shape[:-1]
+    _need(x, "x", shape, dt, dev)
+    _norm_vector(weight, "weight", d, dt, dev)
+    if residual is not None:
+        _need(residual, "residual", shape, dt, dev)
+        H = torch.empty_like(x) if H is None else H
+        _need(H, "H", shape, dt, dev)
+    bits8 = out_dtype is not None and out_dtype != dt
+    if bits8 and out_dtype != torch.float8_e4m3fn:
+        raise TypeError(f"out_dtype must be {dt} or float8_e4m3fn, got {out_dtype}")
+    if group is not None and (not bits8 or group not in (32, 64, 128)):
+        raise ValueError(f"group must be 32, 64 or 128, and is of 8-bit outputs, got {group}")
+    Y = torch.empty(shape, dtype=out_dtype if bits8 else dt, device=dev) if Y is None else Y
+    _need(Y, "Y", shape, out_dtype if bits8 else dt, dev)
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
+    _need(rstd, "rstd", lead, torch.float32, dev)
+    if bits8:
+        scales = lead if group is None else (*lead, -(-d // group))
+        scale = torch.empty(scales, dtype=torch.float32, device=dev) if scale is None else scale
+        _need(scale, "scale", scales, torch.float32, dev)
+    elif scale is not None:
+        raise ValueError("scale is of 8-bit outputs")
+    _launch(dev, "ttt_rms_norm", lib().ttt_rms_norm, rstd.numel(), d, _dt(dt), float(eps), _at(x), _at(residual),
+            _at(weight), _at(H) if residual is not None else None, _at(Y), _at(rstd), _at(scale), group or 0)
+    return Y, x if residual is None else H, rstd, scale
+
+
+@functools.lru_cache(maxsize=256)
+def ttt_rms_norm_backward_workspace_bytes(rows: int, dim: int, dtype: torch.dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_rms_norm_backward_workspace_bytes(int(rows), int(dim), _dt(dtype), ctypes.byref(out)),
+           "ttt_rms_norm_backward_workspace_bytes")
+    return out.value
+
+
+def ttt_rms_norm_backward(H, weight, dY, rstd, dH=None, dx=None, dweight=None, workspace=None):
+    """Backward of ttt_rms_norm (Y of x's dtype) given its H and rstd; dH, if not None, is what comes back to H from its
+    other uses.  Returns (dx like H, the gradient of x and of the residual, dweight [d] fp32 or None where weight is
+    None)."""
+    shape, dt, dev = H.shape, H.dtype, H.device
+    d, lead = shape[-1], shape[:-1]
+    _need(H, "H", shape, dt, dev)
+    _need(dY, "dY", shape, dt, dev)
+    _norm_vector(weight, "weight", d, dt, dev)
+    _need(rstd, "rstd", lead, torch.float32, dev)
+    if dH is not None:
+        _need(dH, "dH", shape, dt, dev)
+    dx = torch.empty_like(H) if dx is None else dx
+    _need(dx, "dx", shape, dt, dev)
+    if weight is not None and dweight is None:
+        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+    _norm_vector(dweight, "dweight", d, torch.float32, dev)
+    rows = rstd.numel()
+    nbytes = ttt_rms_norm_backward_workspace_bytes(rows, d, dt)
+    ws = _workspace(nbytes, dev, workspace)
+    _launch(dev, "ttt_rms_norm_backward", lib().ttt_rms_norm_backward, rows, d, _dt(dt), _at(H), _at(weight), _at(dY),
+            _at(rstd), _at(dH), _at(dx), _at(dweight), _at(ws), nbytes)
+    return dx, dweight
+
+
+def _rows(meta, name, shape, dtype, out=False) -> RowStrides:
+    """Checks a [B, n, d] tensor of any batch and token strides, and gives them.  Outputs must not hold two elements at
+    one place."""
+    size, st, dt = meta
+    if size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {shape}")
+    if dt != dtype:
+        raise TypeError(f"{name} has dtype {dt}, expected {dtype}")
+    if 0 not in shape:
+        if st[2] != 1 and shape[2] > 1:
+            raise ValueError(f"{name}'s last index must be contiguous (strides {st})")
+        reach = shape[2]
+        for s, n in sorted((s, n) for s, n in zip(st[:2], shape) if n > 1):
+            if out and s < reach:
+                raise ValueError(f"{name} is written and must not overlap itself (strides {st})")
+            reach = s * n
+    return RowStrides(*(s if n > 1 else 0 for s, n in zip(st[:2], shape)))
+
+
+def _conv_shape(x, w):
+    if len(x[0]) != 3 or len(w[0]) != 2:
+        raise ValueError(f"x is [B, n, d] and conv_w [d, K], got {tuple(x[0])} and {tuple(w[0])}")
+    return ConvShape(*x[0], w[0][1])
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_plan(x, w, Y, num):
+    """(byref of ConvShape, its dtype code, ConvLayout, x_final's shape) of a forward call."""
+    shape = _conv_shape(x, w)
+    layout = ConvLayout(_rows(x, "x", tuple(x[0]), x[2]), _rows(Y, "Y", tuple(x[0]), x[2], out=True))
+    return ctypes.byref(shape), _dt(x[2]), layout, (shape.batch if num < 0 else num, max(shape.taps - 1, 0), shape.dim)
+
+
+def _conv_vectors(conv_w, bias, d, dt, dev):
+    _need(conv_w, "conv_w", (d, conv_w.shape[-1]), dt, dev)
+    _norm_vector(bias, "bias", d, dt, dev)
+
+
+def ttt_short_conv(x, conv_w, bias=None, silu=True, x_init=None, seq_starts=None, Y=None, x_final=None):
+    """Causal depthwise convolution over the tokens, with SiLU unless silu is False: z_t = bias + sum_j conv_w[:, j]
+    x_{t-K+1+j}.  Returns (Y [B, n, d], x_final [sequences, K - 1, d], each sequence's last K - 1 rows).
+
+    x [B, n, d] of any batch and token strides (Y, if not given, is contiguous), conv_w [d, K] (K in 1..8) and bias [d]
+    of its dtype.  x_init [sequences, K - 1, d]: the rows before each sequence's first (an earlier call's x_final; zero
+    if None).  seq_starts, an int32 device tensor [sequences + 1]: packed sequences in one batch row; tokens that belong
+    to none are not read and their rows of Y are left as they are."""
+    dev, dt = x.device, x.dtype
+    _conv_vectors(conv_w, bias, x.shape[-1], dt, dev)
+    num = _seq_starts(seq_starts, x.shape[0], dev)
+    Y = torch.empty(x.shape, dtype=dt, device=dev) if Y is None else Y
+    shape, code, layout, halo = _conv_plan(_meta(x, "x", dev, False), _meta(conv_w, "conv_w", dev, False),
+                                           _meta(Y, "Y", dev, False), num)
+    if x_init is not None:
+        _need(x_init, "x_init", halo, dt, dev)
+    x_final = torch.empty(halo, dtype=dt, device=dev) if x_final is None else x_final
+    _need(x_final, "x_final", halo, dt, dev)
+    opts = ConvOptions(_at(bias), bool(silu), _at(x_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
+    _launch(dev, "ttt_short_conv", lib().ttt_short_conv, shape, code, _at(x), _at(conv_w), ctypes.byref(opts), _at(Y),
+            _at(x_final))
+    return Y, x_final
+
+
+def ttt_short_conv_backward_workspace_bytes(shape: ConvShape, dtype: torch.dtype, num_seqs: int = -1) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_short_conv_backward_workspace_bytes(ctypes.byref(shape), _dt(dtype), int(num_seqs),
+                                                         ctypes.byref(out)), "ttt_short_conv_backward_workspace_bytes")
+    return out.value
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_backward_plan(x, w, dY, dx, num):
+    shape, size, dt = _conv_shape(x, w), tuple(x[0]), x[2]
+    layout = ConvLayout(_rows(x, "x", size, dt), RowStrides())
+    grads = ConvGradLayout(_rows(dY, "dY", size, dt), _rows(dx, "dx", size, dt, out=True))
+    return (ctypes.byref(shape), _dt(dt), layout, grads, ttt_short_conv_backward_workspace_bytes(shape, dt, num),
+            (shape.batch if num < 0 else num, max(shape.taps - 1, 0), shape.dim))
+
+
+def ttt_short_conv_backward(x, conv_w, dY, bias=None, silu=True, x_init=None, seq_starts=None, dx_final=None, dx=None,
+                            dconv_w=None, dbias=None, dx_init=None, workspace=None):
+    """Backward of ttt_short_conv from its inputs, dY [B, n, d] and, where the loss depends on x_final too, dx_final.
+    Returns (dx [B, n, d], dconv_w [d, K] fp32, dbias [d] fp32 (None without bias, unless given), dx_init [sequences,
+    K - 1, d] (None without x_init, unless given)).  Rows of tokens that belong to no sequence are left as they are."""
+    dev, dt = x.device, x.dtype
+    _conv_vectors(conv_w, bias, x.shape[-1], dt, dev)
+    num = _seq_starts(seq_starts, x.shape[0], dev)
+    dx = torch.empty(x.shape, dtype=dt, device=dev) if dx is None else dx
+    shape, code, layout, grads, nbytes, halo = _conv_backward_plan(
+        _meta(x, "x", dev, False), _meta(conv_w, "conv_w", dev, False), _meta(dY, "dY", dev, False),
+        _meta(dx, "dx", dev, False), num)
+    if x_init is not None and dx_init is None:
+        dx_init = torch.empty(halo, dtype=dt, device=dev)
+    for t, name in ((x_init, "x_init"), (dx_final, "dx_final"), (dx_init, "dx_init")):
+        if t is not None:
+            _need(t, name, halo, dt, dev)
+    dconv_w = torch.empty(conv_w.shape, dtype=torch.float32, device=dev) if dconv_w is None else dconv_w
+    _need(dconv_w, "dconv_w", conv_w.shape, torch.float32, dev)
+    if bias is not None and dbias is None:
+        dbias = torch.empty(bias.shape, dtype=torch.float32, device=dev)
+    _norm_vector(dbias, "dbias", x.shape[-1], torch.float32, dev)
+    ws = _workspace(nbytes, dev, workspace)
+    opts = ConvOptions(_at(bias), bool(silu), _at(x_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
+    _launch(dev, "ttt_short_conv_backward", lib().ttt_short_conv_backward, shape, code, _at(x), _at(conv_w), _at(dY),
+            _at(dx_final), ctypes.byref(opts), ctypes.byref(grads), _at(dx), _at(dconv_w), _at(dbias), _at(dx_init),
+            _at(ws), nbytes)
+    return dx, dconv_w, dbias, dx_init
+
+
+def ttt_short_conv_step(x, conv_w, halo, bias=None, silu=True, slots=None, Y=None):
+    """One token of the short convolution for each row of a serving batch.  x [rows, d], conv_w [d, K], bias [d] of one
+    dtype; halo [states, K - 1, d] is the pool of earlier rows, moved on in place; slots [rows] int32 on the device
+    names each row's (a slot outside the pool, such as -1: a padding row, whose output is zero; rows of one slot go in
+    row order; at most 65536 rows; None: row r's is halo[r]).  Returns Y [rows, d]."""
+    (R, d), (P, K1, _), dt, dev = x.shape, halo.shape, x.dtype, x.device
+    _need(x, "x", (R, d), dt, dev)
+    _need(conv_w, "conv_w", (d, K1 + 1), dt, dev)
+    _norm_vector(bias, "bias", d, dt, dev)
+    _need(halo, "halo", (P, K1, d), dt, dev)
+    if slots is not None:
+        _need(slots, "slots", (R,), torch.int32, dev)
+    if Y is None:
+        Y = torch.empty_like(x)
+    else:
+        _need(Y, "Y", (R, d), dt, dev)
+    _launch(dev, "ttt_short_conv_step", lib().ttt_short_conv_step, R, P, d, K1 + 1, _dt(dt), bool(silu), _at(x),
+            _at(conv_w), _at(bias), _at(halo), _at(slots), _at(Y))
+    return Y
+
+
+def _scan_heads(A, D, dt_bias, H, dev):
+    _need(A, "A", (H,), torch.float32, dev)
+    _norm_vector(D, "D", H, torch.float32, dev)
+    _norm_vector(dt_bias, "dt_bias", H, torch.float32, dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_step_shape(*sizes):
+    return ctypes.byref(ScanStepShape(*sizes))
+
+
+def ttt_selective_scan_step(x, dt, A, B, C, S, D=None, dt_bias=None, softplus=False, slots=None, O=None):
+    """One token of the selective scan for each row of a serving batch.  x [rows, H, P], B, C [rows, G, N] of one dtype,
+    dt [rows, H], A, D, dt_bias [H] fp32; S [states, H, P, N] fp32 is the pool of states, updated in place; slots
+    [rows] int32 on the device names each row's state (a slot outside the pool, such as -1: a padding row, whose output
+    is zero; rows of one slot go in row order; at most 65536 rows; None: row r's state is S[r]).  Returns O [rows, H,
+    P]."""
+    (R, H, P), (_, G, N), pool = x.shape, B.shape, S.shape[0]
+    t, dev = x.dtype, x.device
+    _need(x, "x", (R, H, P), t, dev)
+    _need(dt, "dt", (R, H), torch.float32, dev)
+    _scan_heads(A, D, dt_bias, H, dev)
+    _need(B, "B", (R, G, N), t, dev)
+    _need(C, "C", (R, G, N), t, dev)
+    _need(S, "S", (pool, H, P, N), torch.float32, dev)
+    if slots is not None:
+        _need(slots, "slots", (R,), torch.int32, dev)
+    if O is None:
+        O = torch.empty_like(x)
+    else:
+        _need(O, "O", (R, H, P), t, dev)
+    _launch(dev, "ttt_selective_scan_step", lib().ttt_selective_scan_step, _scan_step_shape(R, pool, H, G, P, N), _dt(t),
+            _at(x), _at(dt), _at(A), _at(B), _at(C), _at(D), _at(dt_bias), bool(softplus), _at(S), _at(slots), _at(O))
+    return O

@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libttt.so")
 SOURCES = ["inplace.hip", "lact.hip", "lact_bwd.hip", "delta.hip", "delta_bwd.hip", "delta_step.hip", "norm.hip",
-           "api.cpp", "api_delta.cpp"]
+           "rms.hip", "conv.hip", "scan_step.hip", "api.cpp", "api_delta.cpp", "api_scan.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

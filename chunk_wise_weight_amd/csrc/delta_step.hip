@@ -14,8 +14,8 @@
 // heads of 128 210 us instead of 204, 1024 rows 858 instead of 813, 4096 rows
 // 3.76 ms instead of 3.37; 16384 rows of 8 heads of 64 1.72 ms instead of 0.78.
 // Hence the limit of 65536 rows.
-#include "common.hpp"
 #include "launch.hpp"
+#include "slots.hpp"
 
 namespace ttt {
 namespace {
@@ -27,27 +27,6 @@ __device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
   for (int m = LPR / 2; m > 0; m >>= 1) x += __shfl_xor(x, m, 64);
   return x;
-}
-
-// The first position >= from of `slot` in slots[0, rows), or rows: blocks of 512 that do not hold it are passed over at
-// two loads a lane (4096 rows of 32 heads: 3.76 ms; all of them by 64 slots a time 6.17), the rest goes by 64.
-__device__ __forceinline__ int next_row(const int32_t* slots, int rows, int from, int slot) {
-  const int lane = threadIdx.x & 63;
-  int at = from;
-  for (; at + 512 <= rows; at += 512) {
-    int4 s[2];
-    bool in = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) __builtin_memcpy(&s[i], slots + at + i * 256 + lane * 4, 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) in |= s[i].x == slot | s[i].y == slot | s[i].z == slot | s[i].w == slot;
-    if (__ballot(in)) break;
-  }
-  for (; at < rows; at += 64) {
-    const unsigned long long hit = __ballot(at + lane < rows && slots[at + lane < rows ? at + lane : from] == slot);
-    if (hit) return at + __builtin_ctzll(hit);
-  }
-  return rows;
 }
 
 // LPR lanes hold a state row (4 elements each, dk <= 4 LPR); a wave holds 64 /

@@ -271,4 +271,83 @@ size_t delta_grad_workspace_bytes(const DeltaArgs& a);
 template <typename T>
 hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s);
 
+// Root-mean-square norm.  group: columns that share a scale (0: a row); scale null: y is of the inputs' type, else e4m3.
+struct RmsArgs {
+  int64_t rows;
+  int d, group;
+  float eps;
+  const void *x, *residual, *weight;   // residual, weight or null
+  void *h, *y;                         // h only with a residual
+  float *rstd, *scale;
+};
+template <typename T>
+hipError_t launch_rms(const RmsArgs& a, hipStream_t s);
+struct RmsGradArgs {
+  int64_t rows;
+  int d;
+  const void *h, *weight, *dy, *dh;    // weight, dh or null
+  const float* rstd;
+  void* dx;
+  float *dweight, *part;               // dweight or null; part [blocks, d]
+};
+template <typename T>
+int rms_grad_blocks(int64_t rows, int d);
+template <typename T>
+hipError_t launch_rms_grad(const RmsGradArgs& a, hipStream_t s);
+
+// Short convolution.  Strides of a [B, n, d] tensor use b and t.
+struct ConvArgs {
+  int batch, d, K;
+  bool silu, rag;                      // rag: rows that are not whole aligned vectors of 16 bytes
+  DeltaSeqs seqs;
+  const void *x, *w, *bias, *x_init;   // bias, x_init or null
+  DeltaStrides sx, sy;
+  void *Y, *x_final;
+};
+struct ConvGradArgs {
+  ConvArgs f;                          // Y and x_final unused
+  const void *dY, *dx_final;           // dx_final or null: zero
+  DeltaStrides sdy, sdx;
+  void *dx, *dx_init;                  // dx_init or null: not wanted
+  float *dw, *dbias, *part;            // dbias or null; part [runs, K + 1, d]
+};
+// How a launch deals tokens and channels to threads (conv.hip).
+struct ConvPlan {
+  int cv, blocks_c, run, runs, seqs;
+  int64_t blocks, seq_blocks;
+};
+struct ConvStepArgs {
+  int rows, d, K;
+  bool silu, rag;
+  int64_t pool;
+  const void *x, *w, *bias;
+  void* halo;                          // [pool, K - 1, d]
+  const int32_t* slots;
+  void* Y;
+};
+template <typename T>
+hipError_t launch_conv(const ConvArgs& a, hipStream_t s);
+template <typename T>
+int64_t conv_blocks(const ConvArgs& a, bool grad);   // workgroups of a launch
+template <typename T>
+int64_t conv_grad_runs(const ConvArgs& a);
+template <typename T>
+hipError_t launch_conv_grad(const ConvGradArgs& a, hipStream_t s);
+template <typename T>
+hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t s);
+
+// Selective scan.
+struct ScanStepArgs {
+  int rows, H, G, P, N;
+  bool softplus;
+  int64_t pool;
+  const void *x, *B, *C;               // [rows, H, P], [rows, G, N]
+  const float *dt, *A, *D, *dt_bias;   // [rows, H], [H]; D, dt_bias or null
+  float* S;                            // [pool, H, P, N]
+  const int32_t* slots;
+  void* O;
+};
+template <typename T>
+hipError_t launch_scan_step(const ScanStepArgs& a, hipStream_t s);
+
 }  // namespace ttt

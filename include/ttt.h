@@ -849,6 +849,149 @@ int ttt_layer_norm_backward(int64_t rows, int64_t dim, int dtype, const void* x,
                             const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ root-mean-square norm */
+
+/* The norm of the residual stream: h = x + residual, rounded to dtype, and
+ * y = h rstd weight, rstd = 1 / sqrt(mean(h^2) + eps), over rows of `dim`
+ * elements, sums in fp32.
+ *   x, residual  [rows, dim]  dtype; residual may be NULL: h is x and not written
+ *   weight       [dim]        dtype, or NULL: 1
+ *   h            [rows, dim]  dtype (written where there is a residual)
+ *   rstd         [rows]       fp32 (written; 4-byte aligned)
+ *   scale NULL:
+ *     y          [rows, dim]  dtype (written)
+ *   scale given: 8 bits (e4m3, one byte an element),
+ *     scale      [rows, ceil(dim / group)] fp32 (written; 4-byte aligned): the
+ *                largest |h rstd weight| of the row (group 0: one scale a row)
+ *                or of each `group` (32, 64 or 128) of its columns, divided
+ *                by 448, at least 2^-126
+ *     y          [rows, dim]  e4m3 (written): h rstd weight / scale, rounded to
+ *                nearest even
+ * dim <= 65536 (else TTT_ERR_UNSUPPORTED); eps finite and not negative; other
+ * groups, or a group without scale: TTT_ERR_ARG.  Where dim is no multiple of
+ * 16 bytes the tensors need their elements' alignment only.  A row that holds
+ * values that are not finite, or whose squares' sum is past fp32, has undefined
+ * outputs, no other row. */
+int ttt_rms_norm(int64_t rows, int64_t dim, int dtype, float eps, const void* x, const void* residual, const void* weight,
+                 void* h, void* y, float* rstd, float* scale, int64_t group, void* stream);
+
+int ttt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t dim, int dtype, size_t* bytes);
+
+/* Its backward (dtype output), given h (x, where there was no residual) and
+ * rstd: with n = h rstd and a = dy weight,
+ *   dx      [rows, dim] dtype   rstd (a - n mean(a n)) + dh: the gradient of x
+ *                               and of the residual, dh [rows, dim] being what
+ *                               comes back to h from its other uses, or NULL
+ *   dweight [dim] fp32          sum over rows of dy n, or NULL: not wanted
+ * rows == 0 gives zero sums.  The sums are made in a fixed order. */
+int ttt_rms_norm_backward(int64_t rows, int64_t dim, int dtype, const void* h, const void* weight, const void* dy,
+                          const float* rstd, const void* dh, void* dx, float* dweight, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ short convolution */
+
+/* Causal depthwise convolution over the tokens with SiLU, as it stands in
+ * front of the selective scan and of the gated delta rule:
+ *   z_t = bias + sum_j conv_w[:, j] x_{t-K+1+j},   y_t = silu(z_t), or z_t
+ * K = taps; the rows before a sequence's first are x_init's or zero.
+ * Supported: taps in 1..8, dim <= 2^20, batch * seq_len <= 2^30 (else
+ * TTT_ERR_UNSUPPORTED), any dim, and any strides: tensors need their elements'
+ * alignment only (whole rows of 16 bytes at 16-byte addresses are faster). */
+typedef struct {
+  int64_t batch, seq_len, dim, taps;
+} ttt_conv_shape;
+
+/* Strides, in elements, of a [B, n, d] tensor whose last index is contiguous.
+ * Nonnegative and at most 2^40; zero strides repeat a row, in inputs only: a
+ * written tensor's put no two elements at one place, as in ttt_delta_strides.
+ * (Else TTT_ERR_ARG.) */
+typedef struct {
+  int64_t batch, token;
+} ttt_row_strides;
+typedef struct {
+  ttt_row_strides x, y;
+} ttt_conv_layout;
+
+/* A NULL pointer or all fields zero: no bias, no SiLU, rows of one sequence
+ * each with zeros before it, contiguous tensors. */
+typedef struct {
+  const void* bias;          /* [d] dtype or NULL */
+  int silu;
+  const void* x_init;        /* [sequences, K-1, d] dtype, or NULL: zero */
+  const int32_t* seq_starts; /* packed sequences, as in ttt_delta_options */
+  int64_t num_seqs;
+  const ttt_conv_layout* layout;  /* HOST; NULL: contiguous */
+} ttt_conv_options;
+
+/*   x        [B, n, d]              dtype
+ *   conv_w   [d, K]                 dtype   tap K-1 multiplies the token itself
+ *   y        [B, n, d]              dtype   (written; rows of tokens that belong to no sequence are left as they are)
+ *   x_final  [sequences, K-1, d]    dtype   (written; NULL where K is 1) the last K-1 rows of each sequence behind its
+ *                                   x_init: the next call's x_init, or the rows of ttt_short_conv_step */
+int ttt_short_conv(const ttt_conv_shape* shape, int dtype, const void* x, const void* conv_w,
+                   const ttt_conv_options* options, void* y, void* x_final, void* stream);
+
+typedef struct {
+  ttt_row_strides dy, dx;
+} ttt_conv_grad_layout;
+
+/* num_seqs < 0: not packed. */
+int ttt_short_conv_backward_workspace_bytes(const ttt_conv_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
+
+/* Its backward from the forward call's inputs (z is made again), dy and, where
+ * the loss depends on x_final too, dx_final (else NULL):
+ *   dx       [B, n, d]            dtype (written; rows of tokens that belong to no sequence are left as they are)
+ *   dconv_w  [d, K] fp32          (written)
+ *   dbias    [d] fp32             (written), or NULL: not wanted
+ *   dx_init  [sequences, K-1, d]  dtype (written), or NULL: not wanted
+ * options' layout gives x's strides (its y is not used).  No atomics: the same
+ * bits at every call. */
+int ttt_short_conv_backward(const ttt_conv_shape* shape, int dtype, const void* x, const void* conv_w, const void* dy,
+                            const void* dx_final, const ttt_conv_options* options,
+                            const ttt_conv_grad_layout* grad_layout, void* dx, float* dconv_w, float* dbias,
+                            void* dx_init, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each row of a serving batch, on earlier rows that stay in a
+ * pool and are moved on IN PLACE.
+ *   x      [rows, d]          dtype
+ *   halo   [states, K-1, d]   dtype   (read and written)
+ *   slots  [rows] int32, DEVICE, as for ttt_gated_delta_step: a slot outside
+ *          the pool marks a padding row, whose output is zero; rows of one slot
+ *          take their tokens in row order; at most 65536 rows with slots.
+ *          NULL: row r's is halo[r].
+ *   y      [rows, d]          dtype   (written)
+ * rows * ceil(d / 1024) below 2^24, else TTT_ERR_UNSUPPORTED. */
+int ttt_short_conv_step(int64_t rows, int64_t states, int64_t dim, int64_t taps, int dtype, int silu, const void* x,
+                        const void* conv_w, const void* bias, void* halo, const int32_t* slots, void* y, void* stream);
+
+/* ------------------------------------------------------------------ selective scan */
+
+/* Sizes of a step: rows of a serving batch, states in the pool. */
+typedef struct {
+  int64_t rows, states, heads, groups, head_dim, state;
+} ttt_scan_step_shape;
+
+/* One token for each row of a serving batch, on states that stay in a pool and
+ * are updated IN PLACE.
+ *   x         [rows, H, P]  dtype
+ *   dt        [rows, H]     fp32 (4-byte aligned)
+ *   A         [H]           fp32
+ *   B, C      [rows, G, N]  dtype
+ *   D         [H]           fp32, or NULL: 0
+ *   dt_bias   [H]           fp32, or NULL: 0
+ *   S         [states, H, P, N] fp32   (read and written)
+ *   slots     [rows] int32, DEVICE, as for ttt_gated_delta_step: a slot outside
+ *             the pool marks a padding row, whose output is zero; rows of one
+ *             slot take their tokens in row order; at most 65536 rows with
+ *             slots.  NULL: row r's state is S[r].
+ *   O         [rows, H, P]  dtype   (written)
+ * A decay exp(A r) that rounds to zero empties the state, whatever values it
+ * holds.  All arithmetic and the state are fp32.  rows * heads * ceil(head_dim
+ * / 8) below 2^24, else TTT_ERR_UNSUPPORTED. */
+int ttt_selective_scan_step(const ttt_scan_step_shape* shape, int dtype, const void* x, const float* dt, const float* A,
+                            const void* B, const void* C, const float* D, const float* dt_bias, int softplus, float* S,
+                            const int32_t* slots, void* O, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

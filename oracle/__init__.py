@@ -15,9 +15,11 @@ Modules:
 
   delta    -- the gated delta rule token by token, its reverse recurrence,
               and layer norm with its backward.
+  scan     -- the selective scan token by token, its reverse recurrence, the
+              short convolution and the root-mean-square norm with theirs.
 
 Every function is pinned by the CPU tests against something other than
 itself (library routines, closed forms, brute force, finite differences,
 autograd).  Nothing here is "parity unpinned".
 """
-from . import delta, inplace, lact  # noqa: F401
+from . import delta, inplace, lact, scan  # noqa: F401
