@@ -119,6 +119,20 @@ class ConvOptions(ctypes.Structure):
                 ("seq_starts", ctypes.c_void_p), ("num_seqs", ctypes.c_int64), ("layout", ctypes.POINTER(ConvLayout))]
 
 
+class ScanShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seq_len", "heads", "groups", "head_dim", "state")]
+
+
+class ScanLayout(ctypes.Structure):
+    _fields_ = [(n, DeltaStrides) for n in ("x", "dt", "B", "C", "O")]
+
+
+class ScanOptions(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("softplus", ctypes.c_int),
+                ("S_init", ctypes.c_void_p), ("seq_starts", ctypes.c_void_p), ("num_seqs", ctypes.c_int64),
+                ("layout", ctypes.POINTER(ScanLayout))]
+
+
 class ScanStepShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("rows", "states", "heads", "groups", "head_dim", "state")]
 
@@ -195,6 +209,9 @@ _SIGNATURES = {
     "ttt_short_conv_backward": (_I, [ctypes.POINTER(ConvShape), _I] + [_P] * 4 + [ctypes.POINTER(ConvOptions),
                                      ctypes.POINTER(ConvGradLayout)] + [_P] * 5 + [_S, _P]),
     "ttt_short_conv_step": (_I, [ctypes.c_int64] * 4 + [_I, _I] + [_P] * 7),
+    "ttt_selective_scan_workspace_bytes": (_I, [ctypes.POINTER(ScanShape), _I, ctypes.c_int64, ctypes.POINTER(_S)]),
+    "ttt_selective_scan": (_I, [ctypes.POINTER(ScanShape), _I] + [_P] * 5 + [ctypes.POINTER(ScanOptions)] + [_P] * 3 +
+                           [_S, _P]),
     "ttt_selective_scan_step": (_I, [ctypes.POINTER(ScanStepShape), _I] + [_P] * 7 + [_I] + [_P] * 4),
 }
 
@@ -1298,6 +1315,63 @@ def _scan_heads(A, D, dt_bias, H, dev):
     _need(A, "A", (H,), torch.float32, dev)
     _norm_vector(D, "D", H, torch.float32, dev)
     _norm_vector(dt_bias, "dt_bias", H, torch.float32, dev)
+
+
+def _scan_strides(x, dt, B, C):
+    if len(x[0]) != 4 or len(B[0]) != 4:
+        raise ValueError(f"x is [B, H, n, P] and B [B, G, n, N], got {tuple(x[0])} and {tuple(B[0])}")
+    (b, H, n, P), G, N, t = x[0], B[0][1], B[0][3], x[2]
+    return ScanShape(b, n, H, G, P, N), (
+        _strides(x, "x", (b, H, n, P), t), _strides(dt, "dt", (b, H, n), torch.float32, rows=False),
+        _strides(B, "B", (b, G, n, N), t), _strides(C, "C", (b, G, n, N), t))
+
+
+def _scan_metas(x, dt, B, C, dev):
+    return _meta(x, "x", dev), _meta(dt, "dt", dev, False), _meta(B, "B", dev), _meta(C, "C", dev)
+
+
+def ttt_selective_scan_workspace_bytes(shape: ScanShape, dtype: torch.dtype, num_seqs: int = -1) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_selective_scan_workspace_bytes(ctypes.byref(shape), _dt(dtype), int(num_seqs), ctypes.byref(out)),
+           "ttt_selective_scan_workspace_bytes")
+    return out.value
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_plan(x, dt, B, C, O, num):
+    """(byref of ScanShape, its dtype code, ScanLayout, workspace bytes, states' shape) of a forward call."""
+    shape, strides = _scan_strides(x, dt, B, C)
+    layout = ScanLayout(*strides, _strides(O, "O", tuple(x[0]), x[2], out=True))
+    return (ctypes.byref(shape), _dt(x[2]), layout, ttt_selective_scan_workspace_bytes(shape, x[2], num),
+            (shape.batch if num < 0 else num, shape.heads, shape.head_dim, shape.state))
+
+
+def ttt_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, softplus=False, S_init=None, seq_starts=None, O=None,
+                       S_final=None, workspace=None):
+    """The selective scan over whole sequences: per head S_t = exp(A r_t) S_{t-1} + r_t x_t B_t^T, o_t = S_t C_t + D x_t
+    with r_t = dt_t + dt_bias, or softplus of that.  Returns (O [B, H, n, P], S_final [sequences, H, P, N] fp32).
+
+    x [B, H, n, P] and B, C [B, G, n, N] share a dtype, dt [B, H, n], A, D and dt_bias [H] are fp32, A r_t at most 0;
+    tensors of tokens may have any batch, head and token strides (a token-major tensor's transpose(1, 2)), and O, if not
+    given, is laid out like x.  H is a multiple of G: head h reads group h // (H // G).  S_init [sequences, H, P, N]
+    fp32: the states to start from (zero if None).  seq_starts, an int32 device tensor [sequences + 1]: packed sequences
+    of any lengths in one batch row; tokens that belong to none are not read and their rows of O are left as they are."""
+    dev = x.device
+    metas = _scan_metas(x, dt, B, C, dev)
+    _scan_heads(A, D, dt_bias, x.shape[1], dev)
+    num = _seq_starts(seq_starts, x.shape[0], dev)
+    O = torch.empty_like(x) if O is None else O
+    shape, code, layout, nbytes, states = _scan_plan(*metas, _meta(O, "O", dev), num)
+    if S_init is not None:
+        _need(S_init, "S_init", states, torch.float32, dev)
+    S_final = torch.empty(states, dtype=torch.float32, device=dev) if S_final is None else S_final
+    _need(S_final, "S_final", states, torch.float32, dev)
+    ws = _workspace(nbytes, dev, workspace)
+    opts = ScanOptions(_at(D), _at(dt_bias), bool(softplus), _at(S_init), _at(seq_starts), max(num, 0),
+                       ctypes.pointer(layout))
+    _launch(dev, "ttt_selective_scan", lib().ttt_selective_scan, shape, code, _at(x), _at(dt), _at(A), _at(B), _at(C),
+            ctypes.byref(opts), _at(O), _at(S_final), _at(ws), nbytes)
+    return O, S_final
 
 
 @functools.lru_cache(maxsize=256)

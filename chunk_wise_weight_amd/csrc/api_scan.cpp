@@ -90,6 +90,73 @@ int take_conv(const ttt_conv_shape* s, int dtype, const void* x, const void* w, 
   return TTT_OK;
 }
 
+int64_t scan_sequences(const ttt_scan_shape* s, int64_t num_seqs) { return num_seqs >= 0 ? num_seqs : s->batch; }
+
+ttt::ScanArgs scan_sizes(const ttt_scan_shape* s, int64_t num_seqs) {
+  ttt::ScanArgs a{};
+  a.batch = (int)s->batch;
+  a.H = (int)s->heads;
+  a.G = (int)s->groups;
+  a.P = (int)s->head_dim;
+  a.N = (int)s->state;
+  static const int32_t some = 0;
+  a.seqs = {num_seqs >= 0 ? &some : nullptr, (int)std::max<int64_t>(num_seqs, 0), (int)s->seq_len};
+  return a;
+}
+
+int check_scan(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
+  if (s == nullptr) return TTT_ERR_ARG;
+  if (!ok_dtype(dtype)) return TTT_ERR_DTYPE;
+  if (s->batch < 0 || s->seq_len < 0) return TTT_ERR_SHAPE;
+  if (int st = check_scan_heads(s->heads, s->groups, s->head_dim, s->state)) return st;
+  if (num_seqs >= 0 && s->batch != 1) return TTT_ERR_SHAPE;
+  const int64_t lim = (int64_t)1 << 30, seqs = scan_sequences(s, num_seqs);
+  if (s->seq_len > lim || seqs > lim || (num_seqs < 0 && s->batch * s->seq_len > lim)) return TTT_ERR_UNSUPPORTED;
+  const ttt::ScanArgs a = scan_sizes(s, num_seqs);
+  // every chunk of 64 tokens and head, a workgroup's grid over segments, and the states' elements by 1024
+  const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + seqs : s->batch * ((s->seq_len + 63) / 64);
+  if (chunks * s->heads > kMaxBlocks || seqs * s->heads * ((s->head_dim * s->state + 1023) / 1024) > kMaxBlocks ||
+      (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
+    return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
+size_t scan_bytes(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
+  const ttt::ScanArgs a = scan_sizes(s, num_seqs);
+  return dtype == TTT_BF16 ? ttt::scan_workspace_bytes<bf16>(a) : ttt::scan_workspace_bytes<float>(a);
+}
+
+// What the forward and the backward call take alike, checked and put into *a.
+int take_scan(const ttt_scan_shape* s, int dtype, const void* x, const float* dt, const float* A, const void* B,
+              const void* C, const ttt_scan_options* opt, ttt::ScanArgs* a) {
+  static const ttt_scan_options none{};
+  if (opt == nullptr) opt = &none;
+  const int64_t num = opt->seq_starts ? opt->num_seqs : -1;
+  if (opt->seq_starts && (num < 0 || !aligned(opt->seq_starts, 4))) return TTT_ERR_ARG;
+  if (int st = check_scan(s, dtype, num)) return st;
+  *a = scan_sizes(s, num);
+  a->seqs.starts = opt->seq_starts;
+  const ttt_scan_layout* l = opt->layout;
+  const int64_t n = s->seq_len, u = 16 / esize(dtype);
+  if (!take_strides(l ? &l->x : nullptr, s->heads, n, s->head_dim, u, &a->sx) ||
+      !take_strides(l ? &l->dt : nullptr, s->heads, n, 1, 1, &a->sdt) ||
+      !take_strides(l ? &l->B : nullptr, s->groups, n, s->state, u, &a->sB) ||
+      !take_strides(l ? &l->C : nullptr, s->groups, n, s->state, u, &a->sC))
+    return TTT_ERR_ARG;
+  if (!ok_ptr(A, 4) || !aligned(opt->D, 4) || !aligned(opt->dt_bias, 4) || !aligned(opt->S_init, 16)) return TTT_ERR_ARG;
+  if (s->batch * n > 0 && (!ok_ptr(x) || !ok_ptr(dt, 4) || !ok_ptr(B) || !ok_ptr(C))) return TTT_ERR_ARG;
+  a->x = x;
+  a->dt = dt;
+  a->A = A;
+  a->B = B;
+  a->C = C;
+  a->D = opt->D;
+  a->dt_bias = opt->dt_bias;
+  a->softplus = opt->softplus != 0;
+  a->S_init = opt->S_init;
+  return TTT_OK;
+}
+
 int64_t conv_sequences(const ttt::ConvArgs& a) { return a.seqs.starts ? a.seqs.num : a.batch; }
 
 }  // namespace
@@ -170,6 +237,33 @@ int ttt_short_conv_step(int64_t rows, int64_t states, int64_t dim, int64_t taps,
   ttt::ConvStepArgs a{(int)rows, (int)dim, (int)taps, silu != 0, rag, states, x, conv_w, bias, halo, slots, y};
   hipStream_t s = (hipStream_t)stream;
   return dev(dtype == TTT_BF16 ? ttt::launch_conv_step<bf16>(a, s) : ttt::launch_conv_step<float>(a, s));
+}
+
+int ttt_selective_scan_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes) {
+  if (bytes == nullptr) return TTT_ERR_ARG;
+  if (int st = check_scan(shape, dtype, num_seqs)) return st;
+  *bytes = scan_bytes(shape, dtype, num_seqs);
+  return TTT_OK;
+}
+
+int ttt_selective_scan(const ttt_scan_shape* shape, int dtype, const void* x, const float* dt, const float* A,
+                       const void* B, const void* C, const ttt_scan_options* options, void* O, float* S_final,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  ttt::ScanArgs a;
+  if (int st = take_scan(shape, dtype, x, dt, A, B, C, options, &a)) return st;
+  const int64_t num = a.seqs.starts ? a.seqs.num : -1;
+  if (!take_out_strides(options && options->layout ? &options->layout->O : nullptr, shape->batch, shape->heads,
+                        shape->seq_len, shape->head_dim, 16 / esize(dtype), &a.sO))
+    return TTT_ERR_ARG;
+  if (scan_sequences(shape, num) > 0 && !ok_ptr(S_final)) return TTT_ERR_ARG;
+  if (shape->batch * shape->seq_len > 0 && !ok_ptr(O)) return TTT_ERR_ARG;
+  const size_t need = scan_bytes(shape, dtype, num);
+  if (need > 0 && (!ok_ptr(workspace) || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
+  a.O = O;
+  a.S_final = S_final;
+  a.ws = (char*)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  return dev(dtype == TTT_BF16 ? ttt::launch_scan<bf16>(a, s) : ttt::launch_scan<float>(a, s));
 }
 
 int ttt_selective_scan_step(const ttt_scan_step_shape* shape, int dtype, const void* x, const float* dt, const float* A,

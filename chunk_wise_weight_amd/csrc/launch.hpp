@@ -337,6 +337,25 @@ template <typename T>
 hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t s);
 
 // Selective scan.
+struct ScanArgs {
+  int batch, H, G, P, N;
+  bool softplus;
+  DeltaSeqs seqs;
+  const void *x, *B, *C;               // [b, H, n, P], [b, G, n, N]
+  const float *dt, *A, *D, *dt_bias;   // [b, H, n], [H]; D, dt_bias or null
+  DeltaStrides sx, sdt, sB, sC, sO;
+  const float* S_init;                 // [sequences, H, P, N] or null: zero
+  void* O;
+  float* S_final;                      // [sequences, H, P, N]
+  char* ws;
+};
+template <typename T>
+size_t scan_workspace_bytes(const ScanArgs& a);
+template <typename T>
+int64_t scan_blocks(const ScanArgs& a);              // workgroups of the largest launch
+template <typename T>
+hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
+
 struct ScanStepArgs {
   int rows, H, G, P, N;
   bool softplus;

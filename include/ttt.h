@@ -966,6 +966,63 @@ int ttt_short_conv_step(int64_t rows, int64_t states, int64_t dim, int64_t taps,
 
 /* ------------------------------------------------------------------ selective scan */
 
+/* A state space recurrence whose rates, inputs and outputs go by token: per
+ * head, the state S [P, N] decays, takes the outer product of the token's x and
+ * B, and is read by the token's C:
+ *   r_t = dt_t + dt_bias, or softplus(dt_t + dt_bias) = log(1 + exp(.))
+ *   S_t = exp(A r_t) S_{t-1} + r_t x_t B_t^T
+ *   o_t = S_t C_t + D x_t
+ * n = seq_len, P = head_dim, N = state; head h reads group h / (heads /
+ * groups) of B and C.  Supported: heads a multiple of groups (else
+ * TTT_ERR_SHAPE); head_dim and state multiples of 8, state <= 256, head_dim <=
+ * 4096, heads <= 65536, batch * seq_len <= 2^30, chunks of 64 tokens (packed:
+ * seq_len / 64 + sequences) times heads and sequences * heads * ceil(P N /
+ * 1024) below 2^24 (else TTT_ERR_UNSUPPORTED). */
+typedef struct {
+  int64_t batch, seq_len, heads, groups, head_dim, state;
+} ttt_scan_shape;
+
+/* Strides as in ttt_delta_strides; dt's as a gate's. */
+typedef struct {
+  ttt_delta_strides x, dt, B, C, O;
+} ttt_scan_layout;
+
+/* A NULL pointer or all fields zero: no D, no bias, rates dt, rows of one
+ * sequence each that start from S = 0, every tensor contiguous. */
+typedef struct {
+  const float* D;            /* [H] or NULL: 0 */
+  const float* dt_bias;      /* [H] or NULL: 0 */
+  int softplus;              /* nonzero: rates are softplus(dt + dt_bias) */
+  const float* S_init;       /* [sequences, H, P, N] (an earlier call's S_final), or NULL: zero */
+  const int32_t* seq_starts; /* packed sequences, as in ttt_delta_options */
+  int64_t num_seqs;
+  const ttt_scan_layout* layout;  /* HOST; NULL: contiguous */
+} ttt_scan_options;
+
+/* Workspace of ttt_selective_scan; num_seqs < 0: not packed.  Zero where every
+ * sequence is one segment, else 4 P N + 4 bytes for each segment and head: few
+ * more than fill the chip once. */
+int ttt_selective_scan_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
+
+/* The recurrence over whole sequences.
+ *   x         [B, H, n, P]  dtype
+ *   dt        [B, H, n]     fp32 (4-byte aligned)
+ *   A         [H]           fp32; A r_t is at most 0
+ *   B, C      [B, G, n, N]  dtype
+ *   O         [B, H, n, P]  dtype   (written; rows of tokens that belong to no sequence are left as they are)
+ *   S_final   [sequences, H, P, N] fp32 (written)  sequences = B, or num_seqs
+ * A log decay A r_t below -104, whose decay rounds to zero, empties the state:
+ * a document boundary inside a sequence; at a sequence's first token S_init's
+ * values are not looked at.  A rate of 0 leaves the state as it
+ * is.  All inputs of tokens that belong to a sequence have to be finite: one
+ * that is not leaves every output of its sequence undefined (x and dt: of its
+ * head), none of other sequences.  With bf16 inputs the state is summed from
+ * products kept to 2^-24, and O is off by its own rounding.  seq_len == 0 or an
+ * empty sequence: S_final is S_init (or zero). */
+int ttt_selective_scan(const ttt_scan_shape* shape, int dtype, const void* x, const float* dt, const float* A,
+                       const void* B, const void* C, const ttt_scan_options* options, void* O, float* S_final,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Sizes of a step: rows of a serving batch, states in the pool. */
 typedef struct {
   int64_t rows, states, heads, groups, head_dim, state;
