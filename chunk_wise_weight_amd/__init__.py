@@ -13,7 +13,7 @@ Functions keep the C names:
   ttt_chunk_apply, ttt_lact_swiglu, ttt_lact_swiglu_backward (and its _ex form), ttt_gated_delta,
   ttt_gated_delta_backward, ttt_gated_delta_step, ttt_layer_norm, ttt_layer_norm_backward,
   ttt_rms_norm, ttt_rms_norm_backward, ttt_short_conv, ttt_short_conv_backward, ttt_short_conv_step,
-  ttt_selective_scan, ttt_selective_scan_step, plus the workspace queries.
+  ttt_selective_scan, ttt_selective_scan_backward, ttt_selective_scan_step, plus the workspace queries.
 """
 from ._lib import (  # noqa: F401
     TTT_OK, TTT_ERR_ARG, TTT_ERR_SHAPE, TTT_ERR_DTYPE, TTT_ERR_WORKSPACE, TTT_ERR_DEVICE,
@@ -37,5 +37,5 @@ from ._lib import (  # noqa: F401
     ConvShape, RowStrides, ConvLayout, ConvGradLayout, ConvOptions, ttt_short_conv,
     ttt_short_conv_backward_workspace_bytes, ttt_short_conv_backward, ttt_short_conv_step,
     ScanShape, ScanLayout, ScanOptions, ScanStepShape, ttt_selective_scan_workspace_bytes, ttt_selective_scan,
-    ttt_selective_scan_step,
+    ScanGradLayout, ttt_selective_scan_backward_workspace_bytes, ttt_selective_scan_backward, ttt_selective_scan_step,
 )

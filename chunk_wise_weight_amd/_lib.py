@@ -127,6 +127,10 @@ class ScanLayout(ctypes.Structure):
     _fields_ = [(n, DeltaStrides) for n in ("x", "dt", "B", "C", "O")]
 
 
+class ScanGradLayout(ctypes.Structure):
+    _fields_ = [(n, DeltaStrides) for n in ("dO", "dx", "ddt", "dB", "dC")]
+
+
 class ScanOptions(ctypes.Structure):
     _fields_ = [("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("softplus", ctypes.c_int),
                 ("S_init", ctypes.c_void_p), ("seq_starts", ctypes.c_void_p), ("num_seqs", ctypes.c_int64),
@@ -212,6 +216,10 @@ _SIGNATURES = {
     "ttt_selective_scan_workspace_bytes": (_I, [ctypes.POINTER(ScanShape), _I, ctypes.c_int64, ctypes.POINTER(_S)]),
     "ttt_selective_scan": (_I, [ctypes.POINTER(ScanShape), _I] + [_P] * 5 + [ctypes.POINTER(ScanOptions)] + [_P] * 3 +
                            [_S, _P]),
+    "ttt_selective_scan_backward_workspace_bytes": (_I, [ctypes.POINTER(ScanShape), _I, ctypes.c_int64,
+                                                         ctypes.POINTER(_S)]),
+    "ttt_selective_scan_backward": (_I, [ctypes.POINTER(ScanShape), _I] + [_P] * 7 + [ctypes.POINTER(ScanOptions),
+                                         ctypes.POINTER(ScanGradLayout)] + [_P] * 9 + [_S, _P]),
     "ttt_selective_scan_step": (_I, [ctypes.POINTER(ScanStepShape), _I] + [_P] * 7 + [_I] + [_P] * 4),
 }
 
@@ -1372,6 +1380,61 @@ def ttt_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, softplus=False, S_i
     _launch(dev, "ttt_selective_scan", lib().ttt_selective_scan, shape, code, _at(x), _at(dt), _at(A), _at(B), _at(C),
             ctypes.byref(opts), _at(O), _at(S_final), _at(ws), nbytes)
     return O, S_final
+
+
+def ttt_selective_scan_backward_workspace_bytes(shape: ScanShape, dtype: torch.dtype, num_seqs: int = -1) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ttt_selective_scan_backward_workspace_bytes(ctypes.byref(shape), _dt(dtype), int(num_seqs),
+                                                             ctypes.byref(out)),
+           "ttt_selective_scan_backward_workspace_bytes")
+    return out.value
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_backward_plan(x, dt, B, C, dO, dx, ddt, dB, dC, num):
+    shape, strides = _scan_strides(x, dt, B, C)
+    xs, ds, bs, t = tuple(x[0]), tuple(dt[0]), tuple(B[0]), x[2]
+    grads = ScanGradLayout(_strides(dO, "dO", xs, t), _strides(dx, "dx", xs, t, out=True),
+                           _strides(ddt, "ddt", ds, torch.float32, rows=False, out=True),
+                           _strides(dB, "dB", bs, t, out=True), _strides(dC, "dC", bs, t, out=True))
+    return (ctypes.byref(shape), _dt(t), ScanLayout(*strides, DeltaStrides()), grads,
+            ttt_selective_scan_backward_workspace_bytes(shape, t, num),
+            (shape.batch if num < 0 else num, shape.heads, shape.head_dim, shape.state))
+
+
+def ttt_selective_scan_backward(x, dt, A, B, C, dO, D=None, dt_bias=None, softplus=False, dS_final=None, S_init=None,
+                                seq_starts=None, dx=None, ddt=None, dA=None, dB=None, dC=None, dD=None, ddt_bias=None,
+                                dS_init=None, workspace=None):
+    """Backward of ttt_selective_scan from its inputs (the states are made again), dO = dLoss/dO [B, H, n, P] and, where
+    the loss depends on the final states too, dS_final [sequences, H, P, N] fp32.  Returns (dx, ddt, dA, dB, dC, dD,
+    ddt_bias, dS_init): dx, dB, dC in x's dtype, the others fp32, tensors of tokens laid out like their inputs if not
+    given; dD, ddt_bias and dS_init are None without D, dt_bias and S_init, unless given.  dO and the gradients may have
+    any strides that the inputs may; rows of tokens that belong to no sequence are left as they are."""
+    dev, H = x.device, x.shape[1]
+    metas = _scan_metas(x, dt, B, C, dev)
+    _scan_heads(A, D, dt_bias, H, dev)
+    num = _seq_starts(seq_starts, x.shape[0], dev)
+    dx, ddt, dB, dC = (torch.empty_like(t) if d is None else d for d, t in ((dx, x), (ddt, dt), (dB, B), (dC, C)))
+    shape, code, layout, grads, nbytes, states = _scan_backward_plan(
+        *metas, _meta(dO, "dO", dev), _meta(dx, "dx", dev), _meta(ddt, "ddt", dev, False), _meta(dB, "dB", dev),
+        _meta(dC, "dC", dev), num)
+    dA = torch.empty_like(A) if dA is None else dA
+    dD = torch.empty_like(D) if dD is None and D is not None else dD
+    ddt_bias = torch.empty_like(dt_bias) if ddt_bias is None and dt_bias is not None else ddt_bias
+    for t, name in ((dA, "dA"), (dD, "dD"), (ddt_bias, "ddt_bias")):
+        _norm_vector(t, name, H, torch.float32, dev)
+    if S_init is not None and dS_init is None:
+        dS_init = torch.empty_like(S_init)
+    for t, name in ((S_init, "S_init"), (dS_final, "dS_final"), (dS_init, "dS_init")):
+        if t is not None:
+            _need(t, name, states, torch.float32, dev)
+    ws = _workspace(nbytes, dev, workspace)
+    opts = ScanOptions(_at(D), _at(dt_bias), bool(softplus), _at(S_init), _at(seq_starts), max(num, 0),
+                       ctypes.pointer(layout))
+    _launch(dev, "ttt_selective_scan_backward", lib().ttt_selective_scan_backward, shape, code, _at(x), _at(dt), _at(A),
+            _at(B), _at(C), _at(dO), _at(dS_final), ctypes.byref(opts), ctypes.byref(grads), _at(dx), _at(ddt), _at(dA),
+            _at(dB), _at(dC), _at(dD), _at(ddt_bias), _at(dS_init), _at(ws), nbytes)
+    return dx, ddt, dA, dB, dC, dD, ddt_bias, dS_init
 
 
 @functools.lru_cache(maxsize=256)

@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libttt.so")
 SOURCES = ["inplace.hip", "lact.hip", "lact_bwd.hip", "delta.hip", "delta_bwd.hip", "delta_step.hip", "norm.hip",
-           "rms.hip", "conv.hip", "scan.hip", "scan_step.hip", "api.cpp", "api_delta.cpp", "api_scan.cpp"]
+           "rms.hip", "conv.hip", "scan.hip", "scan_bwd.hip", "scan_step.hip", "api.cpp", "api_delta.cpp", "api_scan.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -28,7 +28,7 @@ FLAGS = [
 ]
 # The walks over a state keep it in fp32 accumulators that vector instructions scale and split between products:
 # MFMA results in ordinary registers spare a copy each way per element and product.
-EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("delta.hip", "delta_bwd.hip", "scan.hip")}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("delta.hip", "delta_bwd.hip", "scan.hip", "scan_bwd.hip")}
 
 
 def _run(cmd):

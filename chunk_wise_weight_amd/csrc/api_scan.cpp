@@ -121,6 +121,18 @@ int check_scan(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
   return TTT_OK;
 }
 
+// What the backward pass takes less of: walks in both directions, a workgroup of 512 for each chunk and group, twice the
+// states' elements by 1024.
+int check_scan_backward(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
+  const ttt::ScanArgs a = scan_sizes(s, num_seqs);
+  const int64_t seqs = scan_sequences(s, num_seqs);
+  const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + seqs : s->batch * ((s->seq_len + 63) / 64);
+  if (2 * chunks * s->groups > kMaxBlocks || 2 * seqs * s->heads * ((s->head_dim * s->state + 1023) / 1024) > kMaxBlocks ||
+      2 * (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
+    return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
 size_t scan_bytes(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
   const ttt::ScanArgs a = scan_sizes(s, num_seqs);
   return dtype == TTT_BF16 ? ttt::scan_workspace_bytes<bf16>(a) : ttt::scan_workspace_bytes<float>(a);
@@ -264,6 +276,52 @@ int ttt_selective_scan(const ttt_scan_shape* shape, int dtype, const void* x, co
   a.ws = (char*)workspace;
   hipStream_t s = (hipStream_t)stream;
   return dev(dtype == TTT_BF16 ? ttt::launch_scan<bf16>(a, s) : ttt::launch_scan<float>(a, s));
+}
+
+int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes) {
+  if (bytes == nullptr) return TTT_ERR_ARG;
+  if (int st = check_scan(shape, dtype, num_seqs)) return st;
+  if (int st = check_scan_backward(shape, dtype, num_seqs)) return st;
+  const ttt::ScanArgs a = scan_sizes(shape, num_seqs);
+  *bytes = dtype == TTT_BF16 ? ttt::scan_grad_workspace_bytes<bf16>(a) : ttt::scan_grad_workspace_bytes<float>(a);
+  return TTT_OK;
+}
+
+int ttt_selective_scan_backward(const ttt_scan_shape* shape, int dtype, const void* x, const float* dt, const float* A,
+                                const void* B, const void* C, const void* dO, const float* dS_final,
+                                const ttt_scan_options* options, const ttt_scan_grad_layout* grad_layout, void* dx,
+                                float* ddt, float* dA, void* dB, void* dC, float* dD, float* ddt_bias, float* dS_init,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  ttt::ScanGradArgs a{};
+  if (int st = take_scan(shape, dtype, x, dt, A, B, C, options, &a.f)) return st;
+  const int64_t num = a.f.seqs.starts ? a.f.seqs.num : -1;
+  const ttt_scan_grad_layout* l = grad_layout;
+  const int64_t b = shape->batch, n = shape->seq_len, u = 16 / esize(dtype), H = shape->heads, G = shape->groups;
+  if (!take_strides(l ? &l->dO : nullptr, H, n, shape->head_dim, u, &a.sdO) ||
+      !take_out_strides(l ? &l->dx : nullptr, b, H, n, shape->head_dim, u, &a.sdx) ||
+      !take_out_strides(l ? &l->ddt : nullptr, b, H, n, 1, 1, &a.sddt) ||
+      !take_out_strides(l ? &l->dB : nullptr, b, G, n, shape->state, u, &a.sdB) ||
+      !take_out_strides(l ? &l->dC : nullptr, b, G, n, shape->state, u, &a.sdC))
+    return TTT_ERR_ARG;
+  if (b * n > 0 && (!ok_ptr(dO) || !ok_ptr(dx) || !ok_ptr(ddt, 4) || !ok_ptr(dB) || !ok_ptr(dC))) return TTT_ERR_ARG;
+  if (!ok_ptr(dA, 4) || !aligned(dD, 4) || !aligned(ddt_bias, 4) || !aligned(dS_final, 16) || !aligned(dS_init, 16))
+    return TTT_ERR_ARG;
+  size_t need = 0;
+  if (int st = ttt_selective_scan_backward_workspace_bytes(shape, dtype, num, &need)) return st;
+  if (need > 0 && (!ok_ptr(workspace) || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
+  a.f.ws = (char*)workspace;
+  a.dO = dO;
+  a.dS_final = dS_final;
+  a.dx = dx;
+  a.ddt = ddt;
+  a.dA = dA;
+  a.dB = dB;
+  a.dC = dC;
+  a.dD = dD;
+  a.ddt_bias = ddt_bias;
+  a.dS_init = dS_init;
+  hipStream_t s = (hipStream_t)stream;
+  return dev(dtype == TTT_BF16 ? ttt::launch_scan_grad<bf16>(a, s) : ttt::launch_scan_grad<float>(a, s));
 }
 
 int ttt_selective_scan_step(const ttt_scan_step_shape* shape, int dtype, const void* x, const float* dt, const float* A,

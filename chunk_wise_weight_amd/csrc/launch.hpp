@@ -356,6 +356,22 @@ int64_t scan_blocks(const ScanArgs& a);              // workgroups of the larges
 template <typename T>
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 
+struct ScanGradArgs {
+  ScanArgs f;                          // O and S_final unused
+  const void* dO;
+  const float* dS_final;               // or null: zero
+  void *dx, *dB, *dC;
+  float *ddt, *dA, *dD, *ddt_bias, *dS_init;   // dD, ddt_bias, dS_init or null: not wanted
+  DeltaStrides sdO, sdx, sddt, sdB, sdC;
+  // regions of the workspace, placed by launch_scan_grad
+  char *S, *dS;
+  float* part;
+};
+template <typename T>
+size_t scan_grad_workspace_bytes(const ScanArgs& a);
+template <typename T>
+hipError_t launch_scan_grad(const ScanGradArgs& a, hipStream_t s);
+
 struct ScanStepArgs {
   int rows, H, G, P, N;
   bool softplus;

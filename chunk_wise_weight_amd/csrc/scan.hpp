@@ -66,8 +66,10 @@ struct Gates {
 };
 
 // A chunk's gates from its lanes' dt (one wave; tokens past len leave the state alone).  Log decays below kResetDecay
-// are taken as that: exp of them is zero either way, and sums of 64 stay where `hi` is exact.  Returns the chunk's sum.
-__device__ __forceinline__ double make_gates(float dt, float A, float bias, bool softplus, int len, Gates* o) {
+// are taken as that: exp of them is zero either way, and sums of 64 stay where `hi` is exact.  rest: exp(b_63 - b), if
+// wanted.  Returns the chunk's sum.
+__device__ __forceinline__ double make_gates(float dt, float A, float bias, bool softplus, int len, Gates* o,
+                                             float* rest = nullptr) {
   const int lane = lane_id();
   const float r = lane < len ? scan_rate(dt, bias, softplus) : 0.f;
   double b = lane < len ? fmax((double)A * r, (double)kResetDecay) * 1.4426950408889634 : 0.0;
@@ -82,7 +84,9 @@ __device__ __forceinline__ double make_gates(float dt, float A, float bias, bool
   o->lo[lane] = (float)(b - (double)hi);
   o->eb[lane] = exp2_hw((float)b);
   o->r[lane] = r;
-  o->w[lane] = r * exp2_hw((float)(last - b));
+  const float f = exp2_hw((float)(last - b));
+  o->w[lane] = r * f;
+  if (rest) rest[lane] = f;
   return last;
 }
 
@@ -174,6 +178,20 @@ template <typename T, int CT, int NT> struct StateRows {
       for (int t = 0; t < NT; ++t) {
         const int n = Mat<T>::row(t, 4 * g);
         if (p < P && n < N) *reinterpret_cast<f32x4*>(S + (int64_t)p * N + n) = s[c][t];
+      }
+    }
+  }
+  // += the weighted outer products of a step's tokens: x[c] their features of this wave's blocks, `cols` their rows of N
+  // in LDS.  All blocks of P at once, so that an operand is read once.
+  __device__ __forceinline__ void add(const u32x4 (&x)[CT], const char* cols, int step, const float* weights, int N) {
+    static_assert(CT <= 2, "blocks");
+    const Scaled<T> u0(x[0], weights), u1(x[CT - 1], weights);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t / Mat<T>::TPS * Mat<T>::KB < N) {
+        const u32x4 f = Panels<T>::frag_t(cols, t, step, lane_id());
+        s[0][t] = u0.mma(f, s[0][t]);
+        if (CT == 2) s[CT - 1][t] = u1.mma(f, s[CT - 1][t]);
       }
     }
   }

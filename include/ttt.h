@@ -1023,6 +1023,39 @@ int ttt_selective_scan(const ttt_scan_shape* shape, int dtype, const void* x, co
                        const void* B, const void* C, const ttt_scan_options* options, void* O, float* S_final,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* Strides of the backward call's own tensors, as in ttt_scan_layout. */
+typedef struct {
+  ttt_delta_strides dO, dx, ddt, dB, dC;
+} ttt_scan_grad_layout;
+
+/* Workspace of ttt_selective_scan_backward; num_seqs < 0: not packed.  Chunks
+ * of 64 tokens times groups, sequences * heads * ceil(P N / 1024) below 2^23,
+ * else TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + 16 bytes, and for
+ * each segment and head 8 P N + 8. */
+int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
+
+/* The backward of ttt_selective_scan, from the forward call's inputs alone
+ * (the states are made again), given dO = dLoss/dO and, where the loss depends
+ * on the final states too, dS_final (else NULL):
+ *   dx         [B, H, n, P]  dtype  (written)
+ *   ddt        [B, H, n]     fp32   (written)
+ *   dA         [H]           fp32   (written)
+ *   dB, dC     [B, G, n, N]  dtype  (written) summed over the heads of a group
+ *   dD         [H]           fp32   (written), or NULL: not wanted
+ *   ddt_bias   [H]           fp32   (written), or NULL: not wanted
+ *   dS_init    [sequences, H, P, N] fp32 (written), or NULL: not wanted
+ * options' layout gives the inputs' strides (its O is not used), grad_layout
+ * (NULL: contiguous) those of dO and the gradients.  Rows of tokens that belong
+ * to no sequence are left as they are.  A log decay A r below -104 (an emptied
+ * state) has gradient zero.  A token whose inputs or dO are not finite leaves
+ * every output of its sequence and group, and dA, dD and ddt_bias, undefined.
+ * No atomics: the same bits at every call. */
+int ttt_selective_scan_backward(const ttt_scan_shape* shape, int dtype, const void* x, const float* dt, const float* A,
+                                const void* B, const void* C, const void* dO, const float* dS_final,
+                                const ttt_scan_options* options, const ttt_scan_grad_layout* grad_layout, void* dx,
+                                float* ddt, float* dA, void* dB, void* dC, float* dD, float* ddt_bias, float* dS_init,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Sizes of a step: rows of a serving batch, states in the pool. */
 typedef struct {
   int64_t rows, states, heads, groups, head_dim, state;
