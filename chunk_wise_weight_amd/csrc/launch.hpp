@@ -356,6 +356,7 @@ int64_t scan_blocks(const ScanArgs& a);              // workgroups of the larges
 template <typename T>
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 
+struct KeptGates;
 struct ScanGradArgs {
   ScanArgs f;                          // O and S_final unused
   const void* dO;
@@ -364,8 +365,9 @@ struct ScanGradArgs {
   float *ddt, *dA, *dD, *ddt_bias, *dS_init;   // dD, ddt_bias, dS_init or null: not wanted
   DeltaStrides sdO, sdx, sddt, sdB, sdC;
   // regions of the workspace, placed by launch_scan_grad
-  char *S, *dS;
-  float* part;
+  float *S, *dS, *part;
+  KeptGates* gates;
+  char* sums;
 };
 template <typename T>
 size_t scan_grad_workspace_bytes(const ScanArgs& a);

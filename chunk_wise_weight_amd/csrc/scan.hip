@@ -25,6 +25,8 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   const int p0 = at.part * Z::cols, tile0 = (p0 >> 4) + pw * CT;
   const int64_t sh = (int64_t)at.slot * a.H + h, size = (int64_t)a.P * a.N;
 
+  LaneAt<T> L(lane);
+  L.keep();
   StateRows<T, CT, NT> S;
   S.zero();
   if (mine) {
@@ -73,12 +75,10 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
           for (int u = 0; u < M::TPS; ++u) d[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int ns = 0; ns < NS; ++ns) {
-            if (ns * M::KB < a.N) {
-              const u32x4 c = Panels<T>::frag(Cp, i, ns, g);
+            if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
+            const u32x4 c = L.frag(Cp, t, ns);
 #pragma unroll
-              for (int u = 0; u < M::TPS; ++u)
-                d[u] = M::mma(Panels<T>::frag(Bp, M::row(s * M::TPS + u, m), ns, g), c, d[u]);
-            }
+            for (int u = 0; u < M::TPS; ++u) d[u] = M::mma(L.frag(Bp, s * M::TPS + u, ns), c, d[u]);
           }
           for (int k = 0; k < HW; ++k) {
             const Gates& q = gates[k];
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int s = 0; s < CS; ++s) xf[s][c] = Panels<T>::frag_t(Xh, pw * CT + c, s, lane);
+      for (int s = 0; s < CS; ++s) xf[s][c] = L.frag_t(Xh, pw * CT + c, s);
     {
       f32x4 o[CT][4];
 #pragma unroll
@@ -118,13 +118,14 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
         for (int t = 0; t < 4; ++t) o[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) {
-        if (ns * M::KB < a.N) {
+        if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
+        {
           u32x4 sh_[CT], sl[CT];
 #pragma unroll
           for (int c = 0; c < CT; ++c) M::split(&S.s[c][ns * M::TPS], sh_[c], sl[c]);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const u32x4 f = Panels<T>::frag(Cp, M::row(t, m), ns, g);
+            const u32x4 f = L.frag(Cp, t, ns);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
               if (M::kSplit) o[c][t] = M::mma(sl[c], f, o[c][t]);
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
           for (int k = 0; k < PB; ++k) {
             v[k] = o[c + k][t];
-            if (a.D) v[k] += D * load4((const T*)(Xh + Panels<T>::at(i, p + 4 * k - p0)));
+            if (a.D) v[k] += D * L.at4(Xh, t, pw * CT + c + k);
           }
           if constexpr (PB == 2)
             *reinterpret_cast<u32x4*>(out + p) = M::frag(v);
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     }
     S.decay(q.eb[kDC - 1]);
 #pragma unroll
-    for (int s = 0; s < CS; ++s) S.add(xf[s], Bp, s, q.w + s * M::KB + g * (M::KB / 4), a.N);
+    for (int s = 0; s < CS; ++s) S.add(L, xf[s], Bp, s, q.w + s * M::KB + g * (M::KB / 4), a.N);
   }
   if (mine && sp.last) S.store(a.S_final + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
 }

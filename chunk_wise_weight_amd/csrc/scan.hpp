@@ -60,51 +60,130 @@ __device__ __forceinline__ SeqSlots seq_slots(const DeltaSeqs& q, int seg, int s
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Where a lane reads operands in panels of 64 rows (delta.hpp): the parts that depend on it, kept in registers; blocks and
+// steps are offsets from there.  Row block t: rows row(t, .); column block t: columns row(t, .), the rows being contracted.
+constexpr int kPanel64 = 64 * 128;
+template <typename T> struct LaneAt;
+template <> struct LaneAt<bf16> {
+  unsigned f[2], c[2];
+  __device__ __forceinline__ explicit LaneAt(int lane) {
+    const int m = lane & 15, g = lane >> 4, r = (m >> 2) * 8 + (m & 3), rt = g * 8 + (m >> 2);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f[b] = r * 128 + (((4 * b + g) ^ panel_swz(r)) << 4);
+      c[b] = rt * 128 + (((4 * b + (m & 3)) ^ panel_swz(rt)) << 4);
+    }
+  }
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+v"(f[0]), "+v"(f[1]), "+v"(c[0]), "+v"(c[1]));
+  }
+  __device__ static __forceinline__ int rows(int t) { return (t >> 1) * 4096 + (t & 1) * 512; }
+  // 16 bytes of the lane's row of block t, step s
+  __device__ __forceinline__ u32x4 frag(const char* p, int t, int s) const {
+    return *reinterpret_cast<const u32x4*>(p + f[s & 1] + ((s >> 1) * kPanel64 + rows(t)));
+  }
+  // the lane's column of block t, rows of step s
+  __device__ __forceinline__ u32x4 frag_t(const char* p, int t, int s) const {
+    const char* q = p + c[(t >> 1) & 1] + ((t >> 2) * kPanel64 + s * 4096 + (t & 1) * 8);
+    const u32x2 a = __builtin_bit_cast(u32x2, lds_read_tr16(q)), b = __builtin_bit_cast(u32x2, lds_read_tr16(q + 512));
+    return (u32x4){a[0], a[1], b[0], b[1]};
+  }
+  // columns row(ct, 4 g + 0..3) of the lane's row of block t
+  __device__ __forceinline__ f32x4 at4(const char* p, int t, int ct) const {
+    return load4((const bf16*)(p + f[(ct >> 1) & 1] + ((ct >> 2) * kPanel64 + (ct & 1) * 8 + rows(t))));
+  }
+};
+template <> struct LaneAt<float> {
+  unsigned f[2], c[2][2];
+  __device__ __forceinline__ explicit LaneAt(int lane) {
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f[b] = m * 128 + (((4 * b + g) ^ panel_swz(m)) << 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g * 4 + 2 * i;
+        c[i][b] = r * 128 + (((4 * b + (m >> 2)) ^ panel_swz(r)) << 4) + ((m & 3) << 2);
+      }
+    }
+  }
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+v"(f[0]), "+v"(f[1]), "+v"(c[0][0]), "+v"(c[0][1]), "+v"(c[1][0]), "+v"(c[1][1]));
+  }
+  // (the swizzle of row 16 t + m is that of m with the third bit flipped for odd t)
+  __device__ __forceinline__ u32x4 frag(const char* p, int t, int s) const {
+    return *reinterpret_cast<const u32x4*>(p + f[(s ^ t) & 1] + ((s >> 1) * kPanel64 + t * 2048));
+  }
+  __device__ __forceinline__ u32x4 frag_t(const char* p, int t, int s) const {
+    const int b = (t ^ s) & 1, o = (t >> 1) * kPanel64 + s * 2048;
+    const char *q0 = p + c[0][b] + o, *q1 = p + c[1][b] + o;
+    return (u32x4){*reinterpret_cast<const unsigned*>(q0), *reinterpret_cast<const unsigned*>(q0 + 128),
+                   *reinterpret_cast<const unsigned*>(q1), *reinterpret_cast<const unsigned*>(q1 + 128)};
+  }
+  __device__ __forceinline__ f32x4 at4(const char* p, int t, int ct) const {
+    return *reinterpret_cast<const f32x4*>(p + f[(ct ^ t) & 1] + ((ct >> 1) * kPanel64 + t * 2048));
+  }
+};
+
 // A chunk's gates for one head in LDS, base 2 logarithms: b in two parts, exp(b), the rates, and exp(b_63 - b) r.
 struct Gates {
   float hi[kDC], lo[kDC], eb[kDC], r[kDC], w[kDC];
 };
 
 // A chunk's gates from its lanes' dt (one wave; tokens past len leave the state alone).  Log decays below kResetDecay
-// are taken as that: exp of them is zero either way, and sums of 64 stay where `hi` is exact.  rest: exp(b_63 - b), if
-// wanted.  Returns the chunk's sum.
-__device__ __forceinline__ double make_gates(float dt, float A, float bias, bool softplus, int len, Gates* o,
-                                             float* rest = nullptr) {
+// are taken as that: exp of them is zero either way, and sums of 64 stay where `hi` is exact.  sum: the chunk's.
+struct LaneGates {
+  double sum;
+  float hi, lo, eb, r, w, rest;       // rest: exp(b_63 - b)
+};
+__device__ __forceinline__ LaneGates make_gates(float dt, float A, float bias, bool softplus, int len, Gates* o) {
   const int lane = lane_id();
-  const float r = lane < len ? scan_rate(dt, bias, softplus) : 0.f;
-  double b = lane < len ? fmax((double)A * r, (double)kResetDecay) * 1.4426950408889634 : 0.0;
+  LaneGates v;
+  v.r = lane < len ? scan_rate(dt, bias, softplus) : 0.f;
+  double b = lane < len ? fmax((double)A * v.r, (double)kResetDecay) * 1.4426950408889634 : 0.0;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
     const double up = __shfl_up(b, m, 64);
     if (lane >= m) b += up;
   }
-  const double last = __shfl(b, 63, 64);
-  const float hi = rintf((float)b * 256.f) * (1.f / 256.f);
-  o->hi[lane] = hi;
-  o->lo[lane] = (float)(b - (double)hi);
-  o->eb[lane] = exp2_hw((float)b);
-  o->r[lane] = r;
-  const float f = exp2_hw((float)(last - b));
-  o->w[lane] = r * f;
-  if (rest) rest[lane] = f;
-  return last;
+  v.sum = __shfl(b, 63, 64);
+  v.hi = rintf((float)b * 256.f) * (1.f / 256.f);
+  v.lo = (float)(b - (double)v.hi);
+  v.eb = exp2_hw((float)b);
+  v.rest = exp2_hw((float)(v.sum - b));
+  v.w = v.r * v.rest;
+  o->hi[lane] = v.hi;
+  o->lo[lane] = v.lo;
+  o->eb[lane] = v.eb;
+  o->r[lane] = v.r;
+  o->w[lane] = v.w;
+  return v;
 }
+// The same as the backward pass keeps them for its chunk-local part, with the rate's derivative by dt.
+struct KeptGates {
+  Gates g;
+  float rest[kDC], slope[kDC];
+};
 
-// Values as three bf16 operands.
-__device__ __forceinline__ void split3(const float (&v)[8], u32x4& h, u32x4& m, u32x4& l) {
-  f32x4 c[2] = {{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
-  h = Mat<bf16>::frag(c);
+// Values as three bf16 operands, each the 8 leading bits of what the ones before left: 24 bits in all.
+__device__ __forceinline__ void split3(const float (&x)[8], u32x4& h, u32x4& m, u32x4& l) {
+  unsigned v[8];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const u32x4 w = k ? m : h;
+  for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(x[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int k = 0; k < 3; ++k) {
+    u32x4& w = k == 0 ? h : k == 1 ? m : l;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        c[i][2 * j] -= __uint_as_float(w[2 * i + j] << 16);
-        c[i][2 * j + 1] -= __uint_as_float(w[2 * i + j] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      w[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07060302);
+      if (k < 2) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const unsigned u = v[2 * i + j];
+          v[2 * i + j] = __float_as_uint(__uint_as_float(u) - __uint_as_float(u & 0xffff0000u));
+        }
       }
-    (k ? l : m) = Mat<bf16>::frag(c);
+    }
   }
 }
 
@@ -183,16 +262,17 @@ template <typename T, int CT, int NT> struct StateRows {
   }
   // += the weighted outer products of a step's tokens: x[c] their features of this wave's blocks, `cols` their rows of N
   // in LDS.  All blocks of P at once, so that an operand is read once.
-  __device__ __forceinline__ void add(const u32x4 (&x)[CT], const char* cols, int step, const float* weights, int N) {
+  // Columns past N are zero in LDS; whole halves of the widest states are passed over.
+  __device__ __forceinline__ void add(const LaneAt<T>& L, const u32x4 (&x)[CT], const char* cols, int step,
+                                      const float* weights, int N) {
     static_assert(CT <= 2, "blocks");
     const Scaled<T> u0(x[0], weights), u1(x[CT - 1], weights);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (t / Mat<T>::TPS * Mat<T>::KB < N) {
-        const u32x4 f = Panels<T>::frag_t(cols, t, step, lane_id());
-        s[0][t] = u0.mma(f, s[0][t]);
-        if (CT == 2) s[CT - 1][t] = u1.mma(f, s[CT - 1][t]);
-      }
+      if (NT > 8 && t % 4 == 0 && t * 16 >= N) break;
+      const u32x4 f = L.frag_t(cols, t, step);
+      s[0][t] = u0.mma(f, s[0][t]);
+      if (CT == 2) s[CT - 1][t] = u1.mma(f, s[CT - 1][t]);
     }
   }
   // A decay that is zero in fp32 empties the state, whatever it holds.

@@ -11,7 +11,8 @@
 //   dr_t = x_t . du_t + A dg_t,  dA = sum_t r_t dg_t,  ddt_t = dr_t, with softplus times its derivative.
 // The states S and, walking back, dS' = exp(b_63) dS + sum_i exp(b_i) dO_i C_i^T are kept for every chunk (scan_walk.hpp);
 // what is local to a chunk is made for all chunks at once, a workgroup for a chunk and group, its heads one after the
-// other, dB and dC staying in registers over them.  In bf16 kept states and all fp32 operands are pairs of bf16 values.
+// other, dB and dC staying in registers over them.  In bf16, states enter as three bf16 values (their fp32's 24 bits), the
+// decayed products as two; no product of rounded values goes into dg: the pairs' sums are of fp32 results alone.
 #include "scan_walk.hpp"
 
 namespace ttt {
@@ -23,34 +24,35 @@ template <typename T, bool LDS> struct Features {
   const T* rows;
   int64_t pitch;
   int len, N;
-  __device__ __forceinline__ u32x4 frag(int r, int s, int g) const {
-    if constexpr (LDS) return Panels<T>::frag(lds, r, s, g);
-    const int n = s * 16 + g * 4;
+  __device__ __forceinline__ u32x4 frag(const LaneAt<T>& L, int t, int s) const {
+    if constexpr (LDS) return L.frag(lds, t, s);
+    const int r = Mat<T>::row(t, lane_id() & 15), n = s * 16 + (lane_id() >> 4) * 4;
     return r < len && n < N ? *reinterpret_cast<const u32x4*>(rows + r * pitch + n) : (u32x4){0, 0, 0, 0};
   }
-  __device__ __forceinline__ u32x4 frag_t(int tile, int s, int lane) const {
-    if constexpr (LDS) return Panels<T>::frag_t(lds, tile, s, lane);
-    const int n = tile * 16 + (lane & 15), r = s * 16 + (lane >> 4) * 4;
+  __device__ __forceinline__ u32x4 frag_t(const LaneAt<T>& L, int t, int s) const {
+    if constexpr (LDS) return L.frag_t(lds, t, s);
+    const int n = t * 16 + (lane_id() & 15), r = s * 16 + (lane_id() >> 4) * 4;
     u32x4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = r + i < len && n < N ? __float_as_uint((float)rows[(r + i) * pitch + n]) : 0u;
     return o;
   }
-  __device__ __forceinline__ f32x4 at4(int r, int n) const {
-    if constexpr (LDS) return load4((const T*)(lds + Panels<T>::at(r, n)));
+  __device__ __forceinline__ f32x4 at4(const LaneAt<T>& L, int t, int ct) const {
+    if constexpr (LDS) return L.at4(lds, t, ct);
+    const int r = Mat<T>::row(t, lane_id() & 15), n = Mat<T>::row(ct, (lane_id() >> 4) * 4);
     return r < len && n < N ? load4(rows + r * pitch + n) : (f32x4){0.f, 0.f, 0.f, 0.f};
   }
 };
 
-// BV: rows of P that are in LDS at a time.
-template <typename T, int DN_, int BV_, bool LDS_> struct GradShape {
-  static constexpr int DN = DN_, BV = BV_;
+// A head's block of 64 rows of P: x and dO of the chunk's tokens, and 64 columns of S and dS at a time.
+constexpr int kBV = 64, kBN = 64;
+template <typename T, int DN_, bool LDS_> struct GradShape {
+  static constexpr int DN = DN_, NB = DN / kBN, KS = kBN / Mat<T>::KB;
   static constexpr bool LDS = LDS_;
-  using Rows = Panels<T, BV>;                                // of S and dS
-  static constexpr int BVX = BV * (int)sizeof(T) < 128 ? 128 / (int)sizeof(T) : BV;
-  static constexpr int SP = Mat<T>::kSplit ? 2 : 1;
-  static constexpr int kB = LDS ? Panels<T>::bytes(DN) : 0, kS = Rows::bytes(DN), kX = Panels<T>::bytes(BVX);
-  static constexpr int oS = 2 * kB, oD = oS + SP * kS, oX = oD + SP * kS, oY = oX + kX, kSmem = oY + kX;
+  static constexpr int SP = Mat<T>::kSplit ? 3 : 1;          // planes of a state: their sum is it
+  static constexpr int kB = LDS ? Panels<T>::bytes(DN) : 0, kS = Panels<T, kBV>::bytes(kBN), kX = Panels<T>::bytes(kBV);
+  static constexpr int kM = Panels<T>::bytes(kDC);           // a 64 x 64 matrix (bf16: and what its rounding left)
+  static constexpr int oS = 2 * kB, oX = oS + 2 * SP * kS, oM = oX + 2 * kX, kSmem = oM + kM * (Mat<T>::kSplit ? 2 : 1);
 };
 
 // x summed over the four lanes that hold a token.
@@ -58,323 +60,465 @@ __device__ __forceinline__ float token_sum(float x) {
   x += __shfl_xor(x, 16, 64);
   return x + __shfl_xor(x, 32, 64);
 }
+// x summed over the 16 lanes of a group.
+template <int ROR> __device__ __forceinline__ float ror_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + ROR, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float group_sum(float x) { return ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(x)))); }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]; }
+// Keeps the instructions of a phase together: reads drawn ahead over phases cost registers, and what is then spilled waits
+// for the loads under way.
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
+// 16 bytes at `base` + off, zero for off >= kOOB.
+__device__ __forceinline__ u32x4 load_or_zero(__amdgpu_buffer_rsrc_t rs, unsigned off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+}
 
-// One workgroup of 8 waves per chunk slot and group; waves w and w + 4 have the tokens row(w, .) as their products'
-// columns and half of the features (of P and of N) each.
-template <typename T, int DN, int BV, bool LDS>
+// Row block and step of a triangular matrix's fragment.
+template <typename T> __device__ __forceinline__ void tri_place(int f, int* t, int* s) {
+  if constexpr (sizeof(T) == 2) {
+    *t = f < 2 ? f : 2 + ((f - 2) >> 1);
+    *s = f < 2 ? 0 : (f - 2) & 1;
+  } else {
+    *t = f < 1 ? 0 : f < 3 ? 1 : f < 6 ? 2 : 3;
+    *s = f - *t * (*t + 1) / 2;
+  }
+}
+
+// 8 fp32 values of a row of a state block to its planes: each the 8 leading bits of what the ones before left, 24 in all.
+template <typename T, int SP>
+__device__ __forceinline__ void put_planes(f32x4 a, f32x4 b, char* plane, int stride, int r, int c8) {
+  if constexpr (sizeof(T) == 2) {
+    char* at = plane + r * 128 + ((c8 ^ panel_swz(r)) << 4);
+    unsigned v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __float_as_uint(a[i]);
+      v[4 + i] = __float_as_uint(b[i]);
+    }
+#pragma unroll
+    for (int k = 0; k < SP; ++k) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07060302);
+        if (k + 1 < SP) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const unsigned u = v[2 * i + j];
+            v[2 * i + j] = __float_as_uint(__uint_as_float(u) - __uint_as_float(u & 0xffff0000u));
+          }
+        }
+      }
+      *reinterpret_cast<u32x4*>(at + k * stride) = w;
+    }
+  } else {
+    *reinterpret_cast<f32x4*>(plane + Panels<T, kBV>::at(r, c8 * 8)) = a;
+    *reinterpret_cast<f32x4*>(plane + Panels<T, kBV>::at(r, c8 * 8 + 4)) = b;
+  }
+}
+
+// What the gradients of a chunk's rates are made of, for one head: with Z_ij = (C_i . B_j) (dO_i . x_j) exp(b_i - b_j),
+// by token: sums of Z_ij r_j over j < i (by steps of j), of Z_ij over i > j (by blocks of i), Z_ii and dO_i . x_i; C_i . S^T
+// dO_i and B_j . dS^T x_j by blocks of N; and <S, dS> by waves.
+template <typename T> struct TokenSums {
+  float rows[kDC / Mat<T>::KB][kDC], cols[4][kDC], diag[2][kDC], dots[8][kDC], ss[8], pad[8];
+};
+
+// One workgroup of 8 waves per chunk slot and group, its heads one after the other.
+//   waves 0-3  S^T dO and dC, waves 4-7  dS^T x and dB: block w & 3 of every 64 features of N, all tokens
+//   du         blocks 2 (w & 1) and the next of P, tokens row(w >> 1, .)
+//   C B^T, dO x^T and their decayed forms by fragments, a wave one (fp32: two); they go to LDS once for all waves
+// States come as fp32, the next block's loads under way while one is worked on, and are cut into planes on their way to
+// LDS; sums that go into ddt are of all three planes, dx of two.
+template <typename T, int DN, bool LDS>
 __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
+#if __HIP_DEVICE_COMPILE__
   using M = Mat<T>;
-  using Z = GradShape<T, DN, BV, LDS>;
-  using Rows = typename Z::Rows;
-  constexpr int NS = DN / M::KB, CS = kDC / M::KB, VS = BV / M::KB, NTH = DN / 32, PT = BV / 32, U = M::TPS;
-  constexpr int PB = U == 2 && PT == 2 ? 2 : 1;              // blocks of P that are stored as one
+  using Z = GradShape<T, DN, LDS>;
+  constexpr int NS = DN / M::KB, CS = kDC / M::KB, NB = Z::NB, KS = Z::KS, U = M::TPS, SP = Z::SP;
+  constexpr int F = (M::kTri + 7) / 8, XU = 8 * (int)sizeof(T) / 16;   // fragments a wave; 16-byte pieces of 8 elements
+  constexpr int PB = U;                                      // blocks of P that are stored as one
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ Gates q;
-  __shared__ float rest[kDC], rowsum[kDC], colsum[kDC], qsum[2][kDC], zsum[2][kDC], usum[2][kDC], wsum[8], diag[4];
+  __shared__ KeptGates kept;
+  __shared__ TokenSums<T> sums;
+  const Gates& q = kept.g;
   const ScanArgs& p = a.f;
   const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int grp = id % p.G, slot = id / p.G, shared = p.H / p.G;
+  const int grp = id % p.G, slot = id / p.G, shared = p.H / p.G, head0 = grp * shared;
   const ChunkPlace c = chunk_place(p.seqs, slot);
-  if (c.len <= 0) {                                          // nothing of the sums over tokens
-    for (int i = threadIdx.x; i < 4 * shared; i += 512) a.part[((int64_t)slot * p.H + grp * shared) * 4 + i] = 0.f;
-    return;
-  }
-  const int wave = wave_id(), t = wave & 3, hf = wave >> 2, lane = lane_id(), m = lane & 15, g = lane >> 4;
-  const int tok = M::row(t, m);                              // this lane's token
-  const int64_t size = (int64_t)p.P * p.N;
-  const Features<T, LDS> B{smem, (const T*)p.B + c.b * p.sB.b + grp * p.sB.h + c.tok0 * p.sB.t, p.sB.t, c.len, p.N};
-  const Features<T, LDS> C{smem + Z::kB, (const T*)p.C + c.b * p.sC.b + grp * p.sC.h + c.tok0 * p.sC.t, p.sC.t, c.len, p.N};
+  if (c.len <= 0) return;
+  const int tid = threadIdx.x, wave = wave_id(), side = wave >> 2, nt = wave & 3, lane = lane_id(), m = lane & 15, g = lane >> 4;
+  const int P = p.P, N = p.N, len = c.len;
+  const int64_t size = (int64_t)P * N;
+  const Features<T, LDS> B{smem, (const T*)p.B + c.b * p.sB.b + grp * p.sB.h + c.tok0 * p.sB.t, p.sB.t, len, N};
+  const Features<T, LDS> C{smem + Z::kB, (const T*)p.C + c.b * p.sC.b + grp * p.sC.h + c.tok0 * p.sC.t, p.sC.t, len, N};
   if constexpr (LDS) {
-    PanelLoader<T, DN, 8>(p.sB.t * sizeof(T), p.N * sizeof(T)).issue(B.rows, c.len, smem);
-    PanelLoader<T, DN, 8>(p.sC.t * sizeof(T), p.N * sizeof(T)).issue(C.rows, c.len, smem + Z::kB);
+    PanelLoader<T, DN, 8>(p.sB.t * sizeof(T), N * sizeof(T)).issue(B.rows, len, smem);
+    PanelLoader<T, DN, 8>(p.sC.t * sizeof(T), N * sizeof(T)).issue(C.rows, len, smem + Z::kB);
+  }
+  LaneAt<T> L(lane);
+  L.keep();
+  char *const Sp = smem + Z::oS, *const Dp = Sp + SP * Z::kS, *const Xp = smem + Z::oX, *const Yp = Xp + Z::kX, *const Mp = smem + Z::oM;
+
+  // Heads of the group, from the first on.
+  const float *S = a.S + ((int64_t)slot * p.H + head0) * size, *dS = a.dS + ((int64_t)slot * p.H + head0) * size;
+  const T* x = (const T*)p.x + c.b * p.sx.b + head0 * p.sx.h + c.tok0 * p.sx.t;
+  const T* y = (const T*)a.dO + c.b * a.sdO.b + head0 * a.sdO.h + c.tok0 * a.sdO.t;
+  const char* gates = (const char*)(a.gates + (int64_t)slot * p.H + head0);
+  T* dx = (T*)a.dx + c.b * a.sdx.b + head0 * a.sdx.h + c.tok0 * a.sdx.t;
+  char* to = a.sums + ((int64_t)slot * p.H + head0) * sizeof(TokenSums<T>);
+
+  const int dtile = wave >> 1, dtok = M::row(dtile, m), dblock = 2 * (wave & 1);   // du's tokens and blocks of P
+
+  // What is on its way: 8 columns of a row of S and dS, 8 of a token's x and dO.
+  const int row8 = tid >> 3, col8 = (tid & 7) * 8;
+  const unsigned soff = (unsigned)(row8 * N + col8) * 4u;
+  const unsigned xoff = row8 < len ? (unsigned)row8 * (unsigned)(p.sx.t * sizeof(T)) + col8 * (unsigned)sizeof(T) : kOOB;
+  const unsigned yoff = row8 < len ? (unsigned)row8 * (unsigned)(a.sdO.t * sizeof(T)) + col8 * (unsigned)sizeof(T) : kOOB;
+  const unsigned dxoff = dtok < len ? (unsigned)dtok * (unsigned)(a.sdx.t * sizeof(T)) : kOOB;
+  u32x4 ns[2], nd[2], nx[XU], ny[XU];
+  constexpr int GT = sizeof(KeptGates) / 16;                 // threads that bring the gates
+  u32x4 ngate = {0, 0, 0, 0};
+  auto load_states = [&](const float* s, const float* d, int p0, int n0) __attribute__((always_inline)) {
+    const unsigned off = p0 + row8 < P && n0 + col8 < N ? soff : kOOB;
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(s + (int64_t)p0 * N + n0), rd = rows_rsrc(d + (int64_t)p0 * N + n0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      ns[k] = load_or_zero(rs, off + 16 * k);
+      nd[k] = load_or_zero(rd, off + 16 * k);
+    }
+  };
+  auto load_rows = [&](const T* xh, const T* yh, int p0) __attribute__((always_inline)) {
+    const bool in = p0 + col8 < P;
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(xh + p0), ry = rows_rsrc(yh + p0);
+#pragma unroll
+    for (int k = 0; k < XU; ++k) {
+      nx[k] = load_or_zero(rx, in ? xoff + 16 * k : kOOB);
+      ny[k] = load_or_zero(ry, in ? yoff + 16 * k : kOOB);
+    }
+  };
+  auto load_gates = [&](const char* from) __attribute__((always_inline)) {
+    if (wave < (GT + 63) / 64) ngate = load_or_zero(make_rsrc(from, sizeof(KeptGates)), tid * 16);
+  };
+  load_rows(x, y, 0);
+  load_gates(gates);
+  load_states(S, dS, 0, 0);
+  if constexpr (LDS) {
     wait_vm<0>();
     __syncthreads();
   }
-  const PanelLoader<T, DN, 8, BV> sload(p.N * sizeof(T), p.N * sizeof(T));
-  char *const Sp = smem + Z::oS, *const Dp = smem + Z::oD, *const Xp = smem + Z::oX, *const Yp = smem + Z::oY;
-
-  // C_i . B_j: the lane's token as i with j <= i in the rows, and as j with i >= j
-  f32x4 gi[CS][U], gj[CS][U];
+  // C_i . B_j, token i = row(t, m), j = row(s U + u, 4 g + 0..3)
+  f32x4 G[F][U];
+  int ft[F], fs[F];
 #pragma unroll
-  for (int s = 0; s < CS; ++s)
+  for (int k = 0; k < F; ++k) {
+    tri_place<T>(min(wave + 8 * k, M::kTri - 1), &ft[k], &fs[k]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      gi[s][u] = gj[s][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      const int r = M::row(s * U + u, m);
+    for (int u = 0; u < U; ++u) G[k][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if (wave + 8 * k < M::kTri)
 #pragma unroll
-      for (int ns = 0; ns < NS; ++ns) {
-        if (ns * M::KB >= p.N) continue;
-        if (s < M::steps(t)) gi[s][u] = M::mma(B.frag(r, ns, g), C.frag(tok, ns, g), gi[s][u]);
-        if (s >= M::first(t)) gj[s][u] = M::mma(C.frag(r, ns, g), B.frag(tok, ns, g), gj[s][u]);
+      for (int n = 0; n < NS; ++n) {
+        const u32x4 f = C.frag(L, ft[k], n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) G[k][u] = M::mma(B.frag(L, fs[k] * U + u, n), f, G[k][u]);
       }
-    }
-  f32x4 dC[NTH], dB[NTH];
+  }
+  f32x4 acc[NB][4];                                          // dC or dB: block nt of every 64 of N, tokens row(t, m)
 #pragma unroll
-  for (int k = 0; k < NTH; ++k) dC[k] = dB[k] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[n][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const char *const state = side ? Dp : Sp, *const other = side ? Xp : Yp;
+  const float* const scales = side ? q.w : q.eb;
+  const Features<T, LDS> own = side ? B : C, cross = side ? C : B;
 
-  for (int h = grp * shared; h < (grp + 1) * shared; ++h) {
-    const int64_t sh = (int64_t)slot * p.H + h;
-    const T *S = (const T*)(a.S + sh * kept_bytes(p.P, p.N)), *dS = (const T*)(a.dS + sh * kept_bytes(p.P, p.N));
-    const T* x = (const T*)p.x + c.b * p.sx.b + h * p.sx.h + c.tok0 * p.sx.t;
-    const T* y = (const T*)a.dO + c.b * a.sdO.b + h * a.sdO.h + c.tok0 * a.sdO.t;
-    const float D = p.D ? p.D[h] : 0.f, A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-    const float dt = wave == 0 && lane < c.len ? p.dt[c.b * p.sdt.b + h * p.sdt.h + (c.tok0 + lane) * p.sdt.t] : 0.f;
-    f32x4 so[NTH], sx[NTH], vi[CS][U], vj[CS][U];            // S^T dO, dS^T x; dO_i . x_j, token i, token j
-    u32x4 mh[CS], ml[CS];                                    // (C_i . B_j) exp(b_i - b_j), token j
+  for (int h = head0; h < head0 + shared; ++h) {
+    const float D = p.D ? p.D[h] : 0.f;
+    f32x4 V[F][U], E[F][U];                                  // dO_i . x_j; exp(b_i - b_j), 0 for j > i
 #pragma unroll
-    for (int k = 0; k < NTH; ++k) so[k] = sx[k] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < F; ++k)
 #pragma unroll
-    for (int s = 0; s < CS; ++s)
+      for (int u = 0; u < U; ++u) V[k][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    float ss = 0.f, dot[4] = {0.f, 0.f, 0.f, 0.f};           // <S, dS>; C_i . S^T dO_i or B_j . dS^T x_j
+    for (int p0 = 0; p0 < P; p0 += kBV) {
+      const bool more = p0 + kBV < P, next = more || h + 1 < head0 + shared;
+      f32x4 du[2];
+      du[0] = du[1] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < U; ++u) vi[s][u] = vj[s][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    float ss = 0.f, zs = 0.f, us = 0.f;                      // <S, dS>; x_j . dS B_j; x_j . du_j
-    for (int p0 = 0; p0 < p.P; p0 += BV) {
-      const int rows = min(BV, p.P - p0);
-      __syncthreads();                                       // the block (and the head) before has been read
+      for (int nb = 0; nb < NB; ++nb) {
+        const int n0 = nb * kBN;
+        if (NB > 2 && n0 >= N) continue;
+        if (nb == 0) {
 #pragma unroll
-      for (int k = 0; k < Z::SP; ++k) {
-        sload.issue(S + k * size + (int64_t)p0 * p.N, rows, Sp + k * Z::kS);
-        sload.issue(dS + k * size + (int64_t)p0 * p.N, rows, Dp + k * Z::kS);
+          for (int k = 0; k < XU; ++k) {
+            *reinterpret_cast<u32x4*>(Xp + Panels<T>::at(row8, col8 + k * (16 / (int)sizeof(T)))) = nx[k];
+            *reinterpret_cast<u32x4*>(Yp + Panels<T>::at(row8, col8 + k * (16 / (int)sizeof(T)))) = ny[k];
+          }
+          if (p0 == 0 && tid < GT) reinterpret_cast<u32x4*>(&kept)[tid] = ngate;
+        }
+        f32x4 s2[2], d2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          s2[k] = __builtin_bit_cast(f32x4, ns[k]);
+          d2[k] = __builtin_bit_cast(f32x4, nd[k]);
+          ss += dot4(s2[k], d2[k]);
+        }
+        put_planes<T, SP>(s2[0], s2[1], Sp, Z::kS, row8, tid & 7);
+        put_planes<T, SP>(d2[0], d2[1], Dp, Z::kS, row8, tid & 7);
+        __syncthreads();
+        if (nb + 1 < NB && (NB <= 2 || n0 + kBN < N)) {
+          load_states(S, dS, p0, n0 + kBN);
+        } else if (next) {
+          load_rows(more ? x : x + p.sx.h, more ? y : y + a.sdO.h, more ? p0 + kBV : 0);
+          if (!more) load_gates(gates + sizeof(KeptGates));
+          load_states(more ? S : S + size, more ? dS : dS + size, more ? p0 + kBV : 0, 0);
+        }
+        phase();
+        if (nb == 0) {
+#pragma unroll
+          for (int k = 0; k < F; ++k) {
+            if (wave + 8 * k >= M::kTri) continue;
+            int i = M::row(ft[k], m);
+            asm volatile("" : "+v"(i));                    // (what follows from it is made again, not kept in masks)
+#pragma unroll
+            for (int v = 0; v < KS; ++v) {
+              const u32x4 f = L.frag(Yp, ft[k], v);
+#pragma unroll
+              for (int u = 0; u < U; ++u) V[k][u] = M::mma(L.frag(Xp, fs[k] * U + u, v), f, V[k][u]);
+            }
+            if (p0 == 0) {                                   // (C_i . B_j) exp(b_i - b_j)
+              const float ih = q.hi[i], il = q.lo[i];
+              f32x4 w[U];
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const int j = M::row(fs[k] * U + u, 4 * g);
+                const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jl = *reinterpret_cast<const f32x4*>(q.lo + j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  E[k][u][e] = j + e <= i ? exp2_hw((ih - jh[e]) + (il - jl[e])) : 0.f;
+                  w[u][e] = G[k][u][e] * E[k][u][e];
+                }
+              }
+              u32x4 hi, lo;
+              M::split(w, hi, lo);
+              char* f = Mp + Panels<T>::at(i, M::row(fs[k] * U, 4 * g));
+              *reinterpret_cast<u32x4*>(f) = hi;
+              if (M::kSplit) *reinterpret_cast<u32x4*>(f + Z::kM) = lo;
+            }
+          }
+        }
+        phase();
+        // S^T dO (dS^T x)
+        {
+          u32x4 f[SP][KS];
+#pragma unroll
+          for (int z = 0; z < SP; ++z)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) f[z][s] = L.frag_t(state + z * Z::kS, nt, s);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int i = M::row(t, m);
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              const u32x4 b = L.frag(other, t, s);
+#pragma unroll
+              for (int z = SP - 1; z >= 0; --z) o = M::mma(f[z][s], b, o);
+            }
+            dot[t] += dot4(o, own.at4(L, t, 4 * nb + nt));
+            acc[nb][t] += scales[i] * o;
+            phase();
+          }
+        }
+        // dS B
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const u32x4 b = B.frag(L, dtile, nb * KS + s);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int z = (SP > 1 ? 1 : 0); z >= 0; --z)
+              du[k] = M::mma(L.frag(Dp + z * Z::kS, dblock + k, s), b, du[k]);
+        }
+        __syncthreads();                                     // the planes have been read, (C B^T exp) is there
       }
-      PanelLoader<T, Z::BVX, 8>(p.sx.t * sizeof(T), rows * sizeof(T)).issue(x + p0, c.len, Xp);
-      PanelLoader<T, Z::BVX, 8>(a.sdO.t * sizeof(T), rows * sizeof(T)).issue(y + p0, c.len, Yp);
-      if (p0 == 0 && wave == 0) make_gates(dt, A, bias, p.softplus, c.len, &q, rest);
-      wait_vm<0>();
-      __syncthreads();
-      if (p0 == 0) {
-        const float th = q.hi[tok], tl = q.lo[tok];
+      // dx: of the tokens behind in the chunk, and of the state behind it
+      {
+        const float f = kept.rest[dtok], r = q.r[dtok];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) du[k] *= f;
 #pragma unroll
         for (int s = 0; s < CS; ++s) {
-          if (s < M::first(t)) continue;
-          f32x4 v[U];
+          if (s < M::first(dtile)) continue;
+          const u32x4 hi = L.frag_t(Mp, dtile, s);
+          u32x4 lo;
+          if constexpr (M::kSplit) lo = L.frag_t(Mp + Z::kM, dtile, s);
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int i = M::row(s * U + u, 4 * g);
-            const f32x4 ih = *reinterpret_cast<const f32x4*>(q.hi + i), il = *reinterpret_cast<const f32x4*>(q.lo + i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[u][e] = i + e >= tok ? gj[s][u][e] * exp2_hw((ih[e] - th) + (il[e] - tl)) : 0.f;
-          }
-          M::split(v, mh[s], ml[s]);
-        }
-      }
-      u32x4 fx[VS], fy[VS];                                  // x, dO of the lane's token
-#pragma unroll
-      for (int s = 0; s < VS; ++s) {
-        fx[s] = Panels<T>::frag(Xp, tok, s, g);
-        fy[s] = Panels<T>::frag(Yp, tok, s, g);
-      }
-#pragma unroll
-      for (int s = 0; s < CS; ++s)
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int r = M::row(s * U + u, m);
-#pragma unroll
-          for (int v = 0; v < VS; ++v) {
-            if (s < M::steps(t)) vi[s][u] = M::mma(Panels<T>::frag(Xp, r, v, g), fy[v], vi[s][u]);
-            if (s >= M::first(t)) vj[s][u] = M::mma(Panels<T>::frag(Yp, r, v, g), fx[v], vj[s][u]);
+          for (int k = 0; k < 2; ++k) {
+            const u32x4 o = L.frag_t(Yp, dblock + k, s);
+            if constexpr (M::kSplit) du[k] = M::mma(o, lo, du[k]);
+            du[k] = M::mma(o, hi, du[k]);
           }
         }
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(dx + p0);
 #pragma unroll
-      for (int k = 0; k < NTH; ++k) {
-        const int n = hf * NTH + k;
-        if (n / U * M::KB >= p.N) continue;
-#pragma unroll
-        for (int v = 0; v < VS; ++v)
-#pragma unroll
-          for (int z = Z::SP - 1; z >= 0; --z) {
-            so[k] = M::mma(Rows::frag_t(Sp + z * Z::kS, n, v, lane), fy[v], so[k]);
-            sx[k] = M::mma(Rows::frag_t(Dp + z * Z::kS, n, v, lane), fx[v], sx[k]);
-          }
-      }
-      // du of the lane's token, rows of P
-      const float f = rest[tok], r = q.r[tok];
-      f32x4 du[PT];
-#pragma unroll
-      for (int k = 0; k < PT; ++k) {
-        const int pt = hf * PT + k, row = M::row(pt, m);
-        du[k] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ns = 0; ns < NS; ++ns) {
-          if (ns * M::KB >= p.N) continue;
-          const u32x4 b = B.frag(tok, ns, g);
-#pragma unroll
-          for (int z = Z::SP - 1; z >= 0; --z) du[k] = M::mma(Rows::frag(Dp + z * Z::kS, row, ns, g), b, du[k]);
-        }
-        du[k] *= f;
-        const f32x4 xt = load4((const T*)(Xp + Panels<T>::at(tok, M::row(pt, 4 * g))));
-        zs += dot4(du[k], xt);
-#pragma unroll
-        for (int s = 0; s < CS; ++s) {
-          if (s < M::first(t)) continue;
-          const u32x4 o = Panels<T>::frag_t(Yp, pt, s, lane);
-          if (M::kSplit) du[k] = M::mma(o, ml[s], du[k]);
-          du[k] = M::mma(o, mh[s], du[k]);
-        }
-        us += dot4(du[k], xt);
-      }
-      if (tok < c.len) {
-        T* o = (T*)a.dx + c.b * a.sdx.b + h * a.sdx.h + (int64_t)(c.tok0 + tok) * a.sdx.t + p0;
-#pragma unroll
-        for (int k = 0; k < PT; k += PB) {
-          const int pp = M::row(hf * PT + k, 4 * g);
-          if (pp >= rows) continue;
+        for (int k = 0; k < 2; k += PB) {
+          const int pp = M::row(dblock + k, 4 * g);
           f32x4 v[PB];
 #pragma unroll
-          for (int e = 0; e < PB; ++e) v[e] = r * du[k + e] + D * load4((const T*)(Yp + Panels<T>::at(tok, pp + 4 * e)));
-          if constexpr (PB == 2)
-            *reinterpret_cast<u32x4*>(o + pp) = M::frag(v);
-          else
-            store4(o + pp, v[0][0], v[0][1], v[0][2], v[0][3]);
+          for (int e = 0; e < PB; ++e) v[e] = r * du[k + e] + D * L.at4(Yp, dtile, dblock + k + e);
+          // (outside of the rows and of P: nothing is written)
+          const unsigned off = p0 + pp < P ? dxoff + pp * (unsigned)sizeof(T) : kOOB;
+          __builtin_amdgcn_raw_buffer_store_b128(M::frag(v), rs, off, 0, 0);
         }
       }
-      // rows past the block's are zero in LDS; the same slots of all panels hold the same element
-      for (int at = threadIdx.x * 16; at < Z::kS; at += 512 * 16) {
-        const u32x4 s0 = *reinterpret_cast<const u32x4*>(Sp + at), d0 = *reinterpret_cast<const u32x4*>(Dp + at);
-        if constexpr (M::kSplit) {
-          float u[8], v[8], u1[8], v1[8];
-          unpack8(s0, u);
-          unpack8(d0, v);
-          unpack8(*reinterpret_cast<const u32x4*>(Sp + Z::kS + at), u1);
-          unpack8(*reinterpret_cast<const u32x4*>(Dp + Z::kS + at), v1);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) ss += (u[j] + u1[j]) * (v[j] + v1[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ss += __uint_as_float(s0[j]) * __uint_as_float(d0[j]);
-        }
-      }
+      __syncthreads();                                       // x, dO and (C B^T exp) have been read
     }
-    // W and the tokens' products with it
-    const float th = q.hi[tok], tl = q.lo[tok], tr = q.r[tok], eb = q.eb[tok], wt = q.w[tok];
-    float rs = 0.f, cs = 0.f, trace = 0.f, qs = 0.f;
+    // W to LDS, and the sums of W_ij (C_i . B_j) / r_j over rows and columns
 #pragma unroll
-    for (int s = 0; s < CS; ++s) {
-      if (s < M::steps(t)) {
-        f32x4 v[U];
+    for (int k = 0; k < F; ++k) {
+      if (wave + 8 * k >= M::kTri) continue;
+      const int t = ft[k], s = fs[k];
+      int i = M::row(t, m);
+      asm volatile("" : "+v"(i));
+      f32x4 w[U];
+      float rs = 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = M::row(s * U + u, 4 * g);
-          const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jl = *reinterpret_cast<const f32x4*>(q.lo + j),
-                      jr = *reinterpret_cast<const f32x4*>(q.r + j);
+      for (int u = 0; u < U; ++u) {
+        const int j = M::row(s * U + u, 4 * g);
+        const f32x4 r = *reinterpret_cast<const f32x4*>(q.r + j);
+        f32x4 cs;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[u][e] = j + e <= tok ? vi[s][u][e] * exp2_hw((th - jh[e]) + (tl - jl[e])) * jr[e] : 0.f;
-            if (j + e < tok) rs += v[u][e] * gi[s][u][e];
-            if (j + e == tok) trace += vi[s][u][e];
+        for (int e = 0; e < 4; ++e) {
+          const float v = V[k][u][e] * E[k][u][e], z = v * G[k][u][e];
+          w[u][e] = v * r[e];
+          if (j + e == i) {
+            sums.diag[0][i] = z;
+            sums.diag[1][i] = V[k][u][e];
           }
+          const float below = j + e < i ? z : 0.f;
+          rs += below * r[e];
+          cs[e] = group_sum(below);
         }
-        u32x4 hi, lo;
-        M::split(v, hi, lo);
-#pragma unroll
-        for (int k = 0; k < NTH; ++k) {
-          const int n = hf * NTH + k;
-          if (n / U * M::KB >= p.N) continue;
-          const u32x4 b = B.frag_t(n, s, lane);
-          if (M::kSplit) dC[k] = M::mma(b, lo, dC[k]);
-          dC[k] = M::mma(b, hi, dC[k]);
-        }
+        if (m == 0) *reinterpret_cast<f32x4*>(&sums.cols[t][j]) = cs;
       }
-      if (s >= M::first(t)) {
-        f32x4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = M::row(s * U + u, 4 * g);
-          const f32x4 ih = *reinterpret_cast<const f32x4*>(q.hi + i), il = *reinterpret_cast<const f32x4*>(q.lo + i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[u][e] = i + e >= tok ? vj[s][u][e] * exp2_hw((ih[e] - th) + (il[e] - tl)) * tr : 0.f;
-            if (i + e > tok) cs += v[u][e] * gj[s][u][e];
-          }
-        }
-        u32x4 hi, lo;
-        M::split(v, hi, lo);
-#pragma unroll
-        for (int k = 0; k < NTH; ++k) {
-          const int n = hf * NTH + k;
-          if (n / U * M::KB >= p.N) continue;
-          const u32x4 b = C.frag_t(n, s, lane);
-          if (M::kSplit) dB[k] = M::mma(b, lo, dB[k]);
-          dB[k] = M::mma(b, hi, dB[k]);
-        }
-      }
+      rs = token_sum(rs);
+      if (g == 0) sums.rows[s][i] = rs;
+      u32x4 hi, lo;
+      M::split(w, hi, lo);
+      char* f = Mp + Panels<T>::at(i, M::row(s * U, 4 * g));
+      *reinterpret_cast<u32x4*>(f) = hi;
+      if (M::kSplit) *reinterpret_cast<u32x4*>(f + Z::kM) = lo;
     }
 #pragma unroll
-    for (int k = 0; k < NTH; ++k) {
-      const int n = M::row(hf * NTH + k, 4 * g);
-      if ((hf * NTH + k) / U * M::KB >= p.N) continue;
-      qs += dot4(so[k], C.at4(tok, n));
-      dC[k] += eb * so[k];
-      dB[k] += wt * sx[k];
+    for (int t = 0; t < 4; ++t) {
+      const float d = token_sum(dot[t]);
+      if (g == 0) sums.dots[wave][M::row(t, m)] = d;
     }
-    rs = token_sum(rs);
-    cs = token_sum(cs);
-    qs = token_sum(qs) * eb;
-    zs = token_sum(zs) * tr;
-    us = token_sum(us);
-    trace = token_sum(trace);
-#pragma unroll
-    for (int i = 1; i < 16; i <<= 1) trace += __shfl_xor(trace, i, 64);
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) ss += __shfl_xor(ss, i, 64);
-    if (g == 0) {
-      if (hf == 0) {
-        rowsum[tok] = rs;
-        colsum[tok] = cs;
-      }
-      qsum[hf][tok] = qs;
-      zsum[hf][tok] = zs;
-      usum[hf][tok] = us;
-    }
-    if (lane == 0) {
-      wsum[wave] = ss;
-      if (hf == 0) diag[t] = trace;
-    }
+    ss = token_sum(group_sum(ss));
+    if (lane == 0) sums.ss[wave] = ss;
     __syncthreads();
-    if (wave == 0) {                                         // lane: token
-      double R = (double)colsum[lane] - rowsum[lane], zq = zsum[0][lane] + zsum[1][lane], qq = qsum[0][lane] + qsum[1][lane];
-      const double r0 = R, z0 = zq;
+    // what a token has of the chunk's other tokens
+    auto others = [&](auto back) __attribute__((always_inline)) {
+      constexpr bool BACK = decltype(back)::value;
 #pragma unroll
-      for (int i = 1; i < 64; i <<= 1) {
-        const double up = __shfl_up(R, i, 64), uz = __shfl_up(zq, i, 64), dq = __shfl_down(qq, i, 64);
-        if (lane >= i) {
-          R += up;
-          zq += uz;
+      for (int s = 0; s < CS; ++s) {
+        u32x4 f[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+          if (NB <= 2 || n * kBN < N) f[n] = cross.frag_t(L, 4 * n + nt, s);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (BACK ? s < M::first(t) : s >= M::steps(t)) continue;
+          const u32x4 hi = BACK ? L.frag_t(Mp, t, s) : L.frag(Mp, t, s);
+          u32x4 lo;
+          if constexpr (M::kSplit)
+            lo = BACK ? L.frag_t(Mp + Z::kM, t, s) : L.frag(Mp + Z::kM, t, s);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            if (NB > 2 && n * kBN >= N) continue;
+            if constexpr (M::kSplit) acc[n][t] = M::mma(f[n], lo, acc[n][t]);
+            acc[n][t] = M::mma(f[n], hi, acc[n][t]);
+          }
         }
-        if (lane + i < 64) qq += dq;
       }
-      float dots = 0.f, tr4 = 0.f;
+    };
+    if (side) others(std::true_type()); else others(std::false_type());
+    if (tid < (int)sizeof(sums) / 16) reinterpret_cast<u32x4*>(to)[tid] = reinterpret_cast<const u32x4*>(&sums)[tid];
+    to += sizeof(sums);
+    S += size;
+    dS += size;
+    x += p.sx.h;
+    y += a.sdO.h;
+    gates += sizeof(KeptGates);
+    dx += a.sdx.h;
+    __syncthreads();                                         // W and the sums have been read
+  }
+  T* out = side ? (T*)a.dB + c.b * a.sdB.b + grp * a.sdB.h + c.tok0 * a.sdB.t
+                : (T*)a.dC + c.b * a.sdC.b + grp * a.sdC.h + c.tok0 * a.sdC.t;
+  const int64_t pitch = side ? a.sdB.t : a.sdC.t;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dots += wsum[i];
+  for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tr4 += diag[i];
-      // pairs that token t's decay lies between: those of t - 1, less row t - 1's, and column t - 1's
-      const float dg = (float)((R - r0) + (zq - z0) + qq) + q.eb[kDC - 1] * dots;
-      const float raw = dt + bias, slope = p.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
-      const bool in = lane < c.len;
-      const float ddt = in ? (usum[0][lane] + usum[1][lane] + A * dg) * slope : 0.f;
-      if (in) a.ddt[c.b * a.sddt.b + h * a.sddt.h + (c.tok0 + lane) * a.sddt.t] = ddt;
-      double sa = in ? (double)dg * q.r[lane] : 0.0, sb = ddt;
+    for (int t = 0; t < 4; ++t) {
+      const int i = M::row(t, m), col = n * kBN + M::row(nt, 4 * g);
+      if (i < len && col < N) store4(out + i * pitch + col, acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
+    }
+#endif
+}
+
+// The rates' gradients from their sums: a wave for each chunk slot and head, a lane for each token.  Its parts of dA, dD
+// and ddt_bias go to part.
+template <typename T>
+__global__ __launch_bounds__(256) void k_scan_rates(ScanGradArgs a, int64_t chunk_heads) {
+  using M = Mat<T>;
+  const ScanArgs& p = a.f;
+  const int64_t sh = (int64_t)blockIdx.x * 4 + wave_id();
+  if (sh >= chunk_heads) return;
+  const int slot = (int)(sh / p.H), h = (int)(sh % p.H), lane = lane_id();
+  const ChunkPlace c = chunk_place(p.seqs, slot);
+  f32x4 part = {0.f, 0.f, 0.f, 0.f};
+  if (c.len > 0) {
+    const TokenSums<T>& s = reinterpret_cast<const TokenSums<T>*>(a.sums)[sh];
+    const KeptGates& q = a.gates[sh];
+    float rsum = 0.f, csum = 0.f;
 #pragma unroll
-      for (int i = 1; i < 64; i <<= 1) {
-        sa += __shfl_xor(sa, i, 64);
-        sb += __shfl_xor(sb, i, 64);
+    for (int k = 0; k < kDC / M::KB; ++k) rsum += lane >= k * M::KB ? s.rows[k][lane] : 0.f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) csum += lane / M::KB < M::steps(t) ? s.cols[t][lane] : 0.f;
+    const float r = q.g.r[lane];
+    const float so = (s.dots[0][lane] + s.dots[1][lane]) + (s.dots[2][lane] + s.dots[3][lane]);
+    const float us = q.rest[lane] * ((s.dots[4][lane] + s.dots[5][lane]) + (s.dots[6][lane] + s.dots[7][lane]));   // x . dS B
+    double R = (double)(csum * r) - rsum, z = us * r, y = q.g.eb[lane] * so;
+    const double r0 = R, z0 = z;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) {
+      const double up = __shfl_up(R, i, 64), uz = __shfl_up(z, i, 64), dy = __shfl_down(y, i, 64);
+      if (lane >= i) {
+        R += up;
+        z += uz;
       }
-      if (lane == 0) *reinterpret_cast<f32x4*>(a.part + sh * 4) = (f32x4){(float)sa, tr4, (float)sb, 0.f};
+      if (lane + i < 64) y += dy;
     }
-  }
-  if (tok < c.len) {
-    T* oC = (T*)a.dC + c.b * a.sdC.b + grp * a.sdC.h + (int64_t)(c.tok0 + tok) * a.sdC.t;
-    T* oB = (T*)a.dB + c.b * a.sdB.b + grp * a.sdB.h + (int64_t)(c.tok0 + tok) * a.sdB.t;
+    float all = 0.f;
 #pragma unroll
-    for (int k = 0; k < NTH; k += U) {
-      const int n = M::row(hf * NTH + k, 4 * g);
-      if (n >= p.N) continue;
-      *reinterpret_cast<u32x4*>(oC + n) = M::frag(&dC[k]);
-      *reinterpret_cast<u32x4*>(oB + n) = M::frag(&dB[k]);
+    for (int i = 0; i < 8; ++i) all += s.ss[i];
+    // pairs that token t's decay lies between: those of t - 1, less row t - 1's, and column t - 1's
+    const float dg = (float)((R - r0) + (z - z0) + y) + q.g.eb[kDC - 1] * all;
+    const bool in = lane < c.len;
+    const float ddt = in ? (us + csum + s.diag[0][lane] + p.A[h] * dg) * q.slope[lane] : 0.f;
+    if (in) a.ddt[c.b * a.sddt.b + h * a.sddt.h + (c.tok0 + lane) * a.sddt.t] = ddt;
+    double sa = in ? (double)dg * r : 0.0, sb = ddt, sd = s.diag[1][lane];
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) {
+      sa += __shfl_xor(sa, i, 64);
+      sb += __shfl_xor(sb, i, 64);
+      sd += __shfl_xor(sd, i, 64);
     }
+    part = (f32x4){(float)sa, (float)sd, (float)sb, 0.f};
   }
+  if (lane == 0) *reinterpret_cast<f32x4*>(a.part + sh * 4) = part;
 }
 
 // dA, dD, ddt_bias: the chunks' parts, in a fixed order.
@@ -402,19 +546,19 @@ __global__ __launch_bounds__(256) void k_scan_grad_sum(const float* __restrict__
   }
 }
 
-template <typename T, int DN, int BV, bool LDS>
+template <typename T, int DN, bool LDS>
 hipError_t launch_grads(const ScanGradArgs& a, int64_t chunks, hipStream_t s) {
-  using Z = GradShape<T, DN, BV, LDS>;
-  static_assert(Z::kSmem + 5 * 1024 <= kMaxLds, "LDS");
-  k_scan_grads<T, DN, BV, LDS><<<dim3((unsigned)(chunks * a.f.G)), 512, Z::kSmem, s>>>(a);
+  using Z = GradShape<T, DN, LDS>;
+  static_assert(Z::kSmem + 8 * 1024 <= kMaxLds, "LDS");
+  k_scan_grads<T, DN, LDS><<<dim3((unsigned)(chunks * a.f.G)), 512, Z::kSmem, s>>>(a);
   return hipGetLastError();
 }
 
 // Regions of the workspace, in bytes, multiples of 16.
 struct GradSpace {
   int seg;
-  int64_t slots, chunks, keep, sums, decays, part;
-  int64_t total() const { return 2 * keep + 2 * sums + 2 * decays + part; }
+  int64_t slots, chunks, keep, gates, tokens, sums, decays, part;
+  int64_t total() const { return 2 * keep + gates + tokens + 2 * sums + 2 * decays + part; }
 };
 template <typename T>
 GradSpace grad_space(const ScanArgs& a) {
@@ -423,7 +567,9 @@ GradSpace grad_space(const ScanArgs& a) {
   g.slots = seg_slots(a.seqs, a.batch, g.seg);
   g.chunks = delta_slots(a.seqs, a.batch);
   const bool cut = g.seg < a.seqs.n;
-  g.keep = g.chunks * a.H * kept_bytes(a.P, a.N);
+  g.gates = g.chunks * a.H * sizeof(KeptGates);
+  g.tokens = g.chunks * a.H * sizeof(TokenSums<T>);
+  g.keep = g.chunks * a.H * a.P * a.N * 4;
   g.sums = cut ? g.slots * a.H * a.P * a.N * 4 : 0;
   g.decays = cut ? (g.slots * a.H * 4 + 15) / 16 * 16 : 0;
   g.part = g.chunks * a.H * 16;
@@ -449,13 +595,15 @@ hipError_t launch_scan_grad(const ScanGradArgs& in, hipStream_t s) {
     at += bytes;
     return p;
   };
-  a.S = take(g.keep);
-  a.dS = take(g.keep);
+  a.S = (float*)take(g.keep);
+  a.dS = (float*)take(g.keep);
+  a.gates = (KeptGates*)take(g.gates);
+  a.sums = take(g.tokens);
   const bool cut = g.sums > 0;
   StateWalk one{f.x, f.B, f.sx, f.sB, f.S_init, nullptr, cut ? (float*)take(g.sums) : nullptr,
-                cut ? (float*)take(g.decays) : nullptr, a.S, false};
+                cut ? (float*)take(g.decays) : nullptr, a.S, a.gates, false};
   StateWalk two{a.dO, f.C, a.sdO, f.sC, a.dS_final, a.dS_init, cut ? (float*)take(g.sums) : nullptr,
-                cut ? (float*)take(g.decays) : nullptr, a.dS, true};
+                cut ? (float*)take(g.decays) : nullptr, a.dS, nullptr, true};
   a.part = (float*)take(g.part);
   const int64_t join = sequences * f.H * (((int64_t)f.P * f.N / 4 + 255) / 256);
   if (sequences > 0) {
@@ -474,15 +622,16 @@ hipError_t launch_scan_grad(const ScanGradArgs& in, hipStream_t s) {
   }
   const int64_t chunks = f.seqs.n > 0 ? g.chunks : 0;
   if (chunks > 0) {
-    constexpr bool wide = sizeof(T) == 2;
     hipError_t e;
     if (f.N <= 64)
-      e = launch_grads<T, 64, wide ? 64 : 32, true>(a, chunks, s);
+      e = launch_grads<T, 64, true>(a, chunks, s);
     else if (f.N <= 128)
-      e = launch_grads<T, 128, wide ? 64 : 32, true>(a, chunks, s);
+      e = launch_grads<T, 128, true>(a, chunks, s);
     else
-      e = launch_grads<T, 256, 32, wide>(a, chunks, s);
+      e = launch_grads<T, 256, sizeof(T) == 2>(a, chunks, s);
     if (e != hipSuccess) return e;
+    k_scan_rates<T><<<dim3((unsigned)((chunks * f.H + 3) / 4)), 256, 0, s>>>(a, chunks * f.H);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   k_scan_grad_sum<<<dim3((unsigned)f.H), 256, 0, s>>>(a.part, chunks, f.H, a.dA, a.dD, a.ddt_bias);
   return hipGetLastError();

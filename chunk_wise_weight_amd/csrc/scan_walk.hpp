@@ -28,7 +28,8 @@ struct StateWalk {
   const float* start;                 // S_init or dS_final [sequences, H, P, N], or null: zero
   float* end;                         // dS_init (back) [sequences, H, P, N], or null
   float *sums, *decays;               // of segment slots and heads [P, N], 1; null: sequences are one segment
-  char* keep;                         // of chunk slots and heads: the state before the chunk (back: after it)
+  float* keep;                        // of chunk slots and heads: the state before the chunk (back: after it)
+  KeptGates* gates;                   // of chunk slots and heads, or null
   bool back;
 };
 
@@ -37,31 +38,6 @@ __device__ __forceinline__ int chunk_slot0(const DeltaSeqs& q, int s) {
   return q.starts ? seq_start(q, s) / kDC + s : s * ((q.n + kDC - 1) / kDC);
 }
 __device__ __forceinline__ int seq_first(const DeltaSeqs& q, int s) { return q.starts ? seq_start(q, s) : 0; }
-
-// Bytes of a kept state: its elements, in bf16 as pairs.
-inline __host__ __device__ int64_t kept_bytes(int P, int N) { return (int64_t)P * N * 4; }
-
-// A wave's rows of a kept state [P][N]: bf16 values, then what their rounding left.
-template <typename T, int CT, int NT>
-__device__ __forceinline__ void keep_state(const StateRows<T, CT, NT>& S, char* to, int tile0, int P, int N) {
-  using M = Mat<T>;
-  const int m = lane_id() & 15, g = lane_id() >> 4;
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    const int p = M::row(tile0 + c, m);
-    if (p >= P) continue;
-#pragma unroll
-    for (int s = 0; s < NT / M::TPS; ++s) {
-      const int n = M::row(s * M::TPS, 4 * g);
-      if (n >= N) continue;
-      u32x4 hi, lo;
-      M::split(&S.s[c][s * M::TPS], hi, lo);
-      T* at = (T*)to + (int64_t)p * N + n;
-      *reinterpret_cast<u32x4*>(at) = hi;
-      if (M::kSplit) *reinterpret_cast<u32x4*>(at + (int64_t)P * N) = lo;
-    }
-  }
-}
 
 // The state of a segment: from zero, for the join (KEEP false), or before every chunk, kept for the gradients.
 template <typename T, int DN, int HW, int PW, bool KEEP>
@@ -81,6 +57,8 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const StateWalk&
   const int h = at.group * shared + min(at.head0 + hw, shared - 1);
   const int p0 = at.part * Z::cols, tile0 = (p0 >> 4) + pw * CT;
   const int64_t sh = (int64_t)at.slot * a.H + h, size = (int64_t)a.P * a.N;
+  LaneAt<T> L(lane);
+  L.keep();
   StateRows<T, CT, NT> S;
   S.zero();
   if (KEEP && mine) {
@@ -111,7 +89,18 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const StateWalk&
     bload.issue(B + t0 * k.scols.t, len, Bp);
     if (mine) xload.issue(x + t0 * k.srows.t, len, Xh);
     if (w < HW) {
-      total += make_gates(dt_next, A, bias, a.softplus, len, &gates[w]);
+      const LaneGates v = make_gates(dt_next, A, bias, a.softplus, len, &gates[w]);
+      total += v.sum;
+      if (KEEP && k.gates && at.part == 0) {               // (heads past the group's repeat the last one's)
+        KeptGates* o = k.gates + (int64_t)(slot0 + t0 / kDC) * a.H + gh;
+        o->g.hi[lane] = v.hi;
+        o->g.lo[lane] = v.lo;
+        o->g.eb[lane] = v.eb;
+        o->g.r[lane] = v.r;
+        o->g.w[lane] = v.w;
+        o->rest[lane] = v.rest;
+        o->slope[lane] = a.softplus ? 1.f / (1.f + expf(-(dt_next + bias))) : 1.f;
+      }
       if (i + 1 < chunks && t0 + step + lane < sp.len) dt_next = dt[(t0 + step + lane) * a.sdt.t];
     }
     wait_vm<0>();
@@ -120,7 +109,7 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const StateWalk&
     const Gates& q = gates[hw];
     if constexpr (KEEP) {
       if (!k.back && sp.first && i == 0 && q.eb[0] == 0.f) S.zero();   // emptied by its first token
-      keep_state(S, k.keep + ((int64_t)(slot0 + t0 / kDC) * a.H + h) * kept_bytes(a.P, a.N), tile0, a.P, a.N);
+      S.store(k.keep + ((int64_t)(slot0 + t0 / kDC) * a.H + h) * size, tile0, a.P, a.N);
     }
     S.decay(q.eb[kDC - 1]);
     const float* weights = (k.back ? q.eb : q.w) + g * (M::KB / 4);
@@ -128,8 +117,8 @@ __device__ __forceinline__ void walk_segment(const ScanArgs& a, const StateWalk&
     for (int s = 0; s < CS; ++s) {
       u32x4 xf[CT];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) xf[c] = Panels<T>::frag_t(Xh, pw * CT + c, s, lane);
-      S.add(xf, Bp, s, weights + s * M::KB, a.N);
+      for (int c = 0; c < CT; ++c) xf[c] = L.frag_t(Xh, pw * CT + c, s);
+      S.add(L, xf, Bp, s, weights + s * M::KB, a.N);
     }
   }
   if (!mine) {

@@ -1030,8 +1030,8 @@ typedef struct {
 
 /* Workspace of ttt_selective_scan_backward; num_seqs < 0: not packed.  Chunks
  * of 64 tokens times groups, sequences * heads * ceil(P N / 1024) below 2^23,
- * else TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + 16 bytes, and for
- * each segment and head 8 P N + 8. */
+ * else TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + some 6 KB, and
+ * for each segment and head 8 P N + 8. */
 int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
 
 /* The backward of ttt_selective_scan, from the forward call's inputs alone
