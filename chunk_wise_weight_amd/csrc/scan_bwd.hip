@@ -52,7 +52,10 @@ template <typename T, int DN_, bool LDS_> struct GradShape {
   static constexpr int SP = Mat<T>::kSplit ? 3 : 1;          // planes of a state: their sum is it
   static constexpr int kB = LDS ? Panels<T>::bytes(DN) : 0, kS = Panels<T, kBV>::bytes(kBN), kX = Panels<T>::bytes(kBV);
   static constexpr int kM = Panels<T>::bytes(kDC);           // a 64 x 64 matrix (bf16: and what its rounding left)
-  static constexpr int oS = 2 * kB, oX = oS + 2 * SP * kS, oM = oX + 2 * kX, kSmem = oM + kM * (Mat<T>::kSplit ? 2 : 1);
+  static constexpr int kMs = kM * (Mat<T>::kSplit ? 2 : 1);
+  // x, dO and the gates come by DMA, where LDS has room for it while the block before is worked on.
+  static constexpr int XB = 2 * kB + 2 * SP * kS + 4 * kX + kMs <= kMaxLds - 12 * 1024 ? 2 : 1;
+  static constexpr int oS = 2 * kB, oX = oS + 2 * SP * kS, oM = oX + 2 * XB * kX, kSmem = oM + kMs;
 };
 
 // x summed over the four lanes that hold a token.
@@ -137,12 +140,11 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   using M = Mat<T>;
   using Z = GradShape<T, DN, LDS>;
   constexpr int NS = DN / M::KB, CS = kDC / M::KB, NB = Z::NB, KS = Z::KS, U = M::TPS, SP = Z::SP;
-  constexpr int F = (M::kTri + 7) / 8, XU = 8 * (int)sizeof(T) / 16;   // fragments a wave; 16-byte pieces of 8 elements
+  constexpr int F = (M::kTri + 7) / 8, XB = Z::XB;           // F: fragments a wave
   constexpr int PB = U;                                      // blocks of P that are stored as one
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ KeptGates kept;
+  __shared__ __attribute__((aligned(1024))) char kept[2][2048];   // of a head and the next (KeptGates)
   __shared__ TokenSums<T> sums;
-  const Gates& q = kept.g;
   const ScanArgs& p = a.f;
   const int id = xcd_remap(blockIdx.x, gridDim.x);
   const int grp = id % p.G, slot = id / p.G, shared = p.H / p.G, head0 = grp * shared;
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   }
   LaneAt<T> L(lane);
   L.keep();
-  char *const Sp = smem + Z::oS, *const Dp = Sp + SP * Z::kS, *const Xp = smem + Z::oX, *const Yp = Xp + Z::kX, *const Mp = smem + Z::oM;
+  char *const Sp = smem + Z::oS, *const Dp = Sp + SP * Z::kS, *const Mp = smem + Z::oM;
 
   // Heads of the group, from the first on.
   const float *S = a.S + ((int64_t)slot * p.H + head0) * size, *dS = a.dS + ((int64_t)slot * p.H + head0) * size;
@@ -171,15 +173,12 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
 
   const int dtile = wave >> 1, dtok = M::row(dtile, m), dblock = 2 * (wave & 1);   // du's tokens and blocks of P
 
-  // What is on its way: 8 columns of a row of S and dS, 8 of a token's x and dO.
+  // What is on its way: 8 columns of a row of S and dS.
   const int row8 = tid >> 3, col8 = (tid & 7) * 8;
   const unsigned soff = (unsigned)(row8 * N + col8) * 4u;
-  const unsigned xoff = row8 < len ? (unsigned)row8 * (unsigned)(p.sx.t * sizeof(T)) + col8 * (unsigned)sizeof(T) : kOOB;
-  const unsigned yoff = row8 < len ? (unsigned)row8 * (unsigned)(a.sdO.t * sizeof(T)) + col8 * (unsigned)sizeof(T) : kOOB;
   const unsigned dxoff = dtok < len ? (unsigned)dtok * (unsigned)(a.sdx.t * sizeof(T)) : kOOB;
-  u32x4 ns[2], nd[2], nx[XU], ny[XU];
-  constexpr int GT = sizeof(KeptGates) / 16;                 // threads that bring the gates
-  u32x4 ngate = {0, 0, 0, 0};
+  u32x4 ns[2], nd[2];
+  const PanelLoader<T, kBV, 8> xload(p.sx.t * sizeof(T), kBV * sizeof(T)), yload(a.sdO.t * sizeof(T), kBV * sizeof(T));
   auto load_states = [&](const float* s, const float* d, int p0, int n0) __attribute__((always_inline)) {
     const unsigned off = p0 + row8 < P && n0 + col8 < N ? soff : kOOB;
     const __amdgpu_buffer_rsrc_t rs = rows_rsrc(s + (int64_t)p0 * N + n0), rd = rows_rsrc(d + (int64_t)p0 * N + n0);
@@ -189,20 +188,23 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       nd[k] = load_or_zero(rd, off + 16 * k);
     }
   };
-  auto load_rows = [&](const T* xh, const T* yh, int p0) __attribute__((always_inline)) {
-    const bool in = p0 + col8 < P;
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(xh + p0), ry = rows_rsrc(yh + p0);
-#pragma unroll
-    for (int k = 0; k < XU; ++k) {
-      nx[k] = load_or_zero(rx, in ? xoff + 16 * k : kOOB);
-      ny[k] = load_or_zero(ry, in ? yoff + 16 * k : kOOB);
+  auto load_rows = [&](const T* xh, const T* yh, int p0, char* to) __attribute__((always_inline)) {
+    if (p0 + kBV <= P) {
+      xload.issue(xh + p0, len, to);
+      yload.issue(yh + p0, len, to + Z::kX);
+    } else {
+      PanelLoader<T, kBV, 8>(p.sx.t * sizeof(T), (P - p0) * sizeof(T)).issue(xh + p0, len, to);
+      PanelLoader<T, kBV, 8>(a.sdO.t * sizeof(T), (P - p0) * sizeof(T)).issue(yh + p0, len, to + Z::kX);
     }
   };
-  auto load_gates = [&](const char* from) __attribute__((always_inline)) {
-    if (wave < (GT + 63) / 64) ngate = load_or_zero(make_rsrc(from, sizeof(KeptGates)), tid * 16);
+  auto load_gates = [&](const char* from, char* to) __attribute__((always_inline)) {
+    if (wave < 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(from, sizeof(KeptGates)), (lds_ptr_t)(to + wave * 1024), 16,
+                                               (unsigned)tid * 16u, 0, 0, 0);
   };
-  load_rows(x, y, 0);
-  load_gates(gates);
+  int turn = 0, hturn = 0;                                   // blocks of P, heads
+  load_rows(x, y, 0, smem + Z::oX);
+  load_gates(gates, kept[0]);
   load_states(S, dS, 0, 0);
   if constexpr (LDS) {
     wait_vm<0>();
@@ -229,12 +231,14 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   for (int n = 0; n < NB; ++n)
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[n][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  const char *const state = side ? Dp : Sp, *const other = side ? Xp : Yp;
-  const float* const scales = side ? q.w : q.eb;
+  const char *const state = side ? Dp : Sp;
   const Features<T, LDS> own = side ? B : C, cross = side ? C : B;
 
   for (int h = head0; h < head0 + shared; ++h) {
     const float D = p.D ? p.D[h] : 0.f;
+    const KeptGates& gate = *reinterpret_cast<const KeptGates*>(kept[hturn]);
+    const Gates& q = gate.g;
+    const float* const scales = side ? q.w : q.eb;
     f32x4 V[F][U], E[F][U];                                  // dO_i . x_j; exp(b_i - b_j), 0 for j > i
 #pragma unroll
     for (int k = 0; k < F; ++k)
@@ -243,20 +247,14 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
     float ss = 0.f, dot[4] = {0.f, 0.f, 0.f, 0.f};           // <S, dS>; C_i . S^T dO_i or B_j . dS^T x_j
     for (int p0 = 0; p0 < P; p0 += kBV) {
       const bool more = p0 + kBV < P, next = more || h + 1 < head0 + shared;
+      char *const Xp = smem + Z::oX + turn * 2 * Z::kX, *const Yp = Xp + Z::kX;
+      const char* const other = side ? Xp : Yp;
       f32x4 du[2];
       du[0] = du[1] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int n0 = nb * kBN;
         if (NB > 2 && n0 >= N) continue;
-        if (nb == 0) {
-#pragma unroll
-          for (int k = 0; k < XU; ++k) {
-            *reinterpret_cast<u32x4*>(Xp + Panels<T>::at(row8, col8 + k * (16 / (int)sizeof(T)))) = nx[k];
-            *reinterpret_cast<u32x4*>(Yp + Panels<T>::at(row8, col8 + k * (16 / (int)sizeof(T)))) = ny[k];
-          }
-          if (p0 == 0 && tid < GT) reinterpret_cast<u32x4*>(&kept)[tid] = ngate;
-        }
         f32x4 s2[2], d2[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -266,12 +264,15 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
         }
         put_planes<T, SP>(s2[0], s2[1], Sp, Z::kS, row8, tid & 7);
         put_planes<T, SP>(d2[0], d2[1], Dp, Z::kS, row8, tid & 7);
+        if (nb == 0) wait_vm<0>();                           // x, dO and the gates
         __syncthreads();
         if (nb + 1 < NB && (NB <= 2 || n0 + kBN < N)) {
           load_states(S, dS, p0, n0 + kBN);
         } else if (next) {
-          load_rows(more ? x : x + p.sx.h, more ? y : y + a.sdO.h, more ? p0 + kBV : 0);
-          if (!more) load_gates(gates + sizeof(KeptGates));
+          if (XB == 2) {
+            load_rows(more ? x : x + p.sx.h, more ? y : y + a.sdO.h, more ? p0 + kBV : 0, smem + Z::oX + (turn ^ 1) * 2 * Z::kX);
+            if (!more) load_gates(gates + sizeof(KeptGates), kept[hturn ^ 1]);
+          }
           load_states(more ? S : S + size, more ? dS : dS + size, more ? p0 + kBV : 0, 0);
         }
         phase();
@@ -309,28 +310,30 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
           }
         }
         phase();
-        // S^T dO (dS^T x)
+        // S^T dO (dS^T x), four independent sums
         {
-          u32x4 f[SP][KS];
+          f32x4 o[4];
 #pragma unroll
-          for (int z = 0; z < SP; ++z)
+          for (int t = 0; t < 4; ++t) o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) f[z][s] = L.frag_t(state + z * Z::kS, nt, s);
+          for (int s = 0; s < KS; ++s) {
+            u32x4 f[SP], b[4];
+#pragma unroll
+            for (int z = 0; z < SP; ++z) f[z] = L.frag_t(state + z * Z::kS, nt, s);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) b[t] = L.frag(other, t, s);
+#pragma unroll
+            for (int z = SP - 1; z >= 0; --z)
+#pragma unroll
+              for (int t = 0; t < 4; ++t) o[t] = M::mma(f[z], b[t], o[t]);
+          }
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const int i = M::row(t, m);
-            f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-              const u32x4 b = L.frag(other, t, s);
-#pragma unroll
-              for (int z = SP - 1; z >= 0; --z) o = M::mma(f[z][s], b, o);
-            }
-            dot[t] += dot4(o, own.at4(L, t, 4 * nb + nt));
-            acc[nb][t] += scales[i] * o;
-            phase();
+            dot[t] += dot4(o[t], own.at4(L, t, 4 * nb + nt));
+            acc[nb][t] += scales[M::row(t, m)] * o[t];
           }
         }
+        phase();
         // dS B
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       }
       // dx: of the tokens behind in the chunk, and of the state behind it
       {
-        const float f = kept.rest[dtok], r = q.r[dtok];
+        const float f = gate.rest[dtok], r = q.r[dtok];
 #pragma unroll
         for (int k = 0; k < 2; ++k) du[k] *= f;
 #pragma unroll
@@ -374,6 +377,11 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
         }
       }
       __syncthreads();                                       // x, dO and (C B^T exp) have been read
+      if (XB == 1 && next) {
+        load_rows(more ? x : x + p.sx.h, more ? y : y + a.sdO.h, more ? p0 + kBV : 0, smem + Z::oX);
+        if (!more) load_gates(gates + sizeof(KeptGates), kept[hturn ^ 1]);
+      }
+      turn ^= XB - 1;
     }
     // W to LDS, and the sums of W_ij (C_i . B_j) / r_j over rows and columns
 #pragma unroll
@@ -452,6 +460,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
     x += p.sx.h;
     y += a.sdO.h;
     gates += sizeof(KeptGates);
+    hturn ^= 1;
     dx += a.sdx.h;
     __syncthreads();                                         // W and the sums have been read
   }
@@ -549,7 +558,7 @@ __global__ __launch_bounds__(256) void k_scan_grad_sum(const float* __restrict__
 template <typename T, int DN, bool LDS>
 hipError_t launch_grads(const ScanGradArgs& a, int64_t chunks, hipStream_t s) {
   using Z = GradShape<T, DN, LDS>;
-  static_assert(Z::kSmem + 8 * 1024 <= kMaxLds, "LDS");
+  static_assert(Z::kSmem + 11 * 1024 <= kMaxLds, "LDS");
   k_scan_grads<T, DN, LDS><<<dim3((unsigned)(chunks * a.f.G)), 512, Z::kSmem, s>>>(a);
   return hipGetLastError();
 }
