@@ -5,14 +5,21 @@ namespace ttt {
 namespace {
 
 // The walk over a segment's chunks with outputs.  sums: every slot's and head's [P, N] state before the segment, or
-// null: sequences are one segment.
+// null: sequences are one segment.  A chunk's turn:
+//   C B^T by fragments, decayed for each head (D on its diagonal, so that D x comes with the product), to LDS
+//   S C from the state's two parts, then S' with x and B: B and C have been read, the next chunk's come
+//   the decayed C B^T times x, the outputs packed; they are stored in the next turn, behind its barrier, so that no wait
+//   for loads waits for them
 template <typename T, int DN, int HW, int PW>
 __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, int slots, const float* sums) {
+#if __HIP_DEVICE_COMPILE__
   using Z = ScanShape<T, DN, HW, PW>;
   using M = Mat<T>;
-  constexpr int CT = Z::CT, NT = Z::NT, NS = Z::NS, CS = Z::CS, W = Z::W;
+  constexpr int CT = Z::CT, NT = Z::NT, NS = Z::NS, CS = Z::CS, W = Z::W, U = M::TPS;
+  constexpr int PB = CT == 2 && U == 2 ? 2 : 1, CB = CT / PB;  // blocks of P that are stored as one; of those
+  constexpr int UNITS = M::kTri * HW, PER = (UNITS + W - 1) / W;   // (fragment, head) pairs, a wave's
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ Gates gates[HW];
+  __shared__ Gates gates[2][HW];
   char *const Bp = smem, *const Cp = Bp + Z::kB, *const Xp = Cp + Z::kB, *const Mp = Xp + HW * Z::kX;
   const int shared = a.H / a.G, parts = (a.P + Z::cols - 1) / Z::cols;
   ScanPlace at;
@@ -27,6 +34,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 
   LaneAt<T> L(lane);
   L.keep();
+  const Split<T> split(lane);
   StateRows<T, CT, NT> S;
   S.zero();
   if (mine) {
@@ -46,72 +54,102 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   // the gates of head head0 + w are made by wave w
   const int gh = at.group * shared + min(at.head0 + w, shared - 1);
   const float* dt = a.dt + sp.b * a.sdt.b + gh * a.sdt.h + sp.tok0 * a.sdt.t;
-  const float A = a.A[gh], bias = a.dt_bias ? a.dt_bias[gh] : 0.f, D = a.D ? a.D[h] : 0.f;
+  const float A = a.A[gh], bias = a.dt_bias ? a.dt_bias[gh] : 0.f;
+  const unsigned pitch = (unsigned)(a.sO.t * sizeof(T));
   float dt_next = 0.f;
   if (w < HW && lane < sp.len) dt_next = dt[lane * a.sdt.t];
-
-  for (int t0 = 0; t0 < sp.len; t0 += kDC) {
+  auto make = [&](int t, int turn) __attribute__((always_inline)) {
+    if (w >= HW) return;
+    const LaneGates v = make_gates(dt_next, A, bias, a.softplus, min(kDC, sp.len - t));
+    put_gates<T>(v, &gates[turn][w]);
+    if (t + kDC + lane < sp.len) dt_next = dt[(t + kDC + lane) * a.sdt.t];
+  };
+  u32x4 out[CB][4];                                        // O of the chunk before, of token row(t, m)
+  auto store = [&](int t0) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(O + t0 * a.sO.t);
     const int len = min(kDC, sp.len - t0);
-    if (t0 > 0) __syncthreads();                           // the chunk before has been read
-    bload.issue(B + t0 * a.sB.t, len, Bp);
-    cload.issue(C + t0 * a.sC.t, len, Cp);
-    if (mine) xload.issue(x + t0 * a.sx.t, len, Xh);
-    if (w < HW) {
-      make_gates(dt_next, A, bias, a.softplus, len, &gates[w]);
-      if (t0 + kDC + lane < sp.len) dt_next = dt[(t0 + kDC + lane) * a.sdt.t];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      const int p = M::row(tile0 + c * PB, 4 * g);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int i = M::row(t, m);
+        const unsigned off = p < a.P && i < len ? i * pitch + p * (unsigned)sizeof(T) : kOOB;
+        if constexpr (PB == U)
+          __builtin_amdgcn_raw_buffer_store_b128(out[c][t], rs, off, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b64((u32x2){out[c][t][0], out[c][t][1]}, rs, off, 0, 0);
+      }
     }
+  };
+
+  bload.issue(B, min(kDC, sp.len), Bp);
+  cload.issue(C, min(kDC, sp.len), Cp);
+  if (mine) xload.issue(x, min(kDC, sp.len), Xh);
+  make(0, 0);
+  int turn = 0;
+  for (int t0 = 0; t0 < sp.len; t0 += kDC, turn ^= 1) {
+    const int next = t0 + kDC, nlen = min(kDC, sp.len - next);
     wait_vm<0>();
-    __syncthreads();
-    {
-      // C B^T once for the workgroup's heads, by fragments (t, s) of tokens row(t, .) and those before them
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int s = 0; s < CS; ++s) {
-          if (s >= M::steps(t) || M::tri(t, s) % W != w) continue;
-          const int i = M::row(t, m);
-          f32x4 d[M::TPS];
-#pragma unroll
-          for (int u = 0; u < M::TPS; ++u) d[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int ns = 0; ns < NS; ++ns) {
-            if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
-            const u32x4 c = L.frag(Cp, t, ns);
-#pragma unroll
-            for (int u = 0; u < M::TPS; ++u) d[u] = M::mma(L.frag(Bp, s * M::TPS + u, ns), c, d[u]);
-          }
-          for (int k = 0; k < HW; ++k) {
-            const Gates& q = gates[k];
-            const float bh = q.hi[i], bl = q.lo[i];
-            f32x4 v[M::TPS];
-#pragma unroll
-            for (int u = 0; u < M::TPS; ++u) {
-              const int j = M::row(s * M::TPS + u, 4 * g);
-              const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jl = *reinterpret_cast<const f32x4*>(q.lo + j),
-                          jr = *reinterpret_cast<const f32x4*>(q.r + j);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[u][e] = j + e <= i ? d[u][e] * exp2_hw((bh - jh[e]) + (bl - jl[e])) * jr[e] : 0.f;
-            }
-            u32x4 hi, lo;
-            M::split(v, hi, lo);
-            char* f = Mp + k * Z::kM + M::tri(t, s) * 1024 + lane * 16;
-            *reinterpret_cast<u32x4*>(f) = hi;
-            if (M::kSplit) *reinterpret_cast<u32x4*>(f + M::kTri * 1024) = lo;
-          }
-        }
-      __syncthreads();
-    }
-    if (!mine) continue;
-    const Gates& q = gates[hw];
-    if (t0 == 0 && sp.first && q.eb[0] == 0.f) S.zero();   // emptied by its first token: S_init is not looked at
+    __syncthreads();                                       // the chunk and its gates are there
+    if (mine && t0 > 0) store(t0 - kDC);
     u32x4 xf[CS][CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int s = 0; s < CS; ++s)
 #pragma unroll
-      for (int s = 0; s < CS; ++s) xf[s][c] = L.frag_t(Xh, pw * CT + c, s);
-    {
-      f32x4 o[CT][4];
+      for (int c = 0; c < CT; ++c) xf[s][c] = L.frag_t(Xh, pw * CT + c, s);
+    // C B^T of a fragment's tokens row(t, .) and those before them
+    int made = -1;
+    f32x4 d[U];
+#pragma unroll 1
+    for (int k = 0; k < PER; ++k) {
+      const int unit = w * PER + k;
+      if (unit >= UNITS) break;
+      const int f = unit / HW, hd = unit % HW;
+      int t, s;
+      tri_place<T>(f, &t, &s);
+      if (f != made) {
+        made = f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) d[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ns = 0; ns < NS; ++ns) {
+          if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
+          const u32x4 c = L.frag(Cp, t, ns);
+#pragma unroll
+          for (int u = 0; u < U; ++u) d[u] = M::mma(L.frag(Bp, s * U + u, ns), c, d[u]);
+        }
+      }
+      const Gates& q = gates[turn][hd];
+      const float D = a.D ? a.D[at.group * shared + min(at.head0 + hd, shared - 1)] : 0.f;
+      const int i = M::row(t, m);
+      const float bh = q.hi[i], bl = U == 2 ? 0.f : q.lo[i];
+      f32x4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = M::row(s * U + u, 4 * g);
+        const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jr = *reinterpret_cast<const f32x4*>(q.r + j);
+        f32x4 jl;
+        if constexpr (U == 1) jl = *reinterpret_cast<const f32x4*>(q.lo + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = U == 2 ? bh - jh[e] : (bh - jh[e]) + (bl - jl[e]);
+          v[u][e] = d[u][e] * exp2_hw(x) * jr[e];
+          if (j + e >= i) v[u][e] = j + e == i ? v[u][e] + D : 0.f;
+        }
+      }
+      u32x4 hi, lo;
+      split.two(v, hi, lo);
+      char* to = Mp + hd * Z::kM + f * 1024 + lane * 16;
+      *reinterpret_cast<u32x4*>(to) = hi;
+      if (M::kSplit) *reinterpret_cast<u32x4*>(to + M::kTri * 1024) = lo;
+    }
+    __syncthreads();                                       // it is there, x has been read
+    if (mine && next < sp.len) xload.issue(x + next * a.sx.t, nlen, Xh);
+    const Gates& q = gates[turn][hw];
+    f32x4 o[CT][4];
+    if (mine) {
+      if (t0 == 0 && sp.first && q.eb[0] == 0.f) S.zero(); // emptied by its first token: S_init is not looked at
 #pragma unroll
       for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -119,21 +157,30 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) {
         if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
-        {
-          u32x4 sh_[CT], sl[CT];
+        u32x4 hi[CT], lo[CT];
 #pragma unroll
-          for (int c = 0; c < CT; ++c) M::split(&S.s[c][ns * M::TPS], sh_[c], sl[c]);
+        for (int c = 0; c < CT; ++c) split.two(&S.s[c][ns * U], hi[c], lo[c]);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const u32x4 f = L.frag(Cp, t, ns);
+        for (int t = 0; t < 4; ++t) {
+          const u32x4 f = L.frag(Cp, t, ns);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              if (M::kSplit) o[c][t] = M::mma(sl[c], f, o[c][t]);
-              o[c][t] = M::mma(sh_[c], f, o[c][t]);
-            }
+          for (int c = 0; c < CT; ++c) {
+            if (M::kSplit) o[c][t] = M::mma(lo[c], f, o[c][t]);
+            o[c][t] = M::mma(hi[c], f, o[c][t]);
           }
         }
       }
+      S.decay(q.eb[kDC - 1]);
+#pragma unroll
+      for (int s = 0; s < CS; ++s) S.add(L, split, xf[s], Bp, s, q.w + s * M::KB + g * (M::KB / 4), a.N);
+    }
+    __syncthreads();                                       // B and C have been read
+    if (next < sp.len) {
+      bload.issue(B + next * a.sB.t, nlen, Bp);
+      cload.issue(C + next * a.sC.t, nlen, Cp);
+      make(next, turn ^ 1);
+    }
+    if (mine) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float e = q.eb[M::row(t, m)];
@@ -152,43 +199,33 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
           for (int c = 0; c < CT; ++c) o[c][t] = M::mma(xf[s][c], hi, o[c][t]);
         }
-      }
-      // o[c][t]: p = row(tile0 + c, 4 g + 0..3) of token row(t, m); a pair of blocks has 8 of bf16 together
-      constexpr int PB = CT == 2 && M::TPS == 2 ? 2 : 1;   // blocks that are stored as one
+        // p = row(tile0 + c, 4 g + 0..3) of token row(t, m): bf16 pairs of blocks are 8 together
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int i = M::row(t, m);
-        if (i >= len) continue;
-        T* out = O + (t0 + i) * a.sO.t;
+        for (int c = 0; c < CB; ++c) {
+          if constexpr (PB == U) {
+            f32x4 v[PB];
 #pragma unroll
-        for (int c = 0; c < CT; c += PB) {
-          const int p = M::row(tile0 + c, 4 * g);
-          if (p >= a.P) continue;
-          f32x4 v[PB];
-#pragma unroll
-          for (int k = 0; k < PB; ++k) {
-            v[k] = o[c + k][t];
-            if (a.D) v[k] += D * L.at4(Xh, t, pw * CT + c + k);
+            for (int k = 0; k < PB; ++k) v[k] = o[c * PB + k][t];
+            out[c][t] = M::frag(v);
+          } else {                                         // one block of bf16: 4 together
+            out[c][t] = (u32x4){pack2_bf16(o[c][t][0], o[c][t][1]), pack2_bf16(o[c][t][2], o[c][t][3]), 0, 0};
           }
-          if constexpr (PB == 2)
-            *reinterpret_cast<u32x4*>(out + p) = M::frag(v);
-          else
-            store4(out + p, v[0][0], v[0][1], v[0][2], v[0][3]);
         }
       }
     }
-    S.decay(q.eb[kDC - 1]);
-#pragma unroll
-    for (int s = 0; s < CS; ++s) S.add(L, xf[s], Bp, s, q.w + s * M::KB + g * (M::KB / 4), a.N);
   }
-  if (mine && sp.last) S.store(a.S_final + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
+  if (mine) {
+    store((sp.len - 1) / kDC * kDC);
+    if (sp.last) S.store(a.S_final + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
+  }
+#endif
 }
 
 template <typename T, int DN, int HW, int PW>
 hipError_t launch(const ScanArgs& a, int seg, int64_t slots, const float* sums, hipStream_t s) {
   using Z = ScanShape<T, DN, HW, PW>;
   constexpr int smem = 2 * Z::kB + HW * (Z::kX + Z::kM);
-  static_assert(smem + (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
+  static_assert(smem + 2 * (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
   const int64_t shared = a.H / a.G;
   const int64_t per = (shared + HW - 1) / HW * ((a.P + Z::cols - 1) / Z::cols);
   k_scan<T, DN, HW, PW><<<dim3((unsigned)walk_blocks(slots * a.G, per)), 64 * HW * PW, smem, s>>>(a, seg, (int)slots, sums);

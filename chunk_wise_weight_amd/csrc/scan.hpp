@@ -12,9 +12,8 @@
 // registers.  The outputs are made transposed, rows of P by tokens, so that a lane has consecutive features of a token.
 //
 // Precision (bf16 inputs).  x, B and C enter as they are.  What is fp32 enters as sums of bf16 values: the scaled x of
-// the state's update as three (2^-24), the state and the decayed C B^T of the outputs as two (2^-17), so that the state
-// is fp32's own and O off by its own rounding.  Running sums of log decays are fp64; differences of them are taken from
-// two fp32 parts, the first a multiple of 2^-8, whose differences are exact.
+// the state's update as three (24 bits), the state and the decayed C B^T of the outputs as two (17 bits), so that the
+// state is fp32's own and O off by its own rounding.  Running sums of log decays are fp64.
 #pragma once
 #include "delta.hpp"
 #include "scan_rate.hpp"
@@ -56,6 +55,17 @@ __device__ __forceinline__ SeqSlots seq_slots(const DeltaSeqs& q, int seg, int s
   }
   const int a = seq_start(q, s), e = max(seq_start(q, s + 1), a);
   return {a / seg + s, (int)(((int64_t)(e - a) + seg - 1) / seg)};
+}
+
+// Row block and step of a triangular matrix's fragment.
+template <typename T> __device__ __forceinline__ void tri_place(int f, int* t, int* s) {
+  if constexpr (sizeof(T) == 2) {
+    *t = f < 2 ? f : 2 + ((f - 2) >> 1);
+    *s = f < 2 ? 0 : (f - 2) & 1;
+  } else {
+    *t = f < 1 ? 0 : f < 3 ? 1 : f < 6 ? 2 : 3;
+    *s = f - *t * (*t + 1) / 2;
+  }
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -125,93 +135,112 @@ template <> struct LaneAt<float> {
   }
 };
 
-// A chunk's gates for one head in LDS, base 2 logarithms: b in two parts, exp(b), the rates, and exp(b_63 - b) r.
-struct Gates {
-  float hi[kDC], lo[kDC], eb[kDC], r[kDC], w[kDC];
-};
-
-// A chunk's gates from its lanes' dt (one wave; tokens past len leave the state alone).  Log decays below kResetDecay
-// are taken as that: exp of them is zero either way, and sums of 64 stay where `hi` is exact.  sum: the chunk's.
+// A chunk's gates for one head, base 2 logarithms, a lane for each token (one wave; tokens past len leave the state
+// alone).  Log decays below kLeastLog are taken as that: exp of them is zero either way.
+constexpr double kLeastLog = -120.0;
 struct LaneGates {
-  double sum;
-  float hi, lo, eb, r, w, rest;       // rest: exp(b_63 - b)
+  double b, sum;                      // running sum of the log decays, the chunk's
+  float r;
 };
-__device__ __forceinline__ LaneGates make_gates(float dt, float A, float bias, bool softplus, int len, Gates* o) {
+__device__ __forceinline__ LaneGates make_gates(float dt, float A, float bias, bool softplus, int len) {
   const int lane = lane_id();
   LaneGates v;
   v.r = lane < len ? scan_rate(dt, bias, softplus) : 0.f;
-  double b = lane < len ? fmax((double)A * v.r, (double)kResetDecay) * 1.4426950408889634 : 0.0;
+  v.b = lane < len ? fmax((double)A * v.r, kLeastLog) * 1.4426950408889634 : 0.0;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const double up = __shfl_up(b, m, 64);
-    if (lane >= m) b += up;
+    const double up = __shfl_up(v.b, m, 64);
+    if (lane >= m) v.b += up;
   }
-  v.sum = __shfl(b, 63, 64);
-  v.hi = rintf((float)b * 256.f) * (1.f / 256.f);
-  v.lo = (float)(b - (double)v.hi);
-  v.eb = exp2_hw((float)b);
-  v.rest = exp2_hw((float)(v.sum - b));
-  v.w = v.r * v.rest;
-  o->hi[lane] = v.hi;
-  o->lo[lane] = v.lo;
-  o->eb[lane] = v.eb;
-  o->r[lane] = v.r;
-  o->w[lane] = v.w;
+  v.sum = __shfl(v.b, 63, 64);
   return v;
 }
-// The same as the backward pass keeps them for its chunk-local part, with the rate's derivative by dt.
+// b in two parts, the first a multiple of 2^-8 below 2^14: differences of first parts are exact.
+__device__ __forceinline__ void two_parts(double b, float* hi, float* lo) {
+  *hi = rintf((float)b * 256.f) * (1.f / 256.f);
+  *lo = (float)(b - (double)*hi);
+}
+
+// Gates as they lie in LDS: b (fp32 inputs: in two parts), exp(b), the rates, and exp(b_63 - b) r.  One fp32 b is enough
+// for bf16 outputs: sums of 64 are below 2^14, their differences off by 2^-10 at most.
+struct Gates {
+  float hi[kDC], lo[kDC], eb[kDC], r[kDC], w[kDC];
+};
+template <typename T> __device__ __forceinline__ void put_gates(const LaneGates& v, Gates* o) {
+  const int lane = lane_id();
+  if constexpr (sizeof(T) == 2) {
+    o->hi[lane] = (float)v.b;
+  } else {
+    two_parts(v.b, &o->hi[lane], &o->lo[lane]);
+  }
+  o->eb[lane] = exp2_hw((float)v.b);
+  o->r[lane] = v.r;
+  o->w[lane] = v.r * exp2_hw((float)(v.sum - v.b));
+}
+// The same as the backward pass keeps them for its chunk-local part, b in two parts, with exp(b_63 - b) and the rate's
+// derivative by dt.
 struct KeptGates {
   Gates g;
   float rest[kDC], slope[kDC];
 };
 
-// Values as three bf16 operands, each the 8 leading bits of what the ones before left: 24 bits in all.
-__device__ __forceinline__ void split3(const float (&x)[8], u32x4& h, u32x4& m, u32x4& l) {
-  unsigned v[8];
+// fp32 results to operands of bf16 values whose sum they are.  What a rounding leaves is made by the matrix cores: a
+// result plus (-1 at its own place) times the rounded operand, exact, and off the vector units, which bound these kernels
+// (16 vector instructions less for each operand and part).
+template <typename T> struct Split {
+  u32x4 minus[2];                     // -1 at row(u, lane & 15), u the block of a step
+  __device__ __forceinline__ explicit Split(int lane) {
+    const int m = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(x[i]);
+    for (int u = 0; u < 2; ++u) {
+      const int e = 4 * u + (m & 3);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    u32x4& w = k == 0 ? h : k == 1 ? m : l;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07060302);
-      if (k < 2) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const unsigned u = v[2 * i + j];
-          v[2 * i + j] = __float_as_uint(__uint_as_float(u) - __uint_as_float(u & 0xffff0000u));
-        }
-      }
+      for (int i = 0; i < 4; ++i) minus[u][i] = g == m >> 2 && i == e >> 1 ? 0xbf80u << (16 * (e & 1)) : 0u;
     }
+    asm volatile("" : "+v"(minus[0]), "+v"(minus[1]));
   }
-}
+  __device__ __forceinline__ void rest(f32x4* c, u32x4 h) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) c[u] = Mat<T>::mma(minus[u], h, c[u]);
+  }
+  __device__ __forceinline__ void two(const f32x4* v, u32x4& h, u32x4& l) const {
+    f32x4 c[2] = {v[0], v[1]};
+    h = Mat<T>::frag(c);
+    rest(c, h);
+    l = Mat<T>::frag(c);
+  }
+};
+template <> struct Split<float> {
+  __device__ __forceinline__ explicit Split(int) {}
+  __device__ __forceinline__ void two(const f32x4* v, u32x4& h, u32x4&) const { h = Mat<float>::frag(v); }
+};
 
-// An operand of tokens (contraction over 16 bytes of them) times their weights, as parts whose sum it is.
+// An operand of tokens (contraction over 16 bytes of them) times their weights, as parts whose sum it is: bf16 three, 24
+// bits in all.
 template <typename T> struct Scaled {
   static constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
   u32x4 part[kParts];
-  __device__ __forceinline__ Scaled(u32x4 x, const float* w) {
+  __device__ __forceinline__ Scaled(const Split<T>& sp, u32x4 x, const float* w) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(w);
     if constexpr (sizeof(T) == 2) {
+      const f32x4 b = *reinterpret_cast<const f32x4*>(w + 4);
       float v[8];
       unpack8(x, v);
-      const f32x4 a = *reinterpret_cast<const f32x4*>(w), b = *reinterpret_cast<const f32x4*>(w + 4);
+      f32x4 c[2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] *= a[i];
-        v[4 + i] *= b[i];
+        c[0][i] = v[i] * a[i];
+        c[1][i] = v[4 + i] * b[i];
       }
-      split3(v, part[0], part[1], part[2]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        part[k] = Mat<T>::frag(c);
+        if (k < 2) sp.rest(c, part[k]);
+      }
     } else {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) part[0][i] = __float_as_uint(__uint_as_float(x[i]) * a[i]);
     }
-  }
-  __device__ __forceinline__ f32x4 mma(u32x4 a, f32x4 c) const {
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) c = Mat<T>::mma(a, part[kParts - 1 - i], c);
-    return c;
   }
 };
 
@@ -263,16 +292,19 @@ template <typename T, int CT, int NT> struct StateRows {
   // += the weighted outer products of a step's tokens: x[c] their features of this wave's blocks, `cols` their rows of N
   // in LDS.  All blocks of P at once, so that an operand is read once.
   // Columns past N are zero in LDS; whole halves of the widest states are passed over.
-  __device__ __forceinline__ void add(const LaneAt<T>& L, const u32x4 (&x)[CT], const char* cols, int step,
-                                      const float* weights, int N) {
+  __device__ __forceinline__ void add(const LaneAt<T>& L, const Split<T>& sp, const u32x4 (&x)[CT], const char* cols,
+                                      int step, const float* weights, int N) {
     static_assert(CT <= 2, "blocks");
-    const Scaled<T> u0(x[0], weights), u1(x[CT - 1], weights);
+    const Scaled<T> u0(sp, x[0], weights), u1(sp, x[CT - 1], weights);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (NT > 8 && t % 4 == 0 && t * 16 >= N) break;
       const u32x4 f = L.frag_t(cols, t, step);
-      s[0][t] = u0.mma(f, s[0][t]);
-      if (CT == 2) s[CT - 1][t] = u1.mma(f, s[CT - 1][t]);
+#pragma unroll
+      for (int k = Scaled<T>::kParts - 1; k >= 0; --k) {
+        s[0][t] = Mat<T>::mma(f, u0.part[k], s[0][t]);
+        if (CT == 2) s[CT - 1][t] = Mat<T>::mma(f, u1.part[k], s[CT - 1][t]);
+      }
     }
   }
   // A decay that is zero in fp32 empties the state, whatever it holds.

@@ -77,17 +77,6 @@ __device__ __forceinline__ u32x4 load_or_zero(__amdgpu_buffer_rsrc_t rs, unsigne
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
 }
 
-// Row block and step of a triangular matrix's fragment.
-template <typename T> __device__ __forceinline__ void tri_place(int f, int* t, int* s) {
-  if constexpr (sizeof(T) == 2) {
-    *t = f < 2 ? f : 2 + ((f - 2) >> 1);
-    *s = f < 2 ? 0 : (f - 2) & 1;
-  } else {
-    *t = f < 1 ? 0 : f < 3 ? 1 : f < 6 ? 2 : 3;
-    *s = f - *t * (*t + 1) / 2;
-  }
-}
-
 // 8 fp32 values of a row of a state block to its planes: each the 8 leading bits of what the ones before left, 24 in all.
 template <typename T, int SP>
 __device__ __forceinline__ void put_planes(f32x4 a, f32x4 b, char* plane, int stride, int r, int c8) {
@@ -161,6 +150,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   }
   LaneAt<T> L(lane);
   L.keep();
+  const Split<T> split(lane);
   char *const Sp = smem + Z::oS, *const Dp = Sp + SP * Z::kS, *const Mp = smem + Z::oM;
 
   // Heads of the group, from the first on.
@@ -302,7 +292,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
                 }
               }
               u32x4 hi, lo;
-              M::split(w, hi, lo);
+              split.two(w, hi, lo);
               char* f = Mp + Panels<T>::at(i, M::row(fs[k] * U, 4 * g));
               *reinterpret_cast<u32x4*>(f) = hi;
               if (M::kSplit) *reinterpret_cast<u32x4*>(f + Z::kM) = lo;
@@ -414,7 +404,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       rs = token_sum(rs);
       if (g == 0) sums.rows[s][i] = rs;
       u32x4 hi, lo;
-      M::split(w, hi, lo);
+      split.two(w, hi, lo);
       char* f = Mp + Panels<T>::at(i, M::row(s * U, 4 * g));
       *reinterpret_cast<u32x4*>(f) = hi;
       if (M::kSplit) *reinterpret_cast<u32x4*>(f + Z::kM) = lo;

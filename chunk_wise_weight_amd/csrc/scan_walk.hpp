@@ -39,114 +39,217 @@ __device__ __forceinline__ int chunk_slot0(const DeltaSeqs& q, int s) {
 }
 __device__ __forceinline__ int seq_first(const DeltaSeqs& q, int s) { return q.starts ? seq_start(q, s) : 0; }
 
-// The state of a segment: from zero, for the join (KEEP false), or before every chunk, kept for the gradients.
-template <typename T, int DN, int HW, int PW, bool KEEP>
-__device__ __forceinline__ void walk_segment(const ScanArgs& a, const StateWalk& k, int seg, int slots, int bid, char* smem,
-                                             Gates* gates) {
+// What a workgroup of a walk over states has in hand.
+template <typename T, int DN, int HW, int PW> struct StateWalker {
   using Z = ScanShape<T, DN, HW, PW>;
   using M = Mat<T>;
-  constexpr int CT = Z::CT, NT = Z::NT, CS = Z::CS, W = Z::W;
-  char *const Bp = smem, *const Xp = Bp + Z::kB;
-  const int shared = a.H / a.G, parts = (a.P + Z::cols - 1) / Z::cols;
+  static constexpr int CT = Z::CT, NT = Z::NT, CS = Z::CS, W = Z::W;
+  static constexpr int kStage = Z::kB + HW * Z::kX;
+  // Two stages, the next chunk coming while one is worked on; one, where LDS has no room for more.
+  static constexpr int kStages = 2 * kStage + 2 * (int)sizeof(Gates) * HW <= kMaxLds ? 2 : 1;
+  const ScanArgs& a;
+  const StateWalk& k;
   ScanPlace at;
-  if (!scan_place(bid, slots, a.G, shared, parts, HW, &at)) return;
-  const SegPlace sp = seg_place(a.seqs, seg, at.slot);
-  if (sp.len <= 0 || (!KEEP && (k.back ? sp.first : sp.last))) return;
-  const int w = wave_id(), hw = w / PW, pw = w % PW, lane = lane_id(), g = lane >> 4;
-  const bool mine = at.head0 + hw < shared;                // a head of the group
-  const int h = at.group * shared + min(at.head0 + hw, shared - 1);
-  const int p0 = at.part * Z::cols, tile0 = (p0 >> 4) + pw * CT;
-  const int64_t sh = (int64_t)at.slot * a.H + h, size = (int64_t)a.P * a.N;
-  LaneAt<T> L(lane);
-  L.keep();
-  StateRows<T, CT, NT> S;
-  S.zero();
-  if (KEEP && mine) {
-    if (k.sums)
-      S.load(k.sums + sh * size, tile0, a.P, a.N);
-    else if (k.start)
-      S.load(k.start + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
+  SegPlace sp;
+  int w, hw, pw, lane, h, gh, tile0, chunks;
+  bool mine;                                                 // a head of the group
+  PanelLoader<T, DN, W> cload;
+  PanelLoader<T, Z::DX, PW> rload;
+  const T *cols, *rows;
+  const float* dt;
+  float A, bias;
+  char* smem;
+  __device__ __forceinline__ StateWalker(const ScanArgs& a_, const StateWalk& k_, const ScanPlace& at_, const SegPlace& sp_,
+                                         char* smem_)
+      : a(a_), k(k_), at(at_), sp(sp_), w(wave_id()), hw(w / PW), pw(w % PW), lane(lane_id()),
+        cload(k_.scols.t * sizeof(T), a_.N * sizeof(T)),
+        rload(k_.srows.t * sizeof(T), min(a_.P - at_.part * Z::cols, Z::cols) * sizeof(T)), smem(smem_) {
+    const int shared = a.H / a.G, p0 = at.part * Z::cols;
+    mine = at.head0 + hw < shared;
+    h = at.group * shared + min(at.head0 + hw, shared - 1);
+    gh = at.group * shared + min(at.head0 + w, shared - 1);  // the gates of head head0 + w are made by wave w
+    tile0 = (p0 >> 4) + pw * CT;
+    chunks = (sp.len + kDC - 1) / kDC;
+    cols = (const T*)k.cols + sp.b * k.scols.b + at.group * k.scols.h + sp.tok0 * k.scols.t;
+    rows = (const T*)k.rows + sp.b * k.srows.b + h * k.srows.h + sp.tok0 * k.srows.t + p0;
+    dt = a.dt + sp.b * a.sdt.b + gh * a.sdt.h + sp.tok0 * a.sdt.t;
+    A = a.A[gh];
+    bias = a.dt_bias ? a.dt_bias[gh] : 0.f;
   }
-  const PanelLoader<T, DN, W> bload(k.scols.t * sizeof(T), a.N * sizeof(T));
-  const PanelLoader<T, Z::DX, PW> xload(k.srows.t * sizeof(T), min(a.P - p0, Z::cols) * sizeof(T));
-  const T* B = (const T*)k.cols + sp.b * k.scols.b + at.group * k.scols.h + sp.tok0 * k.scols.t;
-  const T* x = (const T*)k.rows + sp.b * k.srows.b + h * k.srows.h + sp.tok0 * k.srows.t + p0;
-  char* const Xh = Xp + hw * Z::kX;
-  // the gates of head head0 + w are made by wave w
-  const int gh = at.group * shared + min(at.head0 + w, shared - 1);
-  const float* dt = a.dt + sp.b * a.sdt.b + gh * a.sdt.h + sp.tok0 * a.sdt.t;
-  const float A = a.A[gh], bias = a.dt_bias ? a.dt_bias[gh] : 0.f;
-  const int chunks = (sp.len + kDC - 1) / kDC, step = k.back ? -kDC : kDC;
-  const int slot0 = chunk_slot0(a.seqs, sp.seq) + (sp.tok0 - seq_first(a.seqs, sp.seq)) / kDC;
-  int t0 = k.back ? (chunks - 1) * kDC : 0;
-  float dt_next = 0.f;
-  double total = 0.0;
-  if (w < HW && t0 + lane < sp.len) dt_next = dt[(t0 + lane) * a.sdt.t];
-
-  for (int i = 0; i < chunks; ++i, t0 += step) {
-    const int len = min(kDC, sp.len - t0);
-    if (i > 0) __syncthreads();                            // the chunk before has been read
-    bload.issue(B + t0 * k.scols.t, len, Bp);
-    if (mine) xload.issue(x + t0 * k.srows.t, len, Xh);
-    if (w < HW) {
-      const LaneGates v = make_gates(dt_next, A, bias, a.softplus, len, &gates[w]);
-      total += v.sum;
-      if (KEEP && k.gates && at.part == 0) {               // (heads past the group's repeat the last one's)
-        KeptGates* o = k.gates + (int64_t)(slot0 + t0 / kDC) * a.H + gh;
-        o->g.hi[lane] = v.hi;
-        o->g.lo[lane] = v.lo;
-        o->g.eb[lane] = v.eb;
-        o->g.r[lane] = v.r;
-        o->g.w[lane] = v.w;
-        o->rest[lane] = v.rest;
-        o->slope[lane] = a.softplus ? 1.f / (1.f + expf(-(dt_next + bias))) : 1.f;
-      }
-      if (i + 1 < chunks && t0 + step + lane < sp.len) dt_next = dt[(t0 + step + lane) * a.sdt.t];
-    }
-    wait_vm<0>();
-    __syncthreads();
-    if (!mine) continue;
-    const Gates& q = gates[hw];
-    if constexpr (KEEP) {
-      if (!k.back && sp.first && i == 0 && q.eb[0] == 0.f) S.zero();   // emptied by its first token
-      S.store(k.keep + ((int64_t)(slot0 + t0 / kDC) * a.H + h) * size, tile0, a.P, a.N);
-    }
-    S.decay(q.eb[kDC - 1]);
-    const float* weights = (k.back ? q.eb : q.w) + g * (M::KB / 4);
+  __device__ __forceinline__ int len(int t0) const { return min(kDC, sp.len - t0); }
+  __device__ __forceinline__ void load(int t0, int stage) const {
+    char* s = smem + stage * (kStages - 1) * kStage;
+    cload.issue(cols + t0 * k.scols.t, len(t0), s);
+    if (mine) rload.issue(rows + t0 * k.srows.t, len(t0), s + Z::kB + hw * Z::kX);
+  }
+  __device__ __forceinline__ float load_dt(int t0) const {
+    return w < HW && t0 >= 0 && t0 + lane < sp.len ? dt[(t0 + lane) * a.sdt.t] : 0.f;
+  }
+  // += the chunk in a stage, tokens weighted
+  __device__ __forceinline__ void add(StateRows<T, CT, NT>& S, const LaneAt<T>& L, const Split<T>& split, int stage,
+                                      const float* weights) const {
+    const char *s = smem + stage * (kStages - 1) * kStage, *x = s + Z::kB + hw * Z::kX;
 #pragma unroll
-    for (int s = 0; s < CS; ++s) {
+    for (int st = 0; st < CS; ++st) {
       u32x4 xf[CT];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) xf[c] = L.frag_t(Xh, pw * CT + c, s);
-      S.add(L, xf, Bp, s, weights + s * M::KB, a.N);
+      for (int c = 0; c < CT; ++c) xf[c] = L.frag_t(x, pw * CT + c, st);
+      S.add(L, split, xf, s, st, weights + (lane >> 4) * (M::KB / 4) + st * M::KB, a.N);
     }
   }
-  if (!mine) {
-    // (heads past the group's: nothing is theirs)
-  } else if (!KEEP) {
-    S.store(k.sums + sh * size, tile0, a.P, a.N);
-  } else if (k.back && sp.first && k.end) {
-    S.store(k.end + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
+};
+
+// The state of a segment from zero, for the join.  The chunks go by from the segment's far end (forward walks: the last
+// one first), their weights decayed by what lies between, so that the state itself need not be, and none is read whose
+// weights are zero in fp32.
+template <typename T, int DN, int HW, int PW>
+__device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& k, int seg, int slots, int bid, char* smem) {
+  using K = StateWalker<T, DN, HW, PW>;
+  __shared__ float weights[2][HW][kDC];
+  __shared__ int live[2][HW];
+  ScanPlace at;
+  if (!scan_place(bid, slots, a.G, a.H / a.G, (a.P + K::Z::cols - 1) / K::Z::cols, HW, &at)) return;
+  const SegPlace sp = seg_place(a.seqs, seg, at.slot);
+  if (sp.len <= 0 || (k.back ? sp.first : sp.last)) return;
+  const K q(a, k, at, sp, smem);
+  LaneAt<T> L(q.lane);
+  L.keep();
+  const Split<T> split(q.lane);
+  StateRows<T, K::CT, K::NT> S;
+  S.zero();
+  const int step = k.back ? kDC : -kDC, end = k.back ? q.chunks * kDC : -kDC;
+  int t0 = k.back ? 0 : (q.chunks - 1) * kDC, stage = 0;
+  double F = 0.0;                                            // log decays between the chunk and the segment's end
+  constexpr double kNone = -150.0;                           // base 2: nothing of fp32 is left
+  float dt_next = q.load_dt(t0);
+  auto gates = [&](int t, int st) __attribute__((always_inline)) {   // of the chunk at t, by wave w those of head w
+    if (q.w >= HW) return;
+    const LaneGates v = make_gates(dt_next, q.A, q.bias, a.softplus, q.len(t));
+    dt_next = q.load_dt(t + step);
+    weights[st][q.w][q.lane] = k.back ? exp2_hw((float)(F + v.b)) : v.r * exp2_hw((float)(F + v.sum - v.b));
+    if (q.lane == 0) live[st][q.w] = F > kNone;
+    F += v.sum;
+  };
+  q.load(t0, 0);
+  gates(t0, 0);
+  for (; t0 != end; t0 += step) {
+    wait_vm<0>();
+    __syncthreads();                                         // the stage is there, the other one has been read
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < HW; ++i) any |= live[stage][i] != 0;
+    if (!any) break;
+    if (t0 + step != end) {
+      if (K::kStages == 2) q.load(t0 + step, stage ^ 1);
+      gates(t0 + step, stage ^ 1);
+    }
+    if (q.mine) q.add(S, L, split, stage, weights[stage][q.hw]);
+    if (K::kStages == 1 && t0 + step != end) {
+      __syncthreads();
+      q.load(t0 + step, 0);
+    }
+    stage ^= 1;
   }
-  // (waves of heads past the group's repeat the last one's)
-  if (!KEEP && w < HW && lane == 0 && at.part == 0) k.decays[(int64_t)at.slot * a.H + gh] = exp2_hw((float)total);
+  const int64_t size = (int64_t)a.P * a.N;
+  if (q.mine) S.store(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
+  // (heads past the group's repeat the last one's; after a break F is below kNone and stays there)
+  if (q.w < HW && q.lane == 0 && at.part == 0) k.decays[(int64_t)at.slot * a.H + q.gh] = exp2_hw((float)F);
+}
+
+// The states before (back: after) every chunk, kept for the gradients.
+template <typename T, int DN, int HW, int PW>
+__device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk& k, int seg, int slots, int bid, char* smem) {
+  using K = StateWalker<T, DN, HW, PW>;
+  __shared__ Gates gates[2][HW];
+  ScanPlace at;
+  if (!scan_place(bid, slots, a.G, a.H / a.G, (a.P + K::Z::cols - 1) / K::Z::cols, HW, &at)) return;
+  const SegPlace sp = seg_place(a.seqs, seg, at.slot);
+  if (sp.len <= 0) return;
+  const K q(a, k, at, sp, smem);
+  const int64_t size = (int64_t)a.P * a.N;
+  LaneAt<T> L(q.lane);
+  L.keep();
+  const Split<T> split(q.lane);
+  StateRows<T, K::CT, K::NT> S;
+  S.zero();
+  if (q.mine) {
+    if (k.sums)
+      S.load(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
+    else if (k.start)
+      S.load(k.start + ((int64_t)sp.seq * a.H + q.h) * size, q.tile0, a.P, a.N);
+  }
+  const int slot0 = chunk_slot0(a.seqs, sp.seq) + (sp.tok0 - seq_first(a.seqs, sp.seq)) / kDC;
+  const int step = k.back ? -kDC : kDC, end = k.back ? -kDC : q.chunks * kDC;
+  int t0 = k.back ? (q.chunks - 1) * kDC : 0, stage = 0;
+  float dt_next = q.load_dt(t0);
+  auto make = [&](int t, int st) __attribute__((always_inline)) {   // gates of the chunk at t, by wave w those of head w
+    if (q.w >= HW) return;
+    const LaneGates v = make_gates(dt_next, q.A, q.bias, a.softplus, q.len(t));
+    Gates* o = &gates[st][q.w];
+    const float eb = exp2_hw((float)v.b), rest = exp2_hw((float)(v.sum - v.b));
+    o->eb[q.lane] = eb;
+    o->w[q.lane] = v.r * rest;
+    if (k.gates && at.part == 0) {                           // (heads past the group's repeat the last one's)
+      KeptGates* to = k.gates + (int64_t)(slot0 + t / kDC) * a.H + q.gh;
+      two_parts(v.b, &to->g.hi[q.lane], &to->g.lo[q.lane]);
+      to->g.eb[q.lane] = eb;
+      to->g.r[q.lane] = v.r;
+      to->g.w[q.lane] = v.r * rest;
+      to->rest[q.lane] = rest;
+      to->slope[q.lane] = a.softplus ? 1.f / (1.f + expf(-(dt_next + q.bias))) : 1.f;
+    }
+    dt_next = q.load_dt(t + step);
+  };
+  q.load(t0, 0);
+  make(t0, 0);
+  for (; t0 != end; t0 += step) {
+    wait_vm<0>();
+    __syncthreads();                                         // the stage is there, the other one has been read
+    const Gates& g = gates[stage][q.hw];
+    if (q.mine) {
+      if (!k.back && sp.first && t0 == 0 && g.eb[0] == 0.f) S.zero();   // emptied by its first token
+      S.store(k.keep + ((int64_t)(slot0 + t0 / kDC) * a.H + q.h) * size, q.tile0, a.P, a.N);
+    }
+    if (t0 + step != end) {
+      if (K::kStages == 2) q.load(t0 + step, stage ^ 1);
+      make(t0 + step, stage ^ 1);
+    }
+    if (q.mine) {
+      S.decay(g.eb[kDC - 1]);
+      q.add(S, L, split, stage, k.back ? g.eb : g.w);
+    }
+    if (K::kStages == 1 && t0 + step != end) {
+      __syncthreads();
+      q.load(t0 + step, 0);
+    }
+    stage ^= 1;
+  }
+  if (q.mine && k.back && sp.first && k.end)
+    S.store(k.end + ((int64_t)sp.seq * a.H + q.h) * size, q.tile0, a.P, a.N);
 }
 
 // Walks of one or two directions: the first `half` workgroups take `one`, the others `two`.
 template <typename T, int DN, int HW, int PW, bool KEEP>
 __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan_states(ScanArgs a, StateWalk one, StateWalk two, int seg, int slots,
                                                                  int half) {
+#if __HIP_DEVICE_COMPILE__
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ Gates gates[HW];
   const bool second = (int)blockIdx.x >= half;
-  walk_segment<T, DN, HW, PW, KEEP>(a, second ? two : one, seg, slots, second ? blockIdx.x - half : blockIdx.x, smem, gates);
+  const StateWalk& k = second ? two : one;
+  const int bid = second ? blockIdx.x - half : blockIdx.x;
+  if constexpr (KEEP)
+    keep_segment<T, DN, HW, PW>(a, k, seg, slots, bid, smem);
+  else
+    sum_segment<T, DN, HW, PW>(a, k, seg, slots, bid, smem);
+#endif
 }
 
 template <typename T, int DN, int HW, int PW, bool KEEP>
 hipError_t launch_states(const ScanArgs& a, const StateWalk& one, const StateWalk* two, int seg, int64_t slots, hipStream_t s) {
   using Z = ScanShape<T, DN, HW, PW>;
-  constexpr int smem = Z::kB + HW * Z::kX;
-  static_assert(smem + (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
+  using K = StateWalker<T, DN, HW, PW>;
+  constexpr int smem = K::kStages * K::kStage;
+  static_assert(smem + 2 * (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
   const int64_t shared = a.H / a.G;
   const int64_t half = walk_blocks(slots * a.G, (shared + HW - 1) / HW * ((a.P + Z::cols - 1) / Z::cols));
   k_scan_states<T, DN, HW, PW, KEEP><<<dim3((unsigned)(two ? 2 * half : half)), 64 * HW * PW, smem, s>>>(
