@@ -142,17 +142,28 @@ struct LaneGates {
   double b, sum;                      // running sum of the log decays, the chunk's
   float r;
 };
+// Lane i's x added to lane i + by, within the rows of 16 (by < 16) or from row to row (row_bcast), nothing where no lane is.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add(double x) {
+  const u32x2 v = __builtin_bit_cast(u32x2, x);
+  const u32x2 up = {(unsigned)__builtin_amdgcn_update_dpp(0, (int)v[0], CTRL, ROWS, 0xf, false),
+                    (unsigned)__builtin_amdgcn_update_dpp(0, (int)v[1], CTRL, ROWS, 0xf, false)};
+  return x + __builtin_bit_cast(double, up);
+}
 __device__ __forceinline__ LaneGates make_gates(float dt, float A, float bias, bool softplus, int len) {
   const int lane = lane_id();
   LaneGates v;
   v.r = lane < len ? scan_rate(dt, bias, softplus) : 0.f;
-  v.b = lane < len ? fmax((double)A * v.r, kLeastLog) * 1.4426950408889634 : 0.0;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const double up = __shfl_up(v.b, m, 64);
-    if (lane >= m) v.b += up;
-  }
-  v.sum = __shfl(v.b, 63, 64);
+  double b = lane < len ? fmax((double)A * v.r, kLeastLog) * 1.4426950408889634 : 0.0;
+  b = dpp_add<0x111, 0xf>(b);         // row_shr 1, 2, 4, 8
+  b = dpp_add<0x112, 0xf>(b);
+  b = dpp_add<0x114, 0xf>(b);
+  b = dpp_add<0x118, 0xf>(b);
+  b = dpp_add<0x142, 0xa>(b);         // row_bcast 15 into rows 1 and 3, 31 into 2 and 3
+  b = dpp_add<0x143, 0xc>(b);
+  const u32x2 w = __builtin_bit_cast(u32x2, b);
+  const u32x2 l = {(unsigned)__builtin_amdgcn_readlane((int)w[0], 63), (unsigned)__builtin_amdgcn_readlane((int)w[1], 63)};
+  v.b = b;
+  v.sum = __builtin_bit_cast(double, l);
   return v;
 }
 // b in two parts, the first a multiple of 2^-8 below 2^14: differences of first parts are exact.

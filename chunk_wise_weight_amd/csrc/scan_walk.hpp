@@ -196,7 +196,7 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
       to->g.r[q.lane] = v.r;
       to->g.w[q.lane] = v.r * rest;
       to->rest[q.lane] = rest;
-      to->slope[q.lane] = a.softplus ? 1.f / (1.f + expf(-(dt_next + q.bias))) : 1.f;
+      to->slope[q.lane] = scan_rate_slope(dt_next, q.bias, a.softplus);
     }
     dt_next = q.load_dt(t + step);
   };
