@@ -32,8 +32,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   const int p0 = at.part * Z::cols, tile0 = (p0 >> 4) + pw * CT;
   const int64_t sh = (int64_t)at.slot * a.H + h, size = (int64_t)a.P * a.N;
 
-  LaneAt<T> L(lane);
-  L.keep();
+  const LaneAt<T> L(lane);
   const Split<T> split(lane);
   StateRows<T, CT, NT> S;
   S.zero();
@@ -44,8 +43,8 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
       S.load(a.S_init + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
   }
 
-  const PanelLoader<T, DN, W> bload(a.sB.t * sizeof(T), a.N * sizeof(T)), cload(a.sC.t * sizeof(T), a.N * sizeof(T));
-  const PanelLoader<T, Z::DX, PW> xload(a.sx.t * sizeof(T), min(a.P - p0, Z::cols) * sizeof(T));
+  const TileLoader<T, DN, W> bload(a.sB.t * sizeof(T), a.N * sizeof(T)), cload(a.sC.t * sizeof(T), a.N * sizeof(T));
+  const TileLoader<T, Z::DX, PW> xload(a.sx.t * sizeof(T), min(a.P - p0, Z::cols) * sizeof(T));
   const T* B = (const T*)a.B + sp.b * a.sB.b + at.group * a.sB.h + sp.tok0 * a.sB.t;
   const T* C = (const T*)a.C + sp.b * a.sC.b + at.group * a.sC.h + sp.tok0 * a.sC.t;
   const T* x = (const T*)a.x + sp.b * a.sx.b + h * a.sx.h + sp.tok0 * a.sx.t + p0;
@@ -97,7 +96,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
     for (int s = 0; s < CS; ++s)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) xf[s][c] = L.frag_t(Xh, pw * CT + c, s);
+      for (int c = 0; c < CT; ++c) xf[s][c] = L.cols_row(Xh, pw * CT + c, s);
     // C B^T of a fragment's tokens row(t, .) and those before them
     int made = -1;
     f32x4 d[U];
@@ -162,7 +161,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
         for (int c = 0; c < CT; ++c) split.two(&S.s[c][ns * U], hi[c], lo[c]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const u32x4 f = L.frag(Cp, t, ns);
+          const u32x4 f = L.halves(Cp, t, ns);
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             if (M::kSplit) o[c][t] = M::mma(lo[c], f, o[c][t]);

@@ -8,8 +8,7 @@
 // are cut into segments of whole chunks so that the walks fill the chip: a first pass makes every segment's state from
 // zero, a second adds them up over each sequence's segments, and the last has each segment's walk begin where it should.
 //
-// Operands are as in delta.hpp (Mat, Panels): a product's result is the next one's operand without leaving the
-// registers.  The outputs are made transposed, rows of P by tokens, so that a lane has consecutive features of a token.
+// Operands are as in delta.hpp (Mat): a product's result is the next one's operand without leaving the registers.  The outputs are made transposed, rows of P by tokens, so that a lane has consecutive features of a token.
 //
 // Precision (bf16 inputs).  x, B and C enter as they are.  What is fp32 enters as sums of bf16 values: the scaled x of
 // the state's update as three (24 bits), the state and the decayed C B^T of the outputs as two (17 bits), so that the
@@ -70,69 +69,115 @@ template <typename T> __device__ __forceinline__ void tri_place(int f, int* t, i
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Where a lane reads operands in panels of 64 rows (delta.hpp): the parts that depend on it, kept in registers; blocks and
-// steps are offsets from there.  Row block t: rows row(t, .); column block t: columns row(t, .), the rows being contracted.
+// Tiles in LDS: panels of 64 rows of 128 bytes, the 16-byte chunk c of row r in slot c ^ row_swz(r).  Rows are read 16 a
+// time (row(t, .) differ in bits 0, 1, 3 and 4; LDS serves lanes 0-3 and 12-15 of a group with 4-11 of the next, whose
+// slots differ by 1), columns by transposing reads of 8 bytes from 4 rows a lane group, a whole 32 bytes of each: all fall
+// into different banks.
 constexpr int kPanel64 = 64 * 128;
-template <typename T> struct LaneAt;
-template <> struct LaneAt<bf16> {
-  unsigned f[2], c[2];
-  __device__ __forceinline__ explicit LaneAt(int lane) {
-    const int m = lane & 15, g = lane >> 4, r = (m >> 2) * 8 + (m & 3), rt = g * 8 + (m >> 2);
+__device__ __forceinline__ int row_swz(int r) { return ((r >> 1) & 1) << 1 ^ ((r >> 3) & 1) << 2 ^ ((r >> 4) & 1) * 5; }
+template <typename T> constexpr int tile_bytes(int cols) { return cols * (int)sizeof(T) * 64; }
+
+// DMA of a tile of DK columns by NW waves, 8 rows of a panel an instruction.  Rows >= len and columns >= row_bytes read
+// as zero; the lanes' offsets are the same for every chunk of a walk and made once.
+template <typename T, int DK, int NW> struct TileLoader {
+  static constexpr int N = tile_bytes<T>(DK) / 1024 / NW;
+  static_assert(N >= 1, "an instruction a wave");
+  unsigned off[N];
+  __device__ __forceinline__ TileLoader(unsigned pitch, unsigned row_bytes) {
+    const int L = lane_id(), w = wave_id() % NW;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f[b] = r * 128 + (((4 * b + g) ^ panel_swz(r)) << 4);
-      c[b] = rt * 128 + (((4 * b + (m & 3)) ^ panel_swz(rt)) << 4);
+    for (int j = 0; j < N; ++j) {
+      const int i = j * NW + w, b = i % 8, r = b * 8 + (L >> 3);
+      const unsigned byte = (unsigned)(((L & 7) ^ row_swz(r)) << 4) + (unsigned)(i / 8) * 128u;
+      off[j] = byte < row_bytes ? (unsigned)r * pitch + byte : kOOB;
     }
   }
-  __device__ __forceinline__ void keep() {
-    asm volatile("" : "+v"(f[0]), "+v"(f[1]), "+v"(c[0]), "+v"(c[1]));
-  }
-  __device__ static __forceinline__ int rows(int t) { return (t >> 1) * 4096 + (t & 1) * 512; }
-  // 16 bytes of the lane's row of block t, step s
-  __device__ __forceinline__ u32x4 frag(const char* p, int t, int s) const {
-    return *reinterpret_cast<const u32x4*>(p + f[s & 1] + ((s >> 1) * kPanel64 + rows(t)));
-  }
-  // the lane's column of block t, rows of step s
-  __device__ __forceinline__ u32x4 frag_t(const char* p, int t, int s) const {
-    const char* q = p + c[(t >> 1) & 1] + ((t >> 2) * kPanel64 + s * 4096 + (t & 1) * 8);
-    const u32x2 a = __builtin_bit_cast(u32x2, lds_read_tr16(q)), b = __builtin_bit_cast(u32x2, lds_read_tr16(q + 512));
-    return (u32x4){a[0], a[1], b[0], b[1]};
-  }
-  // columns row(ct, 4 g + 0..3) of the lane's row of block t
-  __device__ __forceinline__ f32x4 at4(const char* p, int t, int ct) const {
-    return load4((const bf16*)(p + f[(ct >> 1) & 1] + ((ct >> 2) * kPanel64 + (ct & 1) * 8 + rows(t))));
+  __device__ __forceinline__ void issue(const void* rows, int len, char* t) const {
+#if __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
+    const int L = lane_id(), w = wave_id() % NW;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = j * NW + w;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
+                                               len >= 64 || (i % 8) * 8 + (L >> 3) < len ? off[j] : kOOB, 0, 0, 0);
+    }
+#endif
   }
 };
+
+// Where a lane reads operands of a tile: the parts that depend on it, in registers; blocks and steps are offsets (or flip
+// bits of the slot) from there.
+//   place, frag  16 bytes of row(t, lane & 15) at step s of the columns
+//   halves       the same with the columns in the order in which two blocks of results hold them: 4 g + 0..3 of each
+//   cols         column 16 t + (lane & 15), rows of step s (as a contraction over rows takes them); cols_row: row(t, .)
+//   at, at_row   columns 16 ct + 4 g + 0..3, row(ct, 4 g + 0..3), of row(t, lane & 15)
+template <typename T> struct LaneAt;
+template <> struct LaneAt<bf16> {
+  unsigned f, c, n, h;
+  __device__ __forceinline__ explicit LaneAt(int lane) {
+    const int m = lane & 15, g = lane >> 4, r = (m >> 2) * 8 + (m & 3), rt = g * 8 + (m >> 2);
+    f = r * 128 + ((g ^ row_swz(r)) << 4);
+    h = r * 128 + (((g >> 1) ^ row_swz(r)) << 4) + (g & 1) * 8;
+    c = rt * 128 + (((m & 3) ^ row_swz(rt)) << 4);
+    n = rt * 128 + ((((m >> 1) & 1) ^ row_swz(rt)) << 4) + (m & 1) * 8;
+    asm volatile("" : "+v"(f), "+v"(c), "+v"(n), "+v"(h));
+  }
+  __device__ static __forceinline__ int rows(int t) { return (t >> 1) * 4096 + (t & 1) * 512; }
+  __device__ static __forceinline__ u32x4 pair(u32x2 a, u32x2 b) { return (u32x4){a[0], a[1], b[0], b[1]}; }
+  __device__ static __forceinline__ u32x4 read_t(const char* q) {
+    return pair(__builtin_bit_cast(u32x2, lds_read_tr16(q)), __builtin_bit_cast(u32x2, lds_read_tr16(q + 512)));
+  }
+  __device__ __forceinline__ char* place(char* p, int t, int s) const {
+    return p + (f ^ (unsigned)(s & 1) << 6) + ((s >> 1) * kPanel64 + rows(t));
+  }
+  __device__ __forceinline__ u32x4 frag(const char* p, int t, int s) const {
+    return *reinterpret_cast<const u32x4*>(place(const_cast<char*>(p), t, s));
+  }
+  __device__ __forceinline__ u32x4 halves(const char* p, int t, int s) const {
+    const int o = (s >> 1) * kPanel64 + rows(t);
+    return pair(*reinterpret_cast<const u32x2*>(p + (h ^ (unsigned)(s & 1) << 6) + o),
+                *reinterpret_cast<const u32x2*>(p + (h ^ (unsigned)(s & 1) << 6 ^ 32u) + o));
+  }
+  __device__ __forceinline__ u32x4 cols(const char* p, int t, int s) const {
+    return read_t(p + (n ^ (unsigned)(t & 3) << 5) + ((t >> 2) * kPanel64 + s * 4096));
+  }
+  __device__ __forceinline__ u32x4 cols_row(const char* p, int t, int s) const {
+    return read_t(p + (c ^ (unsigned)((t >> 1) & 1) << 6) + ((t >> 2) * kPanel64 + s * 4096 + (t & 1) * 8));
+  }
+  __device__ __forceinline__ f32x4 at(const char* p, int t, int ct) const {
+    return load4((const bf16*)(p + (h ^ (unsigned)(ct & 3) << 5) + ((ct >> 2) * kPanel64 + rows(t))));
+  }
+  __device__ __forceinline__ f32x4 at_row(const char* p, int t, int ct) const {
+    return load4((const bf16*)(p + (f ^ (unsigned)((ct >> 1) & 1) << 6) + ((ct >> 2) * kPanel64 + (ct & 1) * 8 + rows(t))));
+  }
+};
+// fp32: row(t, i) is 16 t + i, and a step's contraction goes over 16.
 template <> struct LaneAt<float> {
-  unsigned f[2], c[2][2];
+  unsigned f, c;
   __device__ __forceinline__ explicit LaneAt(int lane) {
     const int m = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f[b] = m * 128 + (((4 * b + g) ^ panel_swz(m)) << 4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = g * 4 + 2 * i;
-        c[i][b] = r * 128 + (((4 * b + (m >> 2)) ^ panel_swz(r)) << 4) + ((m & 3) << 2);
-      }
-    }
+    f = m * 128 + ((g ^ row_swz(m)) << 4);
+    c = g * 512 + (((m >> 2) ^ row_swz(4 * g)) << 4) + (m & 3) * 4;
+    asm volatile("" : "+v"(f), "+v"(c));
   }
-  __device__ __forceinline__ void keep() {
-    asm volatile("" : "+v"(f[0]), "+v"(f[1]), "+v"(c[0][0]), "+v"(c[0][1]), "+v"(c[1][0]), "+v"(c[1][1]));
+  __device__ __forceinline__ char* place(char* p, int t, int s) const {
+    return p + (f ^ (unsigned)(s & 1) << 6 ^ (unsigned)(t & 1) * 0x50u) + ((s >> 1) * kPanel64 + t * 2048);
   }
-  // (the swizzle of row 16 t + m is that of m with the third bit flipped for odd t)
   __device__ __forceinline__ u32x4 frag(const char* p, int t, int s) const {
-    return *reinterpret_cast<const u32x4*>(p + f[(s ^ t) & 1] + ((s >> 1) * kPanel64 + t * 2048));
+    return *reinterpret_cast<const u32x4*>(place(const_cast<char*>(p), t, s));
   }
-  __device__ __forceinline__ u32x4 frag_t(const char* p, int t, int s) const {
-    const int b = (t ^ s) & 1, o = (t >> 1) * kPanel64 + s * 2048;
-    const char *q0 = p + c[0][b] + o, *q1 = p + c[1][b] + o;
+  __device__ __forceinline__ u32x4 halves(const char* p, int t, int s) const { return frag(p, t, s); }
+  __device__ __forceinline__ u32x4 cols(const char* p, int t, int s) const {
+    const unsigned q = c ^ (unsigned)(t & 1) << 6 ^ (unsigned)(s & 1) * 0x50u;
+    const int o = (t >> 1) * kPanel64 + s * 2048;
+    const char *q0 = p + q + o, *q1 = p + (q ^ 32u) + o;
     return (u32x4){*reinterpret_cast<const unsigned*>(q0), *reinterpret_cast<const unsigned*>(q0 + 128),
-                   *reinterpret_cast<const unsigned*>(q1), *reinterpret_cast<const unsigned*>(q1 + 128)};
+                   *reinterpret_cast<const unsigned*>(q1 + 256), *reinterpret_cast<const unsigned*>(q1 + 384)};
   }
-  __device__ __forceinline__ f32x4 at4(const char* p, int t, int ct) const {
-    return *reinterpret_cast<const f32x4*>(p + f[(ct ^ t) & 1] + ((ct >> 1) * kPanel64 + t * 2048));
-  }
+  __device__ __forceinline__ u32x4 cols_row(const char* p, int t, int s) const { return cols(p, t, s); }
+  __device__ __forceinline__ f32x4 at(const char* p, int t, int ct) const { return __builtin_bit_cast(f32x4, frag(p, t, ct)); }
+  __device__ __forceinline__ f32x4 at_row(const char* p, int t, int ct) const { return at(p, t, ct); }
 };
 
 // A chunk's gates for one head, base 2 logarithms, a lane for each token (one wave; tokens past len leave the state
@@ -262,11 +307,11 @@ template <typename T, int DN_, int HW_, int PW_> struct ScanShape {
   static constexpr int NT = DN / 16, NS = DN / Mat<T>::KB, CS = kDC / Mat<T>::KB;
   static constexpr int cols = 16 * CT * PW;                 // of P, of a workgroup's heads
   static constexpr int kLine = 128 / (int)sizeof(T), DX = cols < kLine ? kLine : cols;
-  static constexpr int kB = Panels<T>::bytes(DN), kX = Panels<T>::bytes(DX);
+  static constexpr int kB = tile_bytes<T>(DN), kX = tile_bytes<T>(DX);
   static constexpr int kM = Mat<T>::kTri * 1024 * (Mat<T>::kSplit ? 2 : 1);
 };
 
-// State rows of a wave: element p = row(ct, lane & 15) of its rows, n = Mat::row(nt, 4 g + 0..3).
+// State rows of a wave: element p = row(ct, lane & 15) of its rows, n = 16 nt + 4 g + 0..3.
 template <typename T, int CT, int NT> struct StateRows {
   f32x4 s[CT][NT];
   __device__ __forceinline__ void zero() {
@@ -283,7 +328,7 @@ template <typename T, int CT, int NT> struct StateRows {
       const int p = Mat<T>::row(tile0 + c, m);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int n = Mat<T>::row(t, 4 * g);
+        const int n = t * 16 + 4 * g;
         s[c][t] = p < P && n < N ? *reinterpret_cast<const f32x4*>(S + (int64_t)p * N + n) : (f32x4){0.f, 0.f, 0.f, 0.f};
       }
     }
@@ -295,7 +340,7 @@ template <typename T, int CT, int NT> struct StateRows {
       const int p = Mat<T>::row(tile0 + c, m);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int n = Mat<T>::row(t, 4 * g);
+        const int n = t * 16 + 4 * g;
         if (p < P && n < N) *reinterpret_cast<f32x4*>(S + (int64_t)p * N + n) = s[c][t];
       }
     }
@@ -310,7 +355,7 @@ template <typename T, int CT, int NT> struct StateRows {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (NT > 8 && t % 4 == 0 && t * 16 >= N) break;
-      const u32x4 f = L.frag_t(cols, t, step);
+      const u32x4 f = L.cols(cols, t, step);
 #pragma unroll
       for (int k = Scaled<T>::kParts - 1; k >= 0; --k) {
         s[0][t] = Mat<T>::mma(f, u0.part[k], s[0][t]);

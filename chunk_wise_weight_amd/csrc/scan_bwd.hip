@@ -29,17 +29,17 @@ template <typename T, bool LDS> struct Features {
     const int r = Mat<T>::row(t, lane_id() & 15), n = s * 16 + (lane_id() >> 4) * 4;
     return r < len && n < N ? *reinterpret_cast<const u32x4*>(rows + r * pitch + n) : (u32x4){0, 0, 0, 0};
   }
-  __device__ __forceinline__ u32x4 frag_t(const LaneAt<T>& L, int t, int s) const {
-    if constexpr (LDS) return L.frag_t(lds, t, s);
+  __device__ __forceinline__ u32x4 cols(const LaneAt<T>& L, int t, int s) const {
+    if constexpr (LDS) return L.cols(lds, t, s);
     const int n = t * 16 + (lane_id() & 15), r = s * 16 + (lane_id() >> 4) * 4;
     u32x4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = r + i < len && n < N ? __float_as_uint((float)rows[(r + i) * pitch + n]) : 0u;
     return o;
   }
-  __device__ __forceinline__ f32x4 at4(const LaneAt<T>& L, int t, int ct) const {
-    if constexpr (LDS) return L.at4(lds, t, ct);
-    const int r = Mat<T>::row(t, lane_id() & 15), n = Mat<T>::row(ct, (lane_id() >> 4) * 4);
+  __device__ __forceinline__ f32x4 at(const LaneAt<T>& L, int t, int ct) const {
+    if constexpr (LDS) return L.at(lds, t, ct);
+    const int r = Mat<T>::row(t, lane_id() & 15), n = ct * 16 + (lane_id() >> 4) * 4;
     return r < len && n < N ? load4(rows + r * pitch + n) : (f32x4){0.f, 0.f, 0.f, 0.f};
   }
 };
@@ -50,8 +50,8 @@ template <typename T, int DN_, bool LDS_> struct GradShape {
   static constexpr int DN = DN_, NB = DN / kBN, KS = kBN / Mat<T>::KB;
   static constexpr bool LDS = LDS_;
   static constexpr int SP = Mat<T>::kSplit ? 3 : 1;          // planes of a state: their sum is it
-  static constexpr int kB = LDS ? Panels<T>::bytes(DN) : 0, kS = Panels<T, kBV>::bytes(kBN), kX = Panels<T>::bytes(kBV);
-  static constexpr int kM = Panels<T>::bytes(kDC);           // a 64 x 64 matrix (bf16: and what its rounding left)
+  static constexpr int kB = LDS ? tile_bytes<T>(DN) : 0, kS = tile_bytes<T>(kBN), kX = tile_bytes<T>(kBV);
+  static constexpr int kM = tile_bytes<T>(kDC);           // a 64 x 64 matrix (bf16: and what its rounding left)
   static constexpr int kMs = kM * (Mat<T>::kSplit ? 2 : 1);
   // x, dO and the gates come by DMA, where LDS has room for it while the block before is worked on.
   static constexpr int XB = 2 * kB + 2 * SP * kS + 4 * kX + kMs <= kMaxLds - 12 * 1024 ? 2 : 1;
@@ -81,7 +81,7 @@ __device__ __forceinline__ u32x4 load_or_zero(__amdgpu_buffer_rsrc_t rs, unsigne
 template <typename T, int SP>
 __device__ __forceinline__ void put_planes(f32x4 a, f32x4 b, char* plane, int stride, int r, int c8) {
   if constexpr (sizeof(T) == 2) {
-    char* at = plane + r * 128 + ((c8 ^ panel_swz(r)) << 4);
+    char* at = plane + r * 128 + ((c8 ^ row_swz(r)) << 4);
     unsigned v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -105,8 +105,9 @@ __device__ __forceinline__ void put_planes(f32x4 a, f32x4 b, char* plane, int st
       *reinterpret_cast<u32x4*>(at + k * stride) = w;
     }
   } else {
-    *reinterpret_cast<f32x4*>(plane + Panels<T, kBV>::at(r, c8 * 8)) = a;
-    *reinterpret_cast<f32x4*>(plane + Panels<T, kBV>::at(r, c8 * 8 + 4)) = b;
+    char* at = plane + (c8 >> 2) * kPanel64 + r * 128;
+    *reinterpret_cast<f32x4*>(at + (((c8 & 3) * 2 ^ row_swz(r)) << 4)) = a;
+    *reinterpret_cast<f32x4*>(at + (((c8 & 3) * 2 + 1 ^ row_swz(r)) << 4)) = b;
   }
 }
 
@@ -145,11 +146,10 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   const Features<T, LDS> B{smem, (const T*)p.B + c.b * p.sB.b + grp * p.sB.h + c.tok0 * p.sB.t, p.sB.t, len, N};
   const Features<T, LDS> C{smem + Z::kB, (const T*)p.C + c.b * p.sC.b + grp * p.sC.h + c.tok0 * p.sC.t, p.sC.t, len, N};
   if constexpr (LDS) {
-    PanelLoader<T, DN, 8>(p.sB.t * sizeof(T), N * sizeof(T)).issue(B.rows, len, smem);
-    PanelLoader<T, DN, 8>(p.sC.t * sizeof(T), N * sizeof(T)).issue(C.rows, len, smem + Z::kB);
+    TileLoader<T, DN, 8>(p.sB.t * sizeof(T), N * sizeof(T)).issue(B.rows, len, smem);
+    TileLoader<T, DN, 8>(p.sC.t * sizeof(T), N * sizeof(T)).issue(C.rows, len, smem + Z::kB);
   }
-  LaneAt<T> L(lane);
-  L.keep();
+  const LaneAt<T> L(lane);
   const Split<T> split(lane);
   char *const Sp = smem + Z::oS, *const Dp = Sp + SP * Z::kS, *const Mp = smem + Z::oM;
 
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   const unsigned soff = (unsigned)(row8 * N + col8) * 4u;
   const unsigned dxoff = dtok < len ? (unsigned)dtok * (unsigned)(a.sdx.t * sizeof(T)) : kOOB;
   u32x4 ns[2], nd[2];
-  const PanelLoader<T, kBV, 8> xload(p.sx.t * sizeof(T), kBV * sizeof(T)), yload(a.sdO.t * sizeof(T), kBV * sizeof(T));
+  const TileLoader<T, kBV, 8> xload(p.sx.t * sizeof(T), kBV * sizeof(T)), yload(a.sdO.t * sizeof(T), kBV * sizeof(T));
   auto load_states = [&](const float* s, const float* d, int p0, int n0) __attribute__((always_inline)) {
     const unsigned off = p0 + row8 < P && n0 + col8 < N ? soff : kOOB;
     const __amdgpu_buffer_rsrc_t rs = rows_rsrc(s + (int64_t)p0 * N + n0), rd = rows_rsrc(d + (int64_t)p0 * N + n0);
@@ -183,8 +183,8 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       xload.issue(xh + p0, len, to);
       yload.issue(yh + p0, len, to + Z::kX);
     } else {
-      PanelLoader<T, kBV, 8>(p.sx.t * sizeof(T), (P - p0) * sizeof(T)).issue(xh + p0, len, to);
-      PanelLoader<T, kBV, 8>(a.sdO.t * sizeof(T), (P - p0) * sizeof(T)).issue(yh + p0, len, to + Z::kX);
+      TileLoader<T, kBV, 8>(p.sx.t * sizeof(T), (P - p0) * sizeof(T)).issue(xh + p0, len, to);
+      TileLoader<T, kBV, 8>(a.sdO.t * sizeof(T), (P - p0) * sizeof(T)).issue(yh + p0, len, to + Z::kX);
     }
   };
   auto load_gates = [&](const char* from, char* to) __attribute__((always_inline)) {
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
               }
               u32x4 hi, lo;
               split.two(w, hi, lo);
-              char* f = Mp + Panels<T>::at(i, M::row(fs[k] * U, 4 * g));
+              char* f = L.place(Mp, ft[k], fs[k]);
               *reinterpret_cast<u32x4*>(f) = hi;
               if (M::kSplit) *reinterpret_cast<u32x4*>(f + Z::kM) = lo;
             }
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
           for (int s = 0; s < KS; ++s) {
             u32x4 f[SP], b[4];
 #pragma unroll
-            for (int z = 0; z < SP; ++z) f[z] = L.frag_t(state + z * Z::kS, nt, s);
+            for (int z = 0; z < SP; ++z) f[z] = L.cols(state + z * Z::kS, nt, s);
 #pragma unroll
             for (int t = 0; t < 4; ++t) b[t] = L.frag(other, t, s);
 #pragma unroll
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
           }
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            dot[t] += dot4(o[t], own.at4(L, t, 4 * nb + nt));
+            dot[t] += dot4(o[t], own.at(L, t, 4 * nb + nt));
             acc[nb][t] += scales[M::row(t, m)] * o[t];
           }
         }
@@ -344,12 +344,12 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
 #pragma unroll
         for (int s = 0; s < CS; ++s) {
           if (s < M::first(dtile)) continue;
-          const u32x4 hi = L.frag_t(Mp, dtile, s);
+          const u32x4 hi = L.cols_row(Mp, dtile, s);
           u32x4 lo;
-          if constexpr (M::kSplit) lo = L.frag_t(Mp + Z::kM, dtile, s);
+          if constexpr (M::kSplit) lo = L.cols_row(Mp + Z::kM, dtile, s);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const u32x4 o = L.frag_t(Yp, dblock + k, s);
+            const u32x4 o = L.cols_row(Yp, dblock + k, s);
             if constexpr (M::kSplit) du[k] = M::mma(o, lo, du[k]);
             du[k] = M::mma(o, hi, du[k]);
           }
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
           const int pp = M::row(dblock + k, 4 * g);
           f32x4 v[PB];
 #pragma unroll
-          for (int e = 0; e < PB; ++e) v[e] = r * du[k + e] + D * L.at4(Yp, dtile, dblock + k + e);
+          for (int e = 0; e < PB; ++e) v[e] = r * du[k + e] + D * L.at_row(Yp, dtile, dblock + k + e);
           // (outside of the rows and of P: nothing is written)
           const unsigned off = p0 + pp < P ? dxoff + pp * (unsigned)sizeof(T) : kOOB;
           __builtin_amdgcn_raw_buffer_store_b128(M::frag(v), rs, off, 0, 0);
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       if (g == 0) sums.rows[s][i] = rs;
       u32x4 hi, lo;
       split.two(w, hi, lo);
-      char* f = Mp + Panels<T>::at(i, M::row(s * U, 4 * g));
+      char* f = L.place(Mp, t, s);
       *reinterpret_cast<u32x4*>(f) = hi;
       if (M::kSplit) *reinterpret_cast<u32x4*>(f + Z::kM) = lo;
     }
@@ -425,14 +425,14 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
         u32x4 f[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-          if (NB <= 2 || n * kBN < N) f[n] = cross.frag_t(L, 4 * n + nt, s);
+          if (NB <= 2 || n * kBN < N) f[n] = cross.cols(L, 4 * n + nt, s);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           if (BACK ? s < M::first(t) : s >= M::steps(t)) continue;
-          const u32x4 hi = BACK ? L.frag_t(Mp, t, s) : L.frag(Mp, t, s);
+          const u32x4 hi = BACK ? L.cols_row(Mp, t, s) : L.frag(Mp, t, s);
           u32x4 lo;
           if constexpr (M::kSplit)
-            lo = BACK ? L.frag_t(Mp + Z::kM, t, s) : L.frag(Mp + Z::kM, t, s);
+            lo = BACK ? L.cols_row(Mp + Z::kM, t, s) : L.frag(Mp + Z::kM, t, s);
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             if (NB > 2 && n * kBN >= N) continue;
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   for (int n = 0; n < NB; ++n)
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int i = M::row(t, m), col = n * kBN + M::row(nt, 4 * g);
+      const int i = M::row(t, m), col = n * kBN + nt * 16 + 4 * g;
       if (i < len && col < N) store4(out + i * pitch + col, acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
     }
 #endif

@@ -53,8 +53,8 @@ template <typename T, int DN, int HW, int PW> struct StateWalker {
   SegPlace sp;
   int w, hw, pw, lane, h, gh, tile0, chunks;
   bool mine;                                                 // a head of the group
-  PanelLoader<T, DN, W> cload;
-  PanelLoader<T, Z::DX, PW> rload;
+  TileLoader<T, DN, W> cload;
+  TileLoader<T, Z::DX, PW> rload;
   const T *cols, *rows;
   const float* dt;
   float A, bias;
@@ -93,7 +93,7 @@ template <typename T, int DN, int HW, int PW> struct StateWalker {
     for (int st = 0; st < CS; ++st) {
       u32x4 xf[CT];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) xf[c] = L.frag_t(x, pw * CT + c, st);
+      for (int c = 0; c < CT; ++c) xf[c] = L.cols_row(x, pw * CT + c, st);
       S.add(L, split, xf, s, st, weights + (lane >> 4) * (M::KB / 4) + st * M::KB, a.N);
     }
   }
@@ -112,8 +112,7 @@ __device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& 
   const SegPlace sp = seg_place(a.seqs, seg, at.slot);
   if (sp.len <= 0 || (k.back ? sp.first : sp.last)) return;
   const K q(a, k, at, sp, smem);
-  LaneAt<T> L(q.lane);
-  L.keep();
+  const LaneAt<T> L(q.lane);
   const Split<T> split(q.lane);
   StateRows<T, K::CT, K::NT> S;
   S.zero();
@@ -167,8 +166,7 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
   if (sp.len <= 0) return;
   const K q(a, k, at, sp, smem);
   const int64_t size = (int64_t)a.P * a.N;
-  LaneAt<T> L(q.lane);
-  L.keep();
+  const LaneAt<T> L(q.lane);
   const Split<T> split(q.lane);
   StateRows<T, K::CT, K::NT> S;
   S.zero();
