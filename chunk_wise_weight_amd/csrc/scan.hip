@@ -17,7 +17,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   using M = Mat<T>;
   constexpr int CT = Z::CT, NT = Z::NT, NS = Z::NS, CS = Z::CS, W = Z::W, U = M::TPS;
   constexpr int PB = CT == 2 && U == 2 ? 2 : 1, CB = CT / PB;  // blocks of P that are stored as one; of those
-  constexpr int UNITS = M::kTri * HW, PER = (UNITS + W - 1) / W;   // (fragment, head) pairs, a wave's
+  constexpr int FW = (M::kTri + W - 1) / W;                // fragments of C B^T a wave makes: w, w + W, ..
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ Gates gates[2][HW];
   char *const Bp = smem, *const Cp = Bp + Z::kB, *const Xp = Cp + Z::kB, *const Mp = Xp + HW * Z::kX;
@@ -50,17 +50,20 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   const T* x = (const T*)a.x + sp.b * a.sx.b + h * a.sx.h + sp.tok0 * a.sx.t + p0;
   T* O = (T*)a.O + sp.b * a.sO.b + h * a.sO.h + sp.tok0 * a.sO.t;
   char *const Xh = Xp + hw * Z::kX, *const Mh = Mp + hw * Z::kM;
-  // the gates of head head0 + w are made by wave w
-  const int gh = at.group * shared + min(at.head0 + w, shared - 1);
+  // the heads' gates are made by the last waves, which have fewer fragments
+  const int gw = w - (W - HW), gh = at.group * shared + min(at.head0 + max(gw, 0), shared - 1);
   const float* dt = a.dt + sp.b * a.sdt.b + gh * a.sdt.h + sp.tok0 * a.sdt.t;
   const float A = a.A[gh], bias = a.dt_bias ? a.dt_bias[gh] : 0.f;
   const unsigned pitch = (unsigned)(a.sO.t * sizeof(T));
+  float D[HW];
+#pragma unroll
+  for (int i = 0; i < HW; ++i) D[i] = a.D ? a.D[at.group * shared + min(at.head0 + i, shared - 1)] : 0.f;
   float dt_next = 0.f;
-  if (w < HW && lane < sp.len) dt_next = dt[lane * a.sdt.t];
+  if (gw >= 0 && lane < sp.len) dt_next = dt[lane * a.sdt.t];
   auto make = [&](int t, int turn) __attribute__((always_inline)) {
-    if (w >= HW) return;
+    if (gw < 0) return;
     const LaneGates v = make_gates(dt_next, A, bias, a.softplus, min(kDC, sp.len - t));
-    put_gates<T>(v, &gates[turn][w]);
+    put_gates<T>(v, &gates[turn][gw]);
     if (t + kDC + lane < sp.len) dt_next = dt[(t + kDC + lane) * a.sdt.t];
   };
   u32x4 out[CB][4];                                        // O of the chunk before, of token row(t, m)
@@ -97,52 +100,63 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     for (int s = 0; s < CS; ++s)
 #pragma unroll
       for (int c = 0; c < CT; ++c) xf[s][c] = L.cols_row(Xh, pw * CT + c, s);
-    // C B^T of a fragment's tokens row(t, .) and those before them
-    int made = -1;
-    f32x4 d[U];
-#pragma unroll 1
-    for (int k = 0; k < PER; ++k) {
-      const int unit = w * PER + k;
-      if (unit >= UNITS) break;
-      const int f = unit / HW, hd = unit % HW;
-      int t, s;
-      tri_place<T>(f, &t, &s);
-      if (f != made) {
-        made = f;
+    // C B^T of a fragment's tokens row(t, .) and those before them; all of a wave's fragments at once
+    auto decayed = [&](auto count) __attribute__((always_inline)) {
+      constexpr int NF = decltype(count)::value;
+      int ft[NF], fs[NF], fi[NF];
+      f32x4 d[NF][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) d[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < NF; ++k) {
+        tri_place<T>(w + k * W, &ft[k], &fs[k]);
+        fi[k] = M::row(ft[k], m);
 #pragma unroll
-        for (int ns = 0; ns < NS; ++ns) {
-          if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
-          const u32x4 c = L.frag(Cp, t, ns);
+        for (int u = 0; u < U; ++u) d[k][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
-          for (int u = 0; u < U; ++u) d[u] = M::mma(L.frag(Bp, s * U + u, ns), c, d[u]);
+      for (int ns = 0; ns < NS; ++ns) {
+        if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
+#pragma unroll
+        for (int k = 0; k < NF; ++k) {
+          const u32x4 c = L.frag(Cp, ft[k], ns);
+#pragma unroll
+          for (int u = 0; u < U; ++u) d[k][u] = M::mma(L.frag(Bp, fs[k] * U + u, ns), c, d[k][u]);
         }
       }
-      const Gates& q = gates[turn][hd];
-      const float D = a.D ? a.D[at.group * shared + min(at.head0 + hd, shared - 1)] : 0.f;
-      const int i = M::row(t, m);
-      const float bh = q.hi[i], bl = U == 2 ? 0.f : q.lo[i];
-      f32x4 v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = M::row(s * U + u, 4 * g);
-        const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jr = *reinterpret_cast<const f32x4*>(q.r + j);
-        f32x4 jl;
-        if constexpr (U == 1) jl = *reinterpret_cast<const f32x4*>(q.lo + j);
+      for (int hd = 0; hd < HW; ++hd) {
+        const Gates& q = gates[turn][hd];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = U == 2 ? bh - jh[e] : (bh - jh[e]) + (bl - jl[e]);
-          v[u][e] = d[u][e] * exp2_hw(x) * jr[e];
-          if (j + e >= i) v[u][e] = j + e == i ? v[u][e] + D : 0.f;
+        for (int k = 0; k < NF; ++k) {
+          const int i = fi[k];
+          const float bh = q.hi[i], bl = U == 2 ? 0.f : q.lo[i];
+          int behind = i - M::row(fs[k] * U, 4 * g);       // tokens of the lane's row of d before i
+          asm volatile("" : "+v"(behind));                 // (compared again for every chunk, not kept in masks)
+          f32x4 v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int j = M::row(fs[k] * U + u, 4 * g);
+            const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jr = *reinterpret_cast<const f32x4*>(q.r + j);
+            f32x4 jl;
+            if constexpr (U == 1) jl = *reinterpret_cast<const f32x4*>(q.lo + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = U == 2 ? bh - jh[e] : (bh - jh[e]) + (bl - jl[e]);
+              const float z = d[k][u][e] * exp2_hw(x) * jr[e];
+              v[u][e] = 4 * u + e < behind ? z : 4 * u + e == behind ? z + D[hd] : 0.f;
+            }
+          }
+          u32x4 hi, lo;
+          split.two(v, hi, lo);
+          char* to = Mp + hd * Z::kM + (w + k * W) * 1024 + lane * 16;
+          *reinterpret_cast<u32x4*>(to) = hi;
+          if (M::kSplit) *reinterpret_cast<u32x4*>(to + M::kTri * 1024) = lo;
         }
       }
-      u32x4 hi, lo;
-      split.two(v, hi, lo);
-      char* to = Mp + hd * Z::kM + f * 1024 + lane * 16;
-      *reinterpret_cast<u32x4*>(to) = hi;
-      if (M::kSplit) *reinterpret_cast<u32x4*>(to + M::kTri * 1024) = lo;
-    }
+    };
+    if (M::kTri % W == 0 || w < M::kTri % W)
+      decayed(std::integral_constant<int, FW>());
+    else
+      decayed(std::integral_constant<int, (FW > 1 ? FW - 1 : 1)>());
     __syncthreads();                                       // it is there, x has been read
     if (mine && next < sp.len) xload.issue(x + next * a.sx.t, nlen, Xh);
     const Gates& q = gates[turn][hw];
