@@ -113,10 +113,10 @@ int check_scan(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
   const int64_t lim = (int64_t)1 << 30, seqs = scan_sequences(s, num_seqs);
   if (s->seq_len > lim || seqs > lim || (num_seqs < 0 && s->batch * s->seq_len > lim)) return TTT_ERR_UNSUPPORTED;
   const ttt::ScanArgs a = scan_sizes(s, num_seqs);
-  // every chunk of 64 tokens and head, a workgroup's grid over segments, and the states' elements by 1024
+  // every chunk of 64 tokens and head, workgroups of up to 512 over segments, and the states' elements by 1024
   const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + seqs : s->batch * ((s->seq_len + 63) / 64);
   if (chunks * s->heads > kMaxBlocks || seqs * s->heads * ((s->head_dim * s->state + 1023) / 1024) > kMaxBlocks ||
-      (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
+      2 * (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
@@ -128,7 +128,7 @@ int check_scan_backward(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
   const int64_t seqs = scan_sequences(s, num_seqs);
   const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + seqs : s->batch * ((s->seq_len + 63) / 64);
   if (2 * chunks * s->groups > kMaxBlocks || 2 * seqs * s->heads * ((s->head_dim * s->state + 1023) / 1024) > kMaxBlocks ||
-      2 * (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
+      4 * (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }

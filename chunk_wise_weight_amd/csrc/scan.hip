@@ -72,7 +72,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     const int len = min(kDC, sp.len - t0);
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
-      const int p = M::row(tile0 + c * PB, 4 * g);
+      const int p = state_row<T, CT>(tile0 + c * PB, 4 * g);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int i = M::row(t, m);
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
     for (int s = 0; s < CS; ++s)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) xf[s][c] = L.cols_row(Xh, pw * CT + c, s);
+      for (int c = 0; c < CT; ++c) xf[s][c] = state_cols<T, CT>(L, Xh, pw * CT + c, s);
     // C B^T of a fragment's tokens row(t, .) and those before them; all of a wave's fragments at once
     auto decayed = [&](auto count) __attribute__((always_inline)) {
       constexpr int NF = decltype(count)::value;
@@ -155,8 +155,8 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     };
     if (M::kTri % W == 0 || w < M::kTri % W)
       decayed(std::integral_constant<int, FW>());
-    else
-      decayed(std::integral_constant<int, (FW > 1 ? FW - 1 : 1)>());
+    else if constexpr (FW > 1)
+      decayed(std::integral_constant<int, FW - 1>());
     __syncthreads();                                       // it is there, x has been read
     if (mine && next < sp.len) xload.issue(x + next * a.sx.t, nlen, Xh);
     const Gates& q = gates[turn][hw];

@@ -96,11 +96,17 @@ template <typename T, int DK, int NW> struct TileLoader {
 #if __HIP_DEVICE_COMPILE__
     const __amdgpu_buffer_rsrc_t rs = rows_rsrc(rows);
     const int L = lane_id(), w = wave_id() % NW;
+    if (len >= 64) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int i = j * NW + w;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
-                                               len >= 64 || (i % 8) * 8 + (L >> 3) < len ? off[j] : kOOB, 0, 0, 0);
+      for (int j = 0; j < N; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + (j * NW + w) * 1024), 16, off[j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int i = j * NW + w;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(t + i * 1024), 16,
+                                                 (i % 8) * 8 + (L >> 3) < len ? off[j] : kOOB, 0, 0, 0);
+      }
     }
 #endif
   }
@@ -300,10 +306,14 @@ template <typename T> struct Scaled {
   }
 };
 
-// The heads' waves of a workgroup: HW heads of a group, PW waves with 16 CT rows of the state each.
-template <typename T, int DN_, int HW_, int PW_> struct ScanShape {
+// Blocks of P that a wave has: two read B and C from LDS half as often, where the registers hold two (fp32 has its
+// operands in three parts at once).
+template <typename T, int DN> constexpr int kBlocks = sizeof(T) == 2 && DN <= 128 ? 2 : 1;
+
+// The heads' waves of a workgroup: HW heads of a group, PW waves with CT blocks of 16 rows of the state each.
+template <typename T, int DN_, int HW_, int PW_, int CT_ = kBlocks<T, DN_>> struct ScanShape {
   static constexpr int DN = DN_, HW = HW_, PW = PW_, W = HW * PW;
-  static constexpr int CT = DN <= 128 ? 2 : 1;              // blocks of P a wave has
+  static constexpr int CT = CT_;
   static constexpr int NT = DN / 16, NS = DN / Mat<T>::KB, CS = kDC / Mat<T>::KB;
   static constexpr int cols = 16 * CT * PW;                 // of P, of a workgroup's heads
   static constexpr int kLine = 128 / (int)sizeof(T), DX = cols < kLine ? kLine : cols;
@@ -311,7 +321,17 @@ template <typename T, int DN_, int HW_, int PW_> struct ScanShape {
   static constexpr int kM = Mat<T>::kTri * 1024 * (Mat<T>::kSplit ? 2 : 1);
 };
 
-// State rows of a wave: element p = row(ct, lane & 15) of its rows, n = 16 nt + 4 g + 0..3.
+// The row of P that index i of block `tile` stands for: two blocks of bf16 a wave are dealt such that 8 of a result's rows
+// follow one another.
+template <typename T, int CT> __device__ __forceinline__ int state_row(int tile, int i) {
+  return CT == 2 ? Mat<T>::row(tile, i) : tile * 16 + i;
+}
+// The operand of their columns, rows of step s.
+template <typename T, int CT> __device__ __forceinline__ u32x4 state_cols(const LaneAt<T>& L, const char* x, int tile, int s) {
+  return CT == 2 ? L.cols_row(x, tile, s) : L.cols(x, tile, s);
+}
+
+// State rows of a wave: element p = state_row(tile, lane & 15), n = 16 nt + 4 g + 0..3.
 template <typename T, int CT, int NT> struct StateRows {
   f32x4 s[CT][NT];
   __device__ __forceinline__ void zero() {
@@ -325,7 +345,7 @@ template <typename T, int CT, int NT> struct StateRows {
     const int m = lane_id() & 15, g = lane_id() >> 4;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      const int p = Mat<T>::row(tile0 + c, m);
+      const int p = state_row<T, CT>(tile0 + c, m);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int n = t * 16 + 4 * g;
@@ -337,7 +357,7 @@ template <typename T, int CT, int NT> struct StateRows {
     const int m = lane_id() & 15, g = lane_id() >> 4;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      const int p = Mat<T>::row(tile0 + c, m);
+      const int p = state_row<T, CT>(tile0 + c, m);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int n = t * 16 + 4 * g;

@@ -40,8 +40,8 @@ __device__ __forceinline__ int chunk_slot0(const DeltaSeqs& q, int s) {
 __device__ __forceinline__ int seq_first(const DeltaSeqs& q, int s) { return q.starts ? seq_start(q, s) : 0; }
 
 // What a workgroup of a walk over states has in hand.
-template <typename T, int DN, int HW, int PW> struct StateWalker {
-  using Z = ScanShape<T, DN, HW, PW>;
+template <typename T, int DN, int HW, int PW, int CT_> struct StateWalker {
+  using Z = ScanShape<T, DN, HW, PW, CT_>;
   using M = Mat<T>;
   static constexpr int CT = Z::CT, NT = Z::NT, CS = Z::CS, W = Z::W;
   static constexpr int kStage = Z::kB + HW * Z::kX;
@@ -93,7 +93,7 @@ template <typename T, int DN, int HW, int PW> struct StateWalker {
     for (int st = 0; st < CS; ++st) {
       u32x4 xf[CT];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) xf[c] = L.cols_row(x, pw * CT + c, st);
+      for (int c = 0; c < CT; ++c) xf[c] = state_cols<T, CT>(L, x, pw * CT + c, st);
       S.add(L, split, xf, s, st, weights + (lane >> 4) * (M::KB / 4) + st * M::KB, a.N);
     }
   }
@@ -102,9 +102,9 @@ template <typename T, int DN, int HW, int PW> struct StateWalker {
 // The state of a segment from zero, for the join.  The chunks go by from the segment's far end (forward walks: the last
 // one first), their weights decayed by what lies between, so that the state itself need not be, and none is read whose
 // weights are zero in fp32.
-template <typename T, int DN, int HW, int PW>
+template <typename T, int DN, int HW, int PW, int CT>
 __device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& k, int seg, int slots, int bid, char* smem) {
-  using K = StateWalker<T, DN, HW, PW>;
+  using K = StateWalker<T, DN, HW, PW, CT>;
   __shared__ float weights[2][HW][kDC];
   __shared__ int live[2][HW];
   ScanPlace at;
@@ -156,9 +156,9 @@ __device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& 
 }
 
 // The states before (back: after) every chunk, kept for the gradients.
-template <typename T, int DN, int HW, int PW>
+template <typename T, int DN, int HW, int PW, int CT>
 __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk& k, int seg, int slots, int bid, char* smem) {
-  using K = StateWalker<T, DN, HW, PW>;
+  using K = StateWalker<T, DN, HW, PW, CT>;
   __shared__ Gates gates[2][HW];
   ScanPlace at;
   if (!scan_place(bid, slots, a.G, a.H / a.G, (a.P + K::Z::cols - 1) / K::Z::cols, HW, &at)) return;
@@ -227,8 +227,8 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
 }
 
 // Walks of one or two directions: the first `half` workgroups take `one`, the others `two`.
-template <typename T, int DN, int HW, int PW, bool KEEP>
-__global__ __launch_bounds__(64 * HW * PW, 2) void k_scan_states(ScanArgs a, StateWalk one, StateWalk two, int seg, int slots,
+template <typename T, int DN, int HW, int PW, int CT, bool KEEP>
+__global__ __launch_bounds__(64 * HW * PW, KEEP ? 2 : 4) void k_scan_states(ScanArgs a, StateWalk one, StateWalk two, int seg, int slots,
                                                                  int half) {
 #if __HIP_DEVICE_COMPILE__
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -236,21 +236,23 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan_states(ScanArgs a, Sta
   const StateWalk& k = second ? two : one;
   const int bid = second ? blockIdx.x - half : blockIdx.x;
   if constexpr (KEEP)
-    keep_segment<T, DN, HW, PW>(a, k, seg, slots, bid, smem);
+    keep_segment<T, DN, HW, PW, CT>(a, k, seg, slots, bid, smem);
   else
-    sum_segment<T, DN, HW, PW>(a, k, seg, slots, bid, smem);
+    sum_segment<T, DN, HW, PW, CT>(a, k, seg, slots, bid, smem);
 #endif
 }
 
-template <typename T, int DN, int HW, int PW, bool KEEP>
+// PW: the outputs' walk's, whose waves have kBlocks each.
+template <typename T, int DN, int HW, int PW_, bool KEEP>
 hipError_t launch_states(const ScanArgs& a, const StateWalk& one, const StateWalk* two, int seg, int64_t slots, hipStream_t s) {
-  using Z = ScanShape<T, DN, HW, PW>;
-  using K = StateWalker<T, DN, HW, PW>;
+  constexpr int CT = KEEP ? kBlocks<T, DN> : 1, PW = PW_ * kBlocks<T, DN> / CT;
+  using Z = ScanShape<T, DN, HW, PW, CT>;
+  using K = StateWalker<T, DN, HW, PW, CT>;
   constexpr int smem = K::kStages * K::kStage;
   static_assert(smem + 2 * (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
   const int64_t shared = a.H / a.G;
   const int64_t half = walk_blocks(slots * a.G, (shared + HW - 1) / HW * ((a.P + Z::cols - 1) / Z::cols));
-  k_scan_states<T, DN, HW, PW, KEEP><<<dim3((unsigned)(two ? 2 * half : half)), 64 * HW * PW, smem, s>>>(
+  k_scan_states<T, DN, HW, PW, CT, KEEP><<<dim3((unsigned)(two ? 2 * half : half)), 64 * HW * PW, smem, s>>>(
       a, one, two ? *two : one, seg, (int)slots, (int)half);
   return hipGetLastError();
 }
@@ -294,8 +296,11 @@ hipError_t with_scan(int P, int N, int shared, F f) {
     using I2 = integral_constant<int, 2>;
     using I4 = integral_constant<int, 4>;
     if constexpr (decltype(dn)::value <= 128) {
-      if (P <= 32 && shared > 2) return f(dn, I4(), I1());
-      if (P <= 64) return shared > 1 ? f(dn, I2(), I2()) : f(dn, I1(), I2());
+      constexpr int kWide = 4 / kBlocks<T, decltype(dn)::value>;     // waves of 64 columns
+      using W = integral_constant<int, kWide>;
+      if (P <= 32 && shared > 2) return f(dn, I4(), integral_constant<int, kWide / 2>());
+      if (P <= 64) return shared > 1 ? f(dn, I2(), W()) : f(dn, I1(), W());
+      return f(dn, I1(), integral_constant<int, 2 * kWide>());
     }
     return f(dn, I1(), I4());
   };
