@@ -16,7 +16,7 @@ namespace {
 constexpr int kConvThreads = 256;
 
 // Which channels and which run (or sequence) a thread has: cv threads in a row along the channels, the rest along the
-// runs; cv is the next power of two of the vectors in a row, at most a workgroup's threads.
+// runs.
 struct ConvPlace {
   int64_t run;
   int c;                          // first channel
@@ -58,9 +58,8 @@ __device__ __forceinline__ void load_taps(const T* w, const T* bias, int c, int 
 }
 
 // Row r of a sequence whose first token lies at `first` (its channels c..), r < 0: of its earlier rows.
-template <typename T, int K, bool RAG>
-__device__ __forceinline__ Pack<T, Vec<T>::V> conv_row(const T* first, int64_t pitch, const T* init, int d, int c, int r) {
-  constexpr int VEC = Vec<T>::V;
+template <typename T, int K, bool RAG, int VEC = Vec<T>::V>
+__device__ __forceinline__ Pack<T, VEC> conv_row(const T* first, int64_t pitch, const T* init, int d, int c, int r) {
   if (r >= 0) return load_pack<T, VEC, RAG>(first + r * pitch, d - c);
   if (init) return load_pack<T, VEC, RAG>(init + (int64_t)(r + K - 1) * d + c, d - c);
   Pack<T, VEC> z;
@@ -172,10 +171,13 @@ __device__ __forceinline__ float conv_dz(float z, float g, bool silu) {
   return g * (p + z * p * (1.f - p));
 }
 
+// Channels of a thread: 8 of bf16 would take more than half of the registers, for one wave a SIMD.
+constexpr int kGradVec = 4;
+
 // A run's part of the taps' and the bias's gradient goes to part[run][K + 1][d].
 template <typename T, bool RAG, int K>
 __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, ConvPlan p) {
-  constexpr int VEC = Vec<T>::V;
+  constexpr int VEC = kGradVec;
   using V = Pack<T, VEC>;
   const ConvArgs& a = g.f;
   const int d = a.d;
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           float r[VEC];
-          widen(conv_row<T, K, RAG>(first, a.sx.t, init, d, at.c, t - (K - 1) + k), r);
+          widen(conv_row<T, K, RAG, VEC>(first, a.sx.t, init, d, at.c, t - (K - 1) + k), r);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) z[j] += tap[k][j] * r[j];
         }
@@ -257,7 +259,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
     float win[K][VEC], pend[K][VEC];              // row r, and dx of it so far, in place (r - (from - begin)) mod K
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      widen(conv_row<T, K, RAG>(first, a.sx.t, init, d, at.c, from - begin - (K - 1) + j), win[j + 1]);
+      widen(conv_row<T, K, RAG, VEC>(first, a.sx.t, init, d, at.c, from - begin - (K - 1) + j), win[j + 1]);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -424,13 +426,14 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_step(ConvStepArgs p) {
 }
 
 // Runs of `run` tokens a batch row, and the grid over them and the channels.
-template <typename T>
-ConvPlan conv_plan(const ConvArgs& a, int most) {
-  constexpr int VEC = Vec<T>::V;
+ConvPlan conv_plan(const ConvArgs& a, int VEC, int most) {
   ConvPlan p;
   const int units = (a.d + VEC - 1) / VEC;
+  // cv: the next power of two of a row's vectors; long rows: of 64, 128 and 256 the one that leaves fewest threads idle
   p.cv = 1;
-  while (p.cv < units && p.cv < kConvThreads) p.cv *= 2;
+  while (p.cv < units && p.cv < 64) p.cv *= 2;
+  for (int cv = 128; cv <= kConvThreads; cv *= 2)
+    if (units >= 64 && (units + cv - 1) / cv * cv <= (units + p.cv - 1) / p.cv * p.cv) p.cv = cv;
   p.blocks_c = (units + p.cv - 1) / p.cv;
   // Long runs read fewer rows twice; they are shortened until the chip has some 4 waves a SIMD.
   p.run = most;
@@ -470,7 +473,7 @@ hipError_t with_variant(bool rag, int K, F f) {
 
 template <typename T>
 hipError_t launch_conv(const ConvArgs& a, hipStream_t s) {
-  const ConvPlan p = conv_plan<T>(a, kForwardRun);
+  const ConvPlan p = conv_plan(a, Vec<T>::V, kForwardRun);
   const int64_t grid = p.blocks + (a.K > 1 ? p.seq_blocks : 0);
   if (grid == 0) return hipSuccess;
   return with_variant(a.rag, a.K, [&](auto rag, auto k) {
@@ -481,18 +484,18 @@ hipError_t launch_conv(const ConvArgs& a, hipStream_t s) {
 
 template <typename T>
 int64_t conv_blocks(const ConvArgs& a, bool grad) {
-  const ConvPlan p = conv_plan<T>(a, grad ? kGradRun : kForwardRun);
+  const ConvPlan p = grad ? conv_plan(a, kGradVec, kGradRun) : conv_plan(a, Vec<T>::V, kForwardRun);
   return p.blocks + p.seq_blocks;
 }
 
 template <typename T>
 int64_t conv_grad_runs(const ConvArgs& a) {
-  return (int64_t)a.batch * conv_plan<T>(a, kGradRun).runs;
+  return (int64_t)a.batch * conv_plan(a, kGradVec, kGradRun).runs;
 }
 
 template <typename T>
 hipError_t launch_conv_grad(const ConvGradArgs& a, hipStream_t s) {
-  const ConvPlan p = conv_plan<T>(a.f, kGradRun);
+  const ConvPlan p = conv_plan(a.f, kGradVec, kGradRun);
   const int64_t grid = p.blocks + (a.dx_init && a.f.K > 1 ? p.seq_blocks : 0);
   if (grid > 0) {
     hipError_t e = with_variant(a.f.rag, a.f.K, [&](auto rag, auto k) {

@@ -1,4 +1,4 @@
-// What the norms' kernels share (gfx950): rows of elements in 16-byte vectors,
+// What the norms' kernels share (gfx950): rows of elements in vectors,
 // sums over the threads of a row, the variant for a row's width, and the
 // columns' sums of their backward passes.  How the threads hold a row is in
 // norm.hip.
@@ -15,9 +15,17 @@ constexpr int kNormThreads = 256;
 // VEC consecutive elements as they are stored (bf16 stays packed until used).
 template <typename T, int VEC> struct Pack;
 template <> struct Pack<bf16, 8> { u32x4 w; };
+template <> struct Pack<bf16, 4> { u32x2 w; };
 template <> struct Pack<float, 4> { f32x4 w; };
 
 __device__ __forceinline__ void widen(const Pack<bf16, 8>& p, float* o) { unpack8(p.w, o); }
+__device__ __forceinline__ void widen(const Pack<bf16, 4>& p, float* o) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    o[2 * i] = __uint_as_float(p.w[i] << 16);
+    o[2 * i + 1] = __uint_as_float(p.w[i] & 0xffff0000u);
+  }
+}
 __device__ __forceinline__ void widen(const Pack<float, 4>& p, float* o) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = p.w[i];
@@ -26,6 +34,9 @@ __device__ __forceinline__ void widen(const Pack<float, 4>& p, float* o) {
 __device__ __forceinline__ void narrow(const float* o, Pack<bf16, 8>& p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) p.w[i] = pack2_bf16(o[2 * i], o[2 * i + 1]);
+}
+__device__ __forceinline__ void narrow(const float* o, Pack<bf16, 4>& p) {
+  p.w = (u32x2){pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
 }
 __device__ __forceinline__ void narrow(const float* o, Pack<float, 4>& p) { p.w = (f32x4){o[0], o[1], o[2], o[3]}; }
 
