@@ -198,8 +198,8 @@ int ttt_short_conv_backward_workspace_bytes(const ttt_conv_shape* shape, int dty
   if (int st = check_conv(shape, dtype, num_seqs)) return st;
   const ttt::ConvArgs a = conv_sizes(shape, num_seqs);
   if (conv_launch_blocks(a, dtype, true) > kMaxBlocks) return TTT_ERR_UNSUPPORTED;
-  const int64_t runs = dtype == TTT_BF16 ? ttt::conv_grad_runs<bf16>(a) : ttt::conv_grad_runs<float>(a);
-  *bytes = (size_t)runs * (shape->taps + 1) * shape->dim * sizeof(float);
+  const int64_t parts = dtype == TTT_BF16 ? ttt::conv_grad_parts<bf16>(a) : ttt::conv_grad_parts<float>(a);
+  *bytes = (size_t)parts * (shape->taps + 1) * shape->dim * sizeof(float);
   return TTT_OK;
 }
 

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kConvThreads = 256;
 
-// Which channels and which run (or sequence) a thread has: cv threads in a row along the channels, the rest along the
-// runs.
+// Which channels and which run (or sequence) a thread has: cv threads in a row along the channels, a wave at most,
+// the rest along the runs.
 struct ConvPlace {
   int64_t run;
   int c;                          // first channel
@@ -174,7 +174,7 @@ __device__ __forceinline__ float conv_dz(float z, float g, bool silu) {
 // Channels of a thread: 8 of bf16 would take more than half of the registers, for one wave a SIMD.
 constexpr int kGradVec = 4;
 
-// A run's part of the taps' and the bias's gradient goes to part[run][K + 1][d].
+// The taps' and the bias's gradient of a workgroup's runs goes to part[][K + 1][d].
 template <typename T, bool RAG, int K>
 __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, ConvPlan p) {
   constexpr int VEC = kGradVec;
@@ -239,8 +239,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
   }
   const ConvPlace at = conv_place(p.cv, p.blocks_c, VEC, d, blockIdx.x);
   const int64_t row = at.run / p.runs;
-  if (!at.in || row >= a.batch) return;
-  load_taps<T, RAG, K, VEC>((const T*)a.w, (const T*)a.bias, at.c, d, tap, bias);
+  const bool live = at.in && row < a.batch;
+  if (live) load_taps<T, RAG, K, VEC>((const T*)a.w, (const T*)a.bias, at.c, d, tap, bias);
   const int b = (int)row, t0 = (int)(at.run - row * p.runs) * p.run;
   float dw[K][VEC], db[VEC];
 #pragma unroll
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
     for (int k = 0; k < K; ++k) dw[k][j] = 0.f;
   }
   T* dx = (T*)g.dx + b * g.sdx.b + at.c;
-  conv_parts(a.seqs, b, t0, min(t0 + p.run, a.seqs.n), [&](int seq, int begin, int end, int from, int to)
+  if (live) conv_parts(a.seqs, b, t0, min(t0 + p.run, a.seqs.n), [&](int seq, int begin, int end, int from, int to)
                                                            __attribute__((always_inline)) {
     const T* first = x + b * a.sx.b + begin * a.sx.t + at.c;
     const T* dfirst = dY + b * g.sdy.b + begin * g.sdy.t + at.c;
@@ -331,20 +331,35 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
       }
     }
   });
-  float* part = g.part + at.run * (K + 1) * (int64_t)d + at.c;
+  __shared__ float red[kConvThreads / 64][K + 1][64][VEC];
+  const int lane = lane_id(), w = wave_id(), cv = p.cv;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    if (at.c + j < d) {
+  for (int k = 0; k <= K; ++k) {
+    float v[VEC];
 #pragma unroll
-      for (int k = 0; k < K; ++k) part[(int64_t)k * d + j] = dw[k][j];
-      part[(int64_t)K * d + j] = db[j];
-    }
+    for (int j = 0; j < VEC; ++j) v[j] = k < K ? dw[k][j] : db[j];
+    for (int r = cv; r < 64; r *= 2)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] += __shfl_xor(v[j], r, 64);
+    if (lane < cv)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) red[w][k][lane][j] = v[j];
+  }
+  __syncthreads();
+  const int c0 = (int)(blockIdx.x % p.blocks_c) * cv * VEC;
+  float* part = g.part + (int64_t)(blockIdx.x / p.blocks_c) * (K + 1) * d;
+  for (int i = threadIdx.x; i < (K + 1) * cv * VEC; i += kConvThreads) {
+    const int k = i / (cv * VEC), c = i % (cv * VEC);
+    float v = 0.f;
+#pragma unroll
+    for (int r = 0; r < kConvThreads / 64; ++r) v += red[r][k][c / VEC][c % VEC];
+    if (c0 + c < d) part[(int64_t)k * d + c0 + c] = v;
   }
 }
 
-// dw[c][k] and dbias[c]: the runs' parts in a fixed order, 16 channels of a tap a workgroup, each of its 64 rows of
-// threads every 64th run, joined in LDS.
-__global__ __launch_bounds__(1024) void k_conv_sum(const float* __restrict__ part, int64_t runs, int d, int K,
+// dw[c][k] and dbias[c]: the parts in a fixed order, 16 channels of a tap a workgroup, each of its 64 rows of threads
+// every 64th part, joined in LDS.
+__global__ __launch_bounds__(1024) void k_conv_sum(const float* __restrict__ part, int64_t parts, int d, int K,
                                                    float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float sum[64][17];
   const int j = threadIdx.x & 15, r = threadIdx.x >> 4, c = blockIdx.x * 16 + j, k = blockIdx.y;
@@ -352,7 +367,7 @@ __global__ __launch_bounds__(1024) void k_conv_sum(const float* __restrict__ par
   float s = 0.f;
   if (c < d) {
 #pragma unroll 4
-    for (int64_t g = r; g < runs; g += 64) s += part[(g * (K + 1) + k) * d + c];
+    for (int64_t g = r; g < parts; g += 64) s += part[(g * (K + 1) + k) * d + c];
   }
   sum[r][j] = s;
   __syncthreads();
@@ -429,13 +444,10 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_step(ConvStepArgs p) {
 ConvPlan conv_plan(const ConvArgs& a, int VEC, int most) {
   ConvPlan p;
   const int units = (a.d + VEC - 1) / VEC;
-  // cv: the next power of two of a row's vectors; long rows: of 64, 128 and 256 the one that leaves fewest threads idle
   p.cv = 1;
   while (p.cv < units && p.cv < 64) p.cv *= 2;
-  for (int cv = 128; cv <= kConvThreads; cv *= 2)
-    if (units >= 64 && (units + cv - 1) / cv * cv <= (units + p.cv - 1) / p.cv * p.cv) p.cv = cv;
   p.blocks_c = (units + p.cv - 1) / p.cv;
-  // Long runs read fewer rows twice; they are shortened until the chip has some 4 waves a SIMD.
+  // Runs are shortened until the chip has some 4 waves a SIMD.
   p.run = most;
   while (p.run > 8 && (int64_t)a.batch * ((a.seqs.n + p.run - 1) / p.run) * p.blocks_c * p.cv < 256 * 16 * 64) p.run /= 2;
   p.runs = (a.seqs.n + p.run - 1) / p.run;
@@ -446,7 +458,10 @@ ConvPlan conv_plan(const ConvArgs& a, int VEC, int most) {
   return p;
 }
 
-constexpr int kForwardRun = 32, kGradRun = 64;
+// Tokens of a run, at most.  Forward: short ones, so that a wave's rows lie in few pages (65,536 x 6144, K = 4: runs of 8
+// 291 us, 12 287 us, 16 294 us, 32 313 us); backward: each costs a sum of dw (16,458 x 2304: 64 59 us, 24 65 us).
+int forward_run(int K) { return std::max(8, 3 * K); }
+constexpr int kGradRun = 64;
 
 template <typename F>
 hipError_t with_taps(int K, F f) {
@@ -473,7 +488,7 @@ hipError_t with_variant(bool rag, int K, F f) {
 
 template <typename T>
 hipError_t launch_conv(const ConvArgs& a, hipStream_t s) {
-  const ConvPlan p = conv_plan(a, Vec<T>::V, kForwardRun);
+  const ConvPlan p = conv_plan(a, Vec<T>::V, forward_run(a.K));
   const int64_t grid = p.blocks + (a.K > 1 ? p.seq_blocks : 0);
   if (grid == 0) return hipSuccess;
   return with_variant(a.rag, a.K, [&](auto rag, auto k) {
@@ -484,13 +499,14 @@ hipError_t launch_conv(const ConvArgs& a, hipStream_t s) {
 
 template <typename T>
 int64_t conv_blocks(const ConvArgs& a, bool grad) {
-  const ConvPlan p = grad ? conv_plan(a, kGradVec, kGradRun) : conv_plan(a, Vec<T>::V, kForwardRun);
+  const ConvPlan p = grad ? conv_plan(a, kGradVec, kGradRun) : conv_plan(a, Vec<T>::V, forward_run(a.K));
   return p.blocks + p.seq_blocks;
 }
 
 template <typename T>
-int64_t conv_grad_runs(const ConvArgs& a) {
-  return (int64_t)a.batch * conv_plan(a, kGradVec, kGradRun).runs;
+int64_t conv_grad_parts(const ConvArgs& a) {
+  const ConvPlan p = conv_plan(a, kGradVec, kGradRun);
+  return p.blocks / p.blocks_c;
 }
 
 template <typename T>
@@ -504,7 +520,7 @@ hipError_t launch_conv_grad(const ConvGradArgs& a, hipStream_t s) {
     });
     if (e != hipSuccess) return e;
   }
-  k_conv_sum<<<dim3((unsigned)((a.f.d + 15) / 16), a.f.K + 1), 1024, 0, s>>>(a.part, (int64_t)a.f.batch * p.runs, a.f.d,
+  k_conv_sum<<<dim3((unsigned)((a.f.d + 15) / 16), a.f.K + 1), 1024, 0, s>>>(a.part, p.blocks / p.blocks_c, a.f.d,
                                                                              a.f.K, a.dw, a.dbias);
   return hipGetLastError();
 }
@@ -522,7 +538,7 @@ hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t s) {
 #define TTT_CONV(T)                                                      \
   template hipError_t launch_conv<T>(const ConvArgs&, hipStream_t);      \
   template int64_t conv_blocks<T>(const ConvArgs&, bool);                \
-  template int64_t conv_grad_runs<T>(const ConvArgs&);                   \
+  template int64_t conv_grad_parts<T>(const ConvArgs&);                   \
   template hipError_t launch_conv_grad<T>(const ConvGradArgs&, hipStream_t); \
   template hipError_t launch_conv_step<T>(const ConvStepArgs&, hipStream_t);
 TTT_CONV(bf16)

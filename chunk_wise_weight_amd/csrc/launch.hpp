@@ -309,7 +309,7 @@ struct ConvGradArgs {
   const void *dY, *dx_final;           // dx_final or null: zero
   DeltaStrides sdy, sdx;
   void *dx, *dx_init;                  // dx_init or null: not wanted
-  float *dw, *dbias, *part;            // dbias or null; part [runs, K + 1, d]
+  float *dw, *dbias, *part;            // dbias or null; part [parts, K + 1, d]
 };
 // How a launch deals tokens and channels to threads (conv.hip).
 struct ConvPlan {
@@ -330,7 +330,7 @@ hipError_t launch_conv(const ConvArgs& a, hipStream_t s);
 template <typename T>
 int64_t conv_blocks(const ConvArgs& a, bool grad);   // workgroups of a launch
 template <typename T>
-int64_t conv_grad_runs(const ConvArgs& a);
+int64_t conv_grad_parts(const ConvArgs& a);      // of the sums of dw and dbias
 template <typename T>
 hipError_t launch_conv_grad(const ConvGradArgs& a, hipStream_t s);
 template <typename T>
