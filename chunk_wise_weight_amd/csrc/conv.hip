@@ -94,7 +94,7 @@ __device__ __forceinline__ void conv_parts(const DeltaSeqs& q, int b, int t0, in
   }
 }
 
-template <typename T, bool RAG, int K>
+template <typename T, bool RAG, int K, bool STREAM>
 __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, ConvPlan p) {
   constexpr int VEC = Vec<T>::V;
   using V = Pack<T, VEC>;
@@ -135,14 +135,14 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, ConvPlan p) {
     for (int j = 0; j < K - 1; ++j) widen(conv_row<T, K, RAG>(first, a.sx.t, init, d, at.c, from - begin - (K - 1) + j), win[j + 1]);
 #pragma unroll
     for (int u = 0; u < K; ++u)
-      if (from + u < to) next[u] = load_pack<T, VEC, RAG>(first + (from + u - begin) * a.sx.t, d - at.c);
+      if (from + u < to) next[u] = load_pack<T, VEC, RAG, STREAM>(first + (from + u - begin) * a.sx.t, d - at.c);
     for (int t = from; t < to; t += K) {
       V now[K];
 #pragma unroll
       for (int u = 0; u < K; ++u) now[u] = next[u];
 #pragma unroll
       for (int u = 0; u < K; ++u)
-        if (t + K + u < to) next[u] = load_pack<T, VEC, RAG>(first + (t + K + u - begin) * a.sx.t, d - at.c);
+        if (t + K + u < to) next[u] = load_pack<T, VEC, RAG, STREAM>(first + (t + K + u - begin) * a.sx.t, d - at.c);
 #pragma unroll
       for (int u = 0; u < K; ++u) {
         if (t + u < to) {
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, ConvPlan p) {
           }
           V out;
           narrow(o, out);
-          store_pack<T, VEC, RAG>(y + (t + u) * a.sy.t, out, d - at.c);
+          store_pack<T, VEC, RAG, STREAM>(y + (t + u) * a.sy.t, out, d - at.c);
         }
       }
     }
@@ -491,8 +491,14 @@ hipError_t launch_conv(const ConvArgs& a, hipStream_t s) {
   const ConvPlan p = conv_plan(a, Vec<T>::V, forward_run(a.K));
   const int64_t grid = p.blocks + (a.K > 1 ? p.seq_blocks : 0);
   if (grid == 0) return hipSuccess;
+  const bool stream = (int64_t)a.batch * a.seqs.n * a.d * 2 * (int)sizeof(T) > kStreamBytes;
   return with_variant(a.rag, a.K, [&](auto rag, auto k) {
-    k_conv<T, decltype(rag)::value, decltype(k)::value><<<dim3((unsigned)grid), kConvThreads, 0, s>>>(a, p);
+    constexpr bool RAG = decltype(rag)::value;
+    constexpr int K = decltype(k)::value;
+    if (!RAG && stream)
+      k_conv<T, RAG, K, !RAG><<<dim3((unsigned)grid), kConvThreads, 0, s>>>(a, p);
+    else
+      k_conv<T, RAG, K, false><<<dim3((unsigned)grid), kConvThreads, 0, s>>>(a, p);
     return hipGetLastError();
   });
 }

@@ -40,9 +40,14 @@ __device__ __forceinline__ void narrow(const float* o, Pack<bf16, 4>& p) {
 }
 __device__ __forceinline__ void narrow(const float* o, Pack<float, 4>& p) { p.w = (f32x4){o[0], o[1], o[2], o[3]}; }
 
-// `left` elements remain from p to the row's end (RAG; else they are VEC or more); those past it are zero.
-template <typename T, int VEC, bool RAG>
+// `left` elements remain from p to the row's end (RAG; else they are VEC or more); those past it are zero.  STREAM:
+// what passes by is not kept in the caches.
+template <typename T, int VEC, bool RAG, bool STREAM = false>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T* p, int left) {
+  if constexpr (STREAM && !RAG) {
+    const auto* at = reinterpret_cast<const Pack<T, VEC>*>(p);
+    return {__builtin_nontemporal_load(&at->w)};
+  }
   if constexpr (!RAG) return *reinterpret_cast<const Pack<T, VEC>*>(p);
   Pack<T, VEC> o;
   if (left >= VEC) {
@@ -55,9 +60,11 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const T* p, int left) {
   }
   return o;
 }
-template <typename T, int VEC, bool RAG>
+template <typename T, int VEC, bool RAG, bool STREAM = false>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& v, int left) {
-  if constexpr (!RAG) {
+  if constexpr (STREAM && !RAG) {
+    __builtin_nontemporal_store(v.w, &reinterpret_cast<Pack<T, VEC>*>(p)->w);
+  } else if constexpr (!RAG) {
     *reinterpret_cast<Pack<T, VEC>*>(p) = v;
   } else if (left >= VEC) {
     __builtin_memcpy(p, &v, sizeof(v));

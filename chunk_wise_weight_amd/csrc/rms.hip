@@ -40,16 +40,19 @@ __device__ __forceinline__ unsigned pack4_e4m3(float a, float b, float c, float 
 }
 
 // VEC e4m3 values of a row: RAG rows start at any byte and end inside a vector.
-template <int VEC, bool RAG>
+template <int VEC, bool RAG, bool STREAM>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, int left) {
   unsigned w[VEC / 4];
 #pragma unroll
   for (int j = 0; j < VEC / 4; ++j) w[j] = pack4_e4m3(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   if constexpr (!RAG) {
-    if constexpr (VEC == 8)
-      *reinterpret_cast<u32x2*>(p) = (u32x2){w[0], w[1]};
+    using W = std::conditional_t<VEC == 8, u32x2, unsigned>;
+    W all;
+    __builtin_memcpy(&all, w, VEC);
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(all, reinterpret_cast<W*>(p));
     else
-      *reinterpret_cast<unsigned*>(p) = w[0];
+      *reinterpret_cast<W*>(p) = all;
   } else if (left >= VEC) {
     __builtin_memcpy(p, w, VEC);
   } else {
@@ -60,7 +63,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, int left)
 }
 
 // lanes: those that hold a group of columns (a power of two), 0: the scale is the row's.
-template <typename T, bool RAG, int TPR, int NV, bool OUT8>
+template <typename T, bool RAG, int TPR, int NV, bool OUT8, bool STREAM>
 __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
     const T* __restrict__ x, const T* __restrict__ res, const T* __restrict__ weight, T* __restrict__ ho,
     void* __restrict__ yo, float* __restrict__ rstd, float* __restrict__ scale, int64_t rows, int d, float eps, int lanes) {
@@ -76,8 +79,8 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + t) * VEC;
       if (e < d) {
-        raw[i] = load_pack<T, VEC, RAG>(x + row * d + e, d - e);
-        if (res) more[i] = load_pack<T, VEC, RAG>(res + row * d + e, d - e);
+        raw[i] = load_pack<T, VEC, RAG, STREAM>(x + row * d + e, d - e);
+        if (res) more[i] = load_pack<T, VEC, RAG, STREAM>(res + row * d + e, d - e);
       }
     }
     float v[NV][VEC], s[1] = {0.f};
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
           for (int j = 0; j < VEC; ++j) v[i][j] += o[j];
           Pack<T, VEC> h;
           narrow(v[i], h);
-          store_pack<T, VEC, RAG>(ho + row * d + e, h, d - e);
+          store_pack<T, VEC, RAG, STREAM>(ho + row * d + e, h, d - e);
           widen(h, v[i]);
         }
 #pragma unroll
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
         } else {
           Pack<T, VEC> o;
           narrow(v[i], o);
-          store_pack<T, VEC, RAG>((T*)yo + row * d + e, o, d - e);
+          store_pack<T, VEC, RAG, STREAM>((T*)yo + row * d + e, o, d - e);
         }
       }
     }
@@ -146,7 +149,7 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
           if (lanes ? t % lanes == 0 : i == 0 && t == 0) scale[row * groups + (lanes ? e / cols : 0)] = sc;
 #pragma unroll
           for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
-          store_e4m3<VEC, RAG>((uint8_t*)yo + row * d + e, v[i], d - e);
+          store_e4m3<VEC, RAG, STREAM>((uint8_t*)yo + row * d + e, v[i], d - e);
         }
       }
     }
@@ -274,13 +277,18 @@ hipError_t launch_rms(const RmsArgs& a, hipStream_t s) {
   // lanes of a group: never more than have a row
   const int lanes = a.group ? std::min(a.group / Vec<T>::V, p.tpr ? p.tpr : 64) : 0;
   return with_plan<T>(p, [&](auto rag, auto tpr, auto nv) {
-    auto go = [&](auto out8) {
-      k_rms<T, decltype(rag)::value, decltype(tpr)::value, decltype(nv)::value, decltype(out8)::value>
-          <<<dim3((unsigned)grid), p.threads, 0, s>>>((const T*)a.x, (const T*)a.residual, (const T*)a.weight, (T*)a.h,
+    auto go = [&](auto out8, auto streams) {
+      k_rms<T, decltype(rag)::value, decltype(tpr)::value, decltype(nv)::value, decltype(out8)::value,
+            decltype(streams)::value><<<dim3((unsigned)grid), p.threads, 0, s>>>((const T*)a.x, (const T*)a.residual, (const T*)a.weight, (T*)a.h,
                                                       a.y, a.rstd, a.scale, a.rows, a.d, a.eps, lanes);
       return hipGetLastError();
     };
-    return a.scale ? go(std::true_type()) : go(std::false_type());
+    // x, the residual and h, and y
+    const int64_t bytes = a.rows * a.d * ((a.residual ? 3 : 1) * (int)sizeof(T) + (a.scale ? 1 : (int)sizeof(T)));
+    if constexpr (!decltype(rag)::value)
+      if (bytes > kStreamBytes)
+        return a.scale ? go(std::true_type(), std::true_type()) : go(std::false_type(), std::true_type());
+    return a.scale ? go(std::true_type(), std::false_type()) : go(std::false_type(), std::false_type());
   });
 }
 
