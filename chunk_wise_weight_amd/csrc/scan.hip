@@ -161,6 +161,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     if (mine && next < sp.len) xload.issue(x + next * a.sx.t, nlen, Xh);
     const Gates& q = gates[turn][hw];
     f32x4 o[CT][4];
+    __builtin_amdgcn_s_setprio(1);                         // the products before the other waves' decays: 3 %
     if (mine) {
       if (t0 == 0 && sp.first && q.eb[0] == 0.f) S.zero(); // emptied by its first token: S_init is not looked at
 #pragma unroll
@@ -187,6 +188,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
       for (int s = 0; s < CS; ++s) S.add(L, split, xf[s], Bp, s, q.w + s * M::KB + g * (M::KB / 4), a.N);
     }
+    __builtin_amdgcn_s_setprio(0);
     __syncthreads();                                       // B and C have been read
     if (next < sp.len) {
       bload.issue(B + next * a.sB.t, nlen, Bp);
@@ -245,16 +247,24 @@ hipError_t launch(const ScanArgs& a, int seg, int64_t slots, const float* sums, 
   return hipGetLastError();
 }
 
+// 512 workgroups are on the chip at once: one round of them (65,536 tokens x 64 heads: 384 860 us, 512 707 us, 768 794 us,
+// 1024 745 us).  Whole sequences save the pass over the segments' sums: 8 x 64 heads, 256 workgroups, take 91 us for 1,024
+// tokens each (in two segments 109 us) and 341 us for 4,096 (284 us), 12 x 64 heads 425 us for 4,096 (490 us).
+template <typename T>
+int forward_seg(const ScanArgs& a) {
+  return scan_seg<T>(a, 512, a.seqs.n < 2048 ? 256 : 384);
+}
+
 }  // namespace
 
 template <typename T>
 int64_t scan_blocks(const ScanArgs& a) {
-  return (seg_slots(a.seqs, a.batch, scan_seg<T>(a)) + 8) * scan_per_slot<T>(a);
+  return (seg_slots(a.seqs, a.batch, forward_seg<T>(a)) + 8) * scan_per_slot<T>(a);
 }
 
 template <typename T>
 size_t scan_workspace_bytes(const ScanArgs& a) {
-  const int seg = scan_seg<T>(a);
+  const int seg = forward_seg<T>(a);
   if (seg >= a.seqs.n) return 0;
   const int64_t sh = seg_slots(a.seqs, a.batch, seg) * a.H;
   return (size_t)sh * a.P * a.N * 4 + (size_t)((sh * 4 + 15) / 16 * 16);
@@ -262,7 +272,7 @@ size_t scan_workspace_bytes(const ScanArgs& a) {
 
 template <typename T>
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
-  const int seg = scan_seg<T>(a);
+  const int seg = forward_seg<T>(a);
   const int64_t slots = seg_slots(a.seqs, a.batch, seg), sequences = a.seqs.starts ? a.seqs.num : a.batch;
   if (sequences == 0) return hipSuccess;
   const int64_t join = sequences * a.H * (((int64_t)a.P * a.N / 4 + 255) / 256);

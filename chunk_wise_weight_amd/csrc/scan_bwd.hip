@@ -562,7 +562,8 @@ struct GradSpace {
 template <typename T>
 GradSpace grad_space(const ScanArgs& a) {
   GradSpace g;
-  g.seg = scan_seg<T>(a);
+  // both directions' walks run at once: half a round each (4 x 4,096 tokens x 32 heads: 256 485 us, 384 499 us, 512 505 us)
+  g.seg = scan_seg<T>(a, 256, 128);
   g.slots = seg_slots(a.seqs, a.batch, g.seg);
   g.chunks = delta_slots(a.seqs, a.batch);
   const bool cut = g.seg < a.seqs.n;

@@ -322,15 +322,15 @@ int64_t scan_per_slot(const ScanArgs& a) {
   return per;
 }
 
-// Tokens of a segment: as many as leave the chip some workgroups a CU, whole sequences where those do that.
-constexpr int64_t kFill = 1024, kLeastSeg = 256;
+// Tokens of a segment: as many as give the chip `fill` workgroups; whole sequences where those are `whole` or more.
 template <typename T>
-int scan_seg(const ScanArgs& a) {
-  const int64_t n = std::max(a.seqs.n, 1), whole = (n + kDC - 1) / kDC * kDC, per = scan_per_slot<T>(a);
-  if (!a.seqs.starts && a.batch * per >= kFill / 2) return (int)whole;
+int scan_seg(const ScanArgs& a, int64_t fill, int64_t whole) {
+  constexpr int64_t kLeast = 256;
+  const int64_t n = std::max(a.seqs.n, 1), all = (n + kDC - 1) / kDC * kDC, per = scan_per_slot<T>(a);
+  if (!a.seqs.starts && a.batch * per >= whole) return (int)all;
   const int64_t tokens = a.seqs.starts ? n : n * a.batch;
-  const int64_t seg = std::max(kLeastSeg, (tokens * per / kFill + kDC - 1) / kDC * kDC);
-  return (int)std::min(seg, whole);
+  const int64_t seg = std::max(kLeast, (tokens * per / fill + kDC - 1) / kDC * kDC);
+  return (int)std::min(seg, all);
 }
 
 }  // namespace
