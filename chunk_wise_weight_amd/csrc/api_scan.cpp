@@ -104,6 +104,17 @@ ttt::ScanArgs scan_sizes(const ttt_scan_shape* s, int64_t num_seqs) {
   return a;
 }
 
+// At least the workgroups, of up to 512, of a walk's or a gradient's launch: no segment is shorter than a chunk, none
+// takes fewer heads or more than 64 rows of P less than one (the 8 are scan_place's rounding).
+int64_t scan_walks(const ttt_scan_shape* s, int64_t num_seqs) {
+  const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + num_seqs : s->batch * ((s->seq_len + 63) / 64);
+  return (chunks + 8) * s->heads * ((s->head_dim + 63) / 64);
+}
+// The join's workgroups: the states' elements by 1024.
+int64_t scan_states(const ttt_scan_shape* s, int64_t num_seqs) {
+  return scan_sequences(s, num_seqs) * s->heads * ((s->head_dim * s->state + 1023) / 1024);
+}
+
 int check_scan(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
   if (s == nullptr) return TTT_ERR_ARG;
   if (!ok_dtype(dtype)) return TTT_ERR_DTYPE;
@@ -112,24 +123,13 @@ int check_scan(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
   if (num_seqs >= 0 && s->batch != 1) return TTT_ERR_SHAPE;
   const int64_t lim = (int64_t)1 << 30, seqs = scan_sequences(s, num_seqs);
   if (s->seq_len > lim || seqs > lim || (num_seqs < 0 && s->batch * s->seq_len > lim)) return TTT_ERR_UNSUPPORTED;
-  const ttt::ScanArgs a = scan_sizes(s, num_seqs);
-  // every chunk of 64 tokens and head, workgroups of up to 512 over segments, and the states' elements by 1024
-  const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + seqs : s->batch * ((s->seq_len + 63) / 64);
-  if (chunks * s->heads > kMaxBlocks || seqs * s->heads * ((s->head_dim * s->state + 1023) / 1024) > kMaxBlocks ||
-      2 * (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
-    return TTT_ERR_UNSUPPORTED;
+  if (scan_walks(s, num_seqs) > kMaxBlocks / 2 || scan_states(s, num_seqs) > kMaxBlocks) return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 
-// What the backward pass takes less of: walks in both directions, a workgroup of 512 for each chunk and group, twice the
-// states' elements by 1024.
-int check_scan_backward(const ttt_scan_shape* s, int dtype, int64_t num_seqs) {
-  const ttt::ScanArgs a = scan_sizes(s, num_seqs);
-  const int64_t seqs = scan_sequences(s, num_seqs);
-  const int64_t chunks = num_seqs >= 0 ? s->seq_len / 64 + seqs : s->batch * ((s->seq_len + 63) / 64);
-  if (2 * chunks * s->groups > kMaxBlocks || 2 * seqs * s->heads * ((s->head_dim * s->state + 1023) / 1024) > kMaxBlocks ||
-      4 * (dtype == TTT_BF16 ? ttt::scan_blocks<bf16>(a) : ttt::scan_blocks<float>(a)) > kMaxBlocks)
-    return TTT_ERR_UNSUPPORTED;
+// What the backward pass takes less of: walks and joins in both directions at once.
+int check_scan_backward(const ttt_scan_shape* s, int64_t num_seqs) {
+  if (scan_walks(s, num_seqs) > kMaxBlocks / 4 || scan_states(s, num_seqs) > kMaxBlocks / 2) return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 
@@ -281,7 +281,7 @@ int ttt_selective_scan(const ttt_scan_shape* shape, int dtype, const void* x, co
 int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes) {
   if (bytes == nullptr) return TTT_ERR_ARG;
   if (int st = check_scan(shape, dtype, num_seqs)) return st;
-  if (int st = check_scan_backward(shape, dtype, num_seqs)) return st;
+  if (int st = check_scan_backward(shape, num_seqs)) return st;
   const ttt::ScanArgs a = scan_sizes(shape, num_seqs);
   *bytes = dtype == TTT_BF16 ? ttt::scan_grad_workspace_bytes<bf16>(a) : ttt::scan_grad_workspace_bytes<float>(a);
   return TTT_OK;

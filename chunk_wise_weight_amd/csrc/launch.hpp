@@ -358,8 +358,6 @@ struct ScanArgs {
 template <typename T>
 size_t scan_workspace_bytes(const ScanArgs& a);
 template <typename T>
-int64_t scan_blocks(const ScanArgs& a);              // workgroups of the largest launch
-template <typename T>
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 
 struct KeptGates;

@@ -258,11 +258,6 @@ int forward_seg(const ScanArgs& a) {
 }  // namespace
 
 template <typename T>
-int64_t scan_blocks(const ScanArgs& a) {
-  return (seg_slots(a.seqs, a.batch, forward_seg<T>(a)) + 8) * scan_per_slot<T>(a);
-}
-
-template <typename T>
 size_t scan_workspace_bytes(const ScanArgs& a) {
   const int seg = forward_seg<T>(a);
   if (seg >= a.seqs.n) return 0;
@@ -300,7 +295,6 @@ hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
 }
 
 #define TTT_SCAN(T)                                                  \
-  template int64_t scan_blocks<T>(const ScanArgs&);                  \
   template size_t scan_workspace_bytes<T>(const ScanArgs&);          \
   template hipError_t launch_scan<T>(const ScanArgs&, hipStream_t);
 TTT_SCAN(bf16)

@@ -805,7 +805,8 @@ typedef struct {
 } ttt_delta_step_shape;
 
 /* One token for each row of a serving batch, on states that stay in a pool
- * and are updated IN PLACE (the one exception to read-only inputs).
+ * and are updated IN PLACE (as in the other step calls, the exceptions to
+ * read-only inputs).
  *   q, k      [rows, Hk, dk]  dtype
  *   v         [rows, Hv, dv]  dtype
  *   g, beta   [rows, Hv]      fp32 (4-byte aligned)
@@ -975,9 +976,10 @@ int ttt_short_conv_step(int64_t rows, int64_t states, int64_t dim, int64_t taps,
  * n = seq_len, P = head_dim, N = state; head h reads group h / (heads /
  * groups) of B and C.  Supported: heads a multiple of groups (else
  * TTT_ERR_SHAPE); head_dim and state multiples of 8, state <= 256, head_dim <=
- * 4096, heads <= 65536, batch * seq_len <= 2^30, chunks of 64 tokens (packed:
- * seq_len / 64 + sequences) times heads and sequences * heads * ceil(P N /
- * 1024) below 2^24 (else TTT_ERR_UNSUPPORTED). */
+ * 4096, heads <= 65536, batch * seq_len <= 2^30, (chunks + 8) * heads * ceil(P /
+ * 64) below 2^23, chunks being those of 64 tokens (packed: seq_len / 64 +
+ * sequences), and sequences * heads * ceil(P N / 1024) below 2^24 (else
+ * TTT_ERR_UNSUPPORTED). */
 typedef struct {
   int64_t batch, seq_len, heads, groups, head_dim, state;
 } ttt_scan_shape;
@@ -1028,9 +1030,9 @@ typedef struct {
   ttt_delta_strides dO, dx, ddt, dB, dC;
 } ttt_scan_grad_layout;
 
-/* Workspace of ttt_selective_scan_backward; num_seqs < 0: not packed.  Chunks
- * of 64 tokens times groups, sequences * heads * ceil(P N / 1024) below 2^23,
- * else TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + some 6 KB, and
+/* Workspace of ttt_selective_scan_backward; num_seqs < 0: not packed.  The
+ * limits in ttt_scan_shape are half as high (2^22 and 2^23), else
+ * TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + some 6 KB, and
  * for each segment and head 8 P N + 8. */
 int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
 
