@@ -18,6 +18,10 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   constexpr int CT = Z::CT, NT = Z::NT, NS = Z::NS, CS = Z::CS, W = Z::W, U = M::TPS;
   constexpr int PB = CT == 2 && U == 2 ? 2 : 1, CB = CT / PB;  // blocks of P that are stored as one; of those
   constexpr int FW = (M::kTri + W - 1) / W;                // fragments of C B^T a wave makes: w, w + W, ..
+  // Where that gives some waves one more than the others, those E fragments are dealt out by heads: a wave makes W + w % E
+  // for the heads with its w / E (of W / E).
+  constexpr int E = M::kTri - W, Q = E > 0 && E < W ? W / E : 1;
+  constexpr bool kDealt = Q > 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ Gates gates[2][HW];
   char *const Bp = smem, *const Cp = Bp + Z::kB, *const Xp = Cp + Z::kB, *const Mp = Xp + HW * Z::kX;
@@ -100,6 +104,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     for (int s = 0; s < CS; ++s)
 #pragma unroll
       for (int c = 0; c < CT; ++c) xf[s][c] = state_cols<T, CT>(L, Xh, pw * CT + c, s);
+    auto fragment = [&](int k) { return kDealt && k > 0 ? W + w % E : w + k * W; };
     // C B^T of a fragment's tokens row(t, .) and those before them; all of a wave's fragments at once
     auto decayed = [&](auto count) __attribute__((always_inline)) {
       constexpr int NF = decltype(count)::value;
@@ -107,7 +112,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
       f32x4 d[NF][U];
 #pragma unroll
       for (int k = 0; k < NF; ++k) {
-        tri_place<T>(w + k * W, &ft[k], &fs[k]);
+        tri_place<T>(fragment(k), &ft[k], &fs[k]);
         fi[k] = M::row(ft[k], m);
 #pragma unroll
         for (int u = 0; u < U; ++u) d[k][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -127,6 +132,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
         const Gates& q = gates[turn][hd];
 #pragma unroll
         for (int k = 0; k < NF; ++k) {
+          if (kDealt && k > 0 && hd % Q != w / E) continue;
           const int i = fi[k];
           const float bh = q.hi[i], bl = U == 2 ? 0.f : q.lo[i];
           int behind = i - M::row(fs[k] * U, 4 * g);       // tokens of the lane's row of d before i
@@ -147,13 +153,13 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
           }
           u32x4 hi, lo;
           split.two(v, hi, lo);
-          char* to = Mp + hd * Z::kM + (w + k * W) * 1024 + lane * 16;
+          char* to = Mp + hd * Z::kM + fragment(k) * 1024 + lane * 16;
           *reinterpret_cast<u32x4*>(to) = hi;
           if (M::kSplit) *reinterpret_cast<u32x4*>(to + M::kTri * 1024) = lo;
         }
       }
     };
-    if (M::kTri % W == 0 || w < M::kTri % W)
+    if (kDealt ? w / E < HW : M::kTri % W == 0 || w < M::kTri % W)
       decayed(std::integral_constant<int, FW>());
     else if constexpr (FW > 1)
       decayed(std::integral_constant<int, FW - 1>());
