@@ -34,13 +34,14 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   const bool mine = at.head0 + hw < shared;                // a head of the group
   const int h = at.group * shared + min(at.head0 + hw, shared - 1);
   const int p0 = at.part * Z::cols, tile0 = (p0 >> 4) + pw * CT;
+  const bool busy = mine && tile0 * 16 < a.P;              // rows of its state
   const int64_t sh = (int64_t)at.slot * a.H + h, size = (int64_t)a.P * a.N;
 
   const LaneAt<T> L(lane);
   const Split<T> split(lane);
   StateRows<T, CT, NT> S;
   S.zero();
-  if (mine) {
+  if (busy) {
     if (sums)
       S.load(sums + sh * size, tile0, a.P, a.N);
     else if (a.S_init)
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     const int next = t0 + kDC, nlen = min(kDC, sp.len - next);
     wait_vm<0>();
     __syncthreads();                                       // the chunk and its gates are there
-    if (mine && t0 > 0) store(t0 - kDC);
+    if (busy && t0 > 0) store(t0 - kDC);
     u32x4 xf[CS][CT];
 #pragma unroll
     for (int s = 0; s < CS; ++s)
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
       }
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) {
-        if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
+        if (past<T, DN>(ns * M::KB, a.N)) break;
 #pragma unroll
         for (int k = 0; k < NF; ++k) {
           const u32x4 c = L.frag(Cp, ft[k], ns);
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
     const Gates& q = gates[turn][hw];
     f32x4 o[CT][4];
     __builtin_amdgcn_s_setprio(1);                         // the products before the other waves' decays: 3 %
-    if (mine) {
+    if (busy) {
       if (t0 == 0 && sp.first && q.eb[0] == 0.f) S.zero(); // emptied by its first token: S_init is not looked at
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
         for (int t = 0; t < 4; ++t) o[c][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) {
-        if (NS > 128 / M::KB && ns % (64 / M::KB) == 0 && ns * M::KB >= a.N) break;
+        if (past<T, DN>(ns * M::KB, a.N)) break;
         u32x4 hi[CT], lo[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) split.two(&S.s[c][ns * U], hi[c], lo[c]);
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
       cload.issue(C + next * a.sC.t, nlen, Cp);
       make(next, turn ^ 1);
     }
-    if (mine) {
+    if (busy) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float e = q.eb[M::row(t, m)];
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
       }
     }
   }
-  if (mine) {
+  if (busy) {
     store((sp.len - 1) / kDC * kDC);
     if (sp.last) S.store(a.S_final + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
   }

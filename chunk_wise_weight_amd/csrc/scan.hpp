@@ -310,6 +310,12 @@ template <typename T> struct Scaled {
 // operands in three parts at once).
 template <typename T, int DN> constexpr int kBlocks = sizeof(T) == 2 && DN <= 128 ? 2 : 1;
 
+// Whether a state's columns from `col` on, zero past N, may be left out: looked at where a branch costs less than what it
+// saves, every 16 columns in fp32, whose products take eight times as long, every 64 of the widest in bf16.
+template <typename T, int DN> __device__ __forceinline__ bool past(int col, int N) {
+  return (sizeof(T) == 4 ? col > 0 : DN > 128 && col % 64 == 0) && col >= N;
+}
+
 // The heads' waves of a workgroup: HW heads of a group, PW waves with CT blocks of 16 rows of the state each.
 template <typename T, int DN_, int HW_, int PW_, int CT_ = kBlocks<T, DN_>> struct ScanShape {
   static constexpr int DN = DN_, HW = HW_, PW = PW_, W = HW * PW;
@@ -367,14 +373,13 @@ template <typename T, int CT, int NT> struct StateRows {
   }
   // += the weighted outer products of a step's tokens: x[c] their features of this wave's blocks, `cols` their rows of N
   // in LDS.  All blocks of P at once, so that an operand is read once.
-  // Columns past N are zero in LDS; whole halves of the widest states are passed over.
   __device__ __forceinline__ void add(const LaneAt<T>& L, const Split<T>& sp, const u32x4 (&x)[CT], const char* cols,
                                       int step, const float* weights, int N) {
     static_assert(CT <= 2, "blocks");
     const Scaled<T> u0(sp, x[0], weights), u1(sp, x[CT - 1], weights);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (NT > 8 && t % 4 == 0 && t * 16 >= N) break;
+      if (past<T, NT * 16>(t * 16, N)) break;
       const u32x4 f = L.cols(cols, t, step);
 #pragma unroll
       for (int k = Scaled<T>::kParts - 1; k >= 0; --k) {

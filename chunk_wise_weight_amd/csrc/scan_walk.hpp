@@ -52,7 +52,7 @@ template <typename T, int DN, int HW, int PW, int CT_> struct StateWalker {
   ScanPlace at;
   SegPlace sp;
   int w, hw, pw, lane, h, gh, tile0, chunks;
-  bool mine;                                                 // a head of the group
+  bool mine, busy;                                           // a head of the group; rows of its state
   TileLoader<T, DN, W> cload;
   TileLoader<T, Z::DX, PW> rload;
   const T *cols, *rows;
@@ -69,6 +69,7 @@ template <typename T, int DN, int HW, int PW, int CT_> struct StateWalker {
     h = at.group * shared + min(at.head0 + hw, shared - 1);
     gh = at.group * shared + min(at.head0 + w, shared - 1);  // the gates of head head0 + w are made by wave w
     tile0 = (p0 >> 4) + pw * CT;
+    busy = mine && tile0 * 16 < a.P;
     chunks = (sp.len + kDC - 1) / kDC;
     cols = (const T*)k.cols + sp.b * k.scols.b + at.group * k.scols.h + sp.tok0 * k.scols.t;
     rows = (const T*)k.rows + sp.b * k.srows.b + h * k.srows.h + sp.tok0 * k.srows.t + p0;
@@ -142,7 +143,7 @@ __device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& 
       if (K::kStages == 2) q.load(t0 + step, stage ^ 1);
       gates(t0 + step, stage ^ 1);
     }
-    if (q.mine) q.add(S, L, split, stage, weights[stage][q.hw]);
+    if (q.busy) q.add(S, L, split, stage, weights[stage][q.hw]);
     if (K::kStages == 1 && t0 + step != end) {
       __syncthreads();
       q.load(t0 + step, 0);
@@ -150,7 +151,7 @@ __device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& 
     stage ^= 1;
   }
   const int64_t size = (int64_t)a.P * a.N;
-  if (q.mine) S.store(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
+  if (q.busy) S.store(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
   // (heads past the group's repeat the last one's; after a break F is below kNone and stays there)
   if (q.w < HW && q.lane == 0 && at.part == 0) k.decays[(int64_t)at.slot * a.H + q.gh] = exp2_hw((float)F);
 }
@@ -170,7 +171,7 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
   const Split<T> split(q.lane);
   StateRows<T, K::CT, K::NT> S;
   S.zero();
-  if (q.mine) {
+  if (q.busy) {
     if (k.sums)
       S.load(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
     else if (k.start)
@@ -204,7 +205,7 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
     wait_vm<0>();
     __syncthreads();                                         // the stage is there, the other one has been read
     const Gates& g = gates[stage][q.hw];
-    if (q.mine) {
+    if (q.busy) {
       if (!k.back && sp.first && t0 == 0 && g.eb[0] == 0.f) S.zero();   // emptied by its first token
       S.store(k.keep + ((int64_t)(slot0 + t0 / kDC) * a.H + q.h) * size, q.tile0, a.P, a.N);
     }
@@ -212,7 +213,7 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
       if (K::kStages == 2) q.load(t0 + step, stage ^ 1);
       make(t0 + step, stage ^ 1);
     }
-    if (q.mine) {
+    if (q.busy) {
       S.decay(g.eb[kDC - 1]);
       q.add(S, L, split, stage, k.back ? g.eb : g.w);
     }
@@ -222,7 +223,7 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
     }
     stage ^= 1;
   }
-  if (q.mine && k.back && sp.first && k.end)
+  if (q.busy && k.back && sp.first && k.end)
     S.store(k.end + ((int64_t)sp.seq * a.H + q.h) * size, q.tile0, a.P, a.N);
 }
 
