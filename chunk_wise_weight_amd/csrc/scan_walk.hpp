@@ -269,15 +269,22 @@ __device__ __forceinline__ void join_segments(const ScanArgs& a, const StateWalk
   const int64_t o = ((int64_t)s * a.H + h) * size + e;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (k.start) S = *reinterpret_cast<const f32x4*>(k.start + o);
+  constexpr int U = 4;                                       // segments whose loads are under way at once
   if (k.sums)
-    for (int i = 0; i < q.count; ++i) {
-      const int64_t sh = (int64_t)(q.first + (k.back ? q.count - 1 - i : i)) * a.H + h;
-      f32x4* at = reinterpret_cast<f32x4*>(k.sums + sh * size + e);
-      const f32x4 own = *at;                               // the last one's is not made
-      *at = S;
-      if (i + 1 < q.count) {
-        const float d = k.decays[sh];
-        S = d == 0.f ? own : S * d + own;
+    for (int i0 = 0; i0 < q.count; i0 += U) {
+      f32x4 own[U];
+      float d[U];
+      auto slot = [&](int i) { return (int64_t)(q.first + (k.back ? q.count - 1 - i : i)) * a.H + h; };
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u + 1 < q.count) {                          // the last one's is not made
+          own[u] = *reinterpret_cast<const f32x4*>(k.sums + slot(i0 + u) * size + e);
+          d[u] = k.decays[slot(i0 + u)];
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u < q.count) *reinterpret_cast<f32x4*>(k.sums + slot(i0 + u) * size + e) = S;
+        if (i0 + u + 1 < q.count) S = d[u] == 0.f ? own[u] : S * d[u] + own[u];
       }
     }
   if (q.count == 0 && empty) *reinterpret_cast<f32x4*>(empty + o) = S;
