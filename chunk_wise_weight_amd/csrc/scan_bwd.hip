@@ -59,7 +59,7 @@ template <typename T, int DN_, bool LDS_> struct GradShape {
 };
 
 // x summed over the four lanes that hold a token.
-__device__ __forceinline__ float token_sum(float x) {
+template <typename F> __device__ __forceinline__ F token_sum(F x) {
   x += __shfl_xor(x, 16, 64);
   return x + __shfl_xor(x, 32, 64);
 }
@@ -67,7 +67,13 @@ __device__ __forceinline__ float token_sum(float x) {
 template <int ROR> __device__ __forceinline__ float ror_add(float x) {
   return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + ROR, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float group_sum(float x) { return ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(x)))); }
+template <int ROR> __device__ __forceinline__ double ror_add(double x) {
+  u32x2 w = __builtin_bit_cast(u32x2, x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = (unsigned)__builtin_amdgcn_update_dpp(0, (int)w[i], 0x120 + ROR, 0xf, 0xf, true);
+  return x + __builtin_bit_cast(double, w);
+}
+template <typename F> __device__ __forceinline__ F group_sum(F x) { return ror_add<1>(ror_add<2>(ror_add<4>(ror_add<8>(x)))); }
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]; }
 // Keeps the instructions of a phase together: reads drawn ahead over phases cost registers, and what is then spilled waits
 // for the loads under way.
@@ -113,9 +119,12 @@ __device__ __forceinline__ void put_planes(f32x4 a, f32x4 b, char* plane, int st
 
 // What the gradients of a chunk's rates are made of, for one head: with Z_ij = (C_i . B_j) (dO_i . x_j) exp(b_i - b_j),
 // by token: sums of Z_ij r_j over j < i (by steps of j), of Z_ij over i > j (by blocks of i), Z_ii and dO_i . x_i; C_i . S^T
-// dO_i and B_j . dS^T x_j by blocks of N; and <S, dS> by waves.
+// dO_i and B_j . dS^T x_j by blocks of N; and <S, dS> by waves.  The sums of Z are fp64: a decay gets the difference of
+// the rows' and columns' sums up to its token, in which all but the pairs about it have to cancel (in fp32 what was left of
+// them, the same for all tokens that follow, made dA and the bias's gradient of fast heads off by 4e-6).
 template <typename T> struct TokenSums {
-  float rows[kDC / Mat<T>::KB][kDC], cols[4][kDC], diag[2][kDC], dots[8][kDC], ss[8], pad[8];
+  double rows[kDC / Mat<T>::KB][kDC], cols[4][kDC];
+  float diag[2][kDC], dots[8][kDC], ss[8], pad[8];
 };
 
 // One workgroup of 8 waves per chunk slot and group, its heads one after the other.
@@ -381,12 +390,12 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       int i = M::row(t, m);
       asm volatile("" : "+v"(i));
       f32x4 w[U];
-      float rs = 0.f;
+      double rs = 0.0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = M::row(s * U + u, 4 * g);
         const f32x4 r = *reinterpret_cast<const f32x4*>(q.r + j);
-        f32x4 cs;
+        double cs[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = V[k][u][e] * E[k][u][e], z = v * G[k][u][e];
@@ -395,11 +404,13 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
             sums.diag[0][i] = z;
             sums.diag[1][i] = V[k][u][e];
           }
-          const float below = j + e < i ? z : 0.f;
+          const double below = j + e < i ? z : 0.f;
           rs += below * r[e];
           cs[e] = group_sum(below);
         }
-        if (m == 0) *reinterpret_cast<f32x4*>(&sums.cols[t][j]) = cs;
+        if (m == 0)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sums.cols[t][j + e] = cs[e];
       }
       rs = token_sum(rs);
       if (g == 0) sums.rows[s][i] = rs;
@@ -481,15 +492,15 @@ __global__ __launch_bounds__(256) void k_scan_rates(ScanGradArgs a, int64_t chun
   if (c.len > 0) {
     const TokenSums<T>& s = reinterpret_cast<const TokenSums<T>*>(a.sums)[sh];
     const KeptGates& q = a.gates[sh];
-    float rsum = 0.f, csum = 0.f;
+    double rsum = 0.0, csum = 0.0;
 #pragma unroll
-    for (int k = 0; k < kDC / M::KB; ++k) rsum += lane >= k * M::KB ? s.rows[k][lane] : 0.f;
+    for (int k = 0; k < kDC / M::KB; ++k) rsum += lane >= k * M::KB ? s.rows[k][lane] : 0.0;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) csum += lane / M::KB < M::steps(t) ? s.cols[t][lane] : 0.f;
+    for (int t = 0; t < 4; ++t) csum += lane / M::KB < M::steps(t) ? s.cols[t][lane] : 0.0;
     const float r = q.g.r[lane];
     const float so = (s.dots[0][lane] + s.dots[1][lane]) + (s.dots[2][lane] + s.dots[3][lane]);
     const float us = q.rest[lane] * ((s.dots[4][lane] + s.dots[5][lane]) + (s.dots[6][lane] + s.dots[7][lane]));   // x . dS B
-    double R = (double)(csum * r) - rsum, z = us * r, y = q.g.eb[lane] * so;
+    double R = csum * r - rsum, z = us * r, y = q.g.eb[lane] * so;
     const double r0 = R, z0 = z;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) {
@@ -506,7 +517,7 @@ __global__ __launch_bounds__(256) void k_scan_rates(ScanGradArgs a, int64_t chun
     // pairs that token t's decay lies between: those of t - 1, less row t - 1's, and column t - 1's
     const float dg = (float)((R - r0) + (z - z0) + y) + q.g.eb[kDC - 1] * all;
     const bool in = lane < c.len;
-    const float ddt = in ? (us + csum + s.diag[0][lane] + p.A[h] * dg) * q.slope[lane] : 0.f;
+    const float ddt = in ? (us + (float)csum + s.diag[0][lane] + p.A[h] * dg) * q.slope[lane] : 0.f;
     if (in) a.ddt[c.b * a.sddt.b + h * a.sddt.h + (c.tok0 + lane) * a.sddt.t] = ddt;
     double sa = in ? (double)dg * r : 0.0, sb = ddt, sd = s.diag[1][lane];
 #pragma unroll

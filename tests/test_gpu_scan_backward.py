@@ -178,3 +178,21 @@ def test_refusals():
                 dict(dB=B.float()), dict(workspace=torch.empty(0, device="cuda"))):
         with pytest.raises((ValueError, TypeError)):
             cw.ttt_selective_scan_backward(**{**good, **bad})
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sums_over_tokens_of_fast_heads(dtype):
+    """Heads that forget within a few tokens: dA and ddt_bias are sums over thousands of tokens of either sign.  A token's
+    part is off by at most 16 roundings (2^-24) of its own size, each by itself, and the exact sum has the size of as many
+    parts of random sign: 16 * 2^-24 of it.  What errors of a token passed on to those behind it came to was four times
+    that and more."""
+    H, n = 8, 2048
+    *args, D, _ = make(1, H, 1, n, 64, 128, dtype, seed=9)
+    args[2] = torch.linspace(-16, -12, H).cuda()
+    bias = torch.full((H,), -2.25, device="cuda")
+    dO = torch.randn(args[0].shape, generator=torch.Generator().manual_seed(10)).to(dtype).cuda()
+    got = cw.ttt_selective_scan_backward(*args, dO, D=D, dt_bias=bias, softplus=True)
+    want = osc.selective_scan_backward(*(f64(t[0]) if t.dim() > 1 else f64(t) for t in args), f64(dO[0]), f64(D), f64(bias), True)
+    for t, k in ((got[2], "dA"), (got[6], "ddt_bias")):
+        print(k, rel(t, want[k]), flush=True)
+        assert rel(t, want[k]) <= 16 * 2.0 ** -24, k
