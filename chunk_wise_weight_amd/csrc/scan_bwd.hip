@@ -498,8 +498,15 @@ __global__ __launch_bounds__(256) void k_scan_rates(ScanGradArgs a, int64_t chun
 #pragma unroll
     for (int t = 0; t < 4; ++t) csum += lane / M::KB < M::steps(t) ? s.cols[t][lane] : 0.0;
     const float r = q.g.r[lane];
-    const float so = (s.dots[0][lane] + s.dots[1][lane]) + (s.dots[2][lane] + s.dots[3][lane]);
-    const float us = q.rest[lane] * ((s.dots[4][lane] + s.dots[5][lane]) + (s.dots[6][lane] + s.dots[7][lane]));   // x . dS B
+    double so = 0.0, us = 0.0, all = 0.0;                    // dO . S C, x . dS B, <S, dS>
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      so += s.dots[i][lane];
+      us += s.dots[4 + i][lane];
+    }
+    us *= q.rest[lane];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all += s.ss[i];
     double R = csum * r - rsum, z = us * r, y = q.g.eb[lane] * so;
     const double r0 = R, z0 = z;
 #pragma unroll
@@ -511,15 +518,12 @@ __global__ __launch_bounds__(256) void k_scan_rates(ScanGradArgs a, int64_t chun
       }
       if (lane + i < 64) y += dy;
     }
-    float all = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) all += s.ss[i];
     // pairs that token t's decay lies between: those of t - 1, less row t - 1's, and column t - 1's
-    const float dg = (float)((R - r0) + (z - z0) + y) + q.g.eb[kDC - 1] * all;
+    const double dg = (R - r0) + (z - z0) + y + q.g.eb[kDC - 1] * all;
     const bool in = lane < c.len;
-    const float ddt = in ? (us + (float)csum + s.diag[0][lane] + p.A[h] * dg) * q.slope[lane] : 0.f;
-    if (in) a.ddt[c.b * a.sddt.b + h * a.sddt.h + (c.tok0 + lane) * a.sddt.t] = ddt;
-    double sa = in ? (double)dg * r : 0.0, sb = ddt, sd = s.diag[1][lane];
+    const double ddt = in ? (us + csum + s.diag[0][lane] + p.A[h] * dg) * q.slope[lane] : 0.0;
+    if (in) a.ddt[c.b * a.sddt.b + h * a.sddt.h + (c.tok0 + lane) * a.sddt.t] = (float)ddt;
+    double sa = in ? dg * r : 0.0, sb = ddt, sd = s.diag[1][lane];
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) {
       sa += __shfl_xor(sa, i, 64);
