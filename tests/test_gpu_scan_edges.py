@@ -411,3 +411,81 @@ def test_one_tap():
     assert torch.equal(cw.ttt_short_conv_step(x[0, :4].contiguous(), w, halo, b), Y[0, :4])
     dx, dw, db, _ = cw.ttt_short_conv_backward(x, w, torch.ones_like(x), b)
     assert dx.shape == x.shape and torch.isfinite(dx).all() and dw.shape == w.shape and db.shape == b.shape
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_no_tokens_and_no_rows(dtype):
+    """Zero tokens leave the states as they were (or zero) and give zero sums; zero rows and sequences give empty tensors."""
+    H, G, P, N = 2, 1, 24, 16
+    print("empty", dtype, flush=True)
+    for B, n in ((3, 0), (0, 5), (0, 0)):
+        *args, D, bias = make(B, H, G, n, P, N, dtype)
+        S0 = torch.randn(B, H, P, N, device="cuda")
+        more = dict(D=D, dt_bias=bias, softplus=True, S_init=S0)
+        O, S = cw.ttt_selective_scan(*args, **more)
+        assert O.shape == (B, H, n, P) and torch.equal(S, S0)
+        assert (cw.ttt_selective_scan(*args)[1] == 0).all()
+        dS = torch.randn_like(S0)
+        dx, ddt, dA, dB, dC, dD, db, dS0 = cw.ttt_selective_scan_backward(*args, torch.empty_like(args[0]), dS_final=dS, **more)
+        assert dx.shape == (B, H, n, P) and torch.equal(dS0, dS)
+        assert not dA.any() and not dD.any() and not db.any()
+        x, w, b = torch.empty(B, n, 40, dtype=dtype, device="cuda"), torch.randn(40, 4).to(dtype).cuda(), torch.randn(40).to(dtype).cuda()
+        x0 = torch.randn(B, 3, 40).to(dtype).cuda()
+        Y, last = cw.ttt_short_conv(x, w, b, x_init=x0)
+        dx, dw, db, dx0 = cw.ttt_short_conv_backward(x, w, x, b, x_init=x0, dx_final=x0)
+        assert Y.shape == x.shape and dx.shape == x.shape and torch.equal(last, x0) and torch.equal(dx0, x0)
+        assert not dw.any() and not db.any()
+    e = lambda *s: torch.empty(*s, dtype=dtype, device="cuda")
+    f = lambda *s: torch.empty(*s, device="cuda")
+    assert cw.ttt_selective_scan_step(e(0, H, P), f(0, H), f(H), e(0, G, N), e(0, G, N), f(3, H, P, N)).shape == (0, H, P)
+    assert cw.ttt_short_conv_step(e(0, 40), e(40, 4), e(3, 3, 40)).shape == (0, 40)
+    assert cw.ttt_rms_norm(e(0, 40), residual=e(0, 40))[0].shape == (0, 40)
+    dx, dw = cw.ttt_rms_norm_backward(e(0, 40), e(40), e(0, 40), f(0))
+    assert dx.shape == (0, 40) and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,G,P,N", [(1, 1, 1000, 16), (2, 1, 264, 200), (1, 1, 4096, 8), (9, 1, 8, 8), (40, 2, 16, 24)])
+def test_wide_narrow_and_many_heads(H, G, P, N, dtype):
+    """Heads over several workgroups, and groups of more heads than a workgroup has, against the oracle; the bounds of
+    the scan's tests (2^-8 and 2^-13 of bf16 outputs; 320 * 2^-24 of fp32 ones) with 4 times the fp32 bound in the backward
+    pass, which has two such products one behind the other and their sums over heads."""
+    n = 150
+    print("heads", H, G, P, N, dtype, flush=True)
+    *args, D, bias = make(1, H, G, n, P, N, dtype, layout="token")
+    dO = torch.randn(args[0].shape, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    more = dict(D=D, dt_bias=bias, softplus=True)
+    O, S = cw.ttt_selective_scan(*args, **more)
+    ref = [f64(t[0]) if t.dim() > 1 else f64(t) for t in args]
+    Or, Sr = osc.selective_scan(*ref, f64(D), f64(bias), True)
+    fp32 = 320 * 2.0 ** -24
+    out = fp32 if dtype == torch.float32 else 2.0 ** -8 + 2.0 ** -13
+    assert rel(O[0], Or) <= out and rel(S[0], Sr) <= fp32
+    got = cw.ttt_selective_scan_backward(*args, dO, **more)
+    want = osc.selective_scan_backward(*ref, f64(dO[0]), f64(D), f64(bias), True)
+    for t, k in zip(got, ("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias")):
+        v = t[0] if t.dim() > 1 else t
+        print(" ", k, rel(v, want[k]), flush=True)
+        assert rel(v, want[k]) <= (4 * fp32 if t.dtype == torch.float32 else out), k
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_short_sequences_are_a_batch(dtype):
+    """2000 packed sequences of 3 tokens give the bits of a batch of them."""
+    num, n, H, G, P, N = 2000, 3, 2, 1, 64, 32
+    *args, D, bias = make(num, H, G, n, P, N, dtype)
+    dO = torch.randn(num, H, n, P, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    more = dict(D=D, dt_bias=bias, softplus=True)
+    flat = lambda t: t.transpose(1, 2).flatten(0, 1)[None].transpose(1, 2).contiguous()
+    starts = torch.arange(0, num * n + 1, n, dtype=torch.int32, device="cuda")
+    pack = [flat(t) if t.dim() > 1 else t for t in args]
+    O, S = cw.ttt_selective_scan(*args, **more)
+    Op, Sp = cw.ttt_selective_scan(*pack, **more, seq_starts=starts)
+    assert torch.equal(flat(O), Op) and torch.equal(S, Sp)
+    g = cw.ttt_selective_scan_backward(*args, dO, **more)
+    p = cw.ttt_selective_scan_backward(*pack, flat(dO), **more, seq_starts=starts)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(flat(g[i]), p[i]), i
+    # (sums over all tokens: fp64 of the chunks' fp32 parts, in another order)
+    for i in (2, 5, 6):
+        assert rel(p[i], f64(g[i])) <= 4 * 2.0 ** -24, i
