@@ -252,7 +252,7 @@ hipError_t launch(const ScanArgs& a, int seg, int64_t slots, const float* sums, 
   static_assert(smem + 2 * (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
   const int64_t shared = a.H / a.G;
   const int64_t per = (shared + HW - 1) / HW * ((a.P + Z::cols - 1) / Z::cols);
-  k_scan<T, DN, HW, PW><<<dim3((unsigned)walk_blocks(slots * a.G, per)), 64 * HW * PW, smem, s>>>(a, seg, (int)slots, sums);
+  k_scan<T, DN, HW, PW><<<dim3((unsigned)scan_grid(slots * a.G, per)), 64 * HW * PW, smem, s>>>(a, seg, (int)slots, sums);
   return hipGetLastError();
 }
 

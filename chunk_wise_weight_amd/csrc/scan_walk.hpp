@@ -10,15 +10,24 @@ namespace {
 
 constexpr int kMaxLds = 160 * 1024;
 
-// Which (segment slot, group, heads, part of P) a workgroup has: those that read the same B and C go to one XCD.
+// Which (segment slot, group, heads, part of P) a workgroup has.  Up to 4 that read the same B and C go to one
+// XCD: all of them would leave the XCDs unevenly filled where sequences differ (12 packed prompts, 32 heads of one group: all
+// 16 132 us, 8 167 us, 4 126 us, 2 131 us; equal segments of 64 heads: 662, 656, 661, 670 us).
 struct ScanPlace {
   int slot, group, head0, part;       // head0: first head, within the group
 };
+inline __host__ __device__ int scan_near(int per) { return per % 4 == 0 ? 4 : per % 2 == 0 ? 2 : 1; }
 __device__ __forceinline__ bool scan_place(int bid, int slots, int G, int heads, int parts, int HW, ScanPlace* o) {
-  const int per = (heads + HW - 1) / HW * parts, unit = bid / 8 / per * 8 + (bid & 7), j = bid / 8 % per;
+  const int per = (heads + HW - 1) / HW * parts, near = scan_near(per);
+  const int at = (bid / 8 / near * 8 + (bid & 7)) * near + bid / 8 % near, unit = at / per, j = at % per;
   if (unit >= slots * G) return false;
   *o = {unit / G, unit % G, j / parts * HW, j % parts};
   return true;
+}
+
+inline int64_t scan_grid(int64_t units, int64_t per) {
+  const int near = scan_near((int)per);
+  return walk_blocks(units * (per / near), near);
 }
 
 // What a walk over states works on: forward S from B, x and exp(b_63 - b) r, or back dS from C, dO and exp(b).
@@ -254,7 +263,7 @@ hipError_t launch_states(const ScanArgs& a, const StateWalk& one, const StateWal
   constexpr int smem = K::kStages * K::kStage;
   static_assert(smem + 2 * (int)sizeof(Gates) * HW <= kMaxLds, "LDS");
   const int64_t shared = a.H / a.G;
-  const int64_t half = walk_blocks(slots * a.G, (shared + HW - 1) / HW * ((a.P + Z::cols - 1) / Z::cols));
+  const int64_t half = scan_grid(slots * a.G, (shared + HW - 1) / HW * ((a.P + Z::cols - 1) / Z::cols));
   k_scan_states<T, DN, HW, PW, CT, KEEP><<<dim3((unsigned)(two ? 2 * half : half)), 64 * HW * PW, smem, s>>>(
       a, one, two ? *two : one, seg, (int)slots, (int)half);
   return hipGetLastError();
