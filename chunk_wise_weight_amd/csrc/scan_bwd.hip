@@ -221,6 +221,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
     if (wave + 8 * k < M::kTri)
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
+        if (past<T, kBV>(n * M::KB, N)) break;
         const u32x4 f = C.frag(L, ft[k], n);
 #pragma unroll
         for (int u = 0; u < U; ++u) G[k][u] = M::mma(B.frag(L, fs[k] * U + u, n), f, G[k][u]);
@@ -284,6 +285,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
             asm volatile("" : "+v"(i));                    // (what follows from it is made again, not kept in masks)
 #pragma unroll
             for (int v = 0; v < KS; ++v) {
+              if (past<T, kBV>(v * M::KB, P - p0)) break;
               const u32x4 f = L.frag(Yp, ft[k], v);
 #pragma unroll
               for (int u = 0; u < U; ++u) V[k][u] = M::mma(L.frag(Xp, fs[k] * U + u, v), f, V[k][u]);
@@ -311,12 +313,13 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
         }
         phase();
         // S^T dO (dS^T x), four independent sums
-        {
+        if (!past<T, kBV>(n0 + nt * 16, N)) {
           f32x4 o[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
+            if (past<T, kBV>(s * M::KB, P - p0)) break;
             u32x4 f[SP], b[4];
 #pragma unroll
             for (int z = 0; z < SP; ++z) f[z] = L.cols(state + z * Z::kS, nt, s);
@@ -337,12 +340,14 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
         // dS B
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
+          if (past<T, kBV>(n0 + s * M::KB, N)) break;
           const u32x4 b = B.frag(L, dtile, nb * KS + s);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
+            if (!past<T, kBV>((dblock + k) * 16, P - p0))
 #pragma unroll
-            for (int z = (SP > 1 ? 1 : 0); z >= 0; --z)
-              du[k] = M::mma(L.frag(Dp + z * Z::kS, dblock + k, s), b, du[k]);
+              for (int z = (SP > 1 ? 1 : 0); z >= 0; --z)
+                du[k] = M::mma(L.frag(Dp + z * Z::kS, dblock + k, s), b, du[k]);
         }
         __syncthreads();                                     // the planes have been read, (C B^T exp) is there
       }
@@ -359,6 +364,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
           if constexpr (M::kSplit) lo = L.cols_row(Mp + Z::kM, dtile, s);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
+            if (past<T, kBV>((dblock + k) * 16, P - p0)) continue;
             const u32x4 o = L.cols_row(Yp, dblock + k, s);
             if constexpr (M::kSplit) du[k] = M::mma(o, lo, du[k]);
             du[k] = M::mma(o, hi, du[k]);
