@@ -372,6 +372,8 @@ struct ScanGradArgs {
   float *S, *dS, *part;
   KeptGates* gates;
   char* sums;
+  float* shares;                       // of dB and dC, where a group's heads are dealt to several workgroups
+  int parts, heads;                    // workgroups of a chunk and group, heads of each
 };
 template <typename T>
 size_t scan_grad_workspace_bytes(const ScanArgs& a);

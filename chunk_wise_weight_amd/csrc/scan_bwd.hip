@@ -147,7 +147,8 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   __shared__ TokenSums<T> sums;
   const ScanArgs& p = a.f;
   const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int grp = id % p.G, slot = id / p.G, shared = p.H / p.G, head0 = grp * shared;
+  const int share = id % a.parts, grp = id / a.parts % p.G, slot = id / a.parts / p.G, shared = p.H / p.G;
+  const int head0 = grp * shared + share * a.heads, last = min(head0 + a.heads, (grp + 1) * shared);
   const ChunkPlace c = chunk_place(p.seqs, slot);
   if (c.len <= 0) return;
   const int tid = threadIdx.x, wave = wave_id(), side = wave >> 2, nt = wave & 3, lane = lane_id(), m = lane & 15, g = lane >> 4;
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   const Split<T> split(lane);
   char *const Sp = smem + Z::oS, *const Dp = Sp + SP * Z::kS, *const Mp = smem + Z::oM;
 
-  // Heads of the group, from the first on.
+  // The workgroup's heads of the group, from the first on.
   const float *S = a.S + ((int64_t)slot * p.H + head0) * size, *dS = a.dS + ((int64_t)slot * p.H + head0) * size;
   const T* x = (const T*)p.x + c.b * p.sx.b + head0 * p.sx.h + c.tok0 * p.sx.t;
   const T* y = (const T*)a.dO + c.b * a.sdO.b + head0 * a.sdO.h + c.tok0 * a.sdO.t;
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
   const char *const state = side ? Dp : Sp;
   const Features<T, LDS> own = side ? B : C, cross = side ? C : B;
 
-  for (int h = head0; h < head0 + shared; ++h) {
+  for (int h = head0; h < last; ++h) {
     const float D = p.D ? p.D[h] : 0.f;
     const KeptGates& gate = *reinterpret_cast<const KeptGates*>(kept[hturn]);
     const Gates& q = gate.g;
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
       for (int u = 0; u < U; ++u) V[k][u] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float ss = 0.f, dot[4] = {0.f, 0.f, 0.f, 0.f};           // <S, dS>; C_i . S^T dO_i or B_j . dS^T x_j
     for (int p0 = 0; p0 < P; p0 += kBV) {
-      const bool more = p0 + kBV < P, next = more || h + 1 < head0 + shared;
+      const bool more = p0 + kBV < P, next = more || h + 1 < last;
       char *const Xp = smem + Z::oX + turn * 2 * Z::kX, *const Yp = Xp + Z::kX;
       const char* const other = side ? Xp : Yp;
       f32x4 du[2];
@@ -472,6 +473,17 @@ __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
     dx += a.sdx.h;
     __syncthreads();                                         // W and the sums have been read
   }
+  if (a.parts > 1) {
+    float* out = a.shares + (((int64_t)id * 2 + side) * kDC) * N;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int i = M::row(t, m), col = n * kBN + nt * 16 + 4 * g;
+        if (i < len && col < N) *reinterpret_cast<f32x4*>(out + i * N + col) = acc[n][t];
+      }
+    return;
+  }
   T* out = side ? (T*)a.dB + c.b * a.sdB.b + grp * a.sdB.h + c.tok0 * a.sdB.t
                 : (T*)a.dC + c.b * a.sdC.b + grp * a.sdC.h + c.tok0 * a.sdC.t;
   const int64_t pitch = side ? a.sdB.t : a.sdC.t;
@@ -567,19 +579,43 @@ __global__ __launch_bounds__(256) void k_scan_grad_sum(const float* __restrict__
   }
 }
 
+// dB and dC of a chunk and group from its workgroups' shares, in their order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_scan_share_sum(ScanGradArgs a) {
+  const ScanArgs& p = a.f;
+  const int side = blockIdx.x & 1, unit = blockIdx.x >> 1, grp = unit % p.G, slot = unit / p.G, N = p.N;
+  const ChunkPlace c = chunk_place(p.seqs, slot);
+  T* out = side ? (T*)a.dB + c.b * a.sdB.b + grp * a.sdB.h + c.tok0 * a.sdB.t
+                : (T*)a.dC + c.b * a.sdC.b + grp * a.sdC.h + c.tok0 * a.sdC.t;
+  const int64_t pitch = side ? a.sdB.t : a.sdC.t;
+  const float* in = a.shares + (((int64_t)unit * a.parts * 2 + side) * kDC) * N;
+  for (int e = threadIdx.x * 4; e < c.len * N; e += 1024) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < a.parts; ++k) v += *reinterpret_cast<const f32x4*>(in + (int64_t)k * 2 * kDC * N + e);
+    store4(out + e / N * pitch + e % N, v[0], v[1], v[2], v[3]);
+  }
+}
+
 template <typename T, int DN, bool LDS>
 hipError_t launch_grads(const ScanGradArgs& a, int64_t chunks, hipStream_t s) {
   using Z = GradShape<T, DN, LDS>;
   static_assert(Z::kSmem + 11 * 1024 <= kMaxLds, "LDS");
-  k_scan_grads<T, DN, LDS><<<dim3((unsigned)(chunks * a.f.G)), 512, Z::kSmem, s>>>(a);
+  k_scan_grads<T, DN, LDS><<<dim3((unsigned)(chunks * a.f.G * a.parts)), 512, Z::kSmem, s>>>(a);
+  if (a.parts > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_scan_share_sum<T><<<dim3((unsigned)(chunks * a.f.G * 2)), 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
 // Regions of the workspace, in bytes, multiples of 16.
 struct GradSpace {
   int seg;
-  int64_t slots, chunks, keep, gates, tokens, sums, decays, part;
-  int64_t total() const { return 2 * keep + gates + tokens + 2 * sums + 2 * decays + part; }
+  int parts, heads;
+  int64_t slots, chunks, keep, gates, tokens, sums, decays, part, shares;
+  int64_t total() const { return 2 * keep + gates + tokens + 2 * sums + 2 * decays + part + shares; }
 };
 template <typename T>
 GradSpace grad_space(const ScanArgs& a) {
@@ -595,6 +631,14 @@ GradSpace grad_space(const ScanArgs& a) {
   g.sums = cut ? g.slots * a.H * a.P * a.N * 4 : 0;
   g.decays = cut ? (g.slots * a.H * 4 + 15) / 16 * 16 : 0;
   g.part = g.chunks * a.H * 16;
+  // Where the chunks and groups leave half of the CUs idle, the heads of a group are dealt to several workgroups (32 heads of
+  // 64 x 128 in one group, 300 tokens: bf16 241 -> 79 us, fp32 598 -> 100 us; 16 in two, 4,000 tokens: 114 -> 103, 236 -> 187).
+  // Two heads in bf16 are as fast in one (59 us for 63, 5 sequences of 1,177 tokens; fp32 91, 84 us).
+  const int64_t units = std::max<int64_t>(g.chunks * a.G, 1), shared = a.H / a.G;
+  const int64_t parts = shared > 2 || sizeof(T) == 4 ? std::max<int64_t>(std::min(shared, 256 / units), 1) : 1;
+  g.heads = (int)((shared + parts - 1) / parts);
+  g.parts = (int)((shared + g.heads - 1) / g.heads);
+  g.shares = g.parts > 1 ? g.chunks * a.G * g.parts * 2 * kDC * a.N * 4 : 0;
   return g;
 }
 
@@ -627,6 +671,9 @@ hipError_t launch_scan_grad(const ScanGradArgs& in, hipStream_t s) {
   StateWalk two{a.dO, f.C, a.sdO, f.sC, a.dS_final, a.dS_init, cut ? (float*)take(g.sums) : nullptr,
                 cut ? (float*)take(g.decays) : nullptr, a.dS, nullptr, true};
   a.part = (float*)take(g.part);
+  a.shares = (float*)take(g.shares);
+  a.parts = g.parts;
+  a.heads = g.heads;
   const int64_t join = sequences * f.H * (((int64_t)f.P * f.N / 4 + 255) / 256);
   if (sequences > 0) {
     hipError_t e = with_scan<T>(f.P, f.N, f.H / f.G, [&](auto dn, auto hw, auto pw) {
