@@ -631,13 +631,23 @@ GradSpace grad_space(const ScanArgs& a) {
   g.sums = cut ? g.slots * a.H * a.P * a.N * 4 : 0;
   g.decays = cut ? (g.slots * a.H * 4 + 15) / 16 * 16 : 0;
   g.part = g.chunks * a.H * 16;
-  // Where the chunks and groups leave half of the CUs idle, the heads of a group are dealt to several workgroups (32 heads of
-  // 64 x 128 in one group, 300 tokens: bf16 241 -> 79 us, fp32 598 -> 100 us; 16 in two, 4,000 tokens: 114 -> 103, 236 -> 187).
-  // Two heads in bf16 are as fast in one (59 us for 63, 5 sequences of 1,177 tokens; fp32 91, 84 us).
-  const int64_t units = std::max<int64_t>(g.chunks * a.G, 1), shared = a.H / a.G;
-  const int64_t parts = shared > 2 || sizeof(T) == 4 ? std::max<int64_t>(std::min(shared, 256 / units), 1) : 1;
-  g.heads = (int)((shared + parts - 1) / parts);
-  g.parts = (int)((shared + g.heads - 1) / g.heads);
+  // The heads of a group are dealt to as many workgroups as take least, by rounds of one a CU: `once` heads' time for what
+  // each does once, `join` for the sum of the shares (fitted).  32 heads of 64 x 128 in one group, 300 tokens: bf16 241 -> 79
+  // us, fp32 598 -> 100 us; 16 in two, 4,000 tokens: 114 -> 102, 236 -> 185; 64 in eight, 3,000 tokens, two workgroups for one:
+  // bf16 223 -> 231 (not taken), fp32 524 -> 492.
+  const double once = sizeof(T) == 2 ? 1.5 : 0.5, join = sizeof(T) == 2 ? 2.5 : 0.5;
+  const int64_t units = std::max<int64_t>(g.chunks * a.G, 1);
+  const int shared = a.H / a.G;
+  double least = 0.0;
+  for (int parts = 1; parts <= shared && (parts == 1 || units * parts <= 1024); ++parts) {   // shares of 512 KB N at most
+    const int heads = (shared + parts - 1) / parts;
+    const double cost = (double)((units * parts + 255) / 256) * (heads + once) + (parts > 1 ? join : 0.0);
+    if (parts == 1 || cost < least) {
+      least = cost;
+      g.heads = heads;
+      g.parts = (shared + heads - 1) / heads;
+    }
+  }
   g.shares = g.parts > 1 ? g.chunks * a.G * g.parts * 2 * kDC * a.N * 4 : 0;
   return g;
 }

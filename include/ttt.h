@@ -1033,7 +1033,7 @@ typedef struct {
 /* Workspace of ttt_selective_scan_backward; num_seqs < 0: not packed.  The
  * limits in ttt_scan_shape are half as high (2^22 and 2^23), else
  * TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + some 8 KB, for each
- * segment and head 8 P N + 8, and up to 128 KB N for the shares of dB and dC. */
+ * segment and head 8 P N + 8, and up to 512 KB N for the shares of dB and dC. */
 int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
 
 /* The backward of ttt_selective_scan, from the forward call's inputs alone
