@@ -127,7 +127,8 @@ template <typename T> struct TokenSums {
   float diag[2][kDC], dots[8][kDC], ss[8], pad[8];
 };
 
-// One workgroup of 8 waves per chunk slot and group, its heads one after the other.
+// One workgroup of 8 waves per chunk slot and group, its heads one after the other; where several share them, each leaves its
+// fp32 part of dB and dC.
 //   waves 0-3  S^T dO and dC, waves 4-7  dS^T x and dB: block w & 3 of every 64 features of N, all tokens
 //   du         blocks 2 (w & 1) and the next of P, tokens row(w >> 1, .)
 //   C B^T, dO x^T and their decayed forms by fragments, a wave one (fp32: two); they go to LDS once for all waves
