@@ -1135,21 +1135,29 @@ def ttt_rms_norm(x, weight=None, residual=None, eps=1e-5, out_dtype=None, group=
     _norm_vector(weight, "weight", d, dt, dev)
     if residual is not None:
         _need(residual, "residual", shape, dt, dev)
-        H = torch.empty_like(x) if H is None else H
-        _need(H, "H", shape, dt, dev)
+        if H is None:
+            H = torch.empty_like(x)
+        else:
+            _need(H, "H", shape, dt, dev)
     bits8 = out_dtype is not None and out_dtype != dt
     if bits8 and out_dtype != torch.float8_e4m3fn:
         raise TypeError(f"out_dtype must be {dt} or float8_e4m3fn, got {out_dtype}")
     if group is not None and (not bits8 or group not in (32, 64, 128)):
         raise ValueError(f"group must be 32, 64 or 128, and is of 8-bit outputs, got {group}")
-    Y = torch.empty(shape, dtype=out_dtype if bits8 else dt, device=dev) if Y is None else Y
-    _need(Y, "Y", shape, out_dtype if bits8 else dt, dev)
-    rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else rstd
-    _need(rstd, "rstd", lead, torch.float32, dev)
+    if Y is None:
+        Y = torch.empty_like(x, dtype=out_dtype) if bits8 else torch.empty_like(x)
+    else:
+        _need(Y, "Y", shape, out_dtype if bits8 else dt, dev)
+    if rstd is None:
+        rstd = x.new_empty(lead, dtype=torch.float32)
+    else:
+        _need(rstd, "rstd", lead, torch.float32, dev)
     if bits8:
         scales = lead if group is None else (*lead, -(-d // group))
-        scale = torch.empty(scales, dtype=torch.float32, device=dev) if scale is None else scale
-        _need(scale, "scale", scales, torch.float32, dev)
+        if scale is None:
+            scale = x.new_empty(scales, dtype=torch.float32)
+        else:
+            _need(scale, "scale", scales, torch.float32, dev)
     elif scale is not None:
         raise ValueError("scale is of 8-bit outputs")
     _launch(dev, "ttt_rms_norm", lib().ttt_rms_norm, rstd.numel(), d, _dt(dt), float(eps), _at(x), _at(residual),
@@ -1177,11 +1185,14 @@ def ttt_rms_norm_backward(H, weight, dY, rstd, dH=None, dx=None, dweight=None, w
     _need(rstd, "rstd", lead, torch.float32, dev)
     if dH is not None:
         _need(dH, "dH", shape, dt, dev)
-    dx = torch.empty_like(H) if dx is None else dx
-    _need(dx, "dx", shape, dt, dev)
-    if weight is not None and dweight is None:
-        dweight = torch.empty(d, dtype=torch.float32, device=dev)
-    _norm_vector(dweight, "dweight", d, torch.float32, dev)
+    if dx is None:
+        dx = torch.empty_like(H)
+    else:
+        _need(dx, "dx", shape, dt, dev)
+    if dweight is not None:
+        _need(dweight, "dweight", (d,), torch.float32, dev)
+    elif weight is not None:
+        dweight = weight.new_empty(d, dtype=torch.float32)
     rows = rstd.numel()
     nbytes = ttt_rms_norm_backward_workspace_bytes(rows, d, dt)
     ws = _workspace(nbytes, dev, workspace)
