@@ -1250,13 +1250,15 @@ def ttt_short_conv(x, conv_w, bias=None, silu=True, x_init=None, seq_starts=None
     dev, dt = x.device, x.dtype
     _conv_vectors(conv_w, bias, x.shape[-1], dt, dev)
     num = _seq_starts(seq_starts, x.shape[0], dev)
-    Y = torch.empty(x.shape, dtype=dt, device=dev) if Y is None else Y
+    Y = x.new_empty(x.shape) if Y is None else Y
     shape, code, layout, halo = _conv_plan(_meta(x, "x", dev, False), _meta(conv_w, "conv_w", dev, False),
                                            _meta(Y, "Y", dev, False), num)
     if x_init is not None:
         _need(x_init, "x_init", halo, dt, dev)
-    x_final = torch.empty(halo, dtype=dt, device=dev) if x_final is None else x_final
-    _need(x_final, "x_final", halo, dt, dev)
+    if x_final is None:
+        x_final = x.new_empty(halo)
+    else:
+        _need(x_final, "x_final", halo, dt, dev)
     opts = ConvOptions(_at(bias), bool(silu), _at(x_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
     _launch(dev, "ttt_short_conv", lib().ttt_short_conv, shape, code, _at(x), _at(conv_w), ctypes.byref(opts), _at(Y),
             _at(x_final))
@@ -1287,7 +1289,7 @@ def ttt_short_conv_backward(x, conv_w, dY, bias=None, silu=True, x_init=None, se
     dev, dt = x.device, x.dtype
     _conv_vectors(conv_w, bias, x.shape[-1], dt, dev)
     num = _seq_starts(seq_starts, x.shape[0], dev)
-    dx = torch.empty(x.shape, dtype=dt, device=dev) if dx is None else dx
+    dx = x.new_empty(x.shape) if dx is None else dx
     shape, code, layout, grads, nbytes, halo = _conv_backward_plan(
         _meta(x, "x", dev, False), _meta(conv_w, "conv_w", dev, False), _meta(dY, "dY", dev, False),
         _meta(dx, "dx", dev, False), num)
@@ -1296,11 +1298,14 @@ def ttt_short_conv_backward(x, conv_w, dY, bias=None, silu=True, x_init=None, se
     for t, name in ((x_init, "x_init"), (dx_final, "dx_final"), (dx_init, "dx_init")):
         if t is not None:
             _need(t, name, halo, dt, dev)
-    dconv_w = torch.empty(conv_w.shape, dtype=torch.float32, device=dev) if dconv_w is None else dconv_w
-    _need(dconv_w, "dconv_w", conv_w.shape, torch.float32, dev)
-    if bias is not None and dbias is None:
-        dbias = torch.empty(bias.shape, dtype=torch.float32, device=dev)
-    _norm_vector(dbias, "dbias", x.shape[-1], torch.float32, dev)
+    if dconv_w is None:
+        dconv_w = conv_w.new_empty(conv_w.shape, dtype=torch.float32)
+    else:
+        _need(dconv_w, "dconv_w", conv_w.shape, torch.float32, dev)
+    if dbias is not None:
+        _need(dbias, "dbias", (x.shape[-1],), torch.float32, dev)
+    elif bias is not None:
+        dbias = bias.new_empty(bias.shape, dtype=torch.float32)
     ws = _workspace(nbytes, dev, workspace)
     opts = ConvOptions(_at(bias), bool(silu), _at(x_init), _at(seq_starts), max(num, 0), ctypes.pointer(layout))
     _launch(dev, "ttt_short_conv_backward", lib().ttt_short_conv_backward, shape, code, _at(x), _at(conv_w), _at(dY),
@@ -1383,9 +1388,11 @@ def ttt_selective_scan(x, dt, A, B, C, D=None, dt_bias=None, softplus=False, S_i
     shape, code, layout, nbytes, states = _scan_plan(*metas, _meta(O, "O", dev), num)
     if S_init is not None:
         _need(S_init, "S_init", states, torch.float32, dev)
-    S_final = torch.empty(states, dtype=torch.float32, device=dev) if S_final is None else S_final
-    _need(S_final, "S_final", states, torch.float32, dev)
-    ws = _workspace(nbytes, dev, workspace)
+    if S_final is None:
+        S_final = A.new_empty(states)
+    else:
+        _need(S_final, "S_final", states, torch.float32, dev)
+    ws = _workspace(nbytes, dev, workspace) if nbytes else None
     opts = ScanOptions(_at(D), _at(dt_bias), bool(softplus), _at(S_init), _at(seq_starts), max(num, 0),
                        ctypes.pointer(layout))
     _launch(dev, "ttt_selective_scan", lib().ttt_selective_scan, shape, code, _at(x), _at(dt), _at(A), _at(B), _at(C),
