@@ -441,7 +441,7 @@ def run(state):
             return {"dx": dx, "dweight": dweight}
         Y, H, _, scale = cw.ttt_rms_norm(s["x"], s["weight"], s["residual"], eps=EPS,
                                          out_dtype=torch.float8_e4m3fn if case["bits8"] else None, group=case["group"] or None)
-        return {**({"H": H} if case["residual"] else {}), "Y": Y, **({"scale": scale.view(case["rows"], -1)} if case["bits8"] else {})}
+        return {**({"H": H} if case["residual"] else {}), "Y": Y, **({"scale": scale} if case["bits8"] else {})}
     if op == "conv":
         if case["pass"] == "step":
             Y = cw.ttt_short_conv_step(s["x"], s["w"], s["halo"], s["bias"], silu=case["silu"], slots=s["slots"])
