@@ -1015,10 +1015,12 @@ int ttt_selective_scan_workspace_bytes(const ttt_scan_shape* shape, int dtype, i
  *   S_final   [sequences, H, P, N] fp32 (written)  sequences = B, or num_seqs
  * A log decay A r_t below -104, whose decay rounds to zero, empties the state:
  * a document boundary inside a sequence; at a sequence's first token S_init's
- * values are not looked at.  A rate of 0 leaves the state as it
- * is.  All inputs of tokens that belong to a sequence have to be finite: one
- * that is not leaves every output of its sequence undefined (x and dt: of its
- * head), none of other sequences.  With bf16 inputs the state is summed from
+ * values are not looked at.  A rate of 0, as the softplus of dt + dt_bias below
+ * -104 (a mask of the lowest value, too), leaves the state as it is.  All inputs
+ * of tokens that belong to a sequence have to be finite, and their products
+ * r_t x_t and r_t (C_i . B_t) in the range of fp32: one that is not leaves every
+ * output of its sequence undefined (x and dt: of its head), none of other
+ * sequences.  With bf16 inputs the state is summed from
  * products kept to 2^-24, and O is off by its own rounding.  seq_len == 0 or an
  * empty sequence: S_final is S_init (or zero). */
 int ttt_selective_scan(const ttt_scan_shape* shape, int dtype, const void* x, const float* dt, const float* A,
