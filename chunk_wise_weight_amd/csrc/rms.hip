@@ -1,14 +1,15 @@
 // Root-mean-square norm of x + residual, forward (in 8 bits too) and backward, for gfx950.
 //
 //   forward   h = x + residual, rounded to their type,  y = h r w,  r = 1 / sqrt(mean(h^2) + eps)
-//   in 8 bits q = e4m3(y / s),  s = max(max |y| / 448, 2^-126) over the row or a group of its columns
+//   in 8 bits q = e4m3(y / s),  s = max(max |y| / 448, 2^-126) over the row or a group of its columns (y / s as a division
+//             rounds it: y times 1 / s falls on the other side of a border between two codes once in 10^5)
 //   backward  n = h r, a = dY w:  dx = r (a - n mean(a n)) + dH,  dw = sum_rows dY n
 //
 // Rows lie in registers as in the layer norm (norm.hip): read once, summed, written once, bound by HBM.  Sums,
 // scales and y are fp32; h is rounded before it is squared, so that the norm is of the sum as it is kept and the
 // backward pass, which reads it, has the same n.  A group's largest |y| is found among the few lanes that hold its
-// columns, a row's among all of its threads.  131,072 x 2560 with residual, bf16 to e4m3 with 128 columns a scale: 425 us,
-// 5.6 TB/s; backward of 4,099 x 1001 in fp32 with dH: 16 us, 4.1 TB/s.
+// columns, a row's among all of its threads.  131,072 x 2560 with residual, bf16 to e4m3 with 128 columns a scale: 433 us,
+// 5.5 TB/s; backward of 4,099 x 1001 in fp32 with dH: 16 us, 4.1 TB/s.
 #include "launch.hpp"
 #include "norm.hpp"
 
@@ -16,6 +17,9 @@ namespace ttt {
 namespace {
 
 constexpr float kE4m3Max = 448.f, kMinScale = 0x1p-126f;
+// From this scale on the remainder of a quotient that e4m3 tells from zero (2^-10 and more, 2^-24 of that left) is no
+// subnormal.
+constexpr float kFullScale = 0x1p-90f;
 
 // The largest of v over the threads of a row, given to all of them; `red` and `turn` as for row_sum.
 template <int TPR>
@@ -63,9 +67,11 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, int left)
   }
 }
 
-// lanes: those that hold a group of columns (a power of two), 0: the scale is the row's.
+// lanes: those that hold a group of columns (a power of two), 0: the scale is the row's.  Four waves a SIMD
+// for rows of up to 5 vectors a thread (bf16 to e4m3, 131,072 x 2560: 433 us with 4 of 130 registers spilled, 443 with three
+// waves and none).
 template <typename T, bool RAG, int TPR, int NV, bool OUT8, bool STREAM>
-__global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
+__global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads, NV <= 5 ? 4 : 1) void k_rms(
     const T* __restrict__ x, const T* __restrict__ res, const T* __restrict__ weight, T* __restrict__ ho,
     void* __restrict__ yo, float* __restrict__ rstd, float* __restrict__ scale, int64_t rows, int d, float eps, int lanes) {
   constexpr int VEC = Vec<T>::V;
@@ -148,8 +154,17 @@ __global__ __launch_bounds__(TPR == 0 ? 1024 : kNormThreads) void k_rms(
         const float sc = fmaxf(a / kE4m3Max, kMinScale), inv = 1.0f / sc;
         if (e < d) {
           if (lanes ? t % lanes == 0 : i == 0 && t == 0) scale[row * groups + (lanes ? e / cols : 0)] = sc;
+          // y / sc as a division rounds it: what y inv leaves of y, times inv, puts it right
+          if (sc >= kFullScale) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
+            for (int j = 0; j < VEC; ++j) {
+              const float q = v[i][j] * inv;
+              v[i][j] = fmaf(fmaf(-q, sc, v[i][j]), inv, q);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[i][j] /= sc;
+          }
           store_e4m3<VEC, RAG, STREAM>((uint8_t*)yo + row * d + e, v[i], d - e);
         }
       }

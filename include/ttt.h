@@ -866,8 +866,9 @@ int ttt_layer_norm_backward(int64_t rows, int64_t dim, int dtype, const void* x,
  *                largest |h rstd weight| of the row (group 0: one scale a row)
  *                or of each `group` (32, 64 or 128) of its columns, divided
  *                by 448, at least 2^-126
- *     y          [rows, dim]  e4m3 (written): h rstd weight / scale, rounded to
- *                nearest even
+ *     y          [rows, dim]  e4m3 (written): h rstd weight / scale, each
+ *                operation rounded to fp32, the quotient to the nearest e4m3
+ *                value (ties to even)
  * dim <= 65536 (else TTT_ERR_UNSUPPORTED); eps finite and not negative; other
  * groups, or a group without scale: TTT_ERR_ARG.  Where dim is no multiple of
  * 16 bytes the tensors need their elements' alignment only.  A row that holds
