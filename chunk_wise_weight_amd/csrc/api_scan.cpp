@@ -368,7 +368,7 @@ int ttt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t dim, int dtype, 
   if (bytes == nullptr) return TTT_ERR_ARG;
   if (int st = check_norm(rows, dim, dtype)) return st;
   const int G = dtype == TTT_BF16 ? ttt::rms_grad_blocks<bf16>(rows, (int)dim) : ttt::rms_grad_blocks<float>(rows, (int)dim);
-  *bytes = (size_t)G * dim * sizeof(float);
+  *bytes = (size_t)G * dim * sizeof(double);
   return TTT_OK;
 }
 
@@ -381,7 +381,7 @@ int ttt_rms_norm_backward(int64_t rows, int64_t dim, int dtype, const void* h, c
   if (rows > 0 && (!ok_ptr(h, al) || !ok_ptr(dy, al) || !ok_ptr(dx, al) || !ok_ptr(rstd, 4))) return TTT_ERR_ARG;
   if (!aligned(weight, al) || !aligned(dh, al) || !aligned(dweight, 4)) return TTT_ERR_ARG;
   if (need > 0 && (!ok_ptr(workspace) || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
-  ttt::RmsGradArgs a{rows, (int)dim, h, weight, dy, dh, rstd, dx, dweight, (float*)workspace};
+  ttt::RmsGradArgs a{rows, (int)dim, h, weight, dy, dh, rstd, dx, dweight, (double*)workspace};
   hipStream_t s = (hipStream_t)stream;
   return dev(dtype == TTT_BF16 ? ttt::launch_rms_grad<bf16>(a, s) : ttt::launch_rms_grad<float>(a, s));
 }

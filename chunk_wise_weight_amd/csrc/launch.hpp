@@ -294,7 +294,8 @@ struct RmsGradArgs {
   const void *h, *weight, *dy, *dh;    // weight, dh or null
   const float* rstd;
   void* dx;
-  float *dweight, *part;               // dweight or null; part [blocks, d]
+  float* dweight;                      // or null
+  double* part;                        // [blocks, d]
 };
 template <typename T>
 int rms_grad_blocks(int64_t rows, int d);

@@ -257,7 +257,7 @@ hipError_t launch_norm_grad(const T* x, const T* w, const T* dy, const float* me
     if (e != hipSuccess) return e;
   }
   if (dw == nullptr && db == nullptr) return hipSuccess;
-  k_norm_grad_sum<<<dim3((unsigned)((d + 15) / 16), 2), 1024, 0, s>>>(part, G, d, dw, db);
+  k_norm_grad_sum<float><<<dim3((unsigned)((d + 15) / 16), 2), 1024, 0, s>>>(part, G, d, dw, db);
   return hipGetLastError();
 }
 

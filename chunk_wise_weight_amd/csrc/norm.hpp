@@ -102,17 +102,18 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& turn) {
   }
 }
 
-// dw[c], db[c] = the sums of part[0..G)[.][c] (gridDim.y 1: dw alone): a workgroup
+// dw[c], db[c] = the sums, of type S, of part[0..G)[.][c] (gridDim.y 1: dw alone): a workgroup
 // takes 16 columns of one of the two, its 64 rows of threads every 64th block each (narrow columns
 // of many rows, so that few blocks' sums are read one after the other also
 // where d is small), joined in LDS in a fixed order.
-__global__ __launch_bounds__(1024) void k_norm_grad_sum(const float* __restrict__ part, int G, int d,
+template <typename S>
+__global__ __launch_bounds__(1024) void k_norm_grad_sum(const S* __restrict__ part, int G, int d,
                                                         float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sum[64][16];
+  __shared__ S sum[64][16];
   const int j = threadIdx.x & 15, k = threadIdx.x >> 4, c = blockIdx.x * 16 + j, q = blockIdx.y;
   float* out = q == 0 ? dw : db;
   if (out == nullptr) return;
-  float a = 0.f;
+  S a = 0;
   if (c < d) {
 #pragma unroll 4
     for (int g = k; g < G; g += 64) a += part[((int64_t)g * gridDim.y + q) * d + c];
@@ -120,10 +121,10 @@ __global__ __launch_bounds__(1024) void k_norm_grad_sum(const float* __restrict_
   sum[k][j] = a;
   __syncthreads();
   if (k == 0 && c < d) {
-    a = 0.f;
+    a = 0;
 #pragma unroll
     for (int i = 0; i < 64; ++i) a += sum[i][j];
-    out[c] = a;
+    out[c] = (float)a;
   }
 }
 
