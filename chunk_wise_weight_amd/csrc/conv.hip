@@ -175,7 +175,9 @@ __device__ __forceinline__ float conv_dz(float z, float g, bool silu) {
 // Channels of a thread: 8 of bf16 would take more than half of the registers, for one wave a SIMD.
 constexpr int kGradVec = 4;
 
-// The taps' and the bias's gradient of a workgroup's runs goes to part[][K + 1][d].
+// The taps' and the bias's gradient of a workgroup's runs goes to part[][K + 1][d].  Over a run's tokens, 64 at most, it is
+// summed in fp32 (fp64 would take K + 1 registers more a channel, for two waves a SIMD), over runs in fp64 but for lanes
+// side by side and the rounding of a workgroup's.
 template <typename T, bool RAG, int K>
 __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, ConvPlan p) {
   constexpr int VEC = kGradVec;
@@ -351,21 +353,21 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
   float* part = g.part + (int64_t)(blockIdx.x / p.blocks_c) * (K + 1) * d;
   for (int i = threadIdx.x; i < (K + 1) * cv * VEC; i += kConvThreads) {
     const int k = i / (cv * VEC), c = i % (cv * VEC);
-    float v = 0.f;
+    double v = 0.0;
 #pragma unroll
     for (int r = 0; r < kConvThreads / 64; ++r) v += red[r][k][c / VEC][c % VEC];
-    if (c0 + c < d) part[(int64_t)k * d + c0 + c] = v;
+    if (c0 + c < d) part[(int64_t)k * d + c0 + c] = (float)v;
   }
 }
 
-// dw[c][k] and dbias[c]: the parts in a fixed order, 16 channels of a tap a workgroup, each of its 64 rows of threads
+// dw[c][k] and dbias[c]: the parts' sums in fp64 in a fixed order, 16 channels of a tap a workgroup, each of its 64 rows of threads
 // every 64th part, joined in LDS.
 __global__ __launch_bounds__(1024) void k_conv_sum(const float* __restrict__ part, int64_t parts, int d, int K,
                                                    float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sum[64][17];
+  __shared__ double sum[64][17];
   const int j = threadIdx.x & 15, r = threadIdx.x >> 4, c = blockIdx.x * 16 + j, k = blockIdx.y;
   if (k == K && db == nullptr) return;
-  float s = 0.f;
+  double s = 0.0;
   if (c < d) {
 #pragma unroll 4
     for (int64_t g = r; g < parts; g += 64) s += part[(g * (K + 1) + k) * d + c];
@@ -373,13 +375,13 @@ __global__ __launch_bounds__(1024) void k_conv_sum(const float* __restrict__ par
   sum[r][j] = s;
   __syncthreads();
   if (r == 0 && c < d) {
-    s = 0.f;
+    s = 0.0;
 #pragma unroll
     for (int i = 0; i < 64; ++i) s += sum[i][j];
     if (k < K)
-      dw[(int64_t)c * K + k] = s;
+      dw[(int64_t)c * K + k] = (float)s;
     else
-      db[c] = s;
+      db[c] = (float)s;
   }
 }
 
