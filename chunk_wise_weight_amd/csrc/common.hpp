@@ -78,4 +78,13 @@ __device__ __forceinline__ void unpack8(u32x4 w, float* o) {
 __device__ __forceinline__ float sigmoid_f(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 __device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }
 
+// exp(x), x <= 0: 2^(x log2 e) by the hardware's power of two, the product's rounding put right to first order (off by some
+// 2^-23 also far from zero, where the rounded product alone would be off by |x| 2^-24).  What is below -128, exp of which is
+// zero in fp32, is taken as that: the product of the lowest values is not finite, and what puts it right with it.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = x < -128.f ? -128.f : x;          // (NaN stays)
+  const float p = x * 1.44269502f, e = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -p));
+  return __builtin_amdgcn_exp2f(p) * fmaf(e, 0.693147181f, 1.f);
+}
+
 }  // namespace ttt

@@ -16,6 +16,22 @@ namespace {
 
 constexpr int kConvThreads = 256;
 
+// p = 1 / (1 + exp(-z)) and q = 1 - p.  fp32: both from exp(-|z|) and a reciprocal put right by one step of Newton's, off by
+// some 2^-22 of themselves also far from zero; the hardware's own, which bf16 takes, are off by |z| 2^-24 and more (2^-18 at
+// 60), far below its rounding.
+struct Sigmoid {
+  float p, q;
+};
+template <typename T> __device__ __forceinline__ Sigmoid sigmoid_of(float z) {
+  if constexpr (sizeof(T) == 2) {
+    const float p = sigmoid_f(z);
+    return {p, 1.f - p};
+  } else {
+    const float t = exp_neg(-fabsf(z)), d = 1.f + t, r0 = __builtin_amdgcn_rcpf(d), r = fmaf(fmaf(-d, r0, 1.f), r0, r0);
+    return z >= 0.f ? Sigmoid{r, t * r} : Sigmoid{t * r, r};
+  }
+}
+
 // Which channels and which run (or sequence) a thread has: cv threads in a row along the channels, a wave at most,
 // the rest along the runs.
 struct ConvPlace {
@@ -154,7 +170,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, ConvPlan p) {
             float z = bias[j];
 #pragma unroll
             for (int k = 0; k < K; ++k) z += tap[k][j] * win[(u + 1 + k) % K][j];
-            o[j] = a.silu ? silu_f(z) : z;
+            o[j] = a.silu ? z * sigmoid_of<T>(z).p : z;
           }
           V out;
           narrow(o, out);
@@ -166,10 +182,10 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, ConvPlan p) {
 }
 
 // dz from z and dY.
-__device__ __forceinline__ float conv_dz(float z, float g, bool silu) {
+template <typename T> __device__ __forceinline__ float conv_dz(float z, float g, bool silu) {
   if (!silu) return g;
-  const float p = sigmoid_f(z);
-  return g * (p + z * p * (1.f - p));
+  const Sigmoid s = sigmoid_of<T>(z);
+  return g * (s.p + z * s.p * s.q);
 }
 
 // Channels of a thread: 8 of bf16 would take more than half of the registers, for one wave a SIMD.
@@ -225,7 +241,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
         widen(load_pack<T, VEC, RAG>(dfirst + t * g.sdy.t, d - at.c), dy);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float dz = conv_dz(z[j], dy[j], a.silu);
+          const float dz = conv_dz<T>(z[j], dy[j], a.silu);
 #pragma unroll
           for (int k = 0; k < K - 1; ++k)
             if (t + k < K - 1) o[t + k][j] += tap[k][j] * dz;
@@ -298,7 +314,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
             float z = bias[j];
 #pragma unroll
             for (int k = 0; k < K; ++k) z += tap[k][j] * win[(u + 1 + k) % K][j];
-            dz[j] = conv_dz(z, dy[j], a.silu);
+            dz[j] = conv_dz<T>(z, dy[j], a.silu);
           }
           if (t + u < to) {
 #pragma unroll
@@ -426,7 +442,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_step(ConvStepArgs p) {
       }
       if (p.silu)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = silu_f(o[j]);
+        for (int j = 0; j < VEC; ++j) o[j] *= sigmoid_of<T>(o[j]).p;
       V out;
       narrow(o, out);
       store_pack<T, VEC, RAG>((T*)p.Y + (int64_t)r * d + c, out, d - c);

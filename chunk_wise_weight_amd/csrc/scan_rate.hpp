@@ -4,15 +4,6 @@
 
 namespace ttt {
 
-// exp(x), x <= 0: 2^(x log2 e) by the hardware's power of two, the product's rounding put right to first order (off by some
-// 2^-23 also far from zero, where the rounded product alone would be off by |x| 2^-24).  What is below -128, exp of which is
-// zero in fp32, is taken as that: the product of the lowest values is not finite, and what puts it right with it.
-__device__ __forceinline__ float exp_neg(float x) {
-  x = x < -128.f ? -128.f : x;          // (NaN stays)
-  const float p = x * 1.44269502f, e = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -p));
-  return __builtin_amdgcn_exp2f(p) * fmaf(e, 0.693147181f, 1.f);
-}
-
 // log(1 + t), 0 <= t <= 1, as 2 atanh(t / (2 + t)): s <= 1/3 and powers of s^2 to the 7th leave 2^-26.
 __device__ __forceinline__ float log_1p(float t) {
   const float d = 2.f + t, r = __builtin_amdgcn_rcpf(d), s0 = t * r, s = fmaf(fmaf(-s0, d, t), r, s0), z = s * s;
