@@ -67,7 +67,7 @@ __global__ __launch_bounds__(64 * kStepWaves) void k_scan_step(ScanStepArgs p) {
     float xj[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) xj[i] = j0 + i * RPW < p.P ? to_f32(x[j0 + i * RPW]) : 0.f;
-    const float rate = scan_rate(p.dt[rh], bias, p.softplus), a = __expf(A * rate);
+    const float rate = scan_rate(p.dt[rh], bias, p.softplus), a = exp_neg(A * rate);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       s[i] = a == 0.f ? (f32x4){0.f, 0.f, 0.f, 0.f} : s[i] * a;   // an emptied state also loses what is not finite
