@@ -133,11 +133,12 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
 #pragma unroll
       for (int hd = 0; hd < HW; ++hd) {
         const Gates& q = gates[turn][hd];
+        const bool parts = two_part_gates<T>(q);
 #pragma unroll
         for (int k = 0; k < NF; ++k) {
           if (kDealt && k > 0 && hd % Q != w / E) continue;
           const int i = fi[k];
-          const float bh = q.hi[i], bl = U == 2 ? 0.f : q.lo[i];
+          const float bh = q.hi[i];
           int behind = i - M::row(fs[k] * U, 4 * g);       // tokens of the lane's row of d before i
           asm volatile("" : "+v"(behind));                 // (compared again for every chunk, not kept in masks)
           f32x4 v[U];
@@ -145,12 +146,18 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
           for (int u = 0; u < U; ++u) {
             const int j = M::row(fs[k] * U + u, 4 * g);
             const f32x4 jh = *reinterpret_cast<const f32x4*>(q.hi + j), jr = *reinterpret_cast<const f32x4*>(q.r + j);
-            f32x4 jl;
-            if constexpr (U == 1) jl = *reinterpret_cast<const f32x4*>(q.lo + j);
+            f32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = bh - jh[e];
+            if (parts) {
+              const f32x4 jl = *reinterpret_cast<const f32x4*>(q.lo + j);
+              const float bl = q.lo[i];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] += bl - jl[e];
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = U == 2 ? bh - jh[e] : (bh - jh[e]) + (bl - jl[e]);
-              const float z = d[k][u][e] * exp2_hw(x) * jr[e];
+              const float z = d[k][u][e] * exp2_hw(x[e]) * jr[e];
               v[u][e] = 4 * u + e < behind ? z : 4 * u + e == behind ? z + D[hd] : 0.f;
             }
           }

@@ -223,21 +223,28 @@ __device__ __forceinline__ void two_parts(double b, float* hi, float* lo) {
   *lo = (float)(b - (double)*hi);
 }
 
-// Gates as they lie in LDS: b (fp32 inputs: in two parts), exp(b), the rates, and exp(b_63 - b) r.  One fp32 b is enough
-// for bf16 outputs: sums of 64 are below 2^14, their differences off by 2^-10 at most.
+// Gates as they lie in LDS: b in two parts, exp(b), the rates, and exp(b_63 - b) r.  bf16 outputs take one fp32 b, lo 0, where
+// the chunk's sum stays above kOnePart: differences of two such are off by 2^-16 at most, as the products are.  Sums of 64 reach
+// 2^14 (tokens that empty the state), where one part would be off by 2^-10.
+constexpr double kOnePart = -256.0;
 struct Gates {
   float hi[kDC], lo[kDC], eb[kDC], r[kDC], w[kDC];
 };
 template <typename T> __device__ __forceinline__ void put_gates(const LaneGates& v, Gates* o) {
   const int lane = lane_id();
-  if constexpr (sizeof(T) == 2) {
-    o->hi[lane] = (float)v.b;
-  } else {
-    two_parts(v.b, &o->hi[lane], &o->lo[lane]);
-  }
+  float hi, lo;
+  two_parts(v.b, &hi, &lo);
+  const bool one = sizeof(T) == 2 && v.sum >= kOnePart;
+  o->hi[lane] = one ? (float)v.b : hi;
+  o->lo[lane] = one ? 0.f : lo;
   o->eb[lane] = exp2_hw((float)v.b);
   o->r[lane] = v.r;
   o->w[lane] = v.r * exp2_hw((float)(v.sum - v.b));
+}
+// Whether lo may be other than 0 (hi of the last token is off by 2^-9 at most), the same for all lanes.
+template <typename T> __device__ __forceinline__ bool two_part_gates(const Gates& g) {
+  return sizeof(T) == 4 ||
+         __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(g.hi[kDC - 1]))) < (float)kOnePart + 0.5f;
 }
 // The same as the backward pass keeps them for its chunk-local part, b in two parts, with exp(b_63 - b) and the rate's
 // derivative by dt.
