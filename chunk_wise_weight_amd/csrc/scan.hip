@@ -4,8 +4,8 @@
 namespace ttt {
 namespace {
 
-// The walk over a segment's chunks with outputs.  sums: every slot's and head's [P, N] state before the segment, or
-// null: sequences are one segment.  A chunk's turn:
+// The walk over a segment's chunks with outputs.  sums: every cut's and head's [P, N] state, or null: sequences are one
+// segment.  A chunk's turn:
 //   C B^T by fragments, decayed for each head (D on its diagonal, so that D x comes with the product), to LDS
 //   S C from the state's two parts, then S' with x and B: B and C have been read, the next chunk's come
 //   the decayed C B^T times x, the outputs packed; they are stored in the next turn, behind its barrier, so that no wait
@@ -37,15 +37,15 @@ __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, i
   const int h = at.group * shared + min(at.head0 + hw, shared - 1);
   const int p0 = at.part * Z::cols, tile0 = (p0 >> 4) + pw * CT;
   const bool busy = mine && tile0 * 16 < a.P;              // rows of its state
-  const int64_t sh = (int64_t)at.slot * a.H + h, size = (int64_t)a.P * a.N;
+  const int64_t size = (int64_t)a.P * a.N;
 
   const LaneAt<T> L(lane);
   const Split<T> split(lane);
   StateRows<T, CT, NT> S;
   S.zero();
   if (busy) {
-    if (sums)
-      S.load(sums + sh * size, tile0, a.P, a.N);
+    if (!sp.first)
+      S.load(sums + ((int64_t)(sp.cut - 1) * a.H + h) * size, tile0, a.P, a.N);
     else if (a.S_init)
       S.load(a.S_init + ((int64_t)sp.seq * a.H + h) * size, tile0, a.P, a.N);
   }
@@ -277,7 +277,7 @@ template <typename T>
 size_t scan_workspace_bytes(const ScanArgs& a) {
   const int seg = forward_seg<T>(a);
   if (seg >= a.seqs.n) return 0;
-  const int64_t sh = seg_slots(a.seqs, a.batch, seg) * a.H;
+  const int64_t sh = seg_cuts(a.seqs, a.batch, seg) * a.H;
   return (size_t)sh * a.P * a.N * 4 + (size_t)((sh * 4 + 15) / 16 * 16);
 }
 
@@ -295,7 +295,7 @@ hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
   k.start = a.S_init;
   if (seg < a.seqs.n) {
     k.sums = (float*)a.ws;
-    k.decays = k.sums + slots * a.H * a.P * a.N;
+    k.decays = k.sums + seg_cuts(a.seqs, a.batch, seg) * a.H * a.P * a.N;
   }
   return with_scan<T>(a.P, a.N, a.H / a.G, [&](auto dn, auto hw, auto pw) {
     constexpr int DN = decltype(dn)::value, HW = decltype(hw)::value, PW = decltype(pw)::value;

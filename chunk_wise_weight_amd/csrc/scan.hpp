@@ -20,19 +20,26 @@
 namespace ttt {
 
 // Where a segment slot's tokens lie; len <= 0: the slot has none.  Slots are dealt as the chunks' of delta.hpp, with
-// segments of `seg` tokens in place of 64.
+// segments of `seg` tokens in place of 64.  Cuts between segments are numbered without those between sequences: segment c of
+// a packed sequence that starts at a has a / seg + c behind it, since it has c + 1 segments more of a row's n tokens only if
+// they hold as many times seg.
 struct SegPlace {
   int b, tok0, len, seq;
+  int cut;                      // behind it; the one before it is cut - 1
   bool first, last;             // of its sequence
 };
 inline __host__ __device__ int64_t seg_slots(const DeltaSeqs& q, int batch, int seg) {
   if (q.starts) return q.num > 0 ? (int64_t)q.n / seg + q.num : 0;
   return (int64_t)batch * (((int64_t)q.n + seg - 1) / seg);
 }
+inline int64_t seg_cuts(const DeltaSeqs& q, int batch, int seg) {
+  if (q.starts) return q.num > 0 ? q.n / seg : 0;
+  return q.n > 0 ? (int64_t)batch * ((q.n - 1) / seg) : 0;
+}
 __device__ __forceinline__ SegPlace seg_place(const DeltaSeqs& q, int seg, int slot) {
   if (!q.starts) {
     const int m = (int)(((int64_t)q.n + seg - 1) / seg), b = slot / m, c = slot - b * m;
-    return {b, c * seg, min(seg, q.n - c * seg), b, c == 0, c == m - 1};
+    return {b, c * seg, min(seg, q.n - c * seg), b, b * (m - 1) + c, c == 0, c == m - 1};
   }
   int lo = 0, hi = q.num;       // the last sequence whose first slot is not past this one
   while (hi - lo > 1) {
@@ -40,20 +47,20 @@ __device__ __forceinline__ SegPlace seg_place(const DeltaSeqs& q, int seg, int s
     if (seq_start(q, mid) / seg + mid <= slot) lo = mid; else hi = mid;
   }
   const int a = seq_start(q, lo), e = max(seq_start(q, lo + 1), a), c = slot - (a / seg + lo);
-  if (c < 0 || (int64_t)c * seg >= e - a) return {0, 0, 0, lo, false, false};
-  return {0, a + c * seg, min(seg, e - a - c * seg), lo, c == 0, (int64_t)(c + 1) * seg >= e - a};
+  if (c < 0 || (int64_t)c * seg >= e - a) return {0, 0, 0, lo, 0, false, false};
+  return {0, a + c * seg, min(seg, e - a - c * seg), lo, a / seg + c, c == 0, (int64_t)(c + 1) * seg >= e - a};
 }
-// First slot of sequence s and its segments.
-struct SeqSlots {
+// First cut of sequence s and its segments.
+struct SeqCuts {
   int first, count;
 };
-__device__ __forceinline__ SeqSlots seq_slots(const DeltaSeqs& q, int seg, int s) {
+__device__ __forceinline__ SeqCuts seq_cuts(const DeltaSeqs& q, int seg, int s) {
   if (!q.starts) {
     const int m = (int)(((int64_t)q.n + seg - 1) / seg);
-    return {s * m, m};
+    return {s * (m - 1), m};
   }
   const int a = seq_start(q, s), e = max(seq_start(q, s + 1), a);
-  return {a / seg + s, (int)(((int64_t)(e - a) + seg - 1) / seg)};
+  return {a / seg, (int)(((int64_t)(e - a) + seg - 1) / seg)};
 }
 
 // Row block and step of a triangular matrix's fragment.

@@ -625,12 +625,12 @@ GradSpace grad_space(const ScanArgs& a) {
   g.seg = scan_seg<T>(a, 256, 128);
   g.slots = seg_slots(a.seqs, a.batch, g.seg);
   g.chunks = delta_slots(a.seqs, a.batch);
-  const bool cut = g.seg < a.seqs.n;
+  const int64_t cuts = seg_cuts(a.seqs, a.batch, g.seg);
   g.gates = g.chunks * a.H * sizeof(KeptGates);
   g.tokens = g.chunks * a.H * sizeof(TokenSums<T>);
   g.keep = g.chunks * a.H * a.P * a.N * 4;
-  g.sums = cut ? g.slots * a.H * a.P * a.N * 4 : 0;
-  g.decays = cut ? (g.slots * a.H * 4 + 15) / 16 * 16 : 0;
+  g.sums = cuts * a.H * a.P * a.N * 4;
+  g.decays = (cuts * a.H * 4 + 15) / 16 * 16;
   g.part = g.chunks * a.H * 16;
   // The heads of a group are dealt to as many workgroups as take least, by rounds of one a CU: `once` heads' time for what
   // each does once, `join` for the sum of the shares (fitted).  32 heads of 64 x 128 in one group, 300 tokens: bf16 241 -> 79

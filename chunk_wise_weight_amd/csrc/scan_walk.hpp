@@ -36,7 +36,7 @@ struct StateWalk {
   DeltaStrides srows, scols;
   const float* start;                 // S_init or dS_final [sequences, H, P, N], or null: zero
   float* end;                         // dS_init (back) [sequences, H, P, N], or null
-  float *sums, *decays;               // of segment slots and heads [P, N], 1; null: sequences are one segment
+  float *sums, *decays;               // of cuts and heads [P, N], 1; null: sequences are one segment
   float* keep;                        // of chunk slots and heads: the state before the chunk (back: after it)
   KeptGates* gates;                   // of chunk slots and heads, or null
   bool back;
@@ -161,9 +161,10 @@ __device__ __forceinline__ void sum_segment(const ScanArgs& a, const StateWalk& 
     stage ^= 1;
   }
   const int64_t size = (int64_t)a.P * a.N;
-  if (q.busy) S.store(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
+  const int64_t cut = k.back ? sp.cut - 1 : sp.cut;          // at its end in the walk's direction
+  if (q.busy) S.store(k.sums + (cut * a.H + q.h) * size, q.tile0, a.P, a.N);
   // (heads past the group's repeat the last one's; after a break F is below kNone and stays there)
-  if (q.w < HW && q.lane == 0 && at.part == 0) k.decays[(int64_t)at.slot * a.H + q.gh] = exp2_hw((float)F);
+  if (q.w < HW && q.lane == 0 && at.part == 0) k.decays[cut * a.H + q.gh] = exp2_hw((float)F);
 }
 
 // The states before (back: after) every chunk, kept for the gradients.  Bound by their stores: 4 x 4,096 tokens x 32 heads of
@@ -183,8 +184,8 @@ __device__ __forceinline__ void keep_segment(const ScanArgs& a, const StateWalk&
   StateRows<T, K::CT, K::NT> S;
   S.zero();
   if (q.busy) {
-    if (k.sums)
-      S.load(k.sums + ((int64_t)at.slot * a.H + q.h) * size, q.tile0, a.P, a.N);
+    if (!(k.back ? sp.last : sp.first))
+      S.load(k.sums + ((int64_t)(k.back ? sp.cut : sp.cut - 1) * a.H + q.h) * size, q.tile0, a.P, a.N);
     else if (k.start)
       S.load(k.start + ((int64_t)sp.seq * a.H + q.h) * size, q.tile0, a.P, a.N);
   }
@@ -269,36 +270,41 @@ hipError_t launch_states(const ScanArgs& a, const StateWalk& one, const StateWal
   return hipGetLastError();
 }
 
-// The state before (back: after) every segment from the segments' own: a thread has 4 elements of a sequence's and
-// head's state.  Sequences without tokens: their `empty` state is their first.
+// The state at every cut from the segments' own: a thread has 4 elements of a sequence's and head's state.  A cut's place
+// holds the sum of the segment that ends there (in the walk's direction) and then the state that the next one begins with;
+// a sequence's first begins with `start`.  Sequences without tokens: their `empty` state is that.
 __device__ __forceinline__ void join_segments(const ScanArgs& a, const StateWalk& k, float* empty, int seg, int bid) {
   const int64_t size = (int64_t)a.P * a.N;
   const int blocks = (int)((size / 4 + 255) / 256), s = bid / blocks / a.H, h = bid / blocks % a.H;
   const int64_t e = ((int64_t)(bid % blocks) * 256 + threadIdx.x) * 4;
-  if (e >= size) return;
-  const SeqSlots q = seq_slots(a.seqs, seg, s);
+  const SeqCuts q = seq_cuts(a.seqs, seg, s);
+  const int cuts = q.count - 1;
+  if (e >= size || (q.count == 0 ? empty == nullptr : cuts == 0)) return;
   const int64_t o = ((int64_t)s * a.H + h) * size + e;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (k.start) S = *reinterpret_cast<const f32x4*>(k.start + o);
-  constexpr int U = 4;                                       // segments whose loads are under way at once
-  if (k.sums)
-    for (int i0 = 0; i0 < q.count; i0 += U) {
-      f32x4 own[U];
-      float d[U];
-      auto slot = [&](int i) { return (int64_t)(q.first + (k.back ? q.count - 1 - i : i)) * a.H + h; };
+  if (q.count == 0) {
+    *reinterpret_cast<f32x4*>(empty + o) = S;
+    return;
+  }
+  constexpr int U = 4;                                       // cuts whose loads are under way at once
+  for (int i0 = 0; i0 < cuts; i0 += U) {
+    f32x4 own[U];
+    float d[U];
+    auto place = [&](int i) { return (int64_t)(q.first + (k.back ? cuts - 1 - i : i)) * a.H + h; };
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u + 1 < q.count) {                          // the last one's is not made
-          own[u] = *reinterpret_cast<const f32x4*>(k.sums + slot(i0 + u) * size + e);
-          d[u] = k.decays[slot(i0 + u)];
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i0 + u < q.count) *reinterpret_cast<f32x4*>(k.sums + slot(i0 + u) * size + e) = S;
-        if (i0 + u + 1 < q.count) S = d[u] == 0.f ? own[u] : S * d[u] + own[u];
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < cuts) {
+        own[u] = *reinterpret_cast<const f32x4*>(k.sums + place(i0 + u) * size + e);
+        d[u] = k.decays[place(i0 + u)];
       }
-    }
-  if (q.count == 0 && empty) *reinterpret_cast<f32x4*>(empty + o) = S;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < cuts) {
+        S = d[u] == 0.f ? own[u] : S * d[u] + own[u];
+        *reinterpret_cast<f32x4*>(k.sums + place(i0 + u) * size + e) = S;
+      }
+  }
 }
 __global__ __launch_bounds__(256) void k_scan_join(ScanArgs a, StateWalk one, float* empty1, StateWalk two, float* empty2,
                                                    int seg, int half) {

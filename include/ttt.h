@@ -1002,9 +1002,11 @@ typedef struct {
   const ttt_scan_layout* layout;  /* HOST; NULL: contiguous */
 } ttt_scan_options;
 
-/* Workspace of ttt_selective_scan; num_seqs < 0: not packed.  Zero where every
- * sequence is one segment, else 4 P N + 4 bytes for each segment and head: few
- * more than fill the chip once. */
+/* Workspace of ttt_selective_scan; num_seqs < 0: not packed.  4 P N + 4 bytes
+ * for each head and place where a row may be cut into segments: (seq_len - 1) /
+ * segment a row, seq_len / segment where it is packed, however many sequences
+ * it holds; segments are as long as fill the chip once, and zero bytes where
+ * one takes a whole row. */
 int ttt_selective_scan_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
 
 /* The recurrence over whole sequences.
@@ -1035,8 +1037,9 @@ typedef struct {
 
 /* Workspace of ttt_selective_scan_backward; num_seqs < 0: not packed.  The
  * limits in ttt_scan_shape are half as high (2^22 and 2^23), else
- * TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + some 8 KB, for each
- * segment and head 8 P N + 8, and up to 512 KB N for the shares of dB and dC. */
+ * TTT_ERR_UNSUPPORTED.  For each chunk and head 8 P N + some 8 KB (a packed
+ * sequence's last chunk counts whole: seq_len / 64 + sequences), for each cut
+ * and head 8 P N + 8, and up to 512 KB N for the shares of dB and dC. */
 int ttt_selective_scan_backward_workspace_bytes(const ttt_scan_shape* shape, int dtype, int64_t num_seqs, size_t* bytes);
 
 /* The backward of ttt_selective_scan, from the forward call's inputs alone
