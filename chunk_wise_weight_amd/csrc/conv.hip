@@ -5,8 +5,8 @@
 //
 // Bound by HBM: x is read once and y written once.  A thread has 16 bytes of channels and walks over a run of tokens
 // with the last K rows in registers (named in turn, so that none is moved), the next K rows' loads under way; a run
-// reads the K - 1 rows before it again.  All sums are fp32.  65,536 x 6144 in bf16, K = 4: 253 us, 6.4 TB/s; backward of
-// 16,458 x 2304: 54 us, 4.2 TB/s; 256 tokens x 6144: 7 us.
+// reads the K - 1 rows before it again.  Sums are fp32, those of gradients over runs fp64.  65,536 x 6144 in bf16, K = 4: 253
+// us, 6.4 TB/s; backward of 16,458 x 2304: 54 us, 4.2 TB/s; a step of 256 rows x 6144: 7 us.
 #include "delta.hpp"
 #include "norm.hpp"
 #include "slots.hpp"
@@ -376,8 +376,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_grad(ConvGradArgs g, Conv
   }
 }
 
-// dw[c][k] and dbias[c]: the parts' sums in fp64 in a fixed order, 16 channels of a tap a workgroup, each of its 64 rows of threads
-// every 64th part, joined in LDS.
+// dw[c][k] and dbias[c]: the parts' sums in fp64 in a fixed order, 16 channels of a tap a workgroup, each of its 64 rows of
+// threads every 64th part, joined in LDS.
 __global__ __launch_bounds__(1024) void k_conv_sum(const float* __restrict__ part, int64_t parts, int d, int K,
                                                    float* __restrict__ dw, float* __restrict__ db) {
   __shared__ double sum[64][17];
@@ -477,8 +477,10 @@ ConvPlan conv_plan(const ConvArgs& a, int VEC, int most) {
   return p;
 }
 
-// Tokens of a run, at most.  Forward: short ones, so that a wave's rows lie in few pages (65,536 x 6144, K = 4: runs of 8
-// 291 us, 12 287 us, 16 294 us, 32 313 us); backward: each costs a sum of dw (16,458 x 2304: 64 59 us, 24 65 us).
+// Tokens of a run, at most.  Forward: short ones, so that a wave's rows lie in few pages, and longer where more rows before a
+// run are read again (65,536 x 6144 in bf16, us for runs of 8, 12, 16, 24, 48: K = 2 253, 275, 285, 290, 307; K = 4 265, 253,
+// 262, 274, 302; K = 6 327, 277, 266, 278, 297; K = 8 375, 318, 292, 299, 301); backward: each costs a sum of dw (16,458 x
+// 2304: 64 59 us, 24 65 us).
 int forward_run(int K) { return std::max(8, 3 * K); }
 constexpr int kGradRun = 64;
 

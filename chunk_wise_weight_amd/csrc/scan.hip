@@ -10,8 +10,9 @@ namespace {
 //   S C from the state's two parts, then S' with x and B: B and C have been read, the next chunk's come
 //   the decayed C B^T times x, the outputs packed; they are stored in the next turn, behind its barrier, so that no wait
 //   for loads waits for them
-// Bound by the chain of a chunk on two waves a SIMD (registers): 65,536 tokens x 64 heads of 64 x 128 in bf16 506 us, the
-// matrix cores busy for 45 % of it; a block of columns less a wave and four waves a SIMD spill and take 1,469 us.
+// Bound by the chain of a chunk on two waves a SIMD (registers): 65,536 tokens x 64 heads of 64 x 128 in bf16 take 72 % of
+// the call's time (traced: 523 us at the least), the matrix cores busy for 47 % of its cycles; a block of columns less a wave
+// and four waves a SIMD spill and take 1,469 us.
 template <typename T, int DN, int HW, int PW>
 __global__ __launch_bounds__(64 * HW * PW, 2) void k_scan(ScanArgs a, int seg, int slots, const float* sums) {
 #if __HIP_DEVICE_COMPILE__
@@ -263,9 +264,11 @@ hipError_t launch(const ScanArgs& a, int seg, int64_t slots, const float* sums, 
   return hipGetLastError();
 }
 
-// 512 workgroups are on the chip at once: one round of them (65,536 tokens x 64 heads: 384 860 us, 512 707 us, 768 794 us,
-// 1024 745 us).  Whole sequences save the pass over the segments' sums: 8 x 64 heads, 256 workgroups, take 91 us for 1,024
-// tokens each (in two segments 109 us) and 341 us for 4,096 (284 us), 12 x 64 heads 425 us for 4,096 (490 us).
+// 512 workgroups are on the chip at once: one round of them, by the tokens in all (the ends of packed sequences come on top:
+// 12 prompts of 16,456 tokens have 576; longer segments for them gained for one long prompt and lost for equal ones).
+// 65,536 tokens x 64 heads: 384 860 us, 512 707 us, 768 794 us, 1024 745 us.  Whole sequences save the pass over the
+// segments' sums: 8 x 64 heads, 256 workgroups, take 91 us for 1,024 tokens each (in two segments 109 us) and 341 us for
+// 4,096 (284 us), 12 x 64 heads 425 us for 4,096 (490 us).
 template <typename T>
 int forward_seg(const ScanArgs& a) {
   return scan_seg<T>(a, 512, a.seqs.n < 2048 ? 256 : 384);

@@ -231,8 +231,8 @@ __device__ __forceinline__ void two_parts(double b, float* hi, float* lo) {
 }
 
 // Gates as they lie in LDS: b in two parts, exp(b), the rates, and exp(b_63 - b) r.  bf16 outputs take one fp32 b, lo 0, where
-// the chunk's sum stays above kOnePart: differences of two such are off by 2^-16 at most, as the products are.  Sums of 64 reach
-// 2^14 (tokens that empty the state), where one part would be off by 2^-10.
+// the chunk's sum stays above kOnePart: differences of two such are off by 2^-16 at most, as the products are.  Sums of 64
+// reach 2^14 (tokens that empty the state), where one part would be off by 2^-10.
 constexpr double kOnePart = -256.0;
 struct Gates {
   float hi[kDC], lo[kDC], eb[kDC], r[kDC], w[kDC];

@@ -133,8 +133,9 @@ template <typename T> struct TokenSums {
 //   du         blocks 2 (w & 1) and the next of P, tokens row(w >> 1, .)
 //   C B^T, dO x^T and their decayed forms by fragments, a wave one (fp32: two); they go to LDS once for all waves
 // States come as fp32, the next block's loads under way while one is worked on, and are cut into planes on their way to
-// LDS; sums that go into ddt are of all three planes, dx of two.  4 x 4,096 tokens x 32 heads of 64 x 128 in bf16: 263 us, 2.2
-// TB/s; one workgroup a CU fits LDS, and its barriers leave the matrix cores busy for 17 %, LDS for 30 %.
+// LDS; sums that go into ddt are of all three planes, dx of two.  4 x 4,096 tokens x 32 heads of 64 x 128 in bf16: 268 us at the
+// least under a trace, 2.2 TB/s; one workgroup a CU fits LDS, and its barriers leave the matrix cores busy for 16 % of the
+// cycles, LDS for 30 %.
 template <typename T, int DN, bool LDS>
 __global__ __launch_bounds__(512, 2) void k_scan_grads(ScanGradArgs a) {
 #if __HIP_DEVICE_COMPILE__
